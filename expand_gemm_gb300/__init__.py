@@ -30,7 +30,8 @@ from ._lib import (LoraError, LORA_MAX_LORAS, LORA_MAX_RANK, LORA_MAX_SLICES,  #
 
 __all__ = ["LoRAKernelMeta", "lora_meta_prepare", "lora_shrink", "lora_expand",
            "lora_linear", "lora_linear_noalloc", "add_lora_linear", "add_lora_embedding",
-           "add_lora_logits", "reload_options", "LoraError", "library", "build"]
+           "add_lora_logits", "lora_cross_entropy", "lora_cross_entropy_workspace",
+           "reload_options", "LoraError", "library", "build"]
 
 
 def library():
@@ -390,3 +391,110 @@ def lora_linear_noalloc(token_lora_mapping: torch.Tensor, x: torch.Tensor, lora_
     _same_device(meta, a["named"])
     _call("lora_linear_noalloc", x.device, *a["head"], float(scale), *a["tail"],
           ctypes.byref(meta.c), _stream_handle(x.device))
+
+
+# ------------------------------------------------------------ training the adapters
+
+def _workspace_bytes(fn: str, device, *args) -> int:
+    with torch.cuda.device(device):
+        n = getattr(_lib.load(), fn)(*args)
+    if n < 0:
+        _lib.check(fn, int(n))
+    return int(n)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    """The caller's workspace after its checks, or a new one."""
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8)
+    if not workspace.is_contiguous() or workspace.numel() < need:
+        raise ValueError("workspace must be contiguous with at least %d bytes" % need)
+    return workspace
+
+
+def _same_gpu(ref: torch.Tensor, named) -> None:
+    for name, t in named:
+        if t is not None and t.get_device() != ref.get_device():
+            raise ValueError("%s is on cuda:%d, expected cuda:%d"
+                             % (name, t.get_device(), ref.get_device()))
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype) -> torch.Tensor:
+    """A [rows, cols] view of t whose rows are contiguous."""
+    _need(t, name, dtype)
+    t2 = t.view(-1, t.shape[-1]) if t.dim() != 2 else t
+    if t2.stride(1) != 1 and t2.size(1) > 1 or t2.size(0) > 1 and t2.stride(0) < t2.size(1):
+        raise ValueError("%s needs contiguous rows that do not overlap" % name)
+    return t2
+
+
+def _ld(t2: torch.Tensor) -> int:
+    return max(t2.stride(0), t2.size(1))
+
+
+def _vector(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int) -> Optional[int]:
+    if t is None:
+        return None
+    _need(t, name, dtype)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with %d elements" % (name, n))
+    return t.data_ptr()
+
+
+def lora_cross_entropy_workspace(num_tokens: int, hidden: int, vocab: int, *,
+                                 hidden_grad: bool = True, weight_grad: bool = False,
+                                 device="cuda") -> int:
+    """Bytes of workspace of :func:`lora_cross_entropy` at these sizes."""
+    return _workspace_bytes("lora_cross_entropy_workspace", device, num_tokens, hidden, vocab,
+                            int(hidden_grad), int(weight_grad))
+
+
+def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                       loss: torch.Tensor, *, token_weight: Optional[torch.Tensor] = None,
+                       logsumexp: Optional[torch.Tensor] = None,
+                       hidden_grad: Optional[torch.Tensor] = None,
+                       weight_grad: Optional[torch.Tensor] = None,
+                       error_word: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None) -> None:
+    """Cross entropy of the logits hidden @ weight^T against targets, and its
+    gradients, without keeping the logits.
+
+    loss[t] (fp32) = w_t (logsumexp_t - logit of targets[t]), w_t =
+    token_weight[t] (fp32; 1 when None).  A target outside [0, vocab) (-100,
+    say) means none: zero loss and gradient.  hidden_grad (bf16, like hidden)
+    and weight_grad (bf16, like weight) are overwritten when given;
+    error_word (int32 [1]) receives the count of targets >= vocab.  A
+    workspace (uint8) is allocated when none is given."""
+    h = _rows(hidden, "hidden", torch.bfloat16)
+    T, H = h.shape
+    _need(weight, "weight", torch.bfloat16)
+    if weight.dim() != 2 or weight.size(1) != H or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous [vocab, %d] tensor" % H)
+    V = weight.size(0)
+    _need(loss, "loss", torch.float32)
+    t_ptr = _vector(targets, "targets", torch.int32, T)
+    l_ptr = _vector(loss, "loss", torch.float32, T)
+    w_ptr = _vector(token_weight, "token_weight", torch.float32, T)
+    s_ptr = _vector(logsumexp, "logsumexp", torch.float32, T)
+    e_ptr = _vector(error_word, "error_word", torch.int32, 1)
+    dh = None
+    if hidden_grad is not None:
+        dh = _rows(hidden_grad, "hidden_grad", torch.bfloat16)
+        if dh.shape != h.shape:
+            raise ValueError("hidden_grad must be [%d, %d]" % (T, H))
+    if weight_grad is not None:
+        _need(weight_grad, "weight_grad", torch.bfloat16)
+        if weight_grad.shape != weight.shape or not weight_grad.is_contiguous():
+            raise ValueError("weight_grad must be contiguous like weight")
+    _same_gpu(hidden, [("weight", weight), ("targets", targets), ("loss", loss),
+                       ("token_weight", token_weight), ("logsumexp", logsumexp),
+                       ("hidden_grad", hidden_grad), ("weight_grad", weight_grad),
+                       ("error_word", error_word), ("workspace", workspace)])
+    dev = hidden.device
+    ws = _workspace(workspace, lora_cross_entropy_workspace(
+        T, H, V, hidden_grad=dh is not None, weight_grad=weight_grad is not None, device=dev), dev)
+    _call("lora_cross_entropy", dev, h.data_ptr(), T, H, _ld(h), weight.data_ptr(), V, t_ptr, w_ptr,
+          l_ptr, s_ptr, None if dh is None else dh.data_ptr(), H if dh is None else _ld(dh),
+          None if weight_grad is None else weight_grad.data_ptr(), e_ptr, ws.data_ptr(), ws.numel(),
+          _stream_handle(dev))

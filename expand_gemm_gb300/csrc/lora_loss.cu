@@ -1,0 +1,761 @@
+// lora_loss.cu -- softmax cross entropy over a vocabulary whose logits are
+// never kept, with the gradients of the hidden states and of the head.
+//
+//   S = h W^T,  loss_t = w_t (log sum_v exp S_tv - S_ty)
+//   dh_t = w_t (sum_{v != y} p_tv W_v - (1 - p_ty) W_y),  p = softmax(S)
+//   dW_v = sum_t w_t (p_tv - [v = y_t]) h_t
+//
+// The vocabulary is walked in pieces.  For each piece one product gives its
+// logits in TMEM, the epilogue turns them into powers of two relative to a
+// whole-number reference of the row and writes those as bf16 (the piece's
+// scratch), and a second product adds scratch x W to the fp32 rows of dh.
+// The softmax's sum is known only after the last piece, so dh is divided by
+// it at the end.  The target's column stays zero in the scratch and enters
+// as -(1 - p_y) W_y in fp32: 1 - p_y is the sum over the other columns, so
+// nothing cancels when the model is sure of the target.
+//
+// References.  A bf16 power of two keeps its 8 bits anywhere between 2^-126
+// and 2^127, so a reference need not be the row's maximum: it starts at 0
+// and a tile whose largest exponent lies within 60 of it uses it.  A tile
+// outside that window takes its own maximum, and join_kernel then brings
+// the row's scratch to one reference (multiplications by powers of two,
+// exact).
+//
+// dW needs the finished sums, so with a head gradient the pieces are walked
+// a second time: the same product, the epilogue writes w (p - [y]) and a
+// third product contracts it with h over the tokens.
+//
+// Tokens without a target (outside [0, V)) are left out from the start:
+// pack_kernel copies the others' rows next to each other, so a prompt's
+// masked tokens cost nothing, and what their rows hold is never read.
+#include <math.h>
+
+#include "lora_pair_gemm.cuh"
+
+namespace lora {
+
+constexpr int LS_PIECE_ELEMS = 64 << 20;      // tokens x columns of one piece's scratch
+constexpr int LS_MIN_PIECE = 1024;            // columns
+constexpr int LS_WINDOW = 60;                 // exponents a tile may be off the reference
+constexpr int LS_MAX_SPLIT = 8;
+constexpr int LS_PACK_TOKENS = 32;            // tokens of one block of pack_kernel
+constexpr float LS_LOG2E = 1.4426950408889634f;
+constexpr float LS_LN2 = 0.6931471805599453f;
+
+// What a call's workspace holds; every part begins on a 256-byte boundary.
+struct LossLayout {
+    int64_t tokens;        // T rounded up to whole tiles
+    int64_t piece;         // columns of a piece, a multiple of PG_TILE
+    int pieces, split;
+    int64_t count, row, target, weight, ref, sum, logit, factor, inv, share, lse, stat, h, p, acc;
+    int64_t bytes;
+};
+
+static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad, bool weight_grad,
+                              int pairs)
+{
+    LossLayout l;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b * b; };
+    l.tokens = up(T > 0 ? T : 1, PG_TILE);
+    int64_t most = LS_PIECE_ELEMS / l.tokens / PG_TILE * PG_TILE;
+    if (most < LS_MIN_PIECE) most = LS_MIN_PIECE;
+    l.pieces = int((V + most - 1) / most);
+    l.piece = up((V + l.pieces - 1) / l.pieces, PG_TILE);
+    l.pieces = int((V + l.piece - 1) / l.piece);
+    // The product of the scratch and W has few tiles when there are few
+    // tokens: its K (the piece) is then split over up to LS_MAX_SPLIT
+    // partial sums, joined in a fixed order by finish_kernel.
+    const int64_t tiles = l.tokens / PG_TILE * ((H + PG_TILE - 1) / PG_TILE);
+    int64_t split = pairs / tiles;
+    if (split > LS_MAX_SPLIT) split = LS_MAX_SPLIT;
+    if (split > l.piece / PG_BK / 8) split = l.piece / PG_BK / 8;
+    l.split = split < 1 ? 1 : int(split);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes, 256);
+        return here;
+    };
+    l.count = take(4);
+    l.row = take(l.tokens * 4);
+    l.target = take(l.tokens * 4);
+    l.weight = take(l.tokens * 4);
+    l.ref = take(l.tokens * 4);
+    l.sum = take(l.tokens * 4);
+    l.logit = take(l.tokens * 4);
+    l.factor = take(l.tokens * 4);
+    l.inv = take(l.tokens * 4);
+    l.share = take(l.tokens * 4);
+    l.lse = take(l.tokens * 4);
+    l.stat = take(l.tokens * (l.piece / PG_TILE) * 8);
+    l.h = take(l.tokens * H * 2);
+    l.p = take(hidden_grad || weight_grad ? l.tokens * l.piece * 2 : 0);
+    l.acc = take(hidden_grad ? l.split * l.tokens * H * 4 : 0);
+    l.bytes = at;
+    return l;
+}
+
+struct LossArgs {
+    const uint16_t *hidden;
+    int64_t hidden_ld;
+    const uint16_t *weight;
+    const int32_t *targets;
+    const float *token_weight;
+    float *loss, *logsumexp;
+    uint16_t *dh;
+    int64_t dh_ld;
+    int32_t T, H, V;
+    int32_t hidden_vec, dh_vec;        // rows allow 16-byte accesses
+    int32_t *error_word;
+    // workspace
+    int32_t *count;                    // tokens with a target
+    int32_t *row, *target, *ref;
+    float *wt, *sum, *logit, *factor, *inv, *share, *lse;
+    float2 *stat;                      // [piece tiles][tokens]: reference, sum
+    uint16_t *h, *p;
+    float *acc;
+    int64_t tokens, piece;
+    int32_t split;
+};
+
+// ---------------------------------------------------------------- pack
+
+// Block b copies tokens [32 b, 32 b + 32) that have a target to their place
+// among those that have one (the count of targets before them, which every
+// block takes itself), and clears the outputs of the others.  The last block
+// also fills the tile behind the last row with zeros.  The target's logit is
+// summed here, in ordinary fp32: the loss is a difference with it, and the
+// tensor cores' sums truncate (over 4096 products they leave the loss 4
+// times further off).
+__global__ void __launch_bounds__(256) pack_kernel(const LossArgs p)
+{
+    __shared__ int s_part[2][8];
+    __shared__ int s_place[LS_PACK_TOKENS];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c0 = blockIdx.x * LS_PACK_TOKENS;
+    int before = 0, bad = 0;
+    for (int t = tid; t < c0; t += 256) {
+        const int y = p.targets[t];
+        before += y >= 0 && y < p.V;
+        bad += y >= p.V;
+    }
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        bad += __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    if (lane == 0) {
+        s_part[0][warp] = before;
+        s_part[1][warp] = bad;
+    }
+    __syncthreads();
+    before = bad = 0;
+    for (int i = 0; i < 8; ++i) {
+        before += s_part[0][i];
+        bad += s_part[1][i];
+    }
+    const int t = c0 + lane;
+    const int y = t < p.T ? p.targets[t] : -1;
+    const bool valid = y >= 0 && y < p.V;
+    const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+    const int place = before + __popc(mask & ((1u << lane) - 1u));
+    const int n = before + __popc(mask);
+    if (warp == 0) {
+        s_place[lane] = valid ? place : -1;
+        if (valid) {
+            p.row[place] = t;
+            p.target[place] = y;
+            p.wt[place] = p.token_weight != nullptr ? p.token_weight[t] : 1.0f;
+            p.ref[place] = 0;
+            p.sum[place] = 0.0f;
+        } else if (t < p.T) {
+            p.loss[t] = 0.0f;
+            if (p.logsumexp != nullptr) p.logsumexp[t] = 0.0f;
+        }
+    }
+    const bool last = blockIdx.x == gridDim.x - 1;
+    const int n_up = (n + PG_TILE - 1) / PG_TILE * PG_TILE;
+    if (last) {
+        bad += __popc(__ballot_sync(0xffffffffu, y >= p.V));
+        if (tid == 0) {
+            *p.count = n;
+            if (p.error_word != nullptr) *p.error_word = bad;
+        }
+        for (int r = n + tid; r < n_up; r += 256) {
+            p.row[r] = -1;
+            p.target[r] = -1;
+            p.wt[r] = 0.0f;
+            p.ref[r] = 0;
+            p.sum[r] = 0.0f;
+            p.logit[r] = 0.0f;
+        }
+        for (int64_t i = tid; i < int64_t(n_up - n) * (p.H / 8); i += 256)
+            reinterpret_cast<uint4 *>(p.h + int64_t(n) * p.H)[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    for (int i = warp; i < LS_PACK_TOKENS && c0 + i < p.T; i += 8) {
+        const int to = s_place[i];
+        if (to >= 0) {
+            const uint16_t *src = p.hidden + int64_t(c0 + i) * p.hidden_ld;
+            uint16_t *dst = p.h + int64_t(to) * p.H;
+            const uint16_t *w = p.weight + int64_t(p.targets[c0 + i]) * p.H;
+            float dot = 0.0f;
+            for (int c = lane * 8; c < p.H; c += 256) {
+                uint4 v;
+                if (p.hidden_vec) {
+                    v = *reinterpret_cast<const uint4 *>(src + c);
+                } else {
+                    v.x = src[c] | uint32_t(src[c + 1]) << 16;
+                    v.y = src[c + 2] | uint32_t(src[c + 3]) << 16;
+                    v.z = src[c + 4] | uint32_t(src[c + 5]) << 16;
+                    v.w = src[c + 6] | uint32_t(src[c + 7]) << 16;
+                }
+                *reinterpret_cast<uint4 *>(dst + c) = v;
+                const uint4 u = *reinterpret_cast<const uint4 *>(w + c);
+                const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dot = fmaf(bf16_lo(a[j]), bf16_lo(b[j]), dot);
+                    dot = fmaf(bf16_hi(a[j]), bf16_hi(b[j]), dot);
+                }
+            }
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            if (lane == 0) p.logit[to] = dot * LS_LOG2E;
+        } else if (p.dh != nullptr) {
+            uint16_t *dst = p.dh + int64_t(c0 + i) * p.dh_ld;
+            if (p.dh_vec) {
+                for (int c = lane; c < p.H / 8; c += 32)
+                    reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int c = lane; c < p.H; c += 32) dst[c] = 0;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- products
+
+struct LossGemm {
+    CUtensorMap a, b;
+    LossArgs l;
+    int32_t col0, cols;       // this piece of the vocabulary
+    int32_t store;            // logits: write the scratch
+    int32_t first;            // scratch x W: the rows of dh start here
+    uint16_t *dw;             // head gradient
+};
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Logits of a piece: 256 tokens x 256 columns a tile, tokens innermost (the
+// packed rows stay in L2 while a few tiles of W pass).
+// GRAD: the sums are known, the scratch becomes w (p - [y]).
+template <bool GRAD>
+__global__ void __launch_bounds__(PG_THREADS, 1)
+logits_kernel(const __grid_constant__ LossGemm g)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const LossArgs &l = g.l;
+    const int mt = (*l.count + PG_TILE - 1) / PG_TILE;
+    const int nt = (g.cols + PG_TILE - 1) / PG_TILE;
+    const int kb = (l.H + PG_BK - 1) / PG_BK;
+    auto item = [&](int i) {
+        return PairItem{(i % mt) * PG_TILE, g.col0 + (i / mt) * PG_TILE, 0, kb};
+    };
+    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int rank, bool) {
+        const int row = it.row_a + rank * PG_HALF + r;
+        const int tile = i / mt;
+        const int lim = min(PG_TILE, g.col0 + g.cols - it.row_b);       // columns of this tile
+        const int y = l.target[row] - it.row_b;                         // column of the target
+        uint16_t *dst = l.p + int64_t(row) * l.piece + tile * PG_TILE;
+        uint32_t v[32];
+        float ref, scale = 1.0f, q = 0.0f, sum = 0.0f;
+        if constexpr (GRAD) {
+            ref = l.lse[row];
+            scale = l.wt[row];
+            q = -l.share[row];
+        } else {
+            float top = -INFINITY;
+            for (int c = 0; c < lim; c += 32) {
+                tmem_ld32_nowait(tmem + c, v);
+                tmem_wait_ld();
+                if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j == y) v[j] = 0xff800000u;             // -inf
+                }
+                if (c + 32 <= lim) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(v[j]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < lim) top = fmaxf(top, __uint_as_float(v[j]));
+                }
+            }
+            const int have = l.ref[row];
+            top *= LS_LOG2E;
+            ref = float(have);
+            if (top > -INFINITY && !(fabsf(top - ref) <= float(LS_WINDOW)))
+                ref = ceilf(fminf(fmaxf(top, -1e9f), 1e9f));
+        }
+        for (int c = 0; c < PG_TILE; c += 32) {
+            if (GRAD ? c >= lim : (c >= lim && !g.store)) break;
+            uint32_t pk[16];
+            if (c < lim) {
+                tmem_ld32_nowait(tmem + c, v);
+                tmem_wait_ld();
+                float e[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), LS_LOG2E, -ref));
+                if (c + 32 > lim) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j >= lim) e[j] = 0.0f;
+                }
+                if constexpr (GRAD) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) e[j] *= scale;
+                }
+                if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j == y) e[j] = q;
+                }
+                if constexpr (!GRAD) {
+                    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        s0 += e[j];
+                        s1 += e[j + 1];
+                    }
+                    sum += s0 + s1;
+                }
+                // rounded to bf16 for the second product: relative 2^-9 of
+                // each term, the size of the output's own rounding
+#pragma unroll
+                for (int j = 0; j < 16; ++j) pk[j] = pack_bf16x2(e[2 * j], e[2 * j + 1]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) pk[j] = 0u;
+            }
+            if (GRAD || g.store) {
+                const uint32_t lo[8] = {pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]};
+                const uint32_t hi[8] = {pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]};
+                st_global_v8(dst + c, lo);
+                st_global_v8(dst + c + 16, hi);
+            }
+        }
+        if constexpr (!GRAD) l.stat[int64_t(tile) * l.tokens + row] = make_float2(ref, sum);
+    };
+    pair_gemm<false, false>(&g.a, &g.b, mt * nt, l.error_word, item, epilogue);
+}
+
+// acc[split][token][h] (+)= scratch x W over a share of the piece's columns
+// (W's rows are the K dimension: its rows are contiguous along N).
+__global__ void __launch_bounds__(PG_THREADS, 1)
+hidden_grad_kernel(const __grid_constant__ LossGemm g)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const LossArgs &l = g.l;
+    const int mt = (*l.count + PG_TILE - 1) / PG_TILE;
+    const int nt = (l.H + PG_TILE - 1) / PG_TILE;
+    const int kb = (g.cols + PG_BK - 1) / PG_BK;
+    const int per = (kb + l.split - 1) / l.split;
+    auto item = [&](int i) {
+        const int s = i / (mt * nt), j = i % (mt * nt);
+        return PairItem{(j % mt) * PG_TILE, (j / mt) * PG_TILE, min(kb, s * per),
+                        min(kb, (s + 1) * per)};
+    };
+    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int rank, bool empty) {
+        const int row = it.row_a + rank * PG_HALF + r;
+        const int s = i / (mt * nt);
+        float *dst = l.acc + (int64_t(s) * l.tokens + row) * l.H + it.row_b;
+        const float f = g.first ? 0.0f : l.factor[row];
+        const int lim = min(PG_TILE, l.H - it.row_b);
+        for (int c = 0; c < lim; c += 32) {
+            uint32_t v[32];
+            if (empty) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0u;
+            } else {
+                tmem_ld32_nowait(tmem + c, v);
+                tmem_wait_ld();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                if (c + j >= lim) break;                       // H is a multiple of 8
+                float4 o = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                       __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                float4 *at = reinterpret_cast<float4 *>(dst + c + j);
+                if (!g.first) {
+                    const float4 was = *at;
+                    o.x = fmaf(was.x, f, o.x);
+                    o.y = fmaf(was.y, f, o.y);
+                    o.z = fmaf(was.z, f, o.z);
+                    o.w = fmaf(was.w, f, o.w);
+                }
+                *at = o;
+            }
+        }
+    };
+    pair_gemm<false, true>(&g.a, &g.b, mt * nt * l.split, l.error_word, item, epilogue);
+}
+
+// dW[v] = sum over tokens of scratch[t][v] h[t]: both operands have their
+// rows contiguous.
+__global__ void __launch_bounds__(PG_THREADS, 1)
+head_grad_kernel(const __grid_constant__ LossGemm g)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const LossArgs &l = g.l;
+    const int mt = (g.cols + PG_TILE - 1) / PG_TILE;
+    const int nt = (l.H + PG_TILE - 1) / PG_TILE;
+    const int kb = (*l.count + PG_BK - 1) / PG_BK;
+    auto item = [&](int i) {
+        return PairItem{(i / nt) * PG_TILE, (i % nt) * PG_TILE, 0, kb};
+    };
+    auto epilogue = [&](int, const PairItem &it, uint32_t tmem, int r, int rank, bool empty) {
+        const int v0 = it.row_a + rank * PG_HALF + r;
+        const int lim = min(PG_TILE, l.H - it.row_b);
+        uint16_t *dst = g.dw + int64_t(g.col0 + v0) * l.H + it.row_b;
+        for (int c = 0; c < lim; c += 32) {
+            uint32_t v[32];
+            if (empty) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0u;
+            } else {
+                tmem_ld32_nowait(tmem + c, v);
+                tmem_wait_ld();
+            }
+            if (v0 >= g.cols) continue;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                if (c + j >= lim) break;
+                uint4 o;
+                o.x = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                o.y = pack_bf16x2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                o.z = pack_bf16x2(__uint_as_float(v[j + 4]), __uint_as_float(v[j + 5]));
+                o.w = pack_bf16x2(__uint_as_float(v[j + 6]), __uint_as_float(v[j + 7]));
+                *reinterpret_cast<uint4 *>(dst + c + j) = o;
+            }
+        }
+    };
+    pair_gemm<true, true>(&g.a, &g.b, mt * nt, l.error_word, item, epilogue);
+}
+
+// ---------------------------------------------------------------- join
+
+struct JoinArgs {
+    LossArgs l;
+    int32_t tiles;       // of the piece
+    int32_t last;        // no piece follows: also the loss and the row factors
+    int32_t store;
+};
+
+// After a piece's logits: one thread per row adds the tiles' sums to the
+// row's and, where a tile fell outside the window, brings the row to a
+// common reference (the block then rescales the row's scratch).
+__global__ void __launch_bounds__(128) join_kernel(const JoinArgs a)
+{
+    __shared__ int s_rows, s_row[128];
+    __shared__ float s_new[128];
+    pdl_wait();
+    pdl_launch_dependents();
+    const LossArgs &l = a.l;
+    if (threadIdx.x == 0) s_rows = 0;
+    __syncthreads();
+    const int row = blockIdx.x * 128 + threadIdx.x;
+    const int n = *l.count;
+    if (row < n) {
+        const float have = float(l.ref[row]);
+        const float old = l.sum[row];
+        float sum = 0.0f, own = -INFINITY;
+        bool off = false, used = old > 0.0f;
+        for (int j = 0; j < a.tiles; ++j) {
+            const float2 s = l.stat[int64_t(j) * l.tokens + row];
+            sum += s.x == have ? s.y : 0.0f;
+            if (s.x == have) used = used || s.y > 0.0f;
+            else {
+                off = true;
+                own = fmaxf(own, s.x);
+            }
+        }
+        float ref = have, f = 1.0f, total = old + sum;
+        if (off) {
+            ref = used ? fmaxf(have, own) : own;
+            f = used ? exp2f(have - ref) : 0.0f;
+            total = used ? total * f : 0.0f;
+            for (int j = 0; j < a.tiles; ++j) {
+                const float2 s = l.stat[int64_t(j) * l.tokens + row];
+                if (s.x != have) total += s.y * exp2f(s.x - ref);
+            }
+            if (a.store) {
+                const int k = atomicAdd(&s_rows, 1);      // order among rows is of no matter
+                s_row[k] = row;
+                s_new[k] = ref;
+            }
+            l.ref[row] = int(ref);
+        }
+        l.sum[row] = total;
+        l.factor[row] = f;
+        if (a.last) {
+            // total: the other columns, in units of 2^ref; d: the target's exponent
+            const float w = l.wt[row], d = l.logit[row] - ref;
+            float lse2, loss, inv, share;
+            if (total == 0.0f) {                  // the target is the only column left
+                lse2 = l.logit[row];
+                loss = inv = share = 0.0f;
+            } else if (d >= 0.0f) {
+                const float back = total * exp2f(-d);           // others relative to the target
+                loss = log1pf(back);
+                lse2 = l.logit[row] + loss * LS_LOG2E;
+                share = back / (1.0f + back);
+                inv = exp2f(-d) / (1.0f + back);
+            } else {
+                const float all = total + exp2f(d);
+                const float lg = log2f(all);
+                loss = (lg - d) * LS_LN2;
+                lse2 = ref + lg;
+                share = total / all;
+                inv = 1.0f / all;
+            }
+            const int t = l.row[row];
+            l.loss[t] = w * loss;
+            if (l.logsumexp != nullptr) l.logsumexp[t] = lse2 * LS_LN2;
+            l.inv[row] = w * inv;
+            l.share[row] = w * share;
+            l.lse[row] = lse2;
+        }
+    } else if (a.last && row < l.tokens) {
+        l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
+    }
+    __syncthreads();
+    for (int k = 0; k < s_rows; ++k) {
+        const int r = s_row[k];
+        for (int j = 0; j < a.tiles; ++j) {
+            const float was = l.stat[int64_t(j) * l.tokens + r].x;
+            if (was == s_new[k]) continue;
+            const float f = exp2f(was - s_new[k]);
+            uint32_t *at = reinterpret_cast<uint32_t *>(l.p + int64_t(r) * l.piece + j * PG_TILE);
+            const uint32_t v = at[threadIdx.x];
+            at[threadIdx.x] = pack_bf16x2(bf16_lo(v) * f, bf16_hi(v) * f);
+        }
+    }
+}
+
+// dh[t] = inv * sum of the partial rows - share * W[y]: the only rounding of
+// dh.  One block per row (a stride of the grid apart).
+__global__ void __launch_bounds__(256) finish_kernel(const LossArgs l)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int n = *l.count;
+    for (int row = blockIdx.x; row < n; row += gridDim.x) {
+        const float inv = l.inv[row], share = l.share[row];
+        const uint16_t *w = l.weight + int64_t(l.target[row]) * l.H;
+        uint16_t *dst = l.dh + int64_t(l.row[row]) * l.dh_ld;
+        for (int c = threadIdx.x * 8; c < l.H; c += 256 * 8) {
+            float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            for (int s = 0; s < l.split; ++s) {
+                const float4 *a = reinterpret_cast<const float4 *>(
+                    l.acc + (int64_t(s) * l.tokens + row) * l.H + c);
+                const float4 x = a[0], y = a[1];
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+            }
+            const uint4 wv = *reinterpret_cast<const uint4 *>(w + c);
+            const uint32_t wr[4] = {wv.x, wv.y, wv.z, wv.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[j] = pack_bf16x2(fmaf(-share, bf16_lo(wr[j]), inv * v[2 * j]),
+                                   fmaf(-share, bf16_hi(wr[j]), inv * v[2 * j + 1]));
+            if (l.dh_vec) {
+                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dst[c + 2 * j] = uint16_t(o[j] & 0xFFFFu);
+                    dst[c + 2 * j + 1] = uint16_t(o[j] >> 16);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+static int prepare_kernels()
+{
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return int(e);
+    if (dev < 64 && configured[dev]) return 0;
+    const void *fns[] = {(const void *)logits_kernel<false>, (const void *)logits_kernel<true>,
+                         (const void *)hidden_grad_kernel, (const void *)head_grad_kernel};
+    for (const void *f : fns) {
+        e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, PG_SMEM);
+        if (e != cudaSuccess) return int(e);
+    }
+    if (dev < 64) configured[dev] = 1;
+    return 0;
+}
+
+// Tensor map of a bf16 matrix: an operand with K contiguous is loaded in
+// boxes of 64 K x 128 rows, one with its rows contiguous in 64 x 64.
+static bool operand_map(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int64_t ld,
+                        bool rows_contiguous)
+{
+    return encode_tile_map(m, ptr, uint64_t(rows), uint64_t(cols), uint64_t(ld), PG_BK,
+                           rows_contiguous ? PG_BK : PG_HALF, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_t st)
+{
+    if (int e = prepare_kernels()) return e;
+    const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    LossGemm logits, dhid, grad, head;
+    logits.l = dhid.l = grad.l = head.l = l;
+    const bool store = l.dh != nullptr;
+    if (!operand_map(&logits.a, l.h, lay.tokens, l.H, l.H, false) ||
+        !operand_map(&logits.b, l.weight, l.V, l.H, l.H, false) ||
+        ((store || dw != nullptr) &&
+         (!operand_map(&dhid.a, l.p, lay.tokens, lay.piece, lay.piece, false) ||
+          !operand_map(&head.a, l.p, lay.tokens, lay.piece, lay.piece, true))) ||
+        !operand_map(&head.b, l.h, lay.tokens, l.H, l.H, true))
+        return LORA_ERR_DEVICE;
+    const int blocks = l.T > 0 ? (l.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
+    cudaError_t e = launch_kernel(pack_kernel, dim3(blocks), dim3(256), 0, st, l);
+    if (e != cudaSuccess) return int(e);
+    for (int i = 0; i < lay.pieces; ++i) {
+        const int32_t col0 = int32_t(i * lay.piece);
+        const int32_t cols = int32_t(lay.piece < l.V - col0 ? lay.piece : l.V - col0);
+        logits.col0 = dhid.col0 = col0;
+        logits.cols = dhid.cols = cols;
+        logits.store = store;
+        e = launch_pair_kernel(logits_kernel<false>, pairs, st, logits);
+        if (e != cudaSuccess) return int(e);
+        JoinArgs j;
+        j.l = l;
+        j.tiles = (cols + PG_TILE - 1) / PG_TILE;
+        j.last = i + 1 == lay.pieces;
+        j.store = store;
+        e = launch_kernel(join_kernel, dim3(unsigned(lay.tokens / 128)), dim3(128), 0, st, j);
+        if (e != cudaSuccess) return int(e);
+        if (store) {
+            dhid.first = i == 0;
+            // W's rows of this piece are the K dimension
+            if (!operand_map(&dhid.b, l.weight + int64_t(col0) * l.H, cols, l.H, l.H, true))
+                return LORA_ERR_DEVICE;
+            e = launch_pair_kernel(hidden_grad_kernel, pairs, st, dhid);
+            if (e != cudaSuccess) return int(e);
+        }
+    }
+    if (store) {
+        const int grid = l.T < 4 * 2 * pairs ? (l.T > 0 ? l.T : 1) : 4 * 2 * pairs;
+        e = launch_kernel(finish_kernel, dim3(grid), dim3(256), 0, st, l);
+        if (e != cudaSuccess) return int(e);
+    }
+    if (dw != nullptr) {
+        grad.a = logits.a;
+        grad.b = logits.b;
+        grad.store = 1;
+        head.dw = dw;
+        for (int i = 0; i < lay.pieces; ++i) {
+            const int32_t col0 = int32_t(i * lay.piece);
+            const int32_t cols = int32_t(lay.piece < l.V - col0 ? lay.piece : l.V - col0);
+            grad.col0 = head.col0 = col0;
+            grad.cols = head.cols = cols;
+            e = launch_pair_kernel(logits_kernel<true>, pairs, st, grad);
+            if (e != cudaSuccess) return int(e);
+            e = launch_pair_kernel(head_grad_kernel, pairs, st, head);
+            if (e != cudaSuccess) return int(e);
+        }
+    }
+    return LORA_OK;
+}
+
+}  // namespace lora
+
+LORA_API int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden, int32_t vocab,
+                                              int32_t hidden_grad, int32_t weight_grad)
+{
+    if (num_tokens < 0 || hidden < 8 || hidden % 8 != 0 || vocab < 1) return LORA_ERR_SIZE;
+    const int pairs = lora::device_sm_count() / 2 > 0 ? lora::device_sm_count() / 2 : 1;
+    return lora::loss_layout(num_tokens, hidden, vocab, hidden_grad != 0, weight_grad != 0, pairs)
+        .bytes;
+}
+
+LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, int32_t hidden_size,
+                                int64_t hidden_ld, const lora_bf16_t *weight, int32_t vocab,
+                                const int32_t *targets, const float *token_weight, float *loss,
+                                float *logsumexp, lora_bf16_t *hidden_grad, int64_t hidden_grad_ld,
+                                lora_bf16_t *weight_grad, int32_t *error_word, void *workspace,
+                                int64_t workspace_bytes, void *stream)
+{
+    using namespace lora;
+    NvtxRange nvtx_range("lora_cross_entropy");
+    if (num_tokens < 0 || hidden_size < 8 || vocab < 1 || hidden_ld < hidden_size ||
+        (hidden_grad != nullptr && hidden_grad_ld < hidden_size))
+        return LORA_ERR_SIZE;
+    if (hidden_size % 8 != 0) return LORA_ERR_ALIGN;
+    if (weight == nullptr || workspace == nullptr ||
+        (num_tokens > 0 && (hidden == nullptr || targets == nullptr || loss == nullptr)))
+        return LORA_ERR_NULL;
+    auto bits = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
+    if ((bits(weight) | bits(weight_grad)) & 15u || bits(workspace) & 255u) return LORA_ERR_ALIGN;
+    const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    const LossLayout lay = loss_layout(num_tokens, hidden_size, vocab, hidden_grad != nullptr,
+                                       weight_grad != nullptr, pairs);
+    if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
+    LossArgs l;
+    l.hidden = hidden;
+    l.hidden_ld = hidden_ld;
+    l.weight = weight;
+    l.targets = targets;
+    l.token_weight = token_weight;
+    l.loss = loss;
+    l.logsumexp = logsumexp;
+    l.dh = hidden_grad;
+    l.dh_ld = hidden_grad_ld;
+    l.T = num_tokens;
+    l.H = hidden_size;
+    l.V = vocab;
+    l.hidden_vec = (bits(hidden) & 15u) == 0 && hidden_ld % 8 == 0;
+    l.dh_vec = (bits(hidden_grad) & 15u) == 0 && hidden_grad_ld % 8 == 0;
+    l.error_word = error_word;
+    char *ws = static_cast<char *>(workspace);
+    l.count = reinterpret_cast<int32_t *>(ws + lay.count);
+    l.row = reinterpret_cast<int32_t *>(ws + lay.row);
+    l.target = reinterpret_cast<int32_t *>(ws + lay.target);
+    l.wt = reinterpret_cast<float *>(ws + lay.weight);
+    l.ref = reinterpret_cast<int32_t *>(ws + lay.ref);
+    l.sum = reinterpret_cast<float *>(ws + lay.sum);
+    l.logit = reinterpret_cast<float *>(ws + lay.logit);
+    l.factor = reinterpret_cast<float *>(ws + lay.factor);
+    l.inv = reinterpret_cast<float *>(ws + lay.inv);
+    l.share = reinterpret_cast<float *>(ws + lay.share);
+    l.lse = reinterpret_cast<float *>(ws + lay.lse);
+    l.stat = reinterpret_cast<float2 *>(ws + lay.stat);
+    l.h = reinterpret_cast<uint16_t *>(ws + lay.h);
+    l.p = reinterpret_cast<uint16_t *>(ws + lay.p);
+    l.acc = reinterpret_cast<float *>(ws + lay.acc);
+    l.tokens = lay.tokens;
+    l.piece = lay.piece;
+    l.split = lay.split;
+    if (num_tokens == 0 && weight_grad == nullptr) {
+        if (error_word == nullptr) return LORA_OK;
+    }
+    return run_loss(l, lay, weight_grad, static_cast<cudaStream_t>(stream));
+}

@@ -70,8 +70,10 @@ enum lora_status {
     LORA_ERR_TOKENS = -6,      /* num_tokens > meta->max_num_tokens         */
     LORA_ERR_WIDTH = -7,       /* offset_start + sum(slice_sizes) > y_ld    */
     LORA_ERR_DEVICE = -8,      /* no usable CUDA device / wrong architecture */
-    LORA_ERR_SCRATCH = -9      /* num_slices * num_tokens * rank exceeds
+    LORA_ERR_SCRATCH = -9,     /* num_slices * num_tokens * rank exceeds
                                   LORA_NOALLOC_MAX_FLOATS (lora_linear_noalloc) */
+    LORA_ERR_WORKSPACE = -10   /* the workspace is smaller than the call's
+                                  *_workspace function says                 */
 };
 
 /*
@@ -314,6 +316,61 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
                         const lora_bf16_t *const *lora_bias, const int32_t *slice_sizes,
                         int32_t num_slices, int32_t rank, float scale, lora_bf16_t *y,
                         int64_t y_ld, const lora_meta_t *meta, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training the adapters: the loss over the vocabulary, the gradients of one
+ * layer's adapters, and the orthogonalised update of stacked adapters.  The
+ * pages have no counterpart (they serve adapters); these are additions.
+ * Every call takes a workspace of at least the bytes that its *_workspace
+ * function returns (device memory, 256-byte aligned, contents of no matter
+ * before and after); calls that may overlap need a workspace each.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * lora_cross_entropy -- softmax cross entropy of the logits hidden x weight^T
+ * and its gradients, without keeping the logits (at most about 2^26 of them,
+ * a piece of the vocabulary, exist at a time, in the workspace):
+ *   loss[t] = w_t (log sum_v exp S[t, v] - S[t, y_t]),  S = hidden weight^T
+ *   hidden_grad[t] = w_t (sum_v p[t, v] weight[v] - weight[y_t])
+ *   weight_grad[v] = sum_t w_t (p[t, v] - (v == y_t)) hidden[t]
+ *
+ *   hidden       device bf16 [num_tokens, hidden_ld]; the first hidden_size
+ *                values of each row are used.  Any alignment.
+ *   hidden_size  a multiple of 8.
+ *   weight       device bf16 [vocab, hidden_size], dense, 16-byte aligned.
+ *   targets      device int32 [num_tokens].  A token whose target lies
+ *                outside [0, vocab) has none: its loss, log-sum and gradient
+ *                are zero, its row of hidden is not read, and it costs no
+ *                products.
+ *   token_weight NULL (all ones) or device fp32 [num_tokens]: w_t (a mean
+ *                over an adapter's tokens, a loss scale).
+ *   loss         device fp32 [num_tokens].
+ *   logsumexp    NULL or device fp32 [num_tokens]: log sum_v exp S[t, v].
+ *   hidden_grad  NULL or device bf16 [num_tokens, hidden_grad_ld], written.
+ *   weight_grad  NULL or device bf16 [vocab, hidden_size], dense, 16-byte
+ *                aligned, written.
+ *   error_word   NULL or device int32 [1]: receives the number of targets
+ *                >= vocab; bit 30 is set if a bounded wait ran out (the
+ *                outputs are then not valid).
+ *
+ * Products run on the tensor cores (tcgen05) in bf16 with fp32 sums; the
+ * softmax's terms are rounded to bf16 once for the gradient products,
+ * its sums and the accumulated gradients are fp32, and each gradient is
+ * rounded to bf16 once.  Deterministic.  Errors: LORA_ERR_NULL,
+ * LORA_ERR_SIZE, LORA_ERR_ALIGN (weight, weight_grad, workspace,
+ * hidden_size), LORA_ERR_WORKSPACE, LORA_ERR_DEVICE.
+ */
+int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, int32_t hidden_size,
+                       int64_t hidden_ld, const lora_bf16_t *weight, int32_t vocab,
+                       const int32_t *targets, const float *token_weight, float *loss,
+                       float *logsumexp, lora_bf16_t *hidden_grad, int64_t hidden_grad_ld,
+                       lora_bf16_t *weight_grad, int32_t *error_word, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_cross_entropy on the current device, by whether
+ * the gradients are asked for; LORA_ERR_SIZE for sizes that it refuses. */
+int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden_size, int32_t vocab,
+                                     int32_t hidden_grad, int32_t weight_grad);
 
 /*
  * lora_reload_options -- re-reads the library's tuning variables
