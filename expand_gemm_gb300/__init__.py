@@ -20,6 +20,7 @@ Names follow vLLM's API pages:
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -31,6 +32,7 @@ from ._lib import (LoraError, LORA_MAX_LORAS, LORA_MAX_RANK, LORA_MAX_SLICES,  #
 __all__ = ["LoRAKernelMeta", "lora_meta_prepare", "lora_shrink", "lora_expand",
            "lora_linear", "lora_linear_noalloc", "add_lora_linear", "add_lora_embedding",
            "add_lora_logits", "lora_cross_entropy", "lora_cross_entropy_workspace",
+           "lora_orthogonalize", "lora_orthogonalize_workspace",
            "reload_options", "LoraError", "library", "build"]
 
 
@@ -498,3 +500,45 @@ def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
           l_ptr, s_ptr, None if dh is None else dh.data_ptr(), H if dh is None else _ld(dh),
           None if weight_grad is None else weight_grad.data_ptr(), e_ptr, ws.data_ptr(), ws.numel(),
           _stream_handle(dev))
+
+
+def _stack(t: torch.Tensor, name: str):
+    """(count, rows, cols) of a dense stack of matrices (any leading dimensions)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() < 2 or not t.is_contiguous():
+        raise ValueError("%s must be contiguous [..., rows, cols]" % name)
+    rows, cols = t.shape[-2:]
+    return t.numel() // max(1, rows * cols), rows, cols
+
+
+def lora_orthogonalize_workspace(count: int, rows: int, cols: int, *, device="cuda") -> int:
+    """Bytes of workspace of :func:`lora_orthogonalize` at these sizes."""
+    return _workspace_bytes("lora_orthogonalize_workspace", device, count, rows, cols)
+
+
+def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 5,
+                       scale: float = 1.0, eps: float = 1e-7,
+                       coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                       workspace: Optional[torch.Tensor] = None) -> None:
+    """Newton-Schulz orthogonalisation of stacked updates, as the Muon
+    optimiser takes them: every matrix of update [..., rows, cols] (bf16 or
+    fp32; the shorter side, an adapter's rank, at most 128) divided by its
+    norm and taken through ``steps`` of X <- a X + (b G + c G^2) X, G = X X^T;
+    out (bf16, like update, or update itself) receives scale * X."""
+    count, rows, cols = _stack(update, "update")
+    if update.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("update must be bfloat16 or float32, got %s" % update.dtype)
+    _need(update, "update", update.dtype)
+    _need(out, "out", torch.bfloat16)
+    if out.shape != update.shape or not out.is_contiguous():
+        raise ValueError("out must be contiguous like update")
+    if len(coefficients) != 3:
+        raise ValueError("coefficients must be three numbers")
+    _same_gpu(update, [("out", out), ("workspace", workspace)])
+    dev = update.device
+    ws = _workspace(workspace, lora_orthogonalize_workspace(count, rows, cols, device=dev), dev)
+    a, b, c = (float(v) for v in coefficients)
+    _call("lora_orthogonalize", dev, update.data_ptr(), int(update.dtype == torch.float32), count,
+          rows, cols, int(steps), a, b, c, float(eps), float(scale), out.data_ptr(), ws.data_ptr(),
+          ws.numel(), _stream_handle(dev))

@@ -373,6 +373,39 @@ int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden_size, in
                                      int32_t hidden_grad, int32_t weight_grad);
 
 /*
+ * lora_orthogonalize -- Newton-Schulz steps on `count` stacked matrices, as
+ * the Muon optimiser takes them on an update: for each matrix
+ *   X = U / (|U|_F + eps);  steps times: X <- a X + (b G + c G^2) X, G = X X^T
+ * (on the short side), out = scale X.  With a = 3.4445, b = -4.7750,
+ * c = 2.0315 and five steps the singular values that U has end near 1.
+ *
+ *   update       device [count, rows, cols], dense, 16-byte aligned: bf16
+ *                (update_f32 == 0) or fp32.  Stacked adapter gradients or
+ *                momenta: A [.., rank, hidden], B [.., n, rank].
+ *   count        at most 65535.
+ *   rows, cols   min(rows, cols) <= 128 (an adapter's rank), cols a
+ *                multiple of 8.
+ *   steps        >= 1.
+ *   out          device bf16 [count, rows, cols], dense, 16-byte aligned;
+ *                may be `update` itself where that is bf16.
+ *
+ * A zero matrix gives zeros; a matrix with a NaN or an infinity gives NaN in
+ * its own place only.  |U|_F^2 and the products U U^T are summed in fp32 and
+ * must be finite there (entries up to about 1e17).  The steps run on
+ * r x r matrices in fp32 (every factor is a polynomial in U U^T); `out` is
+ * rounded to bf16 once.  Deterministic.  Errors: LORA_ERR_NULL,
+ * LORA_ERR_SIZE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE.
+ */
+int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, int32_t rows,
+                       int32_t cols, int32_t steps, float coef_a, float coef_b, float coef_c,
+                       float eps, float scale, lora_bf16_t *out, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_orthogonalize on the current device;
+ * LORA_ERR_SIZE for sizes that it refuses. */
+int64_t lora_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols);
+
+/*
  * lora_reload_options -- re-reads the library's tuning variables
  * (LORA_PUNICA_*: which of lora_linear's launch paths a batch takes, which
  * batches the tensor-core kernels take, programmatic dependent launch).
