@@ -32,6 +32,7 @@ from ._lib import (LoraError, LORA_MAX_LORAS, LORA_MAX_RANK, LORA_MAX_SLICES,  #
 __all__ = ["LoRAKernelMeta", "lora_meta_prepare", "lora_shrink", "lora_expand",
            "lora_linear", "lora_linear_noalloc", "add_lora_linear", "add_lora_embedding",
            "add_lora_logits", "lora_cross_entropy", "lora_cross_entropy_workspace",
+           "lora_linear_backward", "lora_linear_backward_workspace",
            "lora_orthogonalize", "lora_orthogonalize_workspace",
            "reload_options", "LoraError", "library", "build"]
 
@@ -499,6 +500,86 @@ def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
     _call("lora_cross_entropy", dev, h.data_ptr(), T, H, _ld(h), weight.data_ptr(), V, t_ptr, w_ptr,
           l_ptr, s_ptr, None if dh is None else dh.data_ptr(), H if dh is None else _ld(dh),
           None if weight_grad is None else weight_grad.data_ptr(), e_ptr, ws.data_ptr(), ws.numel(),
+          _stream_handle(dev))
+
+
+def lora_linear_backward_workspace(num_tokens: int, hidden: int, output_slices, rank: int,
+                                   max_loras: int, *, device="cuda") -> int:
+    """Bytes of workspace of :func:`lora_linear_backward` at these sizes."""
+    sizes = (ctypes.c_int32 * len(output_slices))(*output_slices)
+    return _workspace_bytes("lora_linear_backward_workspace", device, num_tokens, hidden, sizes,
+                            len(output_slices), rank, max_loras)
+
+
+def _grad_array(grads, name: str, like):
+    """Pointer array of the gradients `grads` (None, or one tensor or None
+    per slice), each shaped as the entry of `like`; and the tensors."""
+    if grads is None:
+        return None, []
+    if isinstance(grads, torch.Tensor):
+        grads = (grads,)
+    if len(grads) != len(like):
+        raise ValueError("%s needs one entry per slice" % name)
+    for i, (g, shape) in enumerate(zip(grads, like)):
+        if g is None:
+            continue
+        _need(g, "%s[%d]" % (name, i), torch.bfloat16)
+        if g.numel() != math.prod(shape) or g.shape[0] != shape[0] or g.shape[-1] != shape[-1] \
+                or not g.is_contiguous():
+            raise ValueError("%s[%d] must be a contiguous %s tensor" % (name, i, list(shape)))
+    return _ptr_array(grads), [("%s[%d]" % (name, i), g) for i, g in enumerate(grads)]
+
+
+def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor, lora_a_stacked,
+                         lora_b_stacked, scale: float, meta: LoRAKernelMeta, *,
+                         dx: Optional[torch.Tensor] = None, add_inputs: bool = True,
+                         d_lora_a=None, d_lora_b=None, d_lora_bias=None,
+                         workspace: Optional[torch.Tensor] = None) -> None:
+    """Gradients of one layer that add_lora_linear (or lora_linear) ran:
+    dy is the gradient of its output [T, sum of the slices], x its input,
+    buffer the fp32 buffer it left, meta the batch's metadata.
+
+    Each output is optional and bf16.  dx [T, H]: the adapters' part is added
+    to it, or with add_inputs=False it is overwritten.  d_lora_a, d_lora_b,
+    d_lora_bias: one tensor (or None) per slice, shaped as the weights and
+    biases, overwritten; adapters without tokens get zeros."""
+    dy2, x2 = _rows(dy, "dy", torch.bfloat16), _rows(x, "x", torch.bfloat16)
+    A = _weights(lora_a_stacked, "lora_a_stacked")
+    B = _weights(lora_b_stacked, "lora_b_stacked")
+    if len(A) != len(B):
+        raise ValueError("lora_a_stacked and lora_b_stacked differ in length")
+    T, H = x2.shape
+    S, (L, r, _) = len(A), A[0].shape
+    if any(a.shape != (L, r, H) for a in A):
+        raise ValueError("lora_a_stacked shapes must all be [%d, %d, %d]" % (L, r, H))
+    if any(b.size(0) != L or b.size(2) != r for b in B):
+        raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (L, r))
+    if L != meta.max_loras:
+        raise ValueError("the weights hold %d LoRAs, the metadata %d" % (L, meta.max_loras))
+    sizes = [b.size(1) for b in B]
+    if dy2.size(0) != T or dy2.size(1) != sum(sizes):
+        raise ValueError("dy must be [%d, %d]" % (T, sum(sizes)))
+    _need(buffer, "buffer", torch.float32)
+    if tuple(buffer.shape) != (S, T, r) or not buffer.is_contiguous():
+        raise ValueError("buffer must be a contiguous fp32 [%d, %d, %d] tensor" % (S, T, r))
+    dx2 = None
+    if dx is not None:
+        dx2 = _rows(dx, "dx", torch.bfloat16)
+        if dx2.shape != x2.shape:
+            raise ValueError("dx must be [%d, %d]" % (T, H))
+    da, named_a = _grad_array(d_lora_a, "d_lora_a", [tuple(a.shape) for a in A])
+    db, named_b = _grad_array(d_lora_b, "d_lora_b", [tuple(b.shape) for b in B])
+    dbias, named_c = _grad_array(d_lora_bias, "d_lora_bias", [(L, n) for n in sizes])
+    _same_device(meta, [("dy", dy), ("x", x), ("buffer", buffer), ("dx", dx),
+                        ("workspace", workspace)] + named_a + named_b + named_c +
+                 [("lora_a_stacked[%d]" % i, a) for i, a in enumerate(A)] +
+                 [("lora_b_stacked[%d]" % i, b) for i, b in enumerate(B)])
+    dev = x.device
+    ws = _workspace(workspace, lora_linear_backward_workspace(T, H, sizes, r, L, device=dev), dev)
+    _call("lora_linear_backward", dev, dy2.data_ptr(), _ld(dy2), T, x2.data_ptr(), H, _ld(x2),
+          buffer.data_ptr(), _ptr_array(A), _ptr_array(B), (ctypes.c_int32 * S)(*sizes), S, r,
+          float(scale), None if dx2 is None else dx2.data_ptr(), H if dx2 is None else _ld(dx2),
+          1 if add_inputs else 0, da, db, dbias, ctypes.byref(meta.c), ws.data_ptr(), ws.numel(),
           _stream_handle(dev))
 
 

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(PKG, "liblora_punica.so")
 EXPORTS = ("lora_meta_prepare", "lora_meta_read_no_lora", "lora_shrink", "lora_expand",
            "lora_expand_bf16", "lora_linear", "lora_linear_noalloc",
            "lora_cross_entropy", "lora_cross_entropy_workspace", "lora_orthogonalize",
-           "lora_orthogonalize_workspace", "lora_reload_options",
+           "lora_linear_backward", "lora_linear_backward_workspace", "lora_orthogonalize_workspace", "lora_reload_options",
            "lora_status_string", "lora_version")
 
 LORA_MAX_SLICES = 8
@@ -95,6 +95,12 @@ def load(path: str | None = None):
         lib.lora_cross_entropy_workspace.argtypes = [_I32, _I32, _I32, _I32, _I32]
         lib.lora_cross_entropy_workspace.restype = _I64
         _F = ctypes.c_float
+        lib.lora_linear_backward.argtypes = [_P, _I64, _I32, _P, _I32, _I64, _P, _P, _P, _P, _I32,
+                                             _I32, _F, _P, _I64, _I32, _P, _P, _P,
+                                             ctypes.POINTER(LoraMetaC), _P, _I64, _P]
+        lib.lora_linear_backward.restype = ctypes.c_int
+        lib.lora_linear_backward_workspace.argtypes = [_I32, _I32, _P, _I32, _I32, _I32]
+        lib.lora_linear_backward_workspace.restype = _I64
         lib.lora_orthogonalize.argtypes = [_P, _I32, _I32, _I32, _I32, _I32, _F, _F, _F, _F, _F,
                                            _P, _P, _I64, _P]
         lib.lora_orthogonalize.restype = ctypes.c_int

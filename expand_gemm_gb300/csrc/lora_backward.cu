@@ -1,0 +1,705 @@
+// lora_backward.cu -- the gradients of a linear layer's adapters, for a
+// batch whose tokens use many adapters:
+//   forward   u_t = scale A_a x_t (the fp32 buffer),  y_t += B_a u_t + bias_a
+//   g_t = B_a^T dy_t                  dx_t (+)= scale sum_s A_a^T g_t
+//   dB_a = sum_t dy_t u_t^T           dA_a = scale sum_t g_t x_t^T
+//   dbias_a = sum_t dy_t              (a = id(t); -1: nothing)
+//
+// Tokens are taken in the metadata's order (sorted by adapter), in tiles of
+// 64 tokens of one adapter.  Three kernels:
+//   grad_u_kernel  g of a tile, and u, rounded to bf16 for the products
+//                  that follow and laid out by tile with the rows behind an
+//                  adapter's last token zero (the products over tokens then
+//                  need no masks on them);
+//   grad_x_kernel  dx of a tile x 128 hidden columns, all slices summed;
+//   grad_w_kernel  dB and dA of an adapter x 128 columns, summed over the
+//                  adapter's tokens in a fixed order (no atomics).
+// g and u in bf16 cost a relative 2^-9 a term, like the rounding of the
+// outputs; all sums are fp32.
+#include "lora_frag.cuh"
+
+namespace lora {
+
+constexpr int BW_THREADS = 256;
+constexpr int BW_TOK = 64;                 // tokens of a tile
+constexpr int BW_COLS = 128;               // columns of a tile of dx, dA, dB
+constexpr int BW_MAX_CLUSTER = 8;
+
+struct BackwardArgs {
+    const uint16_t *dy, *x;
+    int64_t dy_ld, x_ld;
+    const float *buf;
+    const uint16_t *a[LORA_MAX_SLICES], *b[LORA_MAX_SLICES];
+    uint16_t *da[LORA_MAX_SLICES], *db[LORA_MAX_SLICES], *dbias[LORA_MAX_SLICES];
+    uint16_t *dx;
+    int64_t dx_ld;
+    int32_t n[LORA_MAX_SLICES], off[LORA_MAX_SLICES];      // widths, first columns in dy
+    // grad_w_kernel's column blocks of one adapter: dB of slice s ends
+    // before block_end[s], dA of slice s before block_end[S + s]
+    int32_t block_end[2 * LORA_MAX_SLICES];
+    int32_t T, H, S, r, L, width;
+    int32_t add, dy_vec, x_vec, dx_vec;
+    float scale;
+    uint16_t *g, *u;                       // [S][rows][RP]
+    int64_t rows;
+    const int32_t *sorted, *counts, *start_loc, *active, *no_lora;
+    int32_t *error_word;
+    int32_t nbins;
+};
+
+// Eight elements of a row from column c; columns outside [lo, hi) give zero
+// and are not read.
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int lo, int hi, bool vec)
+{
+    if (vec && c >= lo && c + 8 <= hi) return *reinterpret_cast<const uint4 *>(row + c);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (c + j >= lo && c + j < hi) w[j >> 1] |= uint32_t(row[c + j]) << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ SegTab load_tab(const BackwardArgs &p, int *mem, int &tiles)
+{
+    const SegTab tab = seg_tab(mem, p.nbins);
+    tiles = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, BW_TOK, tab, false, 0,
+                          p.T, p.error_word);
+    return tab;
+}
+
+// ---------------------------------------------------------------- g and u
+
+template <int RP> struct UShape { static constexpr int WM = 4, WN = RP >= 64 ? 2 : 1, WK = RP >= 64 ? 1 : 2; };
+
+template <int RP>
+constexpr int grad_u_smem() { return 2 * (BW_TOK * 64 * 2 + 64 * RP * 2) + UShape<RP>::WK * BW_TOK * RP * 4; }
+
+// Item: (tile, slice), worked on by a cluster whose CTAs take a share of the
+// slice's columns each; their partial sums are joined through distributed
+// shared memory in the order of the CTAs.
+template <int RP>
+__global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constant__ BackwardArgs p)
+{
+    constexpr int WM = UShape<RP>::WM, WN = UShape<RP>::WN, WK = UShape<RP>::WK;
+    constexpr int NI = RP / WN / 8, CPR = RP / 8;
+    constexpr int SD = BW_TOK * 64 * 2, SB = 64 * RP * 2;
+    constexpr int PB = (64 * CPR + BW_THREADS - 1) / BW_THREADS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *part = reinterpret_cast<float *>(smem + 2 * (SD + SB));
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wm = warp % WM, wn = warp / WM % WN, wk = warp / (WM * WN);
+    uint32_t rank, csize;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+    pdl_wait();
+    pdl_launch_dependents();
+    int tiles;
+    const SegTab tab = load_tab(p, reinterpret_cast<int *>(part + WK * BW_TOK * RP), tiles);
+    const int clusters = int(gridDim.x / csize), cluster = int(blockIdx.x / csize);
+
+    for (int item = cluster; item < tiles * p.S; item += clusters) {
+        const int tile = item / p.S, s = item % p.S;
+        const int seg = find_segment(tab.tile, p.nbins, tile);
+        const int id = tab.id[seg];
+        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
+        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
+        const int lo = p.off[s], hi = lo + p.n[s];
+        const int c0 = p.dy_vec ? lo & ~7 : lo;            // first column of the first step
+        const int steps = (hi - c0 + 63) / 64;
+        const int per = (steps + int(csize) - 1) / int(csize);
+        const int k_lo = min(steps, int(rank) * per), k_hi = min(steps, k_lo + per);
+        const uint16_t *bw = p.b[s] + int64_t(id) * p.n[s] * p.r;
+        const uint16_t *src[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = (tid + i * BW_THREADS) >> 3;
+            const int tok = row < nrows ? checked_token(p.sorted[row0 + row], p.T, p.error_word) : -1;
+            src[i] = tok >= 0 ? p.dy + int64_t(tok) * p.dy_ld : nullptr;
+        }
+        uint4 nd[2], nb[PB];
+        auto fetch = [&](int k) {
+            const int col = c0 + k * 64;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                nd[i] = src[i] != nullptr ? load8(src[i], col + (tid & 7) * 8, lo, hi, p.dy_vec)
+                                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int c = tid + i * BW_THREADS, row = col + c / CPR - lo, ch = c % CPR;
+                nb[i] = make_uint4(0, 0, 0, 0);
+                if (row >= 0 && row < hi - lo && ch * 8 < p.r && c < 64 * CPR)
+                    nb[i] = *reinterpret_cast<const uint4 *>(bw + int64_t(row) * p.r + ch * 8);
+            }
+        };
+        float acc[NI][4] = {};
+        if (k_lo < k_hi) fetch(k_lo);
+        int bufi = 0;
+        for (int k = k_lo; k < k_hi; ++k) {
+            uint8_t *at = smem + bufi * (SD + SB);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = tid + i * BW_THREADS;
+                *reinterpret_cast<uint4 *>(at + tile_at<8, BW_TOK>(c >> 3, c & 7)) = nd[i];
+            }
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                const int c = tid + i * BW_THREADS;
+                if (c < 64 * CPR)
+                    *reinterpret_cast<uint4 *>(at + SD + tile_at<CPR, 64>(c / CPR, c % CPR)) = nb[i];
+            }
+            __syncthreads();
+            if (k + 1 < k_hi) fetch(k + 1);
+            const uint32_t sd = base + bufi * (SD + SB), sb = sd + SD;
+#pragma unroll
+            for (int kk = wk * (64 / WK); kk < (wk + 1) * (64 / WK); kk += 16) {
+                uint32_t a[4];
+                frag_a<8, BW_TOK, true>(sd, wm * 16, kk, a);
+#pragma unroll
+                for (int j = 0; j < NI; j += 2) {
+                    uint32_t b[4];
+                    frag_b<CPR, 64, false>(sb, kk, wn * (RP / WN) + 8 * j, b);
+                    mma_bf16_16816(acc[j], a, b[0], b[1]);
+                    mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
+                }
+            }
+            bufi ^= 1;
+        }
+        const int gq = lane >> 2, t = lane & 3;
+        float *mine = part + wk * BW_TOK * RP;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            float *at = mine + (wm * 16 + gq) * RP + wn * (RP / WN) + 8 * j + 2 * t;
+            *reinterpret_cast<float2 *>(at) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2 *>(at + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+        // this CTA's share of the tile's rows: sums, rounding, and u
+        const int64_t out0 = (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+        const int share = BW_TOK * RP / int(csize) / 4;          // float4s
+        for (int i = tid; i < share; i += BW_THREADS) {
+            const int e = (int(rank) * share + i) * 4, row = e / RP, col = e % RP;
+            float4 v = make_float4(0, 0, 0, 0);
+            for (uint32_t q = 0; q < csize; ++q)
+                for (int w = 0; w < WK; ++w) {
+                    uint32_t ra;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra)
+                        : "r"(smem_addr(part + w * BW_TOK * RP + e)), "r"(q));
+                    float4 x;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(ra));
+                    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+                }
+            *reinterpret_cast<uint2 *>(p.g + out0 + e) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            float4 f = make_float4(0, 0, 0, 0);
+            if (row < nrows && col < p.r) {
+                const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
+                if (tok >= 0)
+                    f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
+            }
+            *reinterpret_cast<uint2 *>(p.u + out0 + e) =
+                make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------------- dx
+
+template <int RP>
+constexpr int grad_x_smem()
+{
+    return BW_TOK * RP * 2 + RP * BW_COLS * 2;
+}
+
+template <int RP>
+__global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constant__ BackwardArgs p)
+{
+    constexpr int CPR = RP / 8;
+    constexpr int SG = BW_TOK * RP * 2;
+    constexpr int PG = (BW_TOK * CPR + BW_THREADS - 1) / BW_THREADS, PA = RP * 16 / BW_THREADS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int m0 = warp % 4 * 16, n0 = warp / 4 * 64;          // 16 tokens x 64 columns a warp
+    pdl_wait();
+    pdl_launch_dependents();
+    int tiles;
+    const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + grad_x_smem<RP>()), tiles);
+    const int hb = (p.H + BW_COLS - 1) / BW_COLS;
+    for (int64_t item = blockIdx.x; item < int64_t(tiles) * hb; item += gridDim.x) {
+        const int tile = int(item / hb), h0 = int(item % hb) * BW_COLS;
+        const int seg = find_segment(tab.tile, p.nbins, tile);
+        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
+        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
+        float acc[8][4] = {};
+        for (int s = 0; s < p.S; ++s) {
+            const uint16_t *gt = p.g + (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+            const uint16_t *aw = p.a[s] + int64_t(tab.id[seg]) * p.r * p.H;
+            uint4 ng[PG], na[PA];
+#pragma unroll
+            for (int i = 0; i < PG; ++i) {
+                const int c = tid + i * BW_THREADS;
+                if (c < BW_TOK * CPR) ng[i] = reinterpret_cast<const uint4 *>(gt)[c];
+            }
+#pragma unroll
+            for (int i = 0; i < PA; ++i) {
+                const int c = tid + i * BW_THREADS, row = c >> 4, col = h0 + (c & 15) * 8;
+                na[i] = make_uint4(0, 0, 0, 0);
+                if (row < p.r && col < p.H)
+                    na[i] = *reinterpret_cast<const uint4 *>(aw + int64_t(row) * p.H + col);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PG; ++i) {
+                const int c = tid + i * BW_THREADS;
+                if (c < BW_TOK * CPR)
+                    *reinterpret_cast<uint4 *>(smem + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)) = ng[i];
+            }
+#pragma unroll
+            for (int i = 0; i < PA; ++i) {
+                const int c = tid + i * BW_THREADS;
+                *reinterpret_cast<uint4 *>(smem + SG + tile_at<16, RP>(c >> 4, c & 15)) = na[i];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int kk = 0; kk < RP; kk += 16) {
+                uint32_t a[4];
+                frag_a<CPR, BW_TOK, true>(base, m0, kk, a);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    uint32_t b[4];
+                    frag_b<16, RP, false>(base + SG, kk, n0 + 8 * j, b);
+                    mma_bf16_16816(acc[j], a, b[0], b[1]);
+                    mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
+                }
+            }
+        }
+        // rows m0 + lane / 4 (+ 8), column pairs n0 + 8 j + 2 (lane % 4)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = m0 + (lane >> 2) + 8 * half;
+            if (row >= nrows) continue;
+            const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
+            if (tok < 0) continue;
+            uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = h0 + n0 + 8 * j + 2 * (lane & 3);
+                if (col >= p.H) continue;                    // H is even
+                float v0 = p.scale * acc[j][2 * half], v1 = p.scale * acc[j][2 * half + 1];
+                if (p.dx_vec) {
+                    uint32_t *at = reinterpret_cast<uint32_t *>(dst + col);
+                    if (p.add) {
+                        const uint32_t was = *at;
+                        v0 += bf16_lo(was);
+                        v1 += bf16_hi(was);
+                    }
+                    *at = pack_bf16x2(v0, v1);
+                } else {
+                    if (p.add) {
+                        v0 += bf16_to_f32(dst[col]);
+                        v1 += bf16_to_f32(dst[col + 1]);
+                    }
+                    const uint32_t w = pack_bf16x2(v0, v1);
+                    dst[col] = uint16_t(w & 0xFFFFu);
+                    dst[col + 1] = uint16_t(w >> 16);
+                }
+            }
+        }
+    }
+    if (p.add) return;
+    // tokens without an adapter: the metadata's first segment, or every
+    // token when the batch has no adapter at all (the order is then unset)
+    const bool none = *p.no_lora != 0;
+    const int rest = none ? p.T : (tab.id[0] == -1 ? tab.count[0] : 0);
+    for (int i = blockIdx.x * 8 + warp; i < rest; i += gridDim.x * 8) {
+        const int tok = none ? i : checked_token(p.sorted[i], p.T, p.error_word);
+        if (tok < 0) continue;
+        uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
+        for (int c = lane * 2; c < p.H; c += 64) {
+            if (p.dx_vec) {
+                *reinterpret_cast<uint32_t *>(dst + c) = 0u;
+            } else {
+                dst[c] = 0;
+                dst[c + 1] = 0;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- dA, dB, dbias
+
+template <int RP> struct WShape { static constexpr int WM = 4, WN = RP >= 32 ? 2 : 1, WK = RP >= 32 ? 1 : 2; };
+
+template <int RP>
+constexpr int grad_w_smem()
+{
+    constexpr int in = 2 * (BW_TOK * BW_COLS * 2 + BW_TOK * RP * 2);
+    constexpr int join = WShape<RP>::WK * BW_COLS * (RP + 1) * 4;
+    return in > join ? in : join;
+}
+
+// Item: (adapter, column block): D[128 columns x RP] = sum over the
+// adapter's tokens of dy^T u (dB) or x^T g (dA).
+template <int RP>
+__global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constant__ BackwardArgs p)
+{
+    constexpr int WM = WShape<RP>::WM, WN = WShape<RP>::WN, WK = WShape<RP>::WK;
+    constexpr int NI = RP / WN / 8, CPR = RP / 8;
+    constexpr int SZ = BW_TOK * BW_COLS * 2, SV = BW_TOK * RP * 2;
+    constexpr int PV = (BW_TOK * CPR + BW_THREADS - 1) / BW_THREADS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wm = warp % WM, wn = warp / WM % WN, wk = warp / (WM * WN);
+    pdl_wait();
+    pdl_launch_dependents();
+    int tiles;
+    int *mem = reinterpret_cast<int *>(smem + grad_w_smem<RP>());
+    const SegTab tab = load_tab(p, mem, tiles);
+    int *seg_of = mem + 4 * p.nbins + 2;
+    for (int i = tid; i < p.L; i += BW_THREADS) seg_of[i] = -1;
+    __syncthreads();
+    if (tiles > 0)
+        for (int k = tid; k < p.nbins; k += BW_THREADS)
+            if (tab.id[k] >= 0 && tab.count[k] > 0) seg_of[tab.id[k]] = k;
+    __syncthreads();
+    const int blocks = p.block_end[2 * p.S - 1];
+    for (int64_t item = blockIdx.x; item < int64_t(p.L) * blocks; item += gridDim.x) {
+        const int id = int(item / blocks), blk = int(item % blocks);
+        int q = 0;                                  // product: dB of slice q, or dA of slice q - S
+        while (blk >= p.block_end[q]) ++q;
+        const bool is_a = q >= p.S;
+        const int s = is_a ? q - p.S : q;
+        const int j0 = blk - (q > 0 ? p.block_end[q - 1] : 0);
+        const int lo = is_a ? 0 : p.off[s], n = is_a ? p.H : p.n[s];
+        const bool vec = is_a ? p.x_vec : p.dy_vec;
+        const int c0 = (vec ? lo & ~7 : lo) + j0 * BW_COLS;      // first column of the block
+        const int width = is_a ? p.H : p.width;                  // readable columns
+        const uint16_t *zsrc = is_a ? p.x : p.dy;
+        const int64_t zld = is_a ? p.x_ld : p.dy_ld;
+        const int seg = seg_of[id];
+        const int start = seg >= 0 ? tab.start[seg] : 0, count = seg >= 0 ? tab.count[seg] : 0;
+        const uint16_t *v = (is_a ? p.g : p.u) +
+                            (int64_t(s) * p.rows + (seg >= 0 ? int64_t(tab.tile[seg]) * BW_TOK : 0)) * RP;
+        uint16_t *dbias = is_a ? nullptr : p.dbias[s];
+        float acc[2][NI][4] = {}, ones[2][4] = {};
+        uint4 nz[4], nv[PV];
+        auto fetch = [&](int k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = k * BW_TOK + (tid >> 4) + i * 16;
+                nz[i] = make_uint4(0, 0, 0, 0);
+                if (row < count) {
+                    const int tok = checked_token(p.sorted[start + row], p.T, p.error_word);
+                    if (tok >= 0) nz[i] = load8(zsrc + tok * zld, c0 + (tid & 15) * 8, 0, width, vec);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < PV; ++i) {
+                const int c = tid + i * BW_THREADS;
+                if (c < BW_TOK * CPR)
+                    nv[i] = reinterpret_cast<const uint4 *>(v + int64_t(k) * BW_TOK * RP)[c];
+            }
+        };
+        const int steps = (count + BW_TOK - 1) / BW_TOK;
+        if (steps > 0) fetch(0);
+        int bufi = 0;
+        for (int k = 0; k < steps; ++k) {
+            uint8_t *at = smem + bufi * (SZ + SV);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4 *>(at + tile_at<16, BW_TOK>((tid >> 4) + i * 16, tid & 15)) = nz[i];
+#pragma unroll
+            for (int i = 0; i < PV; ++i) {
+                const int c = tid + i * BW_THREADS;
+                if (c < BW_TOK * CPR)
+                    *reinterpret_cast<uint4 *>(at + SZ + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)) = nv[i];
+            }
+            __syncthreads();
+            if (k + 1 < steps) fetch(k + 1);
+            const uint32_t sz = base + bufi * (SZ + SV), sv = sz + SZ;
+#pragma unroll
+            for (int kk = wk * (BW_TOK / WK); kk < (wk + 1) * (BW_TOK / WK); kk += 16) {
+                uint32_t a[2][4];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) frag_a<16, BW_TOK, false>(sz, wm * 32 + i * 16, kk, a[i]);
+#pragma unroll
+                for (int j = 0; j < NI; j += 2) {
+                    uint32_t b[4];
+                    frag_b<CPR, BW_TOK, false>(sv, kk, wn * (RP / WN) + 8 * j, b);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
+                        mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
+                    }
+                }
+                if (dbias != nullptr && wn == 0) {
+                    // a product with ones: column 0 of the result
+                    const uint32_t one = lane < 4 ? 0x3F803F80u : 0u;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mma_bf16_16816(ones[i], a[i], one, one);
+                }
+            }
+            bufi ^= 1;
+        }
+        // through shared memory (rows padded by one float), then out
+        __syncthreads();
+        float *stage = reinterpret_cast<float *>(smem);
+        constexpr int LD = RP + 1;
+        const int gq = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                float *at = stage + (wk * BW_COLS + wm * 32 + i * 16 + gq) * LD + wn * (RP / WN) + 8 * j + 2 * t;
+                at[0] = acc[i][j][0];
+                at[1] = acc[i][j][1];
+                at[8 * LD] = acc[i][j][2];
+                at[8 * LD + 1] = acc[i][j][3];
+            }
+        __syncthreads();
+        auto value = [&](int m, int c) {
+            float f = stage[m * LD + c];
+            if constexpr (WK > 1) f += stage[(BW_COLS + m) * LD + c];
+            return f;
+        };
+        if (!is_a) {
+            uint16_t *out = p.db[s];
+            if (out != nullptr) {
+                for (int i = tid; i < BW_COLS * CPR; i += BW_THREADS) {
+                    const int m = i / CPR, c = i % CPR * 8, row = c0 + m - lo;
+                    if (row < 0 || row >= n || c >= p.r) continue;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(value(m, c + 2 * e), value(m, c + 2 * e + 1));
+                    *reinterpret_cast<uint4 *>(out + (int64_t(id) * n + row) * p.r + c) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        } else {
+            uint16_t *out = p.da[s];
+            for (int i = tid; i < 16 * p.r; i += BW_THREADS) {
+                const int c = i >> 4, m = (i & 15) * 8;
+                if (c0 + m >= p.H) continue;
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16x2(p.scale * value(m + 2 * e, c), p.scale * value(m + 2 * e + 1, c));
+                *reinterpret_cast<uint4 *>(out + (int64_t(id) * p.r + c) * p.H + c0 + m) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (dbias != nullptr) {
+            __syncthreads();
+            if (wn == 0 && t == 0)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    stage[wk * BW_COLS + wm * 32 + i * 16 + gq] = ones[i][0];
+                    stage[wk * BW_COLS + wm * 32 + i * 16 + gq + 8] = ones[i][2];
+                }
+            __syncthreads();
+            for (int m = tid; m < BW_COLS; m += BW_THREADS) {
+                const int row = c0 + m - lo;
+                if (row < 0 || row >= n) continue;
+                float f = stage[m];
+                if constexpr (WK > 1) f += stage[BW_COLS + m];
+                dbias[int64_t(id) * n + row] = uint16_t(pack_bf16x2(f, 0.0f) & 0xFFFFu);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+static int padded_rank(int r)
+{
+    int rp = 16;
+    while (rp < r) rp *= 2;
+    return rp;
+}
+
+// Rows of the laid-out g and u of one slice: every adapter that occurs may
+// add a partial tile.
+static int64_t backward_rows(int64_t T, int64_t L)
+{
+    return (T / BW_TOK + (L < T ? L : T)) * BW_TOK;
+}
+
+template <int RP>
+static int run_backward(const BackwardArgs &p, cudaStream_t st)
+{
+    const int tab = int(seg_tab_bytes(p.nbins));
+    const int us = grad_u_smem<RP>() + tab, xs = grad_x_smem<RP>() + tab;
+    const int ws = grad_w_smem<RP>() + tab + p.L * 4;
+    cudaError_t e;
+    static int configured[64] = {0};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return int(e);
+    if (dev >= 64 || !configured[dev]) {
+        constexpr int most = int(seg_tab_bytes(LORA_MAX_LORAS + 1)) + LORA_MAX_LORAS * 4;
+        if ((e = cudaFuncSetAttribute(grad_u_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_u_smem<RP>() + most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(grad_x_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_x_smem<RP>() + most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(grad_w_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_w_smem<RP>() + most)) != cudaSuccess)
+            return int(e);
+        if (dev < 64) configured[dev] = 1;
+    }
+    const int sms = device_sm_count();
+    const int64_t tiles = p.rows / BW_TOK;
+    if (p.T > 0) {
+        // few items: a cluster shares each one's columns
+        int cl = 1;
+        const int64_t items = tiles * p.S;
+        while (cl < BW_MAX_CLUSTER && items * cl < 2 * sms && p.width / p.S / 64 >= 4 * cl) cl *= 2;
+        int64_t clusters = items < 8 * sms / cl ? items : 8 * sms / cl;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(clusters * cl));
+        cfg.blockDim = dim3(BW_THREADS);
+        cfg.dynamicSmemBytes = size_t(us);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(cl);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, grad_u_kernel<RP>, p);
+        if (e != cudaSuccess) return int(e);
+        if (p.dx != nullptr) {
+            const int64_t most = tiles * ((p.H + BW_COLS - 1) / BW_COLS);
+            const int grid = int(most < 8 * sms ? most : 8 * sms);
+            e = launch_kernel(grad_x_kernel<RP>, dim3(grid), dim3(BW_THREADS), xs, st, p);
+            if (e != cudaSuccess) return int(e);
+        }
+    }
+    const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
+    if (items > 0) {
+        const int grid = int(items < 8 * sms ? items : 8 * sms);
+        e = launch_kernel(grad_w_kernel<RP>, dim3(grid), dim3(BW_THREADS), ws, st, p);
+        if (e != cudaSuccess) return int(e);
+    }
+    return LORA_OK;
+}
+
+}  // namespace lora
+
+LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
+                                                const int32_t *slice_sizes, int32_t num_slices,
+                                                int32_t rank, int32_t max_loras)
+{
+    if (slice_sizes == nullptr) return LORA_ERR_NULL;
+    if (hidden < 8 || hidden % 8 != 0 || num_tokens < 0 || max_loras < 1 || max_loras > LORA_MAX_LORAS) return LORA_ERR_SIZE;
+    if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
+    if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
+    const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;
+    return 2 * ((one + 255) / 256 * 256) + 256;
+}
+
+LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,
+                                  const lora_bf16_t *x, int32_t hidden, int64_t x_ld,
+                                  const float *buf, const lora_bf16_t *const *lora_a,
+                                  const lora_bf16_t *const *lora_b, const int32_t *slice_sizes,
+                                  int32_t num_slices, int32_t rank, float scale, lora_bf16_t *dx,
+                                  int64_t dx_ld, int32_t add_inputs, lora_bf16_t *const *d_lora_a,
+                                  lora_bf16_t *const *d_lora_b, lora_bf16_t *const *d_lora_bias,
+                                  const lora_meta_t *meta, void *workspace, int64_t workspace_bytes,
+                                  void *stream)
+{
+    using namespace lora;
+    NvtxRange nvtx_range("lora_linear_backward");
+    if (meta == nullptr || slice_sizes == nullptr || lora_a == nullptr || lora_b == nullptr)
+        return LORA_ERR_NULL;
+    if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
+    if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
+    if (num_tokens < 0 || hidden < 8 || meta->max_loras < 1 || meta->max_loras > LORA_MAX_LORAS)
+        return LORA_ERR_SIZE;
+    if (num_tokens > meta->max_num_tokens) return LORA_ERR_TOKENS;
+    if (hidden % 8 != 0) return LORA_ERR_ALIGN;
+    if (!meta->token_indices_sorted_by_lora_ids || !meta->num_tokens_per_lora ||
+        !meta->lora_token_start_loc || !meta->active_lora_ids || !meta->no_lora_flag ||
+        !meta->error_word || workspace == nullptr)
+        return LORA_ERR_NULL;
+    if (num_tokens > 0 && (dy == nullptr || x == nullptr || buf == nullptr)) return LORA_ERR_NULL;
+    auto bits = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
+    BackwardArgs p;
+    int64_t width = 0;
+    int blocks = 0;
+    for (int s = 0; s < LORA_MAX_SLICES; ++s) {
+        const bool in = s < num_slices;
+        p.a[s] = in ? lora_a[s] : nullptr;
+        p.b[s] = in ? lora_b[s] : nullptr;
+        p.da[s] = in && d_lora_a != nullptr ? d_lora_a[s] : nullptr;
+        p.db[s] = in && d_lora_b != nullptr ? d_lora_b[s] : nullptr;
+        p.dbias[s] = in && d_lora_bias != nullptr ? d_lora_bias[s] : nullptr;
+        p.n[s] = p.off[s] = 0;
+        if (!in) continue;
+        if (p.a[s] == nullptr || p.b[s] == nullptr) return LORA_ERR_NULL;
+        if (slice_sizes[s] < 1) return LORA_ERR_SIZE;
+        if ((bits(p.a[s]) | bits(p.b[s]) | bits(p.da[s]) | bits(p.db[s])) & 15u) return LORA_ERR_ALIGN;
+        p.n[s] = slice_sizes[s];
+        p.off[s] = int32_t(width);
+        width += slice_sizes[s];
+        if (width > (int64_t(1) << 30)) return LORA_ERR_SIZE;
+    }
+    if (dy_ld < width) return LORA_ERR_WIDTH;
+    if (x_ld < hidden || (dx != nullptr && dx_ld < hidden)) return LORA_ERR_SIZE;
+    if ((bits(buf) & 15u) || (bits(workspace) & 255u)) return LORA_ERR_ALIGN;
+    if (workspace_bytes < lora_linear_backward_workspace(num_tokens, hidden, slice_sizes, num_slices, rank,
+                                                         meta->max_loras))
+        return LORA_ERR_WORKSPACE;
+    p.dy = dy;
+    p.dy_ld = dy_ld;
+    p.x = x;
+    p.x_ld = x_ld;
+    p.buf = buf;
+    p.dx = dx;
+    p.dx_ld = dx_ld;
+    p.T = num_tokens;
+    p.H = hidden;
+    p.S = num_slices;
+    p.r = rank;
+    p.L = meta->max_loras;
+    p.width = int32_t(width);
+    p.add = add_inputs != 0;
+    p.dy_vec = (bits(dy) & 15u) == 0 && dy_ld % 8 == 0;
+    p.x_vec = (bits(x) & 15u) == 0 && x_ld % 8 == 0;
+    p.dx_vec = (bits(dx) & 15u) == 0 && dx_ld % 8 == 0;
+    p.scale = scale;
+    for (int s = 0; s < num_slices; ++s) {
+        const int lead = p.dy_vec ? p.off[s] & 7 : 0;
+        if (p.db[s] != nullptr || p.dbias[s] != nullptr) blocks += (lead + p.n[s] + BW_COLS - 1) / BW_COLS;
+        p.block_end[s] = blocks;
+    }
+    for (int s = 0; s < num_slices; ++s) {
+        if (p.da[s] != nullptr) blocks += (hidden + BW_COLS - 1) / BW_COLS;
+        p.block_end[num_slices + s] = blocks;
+    }
+    const int rp = padded_rank(rank);
+    p.rows = backward_rows(num_tokens, p.L);
+    const int64_t one = (p.rows * num_slices * rp * 2 + 255) / 256 * 256;
+    p.g = reinterpret_cast<uint16_t *>(workspace);
+    p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + one);
+    p.sorted = meta->token_indices_sorted_by_lora_ids;
+    p.counts = meta->num_tokens_per_lora;
+    p.start_loc = meta->lora_token_start_loc;
+    p.active = meta->active_lora_ids;
+    p.no_lora = meta->no_lora_flag;
+    p.error_word = meta->error_word;
+    p.nbins = meta->max_loras + 1;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (rp) {
+    case 16: return run_backward<16>(p, st);
+    case 32: return run_backward<32>(p, st);
+    case 64: return run_backward<64>(p, st);
+    default: return run_backward<128>(p, st);
+    }
+}

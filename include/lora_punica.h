@@ -373,6 +373,57 @@ int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden_size, in
                                      int32_t hidden_grad, int32_t weight_grad);
 
 /*
+ * lora_linear_backward -- the gradients of one linear layer's adapters:
+ * with u = buf (what lora_shrink left: scale * x @ A^T) and a = id(t), for
+ * every slice s and every token t with an adapter
+ *   g[s][t]  = lora_b[s][a]^T dy[t, off_s : off_s + n_s]
+ *   dx[t]    (+)= scale * sum_s lora_a[s][a]^T g[s][t]
+ *   d_lora_a[s][a] = scale * sum_t g[s][t] x[t]^T
+ *   d_lora_b[s][a] = sum_t dy[t, slice s] buf[s][t]^T
+ *   d_lora_bias[s][a] = sum_t dy[t, slice s]
+ * with off_s = n_0 + ... + n_{s-1}.
+ *
+ *   dy           device bf16 [num_tokens, dy_ld], dy_ld >= sum of the
+ *                slices: the gradient of the layer's output.  Any alignment
+ *                (16-byte aligned rows are read faster); a slice may begin
+ *                at any column.
+ *   x            device bf16 [num_tokens, x_ld]: the layer's input.  Any
+ *                alignment.  hidden is a multiple of 8.
+ *   buf          device fp32 [num_slices, num_tokens, rank], 16-byte
+ *                aligned: the buffer the forward pass left.
+ *   lora_a, lora_b, slice_sizes, num_slices, rank, scale, meta: those of
+ *                the forward pass; `meta` prepared for these tokens.
+ *   dx           NULL or device bf16 [num_tokens, dx_ld], any alignment.
+ *   add_inputs   nonzero: the adapters' part is added to dx (rows of tokens
+ *                without an adapter are not touched); zero: dx is
+ *                overwritten (those rows with zeros).
+ *   d_lora_a, d_lora_b, d_lora_bias  NULL, or host arrays of num_slices
+ *                entries, each NULL or a device pointer to bf16
+ *                [max_loras, rank, hidden], [max_loras, n_s, rank] (16-byte
+ *                aligned) and [max_loras, n_s].  Overwritten for all
+ *                max_loras adapters: zero for those without tokens.
+ *
+ * g and buf enter the products over tokens as bf16 (rounded once); sums are
+ * fp32 and every output is rounded to bf16 once.  Deterministic.  Invalid
+ * ids were mapped to -1 by the metadata.  Errors: as lora_shrink and
+ * lora_expand, LORA_ERR_WIDTH for dy_ld, LORA_ERR_WORKSPACE.
+ */
+int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,
+                         const lora_bf16_t *x, int32_t hidden, int64_t x_ld, const float *buf,
+                         const lora_bf16_t *const *lora_a, const lora_bf16_t *const *lora_b,
+                         const int32_t *slice_sizes, int32_t num_slices, int32_t rank,
+                         float scale, lora_bf16_t *dx, int64_t dx_ld, int32_t add_inputs,
+                         lora_bf16_t *const *d_lora_a, lora_bf16_t *const *d_lora_b,
+                         lora_bf16_t *const *d_lora_bias, const lora_meta_t *meta,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_linear_backward; a negative status for sizes
+ * that it refuses. */
+int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
+                                       const int32_t *slice_sizes, int32_t num_slices,
+                                       int32_t rank, int32_t max_loras);
+
+/*
  * lora_orthogonalize -- Newton-Schulz steps on `count` stacked matrices, as
  * the Muon optimiser takes them on an update: for each matrix
  *   X = U / (|U|_F + eps);  steps times: X <- a X + (b G + c G^2) X, G = X X^T
