@@ -34,11 +34,14 @@
 
 namespace lora {
 
-constexpr int LS_PIECE_ELEMS = 64 << 20;      // tokens x columns of one piece's scratch
+constexpr int LS_PIECE_ELEMS = 128 << 20;     // tokens x columns of one piece's scratch
 constexpr int LS_MIN_PIECE = 1024;            // columns
 constexpr int LS_WINDOW = 60;                 // exponents a tile may be off the reference
 constexpr int LS_MAX_SPLIT = 8;
-constexpr int LS_PACK_TOKENS = 32;            // tokens of one block of pack_kernel
+constexpr int LS_PACK_TOKENS = 4;             // tokens of one block of pack_kernel
+constexpr int LS_PACK_THREADS = 256;
+constexpr int LS_JOIN_TEAM = 8;               // threads a row in join_kernel
+constexpr int LS_JOIN_ROWS = 16;              // rows of one block
 constexpr float LS_LOG2E = 1.4426950408889634f;
 constexpr float LS_LN2 = 0.6931471805599453f;
 
@@ -90,7 +93,7 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
     l.stat = take(l.tokens * (l.piece / PG_TILE) * 8);
     l.h = take(l.tokens * H * 2);
     l.p = take(hidden_grad || weight_grad ? l.tokens * l.piece * 2 : 0);
-    l.acc = take(hidden_grad ? l.split * l.tokens * H * 4 : 0);
+    l.acc = take(hidden_grad && (l.split > 1 || l.pieces > 1) ? l.split * l.tokens * H * 4 : 0);
     l.bytes = at;
     return l;
 }
@@ -120,23 +123,27 @@ struct LossArgs {
 
 // ---------------------------------------------------------------- pack
 
-// Block b copies tokens [32 b, 32 b + 32) that have a target to their place
+// Block b copies tokens [4 b, 4 b + 4) that have a target to their place
 // among those that have one (the count of targets before them, which every
 // block takes itself), and clears the outputs of the others.  The last block
 // also fills the tile behind the last row with zeros.  The target's logit is
 // summed here, in ordinary fp32: the loss is a difference with it, and the
 // tensor cores' sums truncate (over 4096 products they leave the loss 4
-// times further off).
-__global__ void __launch_bounds__(256) pack_kernel(const LossArgs p)
+// times further off).  Two warps a token with their loads unrolled: at 256
+// tokens x 4096 one warp for four tokens, one load after another, took 64 us.
+__global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
 {
-    __shared__ int s_part[2][8];
-    __shared__ int s_place[LS_PACK_TOKENS];
+    constexpr int WARPS = LS_PACK_THREADS / 32, TEAM = LS_PACK_THREADS / LS_PACK_TOKENS;
+    __shared__ int s_part[2][WARPS];
+    __shared__ float s_dot[WARPS];
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x * LS_PACK_TOKENS;
+    const bool last = blockIdx.x == gridDim.x - 1;
     int before = 0, bad = 0;
-    for (int t = tid; t < c0; t += 256) {
+#pragma unroll 8
+    for (int t = tid; t < c0; t += LS_PACK_THREADS) {
         const int y = p.targets[t];
         before += y >= 0 && y < p.V;
         bad += y >= p.V;
@@ -151,38 +158,22 @@ __global__ void __launch_bounds__(256) pack_kernel(const LossArgs p)
     }
     __syncthreads();
     before = bad = 0;
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         before += s_part[0][i];
         bad += s_part[1][i];
     }
-    const int t = c0 + lane;
-    const int y = t < p.T ? p.targets[t] : -1;
-    const bool valid = y >= 0 && y < p.V;
-    const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-    const int place = before + __popc(mask & ((1u << lane) - 1u));
+    // lane i < LS_PACK_TOKENS of every warp: the block's token i
+    const int y = lane < LS_PACK_TOKENS && c0 + lane < p.T ? p.targets[c0 + lane] : -1;
+    const uint32_t mask = __ballot_sync(0xffffffffu, y >= 0 && y < p.V);
+    bad += __popc(__ballot_sync(0xffffffffu, y >= p.V));
     const int n = before + __popc(mask);
-    if (warp == 0) {
-        s_place[lane] = valid ? place : -1;
-        if (valid) {
-            p.row[place] = t;
-            p.target[place] = y;
-            p.wt[place] = p.token_weight != nullptr ? p.token_weight[t] : 1.0f;
-            p.ref[place] = 0;
-            p.sum[place] = 0.0f;
-        } else if (t < p.T) {
-            p.loss[t] = 0.0f;
-            if (p.logsumexp != nullptr) p.logsumexp[t] = 0.0f;
-        }
-    }
-    const bool last = blockIdx.x == gridDim.x - 1;
-    const int n_up = (n + PG_TILE - 1) / PG_TILE * PG_TILE;
     if (last) {
-        bad += __popc(__ballot_sync(0xffffffffu, y >= p.V));
+        const int n_up = (n + PG_TILE - 1) / PG_TILE * PG_TILE;
         if (tid == 0) {
             *p.count = n;
             if (p.error_word != nullptr) *p.error_word = bad;
         }
-        for (int r = n + tid; r < n_up; r += 256) {
+        for (int r = n + tid; r < n_up; r += LS_PACK_THREADS) {
             p.row[r] = -1;
             p.target[r] = -1;
             p.wt[r] = 0.0f;
@@ -190,46 +181,74 @@ __global__ void __launch_bounds__(256) pack_kernel(const LossArgs p)
             p.sum[r] = 0.0f;
             p.logit[r] = 0.0f;
         }
-        for (int64_t i = tid; i < int64_t(n_up - n) * (p.H / 8); i += 256)
-            reinterpret_cast<uint4 *>(p.h + int64_t(n) * p.H)[i] = make_uint4(0, 0, 0, 0);
+        uint4 *pad = reinterpret_cast<uint4 *>(p.h + int64_t(n) * p.H);
+        for (int64_t i = tid; i < int64_t(n_up - n) * (p.H / 8); i += LS_PACK_THREADS)
+            pad[i] = make_uint4(0, 0, 0, 0);
     }
-    __syncthreads();
-    for (int i = warp; i < LS_PACK_TOKENS && c0 + i < p.T; i += 8) {
-        const int to = s_place[i];
-        if (to >= 0) {
-            const uint16_t *src = p.hidden + int64_t(c0 + i) * p.hidden_ld;
-            uint16_t *dst = p.h + int64_t(to) * p.H;
-            const uint16_t *w = p.weight + int64_t(p.targets[c0 + i]) * p.H;
-            float dot = 0.0f;
-            for (int c = lane * 8; c < p.H; c += 256) {
-                uint4 v;
-                if (p.hidden_vec) {
-                    v = *reinterpret_cast<const uint4 *>(src + c);
-                } else {
-                    v.x = src[c] | uint32_t(src[c + 1]) << 16;
-                    v.y = src[c + 2] | uint32_t(src[c + 3]) << 16;
-                    v.z = src[c + 4] | uint32_t(src[c + 5]) << 16;
-                    v.w = src[c + 6] | uint32_t(src[c + 7]) << 16;
-                }
-                *reinterpret_cast<uint4 *>(dst + c) = v;
-                const uint4 u = *reinterpret_cast<const uint4 *>(w + c);
-                const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
+    const int mine = tid / TEAM, part = tid % TEAM, t = c0 + mine;     // this thread's token
+    const int target = __shfl_sync(0xffffffffu, y, mine);
+    const bool valid = mask >> mine & 1u;
+    const int to = before + __popc(mask & ((1u << mine) - 1u));
+    float dot = 0.0f;
+    if (valid) {
+        const uint16_t *src = p.hidden + int64_t(t) * p.hidden_ld;
+        uint16_t *dst = p.h + int64_t(to) * p.H;
+        const uint16_t *w = p.weight + int64_t(target) * p.H;
+        auto one = [&](int c, const uint4 &v, const uint4 &u) {
+            *reinterpret_cast<uint4 *>(dst + c) = v;
+            const uint32_t a[4] = {v.x, v.y, v.z, v.w}, b[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    dot = fmaf(bf16_lo(a[j]), bf16_lo(b[j]), dot);
-                    dot = fmaf(bf16_hi(a[j]), bf16_hi(b[j]), dot);
-                }
+            for (int j = 0; j < 4; ++j) {
+                dot = fmaf(bf16_lo(a[j]), bf16_lo(b[j]), dot);
+                dot = fmaf(bf16_hi(a[j]), bf16_hi(b[j]), dot);
             }
-            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            if (lane == 0) p.logit[to] = dot * LS_LOG2E;
-        } else if (p.dh != nullptr) {
-            uint16_t *dst = p.dh + int64_t(c0 + i) * p.dh_ld;
-            if (p.dh_vec) {
-                for (int c = lane; c < p.H / 8; c += 32)
-                    reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
-            } else {
-                for (int c = lane; c < p.H; c += 32) dst[c] = 0;
+        };
+        if (p.hidden_vec) {
+            for (int c = part * 8; c < p.H; c += TEAM * 32) {
+                uint4 v[4], u[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + k * TEAM * 8 < p.H) {
+                        v[k] = *reinterpret_cast<const uint4 *>(src + c + k * TEAM * 8);
+                        u[k] = *reinterpret_cast<const uint4 *>(w + c + k * TEAM * 8);
+                    }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + k * TEAM * 8 < p.H) one(c + k * TEAM * 8, v[k], u[k]);
             }
+        } else {
+            for (int c = part * 8; c < p.H; c += TEAM * 8) {
+                uint32_t v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = src[c + 2 * j] | uint32_t(src[c + 2 * j + 1]) << 16;
+                one(c, make_uint4(v[0], v[1], v[2], v[3]), *reinterpret_cast<const uint4 *>(w + c));
+            }
+        }
+    } else if (t < p.T && p.dh != nullptr) {
+        uint16_t *dst = p.dh + int64_t(t) * p.dh_ld;
+        if (p.dh_vec) {
+            for (int c = part * 8; c < p.H; c += TEAM * 8)
+                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int c = part; c < p.H; c += TEAM) dst[c] = 0;
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) s_dot[warp] = dot;
+    __syncthreads();
+    if (part == 0) {
+        if (valid) {
+            float d = 0.0f;
+            for (int i = 0; i < TEAM / 32; ++i) d += s_dot[warp + i];
+            p.row[to] = t;
+            p.target[to] = target;
+            p.wt[to] = p.token_weight != nullptr ? p.token_weight[t] : 1.0f;
+            p.ref[to] = 0;
+            p.sum[to] = 0.0f;
+            p.logit[to] = d * LS_LOG2E;
+        } else if (t < p.T) {
+            p.loss[t] = 0.0f;
+            if (p.logsumexp != nullptr) p.logsumexp[t] = 0.0f;
         }
     }
 }
@@ -242,6 +261,7 @@ struct LossGemm {
     int32_t col0, cols;       // this piece of the vocabulary
     int32_t store;            // logits: write the scratch
     int32_t first;            // scratch x W: the rows of dh start here
+    int32_t last;             // ... and are finished here (no split)
     uint16_t *dw;             // head gradient
 };
 
@@ -358,6 +378,28 @@ logits_kernel(const __grid_constant__ LossGemm g)
     pair_gemm<false, false>(&g.a, &g.b, mt * nt, l.error_word, item, epilogue);
 }
 
+// Eight values of dh: inv * sum - share * W[y], their only rounding.
+__device__ __forceinline__ void finish8(uint16_t *dst, const uint16_t *w, const uint32_t *sum,
+                                        float inv, float share, int vec)
+{
+    const uint4 wv = *reinterpret_cast<const uint4 *>(w);
+    const uint32_t wr[4] = {wv.x, wv.y, wv.z, wv.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        o[j] = pack_bf16x2(fmaf(-share, bf16_lo(wr[j]), inv * __uint_as_float(sum[2 * j])),
+                           fmaf(-share, bf16_hi(wr[j]), inv * __uint_as_float(sum[2 * j + 1])));
+    if (vec) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            dst[2 * j] = uint16_t(o[j] & 0xFFFFu);
+            dst[2 * j + 1] = uint16_t(o[j] >> 16);
+        }
+    }
+}
+
 // acc[split][token][h] (+)= scratch x W over a share of the piece's columns
 // (W's rows are the K dimension: its rows are contiguous along N).
 __global__ void __launch_bounds__(PG_THREADS, 1)
@@ -381,29 +423,55 @@ hidden_grad_kernel(const __grid_constant__ LossGemm g)
         float *dst = l.acc + (int64_t(s) * l.tokens + row) * l.H + it.row_b;
         const float f = g.first ? 0.0f : l.factor[row];
         const int lim = min(PG_TILE, l.H - it.row_b);
+        float inv = 0.0f, share = 0.0f;
+        const uint16_t *w = l.weight;
+        uint16_t *out = nullptr;
+        if (g.last) {
+            const int t = l.row[row];
+            if (t >= 0) {
+                inv = l.inv[row];
+                share = l.share[row];
+                w += int64_t(l.target[row]) * l.H + it.row_b;
+                out = l.dh + int64_t(t) * l.dh_ld + it.row_b;
+            }
+        }
         for (int c = 0; c < lim; c += 32) {
+            const int many = min(32, lim - c);                 // a multiple of 8
             uint32_t v[32];
             if (empty) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0u;
             } else {
                 tmem_ld32_nowait(tmem + c, v);
-                tmem_wait_ld();
             }
+            // all of a chunk's loads before its first store: one after
+            // another they took longer than the tile's product
+            float4 was[8];
+            if (!g.first) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                if (c + j >= lim) break;                       // H is a multiple of 8
-                float4 o = make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                                       __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-                float4 *at = reinterpret_cast<float4 *>(dst + c + j);
-                if (!g.first) {
-                    const float4 was = *at;
-                    o.x = fmaf(was.x, f, o.x);
-                    o.y = fmaf(was.y, f, o.y);
-                    o.z = fmaf(was.z, f, o.z);
-                    o.w = fmaf(was.w, f, o.w);
+                for (int j = 0; j < 8; ++j)
+                    if (4 * j < many) was[j] = *reinterpret_cast<const float4 *>(dst + c + 4 * j);
+            }
+            if (!empty) tmem_wait_ld();
+            if (!g.first) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[4 * j] = __float_as_uint(fmaf(was[j].x, f, __uint_as_float(v[4 * j])));
+                    v[4 * j + 1] = __float_as_uint(fmaf(was[j].y, f, __uint_as_float(v[4 * j + 1])));
+                    v[4 * j + 2] = __float_as_uint(fmaf(was[j].z, f, __uint_as_float(v[4 * j + 2])));
+                    v[4 * j + 3] = __float_as_uint(fmaf(was[j].w, f, __uint_as_float(v[4 * j + 3])));
                 }
-                *at = o;
+            }
+            if (!g.last) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (4 * j < many)
+                        *reinterpret_cast<uint4 *>(dst + c + 4 * j) =
+                            make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            } else if (out != nullptr) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (8 * j < many) finish8(out + c + 8 * j, w + c + 8 * j, v + 8 * j, inv, share, l.dh_vec);
             }
         }
     };
@@ -462,99 +530,118 @@ struct JoinArgs {
     int32_t store;
 };
 
-// After a piece's logits: one thread per row adds the tiles' sums to the
-// row's and, where a tile fell outside the window, brings the row to a
-// common reference (the block then rescales the row's scratch).
-__global__ void __launch_bounds__(128) join_kernel(const JoinArgs a)
+// After a piece's logits: eight threads a row add the tiles' sums to the
+// row's (a fixed order) and, where a tile fell outside the window, bring the
+// row to a common reference (the block then rescales the row's scratch).
+__global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const JoinArgs a)
 {
-    __shared__ int s_rows, s_row[128];
-    __shared__ float s_new[128];
+    constexpr int THREADS = LS_JOIN_ROWS * LS_JOIN_TEAM;
+    __shared__ int s_off[LS_JOIN_ROWS];
+    __shared__ float s_new[LS_JOIN_ROWS];
     pdl_wait();
     pdl_launch_dependents();
     const LossArgs &l = a.l;
-    if (threadIdx.x == 0) s_rows = 0;
-    __syncthreads();
-    const int row = blockIdx.x * 128 + threadIdx.x;
+    const int k = threadIdx.x % LS_JOIN_ROWS, part = threadIdx.x / LS_JOIN_ROWS;
+    __shared__ float s_sum[LS_JOIN_TEAM][LS_JOIN_ROWS], s_own[LS_JOIN_TEAM][LS_JOIN_ROWS];
+    __shared__ int s_used[LS_JOIN_TEAM][LS_JOIN_ROWS];
+    const int row = blockIdx.x * LS_JOIN_ROWS + k;
     const int n = *l.count;
-    if (row < n) {
-        const float have = float(l.ref[row]);
-        const float old = l.sum[row];
-        float sum = 0.0f, own = -INFINITY;
-        bool off = false, used = old > 0.0f;
-        for (int j = 0; j < a.tiles; ++j) {
-            const float2 s = l.stat[int64_t(j) * l.tokens + row];
-            sum += s.x == have ? s.y : 0.0f;
-            if (s.x == have) used = used || s.y > 0.0f;
-            else {
-                off = true;
+    const bool in = row < n;
+    const float2 *stat = l.stat + row;
+    const float have = in ? float(l.ref[row]) : 0.0f;
+    float sum = 0.0f, own = -INFINITY;
+    int used = 0;                           // some tile took the row's reference
+    if (in) {
+#pragma unroll 4
+        for (int j = part; j < a.tiles; j += LS_JOIN_TEAM) {
+            const float2 s = stat[int64_t(j) * l.tokens];
+            if (s.x == have) {
+                sum += s.y;
+                used |= s.y > 0.0f;
+            } else {
                 own = fmaxf(own, s.x);
             }
         }
-        float ref = have, f = 1.0f, total = old + sum;
-        if (off) {
-            ref = used ? fmaxf(have, own) : own;
-            f = used ? exp2f(have - ref) : 0.0f;
-            total = used ? total * f : 0.0f;
-            for (int j = 0; j < a.tiles; ++j) {
-                const float2 s = l.stat[int64_t(j) * l.tokens + row];
-                if (s.x != have) total += s.y * exp2f(s.x - ref);
-            }
-            if (a.store) {
-                const int k = atomicAdd(&s_rows, 1);      // order among rows is of no matter
-                s_row[k] = row;
+    }
+    s_sum[part][k] = sum;
+    s_own[part][k] = own;
+    s_used[part][k] = used;
+    __syncthreads();
+    if (part == 0) {
+        s_off[k] = 0;
+        const float old = in ? l.sum[row] : 0.0f;
+        float total = old;
+        used = old > 0.0f;
+        for (int q = 0; q < LS_JOIN_TEAM; ++q) {
+            total += s_sum[q][k];
+            own = fmaxf(own, s_own[q][k]);
+            used |= s_used[q][k];
+        }
+        if (in) {
+            float ref = have, f = 1.0f;
+            if (own > -INFINITY) {                  // a tile has a reference of its own
+                ref = used ? fmaxf(have, own) : own;
+                f = used ? exp2f(have - ref) : 0.0f;
+                total = used ? total * f : 0.0f;
+                for (int j = 0; j < a.tiles; ++j) {
+                    const float2 s = stat[int64_t(j) * l.tokens];
+                    if (s.x != have) total += s.y * exp2f(s.x - ref);
+                }
+                s_off[k] = a.store;
                 s_new[k] = ref;
+                l.ref[row] = int(ref);
             }
-            l.ref[row] = int(ref);
-        }
-        l.sum[row] = total;
-        l.factor[row] = f;
-        if (a.last) {
-            // total: the other columns, in units of 2^ref; d: the target's exponent
-            const float w = l.wt[row], d = l.logit[row] - ref;
-            float lse2, loss, inv, share;
-            if (total == 0.0f) {                  // the target is the only column left
-                lse2 = l.logit[row];
-                loss = inv = share = 0.0f;
-            } else if (d >= 0.0f) {
-                const float back = total * exp2f(-d);           // others relative to the target
-                loss = log1pf(back);
-                lse2 = l.logit[row] + loss * LS_LOG2E;
-                share = back / (1.0f + back);
-                inv = exp2f(-d) / (1.0f + back);
-            } else {
-                const float all = total + exp2f(d);
-                const float lg = log2f(all);
-                loss = (lg - d) * LS_LN2;
-                lse2 = ref + lg;
-                share = total / all;
-                inv = 1.0f / all;
+            l.sum[row] = total;
+            l.factor[row] = f;
+            if (a.last) {
+                // total: the other columns, in units of 2^ref; d: the target's exponent
+                const float w = l.wt[row], d = l.logit[row] - ref;
+                float lse2, loss, inv, share;
+                if (total == 0.0f) {                // the target is the only column left
+                    lse2 = l.logit[row];
+                    loss = inv = share = 0.0f;
+                } else if (d >= 0.0f) {
+                    const float back = total * exp2f(-d);       // others relative to the target
+                    loss = log1pf(back);
+                    lse2 = l.logit[row] + loss * LS_LOG2E;
+                    share = back / (1.0f + back);
+                    inv = exp2f(-d) / (1.0f + back);
+                } else {
+                    const float all = total + exp2f(d);
+                    const float lg = log2f(all);
+                    loss = (lg - d) * LS_LN2;
+                    lse2 = ref + lg;
+                    share = total / all;
+                    inv = 1.0f / all;
+                }
+                const int t = l.row[row];
+                l.loss[t] = w * loss;
+                if (l.logsumexp != nullptr) l.logsumexp[t] = lse2 * LS_LN2;
+                l.inv[row] = w * inv;
+                l.share[row] = w * share;
+                l.lse[row] = lse2;
             }
-            const int t = l.row[row];
-            l.loss[t] = w * loss;
-            if (l.logsumexp != nullptr) l.logsumexp[t] = lse2 * LS_LN2;
-            l.inv[row] = w * inv;
-            l.share[row] = w * share;
-            l.lse[row] = lse2;
+        } else if (a.last && row < l.tokens) {
+            l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
         }
-    } else if (a.last && row < l.tokens) {
-        l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
     }
     __syncthreads();
-    for (int k = 0; k < s_rows; ++k) {
-        const int r = s_row[k];
+    for (int q = 0; q < LS_JOIN_ROWS; ++q) {
+        if (!s_off[q]) continue;
+        const int r = blockIdx.x * LS_JOIN_ROWS + q;
         for (int j = 0; j < a.tiles; ++j) {
             const float was = l.stat[int64_t(j) * l.tokens + r].x;
-            if (was == s_new[k]) continue;
-            const float f = exp2f(was - s_new[k]);
+            if (was == s_new[q]) continue;
+            const float f = exp2f(was - s_new[q]);
             uint32_t *at = reinterpret_cast<uint32_t *>(l.p + int64_t(r) * l.piece + j * PG_TILE);
-            const uint32_t v = at[threadIdx.x];
-            at[threadIdx.x] = pack_bf16x2(bf16_lo(v) * f, bf16_hi(v) * f);
+            for (int i = threadIdx.x; i < PG_TILE / 2; i += THREADS)
+                at[i] = pack_bf16x2(bf16_lo(at[i]) * f, bf16_hi(at[i]) * f);
         }
     }
 }
 
-// dh[t] = inv * sum of the partial rows - share * W[y]: the only rounding of
-// dh.  One block per row (a stride of the grid apart).
+// dh where the pieces were split: the partial rows summed in order.  One
+// block per row (a stride of the grid apart).
 __global__ void __launch_bounds__(256) finish_kernel(const LossArgs l)
 {
     pdl_wait();
@@ -566,6 +653,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const LossArgs l)
         uint16_t *dst = l.dh + int64_t(l.row[row]) * l.dh_ld;
         for (int c = threadIdx.x * 8; c < l.H; c += 256 * 8) {
             float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
             for (int s = 0; s < l.split; ++s) {
                 const float4 *a = reinterpret_cast<const float4 *>(
                     l.acc + (int64_t(s) * l.tokens + row) * l.H + c);
@@ -573,22 +661,10 @@ __global__ void __launch_bounds__(256) finish_kernel(const LossArgs l)
                 v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
                 v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
             }
-            const uint4 wv = *reinterpret_cast<const uint4 *>(w + c);
-            const uint32_t wr[4] = {wv.x, wv.y, wv.z, wv.w};
-            uint32_t o[4];
+            uint32_t bits[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                o[j] = pack_bf16x2(fmaf(-share, bf16_lo(wr[j]), inv * v[2 * j]),
-                                   fmaf(-share, bf16_hi(wr[j]), inv * v[2 * j + 1]));
-            if (l.dh_vec) {
-                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    dst[c + 2 * j] = uint16_t(o[j] & 0xFFFFu);
-                    dst[c + 2 * j + 1] = uint16_t(o[j] >> 16);
-                }
-            }
+            for (int j = 0; j < 8; ++j) bits[j] = __float_as_uint(v[j]);
+            finish8(dst + c, w + c, bits, inv, share, l.dh_vec);
         }
     }
 }
@@ -636,7 +712,7 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
         !operand_map(&head.b, l.h, lay.tokens, l.H, l.H, true))
         return LORA_ERR_DEVICE;
     const int blocks = l.T > 0 ? (l.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
-    cudaError_t e = launch_kernel(pack_kernel, dim3(blocks), dim3(256), 0, st, l);
+    cudaError_t e = launch_kernel(pack_kernel, dim3(blocks), dim3(LS_PACK_THREADS), 0, st, l);
     if (e != cudaSuccess) return int(e);
     for (int i = 0; i < lay.pieces; ++i) {
         const int32_t col0 = int32_t(i * lay.piece);
@@ -651,10 +727,12 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
         j.tiles = (cols + PG_TILE - 1) / PG_TILE;
         j.last = i + 1 == lay.pieces;
         j.store = store;
-        e = launch_kernel(join_kernel, dim3(unsigned(lay.tokens / 128)), dim3(128), 0, st, j);
+        e = launch_kernel(join_kernel, dim3(unsigned(lay.tokens / LS_JOIN_ROWS)),
+                          dim3(LS_JOIN_ROWS * LS_JOIN_TEAM), 0, st, j);
         if (e != cudaSuccess) return int(e);
         if (store) {
             dhid.first = i == 0;
+            dhid.last = i + 1 == lay.pieces && lay.split == 1;
             // W's rows of this piece are the K dimension
             if (!operand_map(&dhid.b, l.weight + int64_t(col0) * l.H, cols, l.H, l.H, true))
                 return LORA_ERR_DEVICE;
@@ -662,7 +740,7 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
             if (e != cudaSuccess) return int(e);
         }
     }
-    if (store) {
+    if (store && lay.split > 1) {
         const int grid = l.T < 4 * 2 * pairs ? (l.T > 0 ? l.T : 1) : 4 * 2 * pairs;
         e = launch_kernel(finish_kernel, dim3(grid), dim3(256), 0, st, l);
         if (e != cudaSuccess) return int(e);

@@ -328,7 +328,7 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
 
 /*
  * lora_cross_entropy -- softmax cross entropy of the logits hidden x weight^T
- * and its gradients, without keeping the logits (at most about 2^26 of them,
+ * and its gradients, without keeping the logits (at most about 2^27 of them,
  * a piece of the vocabulary, exist at a time, in the workspace):
  *   loss[t] = w_t (log sum_v exp S[t, v] - S[t, y_t]),  S = hidden weight^T
  *   hidden_grad[t] = w_t (sum_v p[t, v] weight[v] - weight[y_t])

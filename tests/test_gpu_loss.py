@@ -43,7 +43,7 @@ def in_64_bits(hidden, weight, targets, token_weight):
     logits = h @ w.T
     mag = (h.abs() @ w.abs().T).amax(1)
     lse = torch.logsumexp(logits, 1)
-    rows = torch.arange(h.shape[0])
+    rows = torch.arange(h.shape[0], device=h.device)
     p = torch.exp(logits - lse[:, None])
     g = p.clone()
     g[rows, y] = 0.0
@@ -58,8 +58,9 @@ def in_64_bits(hidden, weight, targets, token_weight):
     tol_dh = 2.0 ** -8 * dh.abs() + (2.0 ** -8 + rel)[:, None] * (g.abs() @ w.abs())
     tol_dw = 2.0 ** -8 * dw.abs() + (g.abs() * (2.0 ** -8 + rel)[:, None]).T @ h.abs()
     zero = torch.zeros((), dtype=torch.float64)
-    return dict(loss=loss, lse=torch.where(valid, lse, zero), dh=dh, dw=dw, tol_loss=tol_loss,
-                tol_lse=2.0 ** -17 * mag + 2.0 ** -20 * (1 + lse.abs()), tol_dh=tol_dh, tol_dw=tol_dw)
+    ref = dict(loss=loss, lse=torch.where(valid, lse, zero), dh=dh, dw=dw, tol_loss=tol_loss,
+               tol_lse=2.0 ** -17 * mag + 2.0 ** -20 * (1 + lse.abs()), tol_dh=tol_dh, tol_dw=tol_dw)
+    return {k: v.cpu() for k, v in ref.items()}
 
 
 def run(hidden, weight, targets, token_weight, head=True, dh=True, **kw):
@@ -100,10 +101,11 @@ def test_without_some_gradients(head, dh):
     check(run(*a, head=head, dh=dh), in_64_bits(*a))
 
 
-def test_several_pieces(knob):
-    """More tokens than one piece's scratch takes: 4096 tokens x 20000 columns."""
-    a = make(4096, 64, 20000, 5, std=0.1)
-    check(run(*a), in_64_bits(*a))
+@pytest.mark.parametrize("V,std", [(20000, 0.1), (17000, 3.0)])
+def test_several_pieces(V, std):
+    """More logits than one piece's scratch takes (2^27)."""
+    a = make(8200, 64, V, 5, std=std)
+    check(run(*a), in_64_bits(*(v.cuda() for v in a)))
 
 
 @pytest.mark.parametrize("std", [3.0, 30.0])
