@@ -67,25 +67,75 @@ __device__ __forceinline__ SegTab load_tab(const BackwardArgs &p, int *mem, int 
     return tab;
 }
 
+// Tokens without an adapter: the metadata's first segment, or every token
+// when the batch has no adapter at all (the order is then unset).  Their
+// rows of dx are cleared (dx is overwritten, not added to).
+__device__ __forceinline__ void clear_rest(const BackwardArgs &p, const SegTab &tab)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const bool none = *p.no_lora != 0;
+    const int rest = none ? p.T : (tab.id[0] == -1 ? tab.count[0] : 0);
+    for (int64_t i = int64_t(blockIdx.x) * warps + warp; i < rest; i += int64_t(gridDim.x) * warps) {
+        const int tok = none ? int(i) : checked_token(p.sorted[i], p.T, p.error_word);
+        if (tok < 0) continue;
+        uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
+        if (p.dx_vec) {
+            for (int c = lane * 8; c < p.H; c += 256)
+                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int c = lane; c < p.H; c += 32) dst[c] = 0;
+        }
+    }
+}
+
+// The segment of each adapter (-1: no tokens), in the words behind the table.
+__device__ __forceinline__ const int *load_seg_of(const BackwardArgs &p, const SegTab &tab, int tiles,
+                                                  int *mem)
+{
+    int *seg_of = mem + 4 * p.nbins + 2;
+    for (int i = threadIdx.x; i < p.L; i += blockDim.x) seg_of[i] = -1;
+    __syncthreads();
+    if (tiles > 0)
+        for (int k = threadIdx.x; k < p.nbins; k += blockDim.x)
+            if (tab.id[k] >= 0 && tab.count[k] > 0) seg_of[tab.id[k]] = k;
+    __syncthreads();
+    return seg_of;
+}
+
+// One 16-byte chunk of a row into shared memory: asynchronously where all of
+// it lies in [lo, hi) and is aligned, else element by element.
+__device__ __forceinline__ void copy8(uint8_t *dst, const uint16_t *row, int c, int lo, int hi, bool vec)
+{
+    if (vec && c >= lo && c + 8 <= hi)
+        cp_async16(smem_addr(dst), row + c, true);
+    else
+        *reinterpret_cast<uint4 *>(dst) = load8(row, c, lo, hi, false);
+}
+
 // ---------------------------------------------------------------- g and u
 
 template <int RP> struct UShape { static constexpr int WM = 4, WN = RP >= 64 ? 2 : 1, WK = RP >= 64 ? 1 : 2; };
+constexpr int BW_U_STAGES = 4;
 
 template <int RP>
-constexpr int grad_u_smem() { return 2 * (BW_TOK * 64 * 2 + 64 * RP * 2) + UShape<RP>::WK * BW_TOK * RP * 4; }
+constexpr int grad_u_smem()
+{
+    return BW_U_STAGES * (BW_TOK * 64 * 2 + 64 * RP * 2) + UShape<RP>::WK * BW_TOK * RP * 4;
+}
 
 // Item: (tile, slice), worked on by a cluster whose CTAs take a share of the
 // slice's columns each; their partial sums are joined through distributed
-// shared memory in the order of the CTAs.
+// shared memory in the order of the CTAs.  Bound by the reads of dy: a ring
+// of four 64-column steps by cp.async.
 template <int RP>
 __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constant__ BackwardArgs p)
 {
     constexpr int WM = UShape<RP>::WM, WN = UShape<RP>::WN, WK = UShape<RP>::WK;
     constexpr int NI = RP / WN / 8, CPR = RP / 8;
-    constexpr int SD = BW_TOK * 64 * 2, SB = 64 * RP * 2;
+    constexpr int SD = BW_TOK * 64 * 2, SB = 64 * RP * 2, ST = BW_U_STAGES;
     constexpr int PB = (64 * CPR + BW_THREADS - 1) / BW_THREADS;
     extern __shared__ __align__(1024) uint8_t smem[];
-    float *part = reinterpret_cast<float *>(smem + 2 * (SD + SB));
+    float *part = reinterpret_cast<float *>(smem + ST * (SD + SB));
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp % WM, wn = warp / WM % WN, wk = warp / (WM * WN);
@@ -98,8 +148,8 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(part + WK * BW_TOK * RP), tiles);
     const int clusters = int(gridDim.x / csize), cluster = int(blockIdx.x / csize);
 
-    for (int item = cluster; item < tiles * p.S; item += clusters) {
-        const int tile = item / p.S, s = item % p.S;
+    for (int64_t item = cluster; item < int64_t(tiles) * p.S; item += clusters) {
+        const int tile = int(item / p.S), s = int(item % p.S);
         const int seg = find_segment(tab.tile, p.nbins, tile);
         const int id = tab.id[seg];
         const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
@@ -117,40 +167,35 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
             const int tok = row < nrows ? checked_token(p.sorted[row0 + row], p.T, p.error_word) : -1;
             src[i] = tok >= 0 ? p.dy + int64_t(tok) * p.dy_ld : nullptr;
         }
-        uint4 nd[2], nb[PB];
-        auto fetch = [&](int k) {
-            const int col = c0 + k * 64;
+        auto issue = [&](int k) {
+            if (k < k_hi) {
+                uint8_t *at = smem + k % ST * (SD + SB);
+                const int col = c0 + k * 64;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                nd[i] = src[i] != nullptr ? load8(src[i], col + (tid & 7) * 8, lo, hi, p.dy_vec)
-                                          : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 2; ++i) {
+                    const int c = tid + i * BW_THREADS;
+                    uint8_t *dst = at + tile_at<8, BW_TOK>(c >> 3, c & 7);
+                    if (src[i] != nullptr) copy8(dst, src[i], col + (c & 7) * 8, lo, hi, p.dy_vec);
+                    else *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int c = tid + i * BW_THREADS, row = col + c / CPR - lo, ch = c % CPR;
-                nb[i] = make_uint4(0, 0, 0, 0);
-                if (row >= 0 && row < hi - lo && ch * 8 < p.r && c < 64 * CPR)
-                    nb[i] = *reinterpret_cast<const uint4 *>(bw + int64_t(row) * p.r + ch * 8);
+                for (int i = 0; i < PB; ++i) {
+                    const int c = tid + i * BW_THREADS, row = col + c / CPR - lo, ch = c % CPR;
+                    if (c >= 64 * CPR) break;
+                    const bool ok = row >= 0 && row < hi - lo && ch * 8 < p.r;
+                    cp_async16(smem_addr(at + SD + tile_at<CPR, 64>(c / CPR, ch)),
+                               ok ? bw + int64_t(row) * p.r + ch * 8 : bw, ok);
+                }
             }
+            cp_async_commit();
         };
         float acc[NI][4] = {};
-        if (k_lo < k_hi) fetch(k_lo);
-        int bufi = 0;
+        for (int k = k_lo; k < k_lo + ST - 1; ++k) issue(k);
         for (int k = k_lo; k < k_hi; ++k) {
-            uint8_t *at = smem + bufi * (SD + SB);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int c = tid + i * BW_THREADS;
-                *reinterpret_cast<uint4 *>(at + tile_at<8, BW_TOK>(c >> 3, c & 7)) = nd[i];
-            }
-#pragma unroll
-            for (int i = 0; i < PB; ++i) {
-                const int c = tid + i * BW_THREADS;
-                if (c < 64 * CPR)
-                    *reinterpret_cast<uint4 *>(at + SD + tile_at<CPR, 64>(c / CPR, c % CPR)) = nb[i];
-            }
+            cp_async_wait<ST - 2>();
             __syncthreads();
-            if (k + 1 < k_hi) fetch(k + 1);
-            const uint32_t sd = base + bufi * (SD + SB), sb = sd + SD;
+            issue(k + ST - 1);
+            const uint32_t sd = base + k % ST * (SD + SB), sb = sd + SD;
 #pragma unroll
             for (int kk = wk * (64 / WK); kk < (wk + 1) * (64 / WK); kk += 16) {
                 uint32_t a[4];
@@ -163,7 +208,6 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
                     mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
                 }
             }
-            bufi ^= 1;
         }
         const int gq = lane >> 2, t = lane & 3;
         float *mine = part + wk * BW_TOK * RP;
@@ -179,6 +223,12 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
         const int share = BW_TOK * RP / int(csize) / 4;          // float4s
         for (int i = tid; i < share; i += BW_THREADS) {
             const int e = (int(rank) * share + i) * 4, row = e / RP, col = e % RP;
+            float4 f = make_float4(0, 0, 0, 0);
+            if (row < nrows && col < p.r) {
+                const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
+                if (tok >= 0)
+                    f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
+            }
             float4 v = make_float4(0, 0, 0, 0);
             for (uint32_t q = 0; q < csize; ++q)
                 for (int w = 0; w < WK; ++w) {
@@ -192,12 +242,6 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
                 }
             *reinterpret_cast<uint2 *>(p.g + out0 + e) =
                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            float4 f = make_float4(0, 0, 0, 0);
-            if (row < nrows && col < p.r) {
-                const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
-                if (tok >= 0)
-                    f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
-            }
             *reinterpret_cast<uint2 *>(p.u + out0 + e) =
                 make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
         }
@@ -207,19 +251,25 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- dx
 
+constexpr int BW_X_STAGES = 3;
+constexpr int BW_X_LD = BW_COLS + 4;       // floats of a staged row of dx
+
 template <int RP>
 constexpr int grad_x_smem()
 {
-    return BW_TOK * RP * 2 + RP * BW_COLS * 2;
+    return BW_X_STAGES * (BW_TOK * RP * 2 + RP * BW_COLS * 2) + BW_TOK * BW_X_LD * 4;
 }
 
+// Item: (tile, 128 columns), one step a slice; a ring of three steps runs
+// across the items.
 template <int RP>
 __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constant__ BackwardArgs p)
 {
-    constexpr int CPR = RP / 8;
-    constexpr int SG = BW_TOK * RP * 2;
+    constexpr int CPR = RP / 8, ST = BW_X_STAGES;
+    constexpr int SG = BW_TOK * RP * 2, SA = RP * BW_COLS * 2;
     constexpr int PG = (BW_TOK * CPR + BW_THREADS - 1) / BW_THREADS, PA = RP * 16 / BW_THREADS;
     extern __shared__ __align__(1024) uint8_t smem[];
+    float *stage = reinterpret_cast<float *>(smem + ST * (SG + SA));
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int m0 = warp % 4 * 16, n0 = warp / 4 * 64;          // 16 tokens x 64 columns a warp
@@ -228,210 +278,257 @@ __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constan
     int tiles;
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + grad_x_smem<RP>()), tiles);
     const int hb = (p.H + BW_COLS - 1) / BW_COLS;
-    for (int64_t item = blockIdx.x; item < int64_t(tiles) * hb; item += gridDim.x) {
-        const int tile = int(item / hb), h0 = int(item % hb) * BW_COLS;
-        const int seg = find_segment(tab.tile, p.nbins, tile);
-        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
-        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
-        float acc[8][4] = {};
-        for (int s = 0; s < p.S; ++s) {
-            const uint16_t *gt = p.g + (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
-            const uint16_t *aw = p.a[s] + int64_t(tab.id[seg]) * p.r * p.H;
-            uint4 ng[PG], na[PA];
-#pragma unroll
-            for (int i = 0; i < PG; ++i) {
-                const int c = tid + i * BW_THREADS;
-                if (c < BW_TOK * CPR) ng[i] = reinterpret_cast<const uint4 *>(gt)[c];
-            }
-#pragma unroll
-            for (int i = 0; i < PA; ++i) {
-                const int c = tid + i * BW_THREADS, row = c >> 4, col = h0 + (c & 15) * 8;
-                na[i] = make_uint4(0, 0, 0, 0);
-                if (row < p.r && col < p.H)
-                    na[i] = *reinterpret_cast<const uint4 *>(aw + int64_t(row) * p.H + col);
-            }
-            __syncthreads();
+    const int64_t items = int64_t(tiles) * hb;
+
+    // the step that is loaded next
+    int64_t l_item = blockIdx.x;
+    int l_s = 0, l_stage = 0;
+    auto issue = [&]() {
+        if (l_item < items) {
+            const int tile = int(l_item / hb), h0 = int(l_item % hb) * BW_COLS;
+            const int seg = find_segment(tab.tile, p.nbins, tile);
+            const uint16_t *gt = p.g + (int64_t(l_s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+            const uint16_t *aw = p.a[l_s] + int64_t(tab.id[seg]) * p.r * p.H;
+            uint8_t *at = smem + l_stage * (SG + SA);
 #pragma unroll
             for (int i = 0; i < PG; ++i) {
                 const int c = tid + i * BW_THREADS;
                 if (c < BW_TOK * CPR)
-                    *reinterpret_cast<uint4 *>(smem + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)) = ng[i];
+                    cp_async16(smem_addr(at + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)), gt + c * 8, true);
             }
 #pragma unroll
             for (int i = 0; i < PA; ++i) {
-                const int c = tid + i * BW_THREADS;
-                *reinterpret_cast<uint4 *>(smem + SG + tile_at<16, RP>(c >> 4, c & 15)) = na[i];
+                const int c = tid + i * BW_THREADS, row = c >> 4, col = h0 + (c & 15) * 8;
+                const bool ok = row < p.r && col < p.H;
+                cp_async16(smem_addr(at + SG + tile_at<16, RP>(row, c & 15)),
+                           ok ? aw + int64_t(row) * p.H + col : aw, ok);
             }
+            if (++l_s == p.S) {
+                l_s = 0;
+                l_item += gridDim.x;
+            }
+        }
+        l_stage = l_stage + 1 == ST ? 0 : l_stage + 1;
+        cp_async_commit();
+    };
+    for (int i = 0; i < ST - 1; ++i) issue();
+    int stg = 0;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int tile = int(item / hb), h0 = int(item % hb) * BW_COLS;
+        const int seg = find_segment(tab.tile, p.nbins, tile);
+        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
+        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
+        // the rows this thread writes: 16 threads a row, four rows each
+        int tok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (tid >> 4) + 16 * i;
+            tok[i] = row < nrows ? checked_token(p.sorted[row0 + row], p.T, p.error_word) : -1;
+        }
+        float acc[8][4] = {};
+        for (int s = 0; s < p.S; ++s) {
+            cp_async_wait<ST - 2>();
             __syncthreads();
+            issue();
+            const uint32_t sg = base + stg * (SG + SA), sa = sg + SG;
+            stg = stg + 1 == ST ? 0 : stg + 1;
 #pragma unroll
             for (int kk = 0; kk < RP; kk += 16) {
                 uint32_t a[4];
-                frag_a<CPR, BW_TOK, true>(base, m0, kk, a);
+                frag_a<CPR, BW_TOK, true>(sg, m0, kk, a);
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     uint32_t b[4];
-                    frag_b<16, RP, false>(base + SG, kk, n0 + 8 * j, b);
+                    frag_b<16, RP, false>(sa, kk, n0 + 8 * j, b);
                     mma_bf16_16816(acc[j], a, b[0], b[1]);
                     mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
                 }
             }
         }
-        // rows m0 + lane / 4 (+ 8), column pairs n0 + 8 j + 2 (lane % 4)
+        const int gq = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = m0 + (lane >> 2) + 8 * half;
-            if (row >= nrows) continue;
-            const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
-            if (tok < 0) continue;
-            uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
+        for (int j = 0; j < 8; ++j) {
+            float *at = stage + (m0 + gq) * BW_X_LD + n0 + 8 * j + 2 * t;
+            *reinterpret_cast<float2 *>(at) = make_float2(acc[j][0], acc[j][1]);
+            *reinterpret_cast<float2 *>(at + 8 * BW_X_LD) = make_float2(acc[j][2], acc[j][3]);
+        }
+        __syncthreads();
+        const int col = h0 + (tid & 15) * 8;
+        if (col < p.H) {
+            uint4 was[4];
+            if (p.add) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int col = h0 + n0 + 8 * j + 2 * (lane & 3);
-                if (col >= p.H) continue;                    // H is even
-                float v0 = p.scale * acc[j][2 * half], v1 = p.scale * acc[j][2 * half + 1];
+                for (int i = 0; i < 4; ++i)
+                    if (tok[i] >= 0) was[i] = load8(p.dx + int64_t(tok[i]) * p.dx_ld, col, 0, p.H, p.dx_vec);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (tok[i] < 0) continue;
+                const float *v = stage + ((tid >> 4) + 16 * i) * BW_X_LD + (tid & 15) * 8;
+                float f[8];
+                *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(v);
+                *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(v + 4);
+                const uint32_t w[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = p.scale * f[2 * e], y = p.scale * f[2 * e + 1];
+                    if (p.add) {
+                        x += bf16_lo(w[e]);
+                        y += bf16_hi(w[e]);
+                    }
+                    o[e] = pack_bf16x2(x, y);
+                }
+                uint16_t *dst = p.dx + int64_t(tok[i]) * p.dx_ld + col;
                 if (p.dx_vec) {
-                    uint32_t *at = reinterpret_cast<uint32_t *>(dst + col);
-                    if (p.add) {
-                        const uint32_t was = *at;
-                        v0 += bf16_lo(was);
-                        v1 += bf16_hi(was);
-                    }
-                    *at = pack_bf16x2(v0, v1);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
                 } else {
-                    if (p.add) {
-                        v0 += bf16_to_f32(dst[col]);
-                        v1 += bf16_to_f32(dst[col + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        dst[2 * e] = uint16_t(o[e] & 0xFFFFu);
+                        dst[2 * e + 1] = uint16_t(o[e] >> 16);
                     }
-                    const uint32_t w = pack_bf16x2(v0, v1);
-                    dst[col] = uint16_t(w & 0xFFFFu);
-                    dst[col + 1] = uint16_t(w >> 16);
                 }
             }
         }
     }
-    if (p.add) return;
-    // tokens without an adapter: the metadata's first segment, or every
-    // token when the batch has no adapter at all (the order is then unset)
-    const bool none = *p.no_lora != 0;
-    const int rest = none ? p.T : (tab.id[0] == -1 ? tab.count[0] : 0);
-    for (int i = blockIdx.x * 8 + warp; i < rest; i += gridDim.x * 8) {
-        const int tok = none ? i : checked_token(p.sorted[i], p.T, p.error_word);
-        if (tok < 0) continue;
-        uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
-        for (int c = lane * 2; c < p.H; c += 64) {
-            if (p.dx_vec) {
-                *reinterpret_cast<uint32_t *>(dst + c) = 0u;
-            } else {
-                dst[c] = 0;
-                dst[c + 1] = 0;
-            }
-        }
-    }
+    cp_async_wait<0>();
+    if (!p.add) clear_rest(p, tab);
 }
 
 // ---------------------------------------------------------------- dA, dB, dbias
 
-template <int RP> struct WShape { static constexpr int WM = 4, WN = RP >= 32 ? 2 : 1, WK = RP >= 32 ? 1 : 2; };
+template <int RP> struct WShape { static constexpr int WM = RP >= 64 ? 4 : 8, WN = 8 / WM; };
+constexpr int BW_W_STAGES = 3;
+constexpr int BW_W_LD = BW_COLS + 8;       // elements of a staged row of dA
 
 template <int RP>
 constexpr int grad_w_smem()
 {
-    constexpr int in = 2 * (BW_TOK * BW_COLS * 2 + BW_TOK * RP * 2);
-    constexpr int join = WShape<RP>::WK * BW_COLS * (RP + 1) * 4;
-    return in > join ? in : join;
+    return BW_W_STAGES * (BW_TOK * BW_COLS * 2 + BW_TOK * RP * 2) + RP * BW_W_LD * 2;
 }
 
 // Item: (adapter, column block): D[128 columns x RP] = sum over the
-// adapter's tokens of dy^T u (dB) or x^T g (dA).
+// adapter's tokens of dy^T u (dB) or x^T g (dA), 64 tokens a step (an
+// adapter without tokens has one step of zeros).  Per-token adapters give
+// items of a single step, so a ring of three steps runs across the items.
 template <int RP>
 __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constant__ BackwardArgs p)
 {
-    constexpr int WM = WShape<RP>::WM, WN = WShape<RP>::WN, WK = WShape<RP>::WK;
-    constexpr int NI = RP / WN / 8, CPR = RP / 8;
+    constexpr int WM = WShape<RP>::WM, WN = WShape<RP>::WN, ST = BW_W_STAGES;
+    constexpr int MI = BW_COLS / WM / 16, NI = RP / WN / 8, CPR = RP / 8;
     constexpr int SZ = BW_TOK * BW_COLS * 2, SV = BW_TOK * RP * 2;
     constexpr int PV = (BW_TOK * CPR + BW_THREADS - 1) / BW_THREADS;
     extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *stage = smem + ST * (SZ + SV);
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wm = warp % WM, wn = warp / WM % WN, wk = warp / (WM * WN);
+    const int wm = warp % WM, wn = warp / WM;
     pdl_wait();
     pdl_launch_dependents();
     int tiles;
     int *mem = reinterpret_cast<int *>(smem + grad_w_smem<RP>());
     const SegTab tab = load_tab(p, mem, tiles);
-    int *seg_of = mem + 4 * p.nbins + 2;
-    for (int i = tid; i < p.L; i += BW_THREADS) seg_of[i] = -1;
-    __syncthreads();
-    if (tiles > 0)
-        for (int k = tid; k < p.nbins; k += BW_THREADS)
-            if (tab.id[k] >= 0 && tab.count[k] > 0) seg_of[tab.id[k]] = k;
-    __syncthreads();
+    const int *seg_of = load_seg_of(p, tab, tiles, mem);
     const int blocks = p.block_end[2 * p.S - 1];
-    for (int64_t item = blockIdx.x; item < int64_t(p.L) * blocks; item += gridDim.x) {
-        const int id = int(item / blocks), blk = int(item % blocks);
+    const int64_t items = int64_t(p.L) * blocks;
+
+    struct Item {
+        const uint16_t *z, *v;
+        int64_t ld;
+        int id, s, seg, start, count, steps, c0, lo, n, width;
+        bool is_a, vec;
+    };
+    auto decode = [&](int64_t i) {
+        Item it;
+        it.id = int(i / blocks);
+        const int blk = int(i % blocks);
         int q = 0;                                  // product: dB of slice q, or dA of slice q - S
         while (blk >= p.block_end[q]) ++q;
-        const bool is_a = q >= p.S;
-        const int s = is_a ? q - p.S : q;
-        const int j0 = blk - (q > 0 ? p.block_end[q - 1] : 0);
-        const int lo = is_a ? 0 : p.off[s], n = is_a ? p.H : p.n[s];
-        const bool vec = is_a ? p.x_vec : p.dy_vec;
-        const int c0 = (vec ? lo & ~7 : lo) + j0 * BW_COLS;      // first column of the block
-        const int width = is_a ? p.H : p.width;                  // readable columns
-        const uint16_t *zsrc = is_a ? p.x : p.dy;
-        const int64_t zld = is_a ? p.x_ld : p.dy_ld;
-        const int seg = seg_of[id];
-        const int start = seg >= 0 ? tab.start[seg] : 0, count = seg >= 0 ? tab.count[seg] : 0;
-        const uint16_t *v = (is_a ? p.g : p.u) +
-                            (int64_t(s) * p.rows + (seg >= 0 ? int64_t(tab.tile[seg]) * BW_TOK : 0)) * RP;
-        uint16_t *dbias = is_a ? nullptr : p.dbias[s];
-        float acc[2][NI][4] = {}, ones[2][4] = {};
-        uint4 nz[4], nv[PV];
-        auto fetch = [&](int k) {
+        it.is_a = q >= p.S;
+        it.s = it.is_a ? q - p.S : q;
+        it.lo = it.is_a ? 0 : p.off[it.s];
+        it.n = it.is_a ? p.H : p.n[it.s];
+        it.vec = it.is_a ? p.x_vec : p.dy_vec;
+        it.c0 = (it.vec ? it.lo & ~7 : it.lo) + (blk - (q > 0 ? p.block_end[q - 1] : 0)) * BW_COLS;
+        it.width = it.is_a ? p.H : p.width;         // readable columns
+        it.z = it.is_a ? p.x : p.dy;
+        it.ld = it.is_a ? p.x_ld : p.dy_ld;
+        it.seg = seg_of[it.id];
+        it.start = it.seg >= 0 ? tab.start[it.seg] : 0;
+        it.count = it.seg >= 0 ? tab.count[it.seg] : 0;
+        it.steps = max(1, (it.count + BW_TOK - 1) / BW_TOK);
+        it.v = (it.is_a ? p.g : p.u) +
+               (int64_t(it.s) * p.rows + (it.seg >= 0 ? int64_t(tab.tile[it.seg]) * BW_TOK : 0)) * RP;
+        return it;
+    };
+
+    // the step that is loaded next, with its tokens
+    int64_t l_item = blockIdx.x;
+    Item ld;
+    int l_k = 0, l_stage = 0, tok[4];
+    auto tokens = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = l_k * BW_TOK + (tid >> 4) + i * 16;
+            tok[i] = row < ld.count ? checked_token(p.sorted[ld.start + row], p.T, p.error_word) : -1;
+        }
+    };
+    if (l_item < items) {
+        ld = decode(l_item);
+        tokens();
+    }
+    auto issue = [&]() {
+        if (l_item < items) {
+            uint8_t *at = smem + l_stage * (SZ + SV);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = k * BW_TOK + (tid >> 4) + i * 16;
-                nz[i] = make_uint4(0, 0, 0, 0);
-                if (row < count) {
-                    const int tok = checked_token(p.sorted[start + row], p.T, p.error_word);
-                    if (tok >= 0) nz[i] = load8(zsrc + tok * zld, c0 + (tid & 15) * 8, 0, width, vec);
-                }
+                uint8_t *dst = at + tile_at<16, BW_TOK>((tid >> 4) + i * 16, tid & 15);
+                if (tok[i] >= 0) copy8(dst, ld.z + tok[i] * ld.ld, ld.c0 + (tid & 15) * 8, 0, ld.width, ld.vec);
+                else *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
             }
+            const bool ok = ld.seg >= 0;
 #pragma unroll
             for (int i = 0; i < PV; ++i) {
                 const int c = tid + i * BW_THREADS;
                 if (c < BW_TOK * CPR)
-                    nv[i] = reinterpret_cast<const uint4 *>(v + int64_t(k) * BW_TOK * RP)[c];
+                    cp_async16(smem_addr(at + SZ + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)),
+                               ok ? ld.v + int64_t(l_k) * BW_TOK * RP + c * 8 : p.g, ok);
             }
-        };
-        const int steps = (count + BW_TOK - 1) / BW_TOK;
-        if (steps > 0) fetch(0);
-        int bufi = 0;
-        for (int k = 0; k < steps; ++k) {
-            uint8_t *at = smem + bufi * (SZ + SV);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4 *>(at + tile_at<16, BW_TOK>((tid >> 4) + i * 16, tid & 15)) = nz[i];
-#pragma unroll
-            for (int i = 0; i < PV; ++i) {
-                const int c = tid + i * BW_THREADS;
-                if (c < BW_TOK * CPR)
-                    *reinterpret_cast<uint4 *>(at + SZ + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)) = nv[i];
+            if (++l_k == ld.steps) {
+                l_k = 0;
+                l_item += gridDim.x;
+                if (l_item < items) ld = decode(l_item);
             }
+            if (l_item < items) tokens();
+        }
+        l_stage = l_stage + 1 == ST ? 0 : l_stage + 1;
+        cp_async_commit();
+    };
+    for (int i = 0; i < ST - 1; ++i) issue();
+    int stg = 0;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const Item it = decode(item);
+        uint16_t *dbias = it.is_a ? nullptr : p.dbias[it.s];
+        float acc[MI][NI][4] = {}, ones[MI][4] = {};
+        for (int k = 0; k < it.steps; ++k) {
+            cp_async_wait<ST - 2>();
             __syncthreads();
-            if (k + 1 < steps) fetch(k + 1);
-            const uint32_t sz = base + bufi * (SZ + SV), sv = sz + SZ;
+            issue();
+            const uint32_t sz = base + stg * (SZ + SV), sv = sz + SZ;
+            stg = stg + 1 == ST ? 0 : stg + 1;
 #pragma unroll
-            for (int kk = wk * (BW_TOK / WK); kk < (wk + 1) * (BW_TOK / WK); kk += 16) {
-                uint32_t a[2][4];
+            for (int kk = 0; kk < BW_TOK; kk += 16) {
+                uint32_t a[MI][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) frag_a<16, BW_TOK, false>(sz, wm * 32 + i * 16, kk, a[i]);
+                for (int i = 0; i < MI; ++i)
+                    frag_a<16, BW_TOK, false>(sz, wm * (BW_COLS / WM) + i * 16, kk, a[i]);
 #pragma unroll
                 for (int j = 0; j < NI; j += 2) {
                     uint32_t b[4];
                     frag_b<CPR, BW_TOK, false>(sv, kk, wn * (RP / WN) + 8 * j, b);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < MI; ++i) {
                         mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
                         mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
                     }
@@ -440,77 +537,65 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
                     // a product with ones: column 0 of the result
                     const uint32_t one = lane < 4 ? 0x3F803F80u : 0u;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) mma_bf16_16816(ones[i], a[i], one, one);
+                    for (int i = 0; i < MI; ++i) mma_bf16_16816(ones[i], a[i], one, one);
                 }
             }
-            bufi ^= 1;
         }
-        // through shared memory (rows padded by one float), then out
-        __syncthreads();
-        float *stage = reinterpret_cast<float *>(smem);
-        constexpr int LD = RP + 1;
+        // out through shared memory, rounded; dA transposed
         const int gq = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
-                float *at = stage + (wk * BW_COLS + wm * 32 + i * 16 + gq) * LD + wn * (RP / WN) + 8 * j + 2 * t;
-                at[0] = acc[i][j][0];
-                at[1] = acc[i][j][1];
-                at[8 * LD] = acc[i][j][2];
-                at[8 * LD + 1] = acc[i][j][3];
+                const int m = wm * (BW_COLS / WM) + i * 16 + gq, c = wn * (RP / WN) + 8 * j + 2 * t;
+                if (!it.is_a) {
+                    *reinterpret_cast<uint32_t *>(stage + tile_at<CPR, BW_COLS>(m, c / 8) + c % 8 * 2) =
+                        pack_bf16x2(acc[i][j][0], acc[i][j][1]);
+                    *reinterpret_cast<uint32_t *>(stage + tile_at<CPR, BW_COLS>(m + 8, c / 8) + c % 8 * 2) =
+                        pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+                } else {
+                    uint16_t *at = reinterpret_cast<uint16_t *>(stage) + c * BW_W_LD + m;
+                    const uint32_t v0 = pack_bf16x2(p.scale * acc[i][j][0], p.scale * acc[i][j][1]);
+                    const uint32_t v1 = pack_bf16x2(p.scale * acc[i][j][2], p.scale * acc[i][j][3]);
+                    at[0] = uint16_t(v0 & 0xFFFFu);
+                    at[BW_W_LD] = uint16_t(v0 >> 16);
+                    at[8] = uint16_t(v1 & 0xFFFFu);
+                    at[BW_W_LD + 8] = uint16_t(v1 >> 16);
+                }
             }
+        if (dbias != nullptr && wn == 0 && t == 0) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = it.c0 + wm * (BW_COLS / WM) + i * 16 + gq + 8 * half - it.lo;
+                    if (row >= 0 && row < it.n)
+                        dbias[int64_t(it.id) * it.n + row] =
+                            uint16_t(pack_bf16x2(ones[i][2 * half], 0.0f) & 0xFFFFu);
+                }
+        }
         __syncthreads();
-        auto value = [&](int m, int c) {
-            float f = stage[m * LD + c];
-            if constexpr (WK > 1) f += stage[(BW_COLS + m) * LD + c];
-            return f;
-        };
-        if (!is_a) {
-            uint16_t *out = p.db[s];
+        if (!it.is_a) {
+            uint16_t *out = p.db[it.s];
             if (out != nullptr) {
                 for (int i = tid; i < BW_COLS * CPR; i += BW_THREADS) {
-                    const int m = i / CPR, c = i % CPR * 8, row = c0 + m - lo;
-                    if (row < 0 || row >= n || c >= p.r) continue;
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(value(m, c + 2 * e), value(m, c + 2 * e + 1));
-                    *reinterpret_cast<uint4 *>(out + (int64_t(id) * n + row) * p.r + c) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                    const int m = i / CPR, c = i % CPR, row = it.c0 + m - it.lo;
+                    if (row >= 0 && row < it.n && c * 8 < p.r)
+                        *reinterpret_cast<uint4 *>(out + (int64_t(it.id) * it.n + row) * p.r + c * 8) =
+                            *reinterpret_cast<const uint4 *>(stage + tile_at<CPR, BW_COLS>(m, c));
                 }
             }
         } else {
-            uint16_t *out = p.da[s];
+            uint16_t *out = p.da[it.s] + int64_t(it.id) * p.r * p.H + it.c0;
             for (int i = tid; i < 16 * p.r; i += BW_THREADS) {
                 const int c = i >> 4, m = (i & 15) * 8;
-                if (c0 + m >= p.H) continue;
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(p.scale * value(m + 2 * e, c), p.scale * value(m + 2 * e + 1, c));
-                *reinterpret_cast<uint4 *>(out + (int64_t(id) * p.r + c) * p.H + c0 + m) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                if (it.c0 + m < p.H)
+                    *reinterpret_cast<uint4 *>(out + int64_t(c) * p.H + m) =
+                        *reinterpret_cast<const uint4 *>(reinterpret_cast<uint16_t *>(stage) + c * BW_W_LD + m);
             }
         }
-        if (dbias != nullptr) {
-            __syncthreads();
-            if (wn == 0 && t == 0)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    stage[wk * BW_COLS + wm * 32 + i * 16 + gq] = ones[i][0];
-                    stage[wk * BW_COLS + wm * 32 + i * 16 + gq + 8] = ones[i][2];
-                }
-            __syncthreads();
-            for (int m = tid; m < BW_COLS; m += BW_THREADS) {
-                const int row = c0 + m - lo;
-                if (row < 0 || row >= n) continue;
-                float f = stage[m];
-                if constexpr (WK > 1) f += stage[BW_COLS + m];
-                dbias[int64_t(id) * n + row] = uint16_t(pack_bf16x2(f, 0.0f) & 0xFFFFu);
-            }
-        }
-        __syncthreads();
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- host
@@ -551,13 +636,19 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         if (dev < 64) configured[dev] = 1;
     }
     const int sms = device_sm_count();
+    // resident CTAs of a kernel (its shared memory decides, at most six)
+    auto resident = [&](int smem) {
+        const int n = 227 * 1024 / (smem + 1024);
+        return int64_t(sms) * (n < 1 ? 1 : n > 6 ? 6 : n);
+    };
     const int64_t tiles = p.rows / BW_TOK;
     if (p.T > 0) {
         // few items: a cluster shares each one's columns
         int cl = 1;
         const int64_t items = tiles * p.S;
         while (cl < BW_MAX_CLUSTER && items * cl < 2 * sms && p.width / p.S / 64 >= 4 * cl) cl *= 2;
-        int64_t clusters = items < 8 * sms / cl ? items : 8 * sms / cl;
+        const int64_t most_u = resident(us) / cl > 0 ? resident(us) / cl : 1;
+        const int64_t clusters = items < most_u ? items : most_u;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(clusters * cl));
         cfg.blockDim = dim3(BW_THREADS);
@@ -576,15 +667,15 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         if (e != cudaSuccess) return int(e);
         if (p.dx != nullptr) {
             const int64_t most = tiles * ((p.H + BW_COLS - 1) / BW_COLS);
-            const int grid = int(most < 8 * sms ? most : 8 * sms);
-            e = launch_kernel(grad_x_kernel<RP>, dim3(grid), dim3(BW_THREADS), xs, st, p);
+            const int64_t grid = most < resident(xs) ? most : resident(xs);
+            e = launch_kernel(grad_x_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), xs, st, p);
             if (e != cudaSuccess) return int(e);
         }
     }
     const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
     if (items > 0) {
-        const int grid = int(items < 8 * sms ? items : 8 * sms);
-        e = launch_kernel(grad_w_kernel<RP>, dim3(grid), dim3(BW_THREADS), ws, st, p);
+        const int64_t grid = items < resident(ws) ? items : resident(ws);
+        e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);
         if (e != cudaSuccess) return int(e);
     }
     return LORA_OK;
