@@ -14,38 +14,12 @@
 //   grad_x_kernel  dx of a tile x 128 hidden columns, all slices summed;
 //   grad_w_kernel  dB and dA of an adapter x 128 columns, summed over the
 //                  adapter's tokens in a fixed order (no atomics).
-// g and u in bf16 cost a relative 2^-9 a term, like the rounding of the
+// They run on mma.sync; lora_backward_tc.cu holds their forms for ranks above
+// 32 on tcgen05.  g and u in bf16 cost a relative 2^-9 a term, like the rounding of the
 // outputs; all sums are fp32.
-#include "lora_frag.cuh"
+#include "lora_backward.cuh"
 
 namespace lora {
-
-constexpr int BW_THREADS = 256;
-constexpr int BW_TOK = 64;                 // tokens of a tile
-constexpr int BW_COLS = 128;               // columns of a tile of dx, dA, dB
-constexpr int BW_MAX_CLUSTER = 8;
-
-struct BackwardArgs {
-    const uint16_t *dy, *x;
-    int64_t dy_ld, x_ld;
-    const float *buf;
-    const uint16_t *a[LORA_MAX_SLICES], *b[LORA_MAX_SLICES];
-    uint16_t *da[LORA_MAX_SLICES], *db[LORA_MAX_SLICES], *dbias[LORA_MAX_SLICES];
-    uint16_t *dx;
-    int64_t dx_ld;
-    int32_t n[LORA_MAX_SLICES], off[LORA_MAX_SLICES];      // widths, first columns in dy
-    // grad_w_kernel's column blocks of one adapter: dB of slice s ends
-    // before block_end[s], dA of slice s before block_end[S + s]
-    int32_t block_end[2 * LORA_MAX_SLICES];
-    int32_t T, H, S, r, L, width;
-    int32_t add, dy_vec, x_vec, dx_vec;
-    float scale;
-    uint16_t *g, *u;                       // [S][rows][RP]
-    int64_t rows;
-    const int32_t *sorted, *counts, *start_loc, *active, *no_lora;
-    int32_t *error_word;
-    int32_t nbins;
-};
 
 // Eight elements of a row from column c; columns outside [lo, hi) give zero
 // and are not read.
@@ -57,49 +31,6 @@ __device__ __forceinline__ uint4 load8(const uint16_t *row, int c, int lo, int h
     for (int j = 0; j < 8; ++j)
         if (c + j >= lo && c + j < hi) w[j >> 1] |= uint32_t(row[c + j]) << (16 * (j & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-__device__ __forceinline__ SegTab load_tab(const BackwardArgs &p, int *mem, int &tiles)
-{
-    const SegTab tab = seg_tab(mem, p.nbins);
-    tiles = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, BW_TOK, tab, false, 0,
-                          p.T, p.error_word);
-    return tab;
-}
-
-// Tokens without an adapter: the metadata's first segment, or every token
-// when the batch has no adapter at all (the order is then unset).  Their
-// rows of dx are cleared (dx is overwritten, not added to).
-__device__ __forceinline__ void clear_rest(const BackwardArgs &p, const SegTab &tab)
-{
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const bool none = *p.no_lora != 0;
-    const int rest = none ? p.T : (tab.id[0] == -1 ? tab.count[0] : 0);
-    for (int64_t i = int64_t(blockIdx.x) * warps + warp; i < rest; i += int64_t(gridDim.x) * warps) {
-        const int tok = none ? int(i) : checked_token(p.sorted[i], p.T, p.error_word);
-        if (tok < 0) continue;
-        uint16_t *dst = p.dx + int64_t(tok) * p.dx_ld;
-        if (p.dx_vec) {
-            for (int c = lane * 8; c < p.H; c += 256)
-                *reinterpret_cast<uint4 *>(dst + c) = make_uint4(0, 0, 0, 0);
-        } else {
-            for (int c = lane; c < p.H; c += 32) dst[c] = 0;
-        }
-    }
-}
-
-// The segment of each adapter (-1: no tokens), in the words behind the table.
-__device__ __forceinline__ const int *load_seg_of(const BackwardArgs &p, const SegTab &tab, int tiles,
-                                                  int *mem)
-{
-    int *seg_of = mem + 4 * p.nbins + 2;
-    for (int i = threadIdx.x; i < p.L; i += blockDim.x) seg_of[i] = -1;
-    __syncthreads();
-    if (tiles > 0)
-        for (int k = threadIdx.x; k < p.nbins; k += blockDim.x)
-            if (tab.id[k] >= 0 && tab.count[k] > 0) seg_of[tab.id[k]] = k;
-    __syncthreads();
-    return seg_of;
 }
 
 // One 16-byte chunk of a row into shared memory: asynchronously where all of
@@ -642,7 +573,10 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         return int64_t(sms) * (n < 1 ? 1 : n > 6 ? 6 : n);
     };
     const int64_t tiles = p.rows / BW_TOK;
-    if (p.T > 0) {
+    // Ranks above 32 run on tcgen05 where the rows allow TMA.
+    int tc = RP >= 64 && p.T > 0 ? launch_grad_u_tc(p, RP, st) : -1;
+    if (tc > 0) return tc;
+    if (p.T > 0 && tc < 0) {
         // few items: a cluster shares each one's columns
         int cl = 1;
         const int64_t items = tiles * p.S;
@@ -665,7 +599,11 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         cfg.numAttrs = pdl_enabled() ? 2 : 1;
         e = cudaLaunchKernelEx(&cfg, grad_u_kernel<RP>, p);
         if (e != cudaSuccess) return int(e);
-        if (p.dx != nullptr) {
+    }
+    if (p.T > 0 && p.dx != nullptr) {
+        tc = RP >= 64 ? launch_grad_x_tc(p, RP, st) : -1;
+        if (tc > 0) return tc;
+        if (tc < 0) {
             const int64_t most = tiles * ((p.H + BW_COLS - 1) / BW_COLS);
             const int64_t grid = most < resident(xs) ? most : resident(xs);
             e = launch_kernel(grad_x_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), xs, st, p);
@@ -673,6 +611,8 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         }
     }
     const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
+    tc = RP >= 64 ? launch_grad_w_tc(p, RP, st) : -1;
+    if (tc >= 0) return tc;
     if (items > 0) {
         const int64_t grid = items < resident(ws) ? items : resident(ws);
         e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);

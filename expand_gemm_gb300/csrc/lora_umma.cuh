@@ -603,6 +603,12 @@ bool encode_tile_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_
                          uint64_t row_stride, uint32_t box_cols, uint32_t box_rows,
                          CUtensorMapSwizzle swizzle);
 
+// Host: a stack of `count` dense bf16 matrices of `rows` x `cols`, in boxes of
+// one matrix (128-byte swizzle): what a box holds past a matrix's last row or
+// column is zero.
+bool encode_stack_map(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
+                      uint32_t box_cols, uint32_t box_rows);
+
 // Host: encodes the B map of the tensor-core expand over a bf16 matrix of
 // `rows` rows (a multiple of 64) of `rank` elements, whose boxes of
 // `blocks` 64-row blocks land in shared memory with the rows of each block

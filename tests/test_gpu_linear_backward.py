@@ -101,7 +101,10 @@ CASES = [
     (257, 512, 128, 3, (256, 64, 72), 20), (300, 1000, 40, 5, (523, 75, 130), 30),
     (513, 392, 96, 7, (257,), 50), (200, 128, 16, 64, (96, 96), 1), (1000, 256, 128, 2, (384, 130), 400),
     (700, 200, 48, 1, (130, 128), 700), (256, 1032, 16, 8, (40, 40, 40, 40, 40, 40, 40, 40), 4),
-    (90, 64, 8, 1024, (24,), 1)]
+    (90, 64, 8, 1024, (24,), 1), (3500, 264, 128, 4, (136, 72, 64), 300),
+    (1300, 200, 64, 3, (64,) * 8, 40), (1300, 136, 128, 3, (64, 72, 80, 88, 8, 16, 24, 32), 1),
+    (700, 136, 96, 2, (72,) * 5, 100), (700, 72, 64, 2, (72,) * 5, 3), (260, 64, 128, 1, (64,), 260),
+    (5000, 64, 96, 3, (200, 520), 1)]
 
 
 @pytest.mark.parametrize("T,H,r,L,widths,runs", CASES)
