@@ -2,9 +2,13 @@
 // tensor cores (tcgen05), for padded ranks 64 and 128; see lora_backward.cu
 // for the formulas and the layout of g and u.
 //
-// Rows of dy and x are fetched through the token order by TMA gathers (four
-// rows of 64 columns an instruction): a row past an adapter's last token
-// gets an index past the matrix and arrives as zeros.  Weights are mapped
+// Rows of dy and x are fetched through the token order by TMA: each lane of
+// the loading warp has four rows; lanes whose rows follow one another join
+// into one box of up to 128 rows (a sequence's tokens do), the others take
+// their four rows by a gather.  A gather moves 512 bytes in about 90 clocks,
+// so a tile of one box loads many times faster (the whole of grad_u at 16384
+// tokens, rank 128: 197 us by gathers alone).  A row past an adapter's last
+// token gets an index past the matrix and arrives as zeros.  Weights are mapped
 // with a dimension of their own for the adapter, so that what lies behind a
 // slice's last row or column arrives as zeros too, never as a neighbour's
 // values.  Products over tokens take both operands with their rows
@@ -19,7 +23,9 @@ namespace lora {
 
 constexpr int TC_THREADS = 256;
 constexpr int TC_PANEL = 64 * 64 * 2;            // 64 rows of 64 bf16
-constexpr int TC_RING = 192 * 1024;
+constexpr int TC_SMEM = 227 * 1024;              // of a CTA
+constexpr int TC_STAGE_ROWS = 4 * 32 * 128;      // the epilogue's staging: 32 rows x 128 bytes a warp
+constexpr int TC_ONES = 2048;                    // 16 rows of a panel
 constexpr int TC_MAX_STAGES = 8;
 constexpr int TC_BAR_BYTES = 256;
 constexpr int TC_ROWS = 128;                     // tokens of a tile of g and dx
@@ -46,6 +52,65 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+constexpr int TC_HEIGHTS = 6;                    // boxes of 4, 8, ... 128 rows
+
+// The rows a lane loads: its four tokens, or a box of 4 << level rows from
+// the first of them (level 0 .. 5), or nothing (another lane's box holds
+// them).
+struct TcRows {
+    int t[4];
+    int level;              // -1: a gather, -2: nothing
+};
+
+// Joins the lanes' runs of four tokens; lanes that differ in the bits below
+// `stride` load other columns of the same rows.  Called by the whole warp.
+__device__ __forceinline__ void join_rows(TcRows &r, int stride)
+{
+    const int lane = threadIdx.x & 31;
+    bool run = r.t[1] == r.t[0] + 1 && r.t[2] == r.t[0] + 2 && r.t[3] == r.t[0] + 3;
+    r.level = run ? 0 : -1;
+#pragma unroll
+    for (int k = 0; k < TC_HEIGHTS - 1; ++k) {
+        const int bit = stride << k;
+        if (bit >= 32) break;
+        const int other = __shfl_xor_sync(0xffffffffu, r.t[0], bit);
+        const int orun = __shfl_xor_sync(0xffffffffu, int(run), bit);
+        const int first = (lane & bit) ? other : r.t[0], second = (lane & bit) ? r.t[0] : other;
+        run = run && orun && second == first + (4 << k);
+        if (run) {
+            r.t[0] = first;
+            r.level = (lane & bit) ? -2 : (r.level >= 0 ? k + 1 : r.level);
+        }
+    }
+}
+
+// The row number a lane's row has past an adapter's tokens: outside the
+// matrix, and running on, so that such rows join too.
+__device__ __forceinline__ int tc_no_row(int T, int row) { return T + row; }
+
+__device__ __forceinline__ void tc_load_rows(const TcRows &r, uint32_t dst, const CUtensorMap *gather,
+                                             const CUtensorMap *boxes, int col, uint32_t bar)
+{
+    if (r.level >= 0) tma_load_2d(dst, boxes + r.level, col, r.t[0], bar);
+    else if (r.level == -1) tma_gather4(dst, gather, col, r.t[0], r.t[1], r.t[2], r.t[3], bar);
+}
+
+// Host: the maps of one matrix's rows: the gather's, then the boxes'.
+struct TcRowMaps {
+    CUtensorMap gather, box[TC_HEIGHTS];
+};
+static bool encode_row_maps(TcRowMaps *m, const uint16_t *ptr, int64_t rows, int64_t cols, int64_t ld)
+{
+    if (!encode_tile_map(&m->gather, ptr, uint64_t(rows), uint64_t(cols), uint64_t(ld), 64, 1,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+        return false;
+    for (int k = 0; k < TC_HEIGHTS; ++k)
+        if (!encode_tile_map(&m->box[k], ptr, uint64_t(rows), uint64_t(cols), uint64_t(ld), 64, 4u << k,
+                             CU_TENSOR_MAP_SWIZZLE_128B))
+            return false;
+    return true;
+}
+
 // The ring of operand stages and the accumulators' barriers of one CTA.
 struct TcRing {
     uint32_t ring, full, empty, accf, acce, drain, stage_bytes;
@@ -67,20 +132,21 @@ struct TcPos {
     }
 };
 
-// Shared memory: ring, `extra` bytes, barriers; then the caller's tables.
-__device__ __forceinline__ TcRing tc_setup(uint8_t *smem, int stage_bytes, int stages, int extra,
+// Shared memory: `ring` bytes (the stages, and what the kernel keeps behind
+// them), the epilogue's staging, barriers; then the kernel's tables.
+__device__ __forceinline__ TcRing tc_setup(uint8_t *smem, int ring, int stage_bytes, int stages,
                                            int loaders)
 {
     TcRing r;
     r.ring = smem_addr(smem);
-    r.full = r.ring + TC_RING + extra;
+    r.full = r.ring + ring + TC_STAGE_ROWS;
     r.empty = r.full + 8 * TC_MAX_STAGES;
     r.accf = r.empty + 8 * TC_MAX_STAGES;
     r.acce = r.accf + 16;
     r.drain = r.acce + 16;
     r.stage_bytes = uint32_t(stage_bytes);
     r.stages = stages;
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + TC_RING + extra + 16 * TC_MAX_STAGES + 40);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + ring + TC_STAGE_ROWS + 16 * TC_MAX_STAGES + 40);
     r.abort = reinterpret_cast<volatile int *>(misc + 1);
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
@@ -135,20 +201,80 @@ __device__ __forceinline__ void tc_finish(const TcRing &r, int32_t *error_word)
 }
 
 // 32 accumulators of this thread's row as 32 bf16, times f.
-__device__ __forceinline__ void pack32(const uint32_t (&v)[32], float f, uint32_t (&o)[16])
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], float f, uint32_t *o)
 {
 #pragma unroll
     for (int j = 0; j < 16; ++j)
         o[j] = pack_bf16x2(f * __uint_as_float(v[2 * j]), f * __uint_as_float(v[2 * j + 1]));
 }
 
-// Writes the first `many` (a multiple of 8, at most 32) of 32 bf16 values.
-__device__ __forceinline__ void store32(uint16_t *dst, const uint32_t (&o)[16], int many)
+// 64 accumulators from `tmem` on, rounded: 32 words.
+__device__ __forceinline__ void load64(uint32_t tmem, float f, uint32_t (&o)[32])
 {
+    uint32_t v0[32], v1[32];
+    tmem_ld32_nowait(tmem, v0);
+    tmem_ld32_nowait(tmem + 32, v1);
+    tmem_wait_ld();
+    pack32(v0, f, o);
+    pack32(v1, f, o + 16);
+}
+
+// Writes a warp's 32 rows of 64 bf16: lane l holds row l (32 words) and where
+// it goes (null: nowhere); the first `many` columns (a multiple of 8) are
+// written.  Through 4 KB of the warp's shared memory, so that eight lanes
+// write 128 bytes of one row: a store of 16 bytes a lane into 32 rows takes
+// the load/store unit eight times as long.
+__device__ __forceinline__ void store_rows(uint8_t *stage, const uint32_t (&o)[32], uint16_t *dst, int many)
+{
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (8 * j < many)
-            *reinterpret_cast<uint4 *>(dst + 8 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((c ^ lane) & 7) * 16) =
+            make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3);
+        uint16_t *to = reinterpret_cast<uint16_t *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+        if (to != nullptr && 8 * c < many)
+            *reinterpret_cast<uint4 *>(to + 8 * c) =
+                *reinterpret_cast<const uint4 *>(stage + row * 128 + ((c ^ row) & 7) * 16);
+    }
+}
+
+// The same for 32 columns that are added to what is there, in fp32 with one
+// rounding: lane l holds row l's 32 sums.
+__device__ __forceinline__ void add_rows(uint8_t *stage, const uint32_t (&v)[32], float f, uint16_t *dst,
+                                         int many)
+{
+    const int lane = threadIdx.x & 31, c = lane & 7;
+    uint16_t *to[8];
+    uint2 was[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        to[i] = reinterpret_cast<uint16_t *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), 4 * i + (lane >> 3)));
+        was[i] = make_uint2(0u, 0u);
+        if (to[i] != nullptr && 4 * c < many) was[i] = *reinterpret_cast<const uint2 *>(to[i] + 4 * c);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ lane) & 7) * 16) =
+            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + (lane >> 3);
+        if (to[i] == nullptr || 4 * c >= many) continue;
+        const float4 x = *reinterpret_cast<const float4 *>(stage + row * 128 + ((c ^ row) & 7) * 16);
+        *reinterpret_cast<uint2 *>(to[i] + 4 * c) =
+            make_uint2(pack_bf16x2(fmaf(f, x.x, bf16_lo(was[i].x)), fmaf(f, x.y, bf16_hi(was[i].x))),
+                       pack_bf16x2(fmaf(f, x.z, bf16_lo(was[i].y)), fmaf(f, x.w, bf16_hi(was[i].y))));
+    }
 }
 
 __device__ __forceinline__ uint8_t *tc_smem()
@@ -161,12 +287,35 @@ __device__ __forceinline__ uint8_t *tc_smem()
 
 struct GradWTcArgs {
     BackwardArgs b;
-    CUtensorMap dy, x;         // gathers, box 64 columns x 1 row
+    TcRowMaps dy, x;
     CUtensorMap u, g;          // boxes 64 columns x 64 rows of [S * rows][RP]
     int32_t rp, group, groups; // slices of one dA product
     int32_t end[2 * LORA_MAX_SLICES];   // blocks of one adapter: dA groups, then dB slices
-    int32_t kinds, stage_bytes, stages, buffers;
+    int32_t kinds, ring, stage_bytes, stages, buffers;
 };
+
+// The gradients of an adapter without tokens: zeros, written by the 128
+// threads of the epilogue along the rows.
+__device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int id, int s0, int slices,
+                                           int c0, int thread)
+{
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (is_a) {
+        const int chunks = min(16, (p.H - c0) / 8);
+        for (int s = s0; s < s0 + slices; ++s) {
+            if (p.da[s] == nullptr || (thread & 15) >= chunks) continue;
+            uint16_t *out = p.da[s] + int64_t(id) * p.r * p.H + c0 + (thread & 15) * 8;
+            for (int r = thread >> 4; r < p.r; r += 8) *reinterpret_cast<uint4 *>(out + int64_t(r) * p.H) = zero;
+        }
+    } else {
+        const int n = p.n[s0], lo = max(0, c0 - p.off[s0]), hi = min(n, c0 + 128 - p.off[s0]);
+        if (p.db[s0] != nullptr) {
+            uint4 *out = reinterpret_cast<uint4 *>(p.db[s0] + (int64_t(id) * n + lo) * p.r);
+            for (int i = thread; i < (hi - lo) * p.r / 8; i += 128) out[i] = zero;
+        }
+        if (p.dbias[s0] != nullptr && thread < hi - lo) p.dbias[s0][int64_t(id) * n + lo + thread] = 0;
+    }
+}
 
 // dA: rows = (slice, r) in products of 128, columns = 128 of x.
 // dB: rows = 128 columns of dy, columns = r; dbias: one more product with
@@ -178,15 +327,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
     uint8_t *smem = tc_smem();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int RP = q.rp, PPS = RP / 64;                 // panels a slice
-    for (int i = tid; i < TC_PANEL / 4; i += TC_THREADS)
-        reinterpret_cast<uint32_t *>(smem + TC_RING)[i] = 0x3F803F80u;
+    for (int i = tid; i < TC_ONES / 4; i += TC_THREADS)
+        reinterpret_cast<uint32_t *>(smem + q.ring - TC_ONES)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
-    const TcRing ring = tc_setup(smem, q.stage_bytes, q.stages, TC_PANEL, 2);
-    const uint32_t ones = ring.ring + TC_RING;
+    const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
+    const uint32_t ones = ring.ring + q.ring - TC_ONES;
     pdl_wait();
     pdl_launch_dependents();
     int tiles;
-    int *mem = reinterpret_cast<int *>(smem + TC_RING + TC_PANEL + TC_BAR_BYTES);
+    int *mem = reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES);
     const SegTab tab = load_tab(p, mem, tiles);
     const int *seg_of = load_seg_of(p, tab, tiles, mem);
     int *order = mem + backward_tab_words(p.nbins, p.L);
@@ -237,13 +386,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
         const int panel = lane & 1, r4 = (lane >> 1) * 4;
         for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
-            const CUtensorMap *map = it.is_a ? &q.x : &q.dy;
-            int t[4];
+            const TcRowMaps *map = it.is_a ? &q.x : &q.dy;
+            TcRows rows;
             auto tokens = [&](int k) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = k * 64 + r4 + j;
-                    t[j] = row < it.count ? p.sorted[it.start + row] : p.T;
+                    rows.t[j] = row < it.count ? p.sorted[it.start + row] : tc_no_row(p.T, row);
                 }
             };
             if (it.steps > 0) tokens(0);
@@ -254,10 +403,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                     break;
                 }
                 const uint32_t full = ring.full + 8 * pos.stage;
+                join_rows(rows, 2);
                 if (lane == 0) mbar_arrive_expect_tx(full, 2 * TC_PANEL);
                 __syncwarp();
-                tma_gather4(ring.ring + pos.stage * ring.stage_bytes + panel * TC_PANEL + r4 * 128, map,
-                            it.c0 + panel * 64, t[0], t[1], t[2], t[3], full);
+                tc_load_rows(rows, ring.ring + pos.stage * ring.stage_bytes + panel * TC_PANEL + r4 * 128,
+                             &map->gather, map->box, it.c0 + panel * 64, full);
                 if (k + 1 < it.steps) tokens(k + 1);
                 ++issued;
                 pos.next(ring.stages);
@@ -326,7 +476,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                         } else {
                             umma_bf16(d, dz, umma_desc_mn(v + kk * 2048), umma_idesc_bf16(128, RP) | T_AB, acc);
                             if (bias)
-                                umma_bf16(d + uint32_t(RP), dz, umma_desc_mn(ones + kk * 2048),
+                                umma_bf16(d + uint32_t(RP), dz, umma_desc_mn(ones),
                                           umma_idesc_bf16(128, 16) | T_AB, acc);
                         }
                     }
@@ -344,37 +494,29 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
     } else if (warp >= 4) {
         // ------------------------------------------------ epilogue
         const int row = (warp - 4) * 32 + lane;
+        uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
         for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
             const Item it = decode(i);
-            const bool zero = it.steps == 0;
-            const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers)) + (uint32_t((warp - 4) * 32) << 16);
-            if (!zero) {
-                const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
-                if (__all_sync(0xffffffffu, got) == 0) break;
-                tc_fence_after();
+            if (it.steps == 0) {
+                clear_item(p, it.is_a, it.id, it.s, it.slices, it.c0, row);
+                continue;
             }
-            uint32_t v[32], o[16];
-            auto load = [&](uint32_t at) {
-                if (zero) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                } else {
-                    tmem_ld32_nowait(at, v);
-                    tmem_wait_ld();
-                }
-            };
+            const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers)) + (uint32_t((warp - 4) * 32) << 16);
+            const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
+            if (__all_sync(0xffffffffu, got) == 0) break;
+            tc_fence_after();
+            uint32_t o[32];
             if (it.is_a) {
                 const int mt = (it.slices * RP + 127) / 128;
                 for (int m = 0; m < mt; ++m) {
                     const int R = m * 128 + row, s = it.s + R / RP, r = R % RP;
                     uint16_t *out = R < it.slices * RP && r < p.r ? p.da[s] : nullptr;
                     if (out != nullptr) out += (int64_t(it.id) * p.r + r) * p.H + it.c0;
-                    for (int c = 0; c < 128 && it.c0 + c < p.H; c += 32) {
-                        load(d + uint32_t(m * 128 + c));
-                        pack32(v, p.scale, o);
-                        if (out != nullptr) store32(out + c, o, min(32, p.H - it.c0 - c));
+                    for (int c = 0; c < 128 && it.c0 + c < p.H; c += 64) {
+                        load64(d + uint32_t(m * 128 + c), p.scale, o);
+                        store_rows(stage, o, out != nullptr ? out + c : nullptr, p.H - it.c0 - c);
                     }
                 }
             } else {
@@ -382,32 +524,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                 const bool in = at >= 0 && at < n;
                 if (p.db[it.s] != nullptr) {
                     uint16_t *out = p.db[it.s] + (int64_t(it.id) * n + at) * p.r;
-                    for (int c = 0; c < p.r; c += 32) {
-                        load(d + uint32_t(c));
-                        pack32(v, 1.0f, o);
-                        if (in) store32(out + c, o, min(32, p.r - c));
+                    for (int c = 0; c < p.r; c += 64) {
+                        load64(d + uint32_t(c), 1.0f, o);
+                        store_rows(stage, o, in ? out + c : nullptr, p.r - c);
                     }
                 }
                 if (p.dbias[it.s] != nullptr) {
                     uint32_t one[16];
-                    one[0] = 0u;
-                    if (!zero) {
-                        tmem_ld16_nowait(d + uint32_t(RP), one);
-                        tmem_wait_ld();
-                    }
+                    tmem_ld16_nowait(d + uint32_t(RP), one);
+                    tmem_wait_ld();
                     if (in)
                         p.dbias[it.s][int64_t(it.id) * n + at] =
                             uint16_t(pack_bf16x2(__uint_as_float(one[0]), 0.0f) & 0xFFFFu);
                 }
             }
-            if (!zero) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ring.acce + 8 * buf);
-                if (++buf == q.buffers) {
-                    buf = 0;
-                    bphase ^= 1u;
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ring.acce + 8 * buf);
+            if (++buf == q.buffers) {
+                buf = 0;
+                bphase ^= 1u;
             }
         }
     }
@@ -421,10 +557,10 @@ struct GradXTcArgs {
     CUtensorMap g;                       // boxes 64 columns x 128 rows of [S * rows][RP]
     CUtensorMap a[LORA_MAX_SLICES];      // [L][r][H], boxes 64 x 64 x 1
     int32_t rp;
+    int32_t keep;                        // the tile's g stays in shared memory
+    int32_t ring, stages;
 };
 constexpr int TC_X_COLS = 256;
-constexpr int TC_X_STAGE = 6 * TC_PANEL;
-constexpr int TC_X_STAGES = TC_RING / TC_X_STAGE;
 
 // Both segment tables: 64-token tiles (rows of g and u) and 128-token tiles.
 __device__ __forceinline__ int load_tabs(const BackwardArgs &p, int *mem, SegTab &t64, SegTab &t128)
@@ -436,32 +572,58 @@ __device__ __forceinline__ int load_tabs(const BackwardArgs &p, int *mem, SegTab
                          p.T, p.error_word);
 }
 
-// Item: (128-token tile, 256 columns); K = slices x rank.
+// Item: (128-token tile, 256 columns); K = slices x rank.  A CTA takes a run
+// of consecutive items, so it meets few tiles; where the tile's rows of g
+// fit beside three stages of A (slices x rank <= 384) they are loaded once a
+// tile and only A streams (192 instead of 288 KB an item at 384).
 __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_constant__ GradXTcArgs q)
 {
     const BackwardArgs &p = q.b;
     uint8_t *smem = tc_smem();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const TcRing ring = tc_setup(smem, TC_X_STAGE, TC_X_STAGES, 0, 1);
+    const int kps = q.rp / 64, steps = p.S * kps;
+    constexpr int G_BYTES = 2 * TC_PANEL, A_BYTES = 4 * TC_PANEL;
+    const uint32_t stage_bytes = q.keep ? A_BYTES : A_BYTES + G_BYTES;
+    const TcRing ring = tc_setup(smem, q.ring, int(stage_bytes), q.stages, 1);
+    // g of the tile lies behind the ring's stages, one 16 KB block a step
+    const uint32_t g_at = ring.ring + q.stages * stage_bytes;
+    const uint32_t g_full = ring.drain + 24, g_empty = g_full + 8;
+    if (threadIdx.x == 0) {
+        mbar_init(g_full, 1);
+        mbar_init(g_empty, 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     SegTab t64, t128;
-    const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + TC_RING + TC_BAR_BYTES), t64, t128);
+    const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
     const int hb = (p.H + TC_X_COLS - 1) / TC_X_COLS;
     const int64_t items = int64_t(tiles) * hb;
-    const int kps = q.rp / 64, steps = p.S * kps;
+    const int64_t first = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
 
     if (warp == 0) {
         // g and u were written by the stream's previous kernel with ordinary stores
         asm volatile("fence.proxy.async.global;\n" ::: "memory");
         TcPos pos;
-        int issued = 0;
+        int issued = 0, loaded = -1;
+        uint32_t gphase = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        for (int64_t i = first; ok && i < end; ++i) {
             const int tile = int(i / hb), h0 = int(i % hb) * TC_X_COLS;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int64_t row0 = int64_t(t64.tile[seg]) * 64 + int64_t(tile - t128.tile[seg]) * TC_ROWS;
             const int id = t128.id[seg];
+            if (q.keep && tile != loaded) {
+                const bool got = pg_wait(g_empty, gphase ^ 1u, ring.abort);
+                if (__all_sync(0xffffffffu, got) == 0) break;
+                if (lane == 0) mbar_arrive_expect_tx(g_full, uint32_t(steps * G_BYTES));
+                __syncwarp();
+                for (int k = lane; k < steps; k += 32)
+                    tma_load_2d(g_at + k * G_BYTES, &q.g, k % kps * 64, int(k / kps * p.rows + row0), g_full);
+                gphase ^= 1u;
+                loaded = tile;
+            }
             for (int k = 0; k < steps; ++k) {
                 const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
                 if (__all_sync(0xffffffffu, got) == 0) {
@@ -469,26 +631,39 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                     break;
                 }
                 const uint32_t full = ring.full + 8 * pos.stage;
-                const uint32_t at = ring.ring + pos.stage * TC_X_STAGE;
+                const uint32_t at = ring.ring + pos.stage * stage_bytes;
                 const int s = k / kps, kc = k % kps * 64;
-                if (lane == 0) mbar_arrive_expect_tx(full, TC_X_STAGE);
+                if (lane == 0) mbar_arrive_expect_tx(full, stage_bytes);
                 __syncwarp();
-                if (lane == 0) tma_load_2d(at, &q.g, kc, int(s * p.rows + row0), full);
-                else if (lane <= 4)
-                    tma_load_3d(at + (1 + lane) * TC_PANEL, &q.a[s], h0 + (lane - 1) * 64, kc, id, full);
+                if (lane < 4) tma_load_3d(at + lane * TC_PANEL, &q.a[s], h0 + lane * 64, kc, id, full);
+                else if (lane == 4 && !q.keep)
+                    tma_load_2d(at + A_BYTES, &q.g, kc, int(s * p.rows + row0), full);
                 ++issued;
-                pos.next(TC_X_STAGES);
+                pos.next(q.stages);
             }
         }
-        if (lane == 0) tc_drain_loads(ring, issued);
+        if (lane == 0) {
+            tc_drain_loads(ring, issued);
+            // the last tile's g has landed
+            if (loaded >= 0) {
+                const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+                while (!mbar_try_wait(g_full, gphase ^ 1u) && clock64() < dd) {
+                }
+            }
+        }
     } else if (warp == 2) {
         if (lane == 0) {
             TcPos pos;
-            int buf = 0;
-            uint32_t bphase = 0;
+            int buf = 0, tile = -1;
+            uint32_t bphase = 0, gphase = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            for (int64_t i = first; ok && i < end; ++i) {
                 if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
+                if (q.keep && int(i / hb) != tile) {
+                    tile = int(i / hb);
+                    if (!pg_wait(g_full, gphase, ring.abort)) break;
+                    gphase ^= 1u;
+                }
                 tc_fence_after();
                 const uint32_t d = ring.tmem + uint32_t(buf * TC_X_COLS);
                 for (int k = 0; k < steps; ++k) {
@@ -497,25 +672,28 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = ring.ring + pos.stage * TC_X_STAGE, sb = sa + 2 * TC_PANEL;
+                    const uint32_t sb = ring.ring + pos.stage * stage_bytes;
+                    const uint32_t sa = q.keep ? g_at + k * G_BYTES : sb + A_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         umma_bf16(d, umma_desc_sw128(sa + kk * 32), umma_desc_mn(sb + kk * 2048),
                                   umma_idesc_bf16(128, TC_X_COLS) | 1u << 16, k != 0 || kk != 0);
                     umma_commit(ring.empty + 8 * pos.stage);
-                    pos.next(TC_X_STAGES);
+                    pos.next(q.stages);
                 }
                 if (!ok) break;
                 umma_commit(ring.accf + 8 * buf);
+                if (q.keep && i + 1 < end && int((i + 1) / hb) != tile) umma_commit(g_empty);
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1u;
             }
         }
     } else if (warp >= 4) {
         const int row = (warp - 4) * 32 + lane;
+        uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int64_t i = first; i < end; ++i) {
             const int tile = int(i / hb), h0 = int(i % hb) * TC_X_COLS;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int r0 = (tile - t128.tile[seg]) * TC_ROWS;
@@ -526,32 +704,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
             if (__all_sync(0xffffffffu, got) == 0) break;
             tc_fence_after();
             const uint32_t d = ring.tmem + uint32_t(buf * TC_X_COLS) + (uint32_t((warp - 4) * 32) << 16);
-            for (int c = 0; c < TC_X_COLS && h0 + c < p.H; c += 32) {
-                const int many = min(32, p.H - h0 - c);
-                uint32_t v[32], o[16];
-                tmem_ld32_nowait(d + uint32_t(c), v);
-                uint4 was[4];
-                if (p.add && tok >= 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (8 * j < many) was[j] = *reinterpret_cast<const uint4 *>(dst + c + 8 * j);
+            if (p.add) {
+                for (int c = 0; c < TC_X_COLS && h0 + c < p.H; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32_nowait(d + uint32_t(c), v);
+                    tmem_wait_ld();
+                    add_rows(stage, v, p.scale, tok < 0 ? nullptr : dst + c, p.H - h0 - c);
                 }
-                tmem_wait_ld();
-                if (tok < 0) continue;
-                if (p.add) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w[4] = {was[j].x, was[j].y, was[j].z, was[j].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[4 * j + e] = pack_bf16x2(
-                                fmaf(p.scale, __uint_as_float(v[8 * j + 2 * e]), bf16_lo(w[e])),
-                                fmaf(p.scale, __uint_as_float(v[8 * j + 2 * e + 1]), bf16_hi(w[e])));
-                    }
-                } else {
-                    pack32(v, p.scale, o);
+            } else {
+                for (int c = 0; c < TC_X_COLS && h0 + c < p.H; c += 64) {
+                    uint32_t o[32];
+                    load64(d + uint32_t(c), p.scale, o);
+                    store_rows(stage, o, tok < 0 ? nullptr : dst + c, p.H - h0 - c);
                 }
-                store32(dst + c, o, many);
             }
             tc_fence_before();
             __syncwarp();
@@ -568,10 +733,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
 
 struct GradUTcArgs {
     BackwardArgs b;
-    CUtensorMap dy[LORA_MAX_SLICES];     // [T][n_s] of each slice, gathers
+    TcRowMaps dy[LORA_MAX_SLICES];       // [T][n_s] of each slice
     CUtensorMap w[LORA_MAX_SLICES];      // [L][n_s][r], boxes 64 x 64 x 1
     int32_t by_width[LORA_MAX_SLICES];   // slices, widest first
-    int32_t rp, stage_bytes, stages;
+    int32_t rp, ring, stage_bytes, stages;
 };
 
 // Item: (slice, 128-token tile), widest slices first; K = the slice's width.
@@ -580,11 +745,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
     const BackwardArgs &p = q.b;
     uint8_t *smem = tc_smem();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const TcRing ring = tc_setup(smem, q.stage_bytes, q.stages, 0, 2);
+    const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
     pdl_wait();
     pdl_launch_dependents();
     SegTab t64, t128;
-    const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + TC_RING + TC_BAR_BYTES), t64, t128);
+    const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
     const int64_t items = int64_t(tiles) * p.S;
     const int RP = q.rp, panels = RP / 64;
 
@@ -596,10 +761,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
             const int s = q.by_width[i / tiles], tile = int(i % tiles);
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int r0 = (tile - t128.tile[seg]) * TC_ROWS + lane * 4;
-            int t[4];
+            TcRows rows;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                t[j] = r0 + j < t128.count[seg] ? p.sorted[t128.start[seg] + r0 + j] : p.T;
+                rows.t[j] = r0 + j < t128.count[seg] ? p.sorted[t128.start[seg] + r0 + j]
+                                                     : tc_no_row(p.T, r0 + j);
+            join_rows(rows, 1);
             const int steps = (p.n[s] + 63) / 64;
             for (int k = 0; k < steps; ++k) {
                 const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
@@ -610,8 +777,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
                 const uint32_t full = ring.full + 8 * pos.stage;
                 if (lane == 0) mbar_arrive_expect_tx(full, 2 * TC_PANEL);
                 __syncwarp();
-                tma_gather4(ring.ring + pos.stage * ring.stage_bytes + lane * 512, &q.dy[s], k * 64, t[0],
-                            t[1], t[2], t[3], full);
+                tc_load_rows(rows, ring.ring + pos.stage * ring.stage_bytes + lane * 512, &q.dy[s].gather,
+                             q.dy[s].box, k * 64, full);
                 ++issued;
                 pos.next(ring.stages);
             }
@@ -675,6 +842,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
         }
     } else if (warp >= 4) {
         const int row = (warp - 4) * 32 + lane;
+        uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
         for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
@@ -687,30 +855,28 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
                                 ? checked_token(p.sorted[t128.start[seg] + r0 + row], p.T, p.error_word) : -1;
             const int64_t at = (int64_t(s) * p.rows + int64_t(t64.tile[seg]) * 64 + r0 + row) * RP;
             const float *src = p.buf + (int64_t(s) * p.T + (tok < 0 ? 0 : tok)) * p.r;
-            uint32_t v[32], o[16];
-            for (int c = 0; c < RP; c += 32) {
-                float4 f[8];
+            uint32_t o[32];
+            for (int c = 0; c < RP; c += 64) {
+                float4 f[16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     f[j] = make_float4(0, 0, 0, 0);
                     if (tok >= 0 && c + 4 * j < p.r) f[j] = *reinterpret_cast<const float4 *>(src + c + 4 * j);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 16; ++j) {
                     o[2 * j] = pack_bf16x2(f[j].x, f[j].y);
                     o[2 * j + 1] = pack_bf16x2(f[j].z, f[j].w);
                 }
-                if (laid) store32(p.u + at + c, o, 32);
+                store_rows(stage, o, laid ? p.u + at + c : nullptr, 64);
             }
             const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
             if (__all_sync(0xffffffffu, got) == 0) break;
             tc_fence_after();
             const uint32_t d = ring.tmem + uint32_t(buf * 128) + (uint32_t((warp - 4) * 32) << 16);
-            for (int c = 0; c < RP; c += 32) {
-                tmem_ld32_nowait(d + uint32_t(c), v);
-                tmem_wait_ld();
-                pack32(v, 1.0f, o);
-                if (laid) store32(p.g + at + c, o, 32);
+            for (int c = 0; c < RP; c += 64) {
+                load64(d + uint32_t(c), 1.0f, o);
+                store_rows(stage, o, laid ? p.g + at + c : nullptr, 64);
             }
             tc_fence_before();
             __syncwarp();
@@ -734,10 +900,21 @@ static int tc_configure()
     const void *fns[] = {(const void *)grad_w_tc_kernel, (const void *)grad_x_tc_kernel,
                          (const void *)grad_u_tc_kernel};
     for (const void *f : fns)
-        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024)) != cudaSuccess)
+        if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM)) != cudaSuccess)
             return int(e);
     if (dev < 64) configured[dev] = 1;
     return 0;
+}
+
+// What the ring may take beside `tables` words, in whole KB.
+static int tc_ring_bytes(int64_t words)
+{
+    return int((TC_SMEM - 1024 - TC_STAGE_ROWS - TC_BAR_BYTES - words * 4) / 1024 * 1024);
+}
+
+static int tc_stages(int ring, int stage_bytes)
+{
+    return ring / stage_bytes < TC_MAX_STAGES ? ring / stage_bytes : TC_MAX_STAGES;
 }
 
 int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
@@ -766,16 +943,13 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     // empty: its second half reads the (unused) next panel of the stage
     const int panels = has_a ? (q.group * (rp / 64) + 1) / 2 * 2 : rp / 64;
     q.stage_bytes = (2 + panels) * TC_PANEL;
-    q.stages = TC_RING / q.stage_bytes < TC_MAX_STAGES ? TC_RING / q.stage_bytes : TC_MAX_STAGES;
+    q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L);
+    q.stages = tc_stages(q.ring - TC_ONES, q.stage_bytes);
+    if (q.stages < 2) return -1;
     const int cols_a = has_a ? (q.group * rp + 127) / 128 * 128 : 0;
     q.buffers = cols_a <= 256 ? 2 : 1;
-    const int smem = TC_RING + TC_PANEL + TC_BAR_BYTES + 1024 +
-                     (backward_tab_words(p.nbins, p.L) + p.L) * 4;
-    if (smem > 227 * 1024) return -1;
-    if (!encode_tile_map(&q.dy, p.dy, uint64_t(p.T), uint64_t(p.width), uint64_t(p.dy_ld), 64, 1,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tile_map(&q.x, p.x, uint64_t(p.T), uint64_t(p.H), uint64_t(p.x_ld), 64, 1,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!encode_row_maps(&q.dy, p.dy, p.T, p.width, p.dy_ld) ||
+        !encode_row_maps(&q.x, p.x, p.T, p.H, p.x_ld) ||
         !encode_tile_map(&q.u, p.u, uint64_t(p.S) * p.rows, uint64_t(rp), uint64_t(rp), 64, 64,
                          CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tile_map(&q.g, p.g, uint64_t(p.S) * p.rows, uint64_t(rp), uint64_t(rp), 64, 64,
@@ -785,7 +959,7 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     const int64_t items = int64_t(p.L) * blocks;
     const int sms = device_sm_count();
     return int(launch_kernel(grad_w_tc_kernel, dim3(unsigned(items < sms ? items : sms)), dim3(TC_THREADS),
-                             size_t(smem), st, q));
+                             size_t(TC_SMEM), st, q));
 }
 
 int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
@@ -794,16 +968,18 @@ int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     static thread_local GradXTcArgs q;
     q.b = p;
     q.rp = rp;
-    const int smem = TC_RING + TC_BAR_BYTES + 1024 + 2 * int(seg_tab_bytes(p.nbins));
-    if (smem > 227 * 1024) return -1;
     if (!encode_tile_map(&q.g, p.g, uint64_t(p.S) * p.rows, uint64_t(rp), uint64_t(rp), 64, 128,
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return -1;
     for (int s = 0; s < p.S; ++s)
         if (!encode_stack_map(&q.a[s], p.a[s], uint64_t(p.L), uint64_t(p.r), uint64_t(p.H), 64, 64)) return -1;
+    const int g_bytes = p.S * (rp / 64) * 2 * TC_PANEL;
+    q.ring = tc_ring_bytes(2 * (4 * p.nbins + 2));
+    q.keep = q.ring - g_bytes >= 2 * 4 * TC_PANEL;
+    q.stages = q.keep ? tc_stages(q.ring - g_bytes, 4 * TC_PANEL) : tc_stages(q.ring, 6 * TC_PANEL);
     if (int e = tc_configure()) return e;
     return int(launch_kernel(grad_x_tc_kernel, dim3(unsigned(device_sm_count())), dim3(TC_THREADS),
-                             size_t(smem), st, q));
+                             size_t(TC_SMEM), st, q));
 }
 
 int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st)
@@ -815,12 +991,9 @@ int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     static thread_local GradUTcArgs q;
     q.b = p;
     q.rp = rp;
-    const int smem = TC_RING + TC_BAR_BYTES + 1024 + 2 * int(seg_tab_bytes(p.nbins));
-    if (smem > 227 * 1024) return -1;
     for (int s = 0; s < p.S; ++s) {
         if (p.off[s] % 8 != 0) return -1;            // a gather starts on a 16-byte boundary
-        if (!encode_tile_map(&q.dy[s], p.dy + p.off[s], uint64_t(p.T), uint64_t(p.n[s]), uint64_t(p.dy_ld),
-                             64, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        if (!encode_row_maps(&q.dy[s], p.dy + p.off[s], p.T, p.n[s], p.dy_ld) ||
             !encode_stack_map(&q.w[s], p.b[s], uint64_t(p.L), uint64_t(p.n[s]), uint64_t(p.r), 64, 64))
             return -1;
         int at = s;
@@ -828,10 +1001,11 @@ int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st)
         q.by_width[at] = s;
     }
     q.stage_bytes = (2 + rp / 64) * TC_PANEL;
-    q.stages = TC_RING / q.stage_bytes < TC_MAX_STAGES ? TC_RING / q.stage_bytes : TC_MAX_STAGES;
+    q.ring = tc_ring_bytes(2 * (4 * p.nbins + 2));
+    q.stages = tc_stages(q.ring, q.stage_bytes);
     if (int e = tc_configure()) return e;
     return int(launch_kernel(grad_u_tc_kernel, dim3(unsigned(device_sm_count())), dim3(TC_THREADS),
-                             size_t(smem), st, q));
+                             size_t(TC_SMEM), st, q));
 }
 
 }  // namespace lora
