@@ -81,9 +81,14 @@ def _call(fn: str, device: torch.device, *args) -> None:
     """Calls library entry point `fn` with `device` current (the library
     looks up per-device state for the current device), then raises on a
     non-zero status."""
-    with torch.cuda.device(device):
-        st = getattr(_lib.load(), fn)(*args)
-    _lib.check(fn, st)
+    f = getattr(_lib.load(), fn)
+    if device.index is None or device.index == torch.cuda.current_device():
+        st = f(*args)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args)
+    if st:
+        _lib.check(fn, st)
 
 
 def _ptr_array(tensors) -> ctypes.Array:
@@ -397,6 +402,31 @@ def lora_linear_noalloc(token_lora_mapping: torch.Tensor, x: torch.Tensor, lora_
 
 
 # ------------------------------------------------------------ training the adapters
+#
+# These calls are short enough for the checks to show in a small batch, so
+# each makes one quick pass over its tensors and words the error only when
+# something is wrong.
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _all(index: int, *named) -> None:
+    """Each (tensor or None, dtype, name) is a CUDA tensor of that type on GPU `index`."""
+    for t, dtype, name in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
+            _need(t, name, dtype)
+            raise ValueError("%s is on cuda:%d, expected cuda:%d" % (name, t.get_device(), index))
+
+
+def _gpu(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (no CPU path exists)" % name)
+    return t.get_device()
+
 
 def _workspace_bytes(fn: str, device, *args) -> int:
     with torch.cuda.device(device):
@@ -406,40 +436,37 @@ def _workspace_bytes(fn: str, device, *args) -> int:
     return int(n)
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
-    """The caller's workspace after its checks, or a new one."""
+def _call_with(fn: str, workspace: Optional[torch.Tensor], device, size_args, *args) -> None:
+    """Calls fn(*args, workspace, its bytes, the current stream); the
+    workspace is allocated when None."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    _need(workspace, "workspace", torch.uint8)
-    if not workspace.is_contiguous() or workspace.numel() < need:
-        raise ValueError("workspace must be contiguous with at least %d bytes" % need)
-    return workspace
+        workspace = torch.empty(_workspace_bytes(fn + "_workspace", device, *size_args), dtype=_U8,
+                                device=device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    try:
+        _call(fn, device, *args, workspace.data_ptr(), workspace.numel(), _stream_handle(device))
+    except LoraError as e:
+        if e.status == _lib.LORA_ERR_WORKSPACE:
+            raise ValueError("workspace must have at least %d bytes"
+                             % _workspace_bytes(fn + "_workspace", device, *size_args)) from e
+        raise
 
 
-def _same_gpu(ref: torch.Tensor, named) -> None:
-    for name, t in named:
-        if t is not None and t.get_device() != ref.get_device():
-            raise ValueError("%s is on cuda:%d, expected cuda:%d"
-                             % (name, t.get_device(), ref.get_device()))
-
-
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype) -> torch.Tensor:
-    """A [rows, cols] view of t whose rows are contiguous."""
-    _need(t, name, dtype)
-    t2 = t.view(-1, t.shape[-1]) if t.dim() != 2 else t
-    if t2.stride(1) != 1 and t2.size(1) > 1 or t2.size(0) > 1 and t2.stride(0) < t2.size(1):
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, row stride) of t as a matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        t = t.view(-1, t.shape[-1])
+    n, c = t.shape
+    ld = t.stride(0)
+    if (c > 1 and t.stride(1) != 1) or (n > 1 and ld < c):
         raise ValueError("%s needs contiguous rows that do not overlap" % name)
-    return t2
+    return n, c, max(ld, c)
 
 
-def _ld(t2: torch.Tensor) -> int:
-    return max(t2.stride(0), t2.size(1))
-
-
-def _vector(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int) -> Optional[int]:
+def _vector(t: Optional[torch.Tensor], name: str, n: int) -> Optional[int]:
     if t is None:
         return None
-    _need(t, name, dtype)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError("%s must be contiguous with %d elements" % (name, n))
     return t.data_ptr()
@@ -469,38 +496,30 @@ def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
     and weight_grad (bf16, like weight) are overwritten when given;
     error_word (int32 [1]) receives the count of targets >= vocab.  A
     workspace (uint8) is allocated when none is given."""
-    h = _rows(hidden, "hidden", torch.bfloat16)
-    T, H = h.shape
-    _need(weight, "weight", torch.bfloat16)
-    if weight.dim() != 2 or weight.size(1) != H or not weight.is_contiguous():
+    _all(_gpu(hidden, "hidden"), (hidden, _BF16, "hidden"), (weight, _BF16, "weight"),
+         (targets, _I32, "targets"), (loss, _F32, "loss"), (token_weight, _F32, "token_weight"),
+         (logsumexp, _F32, "logsumexp"), (hidden_grad, _BF16, "hidden_grad"),
+         (weight_grad, _BF16, "weight_grad"), (error_word, _I32, "error_word"),
+         (workspace, _U8, "workspace"))
+    T, H, ld = _rows(hidden, "hidden")
+    if weight.dim() != 2 or weight.shape[1] != H or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous [vocab, %d] tensor" % H)
-    V = weight.size(0)
-    _need(loss, "loss", torch.float32)
-    t_ptr = _vector(targets, "targets", torch.int32, T)
-    l_ptr = _vector(loss, "loss", torch.float32, T)
-    w_ptr = _vector(token_weight, "token_weight", torch.float32, T)
-    s_ptr = _vector(logsumexp, "logsumexp", torch.float32, T)
-    e_ptr = _vector(error_word, "error_word", torch.int32, 1)
-    dh = None
+    V = weight.shape[0]
+    dh, dh_ld, dw = None, H, None
     if hidden_grad is not None:
-        dh = _rows(hidden_grad, "hidden_grad", torch.bfloat16)
-        if dh.shape != h.shape:
+        rows, cols, dh_ld = _rows(hidden_grad, "hidden_grad")
+        if (rows, cols) != (T, H):
             raise ValueError("hidden_grad must be [%d, %d]" % (T, H))
+        dh = hidden_grad.data_ptr()
     if weight_grad is not None:
-        _need(weight_grad, "weight_grad", torch.bfloat16)
         if weight_grad.shape != weight.shape or not weight_grad.is_contiguous():
             raise ValueError("weight_grad must be contiguous like weight")
-    _same_gpu(hidden, [("weight", weight), ("targets", targets), ("loss", loss),
-                       ("token_weight", token_weight), ("logsumexp", logsumexp),
-                       ("hidden_grad", hidden_grad), ("weight_grad", weight_grad),
-                       ("error_word", error_word), ("workspace", workspace)])
-    dev = hidden.device
-    ws = _workspace(workspace, lora_cross_entropy_workspace(
-        T, H, V, hidden_grad=dh is not None, weight_grad=weight_grad is not None, device=dev), dev)
-    _call("lora_cross_entropy", dev, h.data_ptr(), T, H, _ld(h), weight.data_ptr(), V, t_ptr, w_ptr,
-          l_ptr, s_ptr, None if dh is None else dh.data_ptr(), H if dh is None else _ld(dh),
-          None if weight_grad is None else weight_grad.data_ptr(), e_ptr, ws.data_ptr(), ws.numel(),
-          _stream_handle(dev))
+        dw = weight_grad.data_ptr()
+    _call_with("lora_cross_entropy", workspace, hidden.device,
+               (T, H, V, int(dh is not None), int(dw is not None)),
+               hidden.data_ptr(), T, H, ld, weight.data_ptr(), V, _vector(targets, "targets", T),
+               _vector(token_weight, "token_weight", T), _vector(loss, "loss", T),
+               _vector(logsumexp, "logsumexp", T), dh, dh_ld, dw, _vector(error_word, "error_word", 1))
 
 
 def lora_linear_backward_workspace(num_tokens: int, hidden: int, output_slices, rank: int,
@@ -511,11 +530,25 @@ def lora_linear_backward_workspace(num_tokens: int, hidden: int, output_slices, 
                             len(output_slices), rank, max_loras)
 
 
-def _grad_array(grads, name: str, like):
-    """Pointer array of the gradients `grads` (None, or one tensor or None
-    per slice), each shaped as the entry of `like`; and the tensors."""
+def _stacks(ws, name: str, index: int) -> Sequence[torch.Tensor]:
+    """One bf16 [max_loras, rows, cols] stack per slice on GPU `index` (a
+    singleton layer dimension, [L, 1, rows, cols], is taken out)."""
+    if isinstance(ws, torch.Tensor):
+        ws = (ws,)
+    for w in ws:
+        if (not isinstance(w, torch.Tensor) or w.dtype is not _BF16 or w.get_device() != index
+                or w.dim() != 3 or not w.is_contiguous()):
+            ws = _weights(ws, name)
+            _all(index, *((w, _BF16, "%s[%d]" % (name, i)) for i, w in enumerate(ws)))
+            break
+    return ws
+
+
+def _grads(grads, name: str, like, index: int):
+    """Pointer array of the gradients (None, or a tensor or None per slice),
+    each with the elements and outer sizes of the shape in `like`."""
     if grads is None:
-        return None, []
+        return None
     if isinstance(grads, torch.Tensor):
         grads = (grads,)
     if len(grads) != len(like):
@@ -523,11 +556,13 @@ def _grad_array(grads, name: str, like):
     for i, (g, shape) in enumerate(zip(grads, like)):
         if g is None:
             continue
-        _need(g, "%s[%d]" % (name, i), torch.bfloat16)
-        if g.numel() != math.prod(shape) or g.shape[0] != shape[0] or g.shape[-1] != shape[-1] \
+        if not isinstance(g, torch.Tensor) or g.dtype is not _BF16 or g.get_device() != index:
+            _all(index, (g, _BF16, "%s[%d]" % (name, i)))
+        s = g.shape
+        if (s != shape and (g.numel() != math.prod(shape) or s[0] != shape[0] or s[-1] != shape[-1])) \
                 or not g.is_contiguous():
             raise ValueError("%s[%d] must be a contiguous %s tensor" % (name, i, list(shape)))
-    return _ptr_array(grads), [("%s[%d]" % (name, i), g) for i, g in enumerate(grads)]
+    return _ptr_array(grads)
 
 
 def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor, lora_a_stacked,
@@ -543,54 +578,44 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     to it, or with add_inputs=False it is overwritten.  d_lora_a, d_lora_b,
     d_lora_bias: one tensor (or None) per slice, shaped as the weights and
     biases, overwritten; adapters without tokens get zeros."""
-    dy2, x2 = _rows(dy, "dy", torch.bfloat16), _rows(x, "x", torch.bfloat16)
-    A = _weights(lora_a_stacked, "lora_a_stacked")
-    B = _weights(lora_b_stacked, "lora_b_stacked")
-    if len(A) != len(B):
-        raise ValueError("lora_a_stacked and lora_b_stacked differ in length")
-    T, H = x2.shape
-    S, (L, r, _) = len(A), A[0].shape
-    if any(a.shape != (L, r, H) for a in A):
+    index = meta.no_lora_flag.get_device()
+    _gpu(dy, "dy")
+    _all(index, (dy, _BF16, "dy"), (x, _BF16, "x"), (buffer, _F32, "buffer"), (dx, _BF16, "dx"),
+         (workspace, _U8, "workspace"))
+    A = _stacks(lora_a_stacked, "lora_a_stacked", index)
+    B = _stacks(lora_b_stacked, "lora_b_stacked", index)
+    S = len(A)
+    if S != len(B) or S == 0:
+        raise ValueError("lora_a_stacked and lora_b_stacked differ in length or are empty")
+    T, H, x_ld = _rows(x, "x")
+    a_shapes, b_shapes = [w.shape for w in A], [w.shape for w in B]
+    L, r, _ = a_shapes[0]
+    if any(s != (L, r, H) for s in a_shapes):
         raise ValueError("lora_a_stacked shapes must all be [%d, %d, %d]" % (L, r, H))
-    if any(b.size(0) != L or b.size(2) != r for b in B):
+    if any(s[0] != L or s[2] != r for s in b_shapes):
         raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (L, r))
     if L != meta.max_loras:
         raise ValueError("the weights hold %d LoRAs, the metadata %d" % (L, meta.max_loras))
-    sizes = [b.size(1) for b in B]
-    if dy2.size(0) != T or dy2.size(1) != sum(sizes):
+    sizes = [s[1] for s in b_shapes]
+    rows, cols, dy_ld = _rows(dy, "dy")
+    if rows != T or cols != sum(sizes):
         raise ValueError("dy must be [%d, %d]" % (T, sum(sizes)))
-    _need(buffer, "buffer", torch.float32)
-    if tuple(buffer.shape) != (S, T, r) or not buffer.is_contiguous():
+    if buffer.shape != (S, T, r) or not buffer.is_contiguous():
         raise ValueError("buffer must be a contiguous fp32 [%d, %d, %d] tensor" % (S, T, r))
-    dx2 = None
+    dx_ptr, dx_ld = None, H
     if dx is not None:
-        dx2 = _rows(dx, "dx", torch.bfloat16)
-        if dx2.shape != x2.shape:
+        rows, cols, dx_ld = _rows(dx, "dx")
+        if rows != T or cols != H:
             raise ValueError("dx must be [%d, %d]" % (T, H))
-    da, named_a = _grad_array(d_lora_a, "d_lora_a", [tuple(a.shape) for a in A])
-    db, named_b = _grad_array(d_lora_b, "d_lora_b", [tuple(b.shape) for b in B])
-    dbias, named_c = _grad_array(d_lora_bias, "d_lora_bias", [(L, n) for n in sizes])
-    _same_device(meta, [("dy", dy), ("x", x), ("buffer", buffer), ("dx", dx),
-                        ("workspace", workspace)] + named_a + named_b + named_c +
-                 [("lora_a_stacked[%d]" % i, a) for i, a in enumerate(A)] +
-                 [("lora_b_stacked[%d]" % i, b) for i, b in enumerate(B)])
-    dev = x.device
-    ws = _workspace(workspace, lora_linear_backward_workspace(T, H, sizes, r, L, device=dev), dev)
-    _call("lora_linear_backward", dev, dy2.data_ptr(), _ld(dy2), T, x2.data_ptr(), H, _ld(x2),
-          buffer.data_ptr(), _ptr_array(A), _ptr_array(B), (ctypes.c_int32 * S)(*sizes), S, r,
-          float(scale), None if dx2 is None else dx2.data_ptr(), H if dx2 is None else _ld(dx2),
-          1 if add_inputs else 0, da, db, dbias, ctypes.byref(meta.c), ws.data_ptr(), ws.numel(),
-          _stream_handle(dev))
-
-
-def _stack(t: torch.Tensor, name: str):
-    """(count, rows, cols) of a dense stack of matrices (any leading dimensions)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if t.dim() < 2 or not t.is_contiguous():
-        raise ValueError("%s must be contiguous [..., rows, cols]" % name)
-    rows, cols = t.shape[-2:]
-    return t.numel() // max(1, rows * cols), rows, cols
+        dx_ptr = dx.data_ptr()
+    c_sizes = (ctypes.c_int32 * S)(*sizes)
+    _call_with("lora_linear_backward", workspace, x.device, (T, H, c_sizes, S, r, L),
+               dy.data_ptr(), dy_ld, T, x.data_ptr(), H, x_ld, buffer.data_ptr(), _ptr_array(A),
+               _ptr_array(B), c_sizes, S, r, float(scale), dx_ptr, dx_ld, 1 if add_inputs else 0,
+               _grads(d_lora_a, "d_lora_a", a_shapes, index),
+               _grads(d_lora_b, "d_lora_b", b_shapes, index),
+               _grads(d_lora_bias, "d_lora_bias", [(L, n) for n in sizes], index),
+               ctypes.byref(meta.c))
 
 
 def lora_orthogonalize_workspace(count: int, rows: int, cols: int, *, device="cuda") -> int:
@@ -601,25 +626,28 @@ def lora_orthogonalize_workspace(count: int, rows: int, cols: int, *, device="cu
 def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 5,
                        scale: float = 1.0, eps: float = 1e-7,
                        coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                       error_word: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None) -> None:
     """Newton-Schulz orthogonalisation of stacked updates, as the Muon
     optimiser takes them: every matrix of update [..., rows, cols] (bf16 or
     fp32; the shorter side, an adapter's rank, at most 128) divided by its
     norm and taken through ``steps`` of X <- a X + (b G + c G^2) X, G = X X^T;
-    out (bf16, like update, or update itself) receives scale * X."""
-    count, rows, cols = _stack(update, "update")
-    if update.dtype not in (torch.bfloat16, torch.float32):
+    out (bf16, like update, or update itself) receives scale * X.  Bit 30 of
+    error_word (int32 [1]) is set if a bounded wait on the GPU ran out."""
+    index = _gpu(update, "update")
+    f32 = update.dtype is _F32
+    if not f32 and update.dtype is not _BF16:
         raise TypeError("update must be bfloat16 or float32, got %s" % update.dtype)
-    _need(update, "update", update.dtype)
-    _need(out, "out", torch.bfloat16)
-    if out.shape != update.shape or not out.is_contiguous():
+    _all(index, (out, _BF16, "out"), (error_word, _I32, "error_word"), (workspace, _U8, "workspace"))
+    if out is None or out.shape != update.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous like update")
+    if update.dim() < 2 or not update.is_contiguous():
+        raise ValueError("update must be contiguous [..., rows, cols]")
     if len(coefficients) != 3:
         raise ValueError("coefficients must be three numbers")
-    _same_gpu(update, [("out", out), ("workspace", workspace)])
-    dev = update.device
-    ws = _workspace(workspace, lora_orthogonalize_workspace(count, rows, cols, device=dev), dev)
-    a, b, c = (float(v) for v in coefficients)
-    _call("lora_orthogonalize", dev, update.data_ptr(), int(update.dtype == torch.float32), count,
-          rows, cols, int(steps), a, b, c, float(eps), float(scale), out.data_ptr(), ws.data_ptr(),
-          ws.numel(), _stream_handle(dev))
+    rows, cols = update.shape[-2:]
+    count = update.numel() // max(1, rows * cols)
+    a, b, c = coefficients
+    _call_with("lora_orthogonalize", workspace, update.device, (count, rows, cols), update.data_ptr(),
+               int(f32), count, rows, cols, int(steps), float(a), float(b), float(c), float(eps),
+               float(scale), out.data_ptr(), _vector(error_word, "error_word", 1))

@@ -23,6 +23,7 @@ LORA_MAX_SLICES = 8
 LORA_MAX_LORAS = 1024
 LORA_MAX_RANK = 128
 LORA_NOALLOC_MAX_FLOATS = 1 << 20
+LORA_ERR_WORKSPACE = -10
 
 
 class LoraMetaC(ctypes.Structure):
@@ -102,7 +103,7 @@ def load(path: str | None = None):
         lib.lora_linear_backward_workspace.argtypes = [_I32, _I32, _P, _I32, _I32, _I32]
         lib.lora_linear_backward_workspace.restype = _I64
         lib.lora_orthogonalize.argtypes = [_P, _I32, _I32, _I32, _I32, _I32, _F, _F, _F, _F, _F,
-                                           _P, _P, _I64, _P]
+                                           _P, _P, _P, _I64, _P]
         lib.lora_orthogonalize.restype = ctypes.c_int
         lib.lora_orthogonalize_workspace.argtypes = [_I32, _I32, _I32]
         lib.lora_orthogonalize_workspace.restype = _I64

@@ -8,65 +8,21 @@
 // and U is read twice (G_0; P U) instead of twice a step.  |U|_F^2 is the
 // trace of U U^T.
 //
-// Three kernels: gram_kernel sums U U^T over shares of the long side (the
-// shares are joined in a fixed order), iterate_kernel runs the steps on one
-// matrix a block in fp32, apply_kernel writes P U.  The products with U run
-// on the tensor cores with U exact: bf16 as it is, fp32 as a sum of two
-// bf16 values (relative 2^-17), P as a sum of two bf16 values -- P holds
-// factors up to a^n = 485 for directions that U has little of, which cancel
-// where U is large, so one bf16 would show in the result.
+// Three kernels: gram_kernel sums U U^T over even runs of the long sides of
+// all matrices, iterate_kernel runs the steps on one matrix a block in fp32,
+// apply_kernel writes P U.  The products with U run on the tensor cores with
+// U exact: bf16 as it is, fp32 as a sum of two bf16 values (relative 2^-17),
+// P as a sum of two bf16 values -- P holds factors up to a^n = 485 for
+// directions that U has little of, which cancel where U is large, so one
+// bf16 would show in the result.
+//
+// This file: ranks up to 64, on mma.sync and FFMA.  lora_ortho_tc.cu: ranks
+// to 128, on tcgen05.
 #include <math.h>
 
-#include "lora_frag.cuh"
+#include "lora_ortho.cuh"
 
 namespace lora {
-
-constexpr int OR_THREADS = 256;
-constexpr int OR_MAX_RANK = 128;
-
-struct OrthoArgs {
-    const void *u;
-    uint16_t *out;
-    int32_t count, rows, cols;    // matrices, each [rows, cols]
-    int32_t r, n;                 // short and long side
-    int32_t shares;               // of the long side in gram_kernel
-    int32_t share;                // its length, a multiple of the K step
-    int32_t steps;
-    float a, b, c, eps, scale;
-    float *gram;                  // [count][shares][RP][RP]
-    uint16_t *p;                  // [count][2][RP][RP]: P as two bf16 terms
-};
-
-// Eight consecutive elements of U as bf16 terms: hi, and (fp32) what hi
-// leaves over.
-template <bool F32>
-struct Chunk {
-    uint4 hi, lo;
-};
-
-template <bool F32>
-__device__ __forceinline__ Chunk<F32> load_chunk(const void *u, int64_t at, bool valid)
-{
-    Chunk<F32> c;
-    c.hi = c.lo = make_uint4(0, 0, 0, 0);
-    if (!valid) return c;
-    if constexpr (F32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(u) + at);
-        const float4 x = src[0], y = src[1];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            l[i] = pack_bf16x2(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
-        }
-        c.hi = make_uint4(h[0], h[1], h[2], h[3]);
-        c.lo = make_uint4(l[0], l[1], l[2], l[3]);
-    } else {
-        c.hi = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at);
-    }
-    return c;
-}
 
 // ---------------------------------------------------------------- gram
 
@@ -75,10 +31,9 @@ template <int RP> struct GramShape;
 template <> struct GramShape<16> { static constexpr int WM = 1, WN = 1, WK = 8; };
 template <> struct GramShape<32> { static constexpr int WM = 1, WN = 1, WK = 8; };
 template <> struct GramShape<64> { static constexpr int WM = 2, WN = 1, WK = 4; };
-template <> struct GramShape<128> { static constexpr int WM = 4, WN = 2, WK = 1; };
 
 template <int RP>
-constexpr int gram_step() { return RP == 128 ? 64 : RP == 64 ? 128 : 256; }
+constexpr int gram_step() { return RP == 64 ? 128 : 256; }
 
 template <int RP, bool F32>
 constexpr int gram_smem()
@@ -88,8 +43,8 @@ constexpr int gram_smem()
     return 2 * tile > join ? 2 * tile : join;
 }
 
-// Block (share, matrix): the sum over its share of the long side.  TALL: U
-// is [n][r] (its rows are K), else [r][n].
+// Each block sums over its run of units.  TALL: U is [n][r] (its rows are
+// K), else [r][n].
 template <int RP, bool TALL, bool F32>
 __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
 {
@@ -101,7 +56,7 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
     constexpr int TERMS = F32 ? 2 : 1;
     constexpr int PER = ROWS * CPR / OR_THREADS;                    // chunks a thread loads
     constexpr int MI = RP / WM / 16, NI = RP / WN / 8;
-    static_assert(PER >= 1 && MI >= 1 && NI >= 2, "shape");
+    static_assert(PER >= 1 && MI >= 1 && NI >= 2 && WK > 1, "shape");
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -109,17 +64,17 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
     const int m0 = wm * (RP / WM), n0 = wn * (RP / WN);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t mat = int64_t(blockIdx.y) * p.rows * p.cols;
-    const int k_lo = blockIdx.x * p.share, k_hi = min(p.n, k_lo + p.share);
+    const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
 
     Chunk<F32> next[PER];
-    auto fetch = [&](int k) {
+    auto fetch = [&](int64_t unit) {
+        const int64_t mat = unit / p.units * p.rows * p.cols;
+        const int k = int(unit % p.units) * KS;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
             const int gr = TALL ? k + row : row, gc = (TALL ? 0 : k) + ch * 8;
-            const bool ok = TALL ? (gr < k_hi && gc < p.r) : (gr < p.r && gc < k_hi);
-            next[i] = load_chunk<F32>(p.u, mat + int64_t(gr) * p.cols + gc, ok);
+            next[i] = load_chunk<F32>(p.u, mat + int64_t(gr) * p.cols + gc, gr < p.rows && gc < p.cols);
         }
     };
     auto put = [&](int buf) {
@@ -133,11 +88,11 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
     };
     float acc[MI][NI][4] = {};
     int buf = 0;
-    if (k_lo < k_hi) fetch(k_lo);
-    for (int k = k_lo; k < k_hi; k += KS) {
+    if (first < end) fetch(first);
+    for (int64_t unit = first; unit < end; ++unit) {
         put(buf);
         __syncthreads();
-        if (k + KS < k_hi) fetch(k + KS);
+        if (unit + 1 < end) fetch(unit + 1);
         const uint32_t hi = base + buf * TILE * TERMS;
 #pragma unroll 2
         for (int kk = wk * (KS / WK); kk < (wk + 1) * (KS / WK); kk += 16) {
@@ -166,10 +121,10 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
             }
         }
         buf ^= 1;
-    }
-    float *out = p.gram + (int64_t(blockIdx.y) * p.shares + blockIdx.x) * RP * RP;
-    const int g = (tid & 31) >> 2, t = tid & 3;
-    if constexpr (WK > 1) {
+        if (unit + 1 < end && (unit + 1) % p.units != 0) continue;
+        // the matrix or the run ends: the warps' sums over K, joined
+        float *out = p.gram + (blockIdx.x + unit / p.units) * RP * RP;
+        const int g = (tid & 31) >> 2, t = tid & 3;
         __syncthreads();
         float *part = reinterpret_cast<float *>(smem) + wk * RP * RP;
 #pragma unroll
@@ -181,6 +136,7 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
                 at[1] = acc[i][j][1];
                 at[8 * RP] = acc[i][j][2];
                 at[8 * RP + 1] = acc[i][j][3];
+                acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
             }
         __syncthreads();
         for (int i = tid; i < RP * RP; i += OR_THREADS) {
@@ -188,22 +144,15 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
             for (int w = 0; w < WK; ++w) s += reinterpret_cast<float *>(smem)[w * RP * RP + i];
             out[i] = s;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                float *at = out + (m0 + 16 * i + g) * RP + n0 + 8 * j + 2 * t;
-                *reinterpret_cast<float2 *>(at) = make_float2(acc[i][j][0], acc[i][j][1]);
-                *reinterpret_cast<float2 *>(at + 8 * RP) = make_float2(acc[i][j][2], acc[i][j][3]);
-            }
+        __syncthreads();
     }
 }
 
 // ---------------------------------------------------------------- iterate
 
-// C = A B for symmetric A, each thread an E x E block: sum over k of rows k
-// of A and B.
+// C = A B where A, B and C are symmetric (polynomials in one matrix): one
+// E x E block (ty, tx) on or above the diagonal a thread, the sum over k of
+// rows k of A and B.
 template <int RP, int E>
 __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int tx, float (&c)[E][E])
 {
@@ -211,7 +160,7 @@ __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int 
     for (int i = 0; i < E; ++i)
 #pragma unroll
         for (int j = 0; j < E; ++j) c[i][j] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < RP; ++k) {
         float a[E], b[E];
 #pragma unroll
@@ -225,7 +174,9 @@ __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int 
     }
 }
 
-// One block per matrix; R, P, Q in shared memory.
+// One block per matrix; R, P, Q in shared memory, in fp32.  The 136 blocks
+// on or above the diagonal of a 16 x 16 grid are a thread's each; the rest
+// is their mirror image.  (All 256 blocks by 256 threads: 49 us at rank 64.)
 template <int RP>
 __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
 {
@@ -233,15 +184,16 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
     extern __shared__ __align__(128) float sm[];
     float *R = sm, *P = R + RP * RP, *Q = P + RP * RP;
     __shared__ float s_norm;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    const int tid = threadIdx.x, m = blockIdx.x;
+    int ty = 0, tx = tid;                     // the tid-th block, row by row
+    while (ty < 16 && tx >= 16 - ty) tx -= 16 - ty++;
+    const bool mine = ty < 16;
+    tx += ty;
     pdl_wait();
     pdl_launch_dependents();
-    const float *gram = p.gram + int64_t(blockIdx.x) * p.shares * RP * RP;
+    const int lo = unit_cta(p, int64_t(m) * p.units), hi = unit_cta(p, int64_t(m + 1) * p.units - 1);
     for (int i = tid; i < RP * RP; i += OR_THREADS) {
-        float s = 0.0f;
-        for (int q = 0; q < p.shares; ++q) s += gram[int64_t(q) * RP * RP + i];
-        R[i] = s;
-        P[i] = i / RP == i % RP ? 1.0f : 0.0f;
+        R[i] = gram_sum<RP>(p, m, lo, hi, i);
     }
     __syncthreads();
     if (tid < 32) {
@@ -257,32 +209,46 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
     float c[E][E];
     auto store = [&](float *to) {
         __syncthreads();                      // every read of `to` is done
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < E; ++i)
+            for (int i = 0; i < E; ++i)
 #pragma unroll
-            for (int j = 0; j < E; ++j) to[(ty * E + i) * RP + tx * E + j] = c[i][j];
+                for (int j = 0; j < E; ++j) to[(ty * E + i) * RP + tx * E + j] = c[i][j];
+            if (tx != ty)
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+#pragma unroll
+                    for (int j = 0; j < E; ++j) to[(tx * E + j) * RP + ty * E + i] = c[i][j];
+        }
         __syncthreads();
     };
     for (int step = 0; step < p.steps; ++step) {
-        mul<RP, E>(R, R, ty, tx, c);
+        if (mine) {
+            mul<RP, E>(R, R, ty, tx, c);
 #pragma unroll
-        for (int i = 0; i < E; ++i)
+            for (int i = 0; i < E; ++i)
 #pragma unroll
-            for (int j = 0; j < E; ++j) {
-                const int y = ty * E + i, x = tx * E + j;
-                c[i][j] = fmaf(p.c, c[i][j], fmaf(p.b, R[y * RP + x], y == x ? p.a : 0.0f));
-            }
+                for (int j = 0; j < E; ++j) {
+                    const int y = ty * E + i, x = tx * E + j;
+                    c[i][j] = fmaf(p.c, c[i][j], fmaf(p.b, R[y * RP + x], y == x ? p.a : 0.0f));
+                }
+        }
         store(Q);
-        mul<RP, E>(Q, P, ty, tx, c);
-        store(P);
+        if (step == 0) {                      // P was the identity
+            for (int i = tid; i < RP * RP; i += OR_THREADS) P[i] = Q[i];
+        } else {
+            if (mine) mul<RP, E>(Q, P, ty, tx, c);
+            store(P);
+        }
         if (step + 1 < p.steps) {
-            mul<RP, E>(Q, R, ty, tx, c);
+            if (mine) mul<RP, E>(Q, R, ty, tx, c);
             store(R);
-            mul<RP, E>(R, Q, ty, tx, c);
+            if (mine) mul<RP, E>(R, Q, ty, tx, c);
             store(R);
         }
     }
-    uint16_t *out = p.p + int64_t(blockIdx.x) * 2 * RP * RP;
+    __syncthreads();
+    uint16_t *out = p.p + int64_t(m) * 2 * RP * RP;
     const float s = f * p.scale;
     for (int i = tid; i < RP * RP / 2; i += OR_THREADS) {
         const float v0 = P[2 * i] * s, v1 = P[2 * i + 1] * s;
@@ -302,8 +268,8 @@ constexpr int apply_smem()
     return 2 * RP * RP * 2 + RP * OR_LONG * 2 * (F32 ? 2 : 1) ;
 }
 
-// Block (tile group, matrix): P in shared memory, then tiles of U: out = P U
-// (or U P, TALL; P is symmetric).
+// Each block takes a run of tiles of the stacked matrices, P of the current
+// one in shared memory: out = P U (or U P, TALL; P is symmetric).
 template <int RP, bool TALL, bool F32>
 __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
 {
@@ -312,7 +278,7 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
     constexpr int TILE = RP * OR_LONG * 2;
     constexpr int PER = ROWS * CPR / OR_THREADS;
     // warps over the [ROWS x COLS] output
-    constexpr int WM = TALL ? 8 : (RP >= 64 ? 4 : RP / 16), WN = 8 / WM;
+    constexpr int WM = TALL ? 8 : RP / 16, WN = 8 / WM;
     constexpr int MI = ROWS / WM / 16, NI = COLS / WN / 8;
     static_assert(PER >= 1 && MI >= 1 && NI >= 2, "shape");
     extern __shared__ __align__(128) uint8_t smem[];
@@ -322,15 +288,14 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
     const int m0 = warp % WM * (ROWS / WM), n0 = warp / WM * (COLS / WN);
     pdl_wait();
     pdl_launch_dependents();
-    const uint4 *gp = reinterpret_cast<const uint4 *>(p.p + int64_t(blockIdx.y) * 2 * RP * RP);
-    for (int i = tid; i < 2 * RP * PCPR; i += OR_THREADS) {
-        const int term = i / (RP * PCPR), c = i % (RP * PCPR);
-        *reinterpret_cast<uint4 *>(smem + term * RP * RP * 2 + tile_at<PCPR, RP>(c / PCPR, c % PCPR)) = gp[i];
-    }
-    const int64_t mat = int64_t(blockIdx.y) * p.rows * p.cols;
     const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
+    const int64_t total = int64_t(p.count) * tiles;
+    const int64_t first = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    int held = -1;
     Chunk<F32> next[PER];
-    auto fetch = [&](int tile) {
+    auto fetch = [&](int64_t item) {
+        const int64_t mat = item / tiles * p.rows * p.cols;
+        const int tile = int(item % tiles);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
@@ -339,9 +304,20 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
             next[i] = load_chunk<F32>(p.u, mat + int64_t(gr) * p.cols + gc, gr < p.rows && gc < p.cols);
         }
     };
-    if (blockIdx.x < unsigned(tiles)) fetch(blockIdx.x);
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    if (first < end) fetch(first);
+    for (int64_t item = first; item < end; ++item) {
+        const int m = int(item / tiles), tile = int(item % tiles);
+        const int64_t mat = int64_t(m) * p.rows * p.cols;
         __syncthreads();
+        if (m != held) {
+            const uint4 *gp = reinterpret_cast<const uint4 *>(p.p + int64_t(m) * 2 * RP * RP);
+            for (int i = tid; i < 2 * RP * PCPR; i += OR_THREADS) {
+                const int term = i / (RP * PCPR), c = i % (RP * PCPR);
+                *reinterpret_cast<uint4 *>(smem + term * RP * RP * 2 +
+                                           tile_at<PCPR, RP>(c / PCPR, c % PCPR)) = gp[i];
+            }
+            held = m;
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int c = tid + i * OR_THREADS;
@@ -350,7 +326,7 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
             if constexpr (F32) *reinterpret_cast<uint4 *>(at + TILE) = next[i].lo;
         }
         __syncthreads();
-        if (tile + int(gridDim.x) < tiles) fetch(tile + gridDim.x);
+        if (item + 1 < end) fetch(item + 1);
         float acc[MI][NI][4] = {};
 #pragma unroll 2
         for (int kk = 0; kk < RP; kk += 16) {
@@ -419,30 +395,40 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
 // ---------------------------------------------------------------- host
 
 struct OrthoLayout {
-    int r, n, rp, shares, share;
-    int64_t gram, p, bytes;
+    int r, n, rp, unit, units, ctas;
+    int64_t p, bytes;
 };
 
-static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, int sms)
+// Blocks of a kernel on an SM by its shared memory, at most four.
+static int blocks_per_sm(int smem)
+{
+    const int n = 227 * 1024 / (smem + 1024);
+    return n > 4 ? 4 : n;
+}
+
+template <bool F32>
+static int gram_blocks(int rp)
+{
+    return rp == 16 ? blocks_per_sm(gram_smem<16, F32>())
+                    : rp == 32 ? blocks_per_sm(gram_smem<32, F32>()) : blocks_per_sm(gram_smem<64, F32>());
+}
+
+// The sum U U^T is cut into units of one tile each and those into as many
+// runs as blocks fit the GPU at once (or as there are units).
+static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, bool f32, int sms)
 {
     OrthoLayout l;
     l.r = rows <= cols ? rows : cols;
     l.n = rows <= cols ? cols : rows;
     l.rp = 16;
     while (l.rp < l.r) l.rp *= 2;
-    const int step = l.rp == 128 ? gram_step<128>() : l.rp == 64 ? gram_step<64>() : gram_step<32>();
-    // About four blocks an SM over all matrices, but no share shorter than
-    // 16 rp elements: its RP x RP partial sum is written and read again.
-    int64_t shares = (int64_t(4) * sms + count - 1) / count;
-    const int64_t most = (l.n + 16 * l.rp - 1) / (16 * l.rp);
-    if (shares > most) shares = most;
-    if (shares < 1) shares = 1;
-    int64_t share = (l.n + shares - 1) / shares;
-    share = (share + step - 1) / step * step;
-    l.share = int(share);
-    l.shares = int((l.n + share - 1) / share);
-    l.gram = 0;
-    l.p = int64_t(count) * l.shares * l.rp * l.rp * 4;
+    l.unit = l.rp == 128 ? OR_TC_UNIT : l.rp == 64 ? gram_step<64>() : gram_step<32>();
+    l.units = (l.n + l.unit - 1) / l.unit;
+    const int64_t most = int64_t(sms) * (l.rp == 128 ? OR_TC_CTAS
+                                                     : f32 ? gram_blocks<true>(l.rp) : gram_blocks<false>(l.rp));
+    const int64_t total = int64_t(count) * l.units;
+    l.ctas = int(total < most ? total : most);
+    l.p = (int64_t(l.ctas) + count) * l.rp * l.rp * 4;
     l.bytes = l.p + int64_t(count) * 2 * l.rp * l.rp * 2;
     return l;
 }
@@ -470,15 +456,14 @@ static int run_ortho(const OrthoArgs &p, cudaStream_t st)
             return int(e);
         if (dev < 64) configured[dev] = 1;
     }
-    e = launch_kernel(gram_kernel<RP, TALL, F32>, dim3(p.shares, p.count), dim3(OR_THREADS), gs, st, p);
+    e = launch_kernel(gram_kernel<RP, TALL, F32>, dim3(p.ctas), dim3(OR_THREADS), gs, st, p);
     if (e != cudaSuccess) return int(e);
     e = launch_kernel(iterate_kernel<RP>, dim3(p.count), dim3(OR_THREADS), is, st, p);
     if (e != cudaSuccess) return int(e);
-    // each block loads P once: two tiles or more a block where there are enough
-    const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
-    int groups = (8 * device_sm_count() + p.count - 1) / p.count;
-    if (groups > tiles) groups = tiles;
-    e = launch_kernel(apply_kernel<RP, TALL, F32>, dim3(groups, p.count), dim3(OR_THREADS), as, st, p);
+    const int64_t tiles = int64_t(p.count) * ((p.n + OR_LONG - 1) / OR_LONG);
+    const int64_t most = int64_t(device_sm_count()) * blocks_per_sm(as);
+    e = launch_kernel(apply_kernel<RP, TALL, F32>, dim3(unsigned(tiles < most ? tiles : most)),
+                      dim3(OR_THREADS), as, st, p);
     return e == cudaSuccess ? LORA_OK : int(e);
 }
 
@@ -488,14 +473,13 @@ static int run_ortho_rank(const OrthoArgs &p, int rp, cudaStream_t st)
     switch (rp) {
     case 16: return run_ortho<16, TALL, F32>(p, st);
     case 32: return run_ortho<32, TALL, F32>(p, st);
-    case 64: return run_ortho<64, TALL, F32>(p, st);
-    default: return run_ortho<128, TALL, F32>(p, st);
+    default: return run_ortho<64, TALL, F32>(p, st);
     }
 }
 
 static bool ortho_sizes_ok(int32_t count, int32_t rows, int32_t cols)
 {
-    // count is a grid's second dimension
+    // count is a grid's dimension
     return count >= 0 && count <= 65535 && rows >= 1 && cols >= 8 && cols % 8 == 0 &&
            (rows <= OR_MAX_RANK || cols <= OR_MAX_RANK);
 }
@@ -505,13 +489,16 @@ static bool ortho_sizes_ok(int32_t count, int32_t rows, int32_t cols)
 LORA_API int64_t lora_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols)
 {
     if (!lora::ortho_sizes_ok(count, rows, cols)) return LORA_ERR_SIZE;
-    return lora::ortho_layout(count > 0 ? count : 1, rows, cols, lora::device_sm_count()).bytes;
+    const int sms = lora::device_sm_count();
+    const int64_t a = lora::ortho_layout(count > 0 ? count : 1, rows, cols, false, sms).bytes;
+    const int64_t b = lora::ortho_layout(count > 0 ? count : 1, rows, cols, true, sms).bytes;
+    return a > b ? a : b;
 }
 
 LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, int32_t rows,
                                 int32_t cols, int32_t steps, float coef_a, float coef_b,
                                 float coef_c, float eps, float scale, lora_bf16_t *out,
-                                void *workspace, int64_t workspace_bytes, void *stream)
+                                int32_t *error_word, void *workspace, int64_t workspace_bytes, void *stream)
 {
     using namespace lora;
     NvtxRange nvtx_range("lora_orthogonalize");
@@ -520,7 +507,7 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     if (update == nullptr || out == nullptr || workspace == nullptr) return LORA_ERR_NULL;
     auto bits = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
     if ((bits(update) | bits(out)) & 15u || bits(workspace) & 255u) return LORA_ERR_ALIGN;
-    const OrthoLayout l = ortho_layout(count, rows, cols, device_sm_count());
+    const OrthoLayout l = ortho_layout(count, rows, cols, update_f32 != 0, device_sm_count());
     if (workspace_bytes < l.bytes) return LORA_ERR_WORKSPACE;
     OrthoArgs p;
     p.u = update;
@@ -530,8 +517,10 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     p.cols = cols;
     p.r = l.r;
     p.n = l.n;
-    p.shares = l.shares;
-    p.share = l.share;
+    p.units = l.units;
+    p.unit = l.unit;
+    p.ctas = l.ctas;
+    p.error_word = error_word;
     p.steps = steps;
     p.a = coef_a;
     p.b = coef_b;
@@ -542,6 +531,7 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     p.p = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + l.p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool tall = rows > cols;
+    if (l.rp == 128) return run_ortho_tc(p, update_f32 != 0, st);
     if (update_f32)
         return tall ? run_ortho_rank<true, true>(p, l.rp, st) : run_ortho_rank<false, true>(p, l.rp, st);
     return tall ? run_ortho_rank<true, false>(p, l.rp, st) : run_ortho_rank<false, false>(p, l.rp, st);

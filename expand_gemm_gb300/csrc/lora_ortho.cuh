@@ -1,0 +1,85 @@
+// lora_ortho.cuh -- what the kernels of lora_orthogonalize share.
+#pragma once
+
+#include "lora_frag.cuh"
+
+namespace lora {
+
+constexpr int OR_THREADS = 256;
+constexpr int OR_MAX_RANK = 128;
+
+struct OrthoArgs {
+    const void *u;
+    uint16_t *out;
+    int32_t count, rows, cols;    // matrices, each [rows, cols]
+    int32_t r, n;                 // short and long side
+    int32_t units, unit;          // of the long side in the sum U U^T; a unit's length
+    int32_t ctas;                 // that share the units of all matrices
+    int32_t steps;
+    float a, b, c, eps, scale;
+    float *gram;                  // partial sums, [ctas + count][RP][RP]
+    uint16_t *p;                  // [count][2][RP][RP]: P as two bf16 terms
+    int32_t *error_word;
+};
+
+// The units of all matrices, in order, are cut into p.ctas even runs.  CTA c
+// takes units [unit_begin(c), unit_begin(c + 1)); its part of matrix m's sum
+// goes to slot c + m (a new slot whenever the CTA or the matrix changes), so
+// matrix m is the sum of slots c + m over the CTAs that hold its units, in
+// that order.
+__device__ __forceinline__ int64_t unit_begin(const OrthoArgs &p, int c)
+{
+    return int64_t(p.count) * p.units * c / p.ctas;
+}
+__device__ __forceinline__ int unit_cta(const OrthoArgs &p, int64_t unit)
+{
+    return int(((unit + 1) * p.ctas - 1) / (int64_t(p.count) * p.units));
+}
+
+// One element of matrix m's sum.
+template <int RP>
+__device__ __forceinline__ float gram_sum(const OrthoArgs &p, int m, int lo, int hi, int e)
+{
+    float s = 0.0f;
+#pragma unroll 4
+    for (int c = lo; c <= hi; ++c) s += p.gram[int64_t(c + m) * RP * RP + e];
+    return s;
+}
+
+// Eight consecutive elements of U as bf16 terms: hi, and (fp32) what hi
+// leaves over.
+template <bool F32>
+struct Chunk {
+    uint4 hi, lo;
+};
+
+template <bool F32>
+__device__ __forceinline__ Chunk<F32> load_chunk(const void *u, int64_t at, bool valid)
+{
+    Chunk<F32> c;
+    c.hi = c.lo = make_uint4(0, 0, 0, 0);
+    if (!valid) return c;
+    if constexpr (F32) {
+        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(u) + at);
+        const float4 x = src[0], y = src[1];
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            l[i] = pack_bf16x2(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
+        }
+        c.hi = make_uint4(h[0], h[1], h[2], h[3]);
+        c.lo = make_uint4(l[0], l[1], l[2], l[3]);
+    } else {
+        c.hi = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at);
+    }
+    return c;
+}
+
+// Rank 65 to 128 (lora_ortho_tc.cu).  Returns 0 or an error.
+int run_ortho_tc(OrthoArgs p, bool f32, cudaStream_t st);
+constexpr int OR_TC_UNIT = 64;
+constexpr int OR_TC_CTAS = 2;         // of the sum U U^T on an SM
+
+}  // namespace lora

@@ -65,15 +65,16 @@ __device__ __forceinline__ bool pg_wait(uint32_t bar, uint32_t parity, volatile 
     return mbar_wait_bounded_cluster(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES);
 }
 
-// Descriptor of an MN-major operand: panels of 64 K rows x 64 elements
+// Descriptor of an MN-major operand: panels of K rows x 64 elements
 // (128-byte rows, 128-byte swizzle).  Eight K rows are 1024 bytes (stride
-// offset); the next 64 elements along M or N begin 8192 bytes on (leading
-// offset).  Advancing K by 16 adds 2048 bytes to the start.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr)
+// offset); the next 64 elements along M or N begin `panel` bytes on (leading
+// offset; 8192 for 64 K rows).  Advancing K by 16 adds 2048 bytes to the
+// start.
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t panel = 8192)
 {
     uint64_t d = 0;
     d |= uint64_t((saddr & 0x3FFFFu) >> 4);
-    d |= uint64_t(8192 >> 4) << 16;
+    d |= uint64_t(panel >> 4) << 16;
     d |= uint64_t(1024 >> 4) << 32;
     d |= uint64_t(1) << 46;
     d |= uint64_t(2) << 61;

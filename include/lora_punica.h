@@ -439,6 +439,9 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
  *   steps        >= 1.
  *   out          device bf16 [count, rows, cols], dense, 16-byte aligned;
  *                may be `update` itself where that is bf16.
+ *   error_word   NULL or device int32 [1]: bit 30 is set in it if a bounded
+ *                wait ran out (the output is then not valid); otherwise it is
+ *                left as it is.
  *
  * A zero matrix gives zeros; a matrix with a NaN or an infinity gives NaN in
  * its own place only.  |U|_F^2 and the products U U^T are summed in fp32 and
@@ -449,8 +452,8 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
  */
 int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, int32_t rows,
                        int32_t cols, int32_t steps, float coef_a, float coef_b, float coef_c,
-                       float eps, float scale, lora_bf16_t *out, void *workspace,
-                       int64_t workspace_bytes, void *stream);
+                       float eps, float scale, lora_bf16_t *out, int32_t *error_word,
+                       void *workspace, int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace of lora_orthogonalize on the current device;
  * LORA_ERR_SIZE for sizes that it refuses. */
