@@ -16,97 +16,136 @@
 // directions that U has little of, which cancel where U is large, so one
 // bf16 would show in the result.
 //
-// This file: ranks up to 64, on mma.sync and FFMA.  lora_ortho_tc.cu: ranks
-// to 128, on tcgen05.
+// This file: ranks up to 64, on mma.sync, and the steps up to 32 in FFMA.
+// lora_ortho_tc.cu: ranks to 128, and the steps from 33, on tcgen05.
 #include <math.h>
 
 #include "lora_ortho.cuh"
 
 namespace lora {
 
+// ---------------------------------------------------------------- rings
+//
+// Tiles of U come by cp.async, several in flight.  A bf16 tile lands
+// swizzled, ready for ldmatrix.  An fp32 tile lands as it is: every thread
+// copies its own chunks of eight entries, and later turns those same chunks
+// into two bf16 terms of a tile that the warps then share.
+
+template <int ROWS, int CPR, bool F32>
+struct TileRing {
+    static constexpr int PER = ROWS * CPR / OR_THREADS;            // chunks of a thread
+    static constexpr int BYTES = ROWS * CPR * (F32 ? 32 : 16);
+    static constexpr int TERM = ROWS * CPR * 16;                   // one bf16 term
+    static_assert(PER >= 1, "a chunk a thread at least");
+
+    __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
+                                                 int col0)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int c = threadIdx.x + i * OR_THREADS, row = row0 + c / CPR, col = col0 + c % CPR * 8;
+            const bool ok = row < p.rows && col < p.cols;
+            const int64_t at = ok ? mat + int64_t(row) * p.cols + col : 0;
+            if constexpr (F32) {
+                const float *src = static_cast<const float *>(p.u) + at;
+                const uint32_t dst = smem_addr(stage + (2 * i * OR_THREADS + threadIdx.x) * 16);
+                cp_async16(dst, src, ok);
+                cp_async16(dst + OR_THREADS * 16, src + 4, ok);
+            } else {
+                cp_async16(smem_addr(stage + tile_at<CPR, ROWS>(c / CPR, c % CPR)),
+                           static_cast<const uint16_t *>(p.u) + at, ok);
+            }
+        }
+    }
+    // fp32: this thread's chunks of a landed stage, as terms of `tile`.
+    __device__ __forceinline__ static void convert(const uint8_t *stage, uint8_t *tile)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const uint8_t *src = stage + (2 * i * OR_THREADS + threadIdx.x) * 16;
+            const Chunk k = split_chunk(*reinterpret_cast<const float4 *>(src),
+                                              *reinterpret_cast<const float4 *>(src + OR_THREADS * 16));
+            const int c = threadIdx.x + i * OR_THREADS;
+            uint8_t *at = tile + tile_at<CPR, ROWS>(c / CPR, c % CPR);
+            *reinterpret_cast<uint4 *>(at) = k.hi;
+            *reinterpret_cast<uint4 *>(at + TERM) = k.lo;
+        }
+    }
+};
+
 // ---------------------------------------------------------------- gram
 
-// Warps of gram_kernel: WM x WN over the RP x RP result, WK over the K step.
-template <int RP> struct GramShape;
-template <> struct GramShape<16> { static constexpr int WM = 1, WN = 1, WK = 8; };
-template <> struct GramShape<32> { static constexpr int WM = 1, WN = 1, WK = 8; };
-template <> struct GramShape<64> { static constexpr int WM = 2, WN = 1, WK = 4; };
+// Warps of gram_kernel: WM over the rows of the RP x RP result, WK over the
+// K step (a tile of 4096 entries).
+template <int RP> struct GramShape { static constexpr int WM = RP == 64 ? 2 : 1, WK = 8 / WM; };
 
 template <int RP>
-constexpr int gram_step() { return RP == 64 ? 128 : 256; }
+constexpr int gram_step() { return 4096 / RP; }
+
+template <bool F32>
+constexpr int gram_stages() { return F32 ? 4 : 6; }
 
 template <int RP, bool F32>
 constexpr int gram_smem()
 {
-    constexpr int tile = RP * gram_step<RP>() * 2 * (F32 ? 2 : 1);
-    constexpr int join = GramShape<RP>::WK > 1 ? GramShape<RP>::WK * RP * RP * 4 : 0;
-    return 2 * tile > join ? 2 * tile : join;
+    return 4096 * (gram_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 8 : 0)) + RP * RP * 4;
 }
 
 // Each block sums over its run of units.  TALL: U is [n][r] (its rows are
 // K), else [r][n].
 template <int RP, bool TALL, bool F32>
-__global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
+__global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
 {
-    constexpr int WM = GramShape<RP>::WM, WN = GramShape<RP>::WN, WK = GramShape<RP>::WK;
-    constexpr int KS = gram_step<RP>();
-    constexpr int ROWS = TALL ? KS : RP, COLS = TALL ? RP : KS;     // of the tile
-    constexpr int CPR = COLS / 8;
-    constexpr int TILE = RP * KS * 2;                               // bytes of one term
-    constexpr int TERMS = F32 ? 2 : 1;
-    constexpr int PER = ROWS * CPR / OR_THREADS;                    // chunks a thread loads
-    constexpr int MI = RP / WM / 16, NI = RP / WN / 8;
-    static_assert(PER >= 1 && MI >= 1 && NI >= 2 && WK > 1, "shape");
+    constexpr int WM = GramShape<RP>::WM, WK = GramShape<RP>::WK;
+    constexpr int KS = gram_step<RP>(), ST = gram_stages<F32>();
+    constexpr int ROWS = TALL ? KS : RP, CPR = (TALL ? RP : KS) / 8;     // of the tile
+    constexpr int MI = RP / WM / 16, NI = RP / 8;
+    using Ring = TileRing<ROWS, CPR, F32>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t base = smem_addr(smem);
+    uint8_t *terms = smem + ST * Ring::BYTES;                       // fp32: two converted tiles
+    float *sum = reinterpret_cast<float *>(terms + (F32 ? 4 * Ring::TERM : 0));
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int wk = warp / (WM * WN), wm = warp % WM, wn = warp / WM % WN;
-    const int m0 = wm * (RP / WM), n0 = wn * (RP / WN);
+    const int wk = warp / WM, m0 = warp % WM * (RP / WM);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
-
-    Chunk<F32> next[PER];
-    auto fetch = [&](int64_t unit) {
-        const int64_t mat = unit / p.units * p.rows * p.cols;
-        const int k = int(unit % p.units) * KS;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
-            const int gr = TALL ? k + row : row, gc = (TALL ? 0 : k) + ch * 8;
-            next[i] = load_chunk<F32>(p.u, mat + int64_t(gr) * p.cols + gc, gr < p.rows && gc < p.cols);
+    auto issue = [&](int64_t unit, int stage) {
+        if (unit < end) {
+            const int k = int(unit % p.units) * KS;
+            Ring::issue(p, smem + stage * Ring::BYTES, unit / p.units * p.rows * p.cols, TALL ? k : 0,
+                        TALL ? 0 : k);
         }
-    };
-    auto put = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = tid + i * OR_THREADS;
-            uint8_t *at = smem + buf * TILE * TERMS + tile_at<CPR, ROWS>(c / CPR, c % CPR);
-            *reinterpret_cast<uint4 *>(at) = next[i].hi;
-            if constexpr (F32) *reinterpret_cast<uint4 *>(at + TILE) = next[i].lo;
-        }
+        cp_async_commit();
     };
     float acc[MI][NI][4] = {};
-    int buf = 0;
-    if (first < end) fetch(first);
+    for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
+    int stage = 0, buf = 0;
     for (int64_t unit = first; unit < end; ++unit) {
-        put(buf);
+        cp_async_wait<ST - 2>();
+        uint32_t hi;
+        if constexpr (F32) {
+            Ring::convert(smem + stage * Ring::BYTES, terms + buf * 2 * Ring::TERM);
+            hi = smem_addr(terms + buf * 2 * Ring::TERM);
+            buf ^= 1;
+        } else {
+            hi = smem_addr(smem + stage * Ring::BYTES);
+        }
         __syncthreads();
-        if (unit + 1 < end) fetch(unit + 1);
-        const uint32_t hi = base + buf * TILE * TERMS;
-#pragma unroll 2
+        issue(unit + ST - 1, (stage + ST - 1) % ST);
+        stage = stage + 1 == ST ? 0 : stage + 1;
+#pragma unroll
         for (int kk = wk * (KS / WK); kk < (wk + 1) * (KS / WK); kk += 16) {
             uint32_t a[MI][4], al[MI][4];
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 frag_a<CPR, ROWS, !TALL>(hi, m0 + 16 * i, kk, a[i]);
-                if constexpr (F32) frag_a<CPR, ROWS, !TALL>(hi + TILE, m0 + 16 * i, kk, al[i]);
+                if constexpr (F32) frag_a<CPR, ROWS, !TALL>(hi + Ring::TERM, m0 + 16 * i, kk, al[i]);
             }
 #pragma unroll
             for (int j = 0; j < NI; j += 2) {
                 uint32_t b[4], bl[4];
-                frag_b<CPR, ROWS, !TALL>(hi, kk, n0 + 8 * j, b);
-                if constexpr (F32) frag_b<CPR, ROWS, !TALL>(hi + TILE, kk, n0 + 8 * j, bl);
+                frag_b<CPR, ROWS, !TALL>(hi, kk, 8 * j, b);
+                if constexpr (F32) frag_b<CPR, ROWS, !TALL>(hi + Ring::TERM, kk, 8 * j, bl);
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
@@ -120,32 +159,29 @@ __global__ void __launch_bounds__(OR_THREADS) gram_kernel(const OrthoArgs p)
                 }
             }
         }
-        buf ^= 1;
         if (unit + 1 < end && (unit + 1) % p.units != 0) continue;
-        // the matrix or the run ends: the warps' sums over K, joined
-        float *out = p.gram + (blockIdx.x + unit / p.units) * RP * RP;
+        // the matrix or the run ends: the warps' sums over K, one after the other
         const int g = (tid & 31) >> 2, t = tid & 3;
-        __syncthreads();
-        float *part = reinterpret_cast<float *>(smem) + wk * RP * RP;
+        for (int w = 0; w < WK; ++w) {
+            if (wk == w) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+                for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) {
-                float *at = part + (m0 + 16 * i + g) * RP + n0 + 8 * j + 2 * t;
-                at[0] = acc[i][j][0];
-                at[1] = acc[i][j][1];
-                at[8 * RP] = acc[i][j][2];
-                at[8 * RP + 1] = acc[i][j][3];
-                acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
+                    for (int j = 0; j < NI; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float2 *at = reinterpret_cast<float2 *>(sum + (m0 + 16 * i + g + 8 * h) * RP + 8 * j + 2 * t);
+                            const float2 was = w > 0 ? *at : make_float2(0.0f, 0.0f);
+                            *at = make_float2(was.x + acc[i][j][2 * h], was.y + acc[i][j][2 * h + 1]);
+                            acc[i][j][2 * h] = acc[i][j][2 * h + 1] = 0.0f;
+                        }
             }
-        __syncthreads();
-        for (int i = tid; i < RP * RP; i += OR_THREADS) {
-            float s = 0.0f;
-            for (int w = 0; w < WK; ++w) s += reinterpret_cast<float *>(smem)[w * RP * RP + i];
-            out[i] = s;
+            __syncthreads();
         }
-        __syncthreads();
+        float4 *out = reinterpret_cast<float4 *>(p.gram + (blockIdx.x + unit / p.units) * RP * RP);
+        for (int i = tid; i < RP * RP / 4; i += OR_THREADS) out[i] = reinterpret_cast<const float4 *>(sum)[i];
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- iterate
@@ -176,7 +212,8 @@ __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int 
 
 // One block per matrix; R, P, Q in shared memory, in fp32.  The 136 blocks
 // on or above the diagonal of a 16 x 16 grid are a thread's each; the rest
-// is their mirror image.  (All 256 blocks by 256 threads: 49 us at rank 64.)
+// is their mirror image.  Ranks up to 32; above, the products are long
+// enough for the tensor cores (rank 40: 59 us here, see lora_ortho_tc.cu).
 template <int RP>
 __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
 {
@@ -263,9 +300,14 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
 constexpr int OR_LONG = 128;              // long-side elements of a tile of apply_kernel
 
 template <int RP, bool F32>
+constexpr int apply_stages() { return RP == 64 ? (F32 ? 2 : 3) : 4; }
+
+// P's terms, the ring, and a tile that holds the converted terms (fp32) and
+// then the output.
+template <int RP, bool F32>
 constexpr int apply_smem()
 {
-    return 2 * RP * RP * 2 + RP * OR_LONG * 2 * (F32 ? 2 : 1) ;
+    return 2 * RP * RP * 2 + RP * OR_LONG * (apply_stages<RP, F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 2));
 }
 
 // Each block takes a run of tiles of the stacked matrices, P of the current
@@ -274,16 +316,15 @@ template <int RP, bool TALL, bool F32>
 __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
 {
     constexpr int ROWS = TALL ? OR_LONG : RP, COLS = TALL ? RP : OR_LONG;
-    constexpr int CPR = COLS / 8, PCPR = RP / 8;
-    constexpr int TILE = RP * OR_LONG * 2;
-    constexpr int PER = ROWS * CPR / OR_THREADS;
+    constexpr int CPR = COLS / 8, PCPR = RP / 8, ST = apply_stages<RP, F32>();
     // warps over the [ROWS x COLS] output
     constexpr int WM = TALL ? 8 : RP / 16, WN = 8 / WM;
     constexpr int MI = ROWS / WM / 16, NI = COLS / WN / 8;
-    static_assert(PER >= 1 && MI >= 1 && NI >= 2, "shape");
+    using Ring = TileRing<ROWS, CPR, F32>;
+    static_assert(MI >= 1 && NI >= 2, "shape");
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *s_u = smem + 2 * RP * RP * 2;
-    const uint32_t sp = smem_addr(smem), su = smem_addr(s_u);
+    uint8_t *ring = smem + 2 * RP * RP * 2, *tile_buf = ring + ST * Ring::BYTES;
+    const uint32_t sp = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5;
     const int m0 = warp % WM * (ROWS / WM), n0 = warp / WM * (COLS / WN);
     pdl_wait();
@@ -291,24 +332,20 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
     const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
     const int64_t total = int64_t(p.count) * tiles;
     const int64_t first = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
-    int held = -1;
-    Chunk<F32> next[PER];
-    auto fetch = [&](int64_t item) {
-        const int64_t mat = item / tiles * p.rows * p.cols;
-        const int tile = int(item % tiles);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
-            const int gr = TALL ? tile * OR_LONG + row : row;
-            const int gc = (TALL ? 0 : tile * OR_LONG) + ch * 8;
-            next[i] = load_chunk<F32>(p.u, mat + int64_t(gr) * p.cols + gc, gr < p.rows && gc < p.cols);
+    auto issue = [&](int64_t item, int stage) {
+        if (item < end) {
+            const int n = int(item % tiles) * OR_LONG;
+            Ring::issue(p, ring + stage * Ring::BYTES, item / tiles * p.rows * p.cols, TALL ? n : 0, TALL ? 0 : n);
         }
+        cp_async_commit();
     };
-    if (first < end) fetch(first);
+    for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
+    int held = -1, stage = 0;
     for (int64_t item = first; item < end; ++item) {
         const int m = int(item / tiles), tile = int(item % tiles);
         const int64_t mat = int64_t(m) * p.rows * p.cols;
-        __syncthreads();
+        cp_async_wait<ST - 2>();
+        __syncthreads();                       // the last tile's output has left
         if (m != held) {
             const uint4 *gp = reinterpret_cast<const uint4 *>(p.p + int64_t(m) * 2 * RP * RP);
             for (int i = tid; i < 2 * RP * PCPR; i += OR_THREADS) {
@@ -316,17 +353,16 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
                 *reinterpret_cast<uint4 *>(smem + term * RP * RP * 2 +
                                            tile_at<PCPR, RP>(c / PCPR, c % PCPR)) = gp[i];
             }
-            held = m;
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = tid + i * OR_THREADS;
-            uint8_t *at = s_u + tile_at<CPR, ROWS>(c / CPR, c % CPR);
-            *reinterpret_cast<uint4 *>(at) = next[i].hi;
-            if constexpr (F32) *reinterpret_cast<uint4 *>(at + TILE) = next[i].lo;
+        uint32_t su = smem_addr(ring + stage * Ring::BYTES);
+        if constexpr (F32) {
+            Ring::convert(ring + stage * Ring::BYTES, tile_buf);
+            su = smem_addr(tile_buf);
         }
-        __syncthreads();
-        if (item + 1 < end) fetch(item + 1);
+        if (F32 || m != held) __syncthreads();
+        held = m;
+        issue(item + ST - 1, (stage + ST - 1) % ST);
+        stage = stage + 1 == ST ? 0 : stage + 1;
         float acc[MI][NI][4] = {};
 #pragma unroll 2
         for (int kk = 0; kk < RP; kk += 16) {
@@ -335,7 +371,7 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
             for (int i = 0; i < MI; ++i) {
                 if constexpr (TALL) {
                     frag_a<CPR, ROWS, true>(su, m0 + 16 * i, kk, a[i]);
-                    if constexpr (F32) frag_a<CPR, ROWS, true>(su + TILE, m0 + 16 * i, kk, al[i]);
+                    if constexpr (F32) frag_a<CPR, ROWS, true>(su + Ring::TERM, m0 + 16 * i, kk, al[i]);
                 } else {
                     frag_a<PCPR, RP, true>(sp, m0 + 16 * i, kk, a[i]);
                     frag_a<PCPR, RP, true>(sp + RP * RP * 2, m0 + 16 * i, kk, al[i]);
@@ -349,7 +385,7 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
                     frag_b<PCPR, RP, true>(sp + RP * RP * 2, kk, n0 + 8 * j, bl);
                 } else {
                     frag_b<CPR, ROWS, false>(su, kk, n0 + 8 * j, b);
-                    if constexpr (F32) frag_b<CPR, ROWS, false>(su + TILE, kk, n0 + 8 * j, bl);
+                    if constexpr (F32) frag_b<CPR, ROWS, false>(su + Ring::TERM, kk, n0 + 8 * j, bl);
                 }
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
@@ -367,29 +403,30 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
             }
         }
         // through shared memory, so that rows are written 16 bytes at a time
-        __syncthreads();
+        if (F32) __syncthreads();
         const int g = (tid & 31) >> 2, t = tid & 3;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int row = m0 + 16 * i + g, col = n0 + 8 * j + 2 * t;
-                *reinterpret_cast<uint32_t *>(s_u + tile_at<CPR, ROWS>(row, col / 8) + col % 8 * 2) =
+                *reinterpret_cast<uint32_t *>(tile_buf + tile_at<CPR, ROWS>(row, col / 8) + col % 8 * 2) =
                     pack_bf16x2(acc[i][j][0], acc[i][j][1]);
-                *reinterpret_cast<uint32_t *>(s_u + tile_at<CPR, ROWS>(row + 8, col / 8) + col % 8 * 2) =
+                *reinterpret_cast<uint32_t *>(tile_buf + tile_at<CPR, ROWS>(row + 8, col / 8) + col % 8 * 2) =
                     pack_bf16x2(acc[i][j][2], acc[i][j][3]);
             }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
+        for (int i = 0; i < Ring::PER; ++i) {
             const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
             const int gr = TALL ? tile * OR_LONG + row : row;
             const int gc = (TALL ? 0 : tile * OR_LONG) + ch * 8;
             if (gr < p.rows && gc < p.cols)
                 *reinterpret_cast<uint4 *>(p.out + mat + int64_t(gr) * p.cols + gc) =
-                    *reinterpret_cast<const uint4 *>(s_u + tile_at<CPR, ROWS>(row, ch));
+                    *reinterpret_cast<const uint4 *>(tile_buf + tile_at<CPR, ROWS>(row, ch));
         }
     }
+    cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- host
@@ -399,18 +436,18 @@ struct OrthoLayout {
     int64_t p, bytes;
 };
 
-// Blocks of a kernel on an SM by its shared memory, at most four.
-static int blocks_per_sm(int smem)
+// Blocks of a kernel on an SM by its shared memory, at most `most`.
+static int blocks_per_sm(int smem, int most)
 {
     const int n = 227 * 1024 / (smem + 1024);
-    return n > 4 ? 4 : n;
+    return n > most ? most : n;
 }
 
 template <bool F32>
 static int gram_blocks(int rp)
 {
-    return rp == 16 ? blocks_per_sm(gram_smem<16, F32>())
-                    : rp == 32 ? blocks_per_sm(gram_smem<32, F32>()) : blocks_per_sm(gram_smem<64, F32>());
+    return rp == 16 ? blocks_per_sm(gram_smem<16, F32>(), 2)
+                    : rp == 32 ? blocks_per_sm(gram_smem<32, F32>(), 2) : blocks_per_sm(gram_smem<64, F32>(), 2);
 }
 
 // The sum U U^T is cut into units of one tile each and those into as many
@@ -422,7 +459,7 @@ static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, bool 
     l.n = rows <= cols ? cols : rows;
     l.rp = 16;
     while (l.rp < l.r) l.rp *= 2;
-    l.unit = l.rp == 128 ? OR_TC_UNIT : l.rp == 64 ? gram_step<64>() : gram_step<32>();
+    l.unit = l.rp == 128 ? OR_TC_UNIT : l.rp == 64 ? gram_step<64>() : l.rp == 32 ? gram_step<32>() : gram_step<16>();
     l.units = (l.n + l.unit - 1) / l.unit;
     const int64_t most = int64_t(sms) * (l.rp == 128 ? OR_TC_CTAS
                                                      : f32 ? gram_blocks<true>(l.rp) : gram_blocks<false>(l.rp));
@@ -444,24 +481,28 @@ static cudaError_t allow_smem(Kern k, int bytes)
 template <int RP, bool TALL, bool F32>
 static int run_ortho(const OrthoArgs &p, cudaStream_t st)
 {
-    constexpr int gs = gram_smem<RP, F32>(), is = 3 * RP * RP * 4, as = apply_smem<RP, F32>();
+    constexpr int gs = gram_smem<RP, F32>(), as = apply_smem<RP, F32>();
+    [[maybe_unused]] constexpr int is = 3 * RP * RP * 4;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return int(e);
     if (dev >= 64 || !configured[dev]) {
         if ((e = allow_smem(gram_kernel<RP, TALL, F32>, gs)) != cudaSuccess ||
-            (e = allow_smem(iterate_kernel<RP>, is)) != cudaSuccess ||
             (e = allow_smem(apply_kernel<RP, TALL, F32>, as)) != cudaSuccess)
             return int(e);
         if (dev < 64) configured[dev] = 1;
     }
     e = launch_kernel(gram_kernel<RP, TALL, F32>, dim3(p.ctas), dim3(OR_THREADS), gs, st, p);
     if (e != cudaSuccess) return int(e);
-    e = launch_kernel(iterate_kernel<RP>, dim3(p.count), dim3(OR_THREADS), is, st, p);
-    if (e != cudaSuccess) return int(e);
+    if constexpr (RP == 64) {
+        if (int r = launch_iterate_tc(p, RP, st)) return r;
+    } else {
+        e = launch_kernel(iterate_kernel<RP>, dim3(p.count), dim3(OR_THREADS), is, st, p);
+        if (e != cudaSuccess) return int(e);
+    }
     const int64_t tiles = int64_t(p.count) * ((p.n + OR_LONG - 1) / OR_LONG);
-    const int64_t most = int64_t(device_sm_count()) * blocks_per_sm(as);
+    const int64_t most = int64_t(device_sm_count()) * blocks_per_sm(as, 4);
     e = launch_kernel(apply_kernel<RP, TALL, F32>, dim3(unsigned(tiles < most ? tiles : most)),
                       dim3(OR_THREADS), as, st, p);
     return e == cudaSuccess ? LORA_OK : int(e);

@@ -46,39 +46,27 @@ __device__ __forceinline__ float gram_sum(const OrthoArgs &p, int m, int lo, int
     return s;
 }
 
-// Eight consecutive elements of U as bf16 terms: hi, and (fp32) what hi
-// leaves over.
-template <bool F32>
+// Eight consecutive fp32 entries as bf16 terms: hi, and what hi leaves over.
 struct Chunk {
     uint4 hi, lo;
 };
 
-template <bool F32>
-__device__ __forceinline__ Chunk<F32> load_chunk(const void *u, int64_t at, bool valid)
+__device__ __forceinline__ Chunk split_chunk(const float4 &x, const float4 &y)
 {
-    Chunk<F32> c;
-    c.hi = c.lo = make_uint4(0, 0, 0, 0);
-    if (!valid) return c;
-    if constexpr (F32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(u) + at);
-        const float4 x = src[0], y = src[1];
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        uint32_t h[4], l[4];
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t h[4], l[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            l[i] = pack_bf16x2(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
-        }
-        c.hi = make_uint4(h[0], h[1], h[2], h[3]);
-        c.lo = make_uint4(l[0], l[1], l[2], l[3]);
-    } else {
-        c.hi = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(u) + at);
+    for (int i = 0; i < 4; ++i) {
+        h[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        l[i] = pack_bf16x2(v[2 * i] - bf16_lo(h[i]), v[2 * i + 1] - bf16_hi(h[i]));
     }
-    return c;
+    return Chunk{make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3])};
 }
 
 // Rank 65 to 128 (lora_ortho_tc.cu).  Returns 0 or an error.
 int run_ortho_tc(OrthoArgs p, bool f32, cudaStream_t st);
+// The steps alone, padded rank 64 or 128.  Returns 0 or an error.
+int launch_iterate_tc(const OrthoArgs &p, int rp, cudaStream_t st);
 constexpr int OR_TC_UNIT = 64;
 constexpr int OR_TC_CTAS = 2;         // of the sum U U^T on an SM
 

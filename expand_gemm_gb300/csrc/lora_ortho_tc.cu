@@ -1,9 +1,10 @@
-// lora_ortho_tc.cu -- lora_orthogonalize for ranks 65 to 128 on tcgen05; see
-// lora_ortho.cu for the mathematics.  Short sides are padded to 128 by the
+// lora_ortho_tc.cu -- lora_orthogonalize on tcgen05: ranks 65 to 128, and the
+// steps of ranks 33 to 64; see lora_ortho.cu for the mathematics.  Short sides are padded to 128 by the
 // loads (zeros).
 //
 // gram_tc_kernel   U U^T: both operands of a UMMA are the same tile.
-// iterate_tc_kernel  the steps on 128 x 128 matrices.  An fp32 value is a sum
+// iterate_tc_kernel  the steps on 128 x 128 matrices, or (ranks 33 to 64) on
+//     two of 64 x 64 at once.  An fp32 value is a sum
 //     of three bf16 terms (24 bits), a product the six pairs of terms down
 //     to 2^-16.  (Two terms in the later steps would save 20 of the about
 //     110 us at 192 matrices; a matrix of rank one then comes out 1% off.)
@@ -28,9 +29,6 @@ constexpr int OT_GRAM_RING = 80 * 1024;          // two CTAs an SM
 constexpr int OT_GRAM_SMEM = OT_GRAM_RING + TC_STAGE_ROWS + TC_BAR_BYTES + 1024;
 constexpr int OT_APPLY_RING = 128 * 1024;
 constexpr int OT_APPLY_SMEM = OT_APPLY_RING + 4 * OT_PANEL + TC_STAGE_ROWS + TC_BAR_BYTES + 1024;
-constexpr int OT_ITER_THREADS = 256;
-constexpr int OT_TERM = 2 * OT_PANEL;            // one bf16 term of a matrix
-constexpr int OT_ITER_SMEM = 6 * OT_TERM + 64 + 1024;
 
 struct OrthoTcArgs {
     OrthoArgs o;
@@ -44,14 +42,20 @@ struct OrthoTcArgs {
 template <int ROWS, int CPR, int THREADS>
 struct Converter {
     static constexpr int PER = ROWS * CPR / THREADS;
-    Chunk<true> c[PER];
+    float4 c[PER][2];
     __device__ __forceinline__ void fetch(const OrthoArgs &p, int m, int row0, int col0, int thread)
     {
         const int64_t mat = int64_t(m) * p.rows * p.cols;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int k = thread + i * THREADS, row = row0 + k / CPR, col = col0 + k % CPR * 8;
-            c[i] = load_chunk<true>(p.u, mat + int64_t(row) * p.cols + col, row < p.rows && col < p.cols);
+            c[i][0] = c[i][1] = make_float4(0, 0, 0, 0);
+            if (row < p.rows && col < p.cols) {
+                const float4 *src = reinterpret_cast<const float4 *>(
+                    static_cast<const float *>(p.u) + mat + int64_t(row) * p.cols + col);
+                c[i][0] = src[0];
+                c[i][1] = src[1];
+            }
         }
     }
     __device__ __forceinline__ void put(uint8_t *dst, int lo, int thread) const
@@ -60,8 +64,9 @@ struct Converter {
         for (int i = 0; i < PER; ++i) {
             const int k = thread + i * THREADS;
             uint8_t *at = dst + tile_at<CPR, ROWS>(k / CPR, k % CPR);
-            *reinterpret_cast<uint4 *>(at) = c[i].hi;
-            *reinterpret_cast<uint4 *>(at + lo) = c[i].lo;
+            const Chunk v = split_chunk(c[i][0], c[i][1]);
+            *reinterpret_cast<uint4 *>(at) = v.hi;
+            *reinterpret_cast<uint4 *>(at + lo) = v.lo;
         }
     }
 };
@@ -196,20 +201,27 @@ __global__ void __launch_bounds__(TC_THREADS, 2) gram_tc_kernel(const __grid_con
 
 // ---------------------------------------------------------------- iterate
 
-// D[128 x 128] = X Y^T for operands of three bf16 terms in shared memory (X
-// also in TMEM: columns of 64 words a term), by pairs of terms (i, j) with
-// i + j <= 2, the small ones first.
-template <bool X_TMEM>
+constexpr int OT_ITER_THREADS = 512;
+
+// The shared memory of one CTA's R and Q as three terms, panels of 64 K.
+template <int K>
+constexpr int iter_smem() { return 6 * (K / 64) * OT_PANEL + 128 + 1024; }
+
+// D[128 x 128] = X Y^T over K for operands of three bf16 terms in shared
+// memory (X also in TMEM: K / 2 columns a term), by pairs of terms (i, j)
+// with i + j <= 2, the small ones first.
+template <int K, bool X_TMEM>
 __device__ __forceinline__ void mul_terms(uint32_t d, uint32_t x, uint32_t y)
 {
     constexpr uint32_t IDESC = umma_idesc_bf16(OT_R, OT_R);
+    constexpr uint32_t TERM = uint32_t(K / 64 * OT_PANEL);
     uint32_t acc = 0;
     for (int sum = 2; sum >= 0; --sum)
         for (int i = 0; i <= sum; ++i) {
-            const uint32_t xt = x + uint32_t(i) * (X_TMEM ? 64u : uint32_t(OT_TERM));
-            const uint32_t yt = y + uint32_t(sum - i) * uint32_t(OT_TERM);
+            const uint32_t xt = x + uint32_t(i) * (X_TMEM ? uint32_t(K / 2) : TERM);
+            const uint32_t yt = y + uint32_t(sum - i) * TERM;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
+            for (int kk = 0; kk < K / 16; ++kk) {
                 const uint32_t off = uint32_t((kk >> 2) * OT_PANEL + (kk & 3) * 32);
                 if constexpr (X_TMEM)
                     umma_bf16_tmem_a(d, xt + uint32_t(kk * 8), umma_desc_sw128(yt + off), IDESC, acc);
@@ -234,22 +246,30 @@ __device__ __forceinline__ void split8(const float *v, uint32_t (&t0)[4], uint32
     }
 }
 
-// One matrix a CTA.  Thread (warp w, lane) holds row 32 (w % 4) + lane,
-// columns 64 (w / 4) to + 63: R in registers.  Shared memory: R (then S = Q
-// R, then R again) and Q as three terms; TMEM: two accumulators and P's
-// terms.  A step: R^2 -> Q; then P Q and Q R together; then (Q R) Q.
+// 128 / K matrices a CTA, one under the other: of D = X Y^T the diagonal
+// blocks are their products.  Thread (warp w, lane) holds row 32 (w % 4) +
+// lane, a quarter of its matrix's columns (w / 4): R in registers.  Shared
+// memory: R (then S = Q R, then R again) and Q as three terms; TMEM: two
+// accumulators and P's terms.  A step: R^2 -> Q; then Q R -> S, then S Q ->
+// R, each after the last one's epilogue; P Q runs on the tensor cores
+// during the epilogue of S, and its own epilogue during S Q.
+template <int K>
 __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const OrthoArgs p)
 {
+    constexpr int C = K / 4;                          // columns of a thread
+    constexpr int TERM = K / 64 * OT_PANEL;
     uint8_t *smem = tc_smem();
-    const uint32_t sr = smem_addr(smem), sq = sr + 3 * OT_TERM, bar = sq + 3 * OT_TERM;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + 6 * OT_TERM + 8);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + 6 * OT_TERM + 12);
-    float *s_trace = reinterpret_cast<float *>(smem + 6 * OT_TERM + 16);      // a warp's each
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = blockIdx.x;
-    const int quarter = warp & 3, half = warp >> 2;
-    const int row = quarter * 32 + lane, col0 = half * 64;
+    const uint32_t sr = smem_addr(smem), sq = sr + 3 * TERM, bar = sq + 3 * TERM, bar_p = bar + 8;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + 6 * TERM + 16);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(smem + 6 * TERM + 20);
+    float *s_trace = reinterpret_cast<float *>(smem + 6 * TERM + 24);         // a warp's each
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int quarter = warp & 3, part = warp >> 2;
+    const int row = quarter * 32 + lane, block = quarter * 32 / K;            // of the stack
+    const int m = blockIdx.x * (OT_R / K) + block, mrow = row % K, col0 = part * C;
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(bar_p, 1);
         mbar_fence_init();
         *s_abort = 0;
     }
@@ -262,16 +282,16 @@ __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const Or
     pdl_wait();
     pdl_launch_dependents();
 
-    float rv[64];                                     // this thread's part of R
-    {
-        const int lo = unit_cta(p, int64_t(m) * p.units), hi = unit_cta(p, int64_t(m + 1) * p.units - 1);
+    float rv[C];                                      // this thread's part of R
 #pragma unroll
-        for (int j = 0; j < 64; ++j) rv[j] = 0.0f;
+    for (int j = 0; j < C; ++j) rv[j] = 0.0f;
+    if (m < p.count) {
+        const int lo = unit_cta(p, int64_t(m) * p.units), hi = unit_cta(p, int64_t(m + 1) * p.units - 1);
         for (int c = lo; c <= hi; ++c) {
             const float4 *src = reinterpret_cast<const float4 *>(
-                p.gram + (int64_t(c + m) * OT_R + row) * OT_R + col0);
+                p.gram + (int64_t(c + m) * K + mrow) * K + col0);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < C / 4; ++j) {
                 const float4 x = src[j];
                 rv[4 * j] += x.x;
                 rv[4 * j + 1] += x.y;
@@ -282,48 +302,59 @@ __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const Or
     }
     float trace = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) trace += col0 + j == row ? rv[j] : 0.0f;
+    for (int j = 0; j < C; ++j) trace += col0 + j == mrow ? rv[j] : 0.0f;
     for (int o = 16; o > 0; o >>= 1) trace += __shfl_xor_sync(0xffffffffu, trace, o);
     if (lane == 0) s_trace[warp] = trace;
     __syncthreads();
     trace = 0.0f;
-    for (int w = 0; w < 8; ++w) trace += s_trace[w];
+    for (int w = 0; w < 16; ++w)
+        if ((w & 3) * 32 / K == block) trace += s_trace[w];
     const float f = 1.0f / (sqrtf(trace) + p.eps);
 #pragma unroll
-    for (int j = 0; j < 64; ++j) rv[j] = rv[j] * f * f;
+    for (int j = 0; j < C; ++j) rv[j] = rv[j] * f * f;
 
-    // eight values of this thread's row from column col0 + 8 c, as terms
-    auto to_smem = [&](uint8_t *at, const float *v, int c) {
-        uint32_t t0[4], t1[4], t2[4];
-        split8(v, t0, t1, t2);
-        uint8_t *dst = at + half * OT_PANEL + row * 128 + ((c ^ row) & 7) * 16;
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-        *reinterpret_cast<uint4 *>(dst + OT_TERM) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4 *>(dst + 2 * OT_TERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-    };
-    auto p_to_tmem = [&](const float *v, int c) {
-        uint32_t t0[4], t1[4], t2[4];
-        split8(v, t0, t1, t2);
-        const uint32_t at = tp + lanes + uint32_t(half * 32 + c * 4);
-        tmem_st<4>(at, t0);
-        tmem_st<4>(at + 64, t1);
-        tmem_st<4>(at + 128, t2);
-    };
-    uint16_t *out = p.p + int64_t(m) * 2 * OT_R * OT_R + row * OT_R + col0;
-    auto p_out = [&](const float *v, int c) {
-        uint32_t h[4], l[4];
+    // this thread's values as terms, into an operand in shared memory
+    auto to_smem = [&](uint8_t *at, const float *v) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = v[2 * j] * f * p.scale, b = v[2 * j + 1] * f * p.scale;
-            h[j] = pack_bf16x2(a, b);
-            l[j] = pack_bf16x2(a - bf16_lo(h[j]), b - bf16_hi(h[j]));
+        for (int c = 0; c < C / 8; ++c) {
+            uint32_t t0[4], t1[4], t2[4];
+            split8(v + 8 * c, t0, t1, t2);
+            const int col = col0 + 8 * c;
+            uint8_t *dst = at + (col >> 6) * OT_PANEL + row * 128 + (((col >> 3) ^ row) & 7) * 16;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+            *reinterpret_cast<uint4 *>(dst + TERM) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+            *reinterpret_cast<uint4 *>(dst + 2 * TERM) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
         }
-        *reinterpret_cast<uint4 *>(out + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(out + OT_R * OT_R + 8 * c) = make_uint4(l[0], l[1], l[2], l[3]);
     };
-    // Every thread's writes of operands are done before, and the UMMAs that
-    // `issue` starts are done after (false: the wait ran out).
-    uint32_t phase = 0;
+    auto p_to_tmem = [&](const float *v) {
+#pragma unroll
+        for (int c = 0; c < C / 8; ++c) {
+            uint32_t t0[4], t1[4], t2[4];
+            split8(v + 8 * c, t0, t1, t2);
+            const uint32_t at = tp + lanes + uint32_t(col0 / 2 + c * 4);
+            tmem_st<4>(at, t0);
+            tmem_st<4>(at + K / 2, t1);
+            tmem_st<4>(at + K, t2);
+        }
+    };
+    uint16_t *out = p.p + (int64_t(m) * 2 * K + mrow) * K + col0;
+    auto p_out = [&](const float *v) {
+        if (m >= p.count) return;
+#pragma unroll
+        for (int c = 0; c < C / 8; ++c) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = v[8 * c + 2 * j] * f * p.scale, b = v[8 * c + 2 * j + 1] * f * p.scale;
+                h[j] = pack_bf16x2(a, b);
+                l[j] = pack_bf16x2(a - bf16_lo(h[j]), b - bf16_hi(h[j]));
+            }
+            *reinterpret_cast<uint4 *>(out + 8 * c) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(out + K * K + 8 * c) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    };
+    // Every thread's writes of operands and reads of accumulators are done
+    // before the UMMAs that thread 0 starts.
     auto products = [&](auto issue) {
         tmem_wait_st();
         fence_proxy_async_smem();
@@ -332,88 +363,123 @@ __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const Or
         if (tid == 0) {
             tc_fence_after();
             issue();
-            umma_commit(bar);
         }
         __syncwarp();
-        const bool got = pg_wait(bar, phase, s_abort);
-        phase ^= 1u;
+    };
+    // ... and the wait for them (false: it ran out, for the whole CTA).
+    uint32_t phase = 0, phase_p = 0;
+    auto done = [&](uint32_t b, uint32_t &ph) {
+        const bool got = pg_wait(b, ph, s_abort);
+        ph ^= 1u;
         tc_fence_after();
         return __syncthreads_and(int(got)) != 0;
     };
-    auto load32 = [&](uint32_t d, int c, float *v) {
-        uint32_t w[32];
-        tmem_ld32_nowait(d + lanes + uint32_t(col0 + c), w);
-        tmem_wait_ld();
+    auto load = [&](uint32_t d, float *v) {
+        const uint32_t at = d + lanes + uint32_t(block * K + col0);
+        if constexpr (C == 32) {
+            uint32_t w[32];
+            tmem_ld32_nowait(at, w);
+            tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
+        } else {
+            uint32_t w[16];
+            tmem_ld16_nowait(at, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(w[j]);
+        }
     };
 
-#pragma unroll
-    for (int c = 0; c < 8; ++c) to_smem(smem, rv + 8 * c, c);
-    for (int step = 0; step < p.steps; ++step) {
+    to_smem(smem, rv);
+    bool ok = true;
+    for (int step = 0; ok && step < p.steps; ++step) {
         const bool last = step + 1 == p.steps;
-        if (!products([&] { mul_terms<false>(d0, sr, sr); })) break;
+        float v[C];
+        products([&] {
+            mul_terms<K, false>(d0, sr, sr);
+            umma_commit(bar);
+        });
+        if (!(ok = done(bar, phase))) break;
+        load(d0, v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            load32(d0, 32 * h, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v[j] = fmaf(p.c, v[j], fmaf(p.b, rv[32 * h + j], col0 + 32 * h + j == row ? p.a : 0.0f));
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (!last || step > 0) to_smem(smem + 3 * OT_TERM, v + 8 * c, 4 * h + c);
-                if (step == 0) {                       // P was the identity
-                    if (last) p_out(v + 8 * c, 4 * h + c);
-                    else p_to_tmem(v + 8 * c, 4 * h + c);
-                }
+        for (int j = 0; j < C; ++j)
+            v[j] = fmaf(p.c, v[j], fmaf(p.b, rv[j], col0 + j == mrow ? p.a : 0.0f));
+        to_smem(smem + 3 * TERM, v);
+        if (step == 0) {                               // P was the identity
+            if (last) {
+                p_out(v);
+                break;
             }
+            p_to_tmem(v);
         }
-        if (step == 0 && last) break;
-        if (!products([&] {
-                if (step > 0) mul_terms<true>(d0, tp, sq);
-                if (!last) mul_terms<false>(d1, sq, sr);
-            }))
-            break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float v[32];
-            if (step > 0) {
-                load32(d0, 32 * h, v);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (last) p_out(v + 8 * c, 4 * h + c);
-                    else p_to_tmem(v + 8 * c, 4 * h + c);
-                }
-            }
+        products([&] {
             if (!last) {
-                load32(d1, 32 * h, v);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) to_smem(smem, v + 8 * c, 4 * h + c);
+                mul_terms<K, false>(d1, sq, sr);
+                umma_commit(bar);
             }
+            if (step > 0) {
+                mul_terms<K, true>(d0, tp, sq);
+                umma_commit(bar_p);
+            }
+        });
+        if (!last) {
+            if (!(ok = done(bar, phase))) break;
+            load(d1, v);
+            to_smem(smem, v);
+            products([&] {
+                mul_terms<K, false>(d1, sr, sq);
+                umma_commit(bar);
+            });
+        }
+        if (step > 0) {
+            if (!(ok = done(bar_p, phase_p))) break;
+            load(d0, v);
+            if (last) p_out(v);
+            else p_to_tmem(v);
         }
         if (last) break;
-        if (!products([&] { mul_terms<false>(d1, sr, sq); })) break;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            load32(d1, 32 * h, rv + 32 * h);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) to_smem(smem, rv + 32 * h + 8 * c, 4 * h + c);
-        }
+        if (!(ok = done(bar, phase))) break;
+        load(d1, rv);
+        to_smem(smem, rv);
     }
-    if (*s_abort) {
-        // the UMMAs of the wait that ran out: one more bounded wait for them
-        if (tid == 0) {
-            if (p.error_word != nullptr) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
-            const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-            while (!mbar_try_wait(bar, phase ^ 1u) && clock64() < dd) {
-            }
+    if (!ok && tid == 0) {
+        // nothing in flight when TMEM is released: a bounded wait for all
+        // products so far
+        if (p.error_word != nullptr) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
+        const uint32_t bar_end = bar + 120;
+        mbar_init(bar_end, 1);
+        mbar_fence_init();
+        umma_commit(bar_end);
+        const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+        while (!mbar_try_wait(bar_end, 0) && clock64() < dd) {
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+int launch_iterate_tc(const OrthoArgs &p, int rp, cudaStream_t st)
+{
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return int(e);
+    if (dev >= 64 || !configured[dev]) {
+        if ((e = cudaFuncSetAttribute(iterate_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      iter_smem<64>())) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(iterate_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      iter_smem<128>())) != cudaSuccess)
+            return int(e);
+        if (dev < 64) configured[dev] = 1;
+    }
+    if (rp == 64)
+        return int(launch_kernel(iterate_tc_kernel<64>, dim3(unsigned((p.count + 1) / 2)), dim3(OT_ITER_THREADS),
+                                 iter_smem<64>(), st, p));
+    return int(launch_kernel(iterate_tc_kernel<128>, dim3(unsigned(p.count)), dim3(OT_ITER_THREADS),
+                             iter_smem<128>(), st, p));
 }
 
 // ---------------------------------------------------------------- apply
@@ -563,8 +629,9 @@ apply_tc_kernel(const __grid_constant__ OrthoTcArgs q)
             for (int k = 0; k < conv.PER; ++k) {
                 const int c = thread + k * 128;
                 uint8_t *to = at + tile_at<16, OT_R>(64 * h + c / 16, c % 16);
-                *reinterpret_cast<uint4 *>(to) = conv.c[k].hi;
-                *reinterpret_cast<uint4 *>(to + 2 * OT_PANEL) = conv.c[k].lo;
+                const Chunk v = split_chunk(conv.c[k][0], conv.c[k][1]);
+                *reinterpret_cast<uint4 *>(to) = v.hi;
+                *reinterpret_cast<uint4 *>(to + 2 * OT_PANEL) = v.lo;
             }
         };
         int issued = 0;
@@ -606,8 +673,6 @@ static int run_tc(const OrthoTcArgs &q, cudaStream_t st)
     if (dev >= 64 || !configured[dev]) {
         if ((e = cudaFuncSetAttribute(gram_tc_kernel<TALL, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       OT_GRAM_SMEM)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(iterate_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      OT_ITER_SMEM)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(apply_tc_kernel<TALL, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       OT_APPLY_SMEM)) != cudaSuccess)
             return int(e);
@@ -615,8 +680,7 @@ static int run_tc(const OrthoTcArgs &q, cudaStream_t st)
     }
     e = launch_kernel(gram_tc_kernel<TALL, F32>, dim3(unsigned(q.o.ctas)), dim3(TC_THREADS), OT_GRAM_SMEM, st, q);
     if (e != cudaSuccess) return int(e);
-    e = launch_kernel(iterate_tc_kernel, dim3(unsigned(q.o.count)), dim3(OT_ITER_THREADS), OT_ITER_SMEM, st, q.o);
-    if (e != cudaSuccess) return int(e);
+    if (int r = launch_iterate_tc(q.o, OT_R, st)) return r;
     const int64_t tiles = int64_t(q.o.count) * ((q.o.n + OT_R - 1) / OT_R);
     const int sms = device_sm_count();
     e = launch_kernel(apply_tc_kernel<TALL, F32>, dim3(unsigned(tiles < sms ? tiles : sms)),
