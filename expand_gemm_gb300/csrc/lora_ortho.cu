@@ -16,8 +16,8 @@
 // directions that U has little of, which cancel where U is large, so one
 // bf16 would show in the result.
 //
-// This file: ranks up to 64, on mma.sync, and the steps up to 32 in FFMA.
-// lora_ortho_tc.cu: ranks to 128, and the steps from 33, on tcgen05.
+// This file: ranks up to 32, on mma.sync, the steps in FFMA.
+// lora_ortho_tc.cu: ranks 33 to 128, on tcgen05.
 #include <math.h>
 
 #include "lora_ortho.cuh"
@@ -26,47 +26,78 @@ namespace lora {
 
 // ---------------------------------------------------------------- rings
 //
-// Tiles of U come by cp.async, several in flight.  A bf16 tile lands
-// swizzled, ready for ldmatrix.  An fp32 tile lands as it is: every thread
-// copies its own chunks of eight entries, and later turns those same chunks
-// into two bf16 terms of a tile that the warps then share.
+// Every warp works by itself on its part of a tile of U, so that no barrier
+// of the block stands in the loops.  Its 16-byte pieces come by cp.async,
+// several tiles ahead, neighbouring lanes copying neighbouring pieces (a
+// lane copying both halves of its eight fp32 entries halved the rate: every
+// 32-byte sector was asked for twice).  A bf16 tile lands swizzled, ready
+// for ldmatrix.  An fp32 tile lands as it is and is turned into two bf16
+// terms in the warp's part of another tile.  SPLIT_ROWS: a warp's part is an
+// eighth of the tile's rows, else of its columns.
 
-template <int ROWS, int CPR, bool F32>
+template <int ROWS, int CPR, bool SPLIT_ROWS, bool F32>
 struct TileRing {
-    static constexpr int PER = ROWS * CPR / OR_THREADS;            // chunks of a thread
+    static constexpr int PER = ROWS * CPR / OR_THREADS;            // chunks of a lane
     static constexpr int BYTES = ROWS * CPR * (F32 ? 32 : 16);
     static constexpr int TERM = ROWS * CPR * 16;                   // one bf16 term
-    static_assert(PER >= 1, "a chunk a thread at least");
+    static_assert(PER >= 1 && (SPLIT_ROWS ? ROWS : CPR) % 8 == 0, "an eighth a warp");
 
+    __device__ __forceinline__ static void place(int i, int &row, int &ch)
+    {
+        const int warp = threadIdx.x >> 5, at = (threadIdx.x & 31) + 32 * i;
+        if constexpr (SPLIT_ROWS) {
+            row = warp * (ROWS / 8) + at / CPR;
+            ch = at % CPR;
+        } else {
+            row = at / (CPR / 8);
+            ch = warp * (CPR / 8) + at % (CPR / 8);
+        }
+    }
     __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
                                                  int col0)
     {
+        if constexpr (F32) {
+            constexpr int PPR = SPLIT_ROWS ? CPR * 2 : CPR / 4;    // pieces a row of the warp's part
+            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int c = threadIdx.x + i * OR_THREADS, row = row0 + c / CPR, col = col0 + c % CPR * 8;
-            const bool ok = row < p.rows && col < p.cols;
-            const int64_t at = ok ? mat + int64_t(row) * p.cols + col : 0;
-            if constexpr (F32) {
-                const float *src = static_cast<const float *>(p.u) + at;
-                const uint32_t dst = smem_addr(stage + (2 * i * OR_THREADS + threadIdx.x) * 16);
-                cp_async16(dst, src, ok);
-                cp_async16(dst + OR_THREADS * 16, src + 4, ok);
-            } else {
-                cp_async16(smem_addr(stage + tile_at<CPR, ROWS>(c / CPR, c % CPR)),
-                           static_cast<const uint16_t *>(p.u) + at, ok);
+            for (int i = 0; i < 2 * PER; ++i) {
+                const int at = lane + 32 * i;
+                const int row = row0 + (SPLIT_ROWS ? warp * (ROWS / 8) : 0) + at / PPR;
+                const int col = col0 + (SPLIT_ROWS ? 0 : warp * CPR) + at % PPR * 4;
+                const bool ok = row < p.rows && col < p.cols;
+                cp_async16(smem_addr(stage + piece(warp, at)),
+                           static_cast<const float *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                int r, ch;
+                place(i, r, ch);
+                const int row = row0 + r, col = col0 + ch * 8;
+                const bool ok = row < p.rows && col < p.cols;
+                cp_async16(smem_addr(stage + tile_at<CPR, ROWS>(r, ch)),
+                           static_cast<const uint16_t *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
             }
         }
     }
-    // fp32: this thread's chunks of a landed stage, as terms of `tile`.
+    // Where a warp's 16-byte piece lies: the even ones first, so that lanes
+    // reading neighbouring pairs meet no bank conflicts.
+    __device__ __forceinline__ static int piece(int warp, int at)
+    {
+        return (warp * 64 * PER + (at & 1) * 32 * PER + (at >> 1)) * 16;
+    }
+    // fp32: a landed stage as terms of `tile`.
     __device__ __forceinline__ static void convert(const uint8_t *stage, uint8_t *tile)
     {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint8_t *src = stage + (2 * i * OR_THREADS + threadIdx.x) * 16;
+            const uint8_t *src = stage + piece(warp, 2 * (lane + 32 * i));
             const Chunk k = split_chunk(*reinterpret_cast<const float4 *>(src),
-                                              *reinterpret_cast<const float4 *>(src + OR_THREADS * 16));
-            const int c = threadIdx.x + i * OR_THREADS;
-            uint8_t *at = tile + tile_at<CPR, ROWS>(c / CPR, c % CPR);
+                                        *reinterpret_cast<const float4 *>(src + 32 * PER * 16));
+            int row, ch;
+            place(i, row, ch);
+            uint8_t *at = tile + tile_at<CPR, ROWS>(row, ch);
             *reinterpret_cast<uint4 *>(at) = k.hi;
             *reinterpret_cast<uint4 *>(at + TERM) = k.lo;
         }
@@ -75,37 +106,32 @@ struct TileRing {
 
 // ---------------------------------------------------------------- gram
 
-// Warps of gram_kernel: WM over the rows of the RP x RP result, WK over the
-// K step (a tile of 4096 entries).
-template <int RP> struct GramShape { static constexpr int WM = RP == 64 ? 2 : 1, WK = 8 / WM; };
-
 template <int RP>
-constexpr int gram_step() { return 4096 / RP; }
+constexpr int gram_step() { return 4096 / RP; }     // of the long side, a tile of 4096 entries
 
 template <bool F32>
-constexpr int gram_stages() { return F32 ? 4 : 6; }
+constexpr int gram_stages() { return F32 ? 3 : 5; }
 
 template <int RP, bool F32>
 constexpr int gram_smem()
 {
-    return 4096 * (gram_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 8 : 0)) + RP * RP * 4;
+    return 4096 * (gram_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 0)) + RP * RP * 4;
 }
 
-// Each block sums over its run of units.  TALL: U is [n][r] (its rows are
-// K), else [r][n].
+// Each block sums over its run of units; a warp takes an eighth of a unit's
+// K, the 8-column blocks on and right of the diagonal.  TALL: U is [n][r]
+// (its rows are K), else [r][n].
 template <int RP, bool TALL, bool F32>
-__global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
+__global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
 {
-    constexpr int WM = GramShape<RP>::WM, WK = GramShape<RP>::WK;
     constexpr int KS = gram_step<RP>(), ST = gram_stages<F32>();
     constexpr int ROWS = TALL ? KS : RP, CPR = (TALL ? RP : KS) / 8;     // of the tile
-    constexpr int MI = RP / WM / 16, NI = RP / 8;
-    using Ring = TileRing<ROWS, CPR, F32>;
+    constexpr int MI = RP / 16, NI = RP / 8;
+    using Ring = TileRing<ROWS, CPR, TALL, F32>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *terms = smem + ST * Ring::BYTES;                       // fp32: two converted tiles
-    float *sum = reinterpret_cast<float *>(terms + (F32 ? 4 * Ring::TERM : 0));
+    uint8_t *terms = smem + ST * Ring::BYTES;                       // fp32: the converted tile
+    float *sum = reinterpret_cast<float *>(terms + (F32 ? 2 * Ring::TERM : 0));
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int wk = warp / WM, m0 = warp % WM * (RP / WM);
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
@@ -119,27 +145,25 @@ __global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
     };
     float acc[MI][NI][4] = {};
     for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
-    int stage = 0, buf = 0;
+    int stage = 0;
     for (int64_t unit = first; unit < end; ++unit) {
         cp_async_wait<ST - 2>();
-        uint32_t hi;
+        uint32_t hi = smem_addr(smem + stage * Ring::BYTES);
+        __syncwarp();
         if constexpr (F32) {
-            Ring::convert(smem + stage * Ring::BYTES, terms + buf * 2 * Ring::TERM);
-            hi = smem_addr(terms + buf * 2 * Ring::TERM);
-            buf ^= 1;
-        } else {
-            hi = smem_addr(smem + stage * Ring::BYTES);
+            Ring::convert(smem + stage * Ring::BYTES, terms);
+            hi = smem_addr(terms);
+            __syncwarp();
         }
-        __syncthreads();
         issue(unit + ST - 1, (stage + ST - 1) % ST);
         stage = stage + 1 == ST ? 0 : stage + 1;
 #pragma unroll
-        for (int kk = wk * (KS / WK); kk < (wk + 1) * (KS / WK); kk += 16) {
+        for (int kk = warp * (KS / 8); kk < (warp + 1) * (KS / 8); kk += 16) {
             uint32_t a[MI][4], al[MI][4];
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                frag_a<CPR, ROWS, !TALL>(hi, m0 + 16 * i, kk, a[i]);
-                if constexpr (F32) frag_a<CPR, ROWS, !TALL>(hi + Ring::TERM, m0 + 16 * i, kk, al[i]);
+                frag_a<CPR, ROWS, !TALL>(hi, 16 * i, kk, a[i]);
+                if constexpr (F32) frag_a<CPR, ROWS, !TALL>(hi + Ring::TERM, 16 * i, kk, al[i]);
             }
 #pragma unroll
             for (int j = 0; j < NI; j += 2) {
@@ -147,7 +171,7 @@ __global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
                 frag_b<CPR, ROWS, !TALL>(hi, kk, 8 * j, b);
                 if constexpr (F32) frag_b<CPR, ROWS, !TALL>(hi + Ring::TERM, kk, 8 * j, bl);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
+                for (int i = 0; i <= j / 2; ++i) {
                     mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
                     mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
                     if constexpr (F32) {
@@ -160,17 +184,18 @@ __global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
             }
         }
         if (unit + 1 < end && (unit + 1) % p.units != 0) continue;
-        // the matrix or the run ends: the warps' sums over K, one after the other
+        // the matrix or the run ends: the warps' sums over K, one after the
+        // other; what lies left of the diagonal is the mirror image
         const int g = (tid & 31) >> 2, t = tid & 3;
-        for (int w = 0; w < WK; ++w) {
-            if (wk == w) {
+        for (int w = 0; w < 8; ++w) {
+            if (warp == w) {
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
-                    for (int j = 0; j < NI; ++j)
+                    for (int j = 2 * i; j < NI; ++j)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float2 *at = reinterpret_cast<float2 *>(sum + (m0 + 16 * i + g + 8 * h) * RP + 8 * j + 2 * t);
+                            float2 *at = reinterpret_cast<float2 *>(sum + (16 * i + g + 8 * h) * RP + 8 * j + 2 * t);
                             const float2 was = w > 0 ? *at : make_float2(0.0f, 0.0f);
                             *at = make_float2(was.x + acc[i][j][2 * h], was.y + acc[i][j][2 * h + 1]);
                             acc[i][j][2 * h] = acc[i][j][2 * h + 1] = 0.0f;
@@ -178,8 +203,12 @@ __global__ void __launch_bounds__(OR_THREADS, 2) gram_kernel(const OrthoArgs p)
             }
             __syncthreads();
         }
-        float4 *out = reinterpret_cast<float4 *>(p.gram + (blockIdx.x + unit / p.units) * RP * RP);
-        for (int i = tid; i < RP * RP / 4; i += OR_THREADS) out[i] = reinterpret_cast<const float4 *>(sum)[i];
+        float *out = p.gram + (blockIdx.x + unit / p.units) * RP * RP;
+        for (int i = tid; i < RP * RP; i += OR_THREADS) {
+            const int y = i / RP, x = i % RP;
+            out[i] = sum[x / 16 < y / 16 ? x * RP + y : i];
+        }
+        __syncthreads();
     }
     cp_async_wait<0>();
 }
@@ -299,34 +328,32 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
 
 constexpr int OR_LONG = 128;              // long-side elements of a tile of apply_kernel
 
-template <int RP, bool F32>
-constexpr int apply_stages() { return RP == 64 ? (F32 ? 2 : 3) : 4; }
+template <bool F32>
+constexpr int apply_stages() { return F32 ? 3 : 4; }
 
 // P's terms, the ring, and a tile that holds the converted terms (fp32) and
 // then the output.
 template <int RP, bool F32>
 constexpr int apply_smem()
 {
-    return 2 * RP * RP * 2 + RP * OR_LONG * (apply_stages<RP, F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 2));
+    return 2 * RP * RP * 2 + RP * OR_LONG * (apply_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 2));
 }
 
-// Each block takes a run of tiles of the stacked matrices, P of the current
-// one in shared memory: out = P U (or U P, TALL; P is symmetric).
+// Each block takes a run of tiles of the stacked matrices: out = P U (or U
+// P, TALL; P is symmetric).  A warp takes 16 of a tile's 128 long-side
+// elements, from load to store; P's fragments stay in its registers.
 template <int RP, bool TALL, bool F32>
-__global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
+__global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
 {
     constexpr int ROWS = TALL ? OR_LONG : RP, COLS = TALL ? RP : OR_LONG;
-    constexpr int CPR = COLS / 8, PCPR = RP / 8, ST = apply_stages<RP, F32>();
-    // warps over the [ROWS x COLS] output
-    constexpr int WM = TALL ? 8 : RP / 16, WN = 8 / WM;
-    constexpr int MI = ROWS / WM / 16, NI = COLS / WN / 8;
-    using Ring = TileRing<ROWS, CPR, F32>;
-    static_assert(MI >= 1 && NI >= 2, "shape");
+    constexpr int CPR = COLS / 8, PCPR = RP / 8, ST = apply_stages<F32>();
+    constexpr int MI = TALL ? 1 : RP / 16, NI = TALL ? RP / 8 : 2, KK = RP / 16;
+    using Ring = TileRing<ROWS, CPR, TALL, F32>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem + 2 * RP * RP * 2, *tile_buf = ring + ST * Ring::BYTES;
     const uint32_t sp = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int m0 = warp % WM * (ROWS / WM), n0 = warp / WM * (COLS / WN);
+    const int m0 = TALL ? warp * 16 : 0, n0 = TALL ? 0 : warp * 16;
     pdl_wait();
     pdl_launch_dependents();
     const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
@@ -341,69 +368,67 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
     };
     for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
     int held = -1, stage = 0;
+    uint32_t pf[2][KK][RP / 16][4];        // P: terms, K steps, 16 rows (or columns) each
     for (int64_t item = first; item < end; ++item) {
         const int m = int(item / tiles), tile = int(item % tiles);
         const int64_t mat = int64_t(m) * p.rows * p.cols;
-        cp_async_wait<ST - 2>();
-        __syncthreads();                       // the last tile's output has left
         if (m != held) {
+            __syncthreads();
             const uint4 *gp = reinterpret_cast<const uint4 *>(p.p + int64_t(m) * 2 * RP * RP);
             for (int i = tid; i < 2 * RP * PCPR; i += OR_THREADS) {
                 const int term = i / (RP * PCPR), c = i % (RP * PCPR);
                 *reinterpret_cast<uint4 *>(smem + term * RP * RP * 2 +
                                            tile_at<PCPR, RP>(c / PCPR, c % PCPR)) = gp[i];
             }
+            __syncthreads();
+            held = m;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int i = 0; i < RP / 16; ++i) {
+                        if constexpr (TALL) frag_b<PCPR, RP, true>(sp + t * RP * RP * 2, 16 * k, 16 * i, pf[t][k][i]);
+                        else frag_a<PCPR, RP, true>(sp + t * RP * RP * 2, 16 * i, 16 * k, pf[t][k][i]);
+                    }
         }
+        cp_async_wait<ST - 2>();
+        __syncwarp();                          // and the last tile's output has left
         uint32_t su = smem_addr(ring + stage * Ring::BYTES);
         if constexpr (F32) {
             Ring::convert(ring + stage * Ring::BYTES, tile_buf);
             su = smem_addr(tile_buf);
+            __syncwarp();
         }
-        if (F32 || m != held) __syncthreads();
-        held = m;
         issue(item + ST - 1, (stage + ST - 1) % ST);
         stage = stage + 1 == ST ? 0 : stage + 1;
         float acc[MI][NI][4] = {};
-#pragma unroll 2
-        for (int kk = 0; kk < RP; kk += 16) {
-            uint32_t a[MI][4], al[MI][4];
 #pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                if constexpr (TALL) {
-                    frag_a<CPR, ROWS, true>(su, m0 + 16 * i, kk, a[i]);
-                    if constexpr (F32) frag_a<CPR, ROWS, true>(su + Ring::TERM, m0 + 16 * i, kk, al[i]);
-                } else {
-                    frag_a<PCPR, RP, true>(sp, m0 + 16 * i, kk, a[i]);
-                    frag_a<PCPR, RP, true>(sp + RP * RP * 2, m0 + 16 * i, kk, al[i]);
-                }
-            }
+        for (int k = 0; k < KK; ++k) {
+            // a term of U's fragments (hi, then lo) with P's terms
 #pragma unroll
-            for (int j = 0; j < NI; j += 2) {
-                uint32_t b[4], bl[4];
-                if constexpr (TALL) {
-                    frag_b<PCPR, RP, true>(sp, kk, n0 + 8 * j, b);
-                    frag_b<PCPR, RP, true>(sp + RP * RP * 2, kk, n0 + 8 * j, bl);
-                } else {
-                    frag_b<CPR, ROWS, false>(su, kk, n0 + 8 * j, b);
-                    if constexpr (F32) frag_b<CPR, ROWS, false>(su + Ring::TERM, kk, n0 + 8 * j, bl);
-                }
+            for (int ut = 0; ut < (F32 ? 2 : 1); ++ut) {
+                uint32_t u[4];
+                if constexpr (TALL) frag_a<CPR, ROWS, true>(su + ut * Ring::TERM, m0, 16 * k, u);
+                else frag_b<CPR, ROWS, false>(su + ut * Ring::TERM, 16 * k, n0, u);
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
-                    mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
-                    if constexpr (F32 || !TALL) {
-                        mma_bf16_16816(acc[i][j], al[i], b[0], b[1]);
-                        mma_bf16_16816(acc[i][j + 1], al[i], b[2], b[3]);
+                for (int t = 0; t < (ut == 0 ? 2 : 1); ++t)
+#pragma unroll
+                    for (int i = 0; i < RP / 16; ++i) {
+                        const uint32_t(&q)[4] = pf[t][k][i];
+                        if constexpr (TALL) {
+                            mma_bf16_16816(acc[0][2 * i], u, q[0], q[1]);
+                            mma_bf16_16816(acc[0][2 * i + 1], u, q[2], q[3]);
+                        } else {
+                            mma_bf16_16816(acc[i][0], q, u[0], u[1]);
+                            mma_bf16_16816(acc[i][1], q, u[2], u[3]);
+                        }
                     }
-                    if constexpr (F32 || TALL) {
-                        mma_bf16_16816(acc[i][j], a[i], bl[0], bl[1]);
-                        mma_bf16_16816(acc[i][j + 1], a[i], bl[2], bl[3]);
-                    }
-                }
             }
         }
-        // through shared memory, so that rows are written 16 bytes at a time
-        if (F32) __syncthreads();
+        // through the warp's part of the tile, so that rows are written 16
+        // bytes at a time
+        __syncwarp();
         const int g = (tid & 31) >> 2, t = tid & 3;
 #pragma unroll
         for (int i = 0; i < MI; ++i)
@@ -415,10 +440,11 @@ __global__ void __launch_bounds__(OR_THREADS) apply_kernel(const OrthoArgs p)
                 *reinterpret_cast<uint32_t *>(tile_buf + tile_at<CPR, ROWS>(row + 8, col / 8) + col % 8 * 2) =
                     pack_bf16x2(acc[i][j][2], acc[i][j][3]);
             }
-        __syncthreads();
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < Ring::PER; ++i) {
-            const int c = tid + i * OR_THREADS, row = c / CPR, ch = c % CPR;
+            int row, ch;
+            Ring::place(i, row, ch);
             const int gr = TALL ? tile * OR_LONG + row : row;
             const int gc = (TALL ? 0 : tile * OR_LONG) + ch * 8;
             if (gr < p.rows && gc < p.cols)
@@ -436,33 +462,25 @@ struct OrthoLayout {
     int64_t p, bytes;
 };
 
-// Blocks of a kernel on an SM by its shared memory, at most `most`.
-static int blocks_per_sm(int smem, int most)
-{
-    const int n = 227 * 1024 / (smem + 1024);
-    return n > most ? most : n;
-}
-
-template <bool F32>
-static int gram_blocks(int rp)
-{
-    return rp == 16 ? blocks_per_sm(gram_smem<16, F32>(), 2)
-                    : rp == 32 ? blocks_per_sm(gram_smem<32, F32>(), 2) : blocks_per_sm(gram_smem<64, F32>(), 2);
-}
+constexpr int OR_BLOCKS = 3;              // of gram_kernel and apply_kernel on an SM
 
 // The sum U U^T is cut into units of one tile each and those into as many
-// runs as blocks fit the GPU at once (or as there are units).
-static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, bool f32, int sms)
+// runs as blocks fit the GPU at once, but not so many that a matrix has more
+// parts than about the root of its units (at least four): the next kernel's
+// one block a matrix reads them all.
+static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, int sms)
 {
     OrthoLayout l;
     l.r = rows <= cols ? rows : cols;
     l.n = rows <= cols ? cols : rows;
     l.rp = 16;
     while (l.rp < l.r) l.rp *= 2;
-    l.unit = l.rp == 128 ? OR_TC_UNIT : l.rp == 64 ? gram_step<64>() : l.rp == 32 ? gram_step<32>() : gram_step<16>();
+    l.unit = l.rp >= 64 ? OR_TC_UNIT : l.rp == 32 ? gram_step<32>() : gram_step<16>();
     l.units = (l.n + l.unit - 1) / l.unit;
-    const int64_t most = int64_t(sms) * (l.rp == 128 ? OR_TC_CTAS
-                                                     : f32 ? gram_blocks<true>(l.rp) : gram_blocks<false>(l.rp));
+    int parts = 4;
+    while (int64_t(parts) * parts < l.units) ++parts;
+    int64_t most = int64_t(sms) * (l.rp >= 64 ? OR_TC_CTAS : OR_BLOCKS);
+    if (int64_t(count) * parts < most) most = int64_t(count) * parts;
     const int64_t total = int64_t(count) * l.units;
     l.ctas = int(total < most ? total : most);
     l.p = (int64_t(l.ctas) + count) * l.rp * l.rp * 4;
@@ -482,7 +500,7 @@ template <int RP, bool TALL, bool F32>
 static int run_ortho(const OrthoArgs &p, cudaStream_t st)
 {
     constexpr int gs = gram_smem<RP, F32>(), as = apply_smem<RP, F32>();
-    [[maybe_unused]] constexpr int is = 3 * RP * RP * 4;
+    constexpr int is = 3 * RP * RP * 4;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -495,27 +513,13 @@ static int run_ortho(const OrthoArgs &p, cudaStream_t st)
     }
     e = launch_kernel(gram_kernel<RP, TALL, F32>, dim3(p.ctas), dim3(OR_THREADS), gs, st, p);
     if (e != cudaSuccess) return int(e);
-    if constexpr (RP == 64) {
-        if (int r = launch_iterate_tc(p, RP, st)) return r;
-    } else {
-        e = launch_kernel(iterate_kernel<RP>, dim3(p.count), dim3(OR_THREADS), is, st, p);
-        if (e != cudaSuccess) return int(e);
-    }
+    e = launch_kernel(iterate_kernel<RP>, dim3(p.count), dim3(OR_THREADS), is, st, p);
+    if (e != cudaSuccess) return int(e);
     const int64_t tiles = int64_t(p.count) * ((p.n + OR_LONG - 1) / OR_LONG);
-    const int64_t most = int64_t(device_sm_count()) * blocks_per_sm(as, 4);
+    const int64_t most = int64_t(device_sm_count()) * OR_BLOCKS;
     e = launch_kernel(apply_kernel<RP, TALL, F32>, dim3(unsigned(tiles < most ? tiles : most)),
                       dim3(OR_THREADS), as, st, p);
     return e == cudaSuccess ? LORA_OK : int(e);
-}
-
-template <bool TALL, bool F32>
-static int run_ortho_rank(const OrthoArgs &p, int rp, cudaStream_t st)
-{
-    switch (rp) {
-    case 16: return run_ortho<16, TALL, F32>(p, st);
-    case 32: return run_ortho<32, TALL, F32>(p, st);
-    default: return run_ortho<64, TALL, F32>(p, st);
-    }
 }
 
 static bool ortho_sizes_ok(int32_t count, int32_t rows, int32_t cols)
@@ -530,10 +534,7 @@ static bool ortho_sizes_ok(int32_t count, int32_t rows, int32_t cols)
 LORA_API int64_t lora_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols)
 {
     if (!lora::ortho_sizes_ok(count, rows, cols)) return LORA_ERR_SIZE;
-    const int sms = lora::device_sm_count();
-    const int64_t a = lora::ortho_layout(count > 0 ? count : 1, rows, cols, false, sms).bytes;
-    const int64_t b = lora::ortho_layout(count > 0 ? count : 1, rows, cols, true, sms).bytes;
-    return a > b ? a : b;
+    return lora::ortho_layout(count > 0 ? count : 1, rows, cols, lora::device_sm_count()).bytes;
 }
 
 LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, int32_t rows,
@@ -548,7 +549,7 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     if (update == nullptr || out == nullptr || workspace == nullptr) return LORA_ERR_NULL;
     auto bits = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
     if ((bits(update) | bits(out)) & 15u || bits(workspace) & 255u) return LORA_ERR_ALIGN;
-    const OrthoLayout l = ortho_layout(count, rows, cols, update_f32 != 0, device_sm_count());
+    const OrthoLayout l = ortho_layout(count, rows, cols, device_sm_count());
     if (workspace_bytes < l.bytes) return LORA_ERR_WORKSPACE;
     OrthoArgs p;
     p.u = update;
@@ -572,8 +573,11 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     p.p = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + l.p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool tall = rows > cols;
-    if (l.rp == 128) return run_ortho_tc(p, update_f32 != 0, st);
-    if (update_f32)
-        return tall ? run_ortho_rank<true, true>(p, l.rp, st) : run_ortho_rank<false, true>(p, l.rp, st);
-    return tall ? run_ortho_rank<true, false>(p, l.rp, st) : run_ortho_rank<false, false>(p, l.rp, st);
+    if (l.rp >= 64) return run_ortho_tc(p, l.rp, update_f32 != 0, st);
+    if (l.rp == 16) {
+        if (update_f32) return tall ? run_ortho<16, true, true>(p, st) : run_ortho<16, false, true>(p, st);
+        return tall ? run_ortho<16, true, false>(p, st) : run_ortho<16, false, false>(p, st);
+    }
+    if (update_f32) return tall ? run_ortho<32, true, true>(p, st) : run_ortho<32, false, true>(p, st);
+    return tall ? run_ortho<32, true, false>(p, st) : run_ortho<32, false, false>(p, st);
 }

@@ -63,10 +63,8 @@ __device__ __forceinline__ Chunk split_chunk(const float4 &x, const float4 &y)
     return Chunk{make_uint4(h[0], h[1], h[2], h[3]), make_uint4(l[0], l[1], l[2], l[3])};
 }
 
-// Rank 65 to 128 (lora_ortho_tc.cu).  Returns 0 or an error.
-int run_ortho_tc(OrthoArgs p, bool f32, cudaStream_t st);
-// The steps alone, padded rank 64 or 128.  Returns 0 or an error.
-int launch_iterate_tc(const OrthoArgs &p, int rp, cudaStream_t st);
+// Padded ranks 64 and 128 (lora_ortho_tc.cu).  Returns 0 or an error.
+int run_ortho_tc(OrthoArgs p, int rp, bool f32, cudaStream_t st);
 constexpr int OR_TC_UNIT = 64;
 constexpr int OR_TC_CTAS = 2;         // of the sum U U^T on an SM
 
