@@ -35,6 +35,28 @@ namespace lora {
 // terms in the warp's part of another tile.  SPLIT_ROWS: a warp's part is an
 // eighth of the tile's rows, else of its columns.
 
+// A walk over the tiles of the stacked matrices, without divisions in the
+// loop (64-bit ones took half of its instructions).
+struct TileWalk {
+    int64_t left;             // tiles still to come
+    int64_t mat;              // first element of the matrix
+    int m, k;                 // matrix, tile in it
+    __device__ __forceinline__ TileWalk(int64_t first, int64_t end, int per, int64_t size)
+        : left(end - first), m(int(first / per)), k(int(first % per))
+    {
+        mat = m * size;
+    }
+    __device__ __forceinline__ void next(int per, int64_t size)
+    {
+        --left;
+        if (++k == per) {
+            k = 0;
+            ++m;
+            mat += size;
+        }
+    }
+};
+
 template <int ROWS, int CPR, bool SPLIT_ROWS, bool F32>
 struct TileRing {
     static constexpr int PER = ROWS * CPR / OR_THREADS;            // chunks of a lane
@@ -135,18 +157,19 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
     pdl_wait();
     pdl_launch_dependents();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
-    auto issue = [&](int64_t unit, int stage) {
-        if (unit < end) {
-            const int k = int(unit % p.units) * KS;
-            Ring::issue(p, smem + stage * Ring::BYTES, unit / p.units * p.rows * p.cols, TALL ? k : 0,
-                        TALL ? 0 : k);
+    const int64_t size = int64_t(p.rows) * p.cols;
+    TileWalk in(first, end, p.units, size), run(first, end, p.units, size);
+    auto issue = [&](int stage) {
+        if (in.left > 0) {
+            Ring::issue(p, smem + stage * Ring::BYTES, in.mat, TALL ? in.k * KS : 0, TALL ? 0 : in.k * KS);
+            in.next(p.units, size);
         }
         cp_async_commit();
     };
     float acc[MI][NI][4] = {};
-    for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
+    for (int i = 0; i < ST - 1; ++i) issue(i);
     int stage = 0;
-    for (int64_t unit = first; unit < end; ++unit) {
+    for (; run.left > 0; run.next(p.units, size)) {
         cp_async_wait<ST - 2>();
         uint32_t hi = smem_addr(smem + stage * Ring::BYTES);
         __syncwarp();
@@ -155,7 +178,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
             hi = smem_addr(terms);
             __syncwarp();
         }
-        issue(unit + ST - 1, (stage + ST - 1) % ST);
+        issue(stage == 0 ? ST - 1 : stage - 1);
         stage = stage + 1 == ST ? 0 : stage + 1;
 #pragma unroll
         for (int kk = warp * (KS / 8); kk < (warp + 1) * (KS / 8); kk += 16) {
@@ -183,7 +206,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
                 }
             }
         }
-        if (unit + 1 < end && (unit + 1) % p.units != 0) continue;
+        if (run.left > 1 && run.k + 1 != p.units) continue;
         // the matrix or the run ends: the warps' sums over K, one after the
         // other; what lies left of the diagonal is the mirror image
         const int g = (tid & 31) >> 2, t = tid & 3;
@@ -203,7 +226,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
             }
             __syncthreads();
         }
-        float *out = p.gram + (blockIdx.x + unit / p.units) * RP * RP;
+        float *out = p.gram + (int64_t(blockIdx.x) + run.m) * RP * RP;
         for (int i = tid; i < RP * RP; i += OR_THREADS) {
             const int y = i / RP, x = i % RP;
             out[i] = sum[x / 16 < y / 16 ? x * RP + y : i];
@@ -359,19 +382,21 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
     const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
     const int64_t total = int64_t(p.count) * tiles;
     const int64_t first = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
-    auto issue = [&](int64_t item, int stage) {
-        if (item < end) {
-            const int n = int(item % tiles) * OR_LONG;
-            Ring::issue(p, ring + stage * Ring::BYTES, item / tiles * p.rows * p.cols, TALL ? n : 0, TALL ? 0 : n);
+    const int64_t size = int64_t(p.rows) * p.cols;
+    TileWalk in(first, end, tiles, size), run(first, end, tiles, size);
+    auto issue = [&](int stage) {
+        if (in.left > 0) {
+            const int n = in.k * OR_LONG;
+            Ring::issue(p, ring + stage * Ring::BYTES, in.mat, TALL ? n : 0, TALL ? 0 : n);
+            in.next(tiles, size);
         }
         cp_async_commit();
     };
-    for (int i = 0; i < ST - 1; ++i) issue(first + i, i);
+    for (int i = 0; i < ST - 1; ++i) issue(i);
     int held = -1, stage = 0;
     uint32_t pf[2][KK][RP / 16][4];        // P: terms, K steps, 16 rows (or columns) each
-    for (int64_t item = first; item < end; ++item) {
-        const int m = int(item / tiles), tile = int(item % tiles);
-        const int64_t mat = int64_t(m) * p.rows * p.cols;
+    for (; run.left > 0; run.next(tiles, size)) {
+        const int m = run.m, tile = run.k;
         if (m != held) {
             __syncthreads();
             const uint4 *gp = reinterpret_cast<const uint4 *>(p.p + int64_t(m) * 2 * RP * RP);
@@ -400,7 +425,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
             su = smem_addr(tile_buf);
             __syncwarp();
         }
-        issue(item + ST - 1, (stage + ST - 1) % ST);
+        issue(stage == 0 ? ST - 1 : stage - 1);
         stage = stage + 1 == ST ? 0 : stage + 1;
         float acc[MI][NI][4] = {};
 #pragma unroll
@@ -448,7 +473,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
             const int gr = TALL ? tile * OR_LONG + row : row;
             const int gc = (TALL ? 0 : tile * OR_LONG) + ch * 8;
             if (gr < p.rows && gc < p.cols)
-                *reinterpret_cast<uint4 *>(p.out + mat + int64_t(gr) * p.cols + gc) =
+                *reinterpret_cast<uint4 *>(p.out + run.mat + int64_t(gr) * p.cols + gc) =
                     *reinterpret_cast<const uint4 *>(tile_buf + tile_at<CPR, ROWS>(row, ch));
         }
     }

@@ -351,22 +351,24 @@ __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const Or
         // where Q will be; a thread's row is then read back (a chunk of four
         // at its place ^ row, against bank conflicts).
         float *sum = reinterpret_cast<float *>(smem + 3 * TERM);
-        for (int i = tid; i < OT_R * K / 4; i += 512) {
-            const int r = i / (K / 4), ch = i % (K / 4);
-            const int mm = blockIdx.x * (OT_R / K) + r / K;
-            float4 v = make_float4(0, 0, 0, 0);
-            if (mm < p.count) {
-                const int lo = unit_cta(p, int64_t(mm) * p.units), hi = unit_cta(p, int64_t(mm + 1) * p.units - 1);
+        for (int b = 0; b < OT_R / K; ++b) {
+            const int mm = blockIdx.x * (OT_R / K) + b;
+            const bool in = mm < p.count;
+            const int lo = in ? unit_cta(p, int64_t(mm) * p.units) : 0;
+            const int hi = in ? unit_cta(p, int64_t(mm + 1) * p.units - 1) : -1;
+            for (int i = tid; i < K * K / 4; i += 512) {
+                const int r = i / (K / 4), ch = i % (K / 4);
+                float4 v = make_float4(0, 0, 0, 0);
 #pragma unroll 4
                 for (int c = lo; c <= hi; ++c) {
-                    const float4 x = reinterpret_cast<const float4 *>(p.gram + (int64_t(c + mm) * K + r % K) * K)[ch];
+                    const float4 x = reinterpret_cast<const float4 *>(p.gram + int64_t(c + mm) * K * K)[i];
                     v.x += x.x;
                     v.y += x.y;
                     v.z += x.z;
                     v.w += x.w;
                 }
+                reinterpret_cast<float4 *>(sum)[(b * K + r) * (K / 4) + (ch ^ (r & 7))] = v;
             }
-            reinterpret_cast<float4 *>(sum)[r * (K / 4) + (ch ^ (r & 7))] = v;
         }
         asm volatile("bar.sync 1, 512;\n" ::: "memory");
         float rv[C];                                  // this thread's part of R
