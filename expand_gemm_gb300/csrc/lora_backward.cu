@@ -74,7 +74,6 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
     pdl_wait();
-    pdl_launch_dependents();
     int tiles;
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(part + WK * BW_TOK * RP), tiles);
     const int clusters = int(gridDim.x / csize), cluster = int(blockIdx.x / csize);
@@ -205,7 +204,6 @@ __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int m0 = warp % 4 * 16, n0 = warp / 4 * 64;          // 16 tokens x 64 columns a warp
     pdl_wait();
-    pdl_launch_dependents();
     int tiles;
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + grad_x_smem<RP>()), tiles);
     const int hb = (p.H + BW_COLS - 1) / BW_COLS;
@@ -356,7 +354,6 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wm = warp % WM, wn = warp / WM;
     pdl_wait();
-    pdl_launch_dependents();
     int tiles;
     int *mem = reinterpret_cast<int *>(smem + grad_w_smem<RP>());
     const SegTab tab = load_tab(p, mem, tiles);

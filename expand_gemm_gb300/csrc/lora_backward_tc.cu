@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
     const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
     const uint32_t ones = ring.ring + q.ring - TC_ONES;
     pdl_wait();
-    pdl_launch_dependents();
     int tiles;
     int *mem = reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES);
     const SegTab tab = load_tab(p, mem, tiles);
@@ -407,7 +406,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
     }
     __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
     SegTab t64, t128;
     const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
     const int hb = (p.H + TC_X_COLS - 1) / TC_X_COLS;
@@ -559,7 +557,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
     pdl_wait();
-    pdl_launch_dependents();
     SegTab t64, t128;
     const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
     const int64_t items = int64_t(tiles) * p.S;

@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
     __shared__ int s_part[2][WARPS];
     __shared__ float s_dot[WARPS];
     pdl_wait();
-    pdl_launch_dependents();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x * LS_PACK_TOKENS;
     const bool last = blockIdx.x == gridDim.x - 1;
@@ -280,7 +279,6 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
 logits_kernel(const __grid_constant__ LossGemm g)
 {
     pdl_wait();
-    pdl_launch_dependents();
     const LossArgs &l = g.l;
     const int mt = (*l.count + PG_TILE - 1) / PG_TILE;
     const int nt = (g.cols + PG_TILE - 1) / PG_TILE;
@@ -406,7 +404,6 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
 hidden_grad_kernel(const __grid_constant__ LossGemm g)
 {
     pdl_wait();
-    pdl_launch_dependents();
     const LossArgs &l = g.l;
     const int mt = (*l.count + PG_TILE - 1) / PG_TILE;
     const int nt = (l.H + PG_TILE - 1) / PG_TILE;
@@ -484,7 +481,6 @@ __global__ void __launch_bounds__(PG_THREADS, 1)
 head_grad_kernel(const __grid_constant__ LossGemm g)
 {
     pdl_wait();
-    pdl_launch_dependents();
     const LossArgs &l = g.l;
     const int mt = (g.cols + PG_TILE - 1) / PG_TILE;
     const int nt = (l.H + PG_TILE - 1) / PG_TILE;
@@ -539,7 +535,6 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const 
     __shared__ int s_off[LS_JOIN_ROWS];
     __shared__ float s_new[LS_JOIN_ROWS];
     pdl_wait();
-    pdl_launch_dependents();
     const LossArgs &l = a.l;
     const int k = threadIdx.x % LS_JOIN_ROWS, part = threadIdx.x / LS_JOIN_ROWS;
     __shared__ float s_sum[LS_JOIN_TEAM][LS_JOIN_ROWS], s_own[LS_JOIN_TEAM][LS_JOIN_ROWS];
@@ -645,7 +640,6 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const 
 __global__ void __launch_bounds__(256) finish_kernel(const LossArgs l)
 {
     pdl_wait();
-    pdl_launch_dependents();
     const int n = *l.count;
     for (int row = blockIdx.x; row < n; row += gridDim.x) {
         const float inv = l.inv[row], share = l.share[row];

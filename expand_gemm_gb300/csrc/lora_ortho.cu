@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
     float *sum = reinterpret_cast<float *>(terms + (F32 ? 2 * Ring::TERM : 0));
     const int tid = threadIdx.x, warp = tid >> 5;
     pdl_wait();
-    pdl_launch_dependents();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
     const int64_t size = int64_t(p.rows) * p.cols;
     TileWalk in(first, end, p.units, size), run(first, end, p.units, size);
@@ -279,7 +278,6 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
     const bool mine = ty < 16;
     tx += ty;
     pdl_wait();
-    pdl_launch_dependents();
     const int lo = unit_cta(p, int64_t(m) * p.units), hi = unit_cta(p, int64_t(m + 1) * p.units - 1);
     for (int i = tid; i < RP * RP; i += OR_THREADS) {
         R[i] = gram_sum<RP>(p, m, lo, hi, i);
@@ -378,7 +376,6 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
     const int tid = threadIdx.x, warp = tid >> 5;
     const int m0 = TALL ? warp * 16 : 0, n0 = TALL ? 0 : warp * 16;
     pdl_wait();
-    pdl_launch_dependents();
     const int tiles = (p.n + OR_LONG - 1) / OR_LONG;
     const int64_t total = int64_t(p.count) * tiles;
     const int64_t first = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;

@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(TC_THREADS, 2) gram_tc_kernel(const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const TcRing ring = tc_setup<256>(smem, OT_GRAM_RING, STAGE, STAGES, F32 ? 4 : 1);
     pdl_wait();
-    pdl_launch_dependents();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
 
     if (warp == 0 && !F32) {
@@ -304,7 +303,6 @@ __global__ void __launch_bounds__(OT_ITER_THREADS, 1) iterate_tc_kernel(const Or
     const uint32_t tmem = *s_tmem, lanes = uint32_t(quarter * 32) << 16;
     const uint32_t d0 = tmem, d1 = tmem + 128, tp = tmem + 256;
     pdl_wait();
-    pdl_launch_dependents();
 
     if (warp == 16) {
         if (lane == 0) {
@@ -516,7 +514,6 @@ apply_tc_kernel(const __grid_constant__ OrthoTcArgs q)
     }
     __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
     const int tiles = (p.n + OT_R - 1) / OT_R;
     const int64_t total = int64_t(p.count) * tiles;
     const int64_t first = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
