@@ -403,11 +403,19 @@ def lora_linear_noalloc(token_lora_mapping: torch.Tensor, x: torch.Tensor, lora_
 
 # ------------------------------------------------------------ training the adapters
 #
-# These calls are short enough for the checks to show in a small batch, so
-# each makes one quick pass over its tensors and words the error only when
-# something is wrong.
+# In a small batch the checks cost more than the kernels (64 tokens: 23 us
+# of Python for 8 us of launches), so each call tests its tensors in one
+# expression and looks for the culprit, to word the error, only when that
+# fails.
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_PTRS = [ctypes.c_void_p * n for n in range(LORA_MAX_SLICES + 1)]
+_SIZES = [ctypes.c_int32 * n for n in range(LORA_MAX_SLICES + 1)]
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream      # what current_stream() wraps, without the object
+except AttributeError:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def _all(index: int, *named) -> None:
@@ -418,6 +426,10 @@ def _all(index: int, *named) -> None:
         if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index:
             _need(t, name, dtype)
             raise ValueError("%s is on cuda:%d, expected cuda:%d" % (name, t.get_device(), index))
+
+
+def _is(t: Optional[torch.Tensor], dtype, index: int) -> bool:
+    return t is None or (t.dtype is dtype and t.get_device() == index)
 
 
 def _gpu(t: torch.Tensor, name: str) -> int:
@@ -445,7 +457,7 @@ def _call_with(fn: str, workspace: Optional[torch.Tensor], device, size_args, *a
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     try:
-        _call(fn, device, *args, workspace.data_ptr(), workspace.numel(), _stream_handle(device))
+        _call(fn, device, *args, workspace.data_ptr(), workspace.numel(), _raw_stream(device.index))
     except LoraError as e:
         if e.status == _lib.LORA_ERR_WORKSPACE:
             raise ValueError("workspace must have at least %d bytes"
@@ -496,11 +508,22 @@ def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
     and weight_grad (bf16, like weight) are overwritten when given;
     error_word (int32 [1]) receives the count of targets >= vocab.  A
     workspace (uint8) is allocated when none is given."""
-    _all(_gpu(hidden, "hidden"), (hidden, _BF16, "hidden"), (weight, _BF16, "weight"),
-         (targets, _I32, "targets"), (loss, _F32, "loss"), (token_weight, _F32, "token_weight"),
-         (logsumexp, _F32, "logsumexp"), (hidden_grad, _BF16, "hidden_grad"),
-         (weight_grad, _BF16, "weight_grad"), (error_word, _I32, "error_word"),
-         (workspace, _U8, "workspace"))
+    try:
+        i = hidden.get_device()
+        ok = (i >= 0 and hidden.dtype is _BF16 and weight.dtype is _BF16 and targets.dtype is _I32
+              and loss.dtype is _F32 and weight.get_device() == i and targets.get_device() == i
+              and loss.get_device() == i and _is(token_weight, _F32, i) and _is(logsumexp, _F32, i)
+              and _is(hidden_grad, _BF16, i) and _is(weight_grad, _BF16, i)
+              and _is(error_word, _I32, i) and _is(workspace, _U8, i))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _all(_gpu(hidden, "hidden"), (hidden, _BF16, "hidden"), (weight, _BF16, "weight"),
+             (targets, _I32, "targets"), (loss, _F32, "loss"), (token_weight, _F32, "token_weight"),
+             (logsumexp, _F32, "logsumexp"), (hidden_grad, _BF16, "hidden_grad"),
+             (weight_grad, _BF16, "weight_grad"), (error_word, _I32, "error_word"),
+             (workspace, _U8, "workspace"))
+        raise TypeError("weight, targets and loss must be tensors")
     T, H, ld = _rows(hidden, "hidden")
     if weight.dim() != 2 or weight.shape[1] != H or not weight.is_contiguous():
         raise ValueError("weight must be a contiguous [vocab, %d] tensor" % H)
@@ -530,18 +553,23 @@ def lora_linear_backward_workspace(num_tokens: int, hidden: int, output_slices, 
                             len(output_slices), rank, max_loras)
 
 
-def _stacks(ws, name: str, index: int) -> Sequence[torch.Tensor]:
-    """One bf16 [max_loras, rows, cols] stack per slice on GPU `index` (a
-    singleton layer dimension, [L, 1, rows, cols], is taken out)."""
+def _stacks(ws, name: str, index: int):
+    """The slices' bf16 [max_loras, rows, cols] stacks on GPU `index` (a
+    singleton layer dimension, [L, 1, rows, cols], is taken out), their
+    shapes, and the array of their pointers."""
     if isinstance(ws, torch.Tensor):
         ws = (ws,)
-    for w in ws:
-        if (not isinstance(w, torch.Tensor) or w.dtype is not _BF16 or w.get_device() != index
-                or w.dim() != 3 or not w.is_contiguous()):
-            ws = _weights(ws, name)
-            _all(index, *((w, _BF16, "%s[%d]" % (name, i)) for i, w in enumerate(ws)))
-            break
-    return ws
+    try:
+        ok = all([w.dtype is _BF16 and w.get_device() == index and w.dim() == 3 and w.is_contiguous()
+                  for w in ws])
+    except AttributeError:
+        ok = False
+    if not ok:
+        ws = _weights(ws, name)
+        _all(index, *((w, _BF16, "%s[%d]" % (name, i)) for i, w in enumerate(ws)))
+    if not 1 <= len(ws) <= LORA_MAX_SLICES:
+        raise ValueError("%s must hold 1 to %d tensors" % (name, LORA_MAX_SLICES))
+    return [w.shape for w in ws], _PTRS[len(ws)](*[w.data_ptr() for w in ws])
 
 
 def _grads(grads, name: str, like, index: int):
@@ -562,7 +590,7 @@ def _grads(grads, name: str, like, index: int):
         if (s != shape and (g.numel() != math.prod(shape) or s[0] != shape[0] or s[-1] != shape[-1])) \
                 or not g.is_contiguous():
             raise ValueError("%s[%d] must be a contiguous %s tensor" % (name, i, list(shape)))
-    return _ptr_array(grads)
+    return _PTRS[len(grads)](*[None if g is None else g.data_ptr() for g in grads])
 
 
 def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor, lora_a_stacked,
@@ -579,21 +607,30 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     d_lora_bias: one tensor (or None) per slice, shaped as the weights and
     biases, overwritten; adapters without tokens get zeros."""
     index = meta.no_lora_flag.get_device()
-    _gpu(dy, "dy")
-    _all(index, (dy, _BF16, "dy"), (x, _BF16, "x"), (buffer, _F32, "buffer"), (dx, _BF16, "dx"),
-         (workspace, _U8, "workspace"))
-    A = _stacks(lora_a_stacked, "lora_a_stacked", index)
-    B = _stacks(lora_b_stacked, "lora_b_stacked", index)
-    S = len(A)
-    if S != len(B) or S == 0:
-        raise ValueError("lora_a_stacked and lora_b_stacked differ in length or are empty")
+    try:
+        ok = (dy.dtype is _BF16 and x.dtype is _BF16 and buffer.dtype is _F32 and dy.get_device() == index
+              and x.get_device() == index and buffer.get_device() == index and _is(dx, _BF16, index)
+              and _is(workspace, _U8, index))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _gpu(dy, "dy")
+        _all(index, (dy, _BF16, "dy"), (x, _BF16, "x"), (buffer, _F32, "buffer"), (dx, _BF16, "dx"),
+             (workspace, _U8, "workspace"))
+        raise TypeError("x and buffer must be tensors")
+    a_shapes, a_ptrs = _stacks(lora_a_stacked, "lora_a_stacked", index)
+    b_shapes, b_ptrs = _stacks(lora_b_stacked, "lora_b_stacked", index)
+    S = len(a_shapes)
+    if S != len(b_shapes):
+        raise ValueError("lora_a_stacked and lora_b_stacked differ in length")
     T, H, x_ld = _rows(x, "x")
-    a_shapes, b_shapes = [w.shape for w in A], [w.shape for w in B]
     L, r, _ = a_shapes[0]
-    if any(s != (L, r, H) for s in a_shapes):
-        raise ValueError("lora_a_stacked shapes must all be [%d, %d, %d]" % (L, r, H))
-    if any(s[0] != L or s[2] != r for s in b_shapes):
-        raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (L, r))
+    for s in a_shapes:
+        if s != (L, r, H):
+            raise ValueError("lora_a_stacked shapes must all be [%d, %d, %d]" % (L, r, H))
+    for s in b_shapes:
+        if s[0] != L or s[2] != r:
+            raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (L, r))
     if L != meta.max_loras:
         raise ValueError("the weights hold %d LoRAs, the metadata %d" % (L, meta.max_loras))
     sizes = [s[1] for s in b_shapes]
@@ -608,12 +645,13 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
         if rows != T or cols != H:
             raise ValueError("dx must be [%d, %d]" % (T, H))
         dx_ptr = dx.data_ptr()
-    c_sizes = (ctypes.c_int32 * S)(*sizes)
+    c_sizes = _SIZES[S](*sizes)
     _call_with("lora_linear_backward", workspace, x.device, (T, H, c_sizes, S, r, L),
-               dy.data_ptr(), dy_ld, T, x.data_ptr(), H, x_ld, buffer.data_ptr(), _ptr_array(A),
-               _ptr_array(B), c_sizes, S, r, float(scale), dx_ptr, dx_ld, 1 if add_inputs else 0,
+               dy.data_ptr(), dy_ld, T, x.data_ptr(), H, x_ld, buffer.data_ptr(), a_ptrs,
+               b_ptrs, c_sizes, S, r, float(scale), dx_ptr, dx_ld, 1 if add_inputs else 0,
                _grads(d_lora_a, "d_lora_a", a_shapes, index),
                _grads(d_lora_b, "d_lora_b", b_shapes, index),
+               None if d_lora_bias is None else
                _grads(d_lora_bias, "d_lora_bias", [(L, n) for n in sizes], index),
                ctypes.byref(meta.c))
 
@@ -638,7 +676,9 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
     f32 = update.dtype is _F32
     if not f32 and update.dtype is not _BF16:
         raise TypeError("update must be bfloat16 or float32, got %s" % update.dtype)
-    _all(index, (out, _BF16, "out"), (error_word, _I32, "error_word"), (workspace, _U8, "workspace"))
+    if not (isinstance(out, torch.Tensor) and _is(out, _BF16, index) and _is(error_word, _I32, index)
+            and _is(workspace, _U8, index)):
+        _all(index, (out, _BF16, "out"), (error_word, _I32, "error_word"), (workspace, _U8, "workspace"))
     if out is None or out.shape != update.shape or not out.is_contiguous():
         raise ValueError("out must be contiguous like update")
     if update.dim() < 2 or not update.is_contiguous():
