@@ -28,8 +28,9 @@
 // Tokens without a target (outside [0, V)) are left out from the start:
 // pack_kernel copies the others' rows next to each other, so a prompt's
 // masked tokens cost nothing, and what their rows hold is never read.
-#include <math.h>
-
+//
+// One or two tokens without a head gradient take lora_loss_row.cu.
+#include "lora_loss.cuh"
 #include "lora_pair_gemm.cuh"
 
 namespace lora {
@@ -40,10 +41,8 @@ constexpr int LS_WINDOW = 60;                 // exponents a tile may be off the
 constexpr int LS_MAX_SPLIT = 8;
 constexpr int LS_PACK_TOKENS = 4;             // tokens of one block of pack_kernel
 constexpr int LS_PACK_THREADS = 256;
-constexpr int LS_JOIN_TEAM = 8;               // threads a row in join_kernel
-constexpr int LS_JOIN_ROWS = 16;              // rows of one block
-constexpr float LS_LOG2E = 1.4426950408889634f;
-constexpr float LS_LN2 = 0.6931471805599453f;
+constexpr int LS_PAD_BLOCKS = 32;
+constexpr int LS_JOIN_ROWS = 8;               // rows of a block of join_kernel, a warp each
 
 // What a call's workspace holds; every part begins on a 256-byte boundary.
 struct LossLayout {
@@ -52,7 +51,13 @@ struct LossLayout {
     int pieces, split;
     int64_t count, row, target, weight, ref, sum, logit, factor, inv, share, lse, stat, h, p, acc;
     int64_t bytes;
+    bool rows;             // one or two tokens: logit, stat and acc of lora_loss_row.cu alone
 };
+
+// Row stride of the packed hidden states: whole 128-byte lines, whatever the
+// caller's stride (a TMA box of rows that straddle lines loads at less than
+// half the rate).
+__host__ __device__ constexpr int64_t packed_ld(int64_t H) { return (H + 63) / 64 * 64; }
 
 static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad, bool weight_grad,
                               int pairs)
@@ -79,6 +84,15 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
         at += up(bytes, 256);
         return here;
     };
+    l.rows = !weight_grad && loss_row_fits(int32_t(T), int32_t(H));
+    if (l.rows) {
+        l.count = l.row = l.target = l.weight = l.ref = l.sum = l.factor = l.inv = l.share = l.lse = l.h = l.p = 0;
+        l.logit = take(T * 4);
+        l.stat = take(loss_row_slots() * T * 8);
+        l.acc = take(hidden_grad ? loss_row_slots() * T * H * 4 : 0);
+        l.bytes = at;
+        return l;
+    }
     l.count = take(4);
     l.row = take(l.tokens * 4);
     l.target = take(l.tokens * 4);
@@ -90,8 +104,8 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
     l.inv = take(l.tokens * 4);
     l.share = take(l.tokens * 4);
     l.lse = take(l.tokens * 4);
-    l.stat = take(l.tokens * (l.piece / PG_TILE) * 8);
-    l.h = take(l.tokens * H * 2);
+    l.stat = take(l.tokens * (l.piece / PG_HALF) * 8);
+    l.h = take(l.tokens * packed_ld(H) * 2);
     l.p = take(hidden_grad || weight_grad ? l.tokens * l.piece * 2 : 0);
     l.acc = take(hidden_grad && (l.split > 1 || l.pieces > 1) ? l.split * l.tokens * H * 4 : 0);
     l.bytes = at;
@@ -114,7 +128,7 @@ struct LossArgs {
     int32_t *count;                    // tokens with a target
     int32_t *row, *target, *ref;
     float *wt, *sum, *logit, *factor, *inv, *share, *lse;
-    float2 *stat;                      // [piece tiles][tokens]: reference, sum
+    float2 *stat;                      // [128 columns each][tokens]: reference, sum
     uint16_t *h, *p;
     float *acc;
     int64_t tokens, piece;
@@ -125,8 +139,9 @@ struct LossArgs {
 
 // Block b copies tokens [4 b, 4 b + 4) that have a target to their place
 // among those that have one (the count of targets before them, which every
-// block takes itself), and clears the outputs of the others.  The last block
-// also fills the tile behind the last row with zeros.  The target's logit is
+// block takes itself), and clears the outputs of the others.  Behind them,
+// for a head gradient, LS_PAD_BLOCKS blocks fill the last tile with zeros
+// (other products never use what rows past the last give).  The target's logit is
 // summed here, in ordinary fp32: the loss is a difference with it, and the
 // tensor cores' sums truncate (over 4096 products they leave the loss 4
 // times further off).  Two warps a token with their loads unrolled: at 256
@@ -139,10 +154,11 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x * LS_PACK_TOKENS;
-    const bool last = blockIdx.x == gridDim.x - 1;
+    const int blocks = p.T > 0 ? (p.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
+    const bool last = int(blockIdx.x) == blocks - 1, pad = int(blockIdx.x) >= blocks;
     int before = 0, bad = 0;
 #pragma unroll 8
-    for (int t = tid; t < c0; t += LS_PACK_THREADS) {
+    for (int t = tid; t < min(c0, p.T); t += LS_PACK_THREADS) {
         const int y = p.targets[t];
         before += y >= 0 && y < p.V;
         bad += y >= p.V;
@@ -160,6 +176,15 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
     for (int i = 0; i < WARPS; ++i) {
         before += s_part[0][i];
         bad += s_part[1][i];
+    }
+    if (pad) {
+        const int n_up = (before + PG_TILE - 1) / PG_TILE * PG_TILE;
+        uint4 *rows = reinterpret_cast<uint4 *>(p.h + int64_t(before) * packed_ld(p.H));
+        const int64_t all = int64_t(n_up - before) * (packed_ld(p.H) / 8);
+        for (int64_t i = int64_t(blockIdx.x - blocks) * LS_PACK_THREADS + tid; i < all;
+             i += LS_PAD_BLOCKS * LS_PACK_THREADS)
+            rows[i] = make_uint4(0, 0, 0, 0);
+        return;
     }
     // lane i < LS_PACK_TOKENS of every warp: the block's token i
     const int y = lane < LS_PACK_TOKENS && c0 + lane < p.T ? p.targets[c0 + lane] : -1;
@@ -180,9 +205,6 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
             p.sum[r] = 0.0f;
             p.logit[r] = 0.0f;
         }
-        uint4 *pad = reinterpret_cast<uint4 *>(p.h + int64_t(n) * p.H);
-        for (int64_t i = tid; i < int64_t(n_up - n) * (p.H / 8); i += LS_PACK_THREADS)
-            pad[i] = make_uint4(0, 0, 0, 0);
     }
     const int mine = tid / TEAM, part = tid % TEAM, t = c0 + mine;     // this thread's token
     const int target = __shfl_sync(0xffffffffu, y, mine);
@@ -191,7 +213,7 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
     float dot = 0.0f;
     if (valid) {
         const uint16_t *src = p.hidden + int64_t(t) * p.hidden_ld;
-        uint16_t *dst = p.h + int64_t(to) * p.H;
+        uint16_t *dst = p.h + int64_t(to) * packed_ld(p.H);
         const uint16_t *w = p.weight + int64_t(target) * p.H;
         auto one = [&](int c, const uint4 &v, const uint4 &u) {
             *reinterpret_cast<uint4 *>(dst + c) = v;
@@ -244,7 +266,7 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
             p.wt[to] = p.token_weight != nullptr ? p.token_weight[t] : 1.0f;
             p.ref[to] = 0;
             p.sum[to] = 0.0f;
-            p.logit[to] = d * LS_LOG2E;
+            p.logit[to] = d * LOSS_LOG2E;
         } else if (t < p.T) {
             p.loss[t] = 0.0f;
             if (p.logsumexp != nullptr) p.logsumexp[t] = 0.0f;
@@ -286,10 +308,11 @@ logits_kernel(const __grid_constant__ LossGemm g)
     auto item = [&](int i) {
         return PairItem{(i % mt) * PG_TILE, g.col0 + (i / mt) * PG_TILE, 0, kb};
     };
-    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int rank, bool) {
+    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int c0, int rank, bool) {
         const int row = it.row_a + rank * PG_HALF + r;
         const int tile = i / mt;
-        const int lim = min(PG_TILE, g.col0 + g.cols - it.row_b);       // columns of this tile
+        const int c_end = c0 + PG_HALF;
+        const int lim = min(c_end, g.col0 + g.cols - it.row_b);         // columns end here
         const int y = l.target[row] - it.row_b;                         // column of the target
         uint16_t *dst = l.p + int64_t(row) * l.piece + tile * PG_TILE;
         uint32_t v[32];
@@ -300,7 +323,7 @@ logits_kernel(const __grid_constant__ LossGemm g)
             q = -l.share[row];
         } else {
             float top = -INFINITY;
-            for (int c = 0; c < lim; c += 32) {
+            for (int c = c0; c < lim; c += 32) {
                 tmem_ld32_nowait(tmem + c, v);
                 tmem_wait_ld();
                 if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
@@ -318,12 +341,12 @@ logits_kernel(const __grid_constant__ LossGemm g)
                 }
             }
             const int have = l.ref[row];
-            top *= LS_LOG2E;
+            top *= LOSS_LOG2E;
             ref = float(have);
             if (top > -INFINITY && !(fabsf(top - ref) <= float(LS_WINDOW)))
                 ref = ceilf(fminf(fmaxf(top, -1e9f), 1e9f));
         }
-        for (int c = 0; c < PG_TILE; c += 32) {
+        for (int c = c0; c < c_end; c += 32) {
             if (GRAD ? c >= lim : (c >= lim && !g.store)) break;
             uint32_t pk[16];
             if (c < lim) {
@@ -332,7 +355,7 @@ logits_kernel(const __grid_constant__ LossGemm g)
                 float e[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), LS_LOG2E, -ref));
+                    e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), LOSS_LOG2E, -ref));
                 if (c + 32 > lim) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -371,7 +394,7 @@ logits_kernel(const __grid_constant__ LossGemm g)
                 st_global_v8(dst + c + 16, hi);
             }
         }
-        if constexpr (!GRAD) l.stat[int64_t(tile) * l.tokens + row] = make_float2(ref, sum);
+        if constexpr (!GRAD) l.stat[int64_t(tile * 2 + c0 / PG_HALF) * l.tokens + row] = make_float2(ref, sum);
     };
     pair_gemm<false, false>(&g.a, &g.b, mt * nt, l.error_word, item, epilogue);
 }
@@ -414,12 +437,12 @@ hidden_grad_kernel(const __grid_constant__ LossGemm g)
         return PairItem{(j % mt) * PG_TILE, (j / mt) * PG_TILE, min(kb, s * per),
                         min(kb, (s + 1) * per)};
     };
-    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int rank, bool empty) {
+    auto epilogue = [&](int i, const PairItem &it, uint32_t tmem, int r, int c0, int rank, bool empty) {
         const int row = it.row_a + rank * PG_HALF + r;
         const int s = i / (mt * nt);
         float *dst = l.acc + (int64_t(s) * l.tokens + row) * l.H + it.row_b;
         const float f = g.first ? 0.0f : l.factor[row];
-        const int lim = min(PG_TILE, l.H - it.row_b);
+        const int lim = min(c0 + PG_HALF, l.H - it.row_b);
         float inv = 0.0f, share = 0.0f;
         const uint16_t *w = l.weight;
         uint16_t *out = nullptr;
@@ -432,7 +455,7 @@ hidden_grad_kernel(const __grid_constant__ LossGemm g)
                 out = l.dh + int64_t(t) * l.dh_ld + it.row_b;
             }
         }
-        for (int c = 0; c < lim; c += 32) {
+        for (int c = c0; c < lim; c += 32) {
             const int many = min(32, lim - c);                 // a multiple of 8
             uint32_t v[32];
             if (empty) {
@@ -488,11 +511,11 @@ head_grad_kernel(const __grid_constant__ LossGemm g)
     auto item = [&](int i) {
         return PairItem{(i / nt) * PG_TILE, (i % nt) * PG_TILE, 0, kb};
     };
-    auto epilogue = [&](int, const PairItem &it, uint32_t tmem, int r, int rank, bool empty) {
+    auto epilogue = [&](int, const PairItem &it, uint32_t tmem, int r, int c0, int rank, bool empty) {
         const int v0 = it.row_a + rank * PG_HALF + r;
-        const int lim = min(PG_TILE, l.H - it.row_b);
+        const int lim = min(c0 + PG_HALF, l.H - it.row_b);
         uint16_t *dst = g.dw + int64_t(g.col0 + v0) * l.H + it.row_b;
-        for (int c = 0; c < lim; c += 32) {
+        for (int c = c0; c < lim; c += 32) {
             uint32_t v[32];
             if (empty) {
 #pragma unroll
@@ -521,67 +544,59 @@ head_grad_kernel(const __grid_constant__ LossGemm g)
 
 struct JoinArgs {
     LossArgs l;
-    int32_t tiles;       // of the piece
+    int32_t tiles;       // of the piece, 128 columns each
     int32_t last;        // no piece follows: also the loss and the row factors
     int32_t store;
 };
 
-// After a piece's logits: eight threads a row add the tiles' sums to the
-// row's (a fixed order) and, where a tile fell outside the window, bring the
-// row to a common reference (the block then rescales the row's scratch).
-__global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const JoinArgs a)
+// After a piece's logits: a warp a row adds the tiles' sums to the row's (a
+// fixed order) and, where a tile fell outside the window, brings the row to
+// a common reference (the block then rescales the row's scratch).
+__global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs a)
 {
-    constexpr int THREADS = LS_JOIN_ROWS * LS_JOIN_TEAM;
+    constexpr int THREADS = LS_JOIN_ROWS * 32;
     __shared__ int s_off[LS_JOIN_ROWS];
     __shared__ float s_new[LS_JOIN_ROWS];
     pdl_wait();
     const LossArgs &l = a.l;
-    const int k = threadIdx.x % LS_JOIN_ROWS, part = threadIdx.x / LS_JOIN_ROWS;
-    __shared__ float s_sum[LS_JOIN_TEAM][LS_JOIN_ROWS], s_own[LS_JOIN_TEAM][LS_JOIN_ROWS];
-    __shared__ int s_used[LS_JOIN_TEAM][LS_JOIN_ROWS];
+    const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row = blockIdx.x * LS_JOIN_ROWS + k;
-    const int n = *l.count;
-    const bool in = row < n;
-    const float2 *stat = l.stat + row;
-    const float have = in ? float(l.ref[row]) : 0.0f;
-    float sum = 0.0f, own = -INFINITY;
-    int used = 0;                           // some tile took the row's reference
+    const bool in = row < *l.count;
+    if (lane == 0) s_off[k] = 0;
     if (in) {
+        const float2 *stat = l.stat + row;
+        const float have = float(l.ref[row]), old = l.sum[row];
+        float sum = 0.0f, own = -INFINITY;
+        bool used = old > 0.0f;                     // something took the row's reference
 #pragma unroll 4
-        for (int j = part; j < a.tiles; j += LS_JOIN_TEAM) {
+        for (int j = lane; j < a.tiles; j += 32) {
             const float2 s = stat[int64_t(j) * l.tokens];
             if (s.x == have) {
                 sum += s.y;
-                used |= s.y > 0.0f;
+                used = used || s.y > 0.0f;
             } else {
                 own = fmaxf(own, s.x);
             }
         }
-    }
-    s_sum[part][k] = sum;
-    s_own[part][k] = own;
-    s_used[part][k] = used;
-    __syncthreads();
-    if (part == 0) {
-        s_off[k] = 0;
-        const float old = in ? l.sum[row] : 0.0f;
-        float total = old;
-        used = old > 0.0f;
-        for (int q = 0; q < LS_JOIN_TEAM; ++q) {
-            total += s_sum[q][k];
-            own = fmaxf(own, s_own[q][k]);
-            used |= s_used[q][k];
+        for (int o = 16; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            own = fmaxf(own, __shfl_xor_sync(0xffffffffu, own, o));
         }
-        if (in) {
-            float ref = have, f = 1.0f;
-            if (own > -INFINITY) {                  // a tile has a reference of its own
-                ref = used ? fmaxf(have, own) : own;
-                f = used ? exp2f(have - ref) : 0.0f;
-                total = used ? total * f : 0.0f;
-                for (int j = 0; j < a.tiles; ++j) {
-                    const float2 s = stat[int64_t(j) * l.tokens];
-                    if (s.x != have) total += s.y * exp2f(s.x - ref);
-                }
+        used = __any_sync(0xffffffffu, used);
+        float ref = have, f = 1.0f, total = old + sum;
+        if (own > -INFINITY) {                      // a tile has a reference of its own
+            ref = used ? fmaxf(have, own) : own;
+            f = used ? exp2f(have - ref) : 0.0f;
+            float more = 0.0f;
+            for (int j = lane; j < a.tiles; j += 32) {
+                const float2 s = stat[int64_t(j) * l.tokens];
+                if (s.x != have) more += s.y * exp2f(s.x - ref);
+            }
+            for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+            total = (used ? total * f : 0.0f) + more;
+        }
+        if (lane == 0) {
+            if (ref != have || own > -INFINITY) {
                 s_off[k] = a.store;
                 s_new[k] = ref;
                 l.ref[row] = int(ref);
@@ -589,36 +604,18 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const 
             l.sum[row] = total;
             l.factor[row] = f;
             if (a.last) {
-                // total: the other columns, in units of 2^ref; d: the target's exponent
-                const float w = l.wt[row], d = l.logit[row] - ref;
-                float lse2, loss, inv, share;
-                if (total == 0.0f) {                // the target is the only column left
-                    lse2 = l.logit[row];
-                    loss = inv = share = 0.0f;
-                } else if (d >= 0.0f) {
-                    const float back = total * exp2f(-d);       // others relative to the target
-                    loss = log1pf(back);
-                    lse2 = l.logit[row] + loss * LS_LOG2E;
-                    share = back / (1.0f + back);
-                    inv = exp2f(-d) / (1.0f + back);
-                } else {
-                    const float all = total + exp2f(d);
-                    const float lg = log2f(all);
-                    loss = (lg - d) * LS_LN2;
-                    lse2 = ref + lg;
-                    share = total / all;
-                    inv = 1.0f / all;
-                }
+                const float w = l.wt[row];
+                const LossRow r = loss_row(total, ref, l.logit[row]);
                 const int t = l.row[row];
-                l.loss[t] = w * loss;
-                if (l.logsumexp != nullptr) l.logsumexp[t] = lse2 * LS_LN2;
-                l.inv[row] = w * inv;
-                l.share[row] = w * share;
-                l.lse[row] = lse2;
+                l.loss[t] = w * r.loss;
+                if (l.logsumexp != nullptr) l.logsumexp[t] = r.lse2 * LOSS_LN2;
+                l.inv[row] = w * r.inv;
+                l.share[row] = w * r.share;
+                l.lse[row] = r.lse2;
             }
-        } else if (a.last && row < l.tokens) {
-            l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
         }
+    } else if (a.last && lane == 0 && row < l.tokens) {
+        l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
     }
     __syncthreads();
     for (int q = 0; q < LS_JOIN_ROWS; ++q) {
@@ -628,8 +625,8 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS *LS_JOIN_TEAM) join_kernel(const 
             const float was = l.stat[int64_t(j) * l.tokens + r].x;
             if (was == s_new[q]) continue;
             const float f = exp2f(was - s_new[q]);
-            uint32_t *at = reinterpret_cast<uint32_t *>(l.p + int64_t(r) * l.piece + j * PG_TILE);
-            for (int i = threadIdx.x; i < PG_TILE / 2; i += THREADS)
+            uint32_t *at = reinterpret_cast<uint32_t *>(l.p + int64_t(r) * l.piece + j * PG_HALF);
+            for (int i = threadIdx.x; i < PG_HALF / 2; i += THREADS)
                 at[i] = pack_bf16x2(bf16_lo(at[i]) * f, bf16_hi(at[i]) * f);
         }
     }
@@ -698,15 +695,16 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
     LossGemm logits, dhid, grad, head;
     logits.l = dhid.l = grad.l = head.l = l;
     const bool store = l.dh != nullptr;
-    if (!operand_map(&logits.a, l.h, lay.tokens, l.H, l.H, false) ||
+    if (!operand_map(&logits.a, l.h, lay.tokens, l.H, packed_ld(l.H), false) ||
         !operand_map(&logits.b, l.weight, l.V, l.H, l.H, false) ||
         ((store || dw != nullptr) &&
          (!operand_map(&dhid.a, l.p, lay.tokens, lay.piece, lay.piece, false) ||
           !operand_map(&head.a, l.p, lay.tokens, lay.piece, lay.piece, true))) ||
-        !operand_map(&head.b, l.h, lay.tokens, l.H, l.H, true))
+        !operand_map(&head.b, l.h, lay.tokens, l.H, packed_ld(l.H), true))
         return LORA_ERR_DEVICE;
     const int blocks = l.T > 0 ? (l.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
-    cudaError_t e = launch_kernel(pack_kernel, dim3(blocks), dim3(LS_PACK_THREADS), 0, st, l);
+    cudaError_t e = launch_kernel(pack_kernel, dim3(unsigned(blocks + (dw != nullptr ? LS_PAD_BLOCKS : 0))),
+                                  dim3(LS_PACK_THREADS), 0, st, l);
     if (e != cudaSuccess) return int(e);
     for (int i = 0; i < lay.pieces; ++i) {
         const int32_t col0 = int32_t(i * lay.piece);
@@ -718,11 +716,11 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
         if (e != cudaSuccess) return int(e);
         JoinArgs j;
         j.l = l;
-        j.tiles = (cols + PG_TILE - 1) / PG_TILE;
+        j.tiles = (cols + PG_HALF - 1) / PG_HALF;
         j.last = i + 1 == lay.pieces;
         j.store = store;
         e = launch_kernel(join_kernel, dim3(unsigned(lay.tokens / LS_JOIN_ROWS)),
-                          dim3(LS_JOIN_ROWS * LS_JOIN_TEAM), 0, st, j);
+                          dim3(LS_JOIN_ROWS * 32), 0, st, j);
         if (e != cudaSuccess) return int(e);
         if (store) {
             dhid.first = i == 0;
@@ -791,6 +789,27 @@ LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, i
     const LossLayout lay = loss_layout(num_tokens, hidden_size, vocab, hidden_grad != nullptr,
                                        weight_grad != nullptr, pairs);
     if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
+    if (lay.rows) {
+        char *at = static_cast<char *>(workspace);
+        LossRowArgs r;
+        r.hidden = hidden;
+        r.weight = weight;
+        r.hidden_ld = hidden_ld;
+        r.dh_ld = hidden_grad_ld;
+        r.targets = targets;
+        r.token_weight = token_weight;
+        r.loss = loss;
+        r.logsumexp = logsumexp;
+        r.dh = hidden_grad;
+        r.T = num_tokens;
+        r.H = hidden_size;
+        r.V = vocab;
+        r.error_word = error_word;
+        r.logit = reinterpret_cast<float *>(at + lay.logit);
+        r.stat = reinterpret_cast<float2 *>(at + lay.stat);
+        r.acc = hidden_grad != nullptr ? reinterpret_cast<float *>(at + lay.acc) : nullptr;
+        return run_loss_row(r, static_cast<cudaStream_t>(stream));
+    }
     LossArgs l;
     l.hidden = hidden;
     l.hidden_ld = hidden_ld;

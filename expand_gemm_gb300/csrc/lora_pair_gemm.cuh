@@ -13,8 +13,9 @@
 // time; with one CTA per tile (128 x 256) it would be 48 KB, and each SM
 // would draw 1.5 times the bytes from L2.
 //
-// Warps: 0 loads (TMA), 1 issues the UMMAs (even CTA only), 2..5 run the
-// epilogue of one accumulator while the next tile fills the other.
+// Warps: 0 loads (TMA), 1 issues the UMMAs (even CTA only), 2..9 run the
+// epilogue of one accumulator (a half of its columns each four) while the
+// next tile fills the other.
 // Both CTAs' loads signal the even CTA's "full" barrier; the UMMAs' commits
 // free the stage in both.
 #pragma once
@@ -29,7 +30,7 @@ constexpr int PG_HALF = 128;          // of them in one CTA
 constexpr int PG_BK = 64;
 constexpr int PG_STAGES = 6;
 constexpr int PG_STAGE_BYTES = 2 * PG_HALF * PG_BK * 2;     // A and B, 32 KB
-constexpr int PG_THREADS = 192;
+constexpr int PG_THREADS = 320;
 constexpr int PG_EPI_WARP0 = 2;
 constexpr int PG_SMEM = PG_STAGES * PG_STAGE_BYTES + 1024 + 256;
 constexpr long long PG_TIMEOUT_CYCLES = 2000000000ll;
@@ -90,8 +91,8 @@ struct PairItem {
 // Runs `total` items on the grid's pairs.  A_T / B_T: the operand is stored
 // with its rows contiguous.  item(i) -> PairItem (every thread computes the
 // same); epilogue(i, item, tmem address of this warp's 32 lanes, row of this
-// thread within the CTA's 128 rows, CTA rank) with kb0 < kb1, or
-// epilogue with `empty` true when the item has no K blocks.
+// thread within the CTA's 128 rows, first of its 128 columns, CTA rank,
+// whether the item has no K blocks).
 template <bool A_T, bool B_T, typename ItemFn, typename EpiFn>
 __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtensorMap *map_b,
                                           int total, int32_t *error_word, ItemFn item_of,
@@ -119,7 +120,7 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_accf + 8 * i, 1);
-            mbar_init(bar_acce + 8 * i, 8);       // four epilogue warps of each CTA
+            mbar_init(bar_acce + 8 * i, 16);      // eight epilogue warps of each CTA
         }
         mbar_init(bar_drain, 1);
         mbar_fence_init();
@@ -252,7 +253,7 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
                 tc_fence_after();
             }
             epilogue(i, it, tmem + uint32_t(acc * PG_TILE) + (uint32_t(q * 32) << 16),
-                     q * 32 + lane, int(rank), empty);
+                     q * 32 + lane, (warp - PG_EPI_WARP0) / 4 * PG_HALF, int(rank), empty);
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();

@@ -95,6 +95,30 @@ def test_sizes(T, H, V):
     check(run(*a), in_64_bits(*a))
 
 
+@pytest.mark.parametrize("T,H,V", [(1, 8, 1), (1, 64, 2), (1, 4096, 1000), (2, 1032, 777), (2, 2056, 3000),
+                                   (1, 8192, 500), (2, 8192, 1200), (1, 8200, 300), (3, 256, 900)])
+@pytest.mark.parametrize("dh", [True, False])
+def test_one_or_two_tokens(T, H, V, dh):
+    a = make(T, H, V, 200 + H + T, std=0.1 if H < 2000 else 0.02, masked=0.0)
+    check(run(*a, head=False, dh=dh), in_64_bits(*a))
+
+
+@pytest.mark.parametrize("std", [3.0, 30.0])
+def test_one_or_two_tokens_wide_logits_and_masks(std):
+    for seed in range(4):
+        hidden, weight, targets, share = make(2, 64, 1500, seed, std=std, masked=0.0, sure=False)
+        check(run(hidden, weight, targets, share, head=False), in_64_bits(hidden, weight, targets, share))
+        targets[seed % 2] = (-1, 1500)[seed // 2]
+        hidden[seed % 2] = math.nan
+        got = run(hidden, weight, targets, share, head=False)
+        assert int(got["err"]) == seed // 2
+        check(got, in_64_bits(torch.nan_to_num(hidden.float()).bfloat16(), weight, targets, share))
+    targets[:] = -100
+    got = run(hidden, weight, targets, share, head=False)
+    for k in ("loss", "lse", "dh"):
+        assert (got[k] == 0).all()
+
+
 @pytest.mark.parametrize("head,dh", [(False, False), (False, True), (True, False)])
 def test_without_some_gradients(head, dh):
     a = make(200, 128, 777, 3)
