@@ -6,8 +6,9 @@
 //   dbias_a = sum_t dy_t              (a = id(t); -1: nothing)
 //
 // Tokens are taken in the metadata's order (sorted by adapter), in tiles of
-// 64 tokens of one adapter.  Three kernels:
-//   grad_u_kernel  g of a tile, and u, rounded to bf16 for the products
+// 64 tokens of one adapter.  The kernels:
+//   grad_u_kernel, join_u_kernel
+//                  g of a tile, and u, rounded to bf16 for the products
 //                  that follow and laid out by tile with the rows behind an
 //                  adapter's last token zero (the products over tokens then
 //                  need no masks on them);
@@ -45,50 +46,57 @@ __device__ __forceinline__ void copy8(uint8_t *dst, const uint16_t *row, int c, 
 
 // ---------------------------------------------------------------- g and u
 
-template <int RP> struct UShape { static constexpr int WM = 4, WN = RP >= 64 ? 2 : 1, WK = RP >= 64 ? 1 : 2; };
+template <int RP> struct UShape { static constexpr int WM = 4, WN = 2; };
 constexpr int BW_U_STAGES = 4;
 
 template <int RP>
-constexpr int grad_u_smem()
+constexpr int grad_u_smem() { return BW_U_STAGES * (BW_TOK * 64 * 2 + 64 * RP * 2); }
+
+// The 64-column steps of all (tile, slice) items, in order, cut into even
+// runs, one a CTA, whatever the number and the widths of the items: CTA c
+// takes steps [step_begin(c), step_begin(c + 1)).
+__device__ __forceinline__ int64_t step_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
+__device__ __forceinline__ int step_cta(int64_t total, int64_t step, int ctas)
 {
-    return BW_U_STAGES * (BW_TOK * 64 * 2 + 64 * RP * 2) + UShape<RP>::WK * BW_TOK * RP * 4;
+    return int(((step + 1) * ctas - 1) / total);
 }
 
-// Item: (tile, slice), worked on by a cluster whose CTAs take a share of the
-// slice's columns each; their partial sums are joined through distributed
-// shared memory in the order of the CTAs.  Bound by the reads of dy: a ring
-// of four 64-column steps by cp.async.
+// Each CTA walks its run of steps; its part of an item's sum goes to slot
+// (CTA + item), a new one whenever the CTA or the item changes.  Bound by
+// the reads of dy: a ring of four steps by cp.async.
 template <int RP>
 __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constant__ BackwardArgs p)
 {
-    constexpr int WM = UShape<RP>::WM, WN = UShape<RP>::WN, WK = UShape<RP>::WK;
+    constexpr int WM = UShape<RP>::WM, WN = UShape<RP>::WN;
     constexpr int NI = RP / WN / 8, CPR = RP / 8;
     constexpr int SD = BW_TOK * 64 * 2, SB = 64 * RP * 2, ST = BW_U_STAGES;
     constexpr int PB = (64 * CPR + BW_THREADS - 1) / BW_THREADS;
     extern __shared__ __align__(1024) uint8_t smem[];
-    float *part = reinterpret_cast<float *>(smem + ST * (SD + SB));
     const uint32_t base = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wm = warp % WM, wn = warp / WM % WN, wk = warp / (WM * WN);
-    uint32_t rank, csize;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+    const int wm = warp % WM, wn = warp / WM;
     pdl_wait();
     int tiles;
-    const SegTab tab = load_tab(p, reinterpret_cast<int *>(part + WK * BW_TOK * RP), tiles);
-    const int clusters = int(gridDim.x / csize), cluster = int(blockIdx.x / csize);
-
-    for (int64_t item = cluster; item < int64_t(tiles) * p.S; item += clusters) {
-        const int tile = int(item / p.S), s = int(item % p.S);
+    const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + ST * (SD + SB)), tiles);
+    const int per_tile = p.step_end[p.S - 1];
+    const int64_t total = int64_t(tiles) * per_tile;
+    const int ctas = int(min(int64_t(gridDim.x), total));      // a step each at least
+    if (int(blockIdx.x) >= ctas) return;
+    int64_t step = step_begin(total, blockIdx.x, ctas);
+    const int64_t end = step_begin(total, blockIdx.x + 1, ctas);
+    int tile = int(step / per_tile), s = 0;
+    int k = int(step % per_tile);                              // of the tile, then of the slice
+    while (k >= p.step_end[s]) ++s;
+    if (s > 0) k -= p.step_end[s - 1];
+    while (step < end) {
         const int seg = find_segment(tab.tile, p.nbins, tile);
         const int id = tab.id[seg];
         const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
         const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
         const int lo = p.off[s], hi = lo + p.n[s];
-        const int c0 = p.dy_vec ? lo & ~7 : lo;            // first column of the first step
-        const int steps = (hi - c0 + 63) / 64;
-        const int per = (steps + int(csize) - 1) / int(csize);
-        const int k_lo = min(steps, int(rank) * per), k_hi = min(steps, k_lo + per);
+        const int c0 = p.dy_vec ? lo & ~7 : lo;                // first column of the first step
+        const int k_lo = k;
+        const int k_hi = int(min(int64_t(p.step_end[s] - (s > 0 ? p.step_end[s - 1] : 0)), k + (end - step)));
         const uint16_t *bw = p.b[s] + int64_t(id) * p.n[s] * p.r;
         const uint16_t *src[2];
 #pragma unroll
@@ -120,62 +128,89 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
             cp_async_commit();
         };
         float acc[NI][4] = {};
-        for (int k = k_lo; k < k_lo + ST - 1; ++k) issue(k);
-        for (int k = k_lo; k < k_hi; ++k) {
+        for (int i = k_lo; i < k_lo + ST - 1; ++i) issue(i);
+        for (int i = k_lo; i < k_hi; ++i) {
             cp_async_wait<ST - 2>();
             __syncthreads();
-            issue(k + ST - 1);
-            const uint32_t sd = base + k % ST * (SD + SB), sb = sd + SD;
+            issue(i + ST - 1);
+            const uint32_t sd = base + i % ST * (SD + SB), sb = sd + SD;
 #pragma unroll
-            for (int kk = wk * (64 / WK); kk < (wk + 1) * (64 / WK); kk += 16) {
+            for (int kk = 0; kk < 64; kk += 16) {
                 uint32_t a[4];
                 frag_a<8, BW_TOK, true>(sd, wm * 16, kk, a);
+                if constexpr (NI == 1) {
+                    uint32_t b[2];
+                    frag_b1<CPR, 64>(sb, kk, wn * 8, b);
+                    mma_bf16_16816(acc[0], a, b[0], b[1]);
+                } else {
 #pragma unroll
-                for (int j = 0; j < NI; j += 2) {
-                    uint32_t b[4];
-                    frag_b<CPR, 64, false>(sb, kk, wn * (RP / WN) + 8 * j, b);
-                    mma_bf16_16816(acc[j], a, b[0], b[1]);
-                    mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
+                    for (int j = 0; j < NI; j += 2) {
+                        uint32_t b[4];
+                        frag_b<CPR, 64, false>(sb, kk, wn * (RP / WN) + 8 * j, b);
+                        mma_bf16_16816(acc[j], a, b[0], b[1]);
+                        mma_bf16_16816(acc[j + 1], a, b[2], b[3]);
+                    }
                 }
             }
         }
         const int gq = lane >> 2, t = lane & 3;
-        float *mine = part + wk * BW_TOK * RP;
+        float *out = p.part + (int64_t(blockIdx.x) + int64_t(tile) * p.S + s) * BW_TOK * RP;
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
-            float *at = mine + (wm * 16 + gq) * RP + wn * (RP / WN) + 8 * j + 2 * t;
+            float *at = out + (wm * 16 + gq) * RP + wn * (RP / WN) + 8 * j + 2 * t;
             *reinterpret_cast<float2 *>(at) = make_float2(acc[j][0], acc[j][1]);
             *reinterpret_cast<float2 *>(at + 8 * RP) = make_float2(acc[j][2], acc[j][3]);
         }
-        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-        // this CTA's share of the tile's rows: sums, rounding, and u
+        __syncthreads();                                       // the ring is free
+        step += k_hi - k_lo;
+        k = 0;
+        if (++s == p.S) {
+            s = 0;
+            ++tile;
+        }
+    }
+}
+
+// The partial sums of a tile, added in the order of the CTAs and rounded: g;
+// and u beside it.
+template <int RP>
+__global__ void __launch_bounds__(BW_THREADS) join_u_kernel(const __grid_constant__ BackwardArgs p)
+{
+    extern __shared__ __align__(16) int join_tab[];
+    pdl_wait();
+    int tiles;
+    const SegTab tab = load_tab(p, join_tab, tiles);
+    const int per_tile = p.step_end[p.S - 1];
+    const int64_t total = int64_t(tiles) * per_tile;
+    const int ctas = int(min(int64_t(p.u_ctas), total));
+    for (int item = blockIdx.x; item < tiles * p.S; item += gridDim.x) {
+        const int tile = item / p.S, s = item % p.S;
+        const int seg = find_segment(tab.tile, p.nbins, tile);
+        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
+        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
+        const int64_t first = int64_t(tile) * per_tile + (s > 0 ? p.step_end[s - 1] : 0);
+        const int c_lo = step_cta(total, first, ctas);
+        const int c_hi = step_cta(total, int64_t(tile) * per_tile + p.step_end[s] - 1, ctas);
         const int64_t out0 = (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
-        const int share = BW_TOK * RP / int(csize) / 4;          // float4s
-        for (int i = tid; i < share; i += BW_THREADS) {
-            const int e = (int(rank) * share + i) * 4, row = e / RP, col = e % RP;
-            float4 f = make_float4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < BW_TOK * RP / 4; i += BW_THREADS) {
+            const int row = i * 4 / RP, col = i * 4 % RP;
+            float4 f = make_float4(0, 0, 0, 0), v = f;
             if (row < nrows && col < p.r) {
                 const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
                 if (tok >= 0)
                     f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
             }
-            float4 v = make_float4(0, 0, 0, 0);
-            for (uint32_t q = 0; q < csize; ++q)
-                for (int w = 0; w < WK; ++w) {
-                    uint32_t ra;
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra)
-                        : "r"(smem_addr(part + w * BW_TOK * RP + e)), "r"(q));
-                    float4 x;
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(ra));
-                    v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-                }
-            *reinterpret_cast<uint2 *>(p.g + out0 + e) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            *reinterpret_cast<uint2 *>(p.u + out0 + e) =
-                make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+#pragma unroll 4
+            for (int c = c_lo; c <= c_hi; ++c) {
+                const float4 x = reinterpret_cast<const float4 *>(p.part + (int64_t(c) + item) * BW_TOK * RP)[i];
+                v.x += x.x;
+                v.y += x.y;
+                v.z += x.z;
+                v.w += x.w;
+            }
+            reinterpret_cast<uint2 *>(p.g + out0)[i] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            reinterpret_cast<uint2 *>(p.u + out0)[i] = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
         }
-        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     }
 }
 
@@ -207,14 +242,14 @@ __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constan
     int tiles;
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + grad_x_smem<RP>()), tiles);
     const int hb = (p.H + BW_COLS - 1) / BW_COLS;
-    const int64_t items = int64_t(tiles) * hb;
+    const int items = tiles * hb;             // T x H fits the memory: below 2^31
 
     // the step that is loaded next
-    int64_t l_item = blockIdx.x;
+    int l_item = blockIdx.x;
     int l_s = 0, l_stage = 0;
     auto issue = [&]() {
         if (l_item < items) {
-            const int tile = int(l_item / hb), h0 = int(l_item % hb) * BW_COLS;
+            const int tile = l_item / hb, h0 = l_item % hb * BW_COLS;
             const int seg = find_segment(tab.tile, p.nbins, tile);
             const uint16_t *gt = p.g + (int64_t(l_s) * p.rows + int64_t(tile) * BW_TOK) * RP;
             const uint16_t *aw = p.a[l_s] + int64_t(tab.id[seg]) * p.r * p.H;
@@ -242,8 +277,8 @@ __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constan
     };
     for (int i = 0; i < ST - 1; ++i) issue();
     int stg = 0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int tile = int(item / hb), h0 = int(item % hb) * BW_COLS;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int tile = item / hb, h0 = item % hb * BW_COLS;
         const int seg = find_segment(tab.tile, p.nbins, tile);
         const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
         const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
@@ -359,7 +394,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     const SegTab tab = load_tab(p, mem, tiles);
     const int *seg_of = load_seg_of(p, tab, tiles, mem);
     const int blocks = p.block_end[2 * p.S - 1];
-    const int64_t items = int64_t(p.L) * blocks;
+    const int items = p.L * blocks;           // the weights fit the memory: below 2^31
 
     struct Item {
         const uint16_t *z, *v;
@@ -367,10 +402,10 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
         int id, s, seg, start, count, steps, c0, lo, n, width;
         bool is_a, vec;
     };
-    auto decode = [&](int64_t i) {
+    auto decode = [&](int i) {
         Item it;
-        it.id = int(i / blocks);
-        const int blk = int(i % blocks);
+        it.id = i / blocks;
+        const int blk = i % blocks;
         int q = 0;                                  // product: dB of slice q, or dA of slice q - S
         while (blk >= p.block_end[q]) ++q;
         it.is_a = q >= p.S;
@@ -392,7 +427,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     };
 
     // the step that is loaded next, with its tokens
-    int64_t l_item = blockIdx.x;
+    int l_item = blockIdx.x;
     Item ld;
     int l_k = 0, l_stage = 0, tok[4];
     auto tokens = [&]() {
@@ -435,7 +470,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     };
     for (int i = 0; i < ST - 1; ++i) issue();
     int stg = 0;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const Item it = decode(item);
         uint16_t *dbias = it.is_a ? nullptr : p.dbias[it.s];
         float acc[MI][NI][4] = {}, ones[MI][4] = {};
@@ -535,6 +570,8 @@ static int padded_rank(int r)
     return rp;
 }
 
+constexpr int BW_RESIDENT = 4;             // CTAs of a kernel on an SM, at most
+
 // Rows of the laid-out g and u of one slice: every adapter that occurs may
 // add a partial tile.
 static int64_t backward_rows(int64_t T, int64_t L)
@@ -564,37 +601,22 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         if (dev < 64) configured[dev] = 1;
     }
     const int sms = device_sm_count();
-    // resident CTAs of a kernel (its shared memory decides, at most six)
+    // resident CTAs of a kernel by its shared memory
     auto resident = [&](int smem) {
         const int n = 227 * 1024 / (smem + 1024);
-        return int64_t(sms) * (n < 1 ? 1 : n > 6 ? 6 : n);
+        return int64_t(sms) * (n < 1 ? 1 : n > BW_RESIDENT ? BW_RESIDENT : n);
     };
     const int64_t tiles = p.rows / BW_TOK;
     // Ranks above 32 run on tcgen05 where the rows allow TMA.
     int tc = RP >= 64 && p.T > 0 ? launch_grad_u_tc(p, RP, st) : -1;
     if (tc > 0) return tc;
     if (p.T > 0 && tc < 0) {
-        // few items: a cluster shares each one's columns
-        int cl = 1;
-        const int64_t items = tiles * p.S;
-        while (cl < BW_MAX_CLUSTER && items * cl < 2 * sms && p.width / p.S / 64 >= 4 * cl) cl *= 2;
-        const int64_t most_u = resident(us) / cl > 0 ? resident(us) / cl : 1;
-        const int64_t clusters = items < most_u ? items : most_u;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(unsigned(clusters * cl));
-        cfg.blockDim = dim3(BW_THREADS);
-        cfg.dynamicSmemBytes = size_t(us);
-        cfg.stream = st;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = unsigned(cl);
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = pdl_enabled() ? 2 : 1;
-        e = cudaLaunchKernelEx(&cfg, grad_u_kernel<RP>, p);
+        BackwardArgs q = p;
+        q.u_ctas = int(resident(us));
+        e = launch_kernel(grad_u_kernel<RP>, dim3(unsigned(q.u_ctas)), dim3(BW_THREADS), us, st, q);
+        if (e != cudaSuccess) return int(e);
+        const int64_t most = tiles * p.S, grid = most < 4 * sms ? most : 4 * sms;
+        e = launch_kernel(join_u_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), tab, st, q);
         if (e != cudaSuccess) return int(e);
     }
     if (p.T > 0 && p.dx != nullptr) {
@@ -629,7 +651,10 @@ LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidd
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
     const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;
-    return 2 * ((one + 255) / 256 * 256) + 256;
+    // g, u, and the slots of partial sums: one an item and one a CTA
+    const int64_t slots = lora::backward_rows(num_tokens, max_loras) / lora::BW_TOK * num_slices +
+                          lora::BW_RESIDENT * lora::device_sm_count();
+    return 2 * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
 }
 
 LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,
@@ -716,6 +741,13 @@ LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t 
     const int64_t one = (p.rows * num_slices * rp * 2 + 255) / 256 * 256;
     p.g = reinterpret_cast<uint16_t *>(workspace);
     p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + one);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * one);
+    p.u_ctas = 0;
+    int steps = 0;
+    for (int s = 0; s < LORA_MAX_SLICES; ++s) {
+        if (s < num_slices) steps += ((p.dy_vec ? p.off[s] & 7 : 0) + p.n[s] + 63) / 64;
+        p.step_end[s] = steps;
+    }
     p.sorted = meta->token_indices_sorted_by_lora_ids;
     p.counts = meta->num_tokens_per_lora;
     p.start_loc = meta->lora_token_start_loc;

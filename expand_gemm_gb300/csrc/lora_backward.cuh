@@ -9,7 +9,6 @@ namespace lora {
 constexpr int BW_THREADS = 256;
 constexpr int BW_TOK = 64;                 // tokens of a tile
 constexpr int BW_COLS = 128;               // columns of a tile of dx, dA, dB
-constexpr int BW_MAX_CLUSTER = 8;
 
 struct BackwardArgs {
     const uint16_t *dy, *x;
@@ -28,6 +27,9 @@ struct BackwardArgs {
     float scale;
     uint16_t *g, *u;                       // [S][rows][RP]
     int64_t rows;
+    float *part;                           // grad_u_kernel's partial sums, [BW_TOK][RP] each
+    int32_t step_end[LORA_MAX_SLICES];     // its 64-column steps of one tile, by slice
+    int32_t u_ctas;
     const int32_t *sorted, *counts, *start_loc, *active, *no_lora;
     int32_t *error_word;
     int32_t nbins;

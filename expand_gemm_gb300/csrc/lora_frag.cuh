@@ -54,4 +54,14 @@ __device__ __forceinline__ void frag_b(uint32_t tile, int k0, int n0, uint32_t (
     }
 }
 
+// One B fragment (16 K x 8 N) at (k0, n0) of a tile whose rows are K.
+template <int CPR, int ROWS>
+__device__ __forceinline__ void frag_b1(uint32_t tile, int k0, int n0, uint32_t (&b)[2])
+{
+    const int lane = threadIdx.x & 15;         // lanes 16 to 31 name rows too, unused
+    const uint32_t addr = tile + tile_at<CPR, ROWS>(k0 + lane, n0 / 8);
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];\n"
+                 : "=r"(b[0]), "=r"(b[1]) : "r"(addr));
+}
+
 }  // namespace lora

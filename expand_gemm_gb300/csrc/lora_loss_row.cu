@@ -9,8 +9,8 @@
 // of two that moves only when a logit lies 60 exponents above it.
 //
 // Bound by HBM: vocabulary 32000 x hidden 4096 is 262 MB, 39 us at the
-// measured copy rate; eight rows (64 KB) a block and two blocks an SM are in
-// flight.
+// measured copy rate; four rows (32 KB) a block are loaded while four are
+// used, two blocks an SM.
 #include "lora_loss.cuh"
 
 namespace lora {
@@ -21,7 +21,7 @@ constexpr int LR_WINDOW = 60;
 // CH: 16-byte chunks of a row a thread; NT: tokens.
 template <int CH, int NT>
 struct RowShape {
-    static constexpr int RB = CH >= 4 ? 4 : 8;                    // rows at a time
+    static constexpr int RB = (CH == 1 ? 8 : 4) / (NT > 1 && CH != 2 ? 2 : 1);     // rows at a time
     static constexpr int BLOCKS = CH >= 4 || NT > 1 ? 1 : 2;      // on an SM
 };
 
@@ -61,17 +61,25 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
     }
     const int batches = (p.V + RB - 1) / RB;
     int parity = 0;
-    for (int b = blockIdx.x; b < batches; b += gridDim.x, parity ^= 1) {
-        uint4 w[RB][CH];
+    uint4 w[RB][CH], next[RB][CH];
+    auto fetch = [&](int b) {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int col = (c * LR_THREADS + part) * 8;
-                w[r][c] = make_uint4(0, 0, 0, 0);
+                next[r][c] = make_uint4(0, 0, 0, 0);
                 if (b * RB + r < p.V && col < p.H)
-                    w[r][c] = *reinterpret_cast<const uint4 *>(p.weight + int64_t(b * RB + r) * p.H + col);
+                    next[r][c] = *reinterpret_cast<const uint4 *>(p.weight + int64_t(b * RB + r) * p.H + col);
             }
+    };
+    fetch(int(blockIdx.x));
+    for (int b = blockIdx.x; b < batches; b += gridDim.x, parity ^= 1) {
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) w[r][c] = next[r][c];
+        fetch(b + int(gridDim.x));
         float dot[RB * NT];
 #pragma unroll
         for (int r = 0; r < RB; ++r)
@@ -166,6 +174,7 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
 
 constexpr int LR_JOIN_THREADS = 512;
 constexpr int LR_JOIN_COLS = 64;
+constexpr int LR_JOIN_AHEAD = 20;         // slots of a warp loaded at once: 320 in all
 
 // Block (64 columns, token): the blocks' partial sums in a fixed order, the
 // loss, and dh.
@@ -177,6 +186,18 @@ __global__ void __launch_bounds__(LR_JOIN_THREADS) loss_row_join_kernel(const Lo
     pdl_wait();
     const int y = p.targets[t];
     const bool valid = y >= 0 && y < p.V;
+    const int col = blockIdx.x * LR_JOIN_COLS + lane * 2;
+    // a warp's slots are warp, warp + 16, ...: their values are asked for
+    // before the sums are known
+    const bool read = valid && p.dh != nullptr && col < p.H;
+    float2 v[LR_JOIN_AHEAD];
+#pragma unroll
+    for (int i = 0; i < LR_JOIN_AHEAD; ++i) {
+        const int s = warp + 16 * i;
+        v[i] = make_float2(0.0f, 0.0f);
+        if (read && s < p.slots)
+            v[i] = *reinterpret_cast<const float2 *>(p.acc + (int64_t(s) * p.nt + t) * p.H + col);
+    }
     if (blockIdx.x == 0 && t == 0 && tid == 0 && p.error_word != nullptr) {
         int bad = 0;
         for (int i = 0; i < p.T; ++i) bad += p.targets[i] >= p.V;
@@ -191,8 +212,8 @@ __global__ void __launch_bounds__(LR_JOIN_THREADS) loss_row_join_kernel(const Lo
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s_red[i]);
         __syncthreads();
         for (int s = tid; s < p.slots; s += LR_JOIN_THREADS) {
-            const float2 v = p.stat[s * p.nt + t];
-            sum += v.x > -INFINITY ? v.y * exp2f(v.x - top) : 0.0f;
+            const float2 x = p.stat[s * p.nt + t];
+            sum += x.x > -INFINITY ? x.y * exp2f(x.x - top) : 0.0f;
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s_red[warp] = sum;
@@ -211,29 +232,31 @@ __global__ void __launch_bounds__(LR_JOIN_THREADS) loss_row_join_kernel(const Lo
         if (p.logsumexp != nullptr) p.logsumexp[t] = row.lse2 * LOSS_LN2;
     }
     if (p.dh == nullptr) return;
-    const int col = blockIdx.x * LR_JOIN_COLS + lane * 2;
     float a = 0.0f, b = 0.0f;
-    if (valid && col < p.H) {
-#pragma unroll 8
-        for (int s = warp; s < p.slots; s += 16) {
-            const float ref = p.stat[s * p.nt + t].x;
-            const float f = ref > -INFINITY ? exp2f(ref - top) : 0.0f;
-            const float2 v = *reinterpret_cast<const float2 *>(p.acc + (int64_t(s) * p.nt + t) * p.H + col);
-            a = fmaf(f, v.x, a);
-            b = fmaf(f, v.y, b);
-        }
+    auto add = [&](int s, const float2 &x) {
+        const float ref = p.stat[s * p.nt + t].x;
+        const float f = ref > -INFINITY ? exp2f(ref - top) : 0.0f;
+        a = fmaf(f, x.x, a);
+        b = fmaf(f, x.y, b);
+    };
+    if (read) {
+#pragma unroll
+        for (int i = 0; i < LR_JOIN_AHEAD; ++i)
+            if (warp + 16 * i < p.slots) add(warp + 16 * i, v[i]);
+        for (int s = warp + 16 * LR_JOIN_AHEAD; s < p.slots; s += 16)
+            add(s, *reinterpret_cast<const float2 *>(p.acc + (int64_t(s) * p.nt + t) * p.H + col));
     }
     s_part[warp][lane * 2] = a;
     s_part[warp][lane * 2 + 1] = b;
     __syncthreads();
     if (tid < LR_JOIN_COLS && blockIdx.x * LR_JOIN_COLS + tid < p.H) {
         const int c = blockIdx.x * LR_JOIN_COLS + tid;
-        float v = 0.0f;
+        float g = 0.0f;
         if (valid) {
-            for (int i = 0; i < 16; ++i) v += s_part[i][tid];
-            v = w * (row.inv * v - row.share * bf16_to_f32(p.weight[int64_t(y) * p.H + c]));
+            for (int i = 0; i < 16; ++i) g += s_part[i][tid];
+            g = w * (row.inv * g - row.share * bf16_to_f32(p.weight[int64_t(y) * p.H + c]));
         }
-        p.dh[t * p.dh_ld + c] = uint16_t(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+        p.dh[t * p.dh_ld + c] = uint16_t(pack_bf16x2(g, 0.0f) & 0xFFFFu);
     }
 }
 
