@@ -106,8 +106,8 @@ struct GradWTcArgs {
     int32_t kinds, ring, stage_bytes, stages, buffers;
 };
 
-// The gradients of an adapter without tokens: zeros, written by the 128
-// threads of the epilogue along the rows.
+// The gradients of an adapter without tokens: zeros, written by 128 threads
+// along the rows.
 __device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int id, int s0, int slices,
                                            int c0, int thread)
 {
@@ -133,13 +133,16 @@ __device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int
 // dB: rows = 128 columns of dy, columns = r; dbias: one more product with
 // ones.  An item's K is its adapter's tokens, 64 a stage.  Adapters are
 // taken by falling token count, so that the CTAs' shares come out even.
-__global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_constant__ GradWTcArgs q)
+// Four more warps write the zeros of the adapters without tokens meanwhile
+// (with 8 of 64 adapters in use they are most of the bytes).
+constexpr int TC_W_THREADS = TC_THREADS + 128;
+__global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid_constant__ GradWTcArgs q)
 {
     const BackwardArgs &p = q.b;
     uint8_t *smem = tc_smem();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int RP = q.rp, PPS = RP / 64;                 // panels a slice
-    for (int i = tid; i < TC_ONES / 4; i += TC_THREADS)
+    for (int i = tid; i < TC_ONES / 4; i += TC_W_THREADS)
         reinterpret_cast<uint32_t *>(smem + q.ring - TC_ONES)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
     const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
@@ -149,44 +152,61 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
     int *mem = reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES);
     const SegTab tab = load_tab(p, mem, tiles);
     const int *seg_of = load_seg_of(p, tab, tiles, mem);
+    // order: the segments of the adapters with tokens, then the adapters without
     int *order = mem + backward_tab_words(p.nbins, p.L);
-    for (int i = tid; i < p.L; i += TC_THREADS) {
-        int at = i;
-        if (p.L <= 256) {                               // more would take longer than it saves
-            const int mine = seg_of[i] >= 0 ? tab.count[seg_of[i]] : 0;
-            at = 0;
-            for (int j = 0; j < p.L; ++j) {
-                const int c = seg_of[j] >= 0 ? tab.count[seg_of[j]] : 0;
-                at += c > mine || (c == mine && j < i);
-            }
+    if (warp == 0) {
+        int used = 0, rest = 0;
+        for (int i0 = 0; i0 < p.L; i0 += 32)
+            used += __popc(__ballot_sync(0xffffffffu, i0 + lane < p.L && seg_of[i0 + lane] >= 0));
+        if (lane == 0) order[p.L] = used;
+        for (int i0 = 0; i0 < p.L; i0 += 32) {
+            const bool none = i0 + lane < p.L && seg_of[i0 + lane] < 0;
+            const uint32_t m = __ballot_sync(0xffffffffu, none);
+            if (none) order[used + rest + __popc(m & ((1u << lane) - 1u))] = i0 + lane;
+            rest += __popc(m);
         }
-        order[at] = i;
+    }
+    __syncthreads();
+    const int active = order[p.L];
+    for (int i = tid; i < p.L; i += TC_W_THREADS) {
+        const int seg = seg_of[i];
+        if (seg < 0) continue;
+        // its place by falling count; among many adapters, as they come
+        // (finding it would take longer than it saves)
+        int at = 0;
+        for (int k = 0; k < p.nbins; ++k) {
+            if (tab.id[k] < 0 || tab.count[k] <= 0) continue;
+            if (active > 256) at += k < seg;
+            else at += tab.count[k] > tab.count[seg] || (tab.count[k] == tab.count[seg] && k < seg);
+        }
+        order[at] = seg;
     }
     __syncthreads();
     const int blocks = q.end[q.kinds - 1];
-    const int64_t items = int64_t(p.L) * blocks;
+    const int items = active * blocks;          // the weights fit the memory: below 2^31
 
     struct Item {
         bool is_a;
-        int id, s, slices, seg, start, count, steps, c0;
+        int id, s, slices, start, count, steps, c0;
         int64_t row0;                                   // in g and u, within a slice
     };
-    auto decode = [&](int64_t i) {
-        Item it;
-        it.id = order[i / blocks];
-        const int blk = int(i % blocks);
+    auto kind = [&](int blk, Item &it) {
         int k = 0;
         while (blk >= q.end[k]) ++k;
-        const int j0 = blk - (k > 0 ? q.end[k - 1] : 0);
         it.is_a = k < q.groups;
         it.s = it.is_a ? k * q.group : k - q.groups;
         it.slices = it.is_a ? min(q.group, p.S - it.s) : 1;
-        it.seg = seg_of[it.id];
-        it.start = it.seg >= 0 ? tab.start[it.seg] : 0;
-        it.count = it.seg >= 0 ? tab.count[it.seg] : 0;
+        it.c0 = (it.is_a ? 0 : p.off[it.s] & ~7) + (blk - (k > 0 ? q.end[k - 1] : 0)) * 128;
+    };
+    auto decode = [&](int i) {
+        Item it;
+        const int seg = order[i / blocks];
+        kind(i % blocks, it);
+        it.id = tab.id[seg];
+        it.start = tab.start[seg];
+        it.count = tab.count[seg];
         it.steps = (it.count + 63) / 64;
-        it.c0 = (it.is_a ? 0 : p.off[it.s] & ~7) + j0 * 128;
-        it.row0 = it.seg >= 0 ? int64_t(tab.tile[it.seg]) * 64 : 0;
+        it.row0 = int64_t(tab.tile[seg]) * 64;
         return it;
     };
     if (warp == 0) {
@@ -195,7 +215,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
         int issued = 0;
         bool ok = true;
         const int panel = lane & 1, r4 = (lane >> 1) * 4;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
             const TcRowMaps *map = it.is_a ? &q.x : &q.dy;
             TcRows rows;
@@ -206,7 +226,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                     rows.t[j] = row < it.count ? p.sorted[it.start + row] : tc_no_row(p.T, row);
                 }
             };
-            if (it.steps > 0) tokens(0);
+            tokens(0);
             for (int k = 0; k < it.steps; ++k) {
                 const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
                 if (__all_sync(0xffffffffu, got) == 0) {
@@ -232,7 +252,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
         TcPos pos;
         int issued = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
             const CUtensorMap *map = it.is_a ? &q.g : &q.u;
             const int panels = it.slices * PPS;
@@ -261,9 +281,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
             int buf = 0;
             uint32_t bphase = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it = decode(i);
-                if (it.steps == 0) continue;
                 if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
                 tc_fence_after();
                 const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers));
@@ -302,18 +321,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------ epilogue
         const int row = (warp - 4) * 32 + lane;
         uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
             const Item it = decode(i);
-            if (it.steps == 0) {
-                clear_item(p, it.is_a, it.id, it.s, it.slices, it.c0, row);
-                continue;
-            }
             const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers)) + (uint32_t((warp - 4) * 32) << 16);
             const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
             if (__all_sync(0xffffffffu, got) == 0) break;
@@ -356,6 +371,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_w_tc_kernel(const __grid_c
                 buf = 0;
                 bphase ^= 1u;
             }
+        }
+    } else if (warp >= 8) {
+        // ------------------------------------------------ adapters without tokens
+        for (int i = blockIdx.x; i < (p.L - active) * blocks; i += gridDim.x) {
+            Item it;
+            kind(i % blocks, it);
+            clear_item(p, it.is_a, order[active + i / blocks], it.s, it.slices, it.c0, tid - TC_THREADS);
         }
     }
     tc_finish(ring, p.error_word);
@@ -409,8 +431,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
     SegTab t64, t128;
     const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
     const int hb = (p.H + TC_X_COLS - 1) / TC_X_COLS;
-    const int64_t items = int64_t(tiles) * hb;
-    const int64_t first = items * blockIdx.x / gridDim.x, end = items * (blockIdx.x + 1) / gridDim.x;
+    const int items = tiles * hb;               // T x H fits the memory: below 2^31
+    const int first = int(int64_t(items) * blockIdx.x / gridDim.x);
+    const int end = int(int64_t(items) * (blockIdx.x + 1) / gridDim.x);
 
     if (warp == 0) {
         // g and u were written by the stream's previous kernel with ordinary stores
@@ -419,8 +442,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
         int issued = 0, loaded = -1;
         uint32_t gphase = 0;
         bool ok = true;
-        for (int64_t i = first; ok && i < end; ++i) {
-            const int tile = int(i / hb), h0 = int(i % hb) * TC_X_COLS;
+        for (int i = first; ok && i < end; ++i) {
+            const int tile = i / hb, h0 = i % hb * TC_X_COLS;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int64_t row0 = int64_t(t64.tile[seg]) * 64 + int64_t(tile - t128.tile[seg]) * TC_ROWS;
             const int id = t128.id[seg];
@@ -467,10 +490,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
             int buf = 0, tile = -1;
             uint32_t bphase = 0, gphase = 0;
             bool ok = true;
-            for (int64_t i = first; ok && i < end; ++i) {
+            for (int i = first; ok && i < end; ++i) {
                 if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
-                if (q.keep && int(i / hb) != tile) {
-                    tile = int(i / hb);
+                if (q.keep && i / hb != tile) {
+                    tile = i / hb;
                     if (!pg_wait(g_full, gphase, ring.abort)) break;
                     gphase ^= 1u;
                 }
@@ -493,7 +516,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                 }
                 if (!ok) break;
                 umma_commit(ring.accf + 8 * buf);
-                if (q.keep && i + 1 < end && int((i + 1) / hb) != tile) umma_commit(g_empty);
+                if (q.keep && i + 1 < end && (i + 1) / hb != tile) umma_commit(g_empty);
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1u;
             }
@@ -503,8 +526,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
         uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
-        for (int64_t i = first; i < end; ++i) {
-            const int tile = int(i / hb), h0 = int(i % hb) * TC_X_COLS;
+        for (int i = first; i < end; ++i) {
+            const int tile = i / hb, h0 = i % hb * TC_X_COLS;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int r0 = (tile - t128.tile[seg]) * TC_ROWS;
             const int tok = r0 + row < t128.count[seg]
@@ -559,15 +582,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
     pdl_wait();
     SegTab t64, t128;
     const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
-    const int64_t items = int64_t(tiles) * p.S;
+    const int items = tiles * p.S;
     const int RP = q.rp, panels = RP / 64;
 
     if (warp == 0) {
         TcPos pos;
         int issued = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const int s = q.by_width[i / tiles], tile = int(i % tiles);
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const int s = q.by_width[i / tiles], tile = i % tiles;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int r0 = (tile - t128.tile[seg]) * TC_ROWS + lane * 4;
             TcRows rows;
@@ -597,8 +620,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
         TcPos pos;
         int issued = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const int s = q.by_width[i / tiles], tile = int(i % tiles);
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const int s = q.by_width[i / tiles], tile = i % tiles;
             const int id = t128.id[find_segment(t128.tile, p.nbins, tile)];
             const int steps = (p.n[s] + 63) / 64;
             for (int k = 0; k < steps; ++k) {
@@ -624,7 +647,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
             int buf = 0;
             uint32_t bphase = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const int steps = (p.n[q.by_width[i / tiles]] + 63) / 64;
                 if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
                 tc_fence_after();
@@ -654,8 +677,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
         uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
-            const int s = q.by_width[i / tiles], tile = int(i % tiles);
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
+            const int s = q.by_width[i / tiles], tile = i % tiles;
             const int seg = find_segment(t128.tile, p.nbins, tile);
             const int r0 = (tile - t128.tile[seg]) * TC_ROWS, count = t128.count[seg];
             // rows up to the end of the 64-token tile are written (zeros)
@@ -741,7 +764,7 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     // empty: its second half reads the (unused) next panel of the stage
     const int panels = has_a ? (q.group * (rp / 64) + 1) / 2 * 2 : rp / 64;
     q.stage_bytes = (2 + panels) * TC_PANEL;
-    q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L);
+    q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L + 1);
     q.stages = tc_stages(q.ring - TC_ONES, q.stage_bytes);
     if (q.stages < 2) return -1;
     const int cols_a = has_a ? (q.group * rp + 127) / 128 * 128 : 0;
@@ -756,7 +779,7 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     if (int e = tc_configure()) return e;
     const int64_t items = int64_t(p.L) * blocks;
     const int sms = device_sm_count();
-    return int(launch_kernel(grad_w_tc_kernel, dim3(unsigned(items < sms ? items : sms)), dim3(TC_THREADS),
+    return int(launch_kernel(grad_w_tc_kernel, dim3(unsigned(items < sms ? items : sms)), dim3(TC_W_THREADS),
                              size_t(TC_SMEM), st, q));
 }
 
