@@ -208,8 +208,20 @@ __global__ void __launch_bounds__(BW_THREADS) join_u_kernel(const __grid_constan
                 v.z += x.z;
                 v.w += x.w;
             }
-            reinterpret_cast<uint2 *>(p.g + out0)[i] = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            reinterpret_cast<uint2 *>(p.u + out0)[i] = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+            const uint2 gv = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            const uint2 uv = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+            reinterpret_cast<uint2 *>(p.g + out0)[i] = gv;
+            if (p.ut != nullptr) {
+                uint16_t *gt = p.gt + out0 + col * BW_TOK + row, *ut = p.ut + out0 + col * BW_TOK + row;
+                const uint32_t a[2] = {gv.x, gv.y}, b[2] = {uv.x, uv.y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    gt[e * BW_TOK] = uint16_t(a[e >> 1] >> (16 * (e & 1)));
+                    ut[e * BW_TOK] = uint16_t(b[e >> 1] >> (16 * (e & 1)));
+                }
+            } else {
+                reinterpret_cast<uint2 *>(p.u + out0)[i] = uv;
+            }
         }
     }
 }
@@ -357,7 +369,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constan
         }
     }
     cp_async_wait<0>();
-    if (!p.add) clear_rest(p, tab);
+    if (!p.add) clear_rest(p, tab, warp, BW_THREADS / 32);
 }
 
 // ---------------------------------------------------------------- dA, dB, dbias
@@ -580,8 +592,10 @@ static int64_t backward_rows(int64_t T, int64_t L)
 }
 
 template <int RP>
-static int run_backward(const BackwardArgs &p, cudaStream_t st)
+static int run_backward(BackwardArgs p, cudaStream_t st)
 {
+    const bool w_tc = grad_w_tc_fits(p, RP);
+    if (!w_tc) p.gt = p.ut = nullptr;
     const int tab = int(seg_tab_bytes(p.nbins));
     const int us = grad_u_smem<RP>() + tab, xs = grad_x_smem<RP>() + tab;
     const int ws = grad_w_smem<RP>() + tab + p.L * 4;
@@ -630,8 +644,7 @@ static int run_backward(const BackwardArgs &p, cudaStream_t st)
         }
     }
     const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
-    tc = RP >= 64 ? launch_grad_w_tc(p, RP, st) : -1;
-    if (tc >= 0) return tc;
+    if (w_tc) return launch_grad_w_tc(p, RP, st);
     if (items > 0) {
         const int64_t grid = items < resident(ws) ? items : resident(ws);
         e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);
@@ -651,10 +664,10 @@ LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidd
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
     const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;
-    // g, u, and the slots of partial sums: one an item and one a CTA
+    // g, u, g transposed, and the slots of partial sums: one an item and one a CTA
     const int64_t slots = lora::backward_rows(num_tokens, max_loras) / lora::BW_TOK * num_slices +
                           lora::BW_RESIDENT * lora::device_sm_count();
-    return 2 * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
+    return (rank > 32 ? 3 : 2) * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
 }
 
 LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,
@@ -741,7 +754,9 @@ LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t 
     const int64_t one = (p.rows * num_slices * rp * 2 + 255) / 256 * 256;
     p.g = reinterpret_cast<uint16_t *>(workspace);
     p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + one);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + 2 * one);
+    p.ut = p.u;
+    p.gt = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 2 * one);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + (rp > 32 ? 3 : 2) * one);
     p.u_ctas = 0;
     int steps = 0;
     for (int s = 0; s < LORA_MAX_SLICES; ++s) {

@@ -26,6 +26,9 @@ struct BackwardArgs {
     int32_t add, dy_vec, x_vec, dx_vec;
     float scale;
     uint16_t *g, *u;                       // [S][rows][RP]
+    // for grad_w_tc_kernel, in the place of u, and beside g: the tiles
+    // transposed, [S][rows / BW_TOK][RP][BW_TOK]; else null
+    uint16_t *gt, *ut;
     int64_t rows;
     float *part;                           // grad_u_kernel's partial sums, [BW_TOK][RP] each
     int32_t step_end[LORA_MAX_SLICES];     // its 64-column steps of one tile, by slice
@@ -48,9 +51,9 @@ __device__ __forceinline__ SegTab load_tab(const BackwardArgs &p, int *mem, int 
 // Tokens without an adapter: the metadata's first segment, or every token
 // when the batch has no adapter at all (the order is then unset).  Their
 // rows of dx are cleared (dx is overwritten, not added to).
-__device__ __forceinline__ void clear_rest(const BackwardArgs &p, const SegTab &tab)
+__device__ __forceinline__ void clear_rest(const BackwardArgs &p, const SegTab &tab, int warp, int warps)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31;
     const bool none = *p.no_lora != 0;
     const int rest = none ? p.T : (tab.id[0] == -1 ? tab.count[0] : 0);
     for (int64_t i = int64_t(blockIdx.x) * warps + warp; i < rest; i += int64_t(gridDim.x) * warps) {
@@ -85,6 +88,8 @@ __device__ __forceinline__ const int *load_seg_of(const BackwardArgs &p, const S
 // or a cudaError_t.
 int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st);
 int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st);
+// grad_w_tc takes the transposed g and u, so whether it fits is known before.
+bool grad_w_tc_fits(const BackwardArgs &p, int rp);
 int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st);
 
 }  // namespace lora

@@ -11,20 +11,16 @@
 // token gets an index past the matrix and arrives as zeros.  Weights are mapped
 // with a dimension of their own for the adapter, so that what lies behind a
 // slice's last row or column arrives as zeros too, never as a neighbour's
-// values.  Products over tokens take both operands with their rows
-// contiguous (MN-major), so nothing is transposed.
+// values.
 //
-// One CTA an SM (dA and dB: pairs of them); warps: 0 gathers, 1 loads boxes,
-// 2 issues UMMAs, 4..7 run the epilogue (thread = TMEM lane = row of the
-// result).
+// One CTA an SM; warps: 0 gathers, 1 loads boxes, 2 issues UMMAs, 4..7 run
+// the epilogue (thread = TMEM lane = row of the result).
 #include "lora_backward.cuh"
 #include "lora_tc.cuh"
 
 namespace lora {
 
-constexpr int TC_ONES = 2048;                    // 16 rows of a panel
 constexpr int TC_ROWS = 128;                     // tokens of a tile of g and dx
-constexpr int TC_MAX_N = 384;                    // slices x rank of one dA product
 
 // Four rows of a 2-D tensor, one 64-column box each.
 __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int col, int r0,
@@ -80,21 +76,6 @@ __device__ __forceinline__ void tc_load_rows(const TcRows &r, uint32_t dst, cons
     else if (r.level == -1) tma_gather4(dst, gather, col, r.t[0], r.t[1], r.t[2], r.t[3], bar);
 }
 
-// The same into this CTA, counted on a barrier of either CTA of a pair.
-__device__ __forceinline__ void tc_load_rows_pair(const TcRows &r, uint32_t dst, const CUtensorMap *gather,
-                                                  const CUtensorMap *boxes, int col, uint32_t bar)
-{
-    if (r.level >= 0) {
-        tma_load_2d_pair(dst, boxes + r.level, col, r.t[0], bar);
-    } else if (r.level == -1) {
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4"
-            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n"
-            :: "r"(dst), "l"(reinterpret_cast<uint64_t>(gather)), "r"(col), "r"(r.t[0]), "r"(r.t[1]),
-               "r"(r.t[2]), "r"(r.t[3]), "r"(bar) : "memory");
-    }
-}
-
 // Host: the maps of one matrix's rows: the gather's, then the boxes'.
 struct TcRowMaps {
     CUtensorMap gather, box[TC_HEIGHTS];
@@ -116,10 +97,10 @@ static bool encode_row_maps(TcRowMaps *m, const uint16_t *ptr, int64_t rows, int
 struct GradWTcArgs {
     BackwardArgs b;
     TcRowMaps dy, x;
-    CUtensorMap u, g;          // boxes 64 columns x 64 rows of [S * rows][RP]
+    CUtensorMap ut, gt;        // [S * rows / 64 * RP][64], boxes 64 x RP: a tile's u or g, transposed
     int32_t rp, group, groups; // slices of one dA product
     int32_t end[2 * LORA_MAX_SLICES];   // blocks of one adapter: dA groups, then dB slices
-    int32_t kinds, ring, stage_bytes, stages, buffers;
+    int32_t kinds, ring, stage_bytes, stages, buffers, ones;
 };
 constexpr int TC_W_COLS = 256;           // columns of dy or x of an item
 constexpr int TC_W_THREADS = TC_THREADS + 128;
@@ -131,53 +112,33 @@ __device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int
 {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     if (is_a) {
-        const int chunks = min(16, (p.H - c0) / 8);
+        const int chunks = min(TC_W_COLS / 8, (p.H - c0) / 8);
         for (int s = s0; s < s0 + slices; ++s) {
-            if (p.da[s] == nullptr || (thread & 15) >= chunks) continue;
-            uint16_t *out = p.da[s] + int64_t(id) * p.r * p.H + c0 + (thread & 15) * 8;
-            for (int r = thread >> 4; r < p.r; r += 8) *reinterpret_cast<uint4 *>(out + int64_t(r) * p.H) = zero;
+            if (p.da[s] == nullptr || (thread & 31) >= chunks) continue;
+            uint16_t *out = p.da[s] + int64_t(id) * p.r * p.H + c0 + (thread & 31) * 8;
+            for (int r = thread >> 5; r < p.r; r += 4) *reinterpret_cast<uint4 *>(out + int64_t(r) * p.H) = zero;
         }
     } else {
-        const int n = p.n[s0], lo = max(0, c0 - p.off[s0]), hi = min(n, c0 + 128 - p.off[s0]);
+        const int n = p.n[s0], lo = max(0, c0 - p.off[s0]), hi = min(n, c0 + TC_W_COLS - p.off[s0]);
         if (p.db[s0] != nullptr) {
             uint4 *out = reinterpret_cast<uint4 *>(p.db[s0] + (int64_t(id) * n + lo) * p.r);
             for (int i = thread; i < (hi - lo) * p.r / 8; i += 128) out[i] = zero;
         }
-        if (p.dbias[s0] != nullptr && thread < hi - lo) p.dbias[s0][int64_t(id) * n + lo + thread] = 0;
+        if (p.dbias[s0] != nullptr)
+            for (int i = thread; i < hi - lo; i += 128) p.dbias[s0][int64_t(id) * n + lo + i] = 0;
     }
 }
 
-// Writes a warp's 32 columns of 64 rows of a row-major matrix: lane l holds
-// column l (64 values, 32 words from the first row down); row r, if below
-// `rows`, goes to dst + r * ld.  `many`: columns that exist.
-__device__ __forceinline__ void store_columns(uint8_t *stage, const uint32_t (&o)[32], uint16_t *dst,
-                                              int64_t ld, int rows, int many)
-{
-    const int lane = threadIdx.x & 31;
-    uint16_t *at = reinterpret_cast<uint16_t *>(stage);
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        at[(2 * j) * 32 + lane] = uint16_t(o[j] & 0xFFFFu);
-        at[(2 * j + 1) * 32 + lane] = uint16_t(o[j] >> 16);
-    }
-    __syncwarp();
-    const int c = (lane & 3) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 8 * i + (lane >> 2);
-        if (r < rows && c < many)
-            *reinterpret_cast<uint4 *>(dst + r * ld + c) = *reinterpret_cast<const uint4 *>(at + r * 32 + c);
-    }
-}
-
-// An item is an adapter x 256 columns of x or dy on a CTA pair: D[256
-// columns x N] += (64 tokens of the columns)^T (64 tokens of g or u), N = the
-// slices' ranks side by side for dA, one slice's for dB; dbias is one more
-// product, with ones.  K is the adapter's tokens.  As single CTAs with 128
-// columns each SM read 8 KB of shared memory for every 64 clocks of UMMA and
-// filled 64 KB a stage beside it, twice what it has (dA and dB at 16384
-// tokens, rank 128: 282 us); a pair shares the g and u panels.
+// An item is an adapter x 256 columns of x or dy: D[r x 256] += (g or u of
+// 64 tokens)^T (64 tokens of the columns); dA of up to two slices at once
+// (one under the other at rank 64), dB of one, dbias as one more product,
+// with ones.  K is the adapter's tokens.
+//
+// Both operands have the tokens along their rows.  A UMMA takes its B that
+// way (MN-major) at full rate, but not its A: with x or dy as A, on CTA
+// pairs too, an M = 128 step took 185 to 280 clocks instead of 64 to 128.
+// So g and u are A, laid out transposed by the kernel that computes them,
+// 64 tokens a row.
 //
 // Adapters are taken by falling token count, so that the CTAs' shares come
 // out even.  Warps 8 to 11 write the zeros of the adapters without tokens
@@ -187,35 +148,13 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
     const BackwardArgs &p = q.b;
     uint8_t *smem = tc_smem();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int pair = int(blockIdx.x >> 1), pairs = int(gridDim.x >> 1);
-    const int PPS = q.rp / 64;                          // panels a slice
-    for (int i = tid; i < TC_ONES / 4; i += TC_W_THREADS)
-        reinterpret_cast<uint32_t *>(smem + q.ring - TC_ONES)[i] = 0x3F803F80u;
+    const int RP = q.rp, A_BYTES = RP * 128;                // one slice's tile of g or u
+    constexpr int Z_BYTES = 4 * TC_PANEL;
+    for (int i = tid; i < q.ones / 4; i += TC_W_THREADS)
+        reinterpret_cast<uint32_t *>(smem + q.ring - q.ones)[i] = 0x3F803F80u;
     fence_proxy_async_smem();
-    const uint32_t base = smem_addr(smem), ones = base + q.ring - TC_ONES;
-    const uint32_t full = base + q.ring + TC_STAGE_ROWS, empty = full + 8 * TC_MAX_STAGES;
-    const uint32_t accf = empty + 8 * TC_MAX_STAGES, acce = accf + 16, drain = acce + 16;
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + q.ring + TC_STAGE_ROWS + 16 * TC_MAX_STAGES + 40);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
-    if (tid == 0) {
-        for (int i = 0; i < q.stages; ++i) {
-            mbar_init(full + 8 * i, 2);                 // the even CTA's two loading warps
-            mbar_init(empty + 8 * i, 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(accf + 8 * i, 1);
-            mbar_init(acce + 8 * i, 8);                 // four epilogue warps of each CTA
-        }
-        mbar_init(drain, 1);
-        mbar_fence_init();
-        *s_abort = 0;
-    }
-    if (warp == 3) tmem_alloc_pair(smem_addr(s_tmem), 512);
-    tc_fence_before();
-    cluster_sync_all();
-    tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const TcRing ring = tc_setup(smem, q.ring, q.stage_bytes, q.stages, 2);
+    const uint32_t ones = ring.ring + q.ring - q.ones;
     pdl_wait();
     int tiles;
     int *mem = reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES);
@@ -253,11 +192,11 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
     __syncthreads();
     const int blocks = q.end[q.kinds - 1];
     const int items = active * blocks;          // the weights fit the memory: below 2^31
+    const int slice_tiles = int(p.rows / BW_TOK);
 
     struct Item {
         bool is_a;
-        int id, s, slices, start, count, steps, c0, panels;     // c0: this CTA's columns
-        int64_t row0;                                           // in g and u, within a slice
+        int id, s, slices, start, count, steps, c0, tile0;
     };
     auto kind = [&](int blk, Item &it) {
         int k = 0;
@@ -265,9 +204,7 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         it.is_a = k < q.groups;
         it.s = it.is_a ? k * q.group : k - q.groups;
         it.slices = it.is_a ? min(q.group, p.S - it.s) : 1;
-        it.c0 = (it.is_a ? 0 : p.off[it.s] & ~7) + (blk - (k > 0 ? q.end[k - 1] : 0)) * TC_W_COLS +
-                int(rank) * 128;
-        it.panels = (it.slices * PPS + 1) / 2 * 2;              // an odd last one is loaded twice
+        it.c0 = (it.is_a ? 0 : p.off[it.s] & ~7) + (blk - (k > 0 ? q.end[k - 1] : 0)) * TC_W_COLS;
     };
     auto decode = [&](int i) {
         Item it;
@@ -277,30 +214,16 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         it.start = tab.start[seg];
         it.count = tab.count[seg];
         it.steps = (it.count + 63) / 64;
-        it.row0 = int64_t(tab.tile[seg]) * 64;
+        it.tile0 = tab.tile[seg];
         return it;
-    };
-    // A loading warp's thread, after its last fill: no copy and no commit
-    // may still target this CTA when it exits.
-    auto drain_loads = [&](int issued) {
-        const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-        for (int i = max(0, issued - q.stages); i < issued; ++i) {
-            const uint32_t ph = uint32_t(i / q.stages) & 1u, b8 = 8u * uint32_t(i % q.stages);
-            if (rank == 0)
-                while (!mbar_try_wait_cluster(full + b8, ph) && clock64() < dd) {
-                }
-            while (!mbar_try_wait_cluster(empty + b8, ph) && !*s_abort && clock64() < dd) {
-            }
-        }
     };
     if (warp == 0) {
         // ------------------------------------------------ columns of dy or x
-        const uint32_t full0 = cluster_map(full, 0);
         TcPos pos;
         int issued = 0;
         bool ok = true;
         const int panel = lane & 1, r4 = (lane >> 1) * 4;
-        for (int i = pair; ok && i < items; i += pairs) {
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
             const TcRowMaps *map = it.is_a ? &q.x : &q.dy;
             TcRows rows;
@@ -313,150 +236,150 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
             };
             tokens(0);
             for (int k = 0; k < it.steps; ++k) {
-                const bool got = pg_wait(empty + 8 * pos.stage, pos.phase ^ 1u, s_abort);
+                const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
                 if (__all_sync(0xffffffffu, got) == 0) {
                     ok = false;
                     break;
                 }
+                const uint32_t full = ring.full + 8 * pos.stage;
                 join_rows(rows, 2);
-                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(full + 8 * pos.stage, 4 * TC_PANEL);
+                if (lane == 0) mbar_arrive_expect_tx(full, Z_BYTES);
                 __syncwarp();
-                tc_load_rows_pair(rows, base + pos.stage * q.stage_bytes + panel * TC_PANEL + r4 * 128, &map->gather,
-                                  map->box, it.c0 + panel * 64, full0 + 8 * pos.stage);
+#pragma unroll
+                for (int j = panel; j < 4; j += 2)
+                    tc_load_rows(rows, ring.ring + pos.stage * ring.stage_bytes + j * TC_PANEL + r4 * 128,
+                                 &map->gather, map->box, it.c0 + j * 64, full);
                 if (k + 1 < it.steps) tokens(k + 1);
                 ++issued;
-                pos.next(q.stages);
+                pos.next(ring.stages);
             }
         }
-        if (lane == 0) drain_loads(issued);
+        if (lane == 0) tc_drain_loads(ring, issued);
     } else if (warp == 1) {
-        // ------------------------------------------------ g or u: every fourth panel pair's half
-        // g and u were written by the stream's previous kernel with ordinary stores
+        // ------------------------------------------------ u or g
+        // written by the stream's previous kernel with ordinary stores
         asm volatile("fence.proxy.async.global;\n" ::: "memory");
-        const uint32_t full0 = cluster_map(full, 0);
         TcPos pos;
         int issued = 0;
         bool ok = true;
-        for (int i = pair; ok && i < items; i += pairs) {
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
-            const CUtensorMap *map = it.is_a ? &q.g : &q.u;
-            // Products take up to four panels, the first half of them from the
-            // even CTA: lane j loads this CTA's j-th.
-            const int chunk = lane >> 1, in_chunk = min(4, it.panels - 4 * chunk);
-            const bool mine = lane < it.panels / 2;
-            const int panel = min(it.slices * PPS - 1,
-                                  4 * chunk + int(rank) * (in_chunk / 2) + (lane & 1));
+            const CUtensorMap *map = it.is_a ? &q.gt : &q.ut;
             for (int k = 0; k < it.steps; ++k) {
-                const bool got = pg_wait(empty + 8 * pos.stage, pos.phase ^ 1u, s_abort);
+                const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
                 if (__all_sync(0xffffffffu, got) == 0) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && rank == 0)
-                    mbar_arrive_expect_tx(full + 8 * pos.stage, uint32_t(it.panels * TC_PANEL));
+                const uint32_t full = ring.full + 8 * pos.stage;
+                if (lane == 0) mbar_arrive_expect_tx(full, uint32_t(it.slices * A_BYTES));
                 __syncwarp();
-                if (mine)
-                    tma_load_2d_pair(base + pos.stage * q.stage_bytes + (2 + lane) * TC_PANEL, map, panel % PPS * 64,
-                                     int((it.s + panel / PPS) * p.rows + it.row0) + k * 64, full0 + 8 * pos.stage);
+                if (lane < it.slices)
+                    tma_load_2d(ring.ring + pos.stage * ring.stage_bytes + Z_BYTES + lane * A_BYTES, map, 0,
+                                ((it.s + lane) * slice_tiles + it.tile0 + k) * RP, full);
                 ++issued;
-                pos.next(q.stages);
+                pos.next(ring.stages);
             }
         }
-        if (lane == 0) drain_loads(issued);
+        if (lane == 0) tc_drain_loads(ring, issued);
     } else if (warp == 2) {
-        // ------------------------------------------------ UMMAs (even CTA)
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t T_AB = (1u << 15) | (1u << 16);
+        // ------------------------------------------------ UMMAs
+        if (lane == 0) {
+            constexpr uint32_t IDESC = umma_idesc_bf16(128, TC_W_COLS) | 1u << 16;
             TcPos pos;
             int buf = 0;
             uint32_t bphase = 0;
             bool ok = true;
-            for (int i = pair; ok && i < items; i += pairs) {
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it = decode(i);
-                if (!pg_wait(acce + 8 * buf, bphase ^ 1u, s_abort)) break;
+                if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + uint32_t(buf * (512 / q.buffers));
+                const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers));
+                const int mt = (it.slices * RP + 127) / 128;
                 const bool bias = !it.is_a && p.dbias[it.s] != nullptr;
                 for (int k = 0; k < it.steps; ++k) {
-                    if (!pg_wait(full + 8 * pos.stage, pos.phase, s_abort)) {
+                    if (!pg_wait(ring.full + 8 * pos.stage, pos.phase, ring.abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t z = base + pos.stage * q.stage_bytes, v = z + 2 * TC_PANEL;
+                    const uint32_t z = ring.ring + pos.stage * ring.stage_bytes, a = z + Z_BYTES;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint32_t acc = k != 0 || kk != 0;
                         const uint64_t dz = umma_desc_mn(z + kk * 2048);
-                        for (int c = 0; c < it.panels; c += 4)
-                            umma_bf16_pair(d + uint32_t(c * 64), dz, umma_desc_mn(v + c / 2 * TC_PANEL + kk * 2048),
-                                           umma_idesc_bf16(256, min(4, it.panels - c) * 64) | T_AB, acc);
+                        for (int m = 0; m < mt; ++m)
+                            umma_bf16(d + uint32_t(m * TC_W_COLS), umma_desc_sw128(a + m * 2 * TC_PANEL + kk * 32),
+                                      dz, IDESC, acc);
                         if (bias)
-                            umma_bf16_pair(d + uint32_t(it.panels * 64), dz, umma_desc_mn(ones),
-                                           umma_idesc_bf16(256, 32) | T_AB, acc);
+                            umma_bf16(d + uint32_t(TC_W_COLS), umma_desc_sw128(ones + kk * 32), dz, IDESC, acc);
                     }
-                    umma_commit_both(empty + 8 * pos.stage);
-                    pos.next(q.stages);
+                    umma_commit(ring.empty + 8 * pos.stage);
+                    pos.next(ring.stages);
                 }
                 if (!ok) break;
-                umma_commit_both(accf + 8 * buf);
+                umma_commit(ring.accf + 8 * buf);
                 if (++buf == q.buffers) {
                     buf = 0;
                     bphase ^= 1u;
                 }
             }
-            if (*s_abort) {       // nothing in flight when TMEM is released
-                umma_commit_pair(cluster_map(drain, 0));
-                const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-                while (!mbar_try_wait_cluster(drain, 0) && clock64() < dd) {
-                }
-            }
         }
     } else if (warp >= 4 && warp < 8) {
         // ------------------------------------------------ epilogue
-        const int row = (warp - 4) * 32 + lane;         // this thread's column of x or dy
-        const uint32_t acce0 = cluster_map(acce, 0);
+        const int row = (warp - 4) * 32 + lane;         // slice and r
         uint8_t *stage = smem + q.ring + (warp - 4) * (TC_STAGE_ROWS / 4);
         int buf = 0;
         uint32_t bphase = 0;
-        for (int i = pair; i < items; i += pairs) {
+        for (int i = blockIdx.x; i < items; i += gridDim.x) {
             const Item it = decode(i);
-            const uint32_t d = tmem + uint32_t(buf * (512 / q.buffers)) + (uint32_t((warp - 4) * 32) << 16);
-            const bool got = pg_wait(accf + 8 * buf, bphase, s_abort);
+            const uint32_t d = ring.tmem + uint32_t(buf * (512 / q.buffers)) + (uint32_t((warp - 4) * 32) << 16);
+            const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
             if (__all_sync(0xffffffffu, got) == 0) break;
             tc_fence_after();
             uint32_t o[32];
             if (it.is_a) {
-                const int h0 = it.c0 + (warp - 4) * 32;
-                for (int j = 0; j < it.slices * PPS; ++j) {
-                    const int s = it.s + j / PPS, r0 = j % PPS * 64;
-                    if (p.da[s] == nullptr || h0 >= p.H) continue;
-                    load64(d + uint32_t(j * 64), p.scale, o);
-                    store_columns(stage, o, p.da[s] + (int64_t(it.id) * p.r + r0) * p.H + h0, p.H, p.r - r0,
-                                  p.H - h0);
-                }
-            } else {
-                const int n = p.n[it.s], at = it.c0 + row - p.off[it.s];
-                const bool in = at >= 0 && at < n;
-                if (p.db[it.s] != nullptr) {
-                    uint16_t *out = p.db[it.s] + (int64_t(it.id) * n + at) * p.r;
-                    for (int c = 0; c < p.r; c += 64) {
-                        load64(d + uint32_t(c), 1.0f, o);
-                        store_rows(stage, o, in ? out + c : nullptr, p.r - c);
+                const int mt = (it.slices * RP + 127) / 128;
+                for (int m = 0; m < mt; ++m) {
+                    const int R = m * 128 + row, s = it.s + R / RP, r = R % RP;
+                    uint16_t *out = R < it.slices * RP && r < p.r ? p.da[s] : nullptr;
+                    if (out != nullptr) out += (int64_t(it.id) * p.r + r) * p.H + it.c0;
+                    for (int c = 0; c < TC_W_COLS && it.c0 + c < p.H; c += 64) {
+                        load64(d + uint32_t(m * TC_W_COLS + c), p.scale, o);
+                        store_rows(stage, o, out != nullptr ? out + c : nullptr, p.H - it.c0 - c);
                     }
                 }
-                if (p.dbias[it.s] != nullptr) {
-                    uint32_t one[16];
-                    tmem_ld16_nowait(d + uint32_t(it.panels * 64), one);
-                    tmem_wait_ld();
-                    if (in)
-                        p.dbias[it.s][int64_t(it.id) * n + at] =
-                            uint16_t(pack_bf16x2(__uint_as_float(one[0]), 0.0f) & 0xFFFFu);
+            } else {
+                const int n = p.n[it.s], r0 = (warp - 4) * 32, n0 = it.c0 - p.off[it.s];
+                uint16_t *out = p.db[it.s];
+                if (out != nullptr && r0 < p.r) {
+                    out += (int64_t(it.id) * n + n0) * p.r + r0;
+                    for (int c = 0; c < TC_W_COLS && n0 + c < n; c += 64) {
+                        load64(d + uint32_t(c), 1.0f, o);
+                        store_columns(stage, o, out + int64_t(c) * p.r, p.r, -(n0 + c), n - n0 - c, p.r - r0);
+                    }
+                }
+                uint16_t *bias = p.dbias[it.s];
+                if (bias != nullptr && warp == 4) {
+                    // every row of the product with ones holds the sums: lane l
+                    // keeps column c + l of each 32
+                    for (int c = 0; c < TC_W_COLS; c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32_nowait(d + uint32_t(TC_W_COLS + c), v);
+                        tmem_wait_ld();
+                        uint32_t mine = 0;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) mine = lane == j ? v[j] : mine;
+                        const int at = n0 + c + lane;
+                        if (at >= 0 && at < n)
+                            bias[int64_t(it.id) * n + at] =
+                                uint16_t(pack_bf16x2(__uint_as_float(mine), 0.0f) & 0xFFFFu);
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acce0 + 8 * buf);
+            if (lane == 0) mbar_arrive(ring.acce + 8 * buf);
             if (++buf == q.buffers) {
                 buf = 0;
                 bphase ^= 1u;
@@ -464,18 +387,13 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         }
     } else if (warp >= 8) {
         // ------------------------------------------------ adapters without tokens
-        for (int i = pair; i < (p.L - active) * blocks; i += pairs) {
+        for (int i = blockIdx.x; i < (p.L - active) * blocks; i += gridDim.x) {
             Item it;
             kind(i % blocks, it);
             clear_item(p, it.is_a, order[active + i / blocks], it.s, it.slices, it.c0, tid - TC_THREADS);
         }
     }
-    __syncwarp();
-    if (tid == 0 && *s_abort) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
-    tc_fence_before();
-    cluster_sync_all();
-    tc_fence_after();
-    if (warp == 3) tmem_dealloc_pair(tmem, 512);
+    tc_finish(ring, p.error_word);
 }
 
 // ---------------------------------------------------------------- dx
@@ -579,6 +497,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                 }
             }
         }
+    } else if (warp == 1 || warp == 3) {
+        if (!p.add) clear_rest(p, t64, warp >> 1, 2);
     } else if (warp == 2) {
         if (lane == 0) {
             TcPos pos;
@@ -654,7 +574,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
         }
     }
     tc_finish(ring, p.error_word);
-    if (!p.add) clear_rest(p, t64);
 }
 
 // ---------------------------------------------------------------- g and u
@@ -781,6 +700,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
             const int tok = r0 + row < count
                                 ? checked_token(p.sorted[t128.start[seg] + r0 + row], p.T, p.error_word) : -1;
             const int64_t at = (int64_t(s) * p.rows + int64_t(t64.tile[seg]) * 64 + r0 + row) * RP;
+            // the transposed tiles [r][64 tokens]: this warp's 32 tokens of one
+            const int64_t tile64 = int64_t(s) * (p.rows / BW_TOK) + t64.tile[seg] + (r0 + row) / BW_TOK;
+            const int64_t turned = tile64 * RP * BW_TOK + row % BW_TOK / 32 * 32;
+            const bool laid_warp = r0 + row / 32 * 32 < (count + 63) / 64 * 64;
             const float *src = p.buf + (int64_t(s) * p.T + (tok < 0 ? 0 : tok)) * p.r;
             uint32_t o[32];
             for (int c = 0; c < RP; c += 64) {
@@ -795,7 +718,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
                     o[2 * j] = pack_bf16x2(f[j].x, f[j].y);
                     o[2 * j + 1] = pack_bf16x2(f[j].z, f[j].w);
                 }
-                store_rows(stage, o, laid ? p.u + at + c : nullptr, 64);
+                if (p.ut != nullptr) store_columns(stage, o, p.ut + turned + c * 64, 64, 0, laid_warp ? RP - c : 0, 32);
+                else store_rows(stage, o, laid ? p.u + at + c : nullptr, 64);
             }
             const bool got = pg_wait(ring.accf + 8 * buf, bphase, ring.abort);
             if (__all_sync(0xffffffffu, got) == 0) break;
@@ -804,6 +728,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
             for (int c = 0; c < RP; c += 64) {
                 load64(d + uint32_t(c), 1.0f, o);
                 store_rows(stage, o, laid ? p.g + at + c : nullptr, 64);
+                if (p.gt != nullptr) store_columns(stage, o, p.gt + turned + c * 64, 64, 0, laid_warp ? RP - c : 0, 32);
             }
             tc_fence_before();
             __syncwarp();
@@ -833,15 +758,20 @@ static int tc_configure()
     return 0;
 }
 
+bool grad_w_tc_fits(const BackwardArgs &p, int rp)
+{
+    return rp >= 64 && p.dy_vec && p.x_vec && p.T >= 1 && p.rows * p.S * 2 < (int64_t(1) << 31);
+}
+
 int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
-    if (rp < 64 || !p.dy_vec || !p.x_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
     static thread_local GradWTcArgs q;
     q.b = p;
     q.rp = rp;
-    q.group = TC_MAX_N / rp < p.S ? TC_MAX_N / rp : p.S;
+    q.group = p.S < 2 ? p.S : 2;
     q.groups = (p.S + q.group - 1) / q.group;
     int blocks = 0;
+    bool bias = false;
     for (int k = 0; k < q.groups; ++k) {
         bool any = false;
         for (int s = k * q.group; s < (k + 1) * q.group && s < p.S; ++s) any = any || p.da[s] != nullptr;
@@ -852,41 +782,30 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     for (int s = 0; s < p.S; ++s) {
         if (p.db[s] != nullptr || p.dbias[s] != nullptr)
             blocks += ((p.off[s] & 7) + p.n[s] + TC_W_COLS - 1) / TC_W_COLS;
+        bias = bias || p.dbias[s] != nullptr;
         q.end[q.groups + s] = blocks;
     }
     q.kinds = q.groups + p.S;
     if (blocks == 0) return 0;
-    const int panels = ((has_a ? q.group : 1) * (rp / 64) + 1) / 2 * 2;
-    q.stage_bytes = (2 + panels / 2) * TC_PANEL;
+    // products of 128 rows: two slices at rank 128, or one and the bias, take
+    // all of TMEM
+    const int slices = has_a ? q.group : 1;
+    q.buffers = slices * rp > 128 || bias ? 1 : 2;
+    q.stage_bytes = 4 * TC_PANEL + (slices * rp > 128 ? slices * rp * 128 : 2 * TC_PANEL);
+    q.ones = bias ? 2 * TC_PANEL : 0;
     q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L + 1);
-    q.stages = tc_stages(q.ring - TC_ONES, q.stage_bytes);
-    if (q.stages < 2) return -1;
-    q.buffers = panels * 64 + 32 <= 256 ? 2 : 1;
+    q.stages = tc_stages(q.ring - q.ones, q.stage_bytes);
+    const uint64_t rows = uint64_t(p.S) * uint64_t(p.rows / BW_TOK) * uint64_t(rp);
     if (!encode_row_maps(&q.dy, p.dy, p.T, p.width, p.dy_ld) ||
         !encode_row_maps(&q.x, p.x, p.T, p.H, p.x_ld) ||
-        !encode_tile_map(&q.u, p.u, uint64_t(p.S) * p.rows, uint64_t(rp), uint64_t(rp), 64, 64,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tile_map(&q.g, p.g, uint64_t(p.S) * p.rows, uint64_t(rp), uint64_t(rp), 64, 64,
-                         CU_TENSOR_MAP_SWIZZLE_128B))
-        return -1;
+        !encode_tile_map(&q.ut, p.ut, rows, 64, 64, 64, uint32_t(rp), CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tile_map(&q.gt, p.gt, rows, 64, 64, 64, uint32_t(rp), CU_TENSOR_MAP_SWIZZLE_128B))
+        return LORA_ERR_DEVICE;
     if (int e = tc_configure()) return e;
-    const int64_t items = int64_t(p.L) * blocks, most = device_sm_count() / 2;
-    if (most < 1) return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * (items < most ? items : most)));
-    cfg.blockDim = dim3(TC_W_THREADS);
-    cfg.dynamicSmemBytes = TC_SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return int(cudaLaunchKernelEx(&cfg, grad_w_tc_kernel, q));
+    const int64_t items = int64_t(p.L) * blocks;
+    const int sms = device_sm_count();
+    return int(launch_kernel(grad_w_tc_kernel, dim3(unsigned(items < sms ? items : sms)), dim3(TC_W_THREADS),
+                             size_t(TC_SMEM), st, q));
 }
 
 int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)

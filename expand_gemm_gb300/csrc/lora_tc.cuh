@@ -194,6 +194,31 @@ __device__ __forceinline__ void add_rows(uint8_t *stage, const uint32_t (&v)[32]
     }
 }
 
+// Writes a warp's 32 columns of 64 rows of a row-major matrix: lane l holds
+// column l (64 values, 32 words from the first row down); row r goes to dst
+// + r * ld where first <= r < rows.  `many`: columns that exist (a multiple
+// of 8).
+__device__ __forceinline__ void store_columns(uint8_t *stage, const uint32_t (&o)[32], uint16_t *dst,
+                                              int64_t ld, int first, int rows, int many)
+{
+    const int lane = threadIdx.x & 31;
+    uint16_t *at = reinterpret_cast<uint16_t *>(stage);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        at[(2 * j) * 32 + lane] = uint16_t(o[j] & 0xFFFFu);
+        at[(2 * j + 1) * 32 + lane] = uint16_t(o[j] >> 16);
+    }
+    __syncwarp();
+    const int c = (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (r >= first && r < rows && c < many)
+            *reinterpret_cast<uint4 *>(dst + r * ld + c) = *reinterpret_cast<const uint4 *>(at + r * 32 + c);
+    }
+}
+
 __device__ __forceinline__ uint8_t *tc_smem()
 {
     extern __shared__ uint8_t tc_smem_raw[];
