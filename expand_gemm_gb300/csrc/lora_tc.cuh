@@ -33,6 +33,27 @@ struct TcRing {
     uint32_t tmem;
 };
 
+// D += A B over 64 of K, as four UMMAs (K = 16): A K-major, B MN-major with
+// panels of 64 x 64, both with the 128-byte swizzle.  The descriptors differ
+// in their low words only, one add each: with 64-bit descriptors built for
+// every UMMA, one thread issued M = 128, N = 128 every 108 clocks instead of
+// every 75.  `more` is 0 for the accumulator's first product.
+__device__ __forceinline__ void umma_k64(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t more)
+{
+    const uint64_t da = umma_desc_sw128(a), db = umma_desc_mn(b);
+    const uint32_t a_hi = uint32_t(da >> 32), b_hi = uint32_t(db >> 32);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        asm volatile(
+            "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+            "mov.b64 a, {%1, %2};\n"
+            "mov.b64 b, {%3, %4};\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n"
+            :: "r"(d_tmem), "r"(uint32_t(da) + kk * 2), "r"(a_hi), "r"(uint32_t(db) + kk * 128), "r"(b_hi),
+               "r"(idesc), "r"(kk == 0 ? more : 1u) : "memory");
+}
+
 // Position in the ring.
 struct TcPos {
     int stage = 0;
