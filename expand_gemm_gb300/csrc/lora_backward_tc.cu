@@ -448,47 +448,47 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
     if (warp == 0) {
         // g and u were written by the stream's previous kernel with ordinary stores
         asm volatile("fence.proxy.async.global;\n" ::: "memory");
-        TcPos pos;
-        int issued = 0, loaded = -1;
-        uint32_t gphase = 0;
-        bool ok = true;
-        for (int i = first; ok && i < end; ++i) {
-            const int tile = i / hb, h0 = i % hb * TC_X_COLS;
-            const int seg = find_segment(t128.tile, p.nbins, tile);
-            const int64_t row0 = int64_t(t64.tile[seg]) * 64 + int64_t(tile - t128.tile[seg]) * TC_ROWS;
-            const int id = t128.id[seg];
-            if (q.keep && tile != loaded) {
-                const bool got = pg_wait(g_empty, gphase ^ 1u, ring.abort);
-                if (__all_sync(0xffffffffu, got) == 0) break;
-                if (lane == 0) mbar_arrive_expect_tx(g_full, uint32_t(steps * G_BYTES));
-                __syncwarp();
-                for (int k = lane; k < steps; k += 32)
-                    tma_load_2d(g_at + k * G_BYTES, &q.g, k % kps * 64, int(k / kps * p.rows + row0), g_full);
-                gphase ^= 1u;
-                loaded = tile;
-            }
-            for (int k = 0; k < steps; ++k) {
-                const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
-                if (__all_sync(0xffffffffu, got) == 0) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t full = ring.full + 8 * pos.stage;
-                const uint32_t at = ring.ring + pos.stage * stage_bytes;
-                const int s = k / kps, kc = k % kps * 64;
-                if (lane == 0) mbar_arrive_expect_tx(full, stage_bytes);
-                __syncwarp();
-                if (lane < 4) tma_load_3d(at + lane * TC_PANEL, &q.a[s], h0 + lane * 64, kc, id, full);
-                else if (lane == 4 && !q.keep)
-                    tma_load_2d(at + A_BYTES, &q.g, kc, int(s * p.rows + row0), full);
-                ++issued;
-                pos.next(q.stages);
-            }
-        }
         if (lane == 0) {
+            TcPos pos;
+            int issued = 0, tile = first / hb, h0 = first % hb * TC_X_COLS;
+            uint32_t gphase = 0;
+            bool ok = true, loaded = false;
+            for (int i = first; ok && i < end; ++tile, h0 = 0) {
+                const int seg = find_segment(t128.tile, p.nbins, tile);
+                const int row0 = t64.tile[seg] * 64 + (tile - t128.tile[seg]) * TC_ROWS;
+                const int id = t128.id[seg];
+                if (q.keep) {
+                    if (!pg_wait(g_empty, gphase ^ 1u, ring.abort)) break;
+                    mbar_arrive_expect_tx(g_full, uint32_t(steps * G_BYTES));
+                    for (int k = 0; k < steps; ++k)
+                        tma_load_2d(g_at + k * G_BYTES, &q.g, k % kps * 64, int(k / kps * p.rows) + row0, g_full);
+                    gphase ^= 1u;
+                    loaded = true;
+                }
+                for (; ok && i < end && h0 < p.H; ++i, h0 += TC_X_COLS) {
+                    int grow = row0;
+                    for (int s = 0; ok && s < p.S; ++s, grow += int(p.rows)) {
+                        const CUtensorMap *map = &q.a[s];
+                        for (int kc = 0; kc < q.rp; kc += 64) {
+                            if (!pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort)) {
+                                ok = false;
+                                break;
+                            }
+                            const uint32_t full = ring.full + 8 * pos.stage;
+                            const uint32_t at = ring.ring + pos.stage * stage_bytes;
+                            mbar_arrive_expect_tx(full, stage_bytes);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) tma_load_3d(at + j * TC_PANEL, map, h0 + j * 64, kc, id, full);
+                            if (!q.keep) tma_load_2d(at + A_BYTES, &q.g, kc, grow, full);
+                            ++issued;
+                            pos.next(q.stages);
+                        }
+                    }
+                }
+            }
             tc_drain_loads(ring, issued);
             // the last tile's g has landed
-            if (loaded >= 0) {
+            if (loaded) {
                 const long long dd = clock64() + PG_TIMEOUT_CYCLES;
                 while (!mbar_try_wait(g_full, gphase ^ 1u) && clock64() < dd) {
                 }
