@@ -240,7 +240,7 @@ constexpr int grad_x_smem()
 // Item: (tile, 128 columns), one step a slice; a ring of three steps runs
 // across the items.
 template <int RP>
-__global__ void __launch_bounds__(BW_THREADS) grad_x_kernel(const __grid_constant__ BackwardArgs p)
+__global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(const __grid_constant__ BackwardArgs p)
 {
     constexpr int CPR = RP / 8, ST = BW_X_STAGES;
     constexpr int SG = BW_TOK * RP * 2, SA = RP * BW_COLS * 2;
