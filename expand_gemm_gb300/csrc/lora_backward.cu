@@ -406,87 +406,108 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     const SegTab tab = load_tab(p, mem, tiles);
     const int *seg_of = load_seg_of(p, tab, tiles, mem);
     const int blocks = p.block_end[2 * p.S - 1];
-    const int items = p.L * blocks;           // the weights fit the memory: below 2^31
 
-    struct Item {
-        const uint16_t *z, *v;
-        int64_t ld;
-        int id, s, seg, start, count, steps, c0, lo, n, width;
-        bool is_a, vec;
+    // A block of an adapter's gradients: its product (dB of slice q, or dA of
+    // slice q - S) and its first column.  Items are taken gridDim.x apart; the
+    // walk adds instead of dividing.
+    struct Walk {
+        int id, blk, q, c0;
     };
-    auto decode = [&](int i) {
-        Item it;
-        it.id = i / blocks;
-        const int blk = i % blocks;
-        int q = 0;                                  // product: dB of slice q, or dA of slice q - S
-        while (blk >= p.block_end[q]) ++q;
-        it.is_a = q >= p.S;
-        it.s = it.is_a ? q - p.S : q;
-        it.lo = it.is_a ? 0 : p.off[it.s];
-        it.n = it.is_a ? p.H : p.n[it.s];
-        it.vec = it.is_a ? p.x_vec : p.dy_vec;
-        it.c0 = (it.vec ? it.lo & ~7 : it.lo) + (blk - (q > 0 ? p.block_end[q - 1] : 0)) * BW_COLS;
-        it.width = it.is_a ? p.H : p.width;         // readable columns
-        it.z = it.is_a ? p.x : p.dy;
-        it.ld = it.is_a ? p.x_ld : p.dy_ld;
-        it.seg = seg_of[it.id];
-        it.start = it.seg >= 0 ? tab.start[it.seg] : 0;
-        it.count = it.seg >= 0 ? tab.count[it.seg] : 0;
-        it.steps = max(1, (it.count + BW_TOK - 1) / BW_TOK);
-        it.v = (it.is_a ? p.g : p.u) +
-               (int64_t(it.s) * p.rows + (it.seg >= 0 ? int64_t(tab.tile[it.seg]) * BW_TOK : 0)) * RP;
-        return it;
+    const int step_id = gridDim.x / blocks, step_blk = gridDim.x % blocks;
+    auto place = [&](Walk &w) {
+        int q = 0, from = 0;
+        while (w.blk >= p.block_end[q]) from = p.block_end[q++];
+        w.q = q;
+        w.c0 = (w.blk - from) * BW_COLS;
+        if (q < p.S) w.c0 += p.dy_vec ? p.off[q] & ~7 : p.off[q];
     };
+    auto next = [&](Walk &w) {
+        w.id += step_id;
+        w.blk += step_blk;
+        if (w.blk >= blocks) {
+            w.blk -= blocks;
+            ++w.id;
+        }
+        if (w.id < p.L) place(w);
+    };
+    Walk at;                                    // the item that is multiplied next
+    at.id = blockIdx.x / blocks;
+    at.blk = blockIdx.x % blocks;
+    if (at.id < p.L) place(at);
 
     // the step that is loaded next, with its tokens
-    int l_item = blockIdx.x;
-    Item ld;
-    int l_k = 0, l_stage = 0, tok[4];
+    Walk to = at;
+    const uint16_t *z = nullptr, *v = nullptr;
+    int64_t z_ld = 0;
+    int start = 0, count = 0, l_k = 0, l_stage = 0, tok[4];
+    bool vec = false, whole = false;
+    const int z_at = int(tile_at<16, BW_TOK>(tid >> 4, tid & 15));
     auto tokens = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = l_k * BW_TOK + (tid >> 4) + i * 16;
-            tok[i] = row < ld.count ? checked_token(p.sorted[ld.start + row], p.T, p.error_word) : -1;
+            tok[i] = row < count ? checked_token(p.sorted[start + row], p.T, p.error_word) : -1;
         }
     };
-    if (l_item < items) {
-        ld = decode(l_item);
+    auto enter = [&]() {
+        if (to.id >= p.L) return;
+        const bool is_a = to.q >= p.S;
+        const int seg = seg_of[to.id], s = is_a ? to.q - p.S : to.q, col = to.c0 + (tid & 15) * 8;
+        const int width = is_a ? p.H : p.width;
+        start = seg >= 0 ? tab.start[seg] : 0;
+        count = seg >= 0 ? tab.count[seg] : 0;
+        z = (is_a ? p.x : p.dy) + col;
+        z_ld = is_a ? p.x_ld : p.dy_ld;
+        vec = is_a ? p.x_vec : p.dy_vec;
+        whole = vec && col + 8 <= width;
+        v = (is_a ? p.g : p.u) +
+            (int64_t(s) * p.rows + (seg >= 0 ? int64_t(tab.tile[seg]) * BW_TOK : 0)) * RP + tid * 8;
         tokens();
-    }
+    };
+    enter();
     auto issue = [&]() {
-        if (l_item < items) {
-            uint8_t *at = smem + l_stage * (SZ + SV);
+        if (to.id < p.L) {
+            uint8_t *dst = smem + l_stage * (SZ + SV) + z_at;
+            if (whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint8_t *dst = at + tile_at<16, BW_TOK>((tid >> 4) + i * 16, tid & 15);
-                if (tok[i] >= 0) copy8(dst, ld.z + tok[i] * ld.ld, ld.c0 + (tid & 15) * 8, 0, ld.width, ld.vec);
-                else *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i)
+                    cp_async16(smem_addr(dst + i * 16 * 128), tok[i] < 0 ? z : z + tok[i] * z_ld, tok[i] >= 0);
+            } else {
+                const int col = to.c0 + (tid & 15) * 8, width = to.q >= p.S ? p.H : p.width;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(dst + i * 16 * 128) =
+                        tok[i] < 0 ? make_uint4(0, 0, 0, 0) : load8(z - col + tok[i] * z_ld, col, 0, width, false);
             }
-            const bool ok = ld.seg >= 0;
+            const uint32_t sv = base + l_stage * (SZ + SV) + SZ;
 #pragma unroll
             for (int i = 0; i < PV; ++i) {
                 const int c = tid + i * BW_THREADS;
                 if (c < BW_TOK * CPR)
-                    cp_async16(smem_addr(at + SZ + tile_at<CPR, BW_TOK>(c / CPR, c % CPR)),
-                               ok ? ld.v + int64_t(l_k) * BW_TOK * RP + c * 8 : p.g, ok);
+                    cp_async16(sv + tile_at<CPR, BW_TOK>(c / CPR, c % CPR),
+                               count > 0 ? v + int64_t(l_k) * BW_TOK * RP + i * BW_THREADS * 8 : p.g, count > 0);
             }
-            if (++l_k == ld.steps) {
+            if (++l_k * BW_TOK >= count) {
                 l_k = 0;
-                l_item += gridDim.x;
-                if (l_item < items) ld = decode(l_item);
+                next(to);
+                enter();
+            } else {
+                tokens();
             }
-            if (l_item < items) tokens();
         }
         l_stage = l_stage + 1 == ST ? 0 : l_stage + 1;
         cp_async_commit();
     };
     for (int i = 0; i < ST - 1; ++i) issue();
     int stg = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const Item it = decode(item);
-        uint16_t *dbias = it.is_a ? nullptr : p.dbias[it.s];
+    for (; at.id < p.L; next(at)) {
+        const bool is_a = at.q >= p.S;
+        const int s = is_a ? at.q - p.S : at.q, seg = seg_of[at.id];
+        const int steps = seg >= 0 ? (tab.count[seg] + BW_TOK - 1) / BW_TOK : 1;
+        const int lo = is_a ? 0 : p.off[s], n = is_a ? p.H : p.n[s];
+        uint16_t *dbias = is_a ? nullptr : p.dbias[s];
         float acc[MI][NI][4] = {}, ones[MI][4] = {};
-        for (int k = 0; k < it.steps; ++k) {
+        for (int k = 0; k < steps; ++k) {
             cp_async_wait<ST - 2>();
             __syncthreads();
             issue();
@@ -523,19 +544,19 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 const int m = wm * (BW_COLS / WM) + i * 16 + gq, c = wn * (RP / WN) + 8 * j + 2 * t;
-                if (!it.is_a) {
+                if (!is_a) {
                     *reinterpret_cast<uint32_t *>(stage + tile_at<CPR, BW_COLS>(m, c / 8) + c % 8 * 2) =
                         pack_bf16x2(acc[i][j][0], acc[i][j][1]);
                     *reinterpret_cast<uint32_t *>(stage + tile_at<CPR, BW_COLS>(m + 8, c / 8) + c % 8 * 2) =
                         pack_bf16x2(acc[i][j][2], acc[i][j][3]);
                 } else {
-                    uint16_t *at = reinterpret_cast<uint16_t *>(stage) + c * BW_W_LD + m;
+                    uint16_t *to_m = reinterpret_cast<uint16_t *>(stage) + c * BW_W_LD + m;
                     const uint32_t v0 = pack_bf16x2(p.scale * acc[i][j][0], p.scale * acc[i][j][1]);
                     const uint32_t v1 = pack_bf16x2(p.scale * acc[i][j][2], p.scale * acc[i][j][3]);
-                    at[0] = uint16_t(v0 & 0xFFFFu);
-                    at[BW_W_LD] = uint16_t(v0 >> 16);
-                    at[8] = uint16_t(v1 & 0xFFFFu);
-                    at[BW_W_LD + 8] = uint16_t(v1 >> 16);
+                    to_m[0] = uint16_t(v0 & 0xFFFFu);
+                    to_m[BW_W_LD] = uint16_t(v0 >> 16);
+                    to_m[8] = uint16_t(v1 & 0xFFFFu);
+                    to_m[BW_W_LD + 8] = uint16_t(v1 >> 16);
                 }
             }
         if (dbias != nullptr && wn == 0 && t == 0) {
@@ -543,28 +564,28 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int row = it.c0 + wm * (BW_COLS / WM) + i * 16 + gq + 8 * half - it.lo;
-                    if (row >= 0 && row < it.n)
-                        dbias[int64_t(it.id) * it.n + row] =
+                    const int row = at.c0 + wm * (BW_COLS / WM) + i * 16 + gq + 8 * half - lo;
+                    if (row >= 0 && row < n)
+                        dbias[int64_t(at.id) * n + row] =
                             uint16_t(pack_bf16x2(ones[i][2 * half], 0.0f) & 0xFFFFu);
                 }
         }
         __syncthreads();
-        if (!it.is_a) {
-            uint16_t *out = p.db[it.s];
+        if (!is_a) {
+            uint16_t *out = p.db[s];
             if (out != nullptr) {
                 for (int i = tid; i < BW_COLS * CPR; i += BW_THREADS) {
-                    const int m = i / CPR, c = i % CPR, row = it.c0 + m - it.lo;
-                    if (row >= 0 && row < it.n && c * 8 < p.r)
-                        *reinterpret_cast<uint4 *>(out + (int64_t(it.id) * it.n + row) * p.r + c * 8) =
+                    const int m = i / CPR, c = i % CPR, row = at.c0 + m - lo;
+                    if (row >= 0 && row < n && c * 8 < p.r)
+                        *reinterpret_cast<uint4 *>(out + (int64_t(at.id) * n + row) * p.r + c * 8) =
                             *reinterpret_cast<const uint4 *>(stage + tile_at<CPR, BW_COLS>(m, c));
                 }
             }
         } else {
-            uint16_t *out = p.da[it.s] + int64_t(it.id) * p.r * p.H + it.c0;
+            uint16_t *out = p.da[s] + int64_t(at.id) * p.r * p.H + at.c0;
             for (int i = tid; i < 16 * p.r; i += BW_THREADS) {
                 const int c = i >> 4, m = (i & 15) * 8;
-                if (it.c0 + m < p.H)
+                if (at.c0 + m < p.H)
                     *reinterpret_cast<uint4 *>(out + int64_t(c) * p.H + m) =
                         *reinterpret_cast<const uint4 *>(reinterpret_cast<uint16_t *>(stage) + c * BW_W_LD + m);
             }
