@@ -132,13 +132,65 @@ template <int RP>
 constexpr int gram_step() { return 4096 / RP; }     // of the long side, a tile of 4096 entries
 
 template <bool F32>
-constexpr int gram_stages() { return F32 ? 3 : 5; }
+constexpr int gram_stages() { return F32 ? 4 : 5; }
 
 template <int RP, bool F32>
-constexpr int gram_smem()
-{
-    return 4096 * (gram_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 0)) + RP * RP * 4;
-}
+constexpr int gram_smem() { return 4096 * gram_stages<F32>() * (F32 ? 4 : 2) + RP * RP * 4; }
+
+// An fp32 tile of 4096 entries.  Fragments are read from it as they are and
+// split in registers (split in shared memory and read with ldmatrix, a
+// 16 x 32 block took 64 passes over the banks in place of 16: 38 in place of
+// 24 us for 64 x 11008 x 32).  A
+// warp's part: K16 x RP of 16-byte pieces, placed so that the lanes of one
+// load meet no bank twice.
+template <int RP, bool TALL>
+struct GramRing {
+    static constexpr int BYTES = 4096 * 4;
+    static constexpr int KW = 4096 / RP / 8;                       // of K, a warp's
+    static constexpr int PPR = (TALL ? RP : KW) / 4;               // pieces of a row
+    static constexpr int PER = 4096 / 4 / OR_THREADS;              // pieces of a lane
+    __device__ __forceinline__ static int spot(int row, int ch)
+    {
+        if constexpr (TALL && PPR == 8) return row * 8 + (ch ^ (row & 6));
+        else if constexpr (TALL) return ((row >> 1) + (row & 1) * (KW / 2)) * 4 + (ch ^ (row >> 1 & 2));
+        else if constexpr (PPR == 8) return row * 8 + (ch ^ (row & 3) << 1);
+        else return row * 4 + (ch ^ (row & 2));
+    }
+    __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
+                                                 int col0)
+    {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (lane + 32 * i) / PPR, ch = (lane + 32 * i) % PPR;
+            const int row = row0 + (TALL ? warp * KW : 0) + r, col = col0 + (TALL ? 0 : warp * KW) + ch * 4;
+            const bool ok = row < p.rows && col < p.cols;
+            cp_async16(smem_addr(stage + warp * (BYTES / 8) + spot(r, ch) * 16),
+                       static_cast<const float *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
+        }
+    }
+    // The A fragment (16 x 16) at (m0, k0) of the warp's part, as two terms.
+    __device__ __forceinline__ static void frag(const uint8_t *part, int m0, int k0, uint32_t (&hi)[4],
+                                                uint32_t (&lo)[4])
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int m = m0 + g + 8 * (q & 1), k = k0 + 2 * t + 8 * (q >> 1);
+            float x, y;
+            if constexpr (TALL) {
+                x = *reinterpret_cast<const float *>(part + spot(k, m >> 2) * 16 + (m & 3) * 4);
+                y = *reinterpret_cast<const float *>(part + spot(k + 1, m >> 2) * 16 + (m & 3) * 4);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(part + spot(m, k >> 2) * 16 + (k & 3) * 4);
+                x = v.x;
+                y = v.y;
+            }
+            hi[q] = pack_bf16x2(x, y);
+            lo[q] = pack_bf16x2(x - bf16_lo(hi[q]), y - bf16_hi(hi[q]));
+        }
+    }
+};
 
 // Each block sums over its run of units; a warp takes an eighth of a unit's
 // K, the 8-column blocks on and right of the diagonal.  TALL: U is [n][r]
@@ -149,10 +201,9 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
     constexpr int KS = gram_step<RP>(), ST = gram_stages<F32>();
     constexpr int ROWS = TALL ? KS : RP, CPR = (TALL ? RP : KS) / 8;     // of the tile
     constexpr int MI = RP / 16, NI = RP / 8;
-    using Ring = TileRing<ROWS, CPR, TALL, F32>;
+    using Ring = std::conditional_t<F32, GramRing<RP, TALL>, TileRing<ROWS, CPR, TALL, false>>;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *terms = smem + ST * Ring::BYTES;                       // fp32: the converted tile
-    float *sum = reinterpret_cast<float *>(terms + (F32 ? 2 * Ring::TERM : 0));
+    float *sum = reinterpret_cast<float *>(smem + ST * Ring::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5;
     pdl_wait();
     const int64_t first = unit_begin(p, blockIdx.x), end = unit_begin(p, blockIdx.x + 1);
@@ -170,40 +221,32 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
     int stage = 0;
     for (; run.left > 0; run.next(p.units, size)) {
         cp_async_wait<ST - 2>();
-        uint32_t hi = smem_addr(smem + stage * Ring::BYTES);
+        const uint8_t *tile = smem + stage * Ring::BYTES;
         __syncwarp();
-        if constexpr (F32) {
-            Ring::convert(smem + stage * Ring::BYTES, terms);
-            hi = smem_addr(terms);
-            __syncwarp();
-        }
         issue(stage == 0 ? ST - 1 : stage - 1);
         stage = stage + 1 == ST ? 0 : stage + 1;
+        // the rows of B are those of A, so its fragments are A's registers
 #pragma unroll
-        for (int kk = warp * (KS / 8); kk < (warp + 1) * (KS / 8); kk += 16) {
+        for (int kk = 0; kk < KS / 8; kk += 16) {
             uint32_t a[MI][4], al[MI][4];
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                frag_a<CPR, ROWS, !TALL>(hi, 16 * i, kk, a[i]);
-                if constexpr (F32) frag_a<CPR, ROWS, !TALL>(hi + Ring::TERM, 16 * i, kk, al[i]);
+                if constexpr (F32) Ring::frag(tile + warp * (Ring::BYTES / 8), 16 * i, kk, a[i], al[i]);
+                else frag_a<CPR, ROWS, !TALL>(smem_addr(tile), 16 * i, warp * (KS / 8) + kk, a[i]);
             }
 #pragma unroll
-            for (int j = 0; j < NI; j += 2) {
-                uint32_t b[4], bl[4];
-                frag_b<CPR, ROWS, !TALL>(hi, kk, 8 * j, b);
-                if constexpr (F32) frag_b<CPR, ROWS, !TALL>(hi + Ring::TERM, kk, 8 * j, bl);
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int i = 0; i <= j / 2; ++i) {
-                    mma_bf16_16816(acc[i][j], a[i], b[0], b[1]);
-                    mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
-                    if constexpr (F32) {
-                        mma_bf16_16816(acc[i][j], al[i], b[0], b[1]);
-                        mma_bf16_16816(acc[i][j + 1], al[i], b[2], b[3]);
-                        mma_bf16_16816(acc[i][j], a[i], bl[0], bl[1]);
-                        mma_bf16_16816(acc[i][j + 1], a[i], bl[2], bl[3]);
+                for (int j = i; j < MI; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float(&d)[4] = acc[i][2 * j + h];
+                        mma_bf16_16816(d, a[i], a[j][h], a[j][h + 2]);
+                        if constexpr (F32) {
+                            mma_bf16_16816(d, al[i], a[j][h], a[j][h + 2]);
+                            mma_bf16_16816(d, a[i], al[j][h], al[j][h + 2]);
+                        }
                     }
-                }
-            }
         }
         if (run.left > 1 && run.k + 1 != p.units) continue;
         // the matrix or the run ends: the warps' sums over K, one after the
