@@ -20,6 +20,8 @@
 // lora_ortho_tc.cu: ranks 33 to 128, on tcgen05.
 #include <math.h>
 
+#include <type_traits>
+
 #include "lora_ortho.cuh"
 
 namespace lora {
@@ -31,9 +33,8 @@ namespace lora {
 // several tiles ahead, neighbouring lanes copying neighbouring pieces (a
 // lane copying both halves of its eight fp32 entries halved the rate: every
 // 32-byte sector was asked for twice).  A bf16 tile lands swizzled, ready
-// for ldmatrix.  An fp32 tile lands as it is and is turned into two bf16
-// terms in the warp's part of another tile.  SPLIT_ROWS: a warp's part is an
-// eighth of the tile's rows, else of its columns.
+// for ldmatrix.  SPLIT_ROWS: a warp's part is an eighth of the tile's rows,
+// else of its columns.
 
 // A walk over the tiles of the stacked matrices, without divisions in the
 // loop (64-bit ones took half of its instructions).
@@ -57,11 +58,10 @@ struct TileWalk {
     }
 };
 
-template <int ROWS, int CPR, bool SPLIT_ROWS, bool F32>
+template <int ROWS, int CPR, bool SPLIT_ROWS>
 struct TileRing {
     static constexpr int PER = ROWS * CPR / OR_THREADS;            // chunks of a lane
-    static constexpr int BYTES = ROWS * CPR * (F32 ? 32 : 16);
-    static constexpr int TERM = ROWS * CPR * 16;                   // one bf16 term
+    static constexpr int BYTES = ROWS * CPR * 16;
     static_assert(PER >= 1 && (SPLIT_ROWS ? ROWS : CPR) % 8 == 0, "an eighth a warp");
 
     __device__ __forceinline__ static void place(int i, int &row, int &ch)
@@ -78,50 +78,69 @@ struct TileRing {
     __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
                                                  int col0)
     {
-        if constexpr (F32) {
-            constexpr int PPR = SPLIT_ROWS ? CPR * 2 : CPR / 4;    // pieces a row of the warp's part
-            const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-            for (int i = 0; i < 2 * PER; ++i) {
-                const int at = lane + 32 * i;
-                const int row = row0 + (SPLIT_ROWS ? warp * (ROWS / 8) : 0) + at / PPR;
-                const int col = col0 + (SPLIT_ROWS ? 0 : warp * CPR) + at % PPR * 4;
-                const bool ok = row < p.rows && col < p.cols;
-                cp_async16(smem_addr(stage + piece(warp, at)),
-                           static_cast<const float *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                int r, ch;
-                place(i, r, ch);
-                const int row = row0 + r, col = col0 + ch * 8;
-                const bool ok = row < p.rows && col < p.cols;
-                cp_async16(smem_addr(stage + tile_at<CPR, ROWS>(r, ch)),
-                           static_cast<const uint16_t *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
-            }
+        for (int i = 0; i < PER; ++i) {
+            int r, ch;
+            place(i, r, ch);
+            const int row = row0 + r, col = col0 + ch * 8;
+            const bool ok = row < p.rows && col < p.cols;
+            cp_async16(smem_addr(stage + tile_at<CPR, ROWS>(r, ch)),
+                       static_cast<const uint16_t *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
         }
     }
-    // Where a warp's 16-byte piece lies: the even ones first, so that lanes
-    // reading neighbouring pairs meet no bank conflicts.
-    __device__ __forceinline__ static int piece(int warp, int at)
+};
+
+// An fp32 tile; a warp's part of it has ROWS rows of PPR 16-byte pieces.
+// Fragments are read from it as they are and split in registers: split in
+// shared memory and read with ldmatrix, a 16 x 32 block took 64 passes over
+// the banks in place of 16 (64 matrices of 11008 x 32: gram 38 us in place
+// of 24, apply 30 in place of 22).  K_ROWS: the rows are K.  The pieces lie
+// so that the lanes of one load meet no bank twice.
+template <int ROWS, int PPR, bool SPLIT_ROWS, bool K_ROWS>
+struct FloatRing {
+    static constexpr int PART = ROWS * PPR * 16, BYTES = 8 * PART;
+    static constexpr int PER = ROWS * PPR / 32;                    // pieces of a lane
+    __device__ __forceinline__ static int spot(int row, int ch)
     {
-        return (warp * 64 * PER + (at & 1) * 32 * PER + (at >> 1)) * 16;
+        if constexpr (K_ROWS && PPR == 8) return row * 8 + (ch ^ (row & 6));
+        else if constexpr (K_ROWS) return ((row >> 1) + (row & 1) * (ROWS / 2)) * 4 + (ch ^ (row >> 1 & 2));
+        else if constexpr (PPR == 8) return row * 8 + (ch ^ (row & 3) << 1);
+        else return row * 4 + (ch ^ (row & 2));
     }
-    // fp32: a landed stage as terms of `tile`.
-    __device__ __forceinline__ static void convert(const uint8_t *stage, uint8_t *tile)
+    __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
+                                                 int col0)
     {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const uint8_t *src = stage + piece(warp, 2 * (lane + 32 * i));
-            const Chunk k = split_chunk(*reinterpret_cast<const float4 *>(src),
-                                        *reinterpret_cast<const float4 *>(src + 32 * PER * 16));
-            int row, ch;
-            place(i, row, ch);
-            uint8_t *at = tile + tile_at<CPR, ROWS>(row, ch);
-            *reinterpret_cast<uint4 *>(at) = k.hi;
-            *reinterpret_cast<uint4 *>(at + TERM) = k.lo;
+            const int r = (lane + 32 * i) / PPR, ch = (lane + 32 * i) % PPR;
+            const int row = row0 + (SPLIT_ROWS ? warp * ROWS : 0) + r;
+            const int col = col0 + (SPLIT_ROWS ? 0 : warp * PPR * 4) + ch * 4;
+            const bool ok = row < p.rows && col < p.cols;
+            cp_async16(smem_addr(stage + warp * PART + spot(r, ch) * 16),
+                       static_cast<const float *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
+        }
+    }
+    // The 16 x 16 block at (m0, k0) of the warp's part as an A fragment, two
+    // terms.  As B it is the same registers: [h], [h + 2] for columns 8 h on.
+    __device__ __forceinline__ static void frag(const uint8_t *part, int m0, int k0, uint32_t (&hi)[4],
+                                                uint32_t (&lo)[4])
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int m = m0 + g + 8 * (q & 1), k = k0 + 2 * t + 8 * (q >> 1);
+            float x, y;
+            if constexpr (K_ROWS) {
+                x = *reinterpret_cast<const float *>(part + spot(k, m >> 2) * 16 + (m & 3) * 4);
+                y = *reinterpret_cast<const float *>(part + spot(k + 1, m >> 2) * 16 + (m & 3) * 4);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(part + spot(m, k >> 2) * 16 + (k & 3) * 4);
+                x = v.x;
+                y = v.y;
+            }
+            hi[q] = pack_bf16x2(x, y);
+            lo[q] = pack_bf16x2(x - bf16_lo(hi[q]), y - bf16_hi(hi[q]));
         }
     }
 };
@@ -137,61 +156,6 @@ constexpr int gram_stages() { return F32 ? 4 : 5; }
 template <int RP, bool F32>
 constexpr int gram_smem() { return 4096 * gram_stages<F32>() * (F32 ? 4 : 2) + RP * RP * 4; }
 
-// An fp32 tile of 4096 entries.  Fragments are read from it as they are and
-// split in registers (split in shared memory and read with ldmatrix, a
-// 16 x 32 block took 64 passes over the banks in place of 16: 38 in place of
-// 24 us for 64 x 11008 x 32).  A
-// warp's part: K16 x RP of 16-byte pieces, placed so that the lanes of one
-// load meet no bank twice.
-template <int RP, bool TALL>
-struct GramRing {
-    static constexpr int BYTES = 4096 * 4;
-    static constexpr int KW = 4096 / RP / 8;                       // of K, a warp's
-    static constexpr int PPR = (TALL ? RP : KW) / 4;               // pieces of a row
-    static constexpr int PER = 4096 / 4 / OR_THREADS;              // pieces of a lane
-    __device__ __forceinline__ static int spot(int row, int ch)
-    {
-        if constexpr (TALL && PPR == 8) return row * 8 + (ch ^ (row & 6));
-        else if constexpr (TALL) return ((row >> 1) + (row & 1) * (KW / 2)) * 4 + (ch ^ (row >> 1 & 2));
-        else if constexpr (PPR == 8) return row * 8 + (ch ^ (row & 3) << 1);
-        else return row * 4 + (ch ^ (row & 2));
-    }
-    __device__ __forceinline__ static void issue(const OrthoArgs &p, uint8_t *stage, int64_t mat, int row0,
-                                                 int col0)
-    {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (lane + 32 * i) / PPR, ch = (lane + 32 * i) % PPR;
-            const int row = row0 + (TALL ? warp * KW : 0) + r, col = col0 + (TALL ? 0 : warp * KW) + ch * 4;
-            const bool ok = row < p.rows && col < p.cols;
-            cp_async16(smem_addr(stage + warp * (BYTES / 8) + spot(r, ch) * 16),
-                       static_cast<const float *>(p.u) + (ok ? mat + int64_t(row) * p.cols + col : 0), ok);
-        }
-    }
-    // The A fragment (16 x 16) at (m0, k0) of the warp's part, as two terms.
-    __device__ __forceinline__ static void frag(const uint8_t *part, int m0, int k0, uint32_t (&hi)[4],
-                                                uint32_t (&lo)[4])
-    {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int m = m0 + g + 8 * (q & 1), k = k0 + 2 * t + 8 * (q >> 1);
-            float x, y;
-            if constexpr (TALL) {
-                x = *reinterpret_cast<const float *>(part + spot(k, m >> 2) * 16 + (m & 3) * 4);
-                y = *reinterpret_cast<const float *>(part + spot(k + 1, m >> 2) * 16 + (m & 3) * 4);
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(part + spot(m, k >> 2) * 16 + (k & 3) * 4);
-                x = v.x;
-                y = v.y;
-            }
-            hi[q] = pack_bf16x2(x, y);
-            lo[q] = pack_bf16x2(x - bf16_lo(hi[q]), y - bf16_hi(hi[q]));
-        }
-    }
-};
-
 // Each block sums over its run of units; a warp takes an eighth of a unit's
 // K, the 8-column blocks on and right of the diagonal.  TALL: U is [n][r]
 // (its rows are K), else [r][n].
@@ -201,7 +165,8 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
     constexpr int KS = gram_step<RP>(), ST = gram_stages<F32>();
     constexpr int ROWS = TALL ? KS : RP, CPR = (TALL ? RP : KS) / 8;     // of the tile
     constexpr int MI = RP / 16, NI = RP / 8;
-    using Ring = std::conditional_t<F32, GramRing<RP, TALL>, TileRing<ROWS, CPR, TALL, false>>;
+    using Ring = std::conditional_t<F32, FloatRing<TALL ? KS / 8 : RP, (TALL ? RP : KS / 8) / 4, TALL, TALL>,
+                                    TileRing<ROWS, CPR, TALL>>;
     extern __shared__ __align__(128) uint8_t smem[];
     float *sum = reinterpret_cast<float *>(smem + ST * Ring::BYTES);
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -231,7 +196,7 @@ __global__ void __launch_bounds__(OR_THREADS, 3) gram_kernel(const OrthoArgs p)
             uint32_t a[MI][4], al[MI][4];
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                if constexpr (F32) Ring::frag(tile + warp * (Ring::BYTES / 8), 16 * i, kk, a[i], al[i]);
+                if constexpr (F32) Ring::frag(tile + warp * Ring::PART, 16 * i, kk, a[i], al[i]);
                 else frag_a<CPR, ROWS, !TALL>(smem_addr(tile), 16 * i, warp * (KS / 8) + kk, a[i]);
             }
 #pragma unroll
@@ -400,7 +365,7 @@ constexpr int apply_stages() { return F32 ? 3 : 4; }
 template <int RP, bool F32>
 constexpr int apply_smem()
 {
-    return 2 * RP * RP * 2 + RP * OR_LONG * (apply_stages<F32>() * (F32 ? 4 : 2) + (F32 ? 4 : 2));
+    return 2 * RP * RP * 2 + RP * OR_LONG * (apply_stages<F32>() * (F32 ? 4 : 2) + 2);
 }
 
 // Each block takes a run of tiles of the stacked matrices: out = P U (or U
@@ -412,7 +377,8 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
     constexpr int ROWS = TALL ? OR_LONG : RP, COLS = TALL ? RP : OR_LONG;
     constexpr int CPR = COLS / 8, PCPR = RP / 8, ST = apply_stages<F32>();
     constexpr int MI = TALL ? 1 : RP / 16, NI = TALL ? RP / 8 : 2, KK = RP / 16;
-    using Ring = TileRing<ROWS, CPR, TALL, F32>;
+    using Out = TileRing<ROWS, CPR, TALL>;
+    using Ring = std::conditional_t<F32, FloatRing<TALL ? 16 : RP, TALL ? RP / 4 : 4, TALL, !TALL>, Out>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *ring = smem + 2 * RP * RP * 2, *tile_buf = ring + ST * Ring::BYTES;
     const uint32_t sp = smem_addr(smem);
@@ -459,37 +425,40 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
         }
         cp_async_wait<ST - 2>();
         __syncwarp();                          // and the last tile's output has left
-        uint32_t su = smem_addr(ring + stage * Ring::BYTES);
-        if constexpr (F32) {
-            Ring::convert(ring + stage * Ring::BYTES, tile_buf);
-            su = smem_addr(tile_buf);
-            __syncwarp();
-        }
+        const uint8_t *u_tile = ring + stage * Ring::BYTES;
         issue(stage == 0 ? ST - 1 : stage - 1);
         stage = stage + 1 == ST ? 0 : stage + 1;
         float acc[MI][NI][4] = {};
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
-            // a term of U's fragments (hi, then lo) with P's terms
+            uint32_t u[2][4];                  // U's terms
+            if constexpr (F32) {
+                Ring::frag(u_tile + warp * Ring::PART, 0, 16 * k, u[0], u[1]);
+            } else if constexpr (TALL) {
+                frag_a<CPR, ROWS, true>(smem_addr(u_tile), m0, 16 * k, u[0]);
+            } else {
+                uint32_t b[4];
+                frag_b<CPR, ROWS, false>(smem_addr(u_tile), 16 * k, n0, b);
+                u[0][0] = b[0];
+                u[0][2] = b[1];
+                u[0][1] = b[2];
+                u[0][3] = b[3];
+            }
 #pragma unroll
-            for (int ut = 0; ut < (F32 ? 2 : 1); ++ut) {
-                uint32_t u[4];
-                if constexpr (TALL) frag_a<CPR, ROWS, true>(su + ut * Ring::TERM, m0, 16 * k, u);
-                else frag_b<CPR, ROWS, false>(su + ut * Ring::TERM, 16 * k, n0, u);
+            for (int ut = 0; ut < (F32 ? 2 : 1); ++ut)
 #pragma unroll
                 for (int t = 0; t < (ut == 0 ? 2 : 1); ++t)
 #pragma unroll
                     for (int i = 0; i < RP / 16; ++i) {
                         const uint32_t(&q)[4] = pf[t][k][i];
                         if constexpr (TALL) {
-                            mma_bf16_16816(acc[0][2 * i], u, q[0], q[1]);
-                            mma_bf16_16816(acc[0][2 * i + 1], u, q[2], q[3]);
+                            mma_bf16_16816(acc[0][2 * i], u[ut], q[0], q[1]);
+                            mma_bf16_16816(acc[0][2 * i + 1], u[ut], q[2], q[3]);
                         } else {
-                            mma_bf16_16816(acc[i][0], q, u[0], u[1]);
-                            mma_bf16_16816(acc[i][1], q, u[2], u[3]);
+                            mma_bf16_16816(acc[i][0], q, u[ut][0], u[ut][2]);
+                            mma_bf16_16816(acc[i][1], q, u[ut][1], u[ut][3]);
                         }
                     }
-            }
         }
         // through the warp's part of the tile, so that rows are written 16
         // bytes at a time
@@ -507,9 +476,9 @@ __global__ void __launch_bounds__(OR_THREADS, 3) apply_kernel(const OrthoArgs p)
             }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < Ring::PER; ++i) {
+        for (int i = 0; i < Out::PER; ++i) {
             int row, ch;
-            Ring::place(i, row, ch);
+            Out::place(i, row, ch);
             const int gr = TALL ? tile * OR_LONG + row : row;
             const int gc = (TALL ? 0 : tile * OR_LONG) + ch * 8;
             if (gr < p.rows && gc < p.cols)
