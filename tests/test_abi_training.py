@@ -11,7 +11,7 @@ PTR = 0x100000          # never read on the host
 
 @pytest.fixture(scope="module")
 def lib():
-    from expand_gemm_gb300 import build as pkg_build
+    from expand_gemm_gb300.build import build as pkg_build
     from expand_gemm_gb300 import _lib
     pkg_build()
     return _lib.load()
