@@ -470,8 +470,10 @@ def _rows(t: torch.Tensor, name: str):
     if t.dim() != 2:
         t = t.view(-1, t.shape[-1])
     n, c = t.shape
-    ld = t.stride(0)
-    if (c > 1 and t.stride(1) != 1) or (n > 1 and ld < c):
+    ld, unit = t.stride()
+    if unit == 1 and ld >= c:
+        return n, c, ld
+    if (c > 1 and unit != 1) or (n > 1 and ld < c):
         raise ValueError("%s needs contiguous rows that do not overlap" % name)
     return n, c, max(ld, c)
 
@@ -559,17 +561,23 @@ def _stacks(ws, name: str, index: int):
     shapes, and the array of their pointers."""
     if isinstance(ws, torch.Tensor):
         ws = (ws,)
+    shapes, ptrs = [], []
     try:
-        ok = all([w.dtype is _BF16 and w.get_device() == index and w.dim() == 3 and w.is_contiguous()
-                  for w in ws])
+        for w in ws:
+            if w.dtype is not _BF16 or w.get_device() != index or w.dim() != 3 or not w.is_contiguous():
+                break
+            shapes.append(w.shape)
+            ptrs.append(w.data_ptr())
+        ok = len(ptrs) == len(ws)
     except AttributeError:
         ok = False
     if not ok:
         ws = _weights(ws, name)
         _all(index, *((w, _BF16, "%s[%d]" % (name, i)) for i, w in enumerate(ws)))
-    if not 1 <= len(ws) <= LORA_MAX_SLICES:
+        shapes, ptrs = [w.shape for w in ws], [w.data_ptr() for w in ws]
+    if not 1 <= len(ptrs) <= LORA_MAX_SLICES:
         raise ValueError("%s must hold 1 to %d tensors" % (name, LORA_MAX_SLICES))
-    return [w.shape for w in ws], _PTRS[len(ws)](*[w.data_ptr() for w in ws])
+    return shapes, _PTRS[len(ptrs)](*ptrs)
 
 
 def _grads(grads, name: str, like, index: int):
@@ -581,16 +589,22 @@ def _grads(grads, name: str, like, index: int):
         grads = (grads,)
     if len(grads) != len(like):
         raise ValueError("%s needs one entry per slice" % name)
-    for i, (g, shape) in enumerate(zip(grads, like)):
+    ptrs = []
+    for g, shape in zip(grads, like):
         if g is None:
+            ptrs.append(None)
             continue
-        if not isinstance(g, torch.Tensor) or g.dtype is not _BF16 or g.get_device() != index:
-            _all(index, (g, _BF16, "%s[%d]" % (name, i)))
-        s = g.shape
-        if (s != shape and (g.numel() != math.prod(shape) or s[0] != shape[0] or s[-1] != shape[-1])) \
-                or not g.is_contiguous():
-            raise ValueError("%s[%d] must be a contiguous %s tensor" % (name, i, list(shape)))
-    return _PTRS[len(grads)](*[None if g is None else g.data_ptr() for g in grads])
+        try:
+            ok = g.dtype is _BF16 and g.get_device() == index and g.shape == shape and g.is_contiguous()
+        except AttributeError:
+            ok = False
+        if not ok:
+            _all(index, (g, _BF16, "%s[%d]" % (name, len(ptrs))))
+            s = g.shape
+            if g.numel() != math.prod(shape) or s[0] != shape[0] or s[-1] != shape[-1] or not g.is_contiguous():
+                raise ValueError("%s[%d] must be a contiguous %s tensor" % (name, len(ptrs), list(shape)))
+        ptrs.append(g.data_ptr())
+    return _PTRS[len(ptrs)](*ptrs)
 
 
 def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor, lora_a_stacked,
@@ -608,7 +622,7 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     biases, overwritten; adapters without tokens get zeros."""
     index = meta.no_lora_flag.get_device()
     try:
-        ok = (dy.dtype is _BF16 and x.dtype is _BF16 and buffer.dtype is _F32 and dy.get_device() == index
+        ok = (index >= 0 and dy.dtype is _BF16 and x.dtype is _BF16 and buffer.dtype is _F32 and dy.get_device() == index
               and x.get_device() == index and buffer.get_device() == index and _is(dx, _BF16, index)
               and _is(workspace, _U8, index))
     except AttributeError:
