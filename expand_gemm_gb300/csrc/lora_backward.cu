@@ -171,58 +171,90 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
     }
 }
 
-// The partial sums of a tile, added in the order of the CTAs and rounded: g;
-// and u beside it.
+// The partial sums of a tile, added in a fixed order and rounded: g; and u
+// beside it.  A block takes 16 tokens x 16 columns at a time, a quarter of
+// the slots each 64 threads: with few tiles there are many slots of each (a
+// block a tile took 53 us at rank 128, 512 tokens, widths 4096, 1024, 1024;
+// this 7).
 template <int RP>
 __global__ void __launch_bounds__(BW_THREADS) join_u_kernel(const __grid_constant__ BackwardArgs p)
 {
+    constexpr int PARTS = RP / 4, TEAMS = BW_THREADS / 64;
     extern __shared__ __align__(16) int join_tab[];
+    __shared__ float4 s_sum[TEAMS - 1][64];
+    __shared__ __align__(16) uint16_t s_turned[2][16][16];
     pdl_wait();
     int tiles;
     const SegTab tab = load_tab(p, join_tab, tiles);
     const int per_tile = p.step_end[p.S - 1];
     const int64_t total = int64_t(tiles) * per_tile;
     const int ctas = int(min(int64_t(p.u_ctas), total));
-    for (int item = blockIdx.x; item < tiles * p.S; item += gridDim.x) {
+    const int team = threadIdx.x >> 6, t = threadIdx.x & 63;
+    for (int unit = blockIdx.x; unit < tiles * p.S * PARTS; unit += gridDim.x) {
+        const int item = unit / PARTS, part = unit % PARTS;
         const int tile = item / p.S, s = item % p.S;
-        const int seg = find_segment(tab.tile, p.nbins, tile);
-        const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
-        const int nrows = min(BW_TOK, tab.start[seg] + tab.count[seg] - row0);
+        const int row = (part & 3) * 16 + (t >> 2), col = (part >> 2) * 16 + (t & 3) * 4;
         const int64_t first = int64_t(tile) * per_tile + (s > 0 ? p.step_end[s - 1] : 0);
         const int c_lo = step_cta(total, first, ctas);
-        const int c_hi = step_cta(total, int64_t(tile) * per_tile + p.step_end[s] - 1, ctas);
-        const int64_t out0 = (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
-        for (int i = threadIdx.x; i < BW_TOK * RP / 4; i += BW_THREADS) {
-            const int row = i * 4 / RP, col = i * 4 % RP;
-            float4 f = make_float4(0, 0, 0, 0), v = f;
-            if (row < nrows && col < p.r) {
-                const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
-                if (tok >= 0)
-                    f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
-            }
+        const int slots = step_cta(total, int64_t(tile) * per_tile + p.step_end[s] - 1, ctas) + 1 - c_lo;
+        const float *from = p.part + (int64_t(c_lo) + item) * BW_TOK * RP + row * RP + col;
+        float4 v = make_float4(0, 0, 0, 0);
+        const int end = slots * (team + 1) / TEAMS;
 #pragma unroll 4
-            for (int c = c_lo; c <= c_hi; ++c) {
-                const float4 x = reinterpret_cast<const float4 *>(p.part + (int64_t(c) + item) * BW_TOK * RP)[i];
+        for (int c = slots * team / TEAMS; c < end; ++c) {
+            const float4 x = *reinterpret_cast<const float4 *>(from + int64_t(c) * BW_TOK * RP);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        if (team > 0) s_sum[team - 1][t] = v;
+        uint2 uv = make_uint2(0u, 0u);
+        if (team == 1) {
+            const int seg = find_segment(tab.tile, p.nbins, tile);
+            const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
+            if (row < tab.start[seg] + tab.count[seg] - row0 && col < p.r) {
+                const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
+                if (tok >= 0) {
+                    const float4 f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
+                    uv = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                }
+            }
+        }
+        __syncthreads();
+        const int64_t out0 = (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+        if (team == 0) {
+#pragma unroll
+            for (int i = 0; i < TEAMS - 1; ++i) {
+                const float4 x = s_sum[i][t];
                 v.x += x.x;
                 v.y += x.y;
                 v.z += x.z;
                 v.w += x.w;
             }
-            const uint2 gv = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-            const uint2 uv = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
-            reinterpret_cast<uint2 *>(p.g + out0)[i] = gv;
-            if (p.ut != nullptr) {
-                uint16_t *gt = p.gt + out0 + col * BW_TOK + row, *ut = p.ut + out0 + col * BW_TOK + row;
-                const uint32_t a[2] = {gv.x, gv.y}, b[2] = {uv.x, uv.y};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    gt[e * BW_TOK] = uint16_t(a[e >> 1] >> (16 * (e & 1)));
-                    ut[e * BW_TOK] = uint16_t(b[e >> 1] >> (16 * (e & 1)));
-                }
-            } else {
-                reinterpret_cast<uint2 *>(p.u + out0)[i] = uv;
+            uv = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+        if (team == 0 || (team == 1 && p.ut == nullptr))
+            *reinterpret_cast<uint2 *>((team == 0 ? p.g : p.u) + out0 + row * RP + col) = uv;
+        if (p.ut != nullptr) {
+            // transposed: 32 bytes of 16 tokens for each column
+            if (team < 2) {
+                uint16_t(&at)[16][16] = s_turned[team];
+                const int y = t >> 2, x = (t & 3) * 4;
+                at[x][y] = uint16_t(uv.x & 0xFFFFu);
+                at[x + 1][y] = uint16_t(uv.x >> 16);
+                at[x + 2][y] = uint16_t(uv.y & 0xFFFFu);
+                at[x + 3][y] = uint16_t(uv.y >> 16);
+            }
+            __syncthreads();
+            if (team == 0) {
+                const int which = t >> 5, x = t >> 1 & 15, half = (t & 1) * 8;
+                *reinterpret_cast<uint4 *>((which == 0 ? p.gt : p.ut) + out0 + ((part >> 2) * 16 + x) * BW_TOK +
+                                           (part & 3) * 16 + half) =
+                    *reinterpret_cast<const uint4 *>(&s_turned[which][x][half]);
             }
         }
+        __syncthreads();
     }
 }
 
@@ -650,7 +682,7 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
         q.u_ctas = int(resident(us));
         e = launch_kernel(grad_u_kernel<RP>, dim3(unsigned(q.u_ctas)), dim3(BW_THREADS), us, st, q);
         if (e != cudaSuccess) return int(e);
-        const int64_t most = tiles * p.S, grid = most < 4 * sms ? most : 4 * sms;
+        const int64_t most = tiles * p.S * (RP / 4), grid = most < 8 * sms ? most : 8 * sms;
         e = launch_kernel(join_u_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), tab, st, q);
         if (e != cudaSuccess) return int(e);
     }

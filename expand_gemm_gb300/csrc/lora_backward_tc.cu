@@ -822,9 +822,12 @@ int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
     if (rp < 64 || !p.dy_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
-    // One CTA walks a tile's whole width: with fewer tiles than half the SMs
-    // the cluster kernel, which shares a tile's columns, is faster.
-    if (int64_t(p.T) / TC_ROWS * p.S < device_sm_count() / 2) return -1;
+    // One CTA walks a tile's whole width; the kernel of lora_backward.cu cuts
+    // the width among CTAs and joins.  Widths 4096, 1024, 1024 at rank 128:
+    // 1024 tokens (24 tiles) 26.6 us here, 23.5 there; 2048 (48 tiles) 27.2
+    // here, 34.3 there; width 4096 at rank 64: 16 tiles 24.9 and 18.8, 64
+    // tiles 27.6 and 35.8.
+    if (int64_t(p.T) / TC_ROWS * p.S < device_sm_count() / 4) return -1;
     static thread_local GradUTcArgs q;
     q.b = p;
     q.rp = rp;
