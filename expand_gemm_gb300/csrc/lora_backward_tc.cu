@@ -751,7 +751,12 @@ static int tc_configure()
 
 bool grad_w_tc_fits(const BackwardArgs &p, int rp)
 {
-    return rp >= 64 && p.dy_vec && p.x_vec && p.T >= 1 && p.rows * p.S * 2 < (int64_t(1) << 31);
+    if (rp < 64 || !p.dy_vec || !p.x_vec || p.T < 1 || p.rows * p.S * 2 >= (int64_t(1) << 31)) return false;
+    // At rank 64 a small batch is faster on mma.sync, whose CTAs are three an
+    // SM: 512 tokens x 4096 to 4096 8.8 us there, 10.7 here (32 adapters by
+    // token 19.5 and 25.2); 2048 tokens 24.4 there, 16.8 here.  At rank 128
+    // it never is (128 tokens 15.2 there, 13.0 here).
+    return rp > 64 || int64_t(p.T) / TC_ROWS * ((p.H + p.width) / TC_W_COLS) >= device_sm_count();
 }
 
 int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
@@ -802,6 +807,11 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
     if (rp < 64 || !p.dx_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
+    // Fewer items than SMs: smaller ones on mma.sync are faster.  4096 to
+    // 4096 at rank 64: 512 tokens 13.5 us here, 9.2 there (32 adapters by
+    // token 37 and 21), 2048 tokens 20.8 here, 22.6 there; at rank 128 14.1
+    // and 9.3, 21.8 and 25.4.
+    if (int64_t(p.T) / TC_ROWS * ((p.H + TC_X_COLS - 1) / TC_X_COLS) < device_sm_count()) return -1;
     static thread_local GradXTcArgs q;
     q.b = p;
     q.rp = rp;

@@ -114,6 +114,21 @@ def test_sizes(T, H, r, L, widths, runs, add):
     check(run(c, add), in_64_bits(c, add))
 
 
+# Large enough for every product to take the tensor-core kernels: tails of all
+# kinds, tiles of one adapter's few tokens, g kept beside the stages and not.
+LARGE = [
+    (3500, 1400, 128, 4, (136, 72, 64), 300), (5000, 1096, 40, 3, (200, 520), 1), (5000, 1096, 128, 3, (200, 520), 1),
+    (2600, 2056, 64, 3, (64,) * 8, 40), (2600, 2056, 128, 3, (64, 72, 80, 88, 8, 16, 24, 32), 1),
+    (2600, 2056, 96, 2, (72,) * 5, 100), (4000, 1288, 72, 40, (328,), 7), (3900, 1288, 128, 2, (1000, 24), 1300)]
+
+
+@pytest.mark.parametrize("T,H,r,L,widths,runs", LARGE)
+@pytest.mark.parametrize("add", [True, False])
+def test_large_sizes(T, H, r, L, widths, runs, add):
+    c = make(T, H, r, L, widths, T + H, runs=runs)
+    check(run(c, add), in_64_bits(c, add))
+
+
 @pytest.mark.parametrize("which", [("dx",), ("dA",), ("dB",), ("dbias",), ("dA", "dbias"), ()])
 def test_some_outputs_only(which):
     c = make(150, 136, 32, 4, (72, 131), 5)
