@@ -19,7 +19,7 @@
 // 16384 tokens in sequences, 8 of 64 adapters in use, rank 128, 8192 to
 // 8192, 1024, 1024: g 76 us (323 MB, 4.3 TB/s: 104 tiles of the wide slice
 // on 152 SMs), dx 108 us (506 MB, 4.7 TB/s: a tile's A, 192 KB for 256
-// columns, comes from L2 at 47 bytes a clock), dA and dB 231 us.  By token
+// columns, comes from L2 at 47 bytes a clock), dA and dB 208 us.  By token
 // the gathers bound all three (16384 tokens, 4096 to 4096, 1024, 1024: g 60
 // us in sequences, 209 by token; dA and dB 123 and 294).
 #include "lora_backward.cuh"
@@ -111,6 +111,8 @@ struct GradWTcArgs {
 };
 constexpr int TC_W_COLS = 256;           // columns of dy or x of an item
 constexpr int TC_W_THREADS = TC_THREADS + 128;
+constexpr int TC_W_SLOTS = 8;            // steps' tokens in shared memory
+constexpr int TC_W_AHEAD = 6;            // of them on their way
 
 // The gradients of an adapter without tokens: zeros, written by 128 threads
 // along the rows.
@@ -147,8 +149,8 @@ __device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int
 // leaves in whole rows.  With x or dy as A, on CTA pairs, rank 128 took 279 us
 // in place of 231.
 //
-// At 16384 tokens, hidden 8192, widths 8192, 1024, 1024, 64 adapters: 231 us
-// for the 1.27 GB that it moves, 5.5 TB/s (x is read once for each group of
+// At 16384 tokens, hidden 8192, widths 8192, 1024, 1024, 64 adapters: 208 us
+// for the 1.27 GB that it moves, 6.1 TB/s (x is read once for each group of
 // slices).
 //
 // Adapters are taken by falling token count, so that the CTAs' shares come
@@ -173,6 +175,11 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
     const int *seg_of = load_seg_of(p, tab, tiles, mem);
     // order: the segments of the adapters with tokens, then the adapters without
     int *order = mem + backward_tab_words(p.nbins, p.L);
+    int slot_at = p.L + 1;
+    slot_at += -(slot_at + backward_tab_words(p.nbins, p.L)) & 3;
+    int *slots = order + slot_at;                           // steps' tokens, 16-byte aligned
+    volatile int *done = slots + TC_W_SLOTS * 64;           // steps loaded
+    if (tid == 0) *done = 0;
     if (warp == 0) {
         int used = 0, rest = 0;
         for (int i0 = 0; i0 < p.L; i0 += 32)
@@ -230,41 +237,75 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
     };
     if (warp == 0) {
         // ------------------------------------------------ columns of dy or x
+        // The steps' tokens come by cp.async, six steps ahead and across the
+        // items' ends (loaded one step ahead, into registers, their latency
+        // of 1200 clocks beside the other traffic was over half of this
+        // warp's time: 231 us in place of @@).
+        const uint32_t slots_at = smem_addr(slots);
+        int a_item = blockIdx.x, a_k = 0, a_slot = 0, a_start = 0, a_count = 0;
+        auto enter = [&]() {
+            if (a_item >= items) return;
+            const int seg = order[a_item / blocks];
+            a_start = tab.start[seg];
+            a_count = tab.count[seg];
+        };
+        auto ahead = [&]() {
+            if (a_item < items) {
+#pragma unroll
+                for (int j = lane; j < 64; j += 32)
+                    if (a_k * 64 + j < a_count)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n"
+                                     :: "r"(slots_at + (a_slot * 64 + j) * 4), "l"(p.sorted + a_start + a_k * 64 + j)
+                                     : "memory");
+                if (++a_k * 64 >= a_count) {
+                    a_k = 0;
+                    a_item += gridDim.x;
+                    enter();
+                }
+            }
+            cp_async_commit();
+            a_slot = a_slot + 1 == TC_W_SLOTS ? 0 : a_slot + 1;
+        };
+        enter();
+        for (int i = 0; i < TC_W_AHEAD; ++i) ahead();
         TcPos pos;
-        int issued = 0;
+        int issued = 0, slot = 0;
         bool ok = true;
         const int panel = lane & 1, r4 = (lane >> 1) * 4;
         for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item it = decode(i);
             const TcRowMaps *map = it.is_a ? &q.x : &q.dy;
-            TcRows rows;
-            auto tokens = [&](int k) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = k * 64 + r4 + j;
-                    rows.t[j] = row < it.count ? p.sorted[it.start + row] : tc_no_row(p.T, row);
-                }
-            };
-            tokens(0);
             for (int k = 0; k < it.steps; ++k) {
+                cp_async_wait<TC_W_AHEAD - 1>();
+                __syncwarp();
+                const int4 own = *reinterpret_cast<const int4 *>(slots + slot * 64 + r4);
+                slot = slot + 1 == TC_W_SLOTS ? 0 : slot + 1;
+                const int row = k * 64 + r4;
+                TcRows rows;
+                rows.t[0] = row < it.count ? own.x : tc_no_row(p.T, row);
+                rows.t[1] = row + 1 < it.count ? own.y : tc_no_row(p.T, row + 1);
+                rows.t[2] = row + 2 < it.count ? own.z : tc_no_row(p.T, row + 2);
+                rows.t[3] = row + 3 < it.count ? own.w : tc_no_row(p.T, row + 3);
+                join_rows(rows, 2);
+                ahead();
                 const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
                 if (__all_sync(0xffffffffu, got) == 0) {
                     ok = false;
                     break;
                 }
                 const uint32_t full = ring.full + 8 * pos.stage;
-                join_rows(rows, 2);
                 if (lane == 0) mbar_arrive_expect_tx(full, Z_BYTES);
                 __syncwarp();
 #pragma unroll
                 for (int j = panel; j < 4; j += 2)
                     tc_load_rows(rows, ring.ring + pos.stage * ring.stage_bytes + j * TC_PANEL + r4 * 128,
                                  &map->gather, map->box, it.c0 + j * 64, full);
-                if (k + 1 < it.steps) tokens(k + 1);
                 ++issued;
+                if (lane == 0) *done = issued;
                 pos.next(ring.stages);
             }
         }
+        cp_async_wait<0>();
         if (lane == 0) tc_drain_loads(ring, issued);
     } else if (warp == 1) {
         // ------------------------------------------------ u or g
@@ -391,7 +432,20 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         }
     } else if (warp >= 8) {
         // ------------------------------------------------ adapters without tokens
-        for (int i = blockIdx.x; i < (p.L - active) * blocks; i += gridDim.x) {
+        // Written in step with the products: at full speed the zeros take the
+        // memory from the first half of the products, whose loads wait for
+        // it (231 us in place of 208; 156 without zeros).
+        int steps = 0;
+        for (int i = blockIdx.x + lane * gridDim.x; i < items; i += 32 * gridDim.x)
+            steps += (tab.count[order[i / blocks]] + 63) / 64;
+        steps = int(__reduce_add_sync(0xffffffffu, unsigned(steps)));
+        const int empty = (p.L - active) * blocks;
+        const int mine = empty > int(blockIdx.x) ? (empty - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 0;
+        for (int c = 0; c < mine; ++c) {
+            const int first = int(int64_t(steps) * c / mine);
+            // at most 50 us: the order matters, not the wait
+            for (int tries = 0; *done < first && tries < 100 && !*ring.abort; ++tries) __nanosleep(500);
+            const int i = blockIdx.x + c * gridDim.x;
             Item it;
             kind(i % blocks, it);
             clear_item(p, it.is_a, order[active + i / blocks], it.s, it.slices, it.c0, tid - TC_THREADS);
@@ -796,7 +850,7 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     q.buffers = slices * rp > 128 || bias ? 1 : 2;
     q.stage_bytes = 4 * TC_PANEL + (slices * rp > 128 ? slices * rp * 128 : 2 * TC_PANEL);
     q.ones = bias ? 2 * TC_PANEL : 0;
-    q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L + 1);
+    q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L + 1 + 3 + TC_W_SLOTS * 64 + 1);
     q.stages = tc_stages(q.ring - q.ones, q.stage_bytes);
     const uint64_t rows = uint64_t(p.S) * uint64_t(p.rows / BW_TOK) * uint64_t(rp);
     if (!encode_row_maps(&q.dy, p.dy, p.T, p.width, p.dy_ld) ||
