@@ -9,9 +9,10 @@
 // of two that moves only when a logit lies 60 exponents above it.
 //
 // Bound by HBM: vocabulary 32000 x hidden 4096 is 262 MB, 39 us at the
-// measured copy rate; four rows (32 KB) a block are loaded while four are
-// used, two blocks an SM.  One token takes 55 us: 51 for the pass (5.1 TB/s),
-// then the join of the blocks' sums.
+// measured copy rate.  Rows come by cp.async, 96 KB ahead in each of two
+// blocks an SM; a thread copies the columns that it reads.  One token takes
+// 53 us, 46 for the pass (5.7 TB/s; 51 with the next four rows in registers)
+// and the join of the blocks' sums; two tokens take 62.
 #include "lora_loss.cuh"
 
 namespace lora {
@@ -22,14 +23,17 @@ constexpr int LR_WINDOW = 60;
 // CH: 16-byte chunks of a row a thread; NT: tokens.
 template <int CH, int NT>
 struct RowShape {
-    static constexpr int RB = (CH == 1 ? 8 : 4) / (NT > 1 && CH != 2 ? 2 : 1);     // rows at a time
-    static constexpr int BLOCKS = CH >= 4 || NT > 1 ? 1 : 2;      // on an SM
+    static constexpr int RB = 4 / NT;                             // rows at a time
+    static constexpr int BLOCKS = CH >= 4 ? 1 : 2;                // on an SM
+    static constexpr int STAGE = RB * CH * LR_THREADS * 16;
+    static constexpr int ST = 192 * 1024 / BLOCKS / STAGE;        // of the ring
 };
 
 template <int CH, int NT>
 __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row_kernel(const LossRowArgs p)
 {
-    constexpr int RB = RowShape<CH, NT>::RB;
+    constexpr int RB = RowShape<CH, NT>::RB, ST = RowShape<CH, NT>::ST, STAGE = RowShape<CH, NT>::STAGE;
+    extern __shared__ __align__(16) uint8_t lr_ring[];
     __shared__ float s_dot[2][8][RB * NT];                        // parity, warp
     const int part = threadIdx.x, lane = part & 31, warp = part >> 5;
     pdl_wait();
@@ -62,25 +66,33 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
     }
     const int batches = (p.V + RB - 1) / RB;
     int parity = 0;
-    uint4 w[RB][CH], next[RB][CH];
-    auto fetch = [&](int b) {
+    // a thread reads only what it copied itself, so the ring needs no barrier
+    uint8_t *ring = lr_ring + part * 16;
+    int in = blockIdx.x, in_stage = 0, stage = 0;
+    auto fetch = [&]() {
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int col = (c * LR_THREADS + part) * 8;
-                next[r][c] = make_uint4(0, 0, 0, 0);
-                if (b * RB + r < p.V && col < p.H)
-                    next[r][c] = *reinterpret_cast<const uint4 *>(p.weight + int64_t(b * RB + r) * p.H + col);
+                const bool ok = in < batches && in * RB + r < p.V && col < p.H;
+                cp_async16(smem_addr(ring + in_stage * STAGE + (r * CH + c) * LR_THREADS * 16),
+                           ok ? p.weight + int64_t(in * RB + r) * p.H + col : p.weight, ok);
             }
+        cp_async_commit();
+        in += gridDim.x;
+        in_stage = in_stage + 1 == ST ? 0 : in_stage + 1;
     };
-    fetch(int(blockIdx.x));
+    for (int i = 0; i < ST; ++i) fetch();
     for (int b = blockIdx.x; b < batches; b += gridDim.x, parity ^= 1) {
+        cp_async_wait<ST - 1>();
+        uint4 w[RB][CH];
 #pragma unroll
         for (int r = 0; r < RB; ++r)
 #pragma unroll
-            for (int c = 0; c < CH; ++c) w[r][c] = next[r][c];
-        fetch(b + int(gridDim.x));
+            for (int c = 0; c < CH; ++c)
+                w[r][c] = *reinterpret_cast<const uint4 *>(ring + stage * STAGE + (r * CH + c) * LR_THREADS * 16);
+        stage = stage + 1 == ST ? 0 : stage + 1;
         float dot[RB * NT];
 #pragma unroll
         for (int r = 0; r < RB; ++r)
@@ -98,6 +110,7 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
                 }
                 dot[r * NT + t] = d;
             }
+        fetch();                                // into the stage that was just read
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -155,6 +168,7 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
             }
         }
     }
+    cp_async_wait<0>();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (part == 0) p.stat[blockIdx.x * NT + t] = make_float2(ref[t], sum[t]);
@@ -268,7 +282,17 @@ int loss_row_slots() { return 2 * device_sm_count(); }
 template <int CH, int NT>
 static cudaError_t launch_row(const LossRowArgs &p, cudaStream_t st)
 {
-    return launch_kernel(loss_row_kernel<CH, NT>, dim3(unsigned(p.slots)), dim3(LR_THREADS), 0, st, p);
+    constexpr int smem = RowShape<CH, NT>::ST * RowShape<CH, NT>::STAGE;
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(loss_row_kernel<CH, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured[dev] = 1;
+    }
+    return launch_kernel(loss_row_kernel<CH, NT>, dim3(unsigned(p.slots)), dim3(LR_THREADS), size_t(smem), st, p);
 }
 
 template <int NT>
