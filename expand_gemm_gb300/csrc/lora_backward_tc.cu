@@ -18,8 +18,8 @@
 //
 // 16384 tokens in sequences, 8 of 64 adapters in use, rank 128, 8192 to
 // 8192, 1024, 1024: g 76 us (323 MB, 4.3 TB/s: 104 tiles of the wide slice
-// on 152 SMs), dx 108 us (506 MB, 4.7 TB/s: a tile's A, 192 KB for 256
-// columns, comes from L2 at 47 bytes a clock), dA and dB 208 us.  By token
+// on 152 SMs), dx 105 us (506 MB, 4.8 TB/s; without old dx to add
+// its writes alone reach 3.2), dA and dB 208 us.  By token
 // the gathers bound all three (16384 tokens, 4096 to 4096, 1024, 1024: g 60
 // us in sequences, 209 by token; dA and dB 123 and 294).
 #include "lora_backward.cuh"
@@ -462,25 +462,24 @@ struct GradXTcArgs {
     CUtensorMap g;                       // boxes 64 columns x 128 rows of [S * rows][RP]
     CUtensorMap a[LORA_MAX_SLICES];      // [L][r][H], boxes 64 x 64 x 1
     int32_t rp;
-    int32_t keep;                        // the tile's g stays in shared memory
     int32_t ring, stages;
 };
 constexpr int TC_X_COLS = 256;
 
-// Both segment tables: 64-token tiles (rows of g and u) and 128-token tiles.
-__device__ __forceinline__ int load_tabs(const BackwardArgs &p, int *mem, SegTab &t64, SegTab &t128)
+// Both segment tables: 64-token tiles (rows of g and u) and tiles of `rows`.
+__device__ __forceinline__ int load_tabs(const BackwardArgs &p, int *mem, SegTab &t64, SegTab &tile_tab,
+                                         int rows = TC_ROWS)
 {
     int tiles;
     t64 = load_tab(p, mem, tiles);
-    t128 = seg_tab(mem + 4 * p.nbins + 2, p.nbins);
-    return load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, TC_ROWS, t128, false, 0,
+    tile_tab = seg_tab(mem + 4 * p.nbins + 2, p.nbins);
+    return load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, rows, tile_tab, false, 0,
                          p.T, p.error_word);
 }
 
-// Item: (128-token tile, 256 columns); K = slices x rank.  A CTA takes a run
-// of consecutive items, so it meets few tiles; where the tile's rows of g
-// fit beside three stages of A (slices x rank <= 384) they are loaded once a
-// tile and only A streams (192 instead of 288 KB an item at 384).
+// Item: (128-token tile, 256 columns); K = slices x rank.  For products whose
+// g does not fit shared memory beside A (slices x rank above 512): both
+// stream.  The others run on grad_x_pair_kernel.
 __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_constant__ GradXTcArgs q)
 {
     const BackwardArgs &p = q.b;
@@ -488,17 +487,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kps = q.rp / 64, steps = p.S * kps;
     constexpr int G_BYTES = 2 * TC_PANEL, A_BYTES = 4 * TC_PANEL;
-    const uint32_t stage_bytes = q.keep ? A_BYTES : A_BYTES + G_BYTES;
-    const TcRing ring = tc_setup(smem, q.ring, int(stage_bytes), q.stages, 1);
-    // g of the tile lies behind the ring's stages, one 16 KB block a step
-    const uint32_t g_at = ring.ring + q.stages * stage_bytes;
-    const uint32_t g_full = ring.drain + 24, g_empty = g_full + 8;
-    if (threadIdx.x == 0) {
-        mbar_init(g_full, 1);
-        mbar_init(g_empty, 1);
-        mbar_fence_init();
-    }
-    __syncthreads();
+    constexpr uint32_t STAGE = A_BYTES + G_BYTES;
+    const TcRing ring = tc_setup(smem, q.ring, int(STAGE), q.stages, 1);
     pdl_wait();
     SegTab t64, t128;
     const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_STAGE_ROWS + TC_BAR_BYTES), t64, t128);
@@ -513,20 +503,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
         if (lane == 0) {
             TcPos pos;
             int issued = 0, tile = first / hb, h0 = first % hb * TC_X_COLS;
-            uint32_t gphase = 0;
-            bool ok = true, loaded = false;
+            bool ok = true;
             for (int i = first; ok && i < end; ++tile, h0 = 0) {
                 const int seg = find_segment(t128.tile, p.nbins, tile);
                 const int row0 = t64.tile[seg] * 64 + (tile - t128.tile[seg]) * TC_ROWS;
                 const int id = t128.id[seg];
-                if (q.keep) {
-                    if (!pg_wait(g_empty, gphase ^ 1u, ring.abort)) break;
-                    mbar_arrive_expect_tx(g_full, uint32_t(steps * G_BYTES));
-                    for (int k = 0; k < steps; ++k)
-                        tma_load_2d(g_at + k * G_BYTES, &q.g, k % kps * 64, int(k / kps * p.rows) + row0, g_full);
-                    gphase ^= 1u;
-                    loaded = true;
-                }
                 for (; ok && i < end && h0 < p.H; ++i, h0 += TC_X_COLS) {
                     int grow = row0;
                     for (int s = 0; ok && s < p.S; ++s, grow += int(p.rows)) {
@@ -537,11 +518,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                                 break;
                             }
                             const uint32_t full = ring.full + 8 * pos.stage;
-                            const uint32_t at = ring.ring + pos.stage * stage_bytes;
-                            mbar_arrive_expect_tx(full, stage_bytes);
+                            const uint32_t at = ring.ring + pos.stage * STAGE;
+                            mbar_arrive_expect_tx(full, STAGE);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) tma_load_3d(at + j * TC_PANEL, map, h0 + j * 64, kc, id, full);
-                            if (!q.keep) tma_load_2d(at + A_BYTES, &q.g, kc, grow, full);
+                            tma_load_2d(at + A_BYTES, &q.g, kc, grow, full);
                             ++issued;
                             pos.next(q.stages);
                         }
@@ -549,28 +530,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                 }
             }
             tc_drain_loads(ring, issued);
-            // the last tile's g has landed
-            if (loaded) {
-                const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-                while (!mbar_try_wait(g_full, gphase ^ 1u) && clock64() < dd) {
-                }
-            }
         }
     } else if (warp == 1 || warp == 3) {
         if (!p.add) clear_rest(p, t64, warp >> 1, 2);
     } else if (warp == 2) {
         if (lane == 0) {
             TcPos pos;
-            int buf = 0, tile = -1;
-            uint32_t bphase = 0, gphase = 0;
+            int buf = 0;
+            uint32_t bphase = 0;
             bool ok = true;
             for (int i = first; ok && i < end; ++i) {
                 if (!pg_wait(ring.acce + 8 * buf, bphase ^ 1u, ring.abort)) break;
-                if (q.keep && i / hb != tile) {
-                    tile = i / hb;
-                    if (!pg_wait(g_full, gphase, ring.abort)) break;
-                    gphase ^= 1u;
-                }
                 tc_fence_after();
                 const uint32_t d = ring.tmem + uint32_t(buf * TC_X_COLS);
                 for (int k = 0; k < steps; ++k) {
@@ -579,15 +549,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sb = ring.ring + pos.stage * stage_bytes;
-                    const uint32_t sa = q.keep ? g_at + k * G_BYTES : sb + A_BYTES;
+                    const uint32_t sb = ring.ring + pos.stage * STAGE, sa = sb + A_BYTES;
                     umma_k64(d, sa, sb, umma_idesc_bf16(128, TC_X_COLS) | 1u << 16, k != 0);
                     umma_commit(ring.empty + 8 * pos.stage);
                     pos.next(q.stages);
                 }
                 if (!ok) break;
                 umma_commit(ring.accf + 8 * buf);
-                if (q.keep && i + 1 < end && (i + 1) / hb != tile) umma_commit(g_empty);
                 buf ^= 1;
                 if (buf == 0) bphase ^= 1u;
             }
@@ -630,6 +598,294 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
         }
     }
     tc_finish(ring, p.error_word);
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                                 int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];\n"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// dx on CTA pairs: 256 tokens of one adapter, 128 of them in each CTA
+// with their g, and half of A's 256 columns in each, which leaves room for
+// more of A in flight and for eight epilogue warps (a half of the columns
+// each four): with four, one on each scheduler, the chain from TMEM through
+// shared memory to dx bounded the kernel: 113 us in place of 75 for 16384
+// tokens, rank 128, 4096 to 4096, 1024, 1024.
+constexpr int TC_XP_THREADS = 384;
+constexpr int TC_XP_SLOT = 32 * 128;             // 32 rows of 64 columns
+constexpr int TC_XP_STAGE = 8 * TC_XP_SLOT;
+
+__global__ void __launch_bounds__(TC_XP_THREADS, 1) grad_x_pair_kernel(const __grid_constant__ GradXTcArgs q)
+{
+    const BackwardArgs &p = q.b;
+    uint8_t *smem = tc_smem();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kps = q.rp / 64, steps = p.S * kps;
+    constexpr int G_BYTES = 2 * TC_PANEL, A_BYTES = 2 * TC_PANEL;
+    const uint32_t base = smem_addr(smem);
+    const uint32_t full = base + q.ring + TC_XP_STAGE, empty = full + 8 * TC_MAX_STAGES;
+    const uint32_t accf = empty + 8 * TC_MAX_STAGES, acce = accf + 16, drain = acce + 16;
+    const uint32_t g_full = drain + 24, g_empty = g_full + 8, acce_odd = g_empty + 8;
+    const uint32_t g_at = base + q.stages * A_BYTES;
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
+    volatile int *abort = reinterpret_cast<volatile int *>(misc + 1);
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < q.stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf + 8 * i, 1);
+            mbar_init(acce + 8 * i, 8);           // this CTA's epilogue warps
+            mbar_init(acce_odd + 8 * i, 1);       // the odd CTA's, in the even one
+        }
+        mbar_init(drain, 1);
+        mbar_init(g_full, 1);
+        mbar_init(g_empty, 1);
+        mbar_fence_init();
+        *abort = 0;
+    }
+    if (warp == 3) tmem_alloc_pair(smem_addr(misc), 512);
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *misc;
+    pdl_wait();
+    SegTab t64, t256;
+    const int tiles = load_tabs(p, reinterpret_cast<int *>(smem + q.ring + TC_XP_STAGE + TC_BAR_BYTES), t64, t256,
+                                2 * TC_ROWS);
+    const int hb = (p.H + TC_X_COLS - 1) / TC_X_COLS;
+    const int items = tiles * hb, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int first = int(int64_t(items) * pair / pairs);
+    const int end = int(int64_t(items) * (pair + 1) / pairs);
+
+    if (warp == 0) {
+        // g and u were written by the stream's previous kernel with ordinary stores
+        asm volatile("fence.proxy.async.global;\n" ::: "memory");
+        if (lane == 0) {
+            const uint32_t full0 = cluster_map(full, 0), g_full0 = cluster_map(g_full, 0);
+            TcPos pos;
+            int issued = 0, tile = first / hb, h0 = first % hb * TC_X_COLS;
+            uint32_t gphase = 0;
+            bool ok = true, loaded = false;
+            for (int i = first; ok && i < end; ++tile, h0 = 0) {
+                const int seg = find_segment(t256.tile, p.nbins, tile);
+                const int row0 = t64.tile[seg] * 64 + (tile - t256.tile[seg]) * 2 * TC_ROWS + int(rank) * TC_ROWS;
+                const int id = t256.id[seg];
+                if (!pg_wait(g_empty, gphase ^ 1u, abort)) break;
+                if (rank == 0) mbar_arrive_expect_tx(g_full, uint32_t(2 * steps * G_BYTES));
+                for (int k = 0; k < steps; ++k)
+                    tma_load_2d_pair(g_at + k * G_BYTES, &q.g, k % kps * 64, int(k / kps * p.rows) + row0, g_full0);
+                gphase ^= 1u;
+                loaded = true;
+                for (; ok && i < end && h0 < p.H; ++i, h0 += TC_X_COLS) {
+                    for (int s = 0; ok && s < p.S; ++s) {
+                        const CUtensorMap *map = &q.a[s];
+                        for (int kc = 0; kc < q.rp; kc += 64) {
+                            if (!pg_wait(empty + 8 * pos.stage, pos.phase ^ 1u, abort)) {
+                                ok = false;
+                                break;
+                            }
+                            if (rank == 0) mbar_arrive_expect_tx(full + 8 * pos.stage, 2 * A_BYTES);
+                            const uint32_t at = base + pos.stage * A_BYTES;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d_pair(at + j * TC_PANEL, map, h0 + int(rank) * 128 + j * 64, kc, id,
+                                                 full0 + 8 * pos.stage);
+                            ++issued;
+                            pos.next(q.stages);
+                        }
+                    }
+                }
+            }
+            // No copy and no commit may still target this CTA when it exits
+            // (the leader's barriers count both CTAs' copies).
+            const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+            for (int i = max(0, issued - q.stages); i < issued; ++i) {
+                const uint32_t ph = uint32_t(i / q.stages) & 1u, b8 = 8u * uint32_t(i % q.stages);
+                if (rank == 0)
+                    while (!mbar_try_wait_cluster(full + b8, ph) && clock64() < dd) {
+                    }
+                while (!mbar_try_wait_cluster(empty + b8, ph) && !*abort && clock64() < dd) {
+                }
+            }
+            if (loaded && rank == 0)
+                while (!mbar_try_wait_cluster(g_full, gphase ^ 1u) && clock64() < dd) {
+                }
+        }
+    } else if (warp == 1 || warp == 3) {
+        if (!p.add) clear_rest(p, t64, warp >> 1, 2);
+    } else if (warp == 2) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t IDESC = umma_idesc_bf16(2 * TC_ROWS, TC_X_COLS) | 1u << 16;
+            TcPos pos;
+            int buf = 0, tile = -1;
+            uint32_t bphase = 0, gphase = 0;
+            bool ok = true;
+            for (int i = first; ok && i < end; ++i) {
+                if (!pg_wait(acce + 8 * buf, bphase ^ 1u, abort) ||
+                    !pg_wait(acce_odd + 8 * buf, bphase ^ 1u, abort))
+                    break;
+                if (i / hb != tile) {
+                    tile = i / hb;
+                    if (!pg_wait(g_full, gphase, abort)) break;
+                    gphase ^= 1u;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + uint32_t(buf * TC_X_COLS);
+                for (int k = 0; k < steps; ++k) {
+                    if (!pg_wait(full + 8 * pos.stage, pos.phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = g_at + k * G_BYTES, sb = base + pos.stage * A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_pair(d, umma_desc_sw128(sa + kk * 32), umma_desc_mn(sb + kk * 2048), IDESC,
+                                       k != 0 || kk != 0);
+                    umma_commit_both(empty + 8 * pos.stage);
+                    pos.next(q.stages);
+                }
+                if (!ok) break;
+                umma_commit_both(accf + 8 * buf);
+                if (i + 1 < end && (i + 1) / hb != tile) umma_commit_both(g_empty);
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1u;
+            }
+            if (*abort) {       // nothing in flight when TMEM is released
+                umma_commit_pair(cluster_map(drain, 0));
+                const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+                while (!mbar_try_wait_cluster(drain, 0) && clock64() < dd) {
+                }
+            }
+        }
+        if (lane == 0 && rank == 1) {
+            // tells the even CTA which accumulators are read.  The epilogue
+            // warps arrive in their own CTA: an arrival at cluster scope
+            // waits for the warp's loads and stores in flight (103 us in
+            // place of 93)
+            const uint32_t to = cluster_map(acce_odd, 0);
+            int buf = 0;
+            uint32_t bphase = 0;
+            for (int i = first; i < end; ++i) {
+                if (!pg_wait(acce + 8 * buf, bphase, abort)) break;
+                tc_fence_after();
+                tc_fence_before();
+                mbar_arrive_cluster(to + 8 * buf);
+                buf ^= 1;
+                if (buf == 0) bphase ^= 1u;
+            }
+        }
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) / 4 * (TC_X_COLS / 2);
+        const int row = int(rank) * TC_ROWS + quarter * 32 + lane;
+        uint8_t *slot = smem + q.ring + (warp - 4) * TC_XP_SLOT;
+        int buf = 0, tile = first / hb, h0 = first % hb * TC_X_COLS + half;
+        uint32_t bphase = 0;
+        // where rows 4 k + lane / 8 of this warp's 32 begin in dx, and whether they exist
+        int token[8];
+        auto find = [&](int of) {
+            const int seg = find_segment(t256.tile, p.nbins, of);
+            const int r = (of - t256.tile[seg]) * 2 * TC_ROWS + row;
+            const int tok =
+                r < t256.count[seg] ? checked_token(p.sorted[t256.start[seg] + r], p.T, p.error_word) : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) token[k] = __shfl_sync(0xffffffffu, tok, 4 * k + (lane >> 3));
+        };
+        uint4 was[8];
+        auto fetch = [&](int c) {               // what dx holds of 64 columns
+            const int col = c + (lane & 7) * 8;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (token[k] >= 0 && col < p.H)
+                    was[k] = *reinterpret_cast<const uint4 *>(p.dx + int64_t(token[k]) * p.dx_ld + col);
+        };
+        if (first < end) find(tile);
+        if (p.add && first < end) fetch(h0);
+        for (int i = first; i < end; ++i) {
+            const bool got = pg_wait(accf + 8 * buf, bphase, abort);
+            if (__all_sync(0xffffffffu, got) == 0) break;
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(buf * TC_X_COLS + half) + (uint32_t(quarter * 32) << 16);
+            const bool turn = h0 - half + TC_X_COLS >= p.H;         // the next item is another tile's
+#pragma unroll
+            for (int c = 0; c < TC_X_COLS / 2; c += 64) {
+                if (p.add) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = 4 * k + (lane >> 3);
+                        *reinterpret_cast<uint4 *>(slot + r * 128 + ((lane ^ r) & 7) * 16) = was[k];
+                    }
+                    if (c == 0) fetch(h0 + 64);
+                    else if (!turn) fetch(h0 + TC_X_COLS);
+                    __syncwarp();
+                }
+                // a lane's own row: the sums and what dx holds, one rounding
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t v[32];
+                    tmem_ld32_nowait(d + uint32_t(c + 32 * e), v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint4 *piece = reinterpret_cast<uint4 *>(slot + lane * 128 + (((4 * e + k) ^ lane) & 7) * 16);
+                        uint32_t o[4];
+                        if (p.add) {
+                            const uint4 x = *piece;
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                o[j] = pack_bf16x2(
+                                    fmaf(p.scale, __uint_as_float(v[8 * k + 2 * j]), bf16_lo(w[j])),
+                                    fmaf(p.scale, __uint_as_float(v[8 * k + 2 * j + 1]), bf16_hi(w[j])));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                o[j] = pack_bf16x2(p.scale * __uint_as_float(v[8 * k + 2 * j]),
+                                                   p.scale * __uint_as_float(v[8 * k + 2 * j + 1]));
+                        }
+                        *piece = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (c + 64 == TC_X_COLS / 2) {
+                    tc_fence_before();                          // the accumulator is read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acce + 8 * buf);
+                }
+                __syncwarp();
+                const int col = h0 + c + (lane & 7) * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + (lane >> 3);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(slot + r * 128 + ((lane ^ r) & 7) * 16);
+                    if (token[k] >= 0 && col < p.H)
+                        *reinterpret_cast<uint4 *>(p.dx + int64_t(token[k]) * p.dx_ld + col) = x;
+                }
+                __syncwarp();
+            }
+            buf ^= 1;
+            if (buf == 0) bphase ^= 1u;
+            h0 += TC_X_COLS;
+            if (turn && i + 1 < end) {
+                h0 = half;
+                find(++tile);
+                if (p.add) fetch(h0);
+            }
+        }
+    }
+    __syncwarp();
+    if (threadIdx.x == 0 && *abort && p.error_word != nullptr) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 3) tmem_dealloc_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------- g and u
@@ -803,7 +1059,7 @@ static int tc_configure()
     if (e != cudaSuccess) return int(e);
     if (dev < 64 && configured[dev]) return 0;
     const void *fns[] = {(const void *)grad_w_tc_kernel, (const void *)grad_x_tc_kernel,
-                         (const void *)grad_u_tc_kernel};
+                         (const void *)grad_x_pair_kernel, (const void *)grad_u_tc_kernel};
     for (const void *f : fns)
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM)) != cudaSuccess)
             return int(e);
@@ -870,9 +1126,8 @@ int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
     if (rp < 64 || !p.dx_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
     // Fewer items than SMs: smaller ones on mma.sync are faster.  4096 to
-    // 4096 at rank 64: 512 tokens 13.5 us here, 9.2 there (32 adapters by
-    // token 37 and 21), 2048 tokens 20.8 here, 22.6 there; at rank 128 14.1
-    // and 9.3, 21.8 and 25.4.
+    // 4096 at rank 64: 1024 tokens 15.3 us here, 14.0 there; 2048 tokens 15.9
+    // here, 22.6 there; at rank 128 16.4 and 15.4, 17.1 and 25.4.
     if (int64_t(p.T) / TC_ROWS * ((p.H + TC_X_COLS - 1) / TC_X_COLS) < device_sm_count()) return -1;
     static thread_local GradXTcArgs q;
     q.b = p;
@@ -884,8 +1139,14 @@ int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
         if (!encode_stack_map(&q.a[s], p.a[s], uint64_t(p.L), uint64_t(p.r), uint64_t(p.H), 64, 64)) return -1;
     const int g_bytes = p.S * (rp / 64) * 2 * TC_PANEL;
     q.ring = tc_ring_bytes(2 * (4 * p.nbins + 2));
-    q.keep = q.ring - g_bytes >= 2 * 4 * TC_PANEL;
-    q.stages = q.keep ? tc_stages(q.ring - g_bytes, 4 * TC_PANEL) : tc_stages(q.ring, 6 * TC_PANEL);
+    const int pair_ring = q.ring - (TC_XP_STAGE - TC_STAGE_ROWS);
+    if (pair_ring - g_bytes >= 4 * 2 * TC_PANEL && device_sm_count() > 1) {
+        q.ring = pair_ring;
+        q.stages = tc_stages(q.ring - g_bytes, 2 * TC_PANEL);
+        if (int e = tc_configure()) return e;
+        return int(launch_pair_kernel(grad_x_pair_kernel, device_sm_count() / 2, st, q, TC_XP_THREADS, TC_SMEM));
+    }
+    q.stages = tc_stages(q.ring, 6 * TC_PANEL);
     if (int e = tc_configure()) return e;
     return int(launch_kernel(grad_x_tc_kernel, dim3(unsigned(device_sm_count())), dim3(TC_THREADS),
                              size_t(TC_SMEM), st, q));

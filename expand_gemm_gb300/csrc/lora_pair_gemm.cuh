@@ -105,8 +105,9 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
     const uint32_t bars = base + PG_STAGES * PG_STAGE_BYTES;
     const uint32_t bar_full = bars, bar_empty = bars + 8 * PG_STAGES;
     const uint32_t bar_accf = bar_empty + 8 * PG_STAGES;      // [2]
-    const uint32_t bar_acce = bar_accf + 16;                  // [2], the even CTA's is used
-    const uint32_t bar_drain = bar_acce + 16;
+    const uint32_t bar_acce = bar_accf + 16;                  // [2]
+    const uint32_t bar_odd = bar_acce + 16;                   // [2], the odd CTA's in the even one
+    const uint32_t bar_drain = bar_odd + 16;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (bar_drain + 8 - base));
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -120,7 +121,8 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_accf + 8 * i, 1);
-            mbar_init(bar_acce + 8 * i, 16);      // eight epilogue warps of each CTA
+            mbar_init(bar_acce + 8 * i, 8);       // this CTA's epilogue warps
+            mbar_init(bar_odd + 8 * i, 1);
         }
         mbar_init(bar_drain, 1);
         mbar_fence_init();
@@ -201,7 +203,9 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
             for (int i = pair; ok && i < total; i += npairs) {
                 const PairItem it = item_of(i);
                 if (it.kb0 >= it.kb1) continue;
-                if (!pg_wait(bar_acce + 8 * acc, acc_phase ^ 1u, s_abort)) break;
+                if (!pg_wait(bar_acce + 8 * acc, acc_phase ^ 1u, s_abort) ||
+                    !pg_wait(bar_odd + 8 * acc, acc_phase ^ 1u, s_abort))
+                    break;
                 tc_fence_after();
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!pg_wait(bar_full + 8 * stage, phase, s_abort)) {
@@ -236,12 +240,28 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
                 while (!mbar_try_wait_cluster(bar_drain, 0) && clock64() < dd) {
                 }
             }
+        } else if (lane == 0) {
+            // tells the even CTA which accumulators the odd one has read.
+            // The epilogue warps arrive in their own CTA: an arrival at
+            // cluster scope waits for the warp's loads and stores in flight.
+            const uint32_t to = cluster_map(bar_odd, 0);
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            for (int i = pair; i < total; i += npairs) {
+                const PairItem it = item_of(i);
+                if (it.kb0 >= it.kb1) continue;
+                if (!pg_wait(bar_acce + 8 * acc, acc_phase, s_abort)) break;
+                tc_fence_after();
+                tc_fence_before();
+                mbar_arrive_cluster(to + 8 * acc);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------- epilogue
         const int q = warp & 3;                   // TMEM lane quarter of this warp
-        const uint32_t acce0 = cluster_map(bar_acce, 0);
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = pair; i < total; i += npairs) {
@@ -257,7 +277,7 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
             if (!empty) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(acce0 + 8 * acc);
+                if (lane == 0) mbar_arrive(bar_acce + 8 * acc);
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
@@ -273,12 +293,13 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
 
 // Launch with clusters of two CTAs.
 template <typename Kern, typename Arg>
-cudaError_t launch_pair_kernel(Kern kernel, int pairs, cudaStream_t stream, const Arg &arg)
+cudaError_t launch_pair_kernel(Kern kernel, int pairs, cudaStream_t stream, const Arg &arg,
+                               int threads = PG_THREADS, int smem = PG_SMEM)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(2 * pairs));
-    cfg.blockDim = dim3(PG_THREADS);
-    cfg.dynamicSmemBytes = PG_SMEM;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
