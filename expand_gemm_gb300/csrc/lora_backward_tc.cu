@@ -18,8 +18,7 @@
 //
 // 16384 tokens in sequences, 8 of 64 adapters in use, rank 128, 8192 to
 // 8192, 1024, 1024: g 76 us (323 MB, 4.3 TB/s: 104 tiles of the wide slice
-// on 152 SMs), dx 105 us (506 MB, 4.8 TB/s; without old dx to add
-// its writes alone reach 3.2), dA and dB 208 us.  By token
+// on 152 SMs), dx 93 us (451 MB, 4.8 TB/s), dA and dB 208 us.  By token
 // the gathers bound all three (16384 tokens, 4096 to 4096, 1024, 1024: g 60
 // us in sequences, 209 by token; dA and dB 123 and 294).
 #include "lora_backward.cuh"
