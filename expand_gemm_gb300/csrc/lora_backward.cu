@@ -53,6 +53,7 @@ __device__ __forceinline__ void copy8(uint8_t *dst, const uint16_t *row, int c, 
 
 template <int RP> struct UShape { static constexpr int WM = 4, WN = 2; };
 constexpr int BW_U_STAGES = 4;
+constexpr int BW_U_WHOLE = 16;
 
 template <int RP>
 constexpr int grad_u_smem() { return BW_U_STAGES * (BW_TOK * 64 * 2 + 64 * RP * 2); }
@@ -69,7 +70,12 @@ __device__ __forceinline__ int step_cta(int64_t total, int64_t step, int ctas)
 // Each CTA walks its run of steps; its part of an item's sum goes to slot
 // (CTA + item), a new one whenever the CTA or the item changes.  Bound by
 // the reads of dy: a ring of four steps by cp.async.
-template <int RP>
+//
+// WHOLE: a CTA takes whole items and writes g and u itself; the join is not
+// launched.  For slices of up to BW_U_WHOLE steps: 512 tokens, rank 32, 16
+// steps 10.1 us, split and joined 10.3 and a launch more; 4 steps 6.1 and
+// 9.5; 24 steps 12.8 and 10.7.
+template <int RP, bool WHOLE>
 __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constant__ BackwardArgs p)
 {
     constexpr int WM = UShape<RP>::WM, WN = UShape<RP>::WN;
@@ -86,14 +92,22 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
     const int per_tile = p.step_end[p.S - 1];
     const int64_t total = int64_t(tiles) * per_tile;
     const int ctas = int(min(int64_t(gridDim.x), total));      // a step each at least
-    if (int(blockIdx.x) >= ctas) return;
-    int64_t step = step_begin(total, blockIdx.x, ctas);
-    const int64_t end = step_begin(total, blockIdx.x + 1, ctas);
-    int tile = int(step / per_tile), s = 0;
-    int k = int(step % per_tile);                              // of the tile, then of the slice
-    while (k >= p.step_end[s]) ++s;
-    if (s > 0) k -= p.step_end[s - 1];
+    if (!WHOLE && int(blockIdx.x) >= ctas) return;
+    // WHOLE: items in place of steps
+    int64_t step = WHOLE ? int64_t(blockIdx.x) : step_begin(total, blockIdx.x, ctas);
+    const int64_t end = WHOLE ? int64_t(tiles) * p.S : step_begin(total, blockIdx.x + 1, ctas);
+    int tile = 0, s = 0, k = 0;
+    if constexpr (!WHOLE) {
+        tile = int(step / per_tile);
+        k = int(step % per_tile);                              // of the tile, then of the slice
+        while (k >= p.step_end[s]) ++s;
+        if (s > 0) k -= p.step_end[s - 1];
+    }
     while (step < end) {
+        if constexpr (WHOLE) {
+            tile = int(step / p.S);
+            s = int(step % p.S);
+        }
         const int seg = find_segment(tab.tile, p.nbins, tile);
         const int id = tab.id[seg];
         const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
@@ -101,7 +115,8 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
         const int lo = p.off[s], hi = lo + p.n[s];
         const int c0 = p.dy_vec ? lo & ~7 : lo;                // first column of the first step
         const int k_lo = k;
-        const int k_hi = int(min(int64_t(p.step_end[s] - (s > 0 ? p.step_end[s - 1] : 0)), k + (end - step)));
+        const int steps = p.step_end[s] - (s > 0 ? p.step_end[s - 1] : 0);
+        const int k_hi = WHOLE ? steps : int(min(int64_t(steps), k + (end - step)));
         const uint16_t *bw = p.b[s] + int64_t(id) * p.n[s] * p.r;
         const uint16_t *src[2];
 #pragma unroll
@@ -134,6 +149,19 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
         };
         float acc[NI][4] = {};
         for (int i = k_lo; i < k_lo + ST - 1; ++i) issue(i);
+        float4 u[WHOLE ? RP / 16 : 1];
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int i = 0; i < RP / 16; ++i) {
+                const int at = (tid + i * BW_THREADS) * 4, row = at / RP, col = at % RP;
+                u[i] = make_float4(0, 0, 0, 0);
+                if (row < nrows && col < p.r) {
+                    const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
+                    if (tok >= 0)
+                        u[i] = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
+                }
+            }
+        }
         for (int i = k_lo; i < k_hi; ++i) {
             cp_async_wait<ST - 2>();
             __syncthreads();
@@ -159,6 +187,22 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
             }
         }
         const int gq = lane >> 2, t = lane & 3;
+        if constexpr (WHOLE) {
+            const int64_t out0 = (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                uint16_t *at = p.g + out0 + (wm * 16 + gq) * RP + wn * (RP / WN) + 8 * j + 2 * t;
+                *reinterpret_cast<uint32_t *>(at) = pack_bf16x2(acc[j][0], acc[j][1]);
+                *reinterpret_cast<uint32_t *>(at + 8 * RP) = pack_bf16x2(acc[j][2], acc[j][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < RP / 16; ++i)
+                reinterpret_cast<uint2 *>(p.u + out0)[tid + i * BW_THREADS] =
+                    make_uint2(pack_bf16x2(u[i].x, u[i].y), pack_bf16x2(u[i].z, u[i].w));
+            __syncthreads();                                   // the ring is free
+            step += gridDim.x;
+            continue;
+        }
         float *out = p.part + (int64_t(blockIdx.x) + int64_t(tile) * p.S + s) * BW_TOK * RP;
 #pragma unroll
         for (int j = 0; j < NI; ++j) {
@@ -663,8 +707,11 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return int(e);
     if (dev >= 64 || !configured[dev]) {
         constexpr int most = int(seg_tab_bytes(LORA_MAX_LORAS + 1)) + LORA_MAX_LORAS * 4;
-        if ((e = cudaFuncSetAttribute(grad_u_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if ((e = cudaFuncSetAttribute(grad_u_kernel<RP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       grad_u_smem<RP>() + most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(grad_u_kernel<RP <= 32 ? RP : 32, true>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_u_smem<RP <= 32 ? RP : 32>() + most)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(grad_x_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       grad_x_smem<RP>() + most)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(grad_w_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -682,10 +729,19 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
     // Ranks above 32 run on tcgen05 where the rows allow TMA.
     int tc = RP >= 64 && p.T > 0 ? launch_grad_u_tc(p, RP, st) : -1;
     if (tc > 0) return tc;
-    if (p.T > 0 && tc < 0) {
+    int longest = 0;                           // steps of a slice
+    for (int k = 0; k < p.S; ++k) {
+        const int steps = p.step_end[k] - (k > 0 ? p.step_end[k - 1] : 0);
+        if (steps > longest) longest = steps;
+    }
+    if (p.T > 0 && RP <= 32 && longest <= BW_U_WHOLE) {
+        const int64_t most = tiles * p.S, grid = most < resident(us) ? most : resident(us);
+        e = launch_kernel(grad_u_kernel<RP <= 32 ? RP : 32, true>, dim3(unsigned(grid)), dim3(BW_THREADS), us, st, p);
+        if (e != cudaSuccess) return int(e);
+    } else if (p.T > 0 && tc < 0) {
         BackwardArgs q = p;
         q.u_ctas = int(resident(us));
-        e = launch_kernel(grad_u_kernel<RP>, dim3(unsigned(q.u_ctas)), dim3(BW_THREADS), us, st, q);
+        e = launch_kernel(grad_u_kernel<RP, false>, dim3(unsigned(q.u_ctas)), dim3(BW_THREADS), us, st, q);
         if (e != cudaSuccess) return int(e);
         const int64_t most = tiles * p.S * (RP / 4), grid = most < 8 * sms ? most : 8 * sms;
         e = launch_kernel(join_u_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), tab, st, q);

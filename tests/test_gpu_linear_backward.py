@@ -114,6 +114,16 @@ def test_sizes(T, H, r, L, widths, runs, add):
     check(run(c, add), in_64_bits(c, add))
 
 
+# Slices of more than 1024 columns, whose g is summed by several blocks.
+@pytest.mark.parametrize("T,H,r,L,widths,runs", [
+    (1, 64, 8, 2, (1500,), 1), (130, 72, 8, 3, (1500, 1031), 1), (700, 64, 32, 5, (2100,), 7),
+    (333, 136, 24, 4, (1100, 65, 3001), 1), (64, 64, 16, 1, (5000,), 64), (1200, 64, 16, 40, (1030, 8), 1)])
+@pytest.mark.parametrize("add", [True, False])
+def test_wide_slices(T, H, r, L, widths, runs, add):
+    c = make(T, H, r, L, widths, T + H, runs=runs)
+    check(run(c, add), in_64_bits(c, add))
+
+
 # Large enough for every product to take the tensor-core kernels: tails of all
 # kinds, tiles of one adapter's few tokens, g kept beside the stages and not.
 LARGE = [
