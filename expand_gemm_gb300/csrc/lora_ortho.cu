@@ -18,11 +18,11 @@
 //
 // This file: ranks up to 32, on mma.sync, the steps in FFMA.
 // lora_ortho_tc.cu: ranks 33 to 128, on tcgen05 (whose tiles of 64 cost rank
-// 32 twice the time: 64 matrices of 11008 x 32 60 us here, 137 there; 8 of
+// 32 twice the time: 64 matrices of 11008 x 32 58 us here, 137 there; 8 of
 // 16 x 4096 13 and 46).
 //
 // Bound by HBM above a few MB: 64 matrices of 11008 x 32 in fp32 (135 MB)
-// take 24 us in gram_kernel (3.7 TB/s), 15 in iterate_kernel, 22 in
+// take 24 us in gram_kernel (3.7 TB/s), 12 in iterate_kernel, 22 in
 // apply_kernel (6.2 TB/s); below, by three launches in a row.
 #include <math.h>
 
@@ -261,7 +261,7 @@ __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int 
     for (int i = 0; i < E; ++i)
 #pragma unroll
         for (int j = 0; j < E; ++j) c[i][j] = 0.0f;
-#pragma unroll 8
+#pragma unroll
     for (int k = 0; k < RP; ++k) {
         float a[E], b[E];
 #pragma unroll
@@ -278,7 +278,8 @@ __device__ __forceinline__ void mul(const float *A, const float *B, int ty, int 
 // One block per matrix; R, P, Q in shared memory, in fp32.  The 136 blocks
 // on or above the diagonal of a 16 x 16 grid are a thread's each; the rest
 // is their mirror image.  Ranks up to 32; above, the products are long
-// enough for the tensor cores (rank 40: 59 us here, see lora_ortho_tc.cu).
+// enough for the tensor cores: five steps at rank 32 take 12 us here and 29
+// in lora_ortho_tc.cu, at rank 40 59 here and 27 there.
 template <int RP>
 __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
 {
@@ -293,8 +294,18 @@ __global__ void __launch_bounds__(OR_THREADS) iterate_kernel(const OrthoArgs p)
     tx += ty;
     pdl_wait();
     const int lo = unit_cta(p, int64_t(m) * p.units), hi = unit_cta(p, int64_t(m + 1) * p.units - 1);
-    for (int i = tid; i < RP * RP; i += OR_THREADS) {
-        R[i] = gram_sum<RP>(p, m, lo, hi, i);
+    // a matrix's slots, all of a thread's loads under way at once
+    if (tid < RP * RP / 4) {
+        float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int c = lo; c <= hi; ++c) {
+            const float4 x = reinterpret_cast<const float4 *>(p.gram + int64_t(c + m) * RP * RP)[tid];
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
+        }
+        reinterpret_cast<float4 *>(R)[tid] = v;
     }
     __syncthreads();
     if (tid < 32) {

@@ -36,16 +36,6 @@ __device__ __forceinline__ int unit_cta(const OrthoArgs &p, int64_t unit)
     return int(((unit + 1) * p.ctas - 1) / (int64_t(p.count) * p.units));
 }
 
-// One element of matrix m's sum.
-template <int RP>
-__device__ __forceinline__ float gram_sum(const OrthoArgs &p, int m, int lo, int hi, int e)
-{
-    float s = 0.0f;
-#pragma unroll 4
-    for (int c = lo; c <= hi; ++c) s += p.gram[int64_t(c + m) * RP * RP + e];
-    return s;
-}
-
 // Eight consecutive fp32 entries as bf16 terms: hi, and what hi leaves over.
 struct Chunk {
     uint4 hi, lo;
