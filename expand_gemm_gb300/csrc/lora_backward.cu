@@ -774,7 +774,8 @@ LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidd
                                                 int32_t rank, int32_t max_loras)
 {
     if (slice_sizes == nullptr) return LORA_ERR_NULL;
-    if (hidden < 8 || hidden % 8 != 0 || num_tokens < 0 || max_loras < 1 || max_loras > LORA_MAX_LORAS) return LORA_ERR_SIZE;
+    if (hidden < 8 || hidden % 8 != 0 || num_tokens < 0 || max_loras < 1 || max_loras > LORA_MAX_LORAS)
+        return LORA_ERR_SIZE;
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
     const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;

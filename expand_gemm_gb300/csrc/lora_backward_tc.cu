@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(TC_XP_THREADS, 1) grad_x_pair_kernel(const __g
         uint8_t *slot = smem + q.ring + (warp - 4) * TC_XP_SLOT;
         int buf = 0, tile = first / hb, h0 = first % hb * TC_X_COLS + half;
         uint32_t bphase = 0;
-        // where rows 4 k + lane / 8 of this warp's 32 begin in dx, and whether they exist
+        // the tokens of rows 4 k + lane / 8 of this warp's 32 (negative: none)
         int token[8];
         auto find = [&](int of) {
             const int seg = find_segment(t256.tile, p.nbins, of);
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(TC_XP_THREADS, 1) grad_x_pair_kernel(const __g
 #pragma unroll
             for (int k = 0; k < 8; ++k) token[k] = __shfl_sync(0xffffffffu, tok, 4 * k + (lane >> 3));
         };
-        uint4 was[8];
+        uint4 was[8] = {};
         auto fetch = [&](int c) {               // what dx holds of 64 columns
             const int col = c + (lane & 7) * 8;
 #pragma unroll
