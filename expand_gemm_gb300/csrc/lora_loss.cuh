@@ -26,7 +26,7 @@ __device__ __forceinline__ LossRow loss_row(float total, float ref, float logit)
     const float d = logit - ref;
     if (total == 0.0f) {                          // the target is the only column left
         r.lse2 = logit;
-        r.loss = r.inv = r.share = 0.0f;
+        r.loss = r.inv = r.share = logit - logit; // 0, or NaN where the logit is
     } else if (d >= 0.0f) {
         const float back = total * exp2f(-d);     // the others relative to the target
         r.loss = log1pf(back);

@@ -228,7 +228,9 @@ __global__ void __launch_bounds__(LR_JOIN_THREADS) loss_row_join_kernel(const Lo
         __syncthreads();
         for (int s = tid; s < p.slots; s += LR_JOIN_THREADS) {
             const float2 x = p.stat[s * p.nt + t];
-            sum += x.x > -INFINITY ? x.y * exp2f(x.x - top) : 0.0f;
+            // a block without a reference has a sum of 0, or NaN if that is
+            // all that its logits were: the row's loss is then NaN too
+            sum += x.x > -INFINITY ? x.y * exp2f(x.x - top) : x.y;
         }
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (lane == 0) s_red[warp] = sum;

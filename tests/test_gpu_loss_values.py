@@ -1,0 +1,46 @@
+"""lora_cross_entropy where values break or lie far out: NaN in valid rows and
+in the head, a tile of the vocabulary that holds nothing but the target,
+targets that are sure although their logit is negative, and logits beyond
+1e9.  References in 64 bits; tolerances as in test_gpu_loss, or stated."""
+import math
+
+import pytest
+import torch
+
+from test_gpu_loss import check, in_64_bits, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dh", [True, False])
+@pytest.mark.parametrize("where", ["row", "entry"])
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_nan_in_a_valid_row(T, where, dh):
+    hidden, weight, targets, share = make(T, 256, 900, 51, masked=0.0)
+    ref = in_64_bits(hidden, weight, targets, share)
+    if where == "row":
+        hidden[0] = math.nan
+    else:
+        hidden[0, 100] = math.nan
+    got = run(hidden, weight, targets, share, head=False, dh=dh)
+    assert torch.isnan(got["loss"][0]) and torch.isnan(got["lse"][0])
+    assert got["dh"] is None or torch.isnan(got["dh"][0].float()).all()
+    check({k: None if got[k] is None else got[k][1:] for k in ("loss", "lse", "dh")},
+          {k: v[1:] for k, v in ref.items()}, ("loss", "lse", "dh"))
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 70])
+@pytest.mark.parametrize("rows", [slice(7, 8), slice(0, 128), slice(0, 900)])
+def test_nan_in_the_head_reaches_every_token(T, rows):
+    hidden, weight, targets, share = make(T, 64, 900, 53, masked=0.0)
+    weight[rows] = math.nan
+    got = run(hidden, weight, targets, share, head=False)
+    for k in ("loss", "lse", "dh"):
+        assert torch.isnan(got[k].float()).all(), k
+
+
+def test_one_column_whose_logit_is_nan():
+    for T in (1, 2, 5):
+        got = run(torch.full((T, 8), math.nan).bfloat16(), torch.ones((1, 8)).bfloat16(),
+                  torch.zeros(T, dtype=torch.int32), torch.ones(T), head=False)
+        assert torch.isnan(got["loss"]).all() and torch.isnan(got["dh"].float()).all()
