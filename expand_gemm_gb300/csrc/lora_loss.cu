@@ -574,13 +574,13 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs 
         const float2 *stat = l.stat + row;
         const float have = float(l.ref[row]), old = l.sum[row];
         float sum = 0.0f, own = -INFINITY;
-        bool used = old > 0.0f;                     // something took the row's reference
+        bool used = old != 0.0f;                    // something took the row's reference (or was NaN)
 #pragma unroll 4
         for (int j = lane; j < a.tiles; j += 32) {
             const float2 s = stat[int64_t(j) * l.tokens];
             if (s.x == have) {
                 sum += s.y;
-                used = used || s.y > 0.0f;
+                used = used || s.y != 0.0f;
             } else {
                 own = fmaxf(own, s.x);
             }

@@ -39,6 +39,18 @@ def test_nan_in_the_head_reaches_every_token(T, rows):
         assert torch.isnan(got[k].float()).all(), k
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 40])
+def test_a_tile_of_nan_beside_tiles_far_below(T):
+    """The other tiles take references of their own."""
+    g = torch.Generator().manual_seed(55)
+    weight = (-3.2 + 0.01 * torch.randn((512, 64), generator=g)).bfloat16()
+    weight[:128] = math.nan
+    targets = torch.full((T,), 300, dtype=torch.int32)
+    got = run(torch.ones((T, 64)).bfloat16(), weight, targets, torch.ones(T), head=False)
+    for k in ("loss", "lse", "dh"):
+        assert torch.isnan(got[k].float()).all(), k
+
+
 def test_one_column_whose_logit_is_nan():
     for T in (1, 2, 5):
         got = run(torch.full((T, 8), math.nan).bfloat16(), torch.ones((1, 8)).bfloat16(),
