@@ -629,9 +629,11 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs 
         if (!s_off[q]) continue;
         const int r = blockIdx.x * LS_JOIN_ROWS + q;
         for (int j = 0; j < a.tiles; ++j) {
-            const float was = l.stat[int64_t(j) * l.tokens + r].x;
-            if (was == s_new[q]) continue;
-            const float f = exp2f(was - s_new[q]);
+            const float2 was = l.stat[int64_t(j) * l.tokens + r];
+            // a tile of zeros (nothing but the target, say) may have kept a
+            // reference far above the new one: 0 * inf
+            if (was.x == s_new[q] || was.y == 0.0f) continue;
+            const float f = exp2f(was.x - s_new[q]);
             uint32_t *at = reinterpret_cast<uint32_t *>(l.p + int64_t(r) * l.piece + j * PG_HALF);
             for (int i = threadIdx.x; i < PG_HALF / 2; i += THREADS)
                 at[i] = pack_bf16x2(bf16_lo(at[i]) * f, bf16_hi(at[i]) * f);

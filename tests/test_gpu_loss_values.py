@@ -56,3 +56,15 @@ def test_one_column_whose_logit_is_nan():
         got = run(torch.full((T, 8), math.nan).bfloat16(), torch.ones((1, 8)).bfloat16(),
                   torch.zeros(T, dtype=torch.int32), torch.ones(T), head=False)
         assert torch.isnan(got["loss"]).all() and torch.isnan(got["dh"].float()).all()
+
+
+@pytest.mark.parametrize("V", [129, 257, 1025])
+@pytest.mark.parametrize("level", [-3.2, -0.8, 3.2])
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_tile_that_holds_only_the_target(T, level, V):
+    """The last column is the target and alone in its tile, the others lie
+    about 64 level above zero."""
+    g = torch.Generator().manual_seed(57)
+    weight = (level + 0.02 * torch.randn((V, 64), generator=g)).bfloat16()
+    a = (torch.ones((T, 64)).bfloat16(), weight, torch.full((T,), V - 1, dtype=torch.int32), torch.ones(T))
+    check(run(*a), in_64_bits(*a))
