@@ -617,7 +617,8 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     buffer the fp32 buffer it left, meta the batch's metadata.
 
     Each output is optional and bf16.  dx [T, H]: the adapters' part is added
-    to it, or with add_inputs=False it is overwritten.  d_lora_a, d_lora_b,
+    to it, or with add_inputs=False it is overwritten; it may be dy or x
+    itself (all of them are read before it is written).  d_lora_a, d_lora_b,
     d_lora_bias: one tensor (or None) per slice, shaped as the weights and
     biases, overwritten; adapters without tokens get zeros."""
     index = meta.no_lora_flag.get_device()

@@ -747,6 +747,15 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
         e = launch_kernel(join_u_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), tab, st, q);
         if (e != cudaSuccess) return int(e);
     }
+    const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
+    if (w_tc) {
+        if (int err = launch_grad_w_tc(p, RP, st)) return err;
+    } else if (items > 0) {
+        const int64_t grid = items < resident(ws) ? items : resident(ws);
+        e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);
+        if (e != cudaSuccess) return int(e);
+    }
+    // dx last: it may be written over dy or x, which the kernels before read
     if (p.T > 0 && p.dx != nullptr) {
         tc = RP >= 64 ? launch_grad_x_tc(p, RP, st) : -1;
         if (tc > 0) return tc;
@@ -756,13 +765,6 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
             e = launch_kernel(grad_x_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), xs, st, p);
             if (e != cudaSuccess) return int(e);
         }
-    }
-    const int64_t items = int64_t(p.L) * p.block_end[2 * p.S - 1];
-    if (w_tc) return launch_grad_w_tc(p, RP, st);
-    if (items > 0) {
-        const int64_t grid = items < resident(ws) ? items : resident(ws);
-        e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);
-        if (e != cudaSuccess) return int(e);
     }
     return LORA_OK;
 }

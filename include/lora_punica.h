@@ -394,6 +394,9 @@ int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden_size, in
  *   lora_a, lora_b, slice_sizes, num_slices, rank, scale, meta: those of
  *                the forward pass; `meta` prepared for these tokens.
  *   dx           NULL or device bf16 [num_tokens, dx_ld], any alignment.
+ *                May be dy or x, or overlap them (a residual layer's gradient
+ *                in place: dy is read before dx is written).  No other output
+ *                may overlap an input or another output.
  *   add_inputs   nonzero: the adapters' part is added to dx (rows of tokens
  *                without an adapter are not touched); zero: dx is
  *                overwritten (those rows with zeros).

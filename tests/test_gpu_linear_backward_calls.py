@@ -1,0 +1,56 @@
+"""lora_linear_backward as callers use it: dx written over dy or over x,
+weights with room for more adapters than the metadata names, sums that are
+exact (a lost or doubled token shows in any element), and norms."""
+import math
+
+import pytest
+import torch
+
+import expand_gemm_gb300 as eg
+from test_gpu_linear_backward import LARGE, in_64_bits, make
+
+pytestmark = pytest.mark.gpu
+
+# T, H = sum of the widths, r, L, widths, runs: mma.sync and tcgen05 forms
+SQUARE = [(5, 64, 8, 2, (64,), 1), (200, 136, 16, 3, (72, 64), 3), (700, 264, 32, 5, (264,), 7),
+          (300, 1000, 40, 5, (523, 477), 30), (3500, 1288, 128, 4, (1024, 128, 136), 300),
+          (5000, 1096, 64, 3, (1000, 96), 50)]
+
+
+def grads(c):
+    def blank(shape):
+        return torch.full(shape, math.nan, dtype=torch.bfloat16, device="cuda")
+    return dict(d_lora_a=[blank(a.shape) for a in c["A"]], d_lora_b=[blank(b.shape) for b in c["B"]],
+                d_lora_bias=[blank(b.shape[:2]) for b in c["B"]])
+
+
+def call(c, dy, x, dx, add, out, meta=None):
+    if meta is None:
+        meta = eg.LoRAKernelMeta.make(c["L"], c["x"].shape[0], "cuda")
+        meta.prepare_tensors(c["ids"].cuda())
+    eg.lora_linear_backward(dy, x, c["buf"].cuda(), [a.cuda() for a in c["A"]], [b.cuda() for b in c["B"]],
+                            c["scale"], meta, dx=dx, add_inputs=add, **out)
+    assert int(meta.error_word) == 0
+
+
+@pytest.mark.parametrize("T,H,r,L,widths,runs", SQUARE)
+@pytest.mark.parametrize("add", [True, False])
+@pytest.mark.parametrize("over", ["dy", "x"])
+def test_dx_in_place(over, add, T, H, r, L, widths, runs):
+    """The same bits as with a dx of its own that held the same values."""
+    assert sum(widths) == H
+    c = make(T, H, r, L, widths, 61, runs=runs)
+    dy, x = c["dy"].cuda(), c["x"].cuda()
+    want, dx = grads(c), (dy if over == "dy" else x).clone()
+    call(c, dy, x, dx, add, want)
+    got = grads(c)
+    call(c, dy, x, dy if over == "dy" else x, add, got)
+    for k in want:
+        for s, (u, v) in enumerate(zip(want[k], got[k])):
+            assert torch.equal(u, v), (k, s)
+    assert torch.equal(dx, dy if over == "dy" else x)
+
+
+EXACT = [(1, 64, 8, 1, (64,), 1), (65, 136, 32, 2, (200,), 65), (700, 200, 48, 1, (130, 128), 700),
+         (1300, 264, 16, 1, (1100,), 1300), (2100, 136, 24, 3, (75, 61), 1)] + [
+         (T, H, r, L, w, runs) for T, H, r, L, w, runs in LARGE if len(w) <= 3]
