@@ -607,6 +607,14 @@ def _grads(grads, name: str, like, index: int):
     return _PTRS[len(ptrs)](*ptrs)
 
 
+def _clear_behind(named: int, *grads) -> None:
+    """Zeros in the gradients of the adapters that the metadata does not name."""
+    for of_slices in grads:
+        for g in (of_slices,) if isinstance(of_slices, torch.Tensor) else of_slices or ():
+            if g is not None:
+                g.detach()[named:].zero_()
+
+
 def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor, lora_a_stacked,
                          lora_b_stacked, scale: float, meta: LoRAKernelMeta, *,
                          dx: Optional[torch.Tensor] = None, add_inputs: bool = True,
@@ -620,7 +628,8 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     to it, or with add_inputs=False it is overwritten; it may be dy or x
     itself (all of them are read before it is written).  d_lora_a, d_lora_b,
     d_lora_bias: one tensor (or None) per slice, shaped as the weights and
-    biases, overwritten; adapters without tokens get zeros."""
+    biases, overwritten; adapters without tokens get zeros, and so do those
+    that the weights hold beyond the metadata's."""
     index = meta.no_lora_flag.get_device()
     try:
         ok = (index >= 0 and dy.dtype is _BF16 and x.dtype is _BF16 and buffer.dtype is _F32 and dy.get_device() == index
@@ -643,11 +652,13 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
     for s in a_shapes:
         if s != (L, r, H):
             raise ValueError("lora_a_stacked shapes must all be [%d, %d, %d]" % (L, r, H))
+    Lb = b_shapes[0][0]
     for s in b_shapes:
-        if s[0] != L or s[2] != r:
-            raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (L, r))
-    if L != meta.max_loras:
-        raise ValueError("the weights hold %d LoRAs, the metadata %d" % (L, meta.max_loras))
+        if s[0] != Lb or s[2] != r:
+            raise ValueError("lora_b_stacked shapes must all be [%d, n, %d]" % (Lb, r))
+    named = meta.max_loras
+    if L < named or Lb < named:
+        raise ValueError("the weights hold %d LoRAs, metadata expects %d" % (min(L, Lb), named))
     sizes = [s[1] for s in b_shapes]
     rows, cols, dy_ld = _rows(dy, "dy")
     if rows != T or cols != sum(sizes):
@@ -661,14 +672,16 @@ def lora_linear_backward(dy: torch.Tensor, x: torch.Tensor, buffer: torch.Tensor
             raise ValueError("dx must be [%d, %d]" % (T, H))
         dx_ptr = dx.data_ptr()
     c_sizes = _SIZES[S](*sizes)
-    _call_with("lora_linear_backward", workspace, x.device, (T, H, c_sizes, S, r, L),
+    _call_with("lora_linear_backward", workspace, x.device, (T, H, c_sizes, S, r, named),
                dy.data_ptr(), dy_ld, T, x.data_ptr(), H, x_ld, buffer.data_ptr(), a_ptrs,
                b_ptrs, c_sizes, S, r, float(scale), dx_ptr, dx_ld, 1 if add_inputs else 0,
                _grads(d_lora_a, "d_lora_a", a_shapes, index),
                _grads(d_lora_b, "d_lora_b", b_shapes, index),
                None if d_lora_bias is None else
-               _grads(d_lora_bias, "d_lora_bias", [(L, n) for n in sizes], index),
+               _grads(d_lora_bias, "d_lora_bias", [(Lb, n) for n in sizes], index),
                ctypes.byref(meta.c))
+    if L > named or Lb > named:
+        _clear_behind(named, d_lora_a, d_lora_b, d_lora_bias)
 
 
 def lora_orthogonalize_workspace(count: int, rows: int, cols: int, *, device="cuda") -> int:

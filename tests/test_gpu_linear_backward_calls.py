@@ -51,6 +51,29 @@ def test_dx_in_place(over, add, T, H, r, L, widths, runs):
     assert torch.equal(dx, dy if over == "dy" else x)
 
 
+@pytest.mark.parametrize("T,H,r,widths", [(90, 72, 16, (40, 33)), (700, 264, 64, (264, 64)), (3500, 1288, 128, (136, 72))])
+def test_weights_with_more_adapters_than_the_metadata(T, H, r, widths):
+    """As lora_expand takes them: the rest have no tokens, so zero gradients."""
+    named, spare = 3, 2
+    c = make(T, H, r, named, widths, 67, runs=5)
+    want = grads(c)
+    call(c, c["dy"].cuda(), c["x"].cuda(), None, True, want)
+    g = torch.Generator().manual_seed(1)
+    meta = eg.LoRAKernelMeta.make(named, T, "cuda")
+    meta.prepare_tensors(c["ids"].cuda())
+    for k, n in (("A", spare), ("B", spare + 1)):
+        c[k] = [torch.cat([w, torch.randn((n,) + w.shape[1:], generator=g).bfloat16()]) for w in c[k]]
+    got = grads(c)
+    dx = c["dx0"].cuda()
+    call(c, c["dy"].cuda(), c["x"].cuda(), dx, True, got, meta)
+    for k in want:
+        for s, (u, v) in enumerate(zip(want[k], got[k])):
+            assert torch.equal(u, v[:named]) and (v[named:] == 0).all(), (k, s)
+    with pytest.raises(ValueError):                  # fewer adapters than the metadata
+        few = {k: [w[:2].contiguous() for w in c[k]] for k in ("A", "B")}
+        call(dict(c, **few), c["dy"].cuda(), c["x"].cuda(), None, True, {}, meta)
+
+
 EXACT = [(1, 64, 8, 1, (64,), 1), (65, 136, 32, 2, (200,), 65), (700, 200, 48, 1, (130, 128), 700),
          (1300, 264, 16, 1, (1100,), 1300), (2100, 136, 24, 3, (75, 61), 1)] + [
          (T, H, r, L, w, runs) for T, H, r, L, w, runs in LARGE if len(w) <= 3]
