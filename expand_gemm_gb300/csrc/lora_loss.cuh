@@ -19,7 +19,8 @@ struct LossRow {
 
 // total: the terms of the columns other than the target's, in units of
 // 2^ref; logit: the target's exponent.  1 - p_y is total over everything, so
-// a sure target costs no digits.
+// a sure target costs no digits: where the others weigh less than it, the
+// loss is log1p of their ratio, wherever the reference lies.
 __device__ __forceinline__ LossRow loss_row(float total, float ref, float logit)
 {
     LossRow r;
@@ -27,7 +28,7 @@ __device__ __forceinline__ LossRow loss_row(float total, float ref, float logit)
     if (total == 0.0f) {                          // the target is the only column left
         r.lse2 = logit;
         r.loss = r.inv = r.share = logit - logit; // 0, or NaN where the logit is
-    } else if (d >= 0.0f) {
+    } else if (total <= exp2f(d)) {
         const float back = total * exp2f(-d);     // the others relative to the target
         r.loss = log1pf(back);
         r.lse2 = logit + r.loss * LOSS_LOG2E;

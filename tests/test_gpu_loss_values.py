@@ -68,3 +68,24 @@ def test_a_tile_that_holds_only_the_target(T, level, V):
     weight = (level + 0.02 * torch.randn((V, 64), generator=g)).bfloat16()
     a = (torch.ones((T, 64)).bfloat16(), weight, torch.full((T,), V - 1, dtype=torch.int32), torch.ones(T))
     check(run(*a), in_64_bits(*a))
+
+
+@pytest.mark.parametrize("T", [1, 2, 40])
+@pytest.mark.parametrize("others", [-30.0, -38.0])
+def test_sure_of_a_target_with_a_negative_logit(T, others):
+    """The loss is about the sum of the others' terms: its error is relative,
+    that of the logits' difference (2^-17 of the sum of magnitudes) and a few
+    roundings."""
+    g = torch.Generator().manual_seed(59)
+    H, V = 64, 600
+    weight = (others / H + 0.002 * torch.randn((V, H), generator=g)).bfloat16()
+    weight[11] = -(2.0 + torch.rand(H, generator=g)).bfloat16() / 32
+    hidden = torch.ones((T, H)).bfloat16()
+    targets = torch.full((T,), 11, dtype=torch.int32)
+    ref = in_64_bits(hidden, weight, targets, torch.ones(T))
+    assert (ref["loss"] < 1e-5).all() and (ref["loss"] > 1e-14).all()
+    got = run(hidden, weight, targets, torch.ones(T), head=False)
+    mag = (hidden.double().abs() @ weight.double().abs().T).amax(1)
+    off = (got["loss"].double().cpu() - ref["loss"]).abs()
+    assert (off <= ref["loss"] * (2.0 ** -17 * mag + 2.0 ** -19)).all(), (off / ref["loss"]).max()
+    check(got, ref, ("lse", "dh"))
