@@ -45,6 +45,7 @@ namespace lora {
 constexpr int LS_PIECE_ELEMS = 128 << 20;     // tokens x columns of one piece's scratch
 constexpr int LS_MIN_PIECE = 1024;            // columns
 constexpr int LS_WINDOW = 60;                 // exponents a tile may be off the reference
+constexpr float LS_FAR = 1048576.0f;          // references whose rounding is no longer small beside 1
 constexpr int LS_MAX_SPLIT = 8;
 constexpr int LS_PACK_TOKENS = 4;             // tokens of one block of pack_kernel
 constexpr int LS_PACK_THREADS = 256;
@@ -56,7 +57,7 @@ struct LossLayout {
     int64_t tokens;        // T rounded up to whole tiles
     int64_t piece;         // columns of a piece, a multiple of PG_TILE
     int pieces, split;
-    int64_t count, row, target, weight, ref, sum, logit, factor, inv, share, lse, stat, h, p, acc;
+    int64_t count, row, target, weight, ref, sum, logit, factor, inv, share, stat, h, p, acc;
     int64_t bytes;
     bool rows;             // one or two tokens: logit, stat and acc of lora_loss_row.cu alone
 };
@@ -93,7 +94,7 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
     };
     l.rows = !weight_grad && loss_row_fits(int32_t(T), int32_t(H));
     if (l.rows) {
-        l.count = l.row = l.target = l.weight = l.ref = l.sum = l.factor = l.inv = l.share = l.lse = l.h = l.p = 0;
+        l.count = l.row = l.target = l.weight = l.ref = l.sum = l.factor = l.inv = l.share = l.h = l.p = 0;
         l.logit = take(T * 4);
         l.stat = take(loss_row_slots() * T * 8);
         l.acc = take(hidden_grad ? loss_row_slots() * T * H * 4 : 0);
@@ -110,7 +111,6 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
     l.factor = take(l.tokens * 4);
     l.inv = take(l.tokens * 4);
     l.share = take(l.tokens * 4);
-    l.lse = take(l.tokens * 4);
     l.stat = take(l.tokens * (l.piece / PG_HALF) * 8);
     l.h = take(l.tokens * packed_ld(H) * 2);
     l.p = take(hidden_grad || weight_grad ? l.tokens * l.piece * 2 : 0);
@@ -133,8 +133,8 @@ struct LossArgs {
     int32_t *error_word;
     // workspace
     int32_t *count;                    // tokens with a target
-    int32_t *row, *target, *ref;
-    float *wt, *sum, *logit, *factor, *inv, *share, *lse;
+    int32_t *row, *target;
+    float *ref, *wt, *sum, *logit, *factor, *inv, *share;
     float2 *stat;                      // [128 columns each][tokens]: reference, sum
     uint16_t *h, *p;
     float *acc;
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
             p.row[r] = -1;
             p.target[r] = -1;
             p.wt[r] = 0.0f;
-            p.ref[r] = 0;
+            p.ref[r] = 0.0f;
             p.sum[r] = 0.0f;
             p.logit[r] = 0.0f;
         }
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
             p.row[to] = t;
             p.target[to] = target;
             p.wt[to] = p.token_weight != nullptr ? p.token_weight[t] : 1.0f;
-            p.ref[to] = 0;
+            p.ref[to] = 0.0f;
             p.sum[to] = 0.0f;
             p.logit[to] = d * LOSS_LOG2E;
         } else if (t < p.T) {
@@ -302,7 +302,9 @@ __device__ __forceinline__ float exp2_fast(float x)
 
 // Logits of a piece: 256 tokens x 256 columns a tile, tokens innermost (the
 // packed rows stay in L2 while a few tiles of W pass).
-// GRAD: the sums are known, the scratch becomes w (p - [y]).
+// GRAD: the sums are known, the scratch becomes w (p - [y]); p is the term
+// relative to the row's reference times 1 / sum (relative to the logarithm of
+// the sum it would lose that logarithm's rounding).
 template <bool GRAD>
 __global__ void __launch_bounds__(PG_THREADS, 1)
 logits_kernel(const __grid_constant__ LossGemm g)
@@ -325,8 +327,8 @@ logits_kernel(const __grid_constant__ LossGemm g)
         uint32_t v[32];
         float ref, scale = 1.0f, q = 0.0f, sum = 0.0f;
         if constexpr (GRAD) {
-            ref = l.lse[row];
-            scale = l.wt[row];
+            ref = l.ref[row];
+            scale = l.inv[row];
             q = -l.share[row];
         } else {
             float top = -INFINITY;
@@ -347,12 +349,16 @@ logits_kernel(const __grid_constant__ LossGemm g)
                         if (c + j < lim) top = fmaxf(top, __uint_as_float(v[j]));
                 }
             }
-            const int have = l.ref[row];
             top *= LOSS_LOG2E;
-            ref = float(have);
+            ref = l.ref[row];
             if (top > -INFINITY && !(fabsf(top - ref) <= float(LS_WINDOW)))
-                ref = ceilf(fminf(fmaxf(top, -1e9f), 1e9f));
+                ref = ceilf(fminf(fmaxf(top, -LOSS_MAX_REF), LOSS_MAX_REF));
         }
+        // Near zero the exponent and its difference to the reference are one
+        // operation, rounded once.  Far out it has to be rounded as the
+        // reference and the target's were, or the three do not match.
+        const bool far = fabsf(ref) >= LS_FAR;
+        const float pre = far ? LOSS_LOG2E : 1.0f, mul = far ? 1.0f : LOSS_LOG2E;
         for (int c = c0; c < c_end; c += 32) {
             if (GRAD ? c >= lim : (c >= lim && !g.store)) break;
             uint32_t pk[16];
@@ -362,7 +368,7 @@ logits_kernel(const __grid_constant__ LossGemm g)
                 float e[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    e[j] = exp2_fast(fmaf(__uint_as_float(v[j]), LOSS_LOG2E, -ref));
+                    e[j] = exp2_fast(fmaf(__uint_as_float(v[j]) * pre, mul, -ref));
                 if (c + 32 > lim) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs 
     if (lane == 0) s_off[k] = 0;
     if (in) {
         const float2 *stat = l.stat + row;
-        const float have = float(l.ref[row]), old = l.sum[row];
+        const float have = l.ref[row], old = l.sum[row];
         float sum = 0.0f, own = -INFINITY;
         bool used = old != 0.0f;                    // something took the row's reference (or was NaN)
 #pragma unroll 4
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs 
             if (ref != have || own > -INFINITY) {
                 s_off[k] = a.store;
                 s_new[k] = ref;
-                l.ref[row] = int(ref);
+                l.ref[row] = ref;
             }
             l.sum[row] = total;
             l.factor[row] = f;
@@ -618,11 +624,10 @@ __global__ void __launch_bounds__(LS_JOIN_ROWS * 32) join_kernel(const JoinArgs 
                 if (l.logsumexp != nullptr) l.logsumexp[t] = r.lse2 * LOSS_LN2;
                 l.inv[row] = w * r.inv;
                 l.share[row] = w * r.share;
-                l.lse[row] = r.lse2;
             }
         }
     } else if (a.last && lane == 0 && row < l.tokens) {
-        l.inv[row] = l.share[row] = l.lse[row] = 0.0f;
+        l.inv[row] = l.share[row] = 0.0f;
     }
     __syncthreads();
     for (int q = 0; q < LS_JOIN_ROWS; ++q) {
@@ -840,13 +845,12 @@ LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, i
     l.row = reinterpret_cast<int32_t *>(ws + lay.row);
     l.target = reinterpret_cast<int32_t *>(ws + lay.target);
     l.wt = reinterpret_cast<float *>(ws + lay.weight);
-    l.ref = reinterpret_cast<int32_t *>(ws + lay.ref);
+    l.ref = reinterpret_cast<float *>(ws + lay.ref);
     l.sum = reinterpret_cast<float *>(ws + lay.sum);
     l.logit = reinterpret_cast<float *>(ws + lay.logit);
     l.factor = reinterpret_cast<float *>(ws + lay.factor);
     l.inv = reinterpret_cast<float *>(ws + lay.inv);
     l.share = reinterpret_cast<float *>(ws + lay.share);
-    l.lse = reinterpret_cast<float *>(ws + lay.lse);
     l.stat = reinterpret_cast<float2 *>(ws + lay.stat);
     l.h = reinterpret_cast<uint16_t *>(ws + lay.h);
     l.p = reinterpret_cast<uint16_t *>(ws + lay.p);

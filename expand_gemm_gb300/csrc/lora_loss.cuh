@@ -9,6 +9,7 @@ namespace lora {
 
 constexpr float LOSS_LOG2E = 1.4426950408889634f;
 constexpr float LOSS_LN2 = 0.6931471805599453f;
+constexpr float LOSS_MAX_REF = 3.4028235e38f;     // references stay finite where exponents do not
 
 // What a finished row gives: its loss, the base-2 log of its sum, the factor
 // of its accumulated terms (of 2^-ref each) and of the target's row of W
@@ -29,7 +30,8 @@ __device__ __forceinline__ LossRow loss_row(float total, float ref, float logit)
         r.lse2 = logit;
         r.loss = r.inv = r.share = logit - logit; // 0, or NaN where the logit is
     } else if (total <= exp2f(d)) {
-        const float back = total * exp2f(-d);     // the others relative to the target
+        // the others relative to the target; NaN for an infinite one
+        const float back = total * exp2f(-d) + (d - d);
         r.loss = log1pf(back);
         r.lse2 = logit + r.loss * LOSS_LOG2E;
         r.share = back / (1.0f + back);

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(LR_THREADS, RowShape<CH, NT>::BLOCKS) loss_row
                 top = fmaxf(top, d);
             }
             if (top > ref[t] + float(LR_WINDOW)) {       // and the first time
-                const float to = ceilf(fminf(top, 1e9f));
+                const float to = ceilf(fminf(top, LOSS_MAX_REF));
                 const float f = exp2f(ref[t] - to);      // 0 from -infinity
                 ref[t] = to;
                 sum[t] *= f;

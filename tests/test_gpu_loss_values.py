@@ -89,3 +89,54 @@ def test_sure_of_a_target_with_a_negative_logit(T, others):
     off = (got["loss"].double().cpu() - ref["loss"]).abs()
     assert (off <= ref["loss"] * (2.0 ** -17 * mag + 2.0 ** -19)).all(), (off / ref["loss"]).max()
     check(got, ref, ("lse", "dh"))
+
+
+@pytest.mark.parametrize("T", [1, 2, 70])
+@pytest.mark.parametrize("size", [2.0 ** 31, -2.0 ** 31, 2.0 ** 45, -2.0 ** 45, -2.0 ** 100])
+def test_equal_logits_far_from_zero(T, size):
+    """Every logit is exactly `size`: the loss is log V, the terms 1 / V."""
+    H, V = 64, 700
+    hidden = torch.zeros((T, H))
+    weight = torch.zeros((V, H))
+    hidden[:, 0] = abs(size) ** 0.5 if math.log2(abs(size)) % 2 == 0 else (abs(size) / 2) ** 0.5
+    weight[:, 0] = size / hidden[0, 0]
+    hidden[:, 1:] = 0.5
+    hidden, weight = hidden.bfloat16(), weight.bfloat16()
+    assert float(hidden[0, 0]) * float(weight[0, 0]) == size
+    targets = torch.arange(T, dtype=torch.int32) * 9
+    got = run(hidden, weight, targets, torch.ones(T), head=T > 2)
+    assert ((got["loss"].double().cpu() - math.log(V)).abs() <= 2.0 ** -18).all(), got["loss"]
+    # sum p W - W_y = 0 up to the terms' roundings, the other columns of W are zero
+    dh = got["dh"].double().cpu()
+    assert (dh[:, 0].abs() <= 2.0 ** -7 * abs(float(weight[0, 0]))).all() and (dh[:, 1:] == 0).all()
+    if T > 2:
+        want = (torch.full((V, T), 1.0 / V, dtype=torch.float64))
+        want[targets.long(), torch.arange(T)] -= 1.0
+        mag = want.abs() @ hidden.double().abs()
+        want = want @ hidden.double()
+        assert ((got["dw"].double().cpu() - want).abs() <= 2.0 ** -8 * (want.abs() + mag)).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 70])
+@pytest.mark.parametrize("others", [0.0, 2.0 ** 30])
+def test_an_infinite_target_logit(T, others):
+    """Past fp32: logsumexp - logit is infinity - infinity, not a loss of 0."""
+    hidden = torch.full((T, 64), 2.0 ** 100).bfloat16()
+    weight = torch.full((300, 64), others).bfloat16()
+    weight[5] = 2.0 ** 30
+    got = run(hidden, weight, torch.full((T,), 5, dtype=torch.int32), torch.ones(T), head=False)
+    assert torch.isnan(got["loss"]).all() and torch.isnan(got["dh"].float()).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 70])
+def test_infinite_logits_of_other_columns(T):
+    hidden = torch.full((T, 64), 2.0 ** 100).bfloat16()
+    weight = torch.zeros((300, 64)).bfloat16()
+    weight[200] = 2.0 ** 30
+    got = run(hidden, weight, torch.full((T,), 5, dtype=torch.int32), torch.ones(T), head=False)
+    assert (got["loss"] == math.inf).all()
+    weight[200] = -2.0 ** 30                 # minus infinity: no term at all
+    a = (hidden, weight, torch.full((T,), 5, dtype=torch.int32), torch.ones(T))
+    got = run(*a, head=False)
+    assert ((got["loss"] - math.log(299.0)).abs() <= 2.0 ** -18).all()
+    assert torch.isfinite(got["dh"].float()).all()
