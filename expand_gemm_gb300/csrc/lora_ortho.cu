@@ -575,9 +575,7 @@ static int run_ortho(const OrthoArgs &p, cudaStream_t st)
 
 static bool ortho_sizes_ok(int32_t count, int32_t rows, int32_t cols)
 {
-    // count is a grid's dimension
-    return count >= 0 && count <= 65535 && rows >= 1 && cols >= 8 && cols % 8 == 0 &&
-           (rows <= OR_MAX_RANK || cols <= OR_MAX_RANK);
+    return count >= 0 && rows >= 1 && cols >= 8 && cols % 8 == 0 && (rows <= OR_MAX_RANK || cols <= OR_MAX_RANK);
 }
 
 }  // namespace lora

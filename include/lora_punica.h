@@ -427,7 +427,7 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
                                        int32_t rank, int32_t max_loras);
 
 /*
- * lora_orthogonalize -- Newton-Schulz steps on `count` stacked matrices, as
+ * lora_orthogonalize -- Newton-Schulz steps on `count` (>= 0) stacked matrices, as
  * the Muon optimiser takes them on an update: for each matrix
  *   X = U / (|U|_F + eps);  steps times: X <- a X + (b G + c G^2) X, G = X X^T
  * (on the short side), out = scale X.  With a = 3.4445, b = -4.7750,
@@ -436,7 +436,6 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
  *   update       device [count, rows, cols], dense, 16-byte aligned: bf16
  *                (update_f32 == 0) or fp32.  Stacked adapter gradients or
  *                momenta: A [.., rank, hidden], B [.., n, rank].
- *   count        at most 65535.
  *   rows, cols   min(rows, cols) <= 128 (an adapter's rank), cols a
  *                multiple of 8.
  *   steps        >= 1.
