@@ -689,6 +689,9 @@ def lora_orthogonalize_workspace(count: int, rows: int, cols: int, *, device="cu
     return _workspace_bytes("lora_orthogonalize_workspace", device, count, rows, cols)
 
 
+_LONG_RUN = math.log(512.0)         # steps x log |a| above which a run is long
+
+
 def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 5,
                        scale: float = 1.0, eps: float = 1e-7,
                        coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
@@ -699,7 +702,10 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
     fp32; the shorter side, an adapter's rank, at most 128) divided by its
     norm and taken through ``steps`` of X <- a X + (b G + c G^2) X, G = X X^T;
     out (bf16, like update, or update itself) receives scale * X.  Bit 30 of
-    error_word (int32 [1]) is set if a bounded wait on the GPU ran out."""
+    error_word (int32 [1]) is set if a bounded wait on the GPU ran out.  Runs
+    of steps with |a|^steps above 512 (six of the default ones) are many times
+    slower: they form X and its products afresh every few steps, a group of
+    matrices at a time (larger groups with a larger workspace)."""
     index = _gpu(update, "update")
     f32 = update.dtype is _F32
     if not f32 and update.dtype is not _BF16:
@@ -716,6 +722,11 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
     rows, cols = update.shape[-2:]
     count = update.numel() // max(1, rows * cols)
     a, b, c = coefficients
+    if workspace is None and count > 1 and abs(a) > 1.0 and steps * math.log(abs(a)) > _LONG_RUN:
+        # matrices of a long run are taken by groups: all at once, up to 4 GB
+        one = lora_orthogonalize_workspace(1, rows, cols, device=update.device)
+        need = lora_orthogonalize_workspace(count, rows, cols, device=update.device)
+        workspace = torch.empty(max(need, min(count * one, 1 << 32)), dtype=_U8, device=update.device)
     _call_with("lora_orthogonalize", workspace, update.device, (count, rows, cols), update.data_ptr(),
                int(f32), count, rows, cols, int(steps), float(a), float(b), float(c), float(eps),
                float(scale), out.data_ptr(), _vector(error_word, "error_word", 1))

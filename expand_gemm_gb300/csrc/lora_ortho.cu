@@ -16,6 +16,10 @@
 // directions that U has little of, which cancel where U is large, so one
 // bf16 would show in the result.
 //
+// The errors of R grow by a^2 a step in directions that U lacks, so where
+// |a|^steps is above 512 the sum is taken afresh every few steps
+// (lora_ortho_long.cu).
+//
 // This file: ranks up to 32, on mma.sync, the steps in FFMA.
 // lora_ortho_tc.cu: ranks 33 to 128, on tcgen05 (whose tiles of 64 cost rank
 // 32 twice the time: 64 matrices of 11008 x 32 58 us here, 137 there; 8 of
@@ -536,6 +540,9 @@ static OrthoLayout ortho_layout(int32_t count, int32_t rows, int32_t cols, int s
     l.ctas = int(total < most ? total : most);
     l.p = (int64_t(l.ctas) + count) * l.rp * l.rp * 4;
     l.bytes = l.p + int64_t(count) * 2 * l.rp * l.rp * 2;
+    // a long run of steps takes its matrices by groups: one must fit
+    const int64_t one = ortho_long_bytes(l.r, l.n, l.rp);
+    if (l.bytes < one) l.bytes = one;
     return l;
 }
 
@@ -622,6 +629,8 @@ LORA_API int lora_orthogonalize(const void *update, int32_t update_f32, int32_t 
     p.p = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + l.p);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool tall = rows > cols;
+    if (pow(fabs(double(coef_a)), double(steps)) > OR_LONG_GROWTH)
+        return run_ortho_long(p, l.rp, update_f32 != 0, workspace, workspace_bytes, st);
     if (l.rp >= 64) return run_ortho_tc(p, l.rp, update_f32 != 0, st);
     if (l.rp == 16) {
         if (update_f32) return tall ? run_ortho<16, true, true>(p, st) : run_ortho<16, false, true>(p, st);

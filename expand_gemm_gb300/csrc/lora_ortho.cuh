@@ -58,4 +58,10 @@ int run_ortho_tc(OrthoArgs p, int rp, bool f32, cudaStream_t st);
 constexpr int OR_TC_UNIT = 64;
 constexpr int OR_TC_CTAS = 2;         // of the sum U U^T on an SM
 
+// Runs of steps that the r x r iteration does not hold (lora_ortho_long.cu):
+// |a|^steps above this.  Five steps of 3.4445 are 485, fifteen of 1.5 are 438.
+constexpr double OR_LONG_GROWTH = 512.0;
+int64_t ortho_long_bytes(int r, int n, int rp);       // of workspace, for one matrix
+int run_ortho_long(const OrthoArgs &o, int rp, bool f32, void *workspace, int64_t bytes, cudaStream_t st);
+
 }  // namespace lora

@@ -447,9 +447,16 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
  *
  * A zero matrix gives zeros; a matrix with a NaN or an infinity gives NaN in
  * its own place only.  |U|_F^2 and the products U U^T are summed in fp32 and
- * must be finite there (entries up to about 1e17).  The steps run on
- * r x r matrices in fp32 (every factor is a polynomial in U U^T); `out` is
- * rounded to bf16 once.  Deterministic.  Errors: LORA_ERR_NULL,
+ * must be finite there (entries up to about 1e17).  Up to |coef_a|^steps =
+ * 512 (five steps with 3.4445) all steps run on r x r matrices in fp32 (every
+ * factor is a polynomial in U U^T); the error is within 2% of the result's
+ * norm for updates of rank one, the worst, and below bf16's rounding for
+ * updates that lack no direction.  Longer runs form X and sum X X^T afresh
+ * every few steps, in fp32: many times slower, a group of matrices at a time
+ * (as many as the workspace holds in fp32 beside their sums; give more than
+ * asked for larger groups).  There a rounding grows by coef_a a step in
+ * directions that U lacks, as in any 32-bit iteration.  `out` is rounded to
+ * bf16 once.  Deterministic.  Errors: LORA_ERR_NULL,
  * LORA_ERR_SIZE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE.
  */
 int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, int32_t rows,
