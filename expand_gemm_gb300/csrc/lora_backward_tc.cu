@@ -75,6 +75,16 @@ __device__ __forceinline__ void join_rows(TcRows &r, int stride)
 // matrix, and running on, so that such rows join too.
 __device__ __forceinline__ int tc_no_row(int T, int row) { return T + row; }
 
+// The row to load for `tok`, read from the sorted list (a debug build takes
+// one outside the batch as none; TMA's own bounds would give zeros, silently).
+__device__ __forceinline__ int tc_row(const BackwardArgs &p, int tok, int row)
+{
+    if constexpr (kDebugChecks) {
+        if (checked_token(tok, p.T, p.error_word) < 0) return tc_no_row(p.T, row);
+    }
+    return tok;
+}
+
 __device__ __forceinline__ void tc_load_rows(const TcRows &r, uint32_t dst, const CUtensorMap *gather,
                                              const CUtensorMap *boxes, int col, uint32_t bar)
 {
@@ -282,10 +292,10 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
                 slot = slot + 1 == TC_W_SLOTS ? 0 : slot + 1;
                 const int row = k * 64 + r4;
                 TcRows rows;
-                rows.t[0] = row < it.count ? own.x : tc_no_row(p.T, row);
-                rows.t[1] = row + 1 < it.count ? own.y : tc_no_row(p.T, row + 1);
-                rows.t[2] = row + 2 < it.count ? own.z : tc_no_row(p.T, row + 2);
-                rows.t[3] = row + 3 < it.count ? own.w : tc_no_row(p.T, row + 3);
+                rows.t[0] = row < it.count ? tc_row(p, own.x, row) : tc_no_row(p.T, row);
+                rows.t[1] = row + 1 < it.count ? tc_row(p, own.y, row + 1) : tc_no_row(p.T, row + 1);
+                rows.t[2] = row + 2 < it.count ? tc_row(p, own.z, row + 2) : tc_no_row(p.T, row + 2);
+                rows.t[3] = row + 3 < it.count ? tc_row(p, own.w, row + 3) : tc_no_row(p.T, row + 3);
                 join_rows(rows, 2);
                 ahead();
                 const bool got = pg_wait(ring.empty + 8 * pos.stage, pos.phase ^ 1u, ring.abort);
@@ -921,7 +931,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_u_tc_kernel(const __grid_c
             TcRows rows;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                rows.t[j] = r0 + j < t128.count[seg] ? p.sorted[t128.start[seg] + r0 + j]
+                rows.t[j] = r0 + j < t128.count[seg] ? tc_row(p, p.sorted[t128.start[seg] + r0 + j], r0 + j)
                                                      : tc_no_row(p.T, r0 + j);
             join_rows(rows, 1);
             const int steps = (p.n[s] + 63) / 64;
