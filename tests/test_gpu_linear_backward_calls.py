@@ -77,3 +77,63 @@ def test_weights_with_more_adapters_than_the_metadata(T, H, r, widths):
 EXACT = [(1, 64, 8, 1, (64,), 1), (65, 136, 32, 2, (200,), 65), (700, 200, 48, 1, (130, 128), 700),
          (1300, 264, 16, 1, (1100,), 1300), (2100, 136, 24, 3, (75, 61), 1)] + [
          (T, H, r, L, w, runs) for T, H, r, L, w, runs in LARGE if len(w) <= 3]
+
+
+@pytest.mark.parametrize("T,H,r,L,widths,runs", EXACT)
+def test_exact_sums(T, H, r, L, widths, runs):
+    """Small whole numbers: every product and sum is exact in the kernels'
+    types (g below 256, sums below 2^24), so each output is the exact sum
+    rounded to bf16 once."""
+    c = make(T, H, r, L, widths, 71, runs=runs)
+    g = torch.Generator().manual_seed(T + r)
+
+    def whole(shape, low, high, share=1.0):
+        v = torch.randint(low, high + 1, shape, generator=g).float()
+        return v * (torch.rand(shape, generator=g) < share)
+    c["dy"] = whole(c["dy"].shape, -1, 1).bfloat16()
+    c["x"] = whole(c["x"].shape, -3, 3).bfloat16()
+    c["buf"] = whole(c["buf"].shape, -4, 4)
+    c["A"] = [whole(a.shape, -2, 2).bfloat16() for a in c["A"]]
+    c["B"] = [whole(b.shape, -1, 1, 0.1).bfloat16() for b in c["B"]]
+    c["dx0"] = whole(c["dx0"].shape, -8, 8).bfloat16()
+    off = 0
+    for s, w in enumerate(widths):
+        top = (c["dy"][:, off:off + w].double().abs() @ c["B"][s].double().abs().amax(0)).max()
+        assert top <= 256
+        off += w
+    ref, mag = in_64_bits(c, True)
+    assert max(float(m.max()) for k in ("dA", "dB", "dbias") for m in mag[k]) < 2 ** 24
+    out, dx = grads(c), c["dx0"].cuda()
+    call(c, c["dy"].cuda(), c["x"].cuda(), dx, True, out)
+    assert torch.equal(dx.cpu(), ref["dx"].bfloat16())
+    for k, name in (("d_lora_a", "dA"), ("d_lora_b", "dB"), ("d_lora_bias", "dbias")):
+        for s, (u, v) in enumerate(zip(out[k], ref[name])):
+            assert torch.equal(u.cpu(), v.bfloat16()), (name, s, int((u.cpu() != v.bfloat16()).sum()))
+
+
+@pytest.mark.parametrize("T,H,r,L,widths,runs", [(1200, 264, 16, 2, (1030, 8), 7)] + LARGE)
+def test_norms(T, H, r, L, widths, runs):
+    """Independent roundings (2^-9 of g or the buffer, and of the output) add
+    up by their squares: the norm of the error is at most 2^-8 of the root of
+    the summed squares of the output and of its products.  dbias is an fp32
+    sum rounded once."""
+    c = make(T, H, r, L, widths, 73, runs=runs)
+    ref, mag = in_64_bits(c, False)
+    out = grads(c)
+    call(c, c["dy"].cuda(), c["x"].cuda(), None, True, out)
+    for s, (u, v, m) in enumerate(zip(out["d_lora_bias"], ref["dbias"], mag["dbias"])):
+        off = (u.double().cpu() - v).abs() - 2.0 ** -8 * v.abs() - 2.0 ** -12 * m
+        assert (off <= 0).all(), ("dbias", s, float(off.max()))
+    squares = [[torch.zeros_like(v) for v in ref[k]] for k in ("dA", "dB")]
+    for a in range(L):
+        at, off = (c["ids"] == a).nonzero()[:, 0], 0
+        for s, w in enumerate(widths):
+            dy = c["dy"][at, off:off + w].double()
+            off += w
+            g = c["scale"] * dy @ c["B"][s][a].double()
+            squares[0][s][a] = (g * g).T @ c["x"][at].double() ** 2
+            squares[1][s][a] = (dy * dy).T @ c["buf"][s, at].double() ** 2
+    for k, name, sq in (("d_lora_a", "dA", squares[0]), ("d_lora_b", "dB", squares[1])):
+        for s, (u, v, q) in enumerate(zip(out[k], ref[name], sq)):
+            off = float(torch.linalg.norm(u.double().cpu() - v))
+            assert off <= 2.0 ** -8 * math.sqrt(float((v * v).sum() + q.sum())), (name, s, off)
