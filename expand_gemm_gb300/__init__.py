@@ -506,8 +506,8 @@ def lora_cross_entropy(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
 
     loss[t] (fp32) = w_t (logsumexp_t - logit of targets[t]), w_t =
     token_weight[t] (fp32; 1 when None).  A target outside [0, vocab) (-100,
-    say) means none: zero loss and gradient.  hidden_grad (bf16, like hidden)
-    and weight_grad (bf16, like weight) are overwritten when given;
+    say) means none: zero loss and gradient.  hidden_grad (bf16, like hidden,
+    or hidden itself) and weight_grad (bf16, like weight) are overwritten when given;
     error_word (int32 [1]) receives the count of targets >= vocab.  A
     workspace (uint8) is allocated when none is given."""
     try:

@@ -346,7 +346,9 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
  *                over an adapter's tokens, a loss scale).
  *   loss         device fp32 [num_tokens].
  *   logsumexp    NULL or device fp32 [num_tokens]: log sum_v exp S[t, v].
- *   hidden_grad  NULL or device bf16 [num_tokens, hidden_grad_ld], written.
+ *   hidden_grad  NULL or device bf16 [num_tokens, hidden_grad_ld], written;
+ *                may be hidden itself.  No other output may overlap an input
+ *                or another output.
  *   weight_grad  NULL or device bf16 [vocab, hidden_size], dense, 16-byte
  *                aligned, written.
  *   error_word   NULL or device int32 [1]: receives the number of targets
@@ -356,7 +358,9 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
  * Products run on the tensor cores (tcgen05) in bf16 with fp32 sums; the
  * softmax's terms are rounded to bf16 once for the gradient products,
  * its sums and the accumulated gradients are fp32, and each gradient is
- * rounded to bf16 once.  Deterministic.  Errors: LORA_ERR_NULL,
+ * rounded to bf16 once.  A NaN logit of a token with a target makes its loss
+ * and gradient NaN, and infinite logits give what the formulas give.
+ * Deterministic.  Errors: LORA_ERR_NULL,
  * LORA_ERR_SIZE, LORA_ERR_ALIGN (weight, weight_grad, workspace,
  * hidden_size), LORA_ERR_WORKSPACE, LORA_ERR_DEVICE.
  */
@@ -445,8 +449,9 @@ int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidden,
  *                wait ran out (the output is then not valid); otherwise it is
  *                left as it is.
  *
- * A zero matrix gives zeros; a matrix with a NaN or an infinity gives NaN in
- * its own place only.  |U|_F^2 and the products U U^T are summed in fp32 and
+ * A zero matrix gives zeros (with eps > 0); a matrix with a NaN or an infinity
+ * gives NaN in its own place only; one whose norm is below about 1e-17 is
+ * divided by eps.  |U|_F^2 and the products U U^T are summed in fp32 and
  * must be finite there (entries up to about 1e17).  Up to |coef_a|^steps =
  * 512 (five steps with 3.4445) all steps run on r x r matrices in fp32 (every
  * factor is a polynomial in U U^T); the error is within 2% of the result's

@@ -7,6 +7,8 @@ import math
 import pytest
 import torch
 
+import expand_gemm_gb300 as eg
+
 from test_gpu_loss import check, in_64_bits, make, run
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +142,15 @@ def test_infinite_logits_of_other_columns(T):
     got = run(*a, head=False)
     assert ((got["loss"] - math.log(299.0)).abs() <= 2.0 ** -18).all()
     assert torch.isfinite(got["dh"].float()).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 300])
+def test_hidden_grad_over_hidden(T):
+    """The same bits as with a gradient of its own."""
+    hidden, weight, targets, share = (v.cuda() for v in make(T, 264, 1025, 61, masked=0.3 if T > 2 else 0.0))
+    want = [torch.empty_like(hidden), torch.empty_like(weight) if T > 2 else None, torch.empty(T, device="cuda")]
+    eg.lora_cross_entropy(hidden, weight, targets, want[2], token_weight=share, hidden_grad=want[0], weight_grad=want[1])
+    got = [hidden, torch.empty_like(weight) if T > 2 else None, torch.empty(T, device="cuda")]
+    eg.lora_cross_entropy(hidden, weight, targets, got[2], token_weight=share, hidden_grad=hidden, weight_grad=got[1])
+    for u, v in zip(want, got):
+        assert u is None or torch.equal(u, v)
