@@ -17,7 +17,15 @@
 //                  adapter's tokens in a fixed order (no atomics).
 // They run on mma.sync; lora_backward_tc.cu holds their forms for ranks above
 // 32 on tcgen05.  g and u in bf16 cost a relative 2^-9 a term, like the
-// rounding of the outputs; all sums are fp32.
+// rounding of the outputs (and u enters as lora_expand took it); all sums are
+// fp32.  The two roundings together leave 1.41 times the error of one, evenly
+// over many terms, but up to 1.9 times over the few of a small batch.  Calls
+// of up to BW_TERMS_TOKENS tokens therefore keep g and u as two bf16 terms
+// (2^-16): the second ones are further steps of the products, on the same rows
+// of A, x and dy.  64 tokens of rank 8, hidden 256: 10.5 us in place of 9.5;
+// 64 of rank 32, 8 adapters, 4096 to 2 x 11008: 36 in place of 30; 16 of rank
+// 128, 8192 to 8192, 1024, 1024, 4 adapters: 55 in place of 45 (64 tokens over
+// 64 adapters: 340 in place of 265).
 //
 // 2048 tokens by token over 32 adapters, rank 32, 4096 to 2 x 11008: grad_u
 // 32 us (126 MB of dy and B, 4.3 TB/s with its ring a third of an SM's
@@ -50,6 +58,17 @@ __device__ __forceinline__ void copy8(uint8_t *dst, const uint16_t *row, int c, 
 }
 
 // ---------------------------------------------------------------- g and u
+
+__device__ __forceinline__ uint2 round4(const float4 &v)
+{
+    return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+// What rounding v to h left over, as bf16.
+__device__ __forceinline__ uint2 rest4(const float4 &v, const uint2 &h)
+{
+    return make_uint2(pack_bf16x2(v.x - bf16_lo(h.x), v.y - bf16_hi(h.x)),
+                      pack_bf16x2(v.z - bf16_lo(h.y), v.w - bf16_hi(h.y)));
+}
 
 template <int RP> struct UShape { static constexpr int WM = 4, WN = 2; };
 constexpr int BW_U_STAGES = 4;
@@ -192,13 +211,22 @@ __global__ void __launch_bounds__(BW_THREADS) grad_u_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < NI; ++j) {
                 uint16_t *at = p.g + out0 + (wm * 16 + gq) * RP + wn * (RP / WN) + 8 * j + 2 * t;
-                *reinterpret_cast<uint32_t *>(at) = pack_bf16x2(acc[j][0], acc[j][1]);
-                *reinterpret_cast<uint32_t *>(at + 8 * RP) = pack_bf16x2(acc[j][2], acc[j][3]);
+                const uint2 h = make_uint2(pack_bf16x2(acc[j][0], acc[j][1]), pack_bf16x2(acc[j][2], acc[j][3]));
+                *reinterpret_cast<uint32_t *>(at) = h.x;
+                *reinterpret_cast<uint32_t *>(at + 8 * RP) = h.y;
+                if (p.low != 0) {
+                    const uint2 l = rest4(make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]), h);
+                    *reinterpret_cast<uint32_t *>(at + p.low) = l.x;
+                    *reinterpret_cast<uint32_t *>(at + p.low + 8 * RP) = l.y;
+                }
             }
 #pragma unroll
-            for (int i = 0; i < RP / 16; ++i)
-                reinterpret_cast<uint2 *>(p.u + out0)[tid + i * BW_THREADS] =
-                    make_uint2(pack_bf16x2(u[i].x, u[i].y), pack_bf16x2(u[i].z, u[i].w));
+            for (int i = 0; i < RP / 16; ++i) {
+                uint16_t *at = p.u + out0 + (tid + i * BW_THREADS) * 4;
+                const uint2 h = round4(u[i]);
+                *reinterpret_cast<uint2 *>(at) = h;
+                if (p.low != 0) *reinterpret_cast<uint2 *>(at + p.low) = rest4(u[i], h);
+            }
             __syncthreads();                                   // the ring is free
             step += gridDim.x;
             continue;
@@ -258,16 +286,14 @@ __global__ void __launch_bounds__(BW_THREADS) join_u_kernel(const __grid_constan
             v.w += x.w;
         }
         if (team > 0) s_sum[team - 1][t] = v;
-        uint2 uv = make_uint2(0u, 0u);
+        float4 uf = make_float4(0, 0, 0, 0);               // u; then, of team 0, g
         if (team == 1) {
             const int seg = find_segment(tab.tile, p.nbins, tile);
             const int row0 = tab.start[seg] + (tile - tab.tile[seg]) * BW_TOK;
             if (row < tab.start[seg] + tab.count[seg] - row0 && col < p.r) {
                 const int tok = checked_token(p.sorted[row0 + row], p.T, p.error_word);
-                if (tok >= 0) {
-                    const float4 f = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
-                    uv = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
-                }
+                if (tok >= 0)
+                    uf = *reinterpret_cast<const float4 *>(p.buf + (int64_t(s) * p.T + tok) * p.r + col);
             }
         }
         __syncthreads();
@@ -281,26 +307,37 @@ __global__ void __launch_bounds__(BW_THREADS) join_u_kernel(const __grid_constan
                 v.z += x.z;
                 v.w += x.w;
             }
-            uv = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            uf = v;
         }
-        if (team == 0 || (team == 1 && p.ut == nullptr))
-            *reinterpret_cast<uint2 *>((team == 0 ? p.g : p.u) + out0 + row * RP + col) = uv;
+        const uint2 uv = round4(uf);
+        if (team == 0 || (team == 1 && p.ut == nullptr)) {
+            uint16_t *at = (team == 0 ? p.g : p.u) + out0 + row * RP + col;
+            *reinterpret_cast<uint2 *>(at) = uv;
+            if (p.low != 0) *reinterpret_cast<uint2 *>(at + p.low) = rest4(uf, uv);
+        }
         if (p.ut != nullptr) {
             // transposed: 32 bytes of 16 tokens for each column
-            if (team < 2) {
-                uint16_t(&at)[16][16] = s_turned[team];
-                const int y = t >> 2, x = (t & 3) * 4;
-                at[x][y] = uint16_t(uv.x & 0xFFFFu);
-                at[x + 1][y] = uint16_t(uv.x >> 16);
-                at[x + 2][y] = uint16_t(uv.y & 0xFFFFu);
-                at[x + 3][y] = uint16_t(uv.y >> 16);
-            }
-            __syncthreads();
-            if (team == 0) {
-                const int which = t >> 5, x = t >> 1 & 15, half = (t & 1) * 8;
-                *reinterpret_cast<uint4 *>((which == 0 ? p.gt : p.ut) + out0 + ((part >> 2) * 16 + x) * BW_TOK +
-                                           (part & 3) * 16 + half) =
-                    *reinterpret_cast<const uint4 *>(&s_turned[which][x][half]);
+            auto turn = [&](const uint2 &v, int64_t low) {
+                if (team < 2) {
+                    uint16_t(&at)[16][16] = s_turned[team];
+                    const int y = t >> 2, x = (t & 3) * 4;
+                    at[x][y] = uint16_t(v.x & 0xFFFFu);
+                    at[x + 1][y] = uint16_t(v.x >> 16);
+                    at[x + 2][y] = uint16_t(v.y & 0xFFFFu);
+                    at[x + 3][y] = uint16_t(v.y >> 16);
+                }
+                __syncthreads();
+                if (team == 0) {
+                    const int which = t >> 5, x = t >> 1 & 15, half = (t & 1) * 8;
+                    *reinterpret_cast<uint4 *>((which == 0 ? p.gt : p.ut) + low + out0 +
+                                               ((part >> 2) * 16 + x) * BW_TOK + (part & 3) * 16 + half) =
+                        *reinterpret_cast<const uint4 *>(&s_turned[which][x][half]);
+                }
+            };
+            turn(uv, 0);
+            if (p.low != 0) {
+                __syncthreads();
+                turn(rest4(uf, uv), p.low);
             }
         }
         __syncthreads();
@@ -318,9 +355,9 @@ constexpr int grad_x_smem()
     return BW_X_STAGES * (BW_TOK * RP * 2 + RP * BW_COLS * 2) + BW_TOK * BW_X_LD * 4;
 }
 
-// Item: (tile, 128 columns), one step a slice; a ring of three steps runs
-// across the items.
-template <int RP>
+// Item: (tile, 128 columns), one step a slice (and term of g); a ring of three
+// steps runs across the items.
+template <int RP, bool TERMS>
 __global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(const __grid_constant__ BackwardArgs p)
 {
     constexpr int CPR = RP / 8, ST = BW_X_STAGES;
@@ -336,6 +373,7 @@ __global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(co
     const SegTab tab = load_tab(p, reinterpret_cast<int *>(smem + grad_x_smem<RP>()), tiles);
     const int hb = (p.H + BW_COLS - 1) / BW_COLS;
     const int items = tiles * hb;             // T x H fits the memory: below 2^31
+    const int steps = TERMS ? 2 * p.S : p.S;
 
     // the step that is loaded next
     int l_item = blockIdx.x;
@@ -344,8 +382,10 @@ __global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(co
         if (l_item < items) {
             const int tile = l_item / hb, h0 = l_item % hb * BW_COLS;
             const int seg = find_segment(tab.tile, p.nbins, tile);
-            const uint16_t *gt = p.g + (int64_t(l_s) * p.rows + int64_t(tile) * BW_TOK) * RP;
-            const uint16_t *aw = p.a[l_s] + int64_t(tab.id[seg]) * p.r * p.H;
+            const bool second = TERMS && l_s >= p.S;
+            const int s = second ? l_s - p.S : l_s;
+            const uint16_t *gt = p.g + (second ? p.low : 0) + (int64_t(s) * p.rows + int64_t(tile) * BW_TOK) * RP;
+            const uint16_t *aw = p.a[s] + int64_t(tab.id[seg]) * p.r * p.H;
             uint8_t *at = smem + l_stage * (SG + SA);
 #pragma unroll
             for (int i = 0; i < PG; ++i) {
@@ -360,7 +400,7 @@ __global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(co
                 cp_async16(smem_addr(at + SG + tile_at<16, RP>(row, c & 15)),
                            ok ? aw + int64_t(row) * p.H + col : aw, ok);
             }
-            if (++l_s == p.S) {
+            if (++l_s == steps) {
                 l_s = 0;
                 l_item += gridDim.x;
             }
@@ -383,7 +423,7 @@ __global__ void __launch_bounds__(BW_THREADS, RP <= 32 ? 3 : 1) grad_x_kernel(co
             tok[i] = row < nrows ? checked_token(p.sorted[row0 + row], p.T, p.error_word) : -1;
         }
         float acc[8][4] = {};
-        for (int s = 0; s < p.S; ++s) {
+        for (int s = 0; s < steps; ++s) {
             cp_async_wait<ST - 2>();
             __syncthreads();
             issue();
@@ -469,7 +509,8 @@ constexpr int grad_w_smem()
 // adapter's tokens of dy^T u (dB) or x^T g (dA), 64 tokens a step (an
 // adapter without tokens has one step of zeros).  Per-token adapters give
 // items of a single step, so a ring of three steps runs across the items.
-template <int RP>
+// TERMS: the same steps again for the second terms of g and u.
+template <int RP, bool TERMS>
 __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constant__ BackwardArgs p)
 {
     constexpr int WM = WShape<RP>::WM, WN = WShape<RP>::WN, ST = BW_W_STAGES;
@@ -520,13 +561,13 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     Walk to = at;
     const uint16_t *z = nullptr, *v = nullptr;
     int64_t z_ld = 0;
-    int start = 0, count = 0, l_k = 0, l_stage = 0, tok[4];
+    int start = 0, count = 0, l_k = 0, l_half = 1, l_stage = 0, tok[4];
     bool vec = false, whole = false;
     const int z_at = int(tile_at<16, BW_TOK>(tid >> 4, tid & 15));
     auto tokens = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = l_k * BW_TOK + (tid >> 4) + i * 16;
+            const int row = (TERMS && l_k >= l_half ? l_k - l_half : l_k) * BW_TOK + (tid >> 4) + i * 16;
             tok[i] = row < count ? checked_token(p.sorted[start + row], p.T, p.error_word) : -1;
         }
     };
@@ -537,6 +578,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
         const int width = is_a ? p.H : p.width;
         start = seg >= 0 ? tab.start[seg] : 0;
         count = seg >= 0 ? tab.count[seg] : 0;
+        if constexpr (TERMS) l_half = count > 0 ? (count + BW_TOK - 1) / BW_TOK : 1;
         z = (is_a ? p.x : p.dy) + col;
         z_ld = is_a ? p.x_ld : p.dy_ld;
         vec = is_a ? p.x_vec : p.dy_vec;
@@ -561,14 +603,16 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
                         tok[i] < 0 ? make_uint4(0, 0, 0, 0) : load8(z - col + tok[i] * z_ld, col, 0, width, false);
             }
             const uint32_t sv = base + l_stage * (SZ + SV) + SZ;
+            int64_t v_at = int64_t(l_k) * BW_TOK * RP;
+            if (TERMS && l_k >= l_half) v_at = p.low + int64_t(l_k - l_half) * BW_TOK * RP;
 #pragma unroll
             for (int i = 0; i < PV; ++i) {
                 const int c = tid + i * BW_THREADS;
                 if (c < BW_TOK * CPR)
                     cp_async16(sv + tile_at<CPR, BW_TOK>(c / CPR, c % CPR),
-                               count > 0 ? v + int64_t(l_k) * BW_TOK * RP + i * BW_THREADS * 8 : p.g, count > 0);
+                               count > 0 ? v + v_at + i * BW_THREADS * 8 : p.g, count > 0);
             }
-            if (++l_k * BW_TOK >= count) {
+            if (TERMS ? ++l_k >= (count > 0 ? 2 * l_half : 1) : ++l_k * BW_TOK >= count) {
                 l_k = 0;
                 next(to);
                 enter();
@@ -584,7 +628,8 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
     for (; at.id < p.L; next(at)) {
         const bool is_a = at.q >= p.S;
         const int s = is_a ? at.q - p.S : at.q, seg = seg_of[at.id];
-        const int steps = seg >= 0 ? (tab.count[seg] + BW_TOK - 1) / BW_TOK : 1;
+        const int firsts = seg >= 0 ? (tab.count[seg] + BW_TOK - 1) / BW_TOK : 1;
+        const int steps = TERMS && seg >= 0 ? 2 * firsts : firsts;
         const int lo = is_a ? 0 : p.off[s], n = is_a ? p.H : p.n[s];
         uint16_t *dbias = is_a ? nullptr : p.dbias[s];
         float acc[MI][NI][4] = {}, ones[MI][4] = {};
@@ -610,7 +655,7 @@ __global__ void __launch_bounds__(BW_THREADS) grad_w_kernel(const __grid_constan
                         mma_bf16_16816(acc[i][j + 1], a[i], b[2], b[3]);
                     }
                 }
-                if (dbias != nullptr && wn == 0) {
+                if (dbias != nullptr && wn == 0 && (!TERMS || k < firsts)) {
                     // a product with ones: column 0 of the result
                     const uint32_t one = lane < 4 ? 0x3F803F80u : 0u;
 #pragma unroll
@@ -693,6 +738,11 @@ static int64_t backward_rows(int64_t T, int64_t L)
     return (T / BW_TOK + (L < T ? L : T)) * BW_TOK;
 }
 
+// Copies of the laid-out g or u in the workspace: g, u, and for ranks above
+// 32 g transposed; each with its second terms behind it in a small batch.
+static int backward_terms(int64_t T) { return T <= BW_TERMS_TOKENS ? 2 : 1; }
+static int backward_parts(int64_t T, int rank) { return (rank > 32 ? 3 : 2) * backward_terms(T); }
+
 template <int RP>
 static int run_backward(BackwardArgs p, cudaStream_t st)
 {
@@ -712,9 +762,13 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
             (e = cudaFuncSetAttribute(grad_u_kernel<RP <= 32 ? RP : 32, true>,
                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       grad_u_smem<RP <= 32 ? RP : 32>() + most)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(grad_x_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (e = cudaFuncSetAttribute(grad_x_kernel<RP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       grad_x_smem<RP>() + most)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(grad_w_kernel<RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (e = cudaFuncSetAttribute(grad_x_kernel<RP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_x_smem<RP>() + most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(grad_w_kernel<RP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      grad_w_smem<RP>() + most)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(grad_w_kernel<RP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       grad_w_smem<RP>() + most)) != cudaSuccess)
             return int(e);
         if (dev < 64) configured[dev] = 1;
@@ -752,7 +806,8 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
         if (int err = launch_grad_w_tc(p, RP, st)) return err;
     } else if (items > 0) {
         const int64_t grid = items < resident(ws) ? items : resident(ws);
-        e = launch_kernel(grad_w_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), ws, st, p);
+        e = launch_kernel(p.low != 0 ? grad_w_kernel<RP, true> : grad_w_kernel<RP, false>, dim3(unsigned(grid)),
+                          dim3(BW_THREADS), ws, st, p);
         if (e != cudaSuccess) return int(e);
     }
     // dx last: it may be written over dy or x, which the kernels before read
@@ -762,7 +817,8 @@ static int run_backward(BackwardArgs p, cudaStream_t st)
         if (tc < 0) {
             const int64_t most = tiles * ((p.H + BW_COLS - 1) / BW_COLS);
             const int64_t grid = most < resident(xs) ? most : resident(xs);
-            e = launch_kernel(grad_x_kernel<RP>, dim3(unsigned(grid)), dim3(BW_THREADS), xs, st, p);
+            e = launch_kernel(p.low != 0 ? grad_x_kernel<RP, true> : grad_x_kernel<RP, false>,
+                              dim3(unsigned(grid)), dim3(BW_THREADS), xs, st, p);
             if (e != cudaSuccess) return int(e);
         }
     }
@@ -781,10 +837,10 @@ LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidd
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
     const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;
-    // g, u, g transposed, and the slots of partial sums: one an item and one a CTA
+    // and the slots of partial sums: one an item and one a CTA
     const int64_t slots = lora::backward_rows(num_tokens, max_loras) / lora::BW_TOK * num_slices +
                           lora::BW_RESIDENT * lora::device_sm_count();
-    return (rank > 32 ? 3 : 2) * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
+    return lora::backward_parts(num_tokens, rank) * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
 }
 
 LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,
@@ -869,11 +925,13 @@ LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t 
     const int rp = padded_rank(rank);
     p.rows = backward_rows(num_tokens, p.L);
     const int64_t one = (p.rows * num_slices * rp * 2 + 255) / 256 * 256;
+    const int64_t part = one * backward_terms(num_tokens);
+    p.low = part > one ? one / 2 : 0;
     p.g = reinterpret_cast<uint16_t *>(workspace);
-    p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + one);
+    p.u = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + part);
     p.ut = p.u;
-    p.gt = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 2 * one);
-    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + (rp > 32 ? 3 : 2) * one);
+    p.gt = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 2 * part);
+    p.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + backward_parts(num_tokens, rank) * one);
     p.u_ctas = 0;
     int steps = 0;
     for (int s = 0; s < LORA_MAX_SLICES; ++s) {

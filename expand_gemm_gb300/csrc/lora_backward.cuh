@@ -9,6 +9,7 @@ namespace lora {
 constexpr int BW_THREADS = 256;
 constexpr int BW_TOK = 64;                 // tokens of a tile
 constexpr int BW_COLS = 128;               // columns of a tile of dx, dA, dB
+constexpr int BW_TERMS_TOKENS = BW_TOK;    // tokens up to which g and u are two bf16 terms
 
 struct BackwardArgs {
     const uint16_t *dy, *x;
@@ -30,6 +31,9 @@ struct BackwardArgs {
     // transposed, [S][rows / BW_TOK][RP][BW_TOK]; else null
     uint16_t *gt, *ut;
     int64_t rows;
+    // elements from g to its second terms, and likewise from u, gt and ut; 0
+    // where each is one bf16 value
+    int64_t low;
     float *part;                           // grad_u_kernel's partial sums, [BW_TOK][RP] each
     int32_t step_end[LORA_MAX_SLICES];     // its 64-column steps of one tile, by slice
     int32_t u_ctas;

@@ -113,7 +113,9 @@ static bool encode_row_maps(TcRowMaps *m, const uint16_t *ptr, int64_t rows, int
 struct GradWTcArgs {
     BackwardArgs b;
     TcRowMaps dy, x;
-    CUtensorMap ut, gt;        // [S * rows / 64 * RP][64], boxes 64 x RP: a tile's u or g, transposed
+    // [S * rows / 64 * RP][64], boxes 64 x RP: a tile's u or g, transposed (and
+    // their second terms behind them)
+    CUtensorMap ut, gt;
     int32_t rp, group, groups; // slices of one dA product
     int32_t end[2 * LORA_MAX_SLICES];   // blocks of one adapter: dA groups, then dB slices
     int32_t kinds, ring, stage_bytes, stages, buffers, ones;
@@ -163,9 +165,12 @@ __device__ __forceinline__ void clear_item(const BackwardArgs &p, bool is_a, int
 // for the 1.27 GB that it moves, 6.1 TB/s (x is read once for each group of
 // slices).
 //
+// TERMS: the same steps again for the second terms of g and u.
+//
 // Adapters are taken by falling token count, so that the CTAs' shares come
 // out even.  Warps 8 to 11 write the zeros of the adapters without tokens
 // meanwhile (with 8 of 64 adapters in use they are most of the bytes).
+template <bool TERMS>
 __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid_constant__ GradWTcArgs q)
 {
     const BackwardArgs &p = q.b;
@@ -226,6 +231,7 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         bool is_a;
         int id, s, slices, start, count, steps, c0, tile0;
     };
+    auto steps_of = [](int count) { return (TERMS ? 2 : 1) * ((count + 63) / 64); };
     auto kind = [&](int blk, Item &it) {
         int k = 0;
         while (blk >= q.end[k]) ++k;
@@ -241,10 +247,12 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         it.id = tab.id[seg];
         it.start = tab.start[seg];
         it.count = tab.count[seg];
-        it.steps = (it.count + 63) / 64;
+        it.steps = steps_of(it.count);
         it.tile0 = tab.tile[seg];
         return it;
     };
+    // a step's 64 tokens of the adapter (the second terms' steps come last)
+    auto tokens_of = [](const Item &it, int k) { return TERMS && 2 * k >= it.steps ? k - it.steps / 2 : k; };
     if (warp == 0) {
         // ------------------------------------------------ columns of dy or x
         // The steps' tokens come by cp.async, six steps ahead and across the
@@ -261,13 +269,14 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         };
         auto ahead = [&]() {
             if (a_item < items) {
+                const int t0 = (TERMS && 2 * a_k >= steps_of(a_count) ? a_k - steps_of(a_count) / 2 : a_k) * 64;
 #pragma unroll
                 for (int j = lane; j < 64; j += 32)
-                    if (a_k * 64 + j < a_count)
+                    if (t0 + j < a_count)
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n"
-                                     :: "r"(slots_at + (a_slot * 64 + j) * 4), "l"(p.sorted + a_start + a_k * 64 + j)
+                                     :: "r"(slots_at + (a_slot * 64 + j) * 4), "l"(p.sorted + a_start + t0 + j)
                                      : "memory");
-                if (++a_k * 64 >= a_count) {
+                if (TERMS ? ++a_k >= steps_of(a_count) : ++a_k * 64 >= a_count) {
                     a_k = 0;
                     a_item += gridDim.x;
                     enter();
@@ -290,7 +299,7 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
                 __syncwarp();
                 const int4 own = *reinterpret_cast<const int4 *>(slots + slot * 64 + r4);
                 slot = slot + 1 == TC_W_SLOTS ? 0 : slot + 1;
-                const int row = k * 64 + r4;
+                const int row = tokens_of(it, k) * 64 + r4;
                 TcRows rows;
                 rows.t[0] = row < it.count ? tc_row(p, own.x, row) : tc_no_row(p.T, row);
                 rows.t[1] = row + 1 < it.count ? tc_row(p, own.y, row + 1) : tc_no_row(p.T, row + 1);
@@ -338,7 +347,8 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
                 __syncwarp();
                 if (lane < it.slices)
                     tma_load_2d(ring.ring + pos.stage * ring.stage_bytes + Z_BYTES + lane * A_BYTES, map, 0,
-                                ((it.s + lane) * slice_tiles + it.tile0 + k) * RP, full);
+                                ((it.s + lane + (tokens_of(it, k) < k ? p.S : 0)) * slice_tiles + it.tile0 +
+                                 tokens_of(it, k)) * RP, full);
                 ++issued;
                 pos.next(ring.stages);
             }
@@ -368,7 +378,7 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
                     const uint32_t z = ring.ring + pos.stage * ring.stage_bytes, a = z + Z_BYTES;
                     umma_k64(d, a, z, IDESC, k != 0);
                     if (mt > 1) umma_k64(d + uint32_t(TC_W_COLS), a + 2 * TC_PANEL, z, IDESC, k != 0);
-                    if (bias) umma_k64(d + uint32_t(TC_W_COLS), ones, z, IDESC, k != 0);
+                    if (bias && tokens_of(it, k) == k) umma_k64(d + uint32_t(TC_W_COLS), ones, z, IDESC, k != 0);
                     umma_commit(ring.empty + 8 * pos.stage);
                     pos.next(ring.stages);
                 }
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         // it (231 us in place of 208; 156 without zeros).
         int steps = 0;
         for (int i = blockIdx.x + lane * gridDim.x; i < items; i += 32 * gridDim.x)
-            steps += (tab.count[order[i / blocks]] + 63) / 64;
+            steps += steps_of(tab.count[order[i / blocks]]);
         steps = int(__reduce_add_sync(0xffffffffu, unsigned(steps)));
         const int empty = (p.L - active) * blocks;
         const int mine = empty > int(blockIdx.x) ? (empty - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 0;
@@ -1067,8 +1077,8 @@ static int tc_configure()
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return int(e);
     if (dev < 64 && configured[dev]) return 0;
-    const void *fns[] = {(const void *)grad_w_tc_kernel, (const void *)grad_x_tc_kernel,
-                         (const void *)grad_x_pair_kernel, (const void *)grad_u_tc_kernel};
+    const void *fns[] = {(const void *)grad_w_tc_kernel<false>, (const void *)grad_w_tc_kernel<true>,
+                         (const void *)grad_x_tc_kernel, (const void *)grad_x_pair_kernel, (const void *)grad_u_tc_kernel};
     for (const void *f : fns)
         if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, TC_SMEM)) != cudaSuccess)
             return int(e);
@@ -1118,7 +1128,7 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     q.ones = bias ? 2 * TC_PANEL : 0;
     q.ring = tc_ring_bytes(backward_tab_words(p.nbins, p.L) + p.L + 1 + 3 + TC_W_SLOTS * 64 + 1);
     q.stages = tc_stages(q.ring - q.ones, q.stage_bytes);
-    const uint64_t rows = uint64_t(p.S) * uint64_t(p.rows / BW_TOK) * uint64_t(rp);
+    const uint64_t rows = uint64_t(p.low != 0 ? 2 : 1) * uint64_t(p.S) * uint64_t(p.rows / BW_TOK) * uint64_t(rp);
     if (!encode_row_maps(&q.dy, p.dy, p.T, p.width, p.dy_ld) ||
         !encode_row_maps(&q.x, p.x, p.T, p.H, p.x_ld) ||
         !encode_tile_map(&q.ut, p.ut, rows, 64, 64, 64, uint32_t(rp), CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -1127,13 +1137,13 @@ int launch_grad_w_tc(const BackwardArgs &p, int rp, cudaStream_t st)
     if (int e = tc_configure()) return e;
     const int64_t items = int64_t(p.L) * blocks;
     const int sms = device_sm_count();
-    return int(launch_kernel(grad_w_tc_kernel, dim3(unsigned(items < sms ? items : sms)), dim3(TC_W_THREADS),
+    return int(launch_kernel(p.low != 0 ? grad_w_tc_kernel<true> : grad_w_tc_kernel<false>, dim3(unsigned(items < sms ? items : sms)), dim3(TC_W_THREADS),
                              size_t(TC_SMEM), st, q));
 }
 
 int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
-    if (rp < 64 || !p.dx_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
+    if (rp < 64 || p.low != 0 || !p.dx_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
     // Fewer items than SMs: smaller ones on mma.sync are faster.  4096 to
     // 4096 at rank 64: 1024 tokens 15.3 us here, 14.0 there; 2048 tokens 15.9
     // here, 22.6 there; at rank 128 16.4 and 15.4, 17.1 and 25.4.
@@ -1163,7 +1173,7 @@ int launch_grad_x_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 
 int launch_grad_u_tc(const BackwardArgs &p, int rp, cudaStream_t st)
 {
-    if (rp < 64 || !p.dy_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
+    if (rp < 64 || p.low != 0 || !p.dy_vec || p.T < 1 || p.rows * p.S >= (int64_t(1) << 31)) return -1;
     // One CTA walks a tile's whole width; the kernel of lora_backward.cu cuts
     // the width among CTAs and joins.  Widths 4096, 1024, 1024 at rank 128:
     // 1024 tokens (24 tiles) 26.6 us here, 23.5 there; 2048 (48 tiles) 27.2

@@ -410,8 +410,9 @@ int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden_size, in
  *                aligned) and [max_loras, n_s].  Overwritten for all
  *                max_loras adapters: zero for those without tokens.
  *
- * g and buf enter the products over tokens as bf16 (rounded once); sums are
- * fp32 and every output is rounded to bf16 once.  Deterministic.  Invalid
+ * g and buf enter the products that follow as bf16 (rounded once; as two bf16
+ * terms, 16 bits, in batches of up to 64 tokens, whose few terms would show
+ * it); sums are fp32 and every output is rounded to bf16 once.  Deterministic.  Invalid
  * ids were mapped to -1 by the metadata.  Errors: as lora_shrink and
  * lora_expand, LORA_ERR_WIDTH for dy_ld, LORA_ERR_WORKSPACE.
  */

@@ -137,3 +137,25 @@ def test_norms(T, H, r, L, widths, runs):
         for s, (u, v, q) in enumerate(zip(out[k], ref[name], sq)):
             off = float(torch.linalg.norm(u.double().cpu() - v))
             assert off <= 2.0 ** -8 * math.sqrt(float((v * v).sum() + q.sum())), (name, s, off)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 20, 63, 64])
+@pytest.mark.parametrize("H,r,L,widths,runs", [
+    (264, 8, 1, (384,), 1), (136, 16, 5, (72, 131), 1), (512, 32, 2, (1500, 64), 9), (1000, 40, 4, (523, 75, 130), 3),
+    (264, 64, 3, (256, 64), 20), (520, 128, 2, (1032, 72, 8), 50), (264, 96, 9, (136, 72, 64), 3), (72, 128, 64, (64,), 1),
+    (264, 128, 2, (75, 64), 30)])
+@pytest.mark.parametrize("add", [True, False])
+def test_small_batches_round_once(add, H, r, L, widths, runs, T):
+    """Up to 64 tokens g and the buffer enter the products with 16 bits: each
+    output is the rounding to bf16 of a value within d = 2^-15 of the sum of
+    magnitudes from the exact one (2^-16 of g or the buffer, and fp32 sums),
+    so it is no further off than the exact one's own rounding and 2 d."""
+    c = make(T, H, r, L, widths, 79 + T, none=0.1, runs=runs)
+    out, dx = grads(c), c["dx0"].cuda()
+    call(c, c["dy"].cuda(), c["x"].cuda(), dx, add, out)
+    ref, mag = in_64_bits(c, add)
+    for name, got in (("dx", [dx]), ("dA", out["d_lora_a"]), ("dB", out["d_lora_b"]), ("dbias", out["d_lora_bias"])):
+        want, m = (ref[name], mag[name]) if name != "dx" else ([ref["dx"]], [mag["dx"]])
+        for s, (u, v, w) in enumerate(zip(got, want, m)):
+            off = (u.double().cpu() - v).abs() - (v.bfloat16().double() - v).abs() - 2.0 ** -14 * w - 1e-30
+            assert (off <= 0).all(), (name, s, float(off.max()))
