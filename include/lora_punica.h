@@ -356,7 +356,8 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
  *                outputs are then not valid).
  *
  * Products run on the tensor cores (tcgen05) in bf16 with fp32 sums; the
- * softmax's terms are rounded to bf16 once for the gradient products,
+ * softmax's terms are rounded to bf16 once for the gradient products (for
+ * weight_grad of up to 128 tokens they are two bf16 terms, 16 bits),
  * its sums and the accumulated gradients are fp32, and each gradient is
  * rounded to bf16 once.  A NaN logit of a token with a target makes its loss
  * and gradient NaN, and infinite logits give what the formulas give.

@@ -154,3 +154,28 @@ def test_hidden_grad_over_hidden(T):
     eg.lora_cross_entropy(hidden, weight, targets, got[2], token_weight=share, hidden_grad=hidden, weight_grad=got[1])
     for u, v in zip(want, got):
         assert u is None or torch.equal(u, v)
+
+
+@pytest.mark.parametrize("T", [1, 2, 5, 16, 63, 64, 100, 127, 128])
+@pytest.mark.parametrize("H,V,masked", [(72, 500, 0.0), (264, 2049, 0.3), (1000, 777, 0.0)])
+def test_head_gradient_of_few_tokens_rounds_once(T, H, V, masked):
+    """Up to 128 tokens the terms w (p - [y]) enter with 16 bits: dW is the
+    rounding to bf16 of a value within d of the exact one, d = 2^-15 (16 bits,
+    fp32 sums) and 2^-17 m (the logits) of the sum of magnitudes, so it is no
+    further off than the exact one's own rounding and 2 d."""
+    hidden, weight, targets, share = make(T, H, V, 67 + T, masked=masked)
+    got = run(hidden, weight, targets, share)
+    ref = in_64_bits(hidden, weight, targets, share)
+    check(got, ref, ("loss", "lse", "dh"))
+    h, w = hidden.double(), weight.double()
+    valid = targets >= 0
+    logits = h @ w.T
+    g = torch.exp(logits - torch.logsumexp(logits, 1)[:, None])
+    rows = torch.arange(T)[valid]
+    y = targets[valid].long()
+    g[rows, y] = 0.0
+    g[rows, y] = -g[rows].sum(1)
+    g = g.abs() * (share * valid)[:, None]
+    d = (g * (2.0 ** -15 + 2.0 ** -17 * (h.abs() @ w.abs().T).amax(1))[:, None]).T @ h.abs()
+    off = (got["dw"].double().cpu() - ref["dw"]).abs() - (ref["dw"].bfloat16().double() - ref["dw"]).abs() - 2 * d - 1e-30
+    assert (off <= 0).all(), (float(off.max()), int((off > 0).sum()))
