@@ -16,7 +16,7 @@
 //   grad_w_kernel  dB and dA of an adapter x 128 columns, summed over the
 //                  adapter's tokens in a fixed order (no atomics).
 // They run on mma.sync; lora_backward_tc.cu holds their forms for ranks above
-// 32 on tcgen05.  g and u in bf16 cost a relative 2^-9 a term, like the
+// 32 on tcgen05.  g and u in bf16 cost about 2^-9 a term, like the
 // rounding of the outputs (and u enters as lora_expand took it); all sums are
 // fp32.  The two roundings together leave 1.41 times the error of one, evenly
 // over many terms, but up to 1.9 times over the few of a small batch.  Calls

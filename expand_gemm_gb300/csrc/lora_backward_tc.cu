@@ -463,7 +463,8 @@ __global__ void __launch_bounds__(TC_W_THREADS, 1) grad_w_tc_kernel(const __grid
         const int mine = empty > int(blockIdx.x) ? (empty - int(blockIdx.x) + int(gridDim.x) - 1) / int(gridDim.x) : 0;
         for (int c = 0; c < mine; ++c) {
             const int first = int(int64_t(steps) * c / mine);
-            // at most 50 us: the order matters, not the wait
+            // a hundred sleeps at most, each up to 1 us, for each item: the
+            // order matters, not the wait
             for (int tries = 0; *done < first && tries < 100 && !*ring.abort; ++tries) __nanosleep(500);
             const int i = blockIdx.x + c * gridDim.x;
             Item it;

@@ -35,7 +35,8 @@
 // masked tokens cost nothing, and what their rows hold is never read.
 //
 // What bounds it: the tensor cores.  8192 tokens (5489 with a target), hidden
-// 4096, vocabulary 32000: 1740 us for 2.88e15 operations, 1655 TFLOP/s; 256
+// 4096, vocabulary 32000: 1900 us for 2.88e12 operations, 1515 TFLOP/s, on a
+// GPU that has warmed up (1740 us, 1655 TFLOP/s, before the power cap); 256
 // tokens: 127 us, where each of the two products reads the 262 MB of W in 55
 // us (4.8 TB/s; 125 tiles on 76 pairs are two rounds, the second two thirds
 // full).
