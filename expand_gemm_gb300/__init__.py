@@ -723,10 +723,10 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
     count = update.numel() // max(1, rows * cols)
     a, b, c = coefficients
     if workspace is None and count > 1 and abs(a) > 1.0 and steps * math.log(abs(a)) > _LONG_RUN:
-        # matrices of a long run are taken by groups: all at once, up to 4 GB
+        # matrices of a long run are taken by groups: all at once, up to 1 GB
         one = lora_orthogonalize_workspace(1, rows, cols, device=update.device)
         need = lora_orthogonalize_workspace(count, rows, cols, device=update.device)
-        workspace = torch.empty(max(need, min(count * one, 1 << 32)), dtype=_U8, device=update.device)
+        workspace = torch.empty(max(need, min(count * one, 1 << 30)), dtype=_U8, device=update.device)
     _call_with("lora_orthogonalize", workspace, update.device, (count, rows, cols), update.data_ptr(),
                int(f32), count, rows, cols, int(steps), float(a), float(b), float(c), float(eps),
                float(scale), out.data_ptr(), _vector(error_word, "error_word", 1))

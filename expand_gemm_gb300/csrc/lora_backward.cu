@@ -743,6 +743,14 @@ static int64_t backward_rows(int64_t T, int64_t L)
 static int backward_terms(int64_t T) { return T <= BW_TERMS_TOKENS ? 2 : 1; }
 static int backward_parts(int64_t T, int rank) { return (rank > 32 ? 3 : 2) * backward_terms(T); }
 
+// g and u, and the slots of partial sums: one an item and one a CTA.
+static int64_t backward_bytes(int64_t T, int S, int rank, int64_t L)
+{
+    const int64_t rows = backward_rows(T, L), one = rows * S * padded_rank(rank) * 2;
+    const int64_t slots = rows / BW_TOK * S + BW_RESIDENT * device_sm_count();
+    return backward_parts(T, rank) * ((one + 255) / 256 * 256) + slots * BW_TOK * padded_rank(rank) * 4;
+}
+
 template <int RP>
 static int run_backward(BackwardArgs p, cudaStream_t st)
 {
@@ -836,11 +844,11 @@ LORA_API int64_t lora_linear_backward_workspace(int32_t num_tokens, int32_t hidd
         return LORA_ERR_SIZE;
     if (num_slices < 1 || num_slices > LORA_MAX_SLICES) return LORA_ERR_SLICES;
     if (rank < 8 || rank > LORA_MAX_RANK || rank % 8 != 0) return LORA_ERR_RANK;
-    const int64_t one = lora::backward_rows(num_tokens, max_loras) * num_slices * lora::padded_rank(rank) * 2;
-    // and the slots of partial sums: one an item and one a CTA
-    const int64_t slots = lora::backward_rows(num_tokens, max_loras) / lora::BW_TOK * num_slices +
-                          lora::BW_RESIDENT * lora::device_sm_count();
-    return lora::backward_parts(num_tokens, rank) * ((one + 255) / 256 * 256) + slots * lora::BW_TOK * lora::padded_rank(rank) * 4;
+    // a workspace holds every smaller batch too, whose g and u may have more terms
+    const int64_t own = lora::backward_bytes(num_tokens, num_slices, rank, max_loras);
+    const int64_t small = num_tokens > lora::BW_TERMS_TOKENS
+                              ? lora::backward_bytes(lora::BW_TERMS_TOKENS, num_slices, rank, max_loras) : 0;
+    return own > small ? own : small;
 }
 
 LORA_API int lora_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_tokens,

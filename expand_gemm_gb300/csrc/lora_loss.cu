@@ -78,7 +78,7 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
 {
     LossLayout l;
     auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b * b; };
-    l.tokens = up(T > 0 ? T : 1, PG_TILE);
+    l.tokens = up(T, PG_TILE);
     int64_t most = LS_PIECE_ELEMS / l.tokens / PG_TILE * PG_TILE;
     if (most < LS_MIN_PIECE) most = LS_MIN_PIECE;
     l.pieces = int((V + most - 1) / most);
@@ -125,6 +125,22 @@ static LossLayout loss_layout(int64_t T, int64_t H, int64_t V, bool hidden_grad,
     return l;
 }
 
+// What a call may need at up to T tokens, with the gradients asked for or
+// without: a training loop sizes its workspace for its largest batch, and
+// smaller ones can take more (larger pieces, more partial sums).
+static int64_t loss_bytes(int64_t T, int64_t H, int64_t V, bool hidden_grad, bool weight_grad, int pairs)
+{
+    if (T == 0) return 256;                   // nothing but clearing outputs
+    int64_t most = loss_layout(T, H, V, hidden_grad, weight_grad, pairs).bytes;
+    auto also = [&](int64_t tokens, bool head) {
+        const int64_t bytes = loss_layout(tokens, H, V, hidden_grad, head, pairs).bytes;
+        if (bytes > most) most = bytes;
+    };
+    for (int64_t t = PG_TILE; t < T; t += PG_TILE) also(t, weight_grad);
+    also(T < LOSS_ROW_TOKENS ? T : LOSS_ROW_TOKENS, false);
+    return most;
+}
+
 struct LossArgs {
     const uint16_t *hidden;
     int64_t hidden_ld;
@@ -168,7 +184,7 @@ __global__ void __launch_bounds__(LS_PACK_THREADS) pack_kernel(const LossArgs p)
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c0 = blockIdx.x * LS_PACK_TOKENS;
-    const int blocks = p.T > 0 ? (p.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
+    const int blocks = (p.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS;
     const bool last = int(blockIdx.x) == blocks - 1, pad = int(blockIdx.x) >= blocks;
     int before = 0, bad = 0;
 #pragma unroll 8
@@ -742,7 +758,7 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
           !operand_map(&head.a, l.p, lay.tokens, lay.piece, lay.piece, true))) ||
         !operand_map(&head.b, l.h, lay.tokens, l.H, packed_ld(l.H), true))
         return LORA_ERR_DEVICE;
-    const int blocks = l.T > 0 ? (l.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS : 1;
+    const int blocks = (l.T + LS_PACK_TOKENS - 1) / LS_PACK_TOKENS;
     cudaError_t e = launch_kernel(pack_kernel, dim3(unsigned(blocks + (dw != nullptr ? LS_PAD_BLOCKS : 0))),
                                   dim3(LS_PACK_THREADS), 0, st, l);
     if (e != cudaSuccess) return int(e);
@@ -773,7 +789,7 @@ static int run_loss(LossArgs l, const LossLayout &lay, uint16_t *dw, cudaStream_
         }
     }
     if (store && lay.split > 1) {
-        const int grid = l.T < 4 * 2 * pairs ? (l.T > 0 ? l.T : 1) : 4 * 2 * pairs;
+        const int grid = l.T < 4 * 2 * pairs ? l.T : 4 * 2 * pairs;
         e = launch_kernel(finish_kernel, dim3(grid), dim3(256), 0, st, l);
         if (e != cudaSuccess) return int(e);
     }
@@ -803,8 +819,7 @@ LORA_API int64_t lora_cross_entropy_workspace(int32_t num_tokens, int32_t hidden
 {
     if (num_tokens < 0 || hidden < 8 || hidden % 8 != 0 || vocab < 1) return LORA_ERR_SIZE;
     const int pairs = lora::device_sm_count() / 2 > 0 ? lora::device_sm_count() / 2 : 1;
-    return lora::loss_layout(num_tokens, hidden, vocab, hidden_grad != 0, weight_grad != 0, pairs)
-        .bytes;
+    return lora::loss_bytes(num_tokens, hidden, vocab, hidden_grad != 0, weight_grad != 0, pairs);
 }
 
 LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, int32_t hidden_size,
@@ -826,9 +841,18 @@ LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, i
     auto bits = [](const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); };
     if ((bits(weight) | bits(weight_grad)) & 15u || bits(workspace) & 255u) return LORA_ERR_ALIGN;
     const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    if (workspace_bytes < loss_bytes(num_tokens, hidden_size, vocab, hidden_grad != nullptr, weight_grad != nullptr,
+                                     pairs))
+        return LORA_ERR_WORKSPACE;
+    if (num_tokens == 0) {
+        const cudaStream_t st = static_cast<cudaStream_t>(stream);
+        cudaError_t e = cudaSuccess;
+        if (weight_grad != nullptr) e = cudaMemsetAsync(weight_grad, 0, size_t(vocab) * hidden_size * 2, st);
+        if (error_word != nullptr && e == cudaSuccess) e = cudaMemsetAsync(error_word, 0, sizeof(int32_t), st);
+        return e == cudaSuccess ? LORA_OK : int(e);
+    }
     const LossLayout lay = loss_layout(num_tokens, hidden_size, vocab, hidden_grad != nullptr,
                                        weight_grad != nullptr, pairs);
-    if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
     if (lay.rows) {
         char *at = static_cast<char *>(workspace);
         LossRowArgs r;
@@ -885,8 +909,5 @@ LORA_API int lora_cross_entropy(const lora_bf16_t *hidden, int32_t num_tokens, i
     l.piece = lay.piece;
     l.split = lay.split;
     l.two = weight_grad != nullptr && num_tokens <= PG_HALF;
-    if (num_tokens == 0 && weight_grad == nullptr) {
-        if (error_word == nullptr) return LORA_OK;
-    }
     return run_loss(l, lay, weight_grad, static_cast<cudaStream_t>(stream));
 }

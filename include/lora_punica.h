@@ -323,7 +323,9 @@ int lora_linear_noalloc(const int32_t *token_lora_mapping, int32_t num_tokens,
  * pages have no counterpart (they serve adapters); these are additions.
  * Every call takes a workspace of at least the bytes that its *_workspace
  * function returns (device memory, 256-byte aligned, contents of no matter
- * before and after); calls that may overlap need a workspace each.
+ * before and after); calls that may overlap need a workspace each.  The bytes
+ * for a number of tokens (or matrices) hold any smaller call of the same
+ * sizes, with fewer gradients too.
  * ------------------------------------------------------------------------ */
 
 /*
