@@ -34,6 +34,9 @@ __all__ = ["LoRAKernelMeta", "lora_meta_prepare", "lora_shrink", "lora_expand",
            "add_lora_logits", "lora_cross_entropy", "lora_cross_entropy_workspace",
            "lora_linear_backward", "lora_linear_backward_workspace",
            "lora_orthogonalize", "lora_orthogonalize_workspace",
+           "lora_expert_linear", "lora_expert_linear_workspace",
+           "lora_expert_linear_backward", "lora_expert_linear_backward_workspace",
+           "lora_quantize_mxfp4", "lora_dequantize_mxfp4", "LoRAGradients", "lora_clip_gradients",
            "reload_options", "LoraError", "library", "build"]
 
 
@@ -730,3 +733,239 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
     _call_with("lora_orthogonalize", workspace, update.device, (count, rows, cols), update.data_ptr(),
                int(f32), count, rows, cols, int(steps), float(a), float(b), float(c), float(eps),
                float(scale), out.data_ptr(), _vector(error_word, "error_word", 1))
+
+
+# ------------------------------------------------------------ the layers under the adapters
+
+def _expert_weight(weight, scale, meta, index: int, k: int):
+    """(experts, rows) of the bf16 or MXFP4 stack, checked against hidden size k."""
+    if scale is None:
+        if weight.dim() != 3 or weight.shape[2] != k or not weight.is_contiguous():
+            raise ValueError("weight must be a contiguous [max_loras, n, %d] tensor" % k)
+    else:
+        if k % 32:
+            raise ValueError("4-bit weights need a hidden size that is a multiple of 32, got %d" % k)
+        if weight.dim() != 3 or weight.shape[2] * 2 != k or not weight.is_contiguous():
+            raise ValueError("weight must be contiguous codes [max_loras, n, %d]" % (k // 2))
+        if tuple(scale.shape) != (*weight.shape[:2], k // 32) or not scale.is_contiguous():
+            raise ValueError("weight_scale must be a contiguous %s tensor" % [*weight.shape[:2], k // 32])
+    if weight.shape[0] < meta.max_loras:
+        raise ValueError("weight holds %d experts, metadata expects %d" % (weight.shape[0], meta.max_loras))
+    return weight.shape[0], weight.shape[1]
+
+
+def _expert_types(first, first_name, meta, named, weight, scale, workspace) -> int:
+    """Checks the types and devices of an expert call's tensors; the GPU's index."""
+    index = meta.no_lora_flag.get_device()
+    try:
+        ok = (index >= 0 and all(_is(t, _BF16, index) for t, _ in named) and _is(workspace, _U8, index)
+              and weight.get_device() == index and weight.dtype is (_BF16 if scale is None else _U8)
+              and _is(scale, _U8, index))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _gpu(first, first_name)
+        _all(index, *((t, _BF16, name) for t, name in named),
+             (weight, _BF16 if scale is None else _U8, "weight"), (scale, _U8, "weight_scale"),
+             (workspace, _U8, "workspace"))
+        raise TypeError("weight must be a tensor")
+    return index
+
+
+def _fan_out(rows: int, tokens: int, meta) -> int:
+    if rows == 0 and tokens == 0:
+        return 1
+    if tokens == 0 or rows % tokens or rows == 0:
+        raise ValueError("%d rows cannot be shared evenly by %d tokens" % (rows, tokens))
+    return rows // tokens
+
+
+def lora_expert_linear_workspace(num_rows: int, hidden: int, out_features: int, max_loras: int, *,
+                                 quantized: bool = False, device="cuda") -> int:
+    """Bytes of workspace of :func:`lora_expert_linear` at these sizes."""
+    return _workspace_bytes("lora_expert_linear_workspace", device, num_rows, hidden, out_features,
+                            max_loras, int(quantized))
+
+
+def lora_expert_linear(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, meta: LoRAKernelMeta, *,
+                       weight_scale: Optional[torch.Tensor] = None, add_inputs: bool = False,
+                       workspace: Optional[torch.Tensor] = None) -> None:
+    """y[i] (+)= weight[id(i)] @ x[i // k]: the product of a mixture of
+    experts, which adapters are then added to (add_lora_linear); with one
+    expert, of one frozen layer.
+
+    meta was prepared for one expert id per row of y (-1: none, the row is left
+    as it is); x has a k-th of the rows, k of them in a row for each token (k =
+    1: as many).  weight is bf16 [max_loras, n, hidden], or the uint8 codes
+    [max_loras, n, hidden / 2] of :func:`lora_quantize_mxfp4` with their
+    weight_scale [max_loras, n, hidden / 32].  A workspace (uint8) is allocated
+    when none is given."""
+    index = _expert_types(x, "x", meta, ((x, "x"), (y, "y")), weight, weight_scale, workspace)
+    if x is None or y is None:
+        raise TypeError("x and y must be tensors")
+    T, K, x_ld = _rows(x, "x")
+    R, cols, y_ld = _rows(y, "y")
+    E, N = _expert_weight(weight, weight_scale, meta, index, K)
+    if cols != N:
+        raise ValueError("y must have %d columns" % N)
+    k = _fan_out(R, T, meta)
+    _call_with("lora_expert_linear", workspace, x.device, (R, K, N, meta.max_loras, int(weight_scale is not None)),
+               x.data_ptr(), x_ld, R, k, K, weight.data_ptr(),
+               None if weight_scale is None else weight_scale.data_ptr(), N, y.data_ptr(), y_ld,
+               1 if add_inputs else 0, ctypes.byref(meta.c))
+
+
+def lora_expert_linear_backward_workspace(num_rows: int, hidden: int, out_features: int, max_loras: int, *,
+                                          fan_out: int = 1, hidden_grad: bool = True, weight_grad: bool = False,
+                                          quantized: bool = False, device="cuda") -> int:
+    """Bytes of workspace of :func:`lora_expert_linear_backward` at these sizes."""
+    return _workspace_bytes("lora_expert_linear_backward_workspace", device, num_rows, fan_out, hidden,
+                            out_features, max_loras, int(hidden_grad), int(weight_grad), int(quantized))
+
+
+def lora_expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, meta: LoRAKernelMeta, *,
+                                weight_scale: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                                add_inputs: bool = False, d_weight: Optional[torch.Tensor] = None,
+                                workspace: Optional[torch.Tensor] = None) -> None:
+    """Gradients of :func:`lora_expert_linear`: dy is the gradient of its
+    output, the rest what it was given.
+
+    dx (bf16, like x): the sum over each token's rows, written, or with
+    add_inputs added to what is there; tokens without an expert get zeros, or
+    are left as they are.  d_weight (bf16 [max_loras, n, hidden], also for
+    4-bit weights) is overwritten; experts without rows get zeros, and so do
+    those that the weights hold beyond the metadata's."""
+    index = _expert_types(dy, "dy", meta, ((dy, "dy"), (x, "x"), (dx, "dx"), (d_weight, "d_weight")), weight,
+                          weight_scale, workspace)
+    if dy is None or x is None:
+        raise TypeError("dy and x must be tensors")
+    T, K, x_ld = _rows(x, "x")
+    R, cols, dy_ld = _rows(dy, "dy")
+    E, N = _expert_weight(weight, weight_scale, meta, index, K)
+    if cols != N:
+        raise ValueError("dy must have %d columns" % N)
+    k = _fan_out(R, T, meta)
+    dx_ptr, dx_ld, dw_ptr = None, K, None
+    if dx is not None:
+        rows, cols, dx_ld = _rows(dx, "dx")
+        if (rows, cols) != (T, K):
+            raise ValueError("dx must be [%d, %d]" % (T, K))
+        dx_ptr = dx.data_ptr()
+    if d_weight is not None:
+        if tuple(d_weight.shape) != (E, N, K) or not d_weight.is_contiguous():
+            raise ValueError("d_weight must be a contiguous %s tensor" % [E, N, K])
+        dw_ptr = d_weight.data_ptr()
+    _call_with("lora_expert_linear_backward", workspace, x.device,
+               (R, k, K, N, meta.max_loras, int(dx_ptr is not None), int(dw_ptr is not None),
+                int(weight_scale is not None)),
+               dy.data_ptr(), dy_ld, R, k, x.data_ptr(), x_ld, K, weight.data_ptr(),
+               None if weight_scale is None else weight_scale.data_ptr(), N, dx_ptr, dx_ld,
+               1 if add_inputs else 0, dw_ptr, ctypes.byref(meta.c))
+    if d_weight is not None and E > meta.max_loras:
+        _clear_behind(meta.max_loras, d_weight)
+
+
+def _mx_tensors(values: torch.Tensor, name: str, codes: torch.Tensor, scales: torch.Tensor) -> int:
+    index = _gpu(values, name)
+    if values.dtype is not _BF16 and values.dtype is not _F32:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, values.dtype))
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor)):
+        raise TypeError("codes and scales must be tensors")
+    _all(index, (codes, _U8, "codes"), (scales, _U8, "scales"))
+    if values.dim() < 1 or values.shape[-1] % 32 or not values.is_contiguous():
+        raise ValueError("%s must be contiguous [..., a multiple of 32]" % name)
+    for t, what, part in ((codes, "codes", 2), (scales, "scales", 32)):
+        if tuple(t.shape) != (*values.shape[:-1], values.shape[-1] // part) or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor"
+                             % (what, [*values.shape[:-1], values.shape[-1] // part]))
+    return index
+
+
+def lora_quantize_mxfp4(weight: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor) -> None:
+    """weight (bf16 or fp32 [..., n], n a multiple of 32) to microscaled 4 bits:
+    codes (uint8 [..., n / 2]) and a scale for every 32 elements (uint8 [..., n
+    / 32]), as :func:`lora_expert_linear` takes them.  A block with a NaN or an
+    infinity becomes NaN as a whole."""
+    index = _mx_tensors(weight, "weight", codes, scales)
+    _call("lora_quantize_mxfp4", weight.device, weight.data_ptr(), int(weight.dtype is _F32), weight.numel(),
+          codes.data_ptr(), scales.data_ptr(), _raw_stream(index))
+
+
+def lora_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor) -> None:
+    """The values that 4-bit codes stand for (bf16 or fp32 [..., n]), exactly."""
+    index = _mx_tensors(out, "out", codes, scales)
+    _call("lora_dequantize_mxfp4", out.device, codes.data_ptr(), scales.data_ptr(), out.numel(), out.data_ptr(),
+          int(out.dtype is _F32), _raw_stream(index))
+
+
+class LoRAGradients:
+    """The gradients of many layers, checked once, for
+    :func:`lora_clip_gradients` to be called on them every step.
+
+    grads: bf16 or fp32 tensors (None is skipped), contiguous, on one GPU.
+    groups: how many adapters their first dimension stacks (1: any shape).
+    out: None (they are scaled in place), or tensors like them that receive the
+    scaled gradients.  The tensors are kept; their storage must stay where it
+    is.  A workspace is allocated with it, so calls on one object must be
+    ordered on one stream."""
+
+    def __init__(self, grads, groups: int = 1, out=None):
+        if isinstance(grads, torch.Tensor):
+            grads = (grads,)
+        if isinstance(out, torch.Tensor):
+            out = (out,)
+        if groups < 1:
+            raise ValueError("groups must be at least 1")
+        if out is not None and len(out) != len(grads):
+            raise ValueError("out needs one entry per gradient")
+        pairs = [(i, g, None if out is None else out[i]) for i, g in enumerate(grads) if g is not None]
+        if not pairs:
+            raise ValueError("there are no gradients")
+        self.index = index = _gpu(pairs[0][1], "grads[%d]" % pairs[0][0])
+        for i, g, o in pairs:
+            _gpu(g, "grads[%d]" % i)
+            if g.dtype is not _BF16 and g.dtype is not _F32:
+                raise TypeError("grads[%d] must be bfloat16 or float32, got %s" % (i, g.dtype))
+            _all(index, (g, g.dtype, "grads[%d]" % i), (o, g.dtype, "out[%d]" % i))
+            if not g.is_contiguous():
+                raise ValueError("grads[%d] must be contiguous" % i)
+            if groups > 1 and (g.dim() < 1 or g.shape[0] != groups):
+                raise ValueError("grads[%d] must stack %d adapters in its first dimension" % (i, groups))
+            if out is not None and (o is None or o.shape != g.shape or not o.is_contiguous()):
+                raise ValueError("out[%d] must be contiguous like its gradient" % i)
+        n = len(pairs)
+        self.grads, self.out, self.groups, self.count = [p[1] for p in pairs], [p[2] for p in pairs], groups, n
+        self.device = self.grads[0].device
+        self.c_grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
+        self.c_out = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
+        self.c_sizes = (ctypes.c_int64 * n)(*[g.numel() // groups for g in self.grads])
+        self.c_f32 = (ctypes.c_int32 * n)(*[int(g.dtype is _F32) for g in self.grads])
+        self.workspace = torch.empty(_workspace_bytes("lora_clip_gradients_workspace", self.device, groups),
+                                     dtype=_U8, device=self.device)
+
+    @staticmethod
+    def make(grads, groups: int = 1, *, out=None) -> "LoRAGradients":
+        return LoRAGradients(grads, groups, out)
+
+
+def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *, eps: float = 1e-6) -> None:
+    """Scales gradients down to a largest norm: norms (fp32 [groups]) receives
+    the root of the sum of squares over all tensors, for each adapter of their
+    stacks (groups of them) or, with one element, over everything; gradients
+    are multiplied by min(1, max_norm / (norm + eps)).
+
+    grads is a :class:`LoRAGradients` (for every step), or the tensors
+    themselves, which are then scaled in place and stack norms.numel() adapters.
+    max_norm None (or infinite) computes the norms alone.  Nothing is read back to the host: a
+    NaN norm makes its adapter's gradients NaN, and leaves the others'."""
+    if not isinstance(norms, torch.Tensor):
+        raise TypeError("norms must be a torch.Tensor")
+    if not isinstance(grads, LoRAGradients):
+        grads = LoRAGradients(grads, norms.numel())
+    _all(grads.index, (norms, _F32, "norms"))
+    limit = math.inf if max_norm is None else float(max_norm)
+    if not limit >= 0.0 or not eps >= 0.0:
+        raise ValueError("max_norm and eps must not be negative")
+    _call("lora_clip_gradients", grads.device, grads.c_grads, grads.c_out, grads.c_sizes, grads.c_f32, grads.count,
+          grads.groups, limit, float(eps), _vector(norms, "norms", grads.groups), grads.workspace.data_ptr(),
+          grads.workspace.numel(), _raw_stream(grads.index))

@@ -16,7 +16,10 @@ LIB_PATH = os.path.join(PKG, "liblora_punica.so")
 EXPORTS = ("lora_meta_prepare", "lora_meta_read_no_lora", "lora_shrink", "lora_expand",
            "lora_expand_bf16", "lora_linear", "lora_linear_noalloc",
            "lora_cross_entropy", "lora_cross_entropy_workspace", "lora_orthogonalize",
-           "lora_linear_backward", "lora_linear_backward_workspace", "lora_orthogonalize_workspace", "lora_reload_options",
+           "lora_linear_backward", "lora_linear_backward_workspace", "lora_orthogonalize_workspace",
+           "lora_expert_linear", "lora_expert_linear_workspace", "lora_expert_linear_backward",
+           "lora_expert_linear_backward_workspace", "lora_quantize_mxfp4", "lora_dequantize_mxfp4",
+           "lora_clip_gradients", "lora_clip_gradients_workspace", "lora_reload_options",
            "lora_status_string", "lora_version")
 
 LORA_MAX_SLICES = 8
@@ -107,6 +110,25 @@ def load(path: str | None = None):
         lib.lora_orthogonalize.restype = ctypes.c_int
         lib.lora_orthogonalize_workspace.argtypes = [_I32, _I32, _I32]
         lib.lora_orthogonalize_workspace.restype = _I64
+        lib.lora_expert_linear.argtypes = [_P, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _I64, _I32,
+                                           ctypes.POINTER(LoraMetaC), _P, _I64, _P]
+        lib.lora_expert_linear.restype = ctypes.c_int
+        lib.lora_expert_linear_workspace.argtypes = [_I32, _I32, _I32, _I32, _I32]
+        lib.lora_expert_linear_workspace.restype = _I64
+        lib.lora_expert_linear_backward.argtypes = [_P, _I64, _I32, _I32, _P, _I64, _I32, _P, _P, _I32,
+                                                    _P, _I64, _I32, _P, ctypes.POINTER(LoraMetaC), _P,
+                                                    _I64, _P]
+        lib.lora_expert_linear_backward.restype = ctypes.c_int
+        lib.lora_expert_linear_backward_workspace.argtypes = [_I32] * 8
+        lib.lora_expert_linear_backward_workspace.restype = _I64
+        lib.lora_quantize_mxfp4.argtypes = [_P, _I32, _I64, _P, _P, _P]
+        lib.lora_quantize_mxfp4.restype = ctypes.c_int
+        lib.lora_dequantize_mxfp4.argtypes = [_P, _P, _I64, _P, _I32, _P]
+        lib.lora_dequantize_mxfp4.restype = ctypes.c_int
+        lib.lora_clip_gradients.argtypes = [_P, _P, _P, _P, _I32, _I32, _F, _F, _P, _P, _I64, _P]
+        lib.lora_clip_gradients.restype = ctypes.c_int
+        lib.lora_clip_gradients_workspace.argtypes = [_I32]
+        lib.lora_clip_gradients_workspace.restype = _I64
         lib.lora_reload_options.argtypes = []
         lib.lora_reload_options.restype = None
         lib.lora_status_string.argtypes = [ctypes.c_int]

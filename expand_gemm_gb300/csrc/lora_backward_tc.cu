@@ -620,16 +620,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) grad_x_tc_kernel(const __grid_c
     tc_finish(ring, p.error_word);
 }
 
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0, int c1,
-                                                 int c2, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];\n"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-
 // dx on CTA pairs: 256 tokens of one adapter, 128 of them in each CTA
 // with their g, and half of A's 256 columns in each, which leaves room for
 // more of A in flight and for eight epilogue warps (a half of the columns

@@ -1,0 +1,392 @@
+// lora_clip.cu -- lora_clip_gradients: the norm of many tensors' gradients,
+// together or for every adapter of their stacks, and the gradients scaled
+// down to a largest norm:
+//   norms[g] = sqrt(sum over tensors and elements of slice g of v^2)
+//   out      = v min(1, max_norm / (norms[g] + eps))
+//
+// Bound by memory: the gradients are read for the norm and once more to be
+// scaled.  Every slice is cut into units of CL_UNIT elements; CTAs take even
+// runs of units, group by group, so that a CTA leaves one partial sum for
+// each group that it meets, in an order that depends on the sizes alone: equal
+// inputs give equal bits.
+//
+// Squares are summed in fp32 over the elements a thread has of one unit and in
+// fp64 from there on.  Eight values whose squares would overflow fp32 or lose
+// digits to underflow (magnitudes above 2^60, or all below 2^-50) are squared
+// in fp64.
+#include <math.h>
+
+#include "lora_common.cuh"
+
+namespace lora {
+
+constexpr int CL_THREADS = 512;
+constexpr int CL_UNIT = 16384;
+constexpr int CL_FEW = 64;                     // tensors of a launch: with so many
+constexpr int CL_MANY = 1024;                  // or so many, 28 bytes of arguments each
+
+struct ClipShared {
+    int32_t tensors, groups;
+    int32_t units;                             // of one slice of all tensors of the launch
+    int32_t add;                               // the sums are added to those of earlier tensors
+    double *part;                              // [CTAs + groups]: CTA c's sum for group g at c + g
+    double *sum;                               // [groups]
+    float *factor, *norms;                     // [groups]
+    float max_norm, eps;
+    int32_t scale;                             // 0: norms only (out then receives copies)
+};
+
+template <int MAX>
+struct ClipArgs {
+    ClipShared s;
+    const void *in[MAX];
+    void *out[MAX];
+    int64_t n[MAX];                            // elements of a slice; bit 62: fp32
+    int32_t end[MAX];                          // units of a slice up to and with this tensor
+};
+constexpr int64_t CL_F32 = int64_t(1) << 62;
+static_assert(sizeof(ClipArgs<CL_MANY>) <= 32764, "kernel arguments");
+
+// CTA c's units: [c total / ctas, (c + 1) total / ctas).
+__host__ __device__ __forceinline__ int64_t clip_first(int64_t total, int c, int ctas)
+{
+    return total / ctas * c + total % ctas * c / ctas;
+}
+
+template <int MAX>
+__device__ __forceinline__ int clip_tensor(const ClipArgs<MAX> &a, int unit)
+{
+    int lo = 0, hi = a.s.tensors - 1;            // the first tensor that ends behind the unit
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a.end[mid] > unit) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ void clip_unpack(const uint4 &w, bool f32, float (&v)[8])
+{
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = f32 ? __uint_as_float(r[j]) : bf16_lo(r[j]);
+        v[2 * j + 1] = f32 ? 0.0f : bf16_hi(r[j]);
+    }
+}
+
+// The squares of eight values (of four where they are fp32).
+__device__ __forceinline__ void clip_add(const float (&v)[8], float &acc, double &far)
+{
+    float s = 0.0f, top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        s = fmaf(v[j], v[j], s);
+        top = fmaxf(top, fabsf(v[j]));
+    }
+    if ((top <= 0x1p60f && top >= 0x1p-50f) || top == 0.0f) {
+        acc += s;                              // NaN among zeros ends here too
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) far += double(v[j]) * double(v[j]);
+    }
+}
+
+__device__ __forceinline__ double block_sum(double v, double *warps)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int w = 0; w < CL_THREADS / 32; ++w) s += warps[w];
+    return s;
+}
+
+// Where unit `unit` of slice `group` lies: its first element and how many.
+struct ClipUnit {
+    const char *in;
+    char *out;
+    int count;
+    bool f32;
+};
+template <int MAX>
+__device__ __forceinline__ ClipUnit clip_unit(const ClipArgs<MAX> &a, int group, int unit)
+{
+    const int t = clip_tensor(a, unit);
+    const int64_t n = a.n[t] & ~CL_F32;
+    ClipUnit u;
+    u.f32 = (a.n[t] & CL_F32) != 0;
+    const int64_t at = int64_t(unit - (t > 0 ? a.end[t - 1] : 0)) * CL_UNIT;
+    const int64_t first = (group * n + at) * (u.f32 ? 4 : 2);
+    u.in = static_cast<const char *>(a.in[t]) + first;
+    u.out = static_cast<char *>(a.out[t]) + first;
+    u.count = int(n - at < CL_UNIT ? n - at : CL_UNIT);
+    return u;
+}
+
+__device__ __forceinline__ float clip_load(const char *p, bool f32, int i)
+{
+    return f32 ? reinterpret_cast<const float *>(p)[i] : bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_constant__ ClipArgs<MAX> a)
+{
+    __shared__ double s_warps[CL_THREADS / 32];
+    pdl_wait();
+    const int64_t total = int64_t(a.s.units) * a.s.groups;
+    const int64_t u0 = clip_first(total, blockIdx.x, gridDim.x), u1 = clip_first(total, blockIdx.x + 1, gridDim.x);
+    double far = 0.0;
+    for (int64_t u = u0; u < u1; ++u) {
+        const int group = int(u / a.s.units);
+        const ClipUnit c = clip_unit(a, group, int(u % a.s.units));
+        const int per = c.f32 ? 4 : 8;
+        float acc = 0.0f;
+        // elements before the first 16-byte boundary and behind the last
+        const int head = min(c.count, int((16 - (reinterpret_cast<uintptr_t>(c.in) & 15u)) & 15u) / (c.f32 ? 4 : 2));
+        const int whole = (c.count - head) / per;
+        const uint4 *src = reinterpret_cast<const uint4 *>(c.in + head * (c.f32 ? 4 : 2));
+        const int rest = c.count - whole * per;              // single elements: head, then tail
+        if (int(threadIdx.x) < rest) {
+            const int i = int(threadIdx.x) < head ? int(threadIdx.x) : int(threadIdx.x) + whole * per;
+            const float v[8] = {clip_load(c.in, c.f32, i), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            clip_add(v, acc, far);
+        }
+        int i = threadIdx.x;
+        for (; i + 3 * CL_THREADS < whole; i += 4 * CL_THREADS) {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = src[i + k * CL_THREADS];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v[8];
+                clip_unpack(w[k], c.f32, v);
+                clip_add(v, acc, far);
+            }
+        }
+        for (; i < whole; i += CL_THREADS) {
+            float v[8];
+            clip_unpack(src[i], c.f32, v);
+            clip_add(v, acc, far);
+        }
+        far += double(acc);
+        if (u + 1 == u1 || (u + 1) / a.s.units != group) {
+            const double s = block_sum(far, s_warps);
+            if (threadIdx.x == 0) a.s.part[blockIdx.x + group] = s;
+            far = 0.0;
+        }
+    }
+}
+
+struct JoinArgs {
+    ClipShared s;
+    int32_t ctas;                              // of the sum
+};
+
+// The partial sums of a group, in order; its norm and factor.  One warp a
+// group.
+__global__ void __launch_bounds__(256) clip_join_kernel(const JoinArgs j)
+{
+    pdl_wait();
+    const ClipShared &a = j.s;
+    const int ctas = j.ctas;
+    const int lane = threadIdx.x & 31;
+    const int64_t total = int64_t(a.units) * a.groups;
+    for (int g = blockIdx.x * 8 + (threadIdx.x >> 5); g < a.groups; g += gridDim.x * 8) {
+        const int64_t first = int64_t(g) * a.units, last = first + a.units;
+        double s = 0.0;
+        for (int c = lane; c < ctas; c += 32)
+            if (clip_first(total, c + 1, ctas) > first && clip_first(total, c, ctas) < last) s += a.part[c + g];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) {
+            if (a.add) s += a.sum[g];
+            const double norm = sqrt(s);
+            a.sum[g] = s;
+            a.norms[g] = float(norm);
+            // of the norm in 64 bits: it may lie beyond fp32.  A zero gradient
+            // stays one; NaN stays NaN.
+            const float f = float(double(a.max_norm) / (norm + double(a.eps)));
+            a.factor[g] = f >= 1.0f || norm == 0.0 ? 1.0f : f;
+        }
+    }
+}
+
+// out = v * factor.  Units are taken from the last one back: the end of what
+// the norm read may still lie in L2.
+template <int MAX>
+__global__ void __launch_bounds__(CL_THREADS) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
+{
+    pdl_wait();
+    const int64_t total = int64_t(a.s.units) * a.s.groups;
+    const int64_t u0 = clip_first(total, blockIdx.x, gridDim.x), u1 = clip_first(total, blockIdx.x + 1, gridDim.x);
+    for (int64_t u = u1 - 1; u >= u0; --u) {
+        const int group = int(u / a.s.units);
+        const ClipUnit c = clip_unit(a, group, int(u % a.s.units));
+        const float f = a.s.scale ? a.s.factor[group] : 1.0f;
+        if (f == 1.0f && c.in == c.out) continue;
+        const int size = c.f32 ? 4 : 2, per = 16 / size;
+        const bool same = ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
+        const int head = same ? min(c.count, int((16 - (reinterpret_cast<uintptr_t>(c.in) & 15u)) & 15u) / size)
+                              : c.count;
+        const int whole = (c.count - head) / per;
+        for (int j = threadIdx.x; j < c.count - whole * per; j += CL_THREADS) {
+            const int i = j < head ? j : j + whole * per;
+            const float v = clip_load(c.in, c.f32, i) * f;
+            if (c.f32) reinterpret_cast<float *>(c.out)[i] = v;
+            else reinterpret_cast<uint16_t *>(c.out)[i] = uint16_t(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+        }
+        const uint4 *src = reinterpret_cast<const uint4 *>(c.in + head * size);
+        uint4 *dst = reinterpret_cast<uint4 *>(c.out + head * size);
+        auto scaled = [&](const uint4 &w) {
+            if (c.f32)
+                return make_uint4(__float_as_uint(__uint_as_float(w.x) * f), __float_as_uint(__uint_as_float(w.y) * f),
+                                  __float_as_uint(__uint_as_float(w.z) * f), __float_as_uint(__uint_as_float(w.w) * f));
+            return make_uint4(pack_bf16x2(bf16_lo(w.x) * f, bf16_hi(w.x) * f),
+                              pack_bf16x2(bf16_lo(w.y) * f, bf16_hi(w.y) * f),
+                              pack_bf16x2(bf16_lo(w.z) * f, bf16_hi(w.z) * f),
+                              pack_bf16x2(bf16_lo(w.w) * f, bf16_hi(w.w) * f));
+        };
+        int i = threadIdx.x;
+        for (; i + 3 * CL_THREADS < whole; i += 4 * CL_THREADS) {
+            uint4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = src[i + k * CL_THREADS];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dst[i + k * CL_THREADS] = scaled(w[k]);
+        }
+        for (; i < whole; i += CL_THREADS) dst[i] = scaled(src[i]);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+struct ClipPlan {
+    int32_t groups;
+    int ctas;                                  // most CTAs of a launch
+    int64_t sum, factor, bytes;
+};
+
+static ClipPlan clip_plan(int32_t groups)
+{
+    ClipPlan p;
+    p.groups = groups;
+    p.ctas = 4 * device_sm_count();
+    const int64_t part = (int64_t(p.ctas) + groups) * 8;
+    p.sum = (part + 255) / 256 * 256;
+    p.factor = p.sum + (int64_t(groups) * 8 + 255) / 256 * 256;
+    p.bytes = p.factor + (int64_t(groups) * 4 + 255) / 256 * 256;
+    return p;
+}
+
+// Tensors [first, first + many) of the call.
+struct ClipCall {
+    const void *const *grads;
+    void *const *out;
+    const int64_t *sizes;
+    const int32_t *f32;
+    int32_t tensors;
+    ClipShared s;
+};
+
+template <int MAX>
+static void clip_args(ClipArgs<MAX> &a, const ClipCall &c, int first)
+{
+    a.s = c.s;
+    a.s.tensors = c.tensors - first < MAX ? c.tensors - first : MAX;
+    int64_t units = 0;
+    for (int i = 0; i < a.s.tensors; ++i) {
+        const int64_t n = c.sizes[first + i];
+        a.in[i] = c.grads[first + i];
+        a.out[i] = c.out != nullptr ? c.out[first + i] : const_cast<void *>(c.grads[first + i]);
+        a.n[i] = n | (c.f32[first + i] ? CL_F32 : 0);
+        units += (n + CL_UNIT - 1) / CL_UNIT;
+        a.end[i] = int32_t(units);
+    }
+    a.s.units = int32_t(units);
+}
+
+template <int MAX>
+static int run_clip(const ClipCall &c, int most, cudaStream_t st)
+{
+    bool any = false;
+    ClipArgs<MAX> a;
+    for (int first = 0; first < c.tensors; first += MAX) {
+        clip_args(a, c, first);
+        const int64_t total = int64_t(a.s.units) * a.s.groups;
+        if (total == 0) continue;
+        a.s.add = any;
+        any = true;
+        const int ctas = int(total < most ? total : most);
+        cudaError_t e = launch_kernel(clip_sum_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
+        if (e != cudaSuccess) return int(e);
+        JoinArgs j{a.s, ctas};
+        const int joins = (c.s.groups + 7) / 8 < 64 ? (c.s.groups + 7) / 8 : 64;
+        e = launch_kernel(clip_join_kernel, dim3(unsigned(joins)), dim3(256), 0, st, j);
+        if (e != cudaSuccess) return int(e);
+    }
+    if (!any) return int(cudaMemsetAsync(c.s.norms, 0, size_t(c.s.groups) * sizeof(float), st));
+    if (!c.s.scale && c.out == nullptr) return LORA_OK;
+    for (int first = 0; first < c.tensors; first += MAX) {
+        clip_args(a, c, first);
+        const int64_t total = int64_t(a.s.units) * a.s.groups;
+        if (total == 0) continue;
+        const int ctas = int(total < most ? total : most);
+        const cudaError_t e = launch_kernel(clip_scale_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
+        if (e != cudaSuccess) return int(e);
+    }
+    return LORA_OK;
+}
+
+}  // namespace lora
+
+LORA_API int64_t lora_clip_gradients_workspace(int32_t groups)
+{
+    if (groups < 1) return LORA_ERR_SIZE;
+    return lora::clip_plan(groups).bytes;
+}
+
+LORA_API int lora_clip_gradients(const void *const *grads, void *const *out, const int64_t *slice_sizes,
+                                 const int32_t *grads_f32, int32_t num_tensors, int32_t groups, float max_norm,
+                                 float eps, float *norms, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    using namespace lora;
+    NvtxRange nvtx_range("lora_clip_gradients");
+    if (num_tensors < 0 || groups < 1 || !(max_norm >= 0.0f) || !(eps >= 0.0f)) return LORA_ERR_SIZE;
+    if (norms == nullptr || workspace == nullptr ||
+        (num_tensors > 0 && (grads == nullptr || slice_sizes == nullptr || grads_f32 == nullptr)))
+        return LORA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return LORA_ERR_ALIGN;
+    int64_t units = 0;
+    for (int i = 0; i < num_tensors; ++i) {
+        if (slice_sizes[i] < 0) return LORA_ERR_SIZE;
+        units += (slice_sizes[i] + CL_UNIT - 1) / CL_UNIT;
+        if (units > INT32_MAX) return LORA_ERR_SIZE;
+        if (slice_sizes[i] == 0) continue;
+        if (grads[i] == nullptr || (out != nullptr && out[i] == nullptr)) return LORA_ERR_NULL;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]) |
+                             (out != nullptr ? reinterpret_cast<uintptr_t>(out[i]) : 0);
+        if (at & (grads_f32[i] ? 3u : 1u)) return LORA_ERR_ALIGN;
+    }
+    const ClipPlan plan = clip_plan(groups);
+    if (workspace_bytes < plan.bytes) return LORA_ERR_WORKSPACE;
+    ClipCall c;
+    c.grads = grads;
+    c.out = out;
+    c.sizes = slice_sizes;
+    c.f32 = grads_f32;
+    c.tensors = num_tensors;
+    char *ws = static_cast<char *>(workspace);
+    c.s = ClipShared{};
+    c.s.groups = groups;
+    c.s.part = reinterpret_cast<double *>(ws);
+    c.s.sum = reinterpret_cast<double *>(ws + plan.sum);
+    c.s.factor = reinterpret_cast<float *>(ws + plan.factor);
+    c.s.norms = norms;
+    c.s.max_norm = max_norm;
+    c.s.eps = eps;
+    c.s.scale = max_norm < INFINITY;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return num_tensors <= CL_FEW ? run_clip<CL_FEW>(c, plan.ctas, st) : run_clip<CL_MANY>(c, plan.ctas, st);
+}

@@ -1,0 +1,384 @@
+// lora_expert.cu -- lora_expert_linear and lora_expert_linear_backward: the
+// products of a mixture of experts (or, with one expert, of one frozen
+// layer), grouped by the ids that LoRAKernelMeta sorts:
+//   y[i]  (+)= W[id(i)] x[i / fan]
+//   dx[t] (+)= sum_{j < fan} W[id]^T dy[t fan + j]
+//   dW[e]  = sum_{i: id(i) = e} dy[i] x[i / fan]^T
+// This file: the copies in the order of experts, the table of tiles, the join
+// of a token's rows, and the C entries.
+#include <stdint.h>
+
+#include "lora_expert.cuh"
+
+namespace lora {
+
+constexpr int EX_PACK_THREADS = 256;
+
+// One row of `cols` bf16, by a warp.  Whole 16-byte pieces where both ends
+// allow it.
+__device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int cols, bool vec)
+{
+    const int lane = threadIdx.x & 31;
+    if (vec) {
+        const int n = cols / 8;
+        const uint4 *from = reinterpret_cast<const uint4 *>(src);
+        uint4 *to = reinterpret_cast<uint4 *>(dst);
+        int c = lane;
+        for (; c + 96 < n; c += 128) {
+            const uint4 a = from[c], b = from[c + 32], d = from[c + 64], e = from[c + 96];
+            to[c] = a;
+            to[c + 32] = b;
+            to[c + 64] = d;
+            to[c + 96] = e;
+        }
+        for (; c < n; c += 32) to[c] = from[c];
+        for (int i = n * 8 + lane; i < cols; i += 32) dst[i] = src[i];
+    } else {
+        for (int i = lane; i < cols; i += 32) dst[i] = src[i];
+    }
+}
+
+// Copies x (blockIdx.y == 0) and dy (1) into the order of experts; a warp
+// takes a row.  The first block also writes the table of tiles and, for dW,
+// each expert's K blocks; rows of dx that no expert adds to are cleared here
+// (dx overwritten, one row a token).
+__global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __grid_constant__ ExpertArgs p)
+{
+    extern __shared__ int ex_tab[];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warps = EX_PACK_THREADS / 32;
+    const SegTab tab = seg_tab(ex_tab, p.nbins);
+    const int pad = p.pad ? EX_PAD : 1;
+    const int units = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, pad, tab, false, 0,
+                                    p.R, p.error_word);
+    const bool dy = blockIdx.y == 1;
+    const uint16_t *src = dy ? p.dy : p.x;
+    uint16_t *dst = dy ? p.dys : p.xs;
+    const int64_t src_ld = dy ? p.dy_ld : p.x_ld, dst_ld = dy ? p.dys_ld : p.K;
+    const int cols = dy ? p.N : p.K, fan = dy ? 1 : p.fan;
+    const bool vec = dy ? p.dy_vec : p.x_vec;
+    if (dst != nullptr) {
+        const int64_t rows = int64_t(units) * pad;
+        for (int64_t q = int64_t(blockIdx.x) * warps + warp; q < rows; q += int64_t(gridDim.x) * warps) {
+            const int k = find_segment(tab.tile, p.nbins, int(q / pad));
+            const int local = int(q - int64_t(tab.tile[k]) * pad);
+            uint16_t *to = dst + q * dst_ld;
+            int row = -1;
+            if (local < tab.count[k]) row = checked_token(p.sorted[tab.start[k] + local], p.R, p.error_word);
+            if (row >= 0) {
+                copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
+            } else {
+                for (int c = lane; c < int(dst_ld / 8); c += 32)
+                    reinterpret_cast<uint4 *>(to)[c] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    if (blockIdx.y == 0 && p.dx != nullptr && p.fan == 1 && !p.add) {
+        const bool none = *p.no_lora != 0;
+        const int rest = none ? p.R : (tab.id[0] == -1 ? tab.count[0] : 0);
+        for (int64_t i = int64_t(blockIdx.x) * warps + warp; i < rest; i += int64_t(gridDim.x) * warps) {
+            const int row = none ? int(i) : checked_token(p.sorted[i], p.R, p.error_word);
+            if (row < 0) continue;
+            uint16_t *to = p.dx + int64_t(row) * p.dx_ld;
+            if (p.dx_vec) {
+                for (int c = lane; c < p.K / 8; c += 32)
+                    reinterpret_cast<uint4 *>(to)[c] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int c = lane; c < p.K; c += 32) to[c] = 0;
+            }
+        }
+    }
+    if (blockIdx.x != 0 || blockIdx.y != 0) return;
+    if (p.blocks != nullptr) {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.blocks[e] = make_int2(0, 0);
+        __syncthreads();
+        for (int k = threadIdx.x; units > 0 && k < p.nbins; k += blockDim.x)
+            if (tab.id[k] >= 0 && tab.count[k] > 0)
+                p.blocks[tab.id[k]] = make_int2(tab.tile[k], tab.tile[k + 1] - tab.tile[k]);
+    }
+    if (p.table == nullptr) return;
+    // the segments' rows in the copy, kept while the same memory takes the tiles'
+    int *first_row = ex_tab + 4 * p.nbins + 2;
+    for (int k = threadIdx.x; units > 0 && k < p.nbins; k += blockDim.x) first_row[k] = tab.tile[k] * pad;
+    __syncthreads();
+    const int tiles = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, p.tile_rows, tab, false, 0,
+                                    p.R, p.error_word);
+    if (threadIdx.x == 0) *p.tiles = tiles;
+    for (int t = threadIdx.x; t < tiles; t += blockDim.x) {
+        const int k = find_segment(tab.tile, p.nbins, t);
+        ExpertTile e;
+        e.base = tab.tile[k];
+        e.tiles = tab.tile[k + 1] - tab.tile[k];
+        e.expert = tab.id[k];
+        e.start = tab.start[k];
+        e.count = tab.count[k];
+        e.row = first_row[k];
+        e.pad0 = e.pad1 = 0;
+        p.table[t] = e;
+    }
+}
+
+// dx[t] (+)= the sum of the token's rows, in fp32 and in their order, rounded
+// once.  Rows without an expert have no part.  A warp takes 32 x 4 columns of
+// a token at a time.
+__global__ void __launch_bounds__(256) expert_join_kernel(const __grid_constant__ ExpertArgs p)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const bool none = *p.no_lora != 0;
+    const int64_t T = p.R / p.fan, warps = int64_t(gridDim.x) * (blockDim.x / 32);
+    for (int64_t t = int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; t < T; t += warps) {
+        const int32_t *ids = p.ids + t * p.fan;
+        const float *part = p.part + t * p.fan * p.K;
+        uint16_t *out = p.dx + t * p.dx_ld;
+        for (int c = lane * 4; c < p.K; c += 128) {
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            bool any = false;
+            if (!none) {
+                for (int j = 0; j < p.fan; ++j) {
+                    const int id = ids[j];
+                    if (id < 0 || id >= p.E) continue;
+                    const float4 v = *reinterpret_cast<const float4 *>(part + int64_t(j) * p.K + c);
+                    // the first part as it is: 0 + -0 would lose its sign
+                    s = any ? make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w) : v;
+                    any = true;
+                }
+            }
+            if (p.add && !any) continue;
+            if (p.dx_vec) {
+                uint2 *to = reinterpret_cast<uint2 *>(out + c);
+                if (p.add) {
+                    const uint2 was = *to;
+                    s = make_float4(s.x + bf16_lo(was.x), s.y + bf16_hi(was.x), s.z + bf16_lo(was.y),
+                                    s.w + bf16_hi(was.y));
+                }
+                *to = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+            } else {
+                if (p.add)
+                    s = make_float4(s.x + bf16_to_f32(out[c]), s.y + bf16_to_f32(out[c + 1]),
+                                    s.z + bf16_to_f32(out[c + 2]), s.w + bf16_to_f32(out[c + 3]));
+                const uint32_t a = pack_bf16x2(s.x, s.y), b = pack_bf16x2(s.z, s.w);
+                out[c] = uint16_t(a & 0xFFFFu);
+                out[c + 1] = uint16_t(a >> 16);
+                out[c + 2] = uint16_t(b & 0xFFFFu);
+                out[c + 3] = uint16_t(b >> 16);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+int expert_shared_memory(const void *kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return int(e);
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return 0;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return int(e);
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return 0;
+}
+
+static int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
+
+// Offsets in the workspace, in bytes.
+struct ExpertLayout {
+    int64_t tiles, table, blocks, xs, dys, part, w, bytes;
+    int64_t rows;                     // of the copies
+};
+
+// A batch of R rows; every size grows with R, so that a workspace for a batch
+// holds each smaller one.
+static ExpertLayout expert_layout(int64_t R, int fan, int64_t K, int64_t N, int64_t E, bool x_copy, bool dx, bool dw,
+                                  bool decode)
+{
+    ExpertLayout l;
+    const int64_t active = R < E ? R : E;
+    l.rows = R + (dw ? (EX_PAD - 1) * active : 0);
+    int64_t at = 256;
+    l.tiles = 0;
+    l.table = at;
+    at += up256((R / EX_TILE + active) * int64_t(sizeof(ExpertTile)));
+    l.blocks = at;
+    at += dw ? up256(E * 8) : 0;
+    l.xs = at;
+    at += x_copy ? up256(l.rows * K * 2) : 0;
+    l.dys = at;
+    at += dx || dw ? up256(l.rows * ((N + 7) / 8 * 8) * 2) : 0;
+    l.part = at;
+    at += dx && fan > 1 ? up256(R * K * 4) : 0;
+    l.w = at;
+    at += decode ? up256(E * N * K * 2) : 0;
+    l.bytes = at;
+    return l;
+}
+
+static uintptr_t bits(const void *ptr) { return reinterpret_cast<uintptr_t>(ptr); }
+
+static int check_sizes(int32_t R, int32_t fan, int32_t K, int32_t N, int32_t E, bool quantized)
+{
+    if (R < 0 || fan < 1 || R % fan != 0 || K < 8 || N < 1 || E < 1 || E > LORA_MAX_LORAS) return LORA_ERR_SIZE;
+    if (K % (quantized ? 32 : 8) != 0) return LORA_ERR_ALIGN;
+    return LORA_OK;
+}
+
+static int fill(ExpertArgs &p, int32_t R, int32_t fan, int32_t K, int32_t N, const lora_bf16_t *x, int64_t x_ld,
+                const void *weight, const uint8_t *scale, const lora_meta_t *meta)
+{
+    if (meta == nullptr || meta->token_lora_mapping == nullptr || meta->token_indices_sorted_by_lora_ids == nullptr ||
+        meta->num_tokens_per_lora == nullptr || meta->lora_token_start_loc == nullptr ||
+        meta->active_lora_ids == nullptr || meta->no_lora_flag == nullptr || meta->error_word == nullptr)
+        return LORA_ERR_NULL;
+    if (int e = check_sizes(R, fan, K, N, meta->max_loras, scale != nullptr)) return e;
+    if (R > meta->max_num_tokens) return LORA_ERR_TOKENS;
+    if (weight == nullptr || (R > 0 && x == nullptr)) return LORA_ERR_NULL;
+    if (x_ld < K) return LORA_ERR_SIZE;
+    if ((bits(weight) | bits(scale)) & 15u) return LORA_ERR_ALIGN;
+    p = ExpertArgs{};
+    p.x = x;
+    p.x_ld = x_ld;
+    p.x_vec = (bits(x) & 15u) == 0 && x_ld % 8 == 0;
+    if (scale != nullptr) {
+        p.codes = static_cast<const uint8_t *>(weight);
+        p.scales = scale;
+    } else {
+        p.w = static_cast<const uint16_t *>(weight);
+    }
+    p.R = R;
+    p.fan = fan;
+    p.K = K;
+    p.N = N;
+    p.E = meta->max_loras;
+    p.nbins = meta->max_loras + 1;
+    p.tile_rows = EX_TILE;
+    p.ids = meta->token_lora_mapping;
+    p.sorted = meta->token_indices_sorted_by_lora_ids;
+    p.counts = meta->num_tokens_per_lora;
+    p.start_loc = meta->lora_token_start_loc;
+    p.active = meta->active_lora_ids;
+    p.no_lora = meta->no_lora_flag;
+    p.error_word = meta->error_word;
+    return LORA_OK;
+}
+
+static int launch_pack(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+{
+    const int64_t want = (rows + EX_PACK_THREADS / 32 - 1) / (EX_PACK_THREADS / 32);
+    const int64_t most = 6ll * device_sm_count();
+    const dim3 grid(unsigned(want < most ? (want > 0 ? want : 1) : most), p.dys != nullptr ? 2 : 1);
+    return int(launch_kernel(expert_pack_kernel, grid, dim3(EX_PACK_THREADS),
+                             seg_tab_bytes(p.nbins) + p.nbins * sizeof(int), st, p));
+}
+
+}  // namespace lora
+
+LORA_API int64_t lora_expert_linear_workspace(int32_t num_rows, int32_t hidden, int32_t out_features,
+                                              int32_t max_loras, int32_t quantized)
+{
+    using namespace lora;
+    if (int e = check_sizes(num_rows, 1, hidden, out_features, max_loras, quantized != 0)) return e;
+    return expert_layout(num_rows, 1, hidden, out_features, max_loras, true, false, false, quantized != 0).bytes;
+}
+
+LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_rows, int32_t fan_out,
+                                int32_t hidden, const void *weight, const uint8_t *weight_scale,
+                                int32_t out_features, lora_bf16_t *y, int64_t y_ld, int32_t add_inputs,
+                                const lora_meta_t *meta, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    using namespace lora;
+    NvtxRange nvtx_range("lora_expert_linear");
+    ExpertArgs p;
+    if (int e = fill(p, num_rows, fan_out, hidden, out_features, x, x_ld, weight, weight_scale, meta)) return e;
+    if (workspace == nullptr || (num_rows > 0 && y == nullptr)) return LORA_ERR_NULL;
+    if (y_ld < out_features) return LORA_ERR_SIZE;
+    if (bits(workspace) & 255u) return LORA_ERR_ALIGN;
+    const bool quantized = weight_scale != nullptr;
+    const ExpertLayout lay = expert_layout(num_rows, 1, hidden, out_features, p.E, true, false, false, quantized);
+    if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
+    if (num_rows == 0) return LORA_OK;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    p.y = y;
+    p.y_ld = y_ld;
+    p.y_vec = (bits(y) & 15u) == 0 && y_ld % 8 == 0 && out_features % 8 == 0;
+    p.add = add_inputs != 0;
+    p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
+    p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);
+    p.xs = reinterpret_cast<uint16_t *>(ws + lay.xs);
+    if (int e = launch_pack(p, lay.rows, st)) return e;
+    if (quantized) {
+        uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
+        if (int e = launch_expert_decode(p, w, st)) return e;
+        p.w = w;
+    }
+    return launch_expert_forward(p, lay.rows, st);
+}
+
+LORA_API int64_t lora_expert_linear_backward_workspace(int32_t num_rows, int32_t fan_out, int32_t hidden,
+                                                       int32_t out_features, int32_t max_loras, int32_t hidden_grad,
+                                                       int32_t weight_grad, int32_t quantized)
+{
+    using namespace lora;
+    if (int e = check_sizes(num_rows, fan_out, hidden, out_features, max_loras, quantized != 0)) return e;
+    return expert_layout(num_rows, fan_out, hidden, out_features, max_loras, weight_grad != 0, hidden_grad != 0,
+                         weight_grad != 0, hidden_grad != 0 && quantized != 0).bytes;
+}
+
+LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_rows, int32_t fan_out,
+                                         const lora_bf16_t *x, int64_t x_ld, int32_t hidden, const void *weight,
+                                         const uint8_t *weight_scale, int32_t out_features, lora_bf16_t *dx,
+                                         int64_t dx_ld, int32_t add_inputs, lora_bf16_t *d_weight,
+                                         const lora_meta_t *meta, void *workspace, int64_t workspace_bytes,
+                                         void *stream)
+{
+    using namespace lora;
+    NvtxRange nvtx_range("lora_expert_linear_backward");
+    ExpertArgs p;
+    if (int e = fill(p, num_rows, fan_out, hidden, out_features, x, x_ld, weight, weight_scale, meta)) return e;
+    if (workspace == nullptr || (num_rows > 0 && dy == nullptr)) return LORA_ERR_NULL;
+    if (dy_ld < out_features || (dx != nullptr && dx_ld < hidden)) return LORA_ERR_SIZE;
+    if ((bits(workspace) & 255u) || (bits(d_weight) & 15u)) return LORA_ERR_ALIGN;
+    const bool hx = dx != nullptr, hw = d_weight != nullptr, decode = hx && weight_scale != nullptr;
+    const ExpertLayout lay = expert_layout(num_rows, fan_out, hidden, out_features, p.E, hw, hx, hw, decode);
+    if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!hx && !hw) return LORA_OK;
+    if (num_rows == 0) {
+        if (!hw) return LORA_OK;
+        return int(cudaMemsetAsync(d_weight, 0, size_t(p.E) * out_features * hidden * 2, st));
+    }
+    char *ws = static_cast<char *>(workspace);
+    p.dy = dy;
+    p.dy_ld = dy_ld;
+    p.dy_vec = (bits(dy) & 15u) == 0 && dy_ld % 8 == 0;
+    p.dys = reinterpret_cast<uint16_t *>(ws + lay.dys);
+    p.dys_ld = (out_features + 7) / 8 * 8;
+    p.xs = hw ? reinterpret_cast<uint16_t *>(ws + lay.xs) : nullptr;
+    p.pad = hw;
+    p.dx = dx;
+    p.dx_ld = dx_ld;
+    p.dx_vec = (bits(dx) & 15u) == 0 && dx_ld % 8 == 0;
+    p.dw = d_weight;
+    p.add = add_inputs != 0;
+    p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
+    p.table = hx ? reinterpret_cast<ExpertTile *>(ws + lay.table) : nullptr;
+    p.blocks = hw ? reinterpret_cast<int2 *>(ws + lay.blocks) : nullptr;
+    p.part = hx && fan_out > 1 ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
+    if (int e = launch_pack(p, lay.rows, st)) return e;
+    if (hw)
+        if (int e = launch_expert_dw(p, lay.rows, st)) return e;
+    if (!hx) return LORA_OK;
+    if (decode) {
+        uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
+        if (int e = launch_expert_decode(p, w, st)) return e;
+        p.w = w;
+    }
+    if (int e = launch_expert_dx(p, lay.rows, st)) return e;
+    if (fan_out == 1) return LORA_OK;
+    const int64_t tokens = num_rows / fan_out, want = (tokens + 7) / 8, most = 8ll * device_sm_count();
+    return int(launch_kernel(expert_join_kernel, dim3(unsigned(want < most ? want : most)), dim3(256), 0, st, p));
+}

@@ -48,6 +48,17 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// The same for a box of one matrix of a stack (encode_stack_map).
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int c0,
+                                                 int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
 // Arrive on the barrier at this shared-memory offset in both CTAs of the
 // pair once every pair UMMA issued so far by this thread has completed.
 __device__ __forceinline__ void umma_commit_both(uint32_t bar)
@@ -82,18 +93,19 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t panel 
     return d;
 }
 
-// One tile of work: its first row of A and of B, its K blocks, and the
-// accumulator's epilogue arguments (what they mean is the kernel's).
+// One tile of work: its first row of A and of B, its K blocks, and, where B is
+// a stack of matrices, which of them.
 struct PairItem {
     int row_a, row_b, kb0, kb1;
+    int mat = 0;
 };
 
 // Runs `total` items on the grid's pairs.  A_T / B_T: the operand is stored
-// with its rows contiguous.  item(i) -> PairItem (every thread computes the
+// with its rows contiguous.  B_STACK: map_b is a stack's (encode_stack_map).  item(i) -> PairItem (every thread computes the
 // same); epilogue(i, item, tmem address of this warp's 32 lanes, row of this
 // thread within the CTA's 128 rows, first of its 128 columns, CTA rank,
 // whether the item has no K blocks).
-template <bool A_T, bool B_T, typename ItemFn, typename EpiFn>
+template <bool A_T, bool B_T, bool B_STACK = false, typename ItemFn, typename EpiFn>
 __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtensorMap *map_b,
                                           int total, int32_t *error_word, ItemFn item_of,
                                           EpiFn epilogue)
@@ -164,7 +176,12 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
                     } else {
                         tma_load_2d_pair(sa, map_a, kb * PG_BK, ra, full);
                     }
-                    if constexpr (B_T) {
+                    if constexpr (B_STACK && B_T) {
+                        tma_load_3d_pair(sb, map_b, rb, kb * PG_BK, it.mat, full);
+                        tma_load_3d_pair(sb + 8192, map_b, rb + 64, kb * PG_BK, it.mat, full);
+                    } else if constexpr (B_STACK) {
+                        tma_load_3d_pair(sb, map_b, kb * PG_BK, rb, it.mat, full);
+                    } else if constexpr (B_T) {
                         tma_load_2d_pair(sb, map_b, rb, kb * PG_BK, full);
                         tma_load_2d_pair(sb + 8192, map_b, rb + 64, kb * PG_BK, full);
                     } else {

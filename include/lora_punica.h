@@ -478,6 +478,145 @@ int lora_orthogonalize(const void *update, int32_t update_f32, int32_t count, in
 int64_t lora_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols);
 
 /*
+ * lora_expert_linear -- the product of a mixture of experts, grouped by the
+ * ids of the metadata (an expert per row): the layer that adapters are added
+ * to.  With one expert it is one frozen layer.
+ *   y[i] (+)= weight[id(i)] x[i / fan_out]        for every row i with an id
+ * Rows without an id are not touched.
+ *
+ *   x            device bf16 [num_rows / fan_out, x_ld], any alignment: the
+ *                tokens.  Token t has rows t * fan_out ... of y and of the
+ *                metadata (a router's choices), each with an id of its own;
+ *                num_rows is a multiple of fan_out >= 1.
+ *   hidden       a multiple of 8 (of 32 with weight_scale).
+ *   weight       device, 16-byte aligned: bf16 [max_loras, out_features,
+ *                hidden] (weight_scale NULL), or the codes of
+ *                lora_quantize_mxfp4, uint8 [max_loras, out_features,
+ *                hidden / 2].
+ *   weight_scale NULL, or the scales of the codes, 16-byte aligned uint8
+ *                [max_loras, out_features, hidden / 32].
+ *   y            device bf16 [num_rows, y_ld], any alignment (rows on 16-byte
+ *                boundaries are written faster).  Must not overlap an input.
+ *   add_inputs   nonzero: added to y; zero: y is overwritten.
+ *   meta         prepared for these num_rows ids; max_loras is the number of
+ *                experts.
+ *   workspace    256-byte aligned, at least lora_expert_linear_workspace
+ *                bytes; a workspace for a batch holds every smaller one.
+ *
+ * Products run in bf16 on the tensor cores with fp32 sums, and each value of y
+ * is rounded to bf16 once; 4-bit weights are bf16 values, so their products
+ * lose nothing beside that (a scale of 2^127 times 6 is an infinity there).
+ * Deterministic.  Bit 30 of meta->error_word: a bounded wait ran out (the
+ * output is then not valid).  Errors: LORA_ERR_NULL, LORA_ERR_SIZE,
+ * LORA_ERR_ALIGN, LORA_ERR_TOKENS, LORA_ERR_WORKSPACE, LORA_ERR_DEVICE.
+ */
+int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_rows, int32_t fan_out,
+                       int32_t hidden, const void *weight, const uint8_t *weight_scale,
+                       int32_t out_features, lora_bf16_t *y, int64_t y_ld, int32_t add_inputs,
+                       const lora_meta_t *meta, void *workspace, int64_t workspace_bytes,
+                       void *stream);
+
+/* Bytes of workspace of lora_expert_linear on the current device; a negative
+ * status for sizes that it refuses. */
+int64_t lora_expert_linear_workspace(int32_t num_rows, int32_t hidden, int32_t out_features,
+                                     int32_t max_loras, int32_t quantized);
+
+/*
+ * lora_expert_linear_backward -- the gradients of lora_expert_linear:
+ *   dx[t] (+)= sum over the token's rows i with an id of weight[id(i)]^T dy[i]
+ *   d_weight[e] = sum over the rows i with id e of dy[i] x[i / fan_out]^T
+ *
+ *   dy           device bf16 [num_rows, dy_ld], any alignment.
+ *   x, fan_out, hidden, weight, weight_scale, out_features, meta: those of
+ *                the forward pass.
+ *   dx           NULL or device bf16 [num_rows / fan_out, dx_ld], any
+ *                alignment.  The sum over a token's rows is fp32, in their
+ *                order, and rounded once.  No output may overlap an input or
+ *                another output.
+ *   add_inputs   nonzero: added to dx (tokens without any id are not
+ *                touched); zero: dx is overwritten (those with zeros).
+ *   d_weight     NULL or device bf16 [max_loras, out_features, hidden],
+ *                16-byte aligned, overwritten: zeros for experts without
+ *                rows.  With 4-bit weights it is the gradient of the values
+ *                that they stand for.
+ *
+ * Deterministic.  Errors as lora_expert_linear.
+ */
+int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, int32_t num_rows,
+                                int32_t fan_out, const lora_bf16_t *x, int64_t x_ld,
+                                int32_t hidden, const void *weight, const uint8_t *weight_scale,
+                                int32_t out_features, lora_bf16_t *dx, int64_t dx_ld,
+                                int32_t add_inputs, lora_bf16_t *d_weight,
+                                const lora_meta_t *meta, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_expert_linear_backward, by whether dx and
+ * d_weight are asked for; a negative status for sizes that it refuses. */
+int64_t lora_expert_linear_backward_workspace(int32_t num_rows, int32_t fan_out, int32_t hidden,
+                                              int32_t out_features, int32_t max_loras,
+                                              int32_t hidden_grad, int32_t weight_grad,
+                                              int32_t quantized);
+
+/*
+ * lora_quantize_mxfp4 / lora_dequantize_mxfp4 -- weights in microscaled 4 bits
+ * (OCP MXFP4) and back.  Every 32 elements that follow one another share a
+ * scale, a power of two: s = floor(log2 max|v|) - 2, at least -127, stored as
+ * the byte s + 127.  An element is v / 2^s rounded to 0, 0.5, 1, 1.5, 2, 3, 4
+ * or 6 with its sign (ties to the even code; beyond 6 to 6), as four bits,
+ * two to a byte, the first in the low half.  A block with a NaN or an
+ * infinity has scale byte 255 and is NaN as a whole.
+ *
+ *   weight     device bf16 (weight_f32 == 0) or fp32 [elements], dense,
+ *              16-byte aligned; elements is a multiple of 32 (rows of a
+ *              multiple of 32 keep blocks within a row).
+ *   codes      device uint8 [elements / 2], 16-byte aligned.
+ *   scales     device uint8 [elements / 32].
+ *   out        device bf16 (out_f32 == 0) or fp32 [elements], 16-byte
+ *              aligned.  Exact in both (6 x 2^127 is an infinity).
+ *
+ * Errors: LORA_ERR_NULL, LORA_ERR_SIZE, LORA_ERR_ALIGN.
+ */
+int lora_quantize_mxfp4(const void *weight, int32_t weight_f32, int64_t elements, uint8_t *codes,
+                        uint8_t *scales, void *stream);
+int lora_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t elements, void *out,
+                          int32_t out_f32, void *stream);
+
+/*
+ * lora_clip_gradients -- the norm of many tensors' gradients, and the
+ * gradients scaled down to a largest norm.  Every tensor is a stack of
+ * `groups` equal slices (one per adapter; groups = 1: one norm over all):
+ *   norms[g] = sqrt(sum over the tensors and the elements of slice g of v^2)
+ *   out = v * min(1, max_norm / (norms[g] + eps))
+ *
+ *   grads        host array of num_tensors device pointers, each to groups *
+ *                slice_sizes[i] dense elements, bf16 or (grads_f32[i]) fp32,
+ *                aligned to an element.
+ *   out          NULL (in place) or as grads; a tensor may be its own out, no
+ *                others may overlap.
+ *   slice_sizes  host int64 [num_tensors], >= 0.
+ *   grads_f32    host int32 [num_tensors].
+ *   max_norm     >= 0; infinite: the norms only (out then receives copies).
+ *   eps          >= 0.
+ *   norms        device fp32 [groups].
+ *   workspace    256-byte aligned, lora_clip_gradients_workspace bytes.
+ *
+ * Sums of squares are fp64 beyond an fp32 sum of a few dozen each, and do not
+ * overflow or underflow for any fp32 values; each gradient is rounded once.
+ * A NaN norm makes its group's gradients NaN, an infinite one makes finite
+ * gradients zero.  Deterministic.  Any number of tensors (1024 a launch).
+ * The host arrays are read during the call only.  Errors: LORA_ERR_NULL,
+ * LORA_ERR_SIZE, LORA_ERR_ALIGN, LORA_ERR_WORKSPACE.
+ */
+int lora_clip_gradients(const void *const *grads, void *const *out, const int64_t *slice_sizes,
+                        const int32_t *grads_f32, int32_t num_tensors, int32_t groups,
+                        float max_norm, float eps, float *norms, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of lora_clip_gradients on the current device;
+ * LORA_ERR_SIZE for groups < 1. */
+int64_t lora_clip_gradients_workspace(int32_t groups);
+
+/*
  * lora_reload_options -- re-reads the library's tuning variables
  * (LORA_PUNICA_*: which of lora_linear's launch paths a batch takes, which
  * batches the tensor-core kernels take, programmatic dependent launch).
