@@ -106,18 +106,30 @@ bool encode_tile_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_stack_map(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
-                      uint32_t box_cols, uint32_t box_rows)
+static bool stack_map(CUtensorMap *m, CUtensorMapDataType type, uint64_t size, const void *ptr, uint64_t count,
+                      uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {cols, rows, count};
-    const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+    const cuuint64_t strides[2] = {cols * size, rows * cols * size};
     const cuuint32_t box[3] = {box_cols, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, type, 3, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_stack_map(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
+                      uint32_t box_cols, uint32_t box_rows)
+{
+    return stack_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, count, rows, cols, box_cols, box_rows);
+}
+
+bool encode_stack_map_u8(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
+                         uint32_t box_cols, uint32_t box_rows)
+{
+    return stack_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, ptr, count, rows, cols, box_cols, box_rows);
 }
 
 bool encode_perm_rows_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint32_t rank,

@@ -191,6 +191,22 @@ struct ExpertLayout {
     int64_t rows;                     // of the copies
 };
 
+// Rows of a tile of the forward product, by how many rows an expert has on
+// average; EX_TILE: the product on CTA pairs, where 4-bit weights are decoded
+// first.  Both sides measured (us; hidden 4096, in a graph): bf16, 16 experts
+// of width 4096, 32 rows: 112.8 with tiles of 32 rows, 114.8 with 64; 64 rows:
+// 133 and 117; 128 rows: 141 with 64, 130 on pairs; one expert of width 11008,
+// 192 rows: 51 and 47.  4 bits: 4 rows (32 experts, 11008): 201 with 16, 252
+// with 64; 32 rows: 98 and 74; 64 rows: 89 with 64, 104 with 128; 256 rows
+// (8 experts, 320): 149 and 143; one expert of width 11008, 1024 rows: 124
+// with 128, 131 decoded; of width 4096, 4096 rows: 165 and 126.
+static int forward_tile(int64_t R, int64_t E, bool quantized)
+{
+    const int64_t mean = R / E;
+    if (!quantized) return mean <= 32 ? 32 : mean <= 96 ? 64 : EX_TILE;
+    return mean <= 12 ? 16 : mean <= 128 ? 64 : mean <= 1024 ? 128 : EX_TILE;
+}
+
 // A batch of R rows; every size grows with R, so that a workspace for a batch
 // holds each smaller one.
 static ExpertLayout expert_layout(int64_t R, int fan, int64_t K, int64_t N, int64_t E, bool x_copy, bool dx, bool dw,
@@ -202,7 +218,7 @@ static ExpertLayout expert_layout(int64_t R, int fan, int64_t K, int64_t N, int6
     int64_t at = 256;
     l.tiles = 0;
     l.table = at;
-    at += up256((R / EX_TILE + active) * int64_t(sizeof(ExpertTile)));
+    at += up256((R / EX_LEAST_TILE + active) * int64_t(sizeof(ExpertTile)));
     l.blocks = at;
     at += dw ? up256(E * 8) : 0;
     l.xs = at;
@@ -281,7 +297,8 @@ LORA_API int64_t lora_expert_linear_workspace(int32_t num_rows, int32_t hidden, 
 {
     using namespace lora;
     if (int e = check_sizes(num_rows, 1, hidden, out_features, max_loras, quantized != 0)) return e;
-    return expert_layout(num_rows, 1, hidden, out_features, max_loras, true, false, false, quantized != 0).bytes;
+    return expert_layout(num_rows, 1, hidden, out_features, max_loras, true, false, false,
+                         quantized != 0 && forward_tile(num_rows, max_loras, true) == EX_TILE).bytes;
 }
 
 LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_rows, int32_t fan_out,
@@ -297,7 +314,9 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     if (y_ld < out_features) return LORA_ERR_SIZE;
     if (bits(workspace) & 255u) return LORA_ERR_ALIGN;
     const bool quantized = weight_scale != nullptr;
-    const ExpertLayout lay = expert_layout(num_rows, 1, hidden, out_features, p.E, true, false, false, quantized);
+    p.tile_rows = forward_tile(num_rows, p.E, quantized);
+    const bool decode = quantized && p.tile_rows == EX_TILE;
+    const ExpertLayout lay = expert_layout(num_rows, 1, hidden, out_features, p.E, true, false, false, decode);
     if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
     if (num_rows == 0) return LORA_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -310,7 +329,8 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);
     p.xs = reinterpret_cast<uint16_t *>(ws + lay.xs);
     if (int e = launch_pack(p, lay.rows, st)) return e;
-    if (quantized) {
+    if (p.tile_rows < EX_TILE) return launch_expert_stream(p, lay.rows, st);
+    if (decode) {
         uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
         if (int e = launch_expert_decode(p, w, st)) return e;
         p.w = w;

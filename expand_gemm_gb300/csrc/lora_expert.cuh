@@ -28,6 +28,7 @@ struct ExpertTile {
 static_assert(sizeof(ExpertTile) == 32, "two 16-byte loads");
 
 constexpr int EX_TILE = 256;          // rows of a pair's tile
+constexpr int EX_LEAST_TILE = 16;     // the smallest tile_rows
 constexpr int EX_PAD = 64;            // rows that a segment is padded to for dW (a K block)
 
 struct ExpertArgs {
@@ -61,6 +62,9 @@ int expert_shared_memory(const void *kernel, int bytes, std::atomic<uint64_t> &d
 int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st);
+
+// lora_expert_stream.cu: few rows an expert, weights in either form.
+int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 
 // lora_mxfp4.cu: the weights of the experts that have rows, decoded to bf16.
 int launch_expert_decode(const ExpertArgs &p, uint16_t *out, cudaStream_t st);

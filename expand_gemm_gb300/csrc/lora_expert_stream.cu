@@ -1,0 +1,498 @@
+// lora_expert_stream.cu -- the forward product of a mixture of experts for few
+// rows an expert, where reading the weights bounds it: a tile is 128 rows of
+// W[e] (the UMMA's M) by up to NT rows of x (its N), so that the tensor core
+// does no more than the rows need and every SM streams weights through one
+// ring, across tiles.
+//
+// Weights in bf16 come by TMA as the operand in shared memory.  Weights in 4
+// bits come as codes, 128 rows of 256 elements a stage; sixteen warps decode
+// them, a thread a row, into TMEM, from where the UMMA reads that operand:
+// through shared memory the decoded tile would be written and read once more
+// (8 bytes for each byte of codes).  A byte's two elements are looked up in a
+// table that each lane has in a bank of its own, and multiplied by their
+// scale: 16 instructions for eight elements, of which the masks' pipe takes
+// four.  (With masks and shifts in its place it was 21 and nine.)
+//
+// Warps: 0 loads, 1 issues UMMAs and owns TMEM, 2..5 run the epilogue (thread
+// = TMEM lane = row of W); with 4-bit weights 6..21 decode and 22 fetches
+// scales.  Two accumulators: the epilogue of one tile runs under the next
+// one's products.
+#include "lora_expert.cuh"
+#include "lora_tc.cuh"
+
+namespace lora {
+
+struct StreamArgs {
+    ExpertArgs p;
+    CUtensorMap w, x;
+    uint32_t pitch;               // 128, the bytes of a byte's row of the table: see decode_block
+};
+
+constexpr int ST_ROWS = 128;                    // of W in a tile
+constexpr int ST_TILE = ST_ROWS * 128;          // bytes of W in a stage: 64 bf16 or 256 codes a row
+constexpr int ST_DEC0 = 6;                      // first decoding warp
+constexpr int ST_SETS = 4;                      // of four warps that decode
+constexpr int ST_SCALE_WARP = ST_DEC0 + 4 * ST_SETS;
+constexpr int ST_MAX_BUFS = 3;                  // decoded stages in TMEM
+constexpr int ST_MAX_STAGES = 12;
+
+template <bool FOUR, int NT>
+struct StreamSizes {
+    static constexpr int KC = FOUR ? 256 : 64;                  // elements of K in a stage
+    static constexpr int PANELS = KC / 64;                      // of x: NT rows of 64
+    static constexpr int LOADED = ST_TILE + PANELS * NT * 128;  // bytes of a stage by TMA
+    static constexpr int STAGE = LOADED + (FOUR ? 1024 : 0);    // and the rows' eight scales
+    static constexpr int THREADS = 32 * (FOUR ? ST_SCALE_WARP + 1 : ST_DEC0);
+    static constexpr int BARS = 512;
+    static constexpr int TABLE = FOUR ? 256 * 128 : 0;
+    static constexpr int ROOM = (232448 - 1024 - BARS - TABLE) / STAGE;
+    static constexpr int STAGES = ROOM < ST_MAX_STAGES ? ROOM : ST_MAX_STAGES;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + BARS + TABLE;
+    static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
+    static constexpr int DECODED = 2 * NT;                     // first TMEM column of the decoded stages
+    static constexpr int BUFS = (512 - DECODED) / 128 < ST_MAX_BUFS ? (512 - DECODED) / 128 : ST_MAX_BUFS;
+    static_assert(!FOUR || BUFS >= 2, "TMEM");
+};
+
+struct StreamItem {
+    int row, valid, start, n0, expert;
+};
+
+// Item i: an expert's tiles of rows take 128 rows of its weights one after
+// another, so that they are read from memory once.
+template <int NT>
+__device__ __forceinline__ StreamItem stream_item(const ExpertArgs &p, int i, int cols)
+{
+    const int4 *at = reinterpret_cast<const int4 *>(p.table + i / cols);
+    const int4 a = at[0], b = at[1];          // base, tiles, expert, start; count, row
+    const int j = i - a.x * cols, tile = j % a.y;
+    StreamItem it;
+    it.row = b.y + tile * NT;
+    it.valid = min(NT, b.x - tile * NT);
+    it.start = a.w + tile * NT;
+    it.n0 = j / a.y * ST_ROWS;
+    it.expert = a.z;
+    return it;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// One lane of the warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+// A block of 32 elements with scale byte c.  `table`: shared memory, a byte's
+// pair of bf16 in this lane's bank every `pitch` bytes.  (The compiler does
+// not know the pitch: it would add by shifts, on the pipe that takes the
+// bytes apart.)  Each product with the scale is exact.  ENDS: c may be 0,
+// which is subnormal, or 255, NaN.
+template <bool ENDS>
+__device__ __forceinline__ void decode_block(uint32_t table, uint32_t pitch, const uint4 &w, uint32_t c, uint32_t *o)
+{
+    uint32_t f = c * 0x00800080u;                  // 2^(c - 127) twice
+    if (ENDS && c == 0u) f = 0x00400040u;
+    if (ENDS && c == 255u) f = 0x7FC07FC0u;
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(__byte_perm(words[i], 0, 0x4440 + j) * pitch + table));
+            o[4 * i + j] = mul_bf16x2(v, f);
+        }
+    }
+}
+
+// Two blocks, with the scale bytes in the low half of sc.
+template <bool ENDS>
+__device__ __forceinline__ void decode_two(uint32_t table, uint32_t pitch, const uint4 *w, uint32_t sc, uint32_t (&o)[32])
+{
+    decode_block<ENDS>(table, pitch, w[0], sc & 255u, o);
+    decode_block<ENDS>(table, pitch, w[1], sc >> 8 & 255u, o + 16);
+}
+
+// Whether one of four bytes is 0 or 255.
+__device__ __forceinline__ bool has_end(uint32_t v)
+{
+    return (((v - 0x01010101u) & ~v) | ((~v - 0x01010101u) & v)) & 0x80808080u;
+}
+
+// The 4-bit element as bf16.
+__device__ __forceinline__ uint32_t e2m1_bf16(uint32_t code)
+{
+    return (__float_as_uint(__uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f)) >> 16;
+}
+
+// One row's eight scale bytes of a stage to `dst` (shared memory) and an
+// arrival at `bar` once they are there; bytes that do not exist stand for 1
+// (their codes are zero).
+__device__ __forceinline__ void fetch_scales(const ExpertArgs &p, uint8_t *dst, int expert, int n, int kb)
+{
+    const int per = p.K / 32, at = kb * 8;
+    const uint8_t *src = p.scales + (int64_t(expert) * p.N + n) * per + at;
+    if (n < p.N && at + 8 <= per && per % 4 == 0) {
+        if (per % 8 == 0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" :: "r"(smem_addr(dst)), "l"(src) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n"
+                         "cp.async.ca.shared.global [%0+4], [%1+4], 4;\n" :: "r"(smem_addr(dst)), "l"(src) : "memory");
+        return;
+    }
+    uint32_t lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t c = 127u;
+        if (n < p.N && at + i < per) c = src[i];
+        if (i < 4) lo |= c << (8 * i);
+        else hi |= c << (8 * i - 32);
+    }
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+}
+
+// D += A B over 64 of K, as four UMMAs: A decoded in TMEM, B K-major; one add
+// to each descriptor.  `more` is 0 for a tile's first block.
+__device__ __forceinline__ void umma_k64_tmem_a(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t more)
+{
+    const uint64_t db = umma_desc_sw128(b);
+    const uint32_t b_lo = uint32_t(db), b_hi = uint32_t(db >> 32);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        asm volatile(
+            "{\n.reg .pred p;\n.reg .b64 b;\n"
+            "mov.b64 b, {%2, %3};\n"
+            "setp.ne.b32 p, %5, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n"
+            :: "r"(d_tmem), "r"(a + kk * 8), "r"(b_lo + kk * 2), "r"(b_hi), "r"(idesc),
+               "r"(kk == 0 ? more : 1u) : "memory");
+}
+
+// The same with both operands K-major in shared memory.
+__device__ __forceinline__ void umma_k64_smem(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t more)
+{
+    const uint64_t da = umma_desc_sw128(a), db = umma_desc_sw128(b);
+    const uint32_t a_lo = uint32_t(da), b_lo = uint32_t(db), hi = uint32_t(da >> 32);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+        asm volatile(
+            "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+            "mov.b64 a, {%1, %3};\n"
+            "mov.b64 b, {%2, %3};\n"
+            "setp.ne.b32 p, %5, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n"
+            :: "r"(d_tmem), "r"(a_lo + kk * 2), "r"(b_lo + kk * 2), "r"(hi), "r"(idesc),
+               "r"(kk == 0 ? more : 1u) : "memory");
+}
+
+template <bool FOUR, int NT>
+__global__ void __launch_bounds__(StreamSizes<FOUR, NT>::THREADS, 1)
+expert_stream_kernel(const __grid_constant__ StreamArgs g)
+{
+    using Z = StreamSizes<FOUR, NT>;
+    extern __shared__ uint8_t st_smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = smem_addr(smem);
+    uint32_t *table = reinterpret_cast<uint32_t *>(smem + Z::STAGES * Z::STAGE);
+    const uint32_t bars = base + Z::STAGES * Z::STAGE + Z::TABLE;
+    const uint32_t full = bars, empty = full + 8 * ST_MAX_STAGES;
+    const uint32_t accf = empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
+    const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
+    volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    // the warp as a value that the compiler knows to be the same in its lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < Z::STAGES; ++i) {
+            mbar_init(full + 8 * i, FOUR ? 33 : 1);                  // the scales' 32 lanes
+            mbar_init(empty + 8 * i, FOUR ? 9 : 1);                  // the UMMAs, eight decoding warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(accf + 8 * i, 1);
+            mbar_init(acce + 8 * i, 4);
+        }
+        for (int i = 0; FOUR && i < ST_MAX_BUFS; ++i) {
+            mbar_init(decf + 8 * i, 8);
+            mbar_init(dece + 8 * i, 1);
+        }
+        mbar_init(drain, 1);
+        mbar_fence_init();
+        *abort = 0;
+        tma_prefetch_map(&g.w);
+        tma_prefetch_map(&g.x);
+    }
+    if constexpr (FOUR) {
+        for (int i = tid; i < 256 * 32; i += Z::THREADS) {
+            const uint32_t byte = uint32_t(i) / 32;
+            table[i] = e2m1_bf16(byte & 15u) | e2m1_bf16(byte >> 4) << 16;
+        }
+    }
+    if (warp == 1) tmem_alloc(smem_addr(s_tmem), Z::COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
+    pdl_wait();
+
+    const ExpertArgs &p = g.p;
+    const int cols = (p.N + ST_ROWS - 1) / ST_ROWS, nk = (p.K + Z::KC - 1) / Z::KC;
+    const int total = *p.tiles * cols;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES);
+    };
+    // for warps that may be late: between polls they leave the issue slots to
+    // the decoding warps
+    auto lazy_wait = [&](uint32_t bar, uint32_t parity, uint32_t ns) {
+        return mbar_try_wait(bar, parity) ||
+               mbar_wait_backoff(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES, ns);
+    };
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- loads
+        if (lane == 0) {
+            asm volatile("fence.proxy.async.global;\n" ::: "memory");      // x was written by an ordinary kernel
+            TcPos pos;
+            int issued = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+                const StreamItem it = stream_item<NT>(p, i, cols);
+                for (int kb = 0; kb < nk; ++kb) {
+                    if (!lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t at = base + pos.stage * Z::STAGE, bar = full + 8 * pos.stage;
+                    mbar_arrive_expect_tx(bar, Z::LOADED);
+                    tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
+#pragma unroll
+                    for (int j = 0; j < Z::PANELS; ++j)
+                        tma_load_2d(at + ST_TILE + j * NT * 128, &g.x, kb * Z::KC + j * 64, it.row, bar);
+                    pos.next(Z::STAGES);
+                    ++issued;
+                }
+            }
+            // no copy may be on its way to this CTA when it exits
+            const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+            for (int i = max(0, issued - Z::STAGES); i < issued; ++i) {
+                const uint32_t ph = uint32_t(i / Z::STAGES) & 1u, b8 = 8u * uint32_t(i % Z::STAGES);
+                while (!mbar_try_wait(full + b8, ph) && clock64() < dd) {
+                }
+                while (!mbar_try_wait(empty + b8, ph) && !*abort && clock64() < dd) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- UMMAs
+        // The whole warp walks the items and one lane issues, so that what
+        // the products are addressed by is in uniform registers: from a
+        // branch of one lane a product takes 75 clocks to issue.
+        TcPos pos, dec;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        const bool leader = elect_one();
+        for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            const StreamItem it = stream_item<NT>(p, i, cols);
+            const uint32_t idesc = __shfl_sync(0xffffffffu, umma_idesc_bf16(ST_ROWS, (it.valid + 15) & ~15), 0);
+            if (!wait(acce + 8 * acc, acc_phase ^ 1u)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + uint32_t(acc * NT);
+            for (int kb = 0; ok && kb < nk; ++kb) {
+                if (!wait(full + 8 * pos.stage, pos.phase)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = base + pos.stage * Z::STAGE;
+                if constexpr (FOUR) {
+                    if (!wait(decf + 8 * dec.stage, dec.phase)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t a = tmem + uint32_t(Z::DECODED + dec.stage * 128);
+#pragma unroll
+                        for (int j = 0; j < Z::PANELS; ++j)
+                            if (kb * Z::KC + j * 64 < p.K)
+                                umma_k64_tmem_a(d, a + j * 32, at + ST_TILE + j * NT * 128, idesc,
+                                                         kb != 0 || j != 0);
+                        umma_commit(dece + 8 * dec.stage);
+                    }
+                    dec.next(Z::BUFS);
+                } else if (leader) {
+                    umma_k64_smem(d, at, at + ST_TILE, idesc, kb != 0);
+                }
+                if (leader) umma_commit(empty + 8 * pos.stage);
+                __syncwarp();
+                pos.next(Z::STAGES);
+            }
+            if (!ok) break;
+            if (leader) umma_commit(accf + 8 * acc);
+            __syncwarp();
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (leader && *abort) {                   // nothing in flight when TMEM is released
+            umma_commit(drain);
+            const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+            while (!mbar_try_wait(drain, 0) && clock64() < dd) {
+            }
+        }
+        __syncwarp();
+    } else if (warp < ST_DEC0) {
+        // ------------------------------------------------------- epilogue
+        const int q = warp & 3;                   // TMEM lane quarter of this warp
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int i = blockIdx.x; i < total; i += gridDim.x) {
+            const StreamItem it = stream_item<NT>(p, i, cols);
+            if (!__all_sync(0xffffffffu, lazy_wait(accf + 8 * acc, acc_phase, 200))) break;
+            tc_fence_after();
+            const int n = it.n0 + q * 32 + lane;
+            const uint32_t t = tmem + uint32_t(acc * NT) + (uint32_t(q * 32) << 16);
+            for (int c = 0; c < it.valid; c += 16) {
+                uint32_t v[16];
+                tmem_ld16_nowait(t + c, v);
+                int row = -1;
+                if (lane < 16 && c + lane < it.valid)
+                    row = checked_token(p.sorted[it.start + c + lane], p.R, p.error_word);
+                tmem_wait_ld();
+                float old[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int r = __shfl_sync(0xffffffffu, row, j);
+                    old[j] = p.add && r >= 0 && n < p.N ? bf16_to_f32(p.y[int64_t(r) * p.y_ld + n]) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int r = __shfl_sync(0xffffffffu, row, j);
+                    float s = __uint_as_float(v[j]);
+                    if (p.add) s += old[j];
+                    if (r >= 0 && n < p.N)
+                        p.y[int64_t(r) * p.y_ld + n] = uint16_t(pack_bf16x2(s, 0.0f) & 0xFFFFu);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce + 8 * acc);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    } else if constexpr (FOUR) {
+        if (warp == ST_SCALE_WARP) {
+            // ---------------------------------------------------- scales
+            TcPos pos;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+                const StreamItem it = stream_item<NT>(p, i, cols);
+                for (int kb = 0; kb < nk; ++kb) {
+                    ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
+                    if (!ok) break;
+                    uint8_t *to = smem + pos.stage * Z::STAGE + Z::LOADED;
+#pragma unroll
+                    for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 8, it.expert, it.n0 + r, kb);
+                    // stores before the arrival, which follows when the copies have landed
+                    __threadfence_block();
+                    cp_async_mbar_arrive_noinc(full + 8 * pos.stage);
+                    pos.next(Z::STAGES);
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+        } else {
+            // -------------------------------------------------- decoding
+            // Two sets of four warps share a stage, the other two the next
+            // one; a set has two of its four blocks of 64.
+            const int set = (warp - ST_DEC0) >> 2, q = warp & 3, row = q * 32 + lane;
+            const int half = set & 1;
+            const uint32_t mine = smem_addr(table) + lane * 4;
+            int turn = set >> 1;                  // stages until this warp's next one
+            TcPos pos, dec;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+                for (int kb = 0; kb < nk; ++kb, pos.next(Z::STAGES), dec.next(Z::BUFS)) {
+                    turn ^= 1;
+                    if (turn == 0) continue;
+                    ok = __all_sync(0xffffffffu, lazy_wait(full + 8 * pos.stage, pos.phase, 20));
+                    if (!ok) break;
+                    const uint8_t *at = smem + pos.stage * Z::STAGE;
+                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(at + Z::LOADED + row * 8 + half * 4);
+                    uint4 w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        w[c] = *reinterpret_cast<const uint4 *>(at + row * 128 + (((4 * half + c) ^ row) & 7) * 16);
+                    const bool ends = __any_sync(0xffffffffu, has_end(sc));
+                    const uint32_t to = tmem + uint32_t(Z::DECODED + dec.stage * 128 + half * 64) + (uint32_t(q * 32) << 16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t o[32];
+                        if (ends) decode_two<true>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
+                        else decode_two<false>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
+                        if (j == 0) {
+                            // what this stage held is in registers
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(empty + 8 * pos.stage);
+                            ok = __all_sync(0xffffffffu, lazy_wait(dece + 8 * dec.stage, dec.phase ^ 1u, 20));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        tmem_st<32>(to + j * 32, o);
+                    }
+                    if (!ok) break;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(decf + 8 * dec.stage);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && *abort && p.error_word != nullptr) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
+    if (warp == 1) tmem_dealloc(tmem, Z::COLS);
+}
+
+// ---------------------------------------------------------------- host
+
+template <bool FOUR, int NT>
+static int run_stream(const StreamArgs &g, cudaStream_t st)
+{
+    using Z = StreamSizes<FOUR, NT>;
+    static std::atomic<uint64_t> done{0};
+    const auto kernel = expert_stream_kernel<FOUR, NT>;
+    if (int e = expert_shared_memory((const void *)kernel, Z::SMEM, done)) return e;
+    return int(launch_kernel(kernel, dim3(unsigned(device_sm_count())), dim3(Z::THREADS), Z::SMEM, st, g));
+}
+
+int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+{
+    StreamArgs g;
+    g.p = p;
+    g.pitch = 128;
+    const bool four = p.scales != nullptr;
+    if (!encode_tile_map(&g.x, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), 64, uint32_t(p.tile_rows),
+                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !(four ? encode_stack_map_u8(&g.w, p.codes, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K / 2), 128, ST_ROWS)
+               : encode_stack_map(&g.w, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), 64, ST_ROWS)))
+        return LORA_ERR_DEVICE;
+    if (four) return p.tile_rows == 16   ? run_stream<true, 16>(g, st)
+                     : p.tile_rows == 64 ? run_stream<true, 64>(g, st)
+                                         : run_stream<true, 128>(g, st);
+    return p.tile_rows == 32 ? run_stream<false, 32>(g, st) : run_stream<false, 64>(g, st);
+}
+
+}  // namespace lora

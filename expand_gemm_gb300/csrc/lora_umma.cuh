@@ -609,6 +609,10 @@ bool encode_tile_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_
 bool encode_stack_map(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
                       uint32_t box_cols, uint32_t box_rows);
 
+// The same over bytes (row and box columns in bytes).
+bool encode_stack_map_u8(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
+                         uint32_t box_cols, uint32_t box_rows);
+
 // Host: encodes the B map of the tensor-core expand over a bf16 matrix of
 // `rows` rows (a multiple of 64) of `rank` elements, whose boxes of
 // `blocks` 64-row blocks land in shared memory with the rows of each block
