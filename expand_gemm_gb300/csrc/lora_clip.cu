@@ -5,13 +5,13 @@
 //   out      = v min(1, max_norm / (norms[g] + eps))
 //
 // Bound by memory: the gradients are read for the norm and once more to be
-// scaled.  Every slice is cut into units of CL_UNIT elements; CTAs take even
-// runs of units, group by group, so that a CTA leaves one partial sum for
+// scaled.  Every slice is cut into units of 2^unit_log elements; CTAs take
+// even runs of units, group by group, so that a CTA leaves one partial sum for
 // each group that it meets, in an order that depends on the sizes alone: equal
 // inputs give equal bits.
 //
-// Squares are summed in fp32 over the elements a thread has of one unit and in
-// fp64 from there on.  Eight values whose squares would overflow fp32 or lose
+// Squares are summed in fp32 over up to 33 elements of a thread and in fp64
+// from there on.  Eight values whose squares would overflow fp32 or lose
 // digits to underflow (magnitudes above 2^60, or all below 2^-50) are squared
 // in fp64.
 #include <math.h>
@@ -21,13 +21,16 @@
 namespace lora {
 
 constexpr int CL_THREADS = 512;
-constexpr int CL_UNIT = 16384;
+constexpr int CL_UNIT_LOG = 14;                // units of 2^14 elements, or of
+constexpr int CL_LONG_LOG = 17;                // 2^17 where there are many
 constexpr int CL_FEW = 64;                     // tensors of a launch: with so many
 constexpr int CL_MANY = 1024;                  // or so many, 28 bytes of arguments each
 
 struct ClipShared {
     int32_t tensors, groups;
+    int32_t unit_log;
     int32_t units;                             // of one slice of all tensors of the launch
+    int64_t run;                               // units of a CTA
     int32_t add;                               // the sums are added to those of earlier tensors
     double *part;                              // [CTAs + groups]: CTA c's sum for group g at c + g
     double *sum;                               // [groups]
@@ -47,22 +50,47 @@ struct ClipArgs {
 constexpr int64_t CL_F32 = int64_t(1) << 62;
 static_assert(sizeof(ClipArgs<CL_MANY>) <= 32764, "kernel arguments");
 
-// CTA c's units: [c total / ctas, (c + 1) total / ctas).
-__host__ __device__ __forceinline__ int64_t clip_first(int64_t total, int c, int ctas)
-{
-    return total / ctas * c + total % ctas * c / ctas;
-}
-
+// A CTA's place among the units: the group, the unit in its slice, and the
+// tensor that the unit belongs to.
 template <int MAX>
-__device__ __forceinline__ int clip_tensor(const ClipArgs<MAX> &a, int unit)
-{
-    int lo = 0, hi = a.s.tensors - 1;            // the first tensor that ends behind the unit
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.end[mid] > unit) hi = mid; else lo = mid + 1;
+struct ClipWalk {
+    int64_t left;                              // units to go, this one among them
+    int group, unit, tensor;
+
+    __device__ __forceinline__ ClipWalk(const ClipArgs<MAX> &a, bool back)
+    {
+        const int64_t total = int64_t(a.s.units) * a.s.groups, first = blockIdx.x * a.s.run;
+        const int64_t last = min(total, first + a.s.run) - 1, at = back ? last : first;
+        left = last - first + 1;
+        group = int(at / a.s.units);
+        unit = int(at - int64_t(group) * a.s.units);
+        int lo = 0, hi = a.s.tensors - 1;      // the first tensor that ends behind the unit
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.end[mid] > unit) hi = mid; else lo = mid + 1;
+        }
+        tensor = lo;
     }
-    return lo;
-}
+    __device__ __forceinline__ void next(const ClipArgs<MAX> &a)
+    {
+        --left;
+        if (++unit == a.s.units) {
+            unit = tensor = 0;
+            ++group;
+        }
+        while (tensor < a.s.tensors - 1 && a.end[tensor] <= unit) ++tensor;
+    }
+    __device__ __forceinline__ void back(const ClipArgs<MAX> &a)
+    {
+        --left;
+        if (--unit < 0) {
+            unit = a.s.units - 1;
+            tensor = a.s.tensors - 1;
+            --group;
+        }
+        while (tensor > 0 && a.end[tensor - 1] > unit) --tensor;
+    }
+};
 
 __device__ __forceinline__ void clip_unpack(const uint4 &w, bool f32, float (&v)[8])
 {
@@ -111,17 +139,17 @@ struct ClipUnit {
     bool f32;
 };
 template <int MAX>
-__device__ __forceinline__ ClipUnit clip_unit(const ClipArgs<MAX> &a, int group, int unit)
+__device__ __forceinline__ ClipUnit clip_unit(const ClipArgs<MAX> &a, const ClipWalk<MAX> &w)
 {
-    const int t = clip_tensor(a, unit);
+    const int t = w.tensor;
     const int64_t n = a.n[t] & ~CL_F32;
     ClipUnit u;
     u.f32 = (a.n[t] & CL_F32) != 0;
-    const int64_t at = int64_t(unit - (t > 0 ? a.end[t - 1] : 0)) * CL_UNIT;
-    const int64_t first = (group * n + at) * (u.f32 ? 4 : 2);
+    const int64_t at = int64_t(w.unit - (t > 0 ? a.end[t - 1] : 0)) << a.s.unit_log;
+    const int64_t first = (w.group * n + at) * (u.f32 ? 4 : 2);
     u.in = static_cast<const char *>(a.in[t]) + first;
     u.out = static_cast<char *>(a.out[t]) + first;
-    u.count = int(n - at < CL_UNIT ? n - at : CL_UNIT);
+    u.count = int(min(n - at, int64_t(1) << a.s.unit_log));
     return u;
 }
 
@@ -135,12 +163,9 @@ __global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_const
 {
     __shared__ double s_warps[CL_THREADS / 32];
     pdl_wait();
-    const int64_t total = int64_t(a.s.units) * a.s.groups;
-    const int64_t u0 = clip_first(total, blockIdx.x, gridDim.x), u1 = clip_first(total, blockIdx.x + 1, gridDim.x);
     double far = 0.0;
-    for (int64_t u = u0; u < u1; ++u) {
-        const int group = int(u / a.s.units);
-        const ClipUnit c = clip_unit(a, group, int(u % a.s.units));
+    for (ClipWalk<MAX> w(a, false); w.left > 0;) {
+        const ClipUnit c = clip_unit(a, w);
         const int per = c.f32 ? 4 : 8;
         float acc = 0.0f;
         // elements before the first 16-byte boundary and behind the last
@@ -164,6 +189,8 @@ __global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_const
                 clip_unpack(w[k], c.f32, v);
                 clip_add(v, acc, far);
             }
+            far += double(acc);                // of up to 33 squares
+            acc = 0.0f;
         }
         for (; i < whole; i += CL_THREADS) {
             float v[8];
@@ -171,7 +198,9 @@ __global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_const
             clip_add(v, acc, far);
         }
         far += double(acc);
-        if (u + 1 == u1 || (u + 1) / a.s.units != group) {
+        const int group = w.group;
+        w.next(a);
+        if (w.left == 0 || w.group != group) {
             const double s = block_sum(far, s_warps);
             if (threadIdx.x == 0) a.s.part[blockIdx.x + group] = s;
             far = 0.0;
@@ -179,25 +208,17 @@ __global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_const
     }
 }
 
-struct JoinArgs {
-    ClipShared s;
-    int32_t ctas;                              // of the sum
-};
-
 // The partial sums of a group, in order; its norm and factor.  One warp a
 // group.
-__global__ void __launch_bounds__(256) clip_join_kernel(const JoinArgs j)
+__global__ void __launch_bounds__(256) clip_join_kernel(const ClipShared a)
 {
     pdl_wait();
-    const ClipShared &a = j.s;
-    const int ctas = j.ctas;
     const int lane = threadIdx.x & 31;
-    const int64_t total = int64_t(a.units) * a.groups;
     for (int g = blockIdx.x * 8 + (threadIdx.x >> 5); g < a.groups; g += gridDim.x * 8) {
         const int64_t first = int64_t(g) * a.units, last = first + a.units;
+        const int from = int(first / a.run), to = int((last - 1) / a.run);
         double s = 0.0;
-        for (int c = lane; c < ctas; c += 32)
-            if (clip_first(total, c + 1, ctas) > first && clip_first(total, c, ctas) < last) s += a.part[c + g];
+        for (int c = from + lane; c <= to; c += 32) s += a.part[c + g];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (lane == 0) {
@@ -219,12 +240,9 @@ template <int MAX>
 __global__ void __launch_bounds__(CL_THREADS) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
     pdl_wait();
-    const int64_t total = int64_t(a.s.units) * a.s.groups;
-    const int64_t u0 = clip_first(total, blockIdx.x, gridDim.x), u1 = clip_first(total, blockIdx.x + 1, gridDim.x);
-    for (int64_t u = u1 - 1; u >= u0; --u) {
-        const int group = int(u / a.s.units);
-        const ClipUnit c = clip_unit(a, group, int(u % a.s.units));
-        const float f = a.s.scale ? a.s.factor[group] : 1.0f;
+    for (ClipWalk<MAX> w(a, true); w.left > 0; w.back(a)) {
+        const ClipUnit c = clip_unit(a, w);
+        const float f = a.s.scale ? a.s.factor[w.group] : 1.0f;
         if (f == 1.0f && c.in == c.out) continue;
         const int size = c.f32 ? 4 : 2, per = 16 / size;
         const bool same = ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
@@ -280,7 +298,8 @@ static ClipPlan clip_plan(int32_t groups)
     return p;
 }
 
-// Tensors [first, first + many) of the call.
+static int64_t clip_units(int64_t n, int log) { return (n + (int64_t(1) << log) - 1) >> log; }
+
 struct ClipCall {
     const void *const *grads;
     void *const *out;
@@ -290,8 +309,9 @@ struct ClipCall {
     ClipShared s;
 };
 
+// Returns the CTAs, 0 where there is nothing to do.
 template <int MAX>
-static void clip_args(ClipArgs<MAX> &a, const ClipCall &c, int first)
+static int clip_args(ClipArgs<MAX> &a, const ClipCall &c, int first, int most)
 {
     a.s = c.s;
     a.s.tensors = c.tensors - first < MAX ? c.tensors - first : MAX;
@@ -301,10 +321,13 @@ static void clip_args(ClipArgs<MAX> &a, const ClipCall &c, int first)
         a.in[i] = c.grads[first + i];
         a.out[i] = c.out != nullptr ? c.out[first + i] : const_cast<void *>(c.grads[first + i]);
         a.n[i] = n | (c.f32[first + i] ? CL_F32 : 0);
-        units += (n + CL_UNIT - 1) / CL_UNIT;
+        units += clip_units(n, a.s.unit_log);
         a.end[i] = int32_t(units);
     }
     a.s.units = int32_t(units);
+    const int64_t total = units * a.s.groups;
+    a.s.run = (total + most - 1) / most;
+    return total > 0 ? int((total + a.s.run - 1) / a.s.run) : 0;
 }
 
 template <int MAX>
@@ -313,26 +336,21 @@ static int run_clip(const ClipCall &c, int most, cudaStream_t st)
     bool any = false;
     ClipArgs<MAX> a;
     for (int first = 0; first < c.tensors; first += MAX) {
-        clip_args(a, c, first);
-        const int64_t total = int64_t(a.s.units) * a.s.groups;
-        if (total == 0) continue;
+        const int ctas = clip_args(a, c, first, most);
+        if (ctas == 0) continue;
         a.s.add = any;
         any = true;
-        const int ctas = int(total < most ? total : most);
         cudaError_t e = launch_kernel(clip_sum_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
         if (e != cudaSuccess) return int(e);
-        JoinArgs j{a.s, ctas};
         const int joins = (c.s.groups + 7) / 8 < 64 ? (c.s.groups + 7) / 8 : 64;
-        e = launch_kernel(clip_join_kernel, dim3(unsigned(joins)), dim3(256), 0, st, j);
+        e = launch_kernel(clip_join_kernel, dim3(unsigned(joins)), dim3(256), 0, st, a.s);
         if (e != cudaSuccess) return int(e);
     }
     if (!any) return int(cudaMemsetAsync(c.s.norms, 0, size_t(c.s.groups) * sizeof(float), st));
     if (!c.s.scale && c.out == nullptr) return LORA_OK;
     for (int first = 0; first < c.tensors; first += MAX) {
-        clip_args(a, c, first);
-        const int64_t total = int64_t(a.s.units) * a.s.groups;
-        if (total == 0) continue;
-        const int ctas = int(total < most ? total : most);
+        const int ctas = clip_args(a, c, first, most);
+        if (ctas == 0) continue;
         const cudaError_t e = launch_kernel(clip_scale_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
         if (e != cudaSuccess) return int(e);
     }
@@ -358,11 +376,12 @@ LORA_API int lora_clip_gradients(const void *const *grads, void *const *out, con
         (num_tensors > 0 && (grads == nullptr || slice_sizes == nullptr || grads_f32 == nullptr)))
         return LORA_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return LORA_ERR_ALIGN;
-    int64_t units = 0;
+    int64_t elements = 0;
     for (int i = 0; i < num_tensors; ++i) {
         if (slice_sizes[i] < 0) return LORA_ERR_SIZE;
-        units += (slice_sizes[i] + CL_UNIT - 1) / CL_UNIT;
-        if (units > INT32_MAX) return LORA_ERR_SIZE;
+        elements += slice_sizes[i];
+        if (elements > INT64_MAX / 8 / groups || clip_units(elements, CL_UNIT_LOG) + num_tensors > INT32_MAX)
+            return LORA_ERR_SIZE;
         if (slice_sizes[i] == 0) continue;
         if (grads[i] == nullptr || (out != nullptr && out[i] == nullptr)) return LORA_ERR_NULL;
         const uintptr_t at = reinterpret_cast<uintptr_t>(grads[i]) |
@@ -380,6 +399,9 @@ LORA_API int lora_clip_gradients(const void *const *grads, void *const *out, con
     char *ws = static_cast<char *>(workspace);
     c.s = ClipShared{};
     c.s.groups = groups;
+    // long units from eight short ones' work a CTA on: finding the next unit
+    // and the round of sums then cost little beside its loads
+    c.s.unit_log = elements * groups >= (int64_t(plan.ctas) << CL_LONG_LOG) ? CL_LONG_LOG : CL_UNIT_LOG;
     c.s.part = reinterpret_cast<double *>(ws);
     c.s.sum = reinterpret_cast<double *>(ws + plan.sum);
     c.s.factor = reinterpret_cast<float *>(ws + plan.factor);
