@@ -159,7 +159,7 @@ __device__ __forceinline__ float clip_load(const char *p, bool f32, int i)
 }
 
 template <int MAX>
-__global__ void __launch_bounds__(CL_THREADS) clip_sum_kernel(const __grid_constant__ ClipArgs<MAX> a)
+__global__ void __launch_bounds__(CL_THREADS, 3) clip_sum_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
     __shared__ double s_warps[CL_THREADS / 32];
     pdl_wait();
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(256) clip_join_kernel(const ClipShared a)
 // out = v * factor.  Units are taken from the last one back: the end of what
 // the norm read may still lie in L2.
 template <int MAX>
-__global__ void __launch_bounds__(CL_THREADS) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
+__global__ void __launch_bounds__(CL_THREADS, 3) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
     pdl_wait();
     for (ClipWalk<MAX> w(a, true); w.left > 0; w.back(a)) {
@@ -290,7 +290,7 @@ static ClipPlan clip_plan(int32_t groups)
 {
     ClipPlan p;
     p.groups = groups;
-    p.ctas = 4 * device_sm_count();
+    p.ctas = 3 * device_sm_count();            // as many as fit
     const int64_t part = (int64_t(p.ctas) + groups) * 8;
     p.sum = (part + 255) / 256 * 256;
     p.factor = p.sum + (int64_t(groups) * 8 + 255) / 256 * 256;
