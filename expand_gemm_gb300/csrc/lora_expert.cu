@@ -323,7 +323,6 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     char *ws = static_cast<char *>(workspace);
     p.y = y;
     p.y_ld = y_ld;
-    p.y_vec = (bits(y) & 15u) == 0 && y_ld % 8 == 0 && out_features % 8 == 0;
     p.add = add_inputs != 0;
     p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
     p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);

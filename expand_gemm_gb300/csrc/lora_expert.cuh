@@ -49,7 +49,7 @@ struct ExpertArgs {
     int2 *blocks;                     // [E]: first K block and K blocks of dW
     int32_t R, fan, K, N, E, nbins;
     int32_t add, pad, tile_rows;
-    int32_t x_vec, dy_vec, y_vec, dx_vec;
+    int32_t x_vec, dy_vec, dx_vec;
     const int32_t *ids, *sorted, *counts, *start_loc, *active, *no_lora;
     int32_t *error_word;
 };

@@ -1,10 +1,12 @@
 // lora_expert_gemm.cu -- the three products of a mixture of experts on CTA
 // pairs (lora_pair_gemm.cuh), over rows copied into the order of experts:
-//   y  = x W[e]^T      A: rows of x, B: rows of W (both K-major)
-//   dx = dy W[e]       A: rows of dy, B: W with its rows as the K dimension
-//   dW[e] = dy^T x     both with the rows as the K dimension; a segment is
-//                      padded with zeros to whole K blocks
-// W is mapped with a dimension of its own for the expert: what lies behind an
+//   y^T  = W[e] x^T     A: rows of W, B: rows of x (both K-major)
+//   dx^T = W[e]^T dy^T  A: W with its rows as the K dimension, B: rows of dy
+//   dW[e] = dy^T x      both with the rows as the K dimension; a segment is
+//                       padded with zeros to whole K blocks
+// The first two have the tokens as the UMMA's N, so that the last tile of an
+// expert costs what its rows need (in steps of 32) and not 256 of them.  W is
+// mapped with a dimension of its own for the expert: what lies behind an
 // expert's last row or column arrives as zeros, never as its neighbour's
 // values.
 #include "lora_expert.cuh"
@@ -18,7 +20,7 @@ struct ExpertGemm {
 };
 
 constexpr int EX_STAGE = 32 * 128;                               // a warp's rows on their way out
-constexpr int EX_SMEM = PG_SMEM + 8 * EX_STAGE;
+constexpr int EX_SMEM = PG_SMEM + 8 * EX_STAGE;                   // of dW
 static_assert(EX_SMEM <= 232448, "shared memory of a CTA");
 constexpr int EX_GROUP = 16;                                     // token tiles that share a sweep over the columns
 
@@ -44,78 +46,20 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs &p, int i, in
     return it;
 }
 
-// 32 columns of a warp's 32 rows, element by element: rows that begin off a
-// 16-byte boundary.
-__device__ __forceinline__ void put_rows_unaligned(uint8_t *stage, const uint32_t (&v)[32], uint16_t *dst, int many,
-                                                   bool add)
+// Sixteen tokens' values of this thread's column, rounded once (added to what
+// is there in fp32 first): a warp writes 64 bytes of a token's row at a time.
+__device__ __forceinline__ void put_tokens(const uint32_t (&v)[16], const int (&row)[16], uint16_t *y, int64_t ld,
+                                           int col, bool in, bool add)
 {
-    const int lane = threadIdx.x & 31;
-    float *at = reinterpret_cast<float *>(stage);
-    __syncwarp();
+    float old[16];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) at[lane * 32 + ((j + lane) & 31)] = __uint_as_float(v[j]);
-    __syncwarp();
-    for (int r = 0; r < 32; ++r) {
-        uint16_t *to = reinterpret_cast<uint16_t *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
-        if (to == nullptr || lane >= many) continue;
-        float s = at[r * 32 + ((lane + r) & 31)];
-        if (add) s += bf16_to_f32(to[lane]);
-        to[lane] = uint16_t(pack_bf16x2(s, 0.0f) & 0xFFFFu);
-    }
-}
-
-// 32 fp32 columns of a warp's 32 rows, 128 bytes of a row at a time.
-__device__ __forceinline__ void put_rows_f32(uint8_t *stage, const uint32_t (&v)[32], float *dst, int many)
-{
-    const int lane = threadIdx.x & 31, c = lane & 7;
-    __syncwarp();
+    for (int j = 0; j < 16; ++j)
+        old[j] = add && in && row[j] >= 0 ? bf16_to_f32(y[int64_t(row[j]) * ld + col]) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ lane) & 7) * 16) =
-            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int row = 4 * i + (lane >> 3);
-        float *to = reinterpret_cast<float *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
-        if (to != nullptr && 4 * c < many)
-            *reinterpret_cast<uint4 *>(to + 4 * c) =
-                *reinterpret_cast<const uint4 *>(stage + row * 128 + ((c ^ row) & 7) * 16);
-    }
-}
-
-// The columns [c0, lim) of a warp's 32 rows from TMEM to dst (null: nowhere),
-// rounded once, or added to what is there in fp32 first.
-__device__ __forceinline__ void put_tile(uint8_t *stage, uint32_t tmem, bool empty, uint16_t *dst, int c0, int lim,
-                                         bool vec, bool add)
-{
-    if (vec && !add) {
-        for (int c = c0; c < lim; c += 64) {
-            uint32_t o[32];
-            if (empty) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = 0u;
-            } else {
-                load64(tmem + c, 1.0f, o);
-            }
-            store_rows(stage, o, dst == nullptr ? nullptr : dst + c, lim - c);
-        }
-        return;
-    }
-    for (int c = c0; c < lim; c += 32) {
-        uint32_t v[32];
-        if (empty) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-        } else {
-            tmem_ld32_nowait(tmem + c, v);
-            tmem_wait_ld();
-        }
-        uint16_t *to = dst == nullptr ? nullptr : dst + c;
-        if (vec) add_rows(stage, v, 1.0f, to, lim - c);
-        else put_rows_unaligned(stage, v, to, min(32, lim - c), add);
+    for (int j = 0; j < 16; ++j) {
+        float s = __uint_as_float(v[j]);
+        if (add) s += old[j];
+        if (in && row[j] >= 0) y[int64_t(row[j]) * ld + col] = uint16_t(pack_bf16x2(s, 0.0f) & 0xFFFFu);
     }
 }
 
@@ -127,58 +71,55 @@ __device__ __forceinline__ uint8_t *warp_stage()
     return smem + PG_STAGES * PG_STAGE_BYTES + 256 + (int(threadIdx.x >> 5) - PG_EPI_WARP0) * EX_STAGE;
 }
 
-__global__ void __launch_bounds__(PG_THREADS, 1) expert_forward_kernel(const __grid_constant__ ExpertGemm g)
+// y or dx: `width` columns of the result, `depth` of the sum.
+template <bool DX>
+__device__ __forceinline__ void expert_product(const ExpertGemm &g)
 {
-    pdl_wait();
     const ExpertArgs &p = g.p;
-    const int cols = (p.N + EX_TILE - 1) / EX_TILE, kb = (p.K + PG_BK - 1) / PG_BK;
+    const int width = DX ? p.K : p.N, depth = DX ? p.N : p.K;
+    const int cols = (width + EX_TILE - 1) / EX_TILE, kb = (depth + PG_BK - 1) / PG_BK;
     const int total = *p.tiles * cols;
     auto item = [&](int i) {
         const ExpertItem it = expert_item(p, i, cols);
-        return PairItem{it.row, it.col, 0, kb, it.expert};
+        return PairItem{it.col, it.row, 0, kb, it.expert, (min(it.valid, EX_TILE) + 31) & ~31};
     };
-    auto epilogue = [&](int i, const PairItem &, uint32_t tmem, int r, int c0, int rank, bool empty) {
+    auto epilogue = [&](int i, const PairItem &, uint32_t tmem, int r, int c0, int rank, bool) {
         const ExpertItem it = expert_item(p, i, cols);
-        const int local = rank * PG_HALF + r;
-        uint16_t *dst = nullptr;
-        if (local < it.valid) {
-            const int row = checked_token(p.sorted[it.start + local], p.R, p.error_word);
-            if (row >= 0) dst = p.y + int64_t(row) * p.y_ld + it.col;
+        const int col = it.col + rank * PG_HALF + r, lane = threadIdx.x & 31;
+        const bool in = col < width;
+        for (int c = c0; c < min(c0 + PG_HALF, it.valid); c += 16) {
+            uint32_t v[16];
+            tmem_ld16_nowait(tmem + c, v);
+            int mine = -1, row[16];
+            if (lane < 16 && c + lane < it.valid)
+                mine = checked_token(p.sorted[it.start + c + lane], p.R, p.error_word);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) row[j] = __shfl_sync(0xffffffffu, mine, j);
+            tmem_wait_ld();
+            if (!DX) {
+                put_tokens(v, row, p.y, p.y_ld, col, in, p.add);
+            } else if (p.part == nullptr) {
+                put_tokens(v, row, p.dx, p.dx_ld, col, in, p.add);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (in && row[j] >= 0) p.part[int64_t(row[j]) * p.K + col] = __uint_as_float(v[j]);
+            }
         }
-        put_tile(warp_stage(), tmem, empty, dst, c0, min(c0 + PG_HALF, p.N - it.col), p.y_vec, p.add);
     };
-    pair_gemm<false, false, true>(&g.a, &g.b, total, p.error_word, item, epilogue);
+    pair_gemm<DX, false, true>(&g.a, &g.b, total, p.error_word, item, epilogue);
+}
+
+__global__ void __launch_bounds__(PG_THREADS, 1) expert_forward_kernel(const __grid_constant__ ExpertGemm g)
+{
+    pdl_wait();
+    expert_product<false>(g);
 }
 
 __global__ void __launch_bounds__(PG_THREADS, 1) expert_dx_kernel(const __grid_constant__ ExpertGemm g)
 {
     pdl_wait();
-    const ExpertArgs &p = g.p;
-    const int cols = (p.K + EX_TILE - 1) / EX_TILE, kb = (p.N + PG_BK - 1) / PG_BK;
-    const int total = *p.tiles * cols;
-    auto item = [&](int i) {
-        const ExpertItem it = expert_item(p, i, cols);
-        return PairItem{it.row, it.col, 0, kb, it.expert};
-    };
-    auto epilogue = [&](int i, const PairItem &, uint32_t tmem, int r, int c0, int rank, bool empty) {
-        const ExpertItem it = expert_item(p, i, cols);
-        const int local = rank * PG_HALF + r, lim = min(c0 + PG_HALF, p.K - it.col);
-        int row = -1;
-        if (local < it.valid) row = checked_token(p.sorted[it.start + local], p.R, p.error_word);
-        if (p.part != nullptr) {
-            float *dst = row >= 0 ? p.part + int64_t(row) * p.K + it.col : nullptr;
-            for (int c = c0; c < lim; c += 32) {
-                uint32_t v[32];
-                tmem_ld32_nowait(tmem + c, v);
-                tmem_wait_ld();
-                put_rows_f32(warp_stage(), v, dst == nullptr ? nullptr : dst + c, lim - c);
-            }
-            return;
-        }
-        uint16_t *dst = row >= 0 ? p.dx + int64_t(row) * p.dx_ld + it.col : nullptr;
-        put_tile(warp_stage(), tmem, empty, dst, c0, lim, p.dx_vec, p.add);
-    };
-    pair_gemm<false, true, true>(&g.a, &g.b, total, p.error_word, item, epilogue);
+    expert_product<true>(g);
 }
 
 __global__ void __launch_bounds__(PG_THREADS, 1) expert_dw_kernel(const __grid_constant__ ExpertGemm g)
@@ -194,7 +135,17 @@ __global__ void __launch_bounds__(PG_THREADS, 1) expert_dw_kernel(const __grid_c
     auto epilogue = [&](int, const PairItem &it, uint32_t tmem, int r, int c0, int rank, bool empty) {
         const int n = it.row_a + rank * PG_HALF + r;
         uint16_t *dst = n < p.N ? p.dw + (int64_t(it.mat) * p.N + n) * p.K + it.row_b : nullptr;
-        put_tile(warp_stage(), tmem, empty, dst, c0, min(c0 + PG_HALF, p.K - it.row_b), true, false);
+        const int lim = min(c0 + PG_HALF, p.K - it.row_b);
+        for (int c = c0; c < lim; c += 64) {
+            uint32_t o[32];
+            if (empty) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = 0u;
+            } else {
+                load64(tmem + c, 1.0f, o);
+            }
+            store_rows(warp_stage(), o, dst == nullptr ? nullptr : dst + c, lim - c);
+        }
     };
     pair_gemm<true, true>(&g.a, &g.b, p.E * nt * kt, p.error_word, item, epilogue);
 }
@@ -202,35 +153,35 @@ __global__ void __launch_bounds__(PG_THREADS, 1) expert_dw_kernel(const __grid_c
 // ---------------------------------------------------------------- host
 
 template <typename Kern>
-static int run_pairs(Kern kernel, std::atomic<uint64_t> &done, const ExpertGemm &g, cudaStream_t st)
+static int run_pairs(Kern kernel, std::atomic<uint64_t> &done, const ExpertGemm &g, int smem, cudaStream_t st)
 {
-    if (int e = expert_shared_memory((const void *)kernel, EX_SMEM, done)) return e;
+    if (int e = expert_shared_memory((const void *)kernel, smem, done)) return e;
     const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
-    return int(launch_pair_kernel(kernel, pairs, st, g, PG_THREADS, EX_SMEM));
+    return int(launch_pair_kernel(kernel, pairs, st, g, PG_THREADS, smem));
 }
 
 int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st)
 {
     ExpertGemm g;
     g.p = p;
-    if (!encode_tile_map(&g.a, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_HALF,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_stack_map(&g.b, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_HALF))
+    if (!encode_stack_map(&g.a, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_HALF) ||
+        !encode_tile_map(&g.b, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_HALF,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_forward_kernel, done, g, st);
+    return run_pairs(expert_forward_kernel, done, g, PG_SMEM, st);
 }
 
 int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st)
 {
     ExpertGemm g;
     g.p = p;
-    if (!encode_tile_map(&g.a, p.dys, uint64_t(rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_HALF,
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_stack_map(&g.b, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_BK))
+    if (!encode_stack_map(&g.a, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_BK) ||
+        !encode_tile_map(&g.b, p.dys, uint64_t(rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_HALF,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_dx_kernel, done, g, st);
+    return run_pairs(expert_dx_kernel, done, g, PG_SMEM, st);
 }
 
 int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st)
@@ -243,7 +194,7 @@ int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st)
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_dw_kernel, done, g, st);
+    return run_pairs(expert_dw_kernel, done, g, EX_SMEM, st);
 }
 
 }  // namespace lora

@@ -82,14 +82,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// One lane of the warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-    return r != 0;
-}
-
 // A block of 32 elements with scale byte c.  `table`: shared memory, a byte's
 // pair of bf16 in this lane's bank every `pitch` bytes.  (The compiler does
 // not know the pitch: it would add by shifts, on the pipe that takes the

@@ -93,19 +93,21 @@ __device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t panel 
     return d;
 }
 
-// One tile of work: its first row of A and of B, its K blocks, and, where B is
-// a stack of matrices, which of them.
+// One tile of work: its first row of A and of B, its K blocks, and, where A is
+// a stack of matrices, which of them and how many rows of B there are (a
+// multiple of 32, at most PG_TILE).
 struct PairItem {
     int row_a, row_b, kb0, kb1;
-    int mat = 0;
+    int mat = 0, n = PG_TILE;
 };
 
 // Runs `total` items on the grid's pairs.  A_T / B_T: the operand is stored
-// with its rows contiguous.  B_STACK: map_b is a stack's (encode_stack_map).  item(i) -> PairItem (every thread computes the
+// with its rows contiguous.  A_STACK: map_a is a stack's (encode_stack_map), and
+// a tile is 256 rows of A by the item's n of B.  item(i) -> PairItem (every thread computes the
 // same); epilogue(i, item, tmem address of this warp's 32 lanes, row of this
 // thread within the CTA's 128 rows, first of its 128 columns, CTA rank,
 // whether the item has no K blocks).
-template <bool A_T, bool B_T, bool B_STACK = false, typename ItemFn, typename EpiFn>
+template <bool A_T, bool B_T, bool A_STACK = false, typename ItemFn, typename EpiFn>
 __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtensorMap *map_b,
                                           int total, int32_t *error_word, ItemFn item_of,
                                           EpiFn epilogue)
@@ -122,7 +124,8 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
     const uint32_t bar_drain = bar_odd + 16;
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (bar_drain + 8 - base));
     volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // the warp as a value that the compiler knows to be the same in its lanes
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = int(blockIdx.x >> 1), npairs = int(gridDim.x >> 1);
 
@@ -146,7 +149,7 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
@@ -160,7 +163,8 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
             bool ok = true;
             for (int i = pair; ok && i < total; i += npairs) {
                 const PairItem it = item_of(i);
-                const int ra = it.row_a + int(rank) * PG_HALF, rb = it.row_b + int(rank) * PG_HALF;
+                const int ra = it.row_a + int(rank) * PG_HALF;
+                const int rb = it.row_b + int(rank) * (A_STACK ? it.n / 2 : PG_HALF);
                 for (int kb = it.kb0; kb < it.kb1; ++kb) {
                     if (!pg_wait(bar_empty + 8 * stage, phase ^ 1u, s_abort)) {
                         ok = false;
@@ -170,18 +174,18 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
                         mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * PG_STAGE_BYTES);
                     const uint32_t sa = base + stage * PG_STAGE_BYTES, sb = sa + PG_STAGE_BYTES / 2;
                     const uint32_t full = full0 + 8 * stage;
-                    if constexpr (A_T) {
+                    if constexpr (A_STACK && A_T) {
+                        tma_load_3d_pair(sa, map_a, ra, kb * PG_BK, it.mat, full);
+                        tma_load_3d_pair(sa + 8192, map_a, ra + 64, kb * PG_BK, it.mat, full);
+                    } else if constexpr (A_STACK) {
+                        tma_load_3d_pair(sa, map_a, kb * PG_BK, ra, it.mat, full);
+                    } else if constexpr (A_T) {
                         tma_load_2d_pair(sa, map_a, ra, kb * PG_BK, full);
                         tma_load_2d_pair(sa + 8192, map_a, ra + 64, kb * PG_BK, full);
                     } else {
                         tma_load_2d_pair(sa, map_a, kb * PG_BK, ra, full);
                     }
-                    if constexpr (B_STACK && B_T) {
-                        tma_load_3d_pair(sb, map_b, rb, kb * PG_BK, it.mat, full);
-                        tma_load_3d_pair(sb + 8192, map_b, rb + 64, kb * PG_BK, it.mat, full);
-                    } else if constexpr (B_STACK) {
-                        tma_load_3d_pair(sb, map_b, kb * PG_BK, rb, it.mat, full);
-                    } else if constexpr (B_T) {
+                    if constexpr (B_T) {
                         tma_load_2d_pair(sb, map_b, rb, kb * PG_BK, full);
                         tma_load_2d_pair(sb + 8192, map_b, rb + 64, kb * PG_BK, full);
                     } else {
@@ -211,47 +215,55 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- UMMAs
-        if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = umma_idesc_bf16(PG_TILE, PG_TILE) |
-                                       (A_T ? 1u << 15 : 0u) | (B_T ? 1u << 16 : 0u);
+        if (rank == 0) {
+            // The whole warp walks the items and one lane issues, so that
+            // what the products are addressed by is in uniform registers:
+            // from a branch of one lane a product takes 75 clocks to issue,
+            // four of them and the waits nearly as long as they run.
+            constexpr uint32_t turned = (A_T ? 1u << 15 : 0u) | (B_T ? 1u << 16 : 0u);
+            const bool leader = elect_one();
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int i = pair; ok && i < total; i += npairs) {
                 const PairItem it = item_of(i);
                 if (it.kb0 >= it.kb1) continue;
+                const uint32_t idesc =
+                    __shfl_sync(0xffffffffu, umma_idesc_bf16(PG_TILE, A_STACK ? it.n : PG_TILE) | turned, 0);
                 if (!pg_wait(bar_acce + 8 * acc, acc_phase ^ 1u, s_abort) ||
                     !pg_wait(bar_odd + 8 * acc, acc_phase ^ 1u, s_abort))
                     break;
                 tc_fence_after();
-                for (int kb = it.kb0; kb < it.kb1; ++kb) {
+                const int blocks = __shfl_sync(0xffffffffu, it.kb1 - it.kb0, 0);
+                for (int kb = 0; kb < blocks; ++kb) {
                     if (!pg_wait(bar_full + 8 * stage, phase, s_abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = base + stage * PG_STAGE_BYTES, sb = sa + PG_STAGE_BYTES / 2;
+                    if (leader) {
+                        const uint64_t da = A_T ? umma_desc_mn(sa) : umma_desc_sw128(sa);
+                        const uint64_t db = B_T ? umma_desc_mn(sb) : umma_desc_sw128(sb);
 #pragma unroll
-                    for (int kk = 0; kk < PG_BK / 16; ++kk) {
-                        const uint64_t da = A_T ? umma_desc_mn(sa + kk * 2048)
-                                                : umma_desc_sw128(sa + kk * 32);
-                        const uint64_t db = B_T ? umma_desc_mn(sb + kk * 2048)
-                                                : umma_desc_sw128(sb + kk * 32);
-                        umma_bf16_pair(tmem + uint32_t(acc * PG_TILE), da, db, idesc,
-                                       kb != it.kb0 || kk != 0);
+                        for (int kk = 0; kk < PG_BK / 16; ++kk)
+                            umma_bf16_pair(tmem + uint32_t(acc * PG_TILE), da + kk * (A_T ? 128 : 2),
+                                           db + kk * (B_T ? 128 : 2), idesc, kb != 0 || kk != 0);
+                        umma_commit_both(bar_empty + 8 * stage);
                     }
-                    umma_commit_both(bar_empty + 8 * stage);
+                    __syncwarp();
                     if (++stage == PG_STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                umma_commit_both(bar_accf + 8 * acc);
+                if (leader) umma_commit_both(bar_accf + 8 * acc);
+                __syncwarp();
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
-            if (*s_abort) {       // nothing in flight when TMEM is released
+            if (leader && *s_abort) {       // nothing in flight when TMEM is released
                 umma_commit_pair(cluster_map(bar_drain, 0));
                 const long long dd = clock64() + PG_TIMEOUT_CYCLES;
                 while (!mbar_try_wait_cluster(bar_drain, 0) && clock64() < dd) {
