@@ -14,30 +14,6 @@ namespace lora {
 
 constexpr int EX_PACK_THREADS = 256;
 
-// One row of `cols` bf16, by a warp.  Whole 16-byte pieces where both ends
-// allow it.
-__device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int cols, bool vec)
-{
-    const int lane = threadIdx.x & 31;
-    if (vec) {
-        const int n = cols / 8;
-        const uint4 *from = reinterpret_cast<const uint4 *>(src);
-        uint4 *to = reinterpret_cast<uint4 *>(dst);
-        int c = lane;
-        for (; c + 96 < n; c += 128) {
-            const uint4 a = from[c], b = from[c + 32], d = from[c + 64], e = from[c + 96];
-            to[c] = a;
-            to[c + 32] = b;
-            to[c + 64] = d;
-            to[c + 96] = e;
-        }
-        for (; c < n; c += 32) to[c] = from[c];
-        for (int i = n * 8 + lane; i < cols; i += 32) dst[i] = src[i];
-    } else {
-        for (int i = lane; i < cols; i += 32) dst[i] = src[i];
-    }
-}
-
 // Copies x (blockIdx.y == 0) and dy (1) into the order of experts; a warp
 // takes a row.  The first block also writes the table of tiles and, for dW,
 // each expert's K blocks; rows of dx that no expert adds to are cleared here
@@ -52,7 +28,7 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
     const int pad = p.pad ? EX_PAD : 1;
     const int units = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, pad, tab, false, 0,
                                     p.R, p.error_word);
-    const bool dy = blockIdx.y == 1;
+    const bool dy = blockIdx.y == 1 || p.later;      // later: dy alone
     const uint16_t *src = dy ? p.dy : p.x;
     uint16_t *dst = dy ? p.dys : p.xs;
     const int64_t src_ld = dy ? p.dy_ld : p.x_ld, dst_ld = dy ? p.dys_ld : p.K;
@@ -66,12 +42,9 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
             uint16_t *to = dst + q * dst_ld;
             int row = -1;
             if (local < tab.count[k]) row = checked_token(p.sorted[tab.start[k] + local], p.R, p.error_word);
-            if (row >= 0) {
-                copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
-            } else {
-                for (int c = lane; c < int(dst_ld / 8); c += 32)
-                    reinterpret_cast<uint4 *>(to)[c] = make_uint4(0, 0, 0, 0);
-            }
+            if (row >= 0) copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
+            else clear_row(to, dst_ld);
+            if (dy && p.from != nullptr && lane == 0) p.from[q] = row;
         }
     }
     if (blockIdx.y == 0 && p.dx != nullptr && p.fan == 1 && !p.add) {
@@ -90,6 +63,7 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
         }
     }
     if (blockIdx.x != 0 || blockIdx.y != 0) return;
+    if (p.copied != nullptr && threadIdx.x == 0) *p.copied = units;
     if (p.blocks != nullptr) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.blocks[e] = make_int2(0, 0);
         __syncthreads();
@@ -119,53 +93,11 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
     }
 }
 
-// dx[t] (+)= the sum of the token's rows, in fp32 and in their order, rounded
-// once.  Rows without an expert have no part.  A warp takes 32 x 4 columns of
-// a token at a time.
 __global__ void __launch_bounds__(256) expert_join_kernel(const __grid_constant__ ExpertArgs p)
 {
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const bool none = *p.no_lora != 0;
-    const int64_t T = p.R / p.fan, warps = int64_t(gridDim.x) * (blockDim.x / 32);
-    for (int64_t t = int64_t(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; t < T; t += warps) {
-        const int32_t *ids = p.ids + t * p.fan;
-        const float *part = p.part + t * p.fan * p.K;
-        uint16_t *out = p.dx + t * p.dx_ld;
-        for (int c = lane * 4; c < p.K; c += 128) {
-            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            bool any = false;
-            if (!none) {
-                for (int j = 0; j < p.fan; ++j) {
-                    const int id = ids[j];
-                    if (id < 0 || id >= p.E) continue;
-                    const float4 v = *reinterpret_cast<const float4 *>(part + int64_t(j) * p.K + c);
-                    // the first part as it is: 0 + -0 would lose its sign
-                    s = any ? make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w) : v;
-                    any = true;
-                }
-            }
-            if (p.add && !any) continue;
-            if (p.dx_vec) {
-                uint2 *to = reinterpret_cast<uint2 *>(out + c);
-                if (p.add) {
-                    const uint2 was = *to;
-                    s = make_float4(s.x + bf16_lo(was.x), s.y + bf16_hi(was.x), s.z + bf16_lo(was.y),
-                                    s.w + bf16_hi(was.y));
-                }
-                *to = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-            } else {
-                if (p.add)
-                    s = make_float4(s.x + bf16_to_f32(out[c]), s.y + bf16_to_f32(out[c + 1]),
-                                    s.z + bf16_to_f32(out[c + 2]), s.w + bf16_to_f32(out[c + 3]));
-                const uint32_t a = pack_bf16x2(s.x, s.y), b = pack_bf16x2(s.z, s.w);
-                out[c] = uint16_t(a & 0xFFFFu);
-                out[c + 1] = uint16_t(a >> 16);
-                out[c + 2] = uint16_t(b & 0xFFFFu);
-                out[c + 3] = uint16_t(b >> 16);
-            }
-        }
-    }
+    const int64_t per = blockDim.x / 32;
+    join_rows(p, blockIdx.x * per + threadIdx.x / 32, gridDim.x * per);
 }
 
 // ---------------------------------------------------------------- host
@@ -187,7 +119,7 @@ static int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 
 // Offsets in the workspace, in bytes.
 struct ExpertLayout {
-    int64_t tiles, table, blocks, xs, dys, part, w, bytes;
+    int64_t tiles, table, blocks, from, xs, dys, part, w, bytes;
     int64_t rows;                     // of the copies
 };
 
@@ -221,6 +153,8 @@ static ExpertLayout expert_layout(int64_t R, int fan, int64_t K, int64_t N, int6
     at += up256((R / EX_LEAST_TILE + active) * int64_t(sizeof(ExpertTile)));
     l.blocks = at;
     at += dw ? up256(E * 8) : 0;
+    l.from = at;
+    at += dx && dw ? up256(l.rows * 4) : 0;
     l.xs = at;
     at += x_copy ? up256(l.rows * K * 2) : 0;
     l.dys = at;
@@ -285,7 +219,7 @@ static int launch_pack(const ExpertArgs &p, int64_t rows, cudaStream_t st)
 {
     const int64_t want = (rows + EX_PACK_THREADS / 32 - 1) / (EX_PACK_THREADS / 32);
     const int64_t most = 6ll * device_sm_count();
-    const dim3 grid(unsigned(want < most ? (want > 0 ? want : 1) : most), p.dys != nullptr ? 2 : 1);
+    const dim3 grid(unsigned(want < most ? (want > 0 ? want : 1) : most), p.dys != nullptr && !p.later ? 2 : 1);
     return int(launch_kernel(expert_pack_kernel, grid, dim3(EX_PACK_THREADS),
                              seg_tab_bytes(p.nbins) + p.nbins * sizeof(int), st, p));
 }
@@ -387,16 +321,22 @@ LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, i
     p.table = hx ? reinterpret_cast<ExpertTile *>(ws + lay.table) : nullptr;
     p.blocks = hw ? reinterpret_cast<int2 *>(ws + lay.blocks) : nullptr;
     p.part = hx && fan_out > 1 ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
+    // With both gradients, what memory has to do for one product runs beside
+    // the other: x is copied under dx's, and the rows of dx are joined under
+    // dW's.
+    p.later = hx && hw;
+    p.copied = p.later ? p.tiles + 1 : nullptr;
+    p.from = p.later ? reinterpret_cast<int32_t *>(ws + lay.from) : nullptr;
     if (int e = launch_pack(p, lay.rows, st)) return e;
-    if (hw)
-        if (int e = launch_expert_dw(p, lay.rows, st)) return e;
-    if (!hx) return LORA_OK;
-    if (decode) {
-        uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
-        if (int e = launch_expert_decode(p, w, st)) return e;
-        p.w = w;
+    if (hx) {
+        if (decode) {
+            uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
+            if (int e = launch_expert_decode(p, w, st)) return e;
+            p.w = w;
+        }
+        if (int e = launch_expert_dx(p, lay.rows, st)) return e;
     }
-    if (int e = launch_expert_dx(p, lay.rows, st)) return e;
+    if (hw) return launch_expert_dw(p, lay.rows, st);
     if (fan_out == 1) return LORA_OK;
     const int64_t tokens = num_rows / fan_out, want = (tokens + 7) / 8, most = 8ll * device_sm_count();
     return int(launch_kernel(expert_join_kernel, dim3(unsigned(want < most ? want : most)), dim3(256), 0, st, p));

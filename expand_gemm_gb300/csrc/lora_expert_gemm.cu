@@ -22,6 +22,7 @@ struct ExpertGemm {
 constexpr int EX_STAGE = 32 * 128;                               // a warp's rows on their way out
 constexpr int EX_SMEM = PG_SMEM + 8 * EX_STAGE;                   // of dW
 static_assert(EX_SMEM <= 232448, "shared memory of a CTA");
+constexpr int EX_SIDE = 4;                                       // warps that copy or join beside a product
 constexpr int EX_GROUP = 16;                                     // token tiles that share a sweep over the columns
 
 // Item i of an expert's tiles: the tile and the column block.  Up to
@@ -107,7 +108,18 @@ __device__ __forceinline__ void expert_product(const ExpertGemm &g)
             }
         }
     };
-    pair_gemm<DX, false, true>(&g.a, &g.b, total, p.error_word, item, epilogue);
+    // x into the order of experts, for dW's product
+    auto copy_x = [&](int warp) {
+        if (!DX || !p.later) return;
+        const int64_t rows = int64_t(*p.copied) * EX_PAD, warps = int64_t(gridDim.x) * EX_SIDE;
+        for (int64_t q = int64_t(blockIdx.x) * EX_SIDE + warp; q < rows; q += warps) {
+            const int row = p.from[q];
+            uint16_t *to = p.xs + q * p.K;
+            if (row >= 0) copy_row(to, p.x + int64_t(row / p.fan) * p.x_ld, p.K, p.x_vec);
+            else clear_row(to, p.K);
+        }
+    };
+    pair_gemm<DX, false, true>(&g.a, &g.b, total, p.error_word, item, epilogue, copy_x);
 }
 
 __global__ void __launch_bounds__(PG_THREADS, 1) expert_forward_kernel(const __grid_constant__ ExpertGemm g)
@@ -116,13 +128,13 @@ __global__ void __launch_bounds__(PG_THREADS, 1) expert_forward_kernel(const __g
     expert_product<false>(g);
 }
 
-__global__ void __launch_bounds__(PG_THREADS, 1) expert_dx_kernel(const __grid_constant__ ExpertGemm g)
+__global__ void __launch_bounds__(PG_THREADS + EX_SIDE * 32, 1) expert_dx_kernel(const __grid_constant__ ExpertGemm g)
 {
     pdl_wait();
     expert_product<true>(g);
 }
 
-__global__ void __launch_bounds__(PG_THREADS, 1) expert_dw_kernel(const __grid_constant__ ExpertGemm g)
+__global__ void __launch_bounds__(PG_THREADS + EX_SIDE * 32, 1) expert_dw_kernel(const __grid_constant__ ExpertGemm g)
 {
     pdl_wait();
     const ExpertArgs &p = g.p;
@@ -147,17 +159,22 @@ __global__ void __launch_bounds__(PG_THREADS, 1) expert_dw_kernel(const __grid_c
             store_rows(warp_stage(), o, dst == nullptr ? nullptr : dst + c, lim - c);
         }
     };
-    pair_gemm<true, true>(&g.a, &g.b, p.E * nt * kt, p.error_word, item, epilogue);
+    auto join = [&](int warp) {
+        if (p.later && p.part != nullptr)
+            join_rows(p, int64_t(blockIdx.x) * EX_SIDE + warp, int64_t(gridDim.x) * EX_SIDE);
+    };
+    pair_gemm<true, true>(&g.a, &g.b, p.E * nt * kt, p.error_word, item, epilogue, join);
 }
 
 // ---------------------------------------------------------------- host
 
 template <typename Kern>
-static int run_pairs(Kern kernel, std::atomic<uint64_t> &done, const ExpertGemm &g, int smem, cudaStream_t st)
+static int run_pairs(Kern kernel, std::atomic<uint64_t> &done, const ExpertGemm &g, int smem, int threads,
+                     cudaStream_t st)
 {
     if (int e = expert_shared_memory((const void *)kernel, smem, done)) return e;
     const int pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
-    return int(launch_pair_kernel(kernel, pairs, st, g, PG_THREADS, smem));
+    return int(launch_pair_kernel(kernel, pairs, st, g, threads, smem));
 }
 
 int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st)
@@ -169,7 +186,7 @@ int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st)
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_forward_kernel, done, g, PG_SMEM, st);
+    return run_pairs(expert_forward_kernel, done, g, PG_SMEM, PG_THREADS, st);
 }
 
 int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st)
@@ -181,7 +198,7 @@ int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st)
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_dx_kernel, done, g, PG_SMEM, st);
+    return run_pairs(expert_dx_kernel, done, g, PG_SMEM, PG_THREADS + EX_SIDE * 32, st);
 }
 
 int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st)
@@ -194,7 +211,7 @@ int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st)
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
-    return run_pairs(expert_dw_kernel, done, g, EX_SMEM, st);
+    return run_pairs(expert_dw_kernel, done, g, EX_SMEM, PG_THREADS + EX_SIDE * 32, st);
 }
 
 }  // namespace lora

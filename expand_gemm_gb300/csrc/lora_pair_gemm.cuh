@@ -101,16 +101,22 @@ struct PairItem {
     int mat = 0, n = PG_TILE;
 };
 
+// What the warps behind the epilogue's do meanwhile: nothing.
+struct NoSideJob {
+    __device__ __forceinline__ void operator()(int) const {}
+};
+
 // Runs `total` items on the grid's pairs.  A_T / B_T: the operand is stored
 // with its rows contiguous.  A_STACK: map_a is a stack's (encode_stack_map), and
 // a tile is 256 rows of A by the item's n of B.  item(i) -> PairItem (every thread computes the
 // same); epilogue(i, item, tmem address of this warp's 32 lanes, row of this
 // thread within the CTA's 128 rows, first of its 128 columns, CTA rank,
-// whether the item has no K blocks).
-template <bool A_T, bool B_T, bool A_STACK = false, typename ItemFn, typename EpiFn>
+// whether the item has no K blocks).  side(warp): what further warps of the
+// launch do beside the products.
+template <bool A_T, bool B_T, bool A_STACK = false, typename ItemFn, typename EpiFn, typename SideFn = NoSideJob>
 __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtensorMap *map_b,
                                           int total, int32_t *error_word, ItemFn item_of,
-                                          EpiFn epilogue)
+                                          EpiFn epilogue, SideFn side = SideFn())
 {
     extern __shared__ uint8_t pg_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -288,6 +294,8 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
             }
         }
         __syncwarp();
+    } else if (warp >= PG_THREADS / 32) {
+        side(warp - PG_THREADS / 32);
     } else {
         // ------------------------------------------------------- epilogue
         const int q = warp & 3;                   // TMEM lane quarter of this warp
