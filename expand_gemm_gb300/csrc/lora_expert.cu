@@ -14,55 +14,10 @@ namespace lora {
 
 constexpr int EX_PACK_THREADS = 256;
 
-// Copies x (blockIdx.y == 0) and dy (1) into the order of experts; a warp
-// takes a row.  The first block also writes the table of tiles and, for dW,
-// each expert's K blocks; rows of dx that no expert adds to are cleared here
-// (dx overwritten, one row a token).
-__global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __grid_constant__ ExpertArgs p)
+// The table of tiles and, for dW, each expert's K blocks: one block.
+__device__ __forceinline__ void expert_tables(const ExpertArgs &p, const SegTab &tab, int units, int *first_row)
 {
-    extern __shared__ int ex_tab[];
-    pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int warps = EX_PACK_THREADS / 32;
-    const SegTab tab = seg_tab(ex_tab, p.nbins);
     const int pad = p.pad ? EX_PAD : 1;
-    const int units = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, pad, tab, false, 0,
-                                    p.R, p.error_word);
-    const bool dy = blockIdx.y == 1 || p.later;      // later: dy alone
-    const uint16_t *src = dy ? p.dy : p.x;
-    uint16_t *dst = dy ? p.dys : p.xs;
-    const int64_t src_ld = dy ? p.dy_ld : p.x_ld, dst_ld = dy ? p.dys_ld : p.K;
-    const int cols = dy ? p.N : p.K, fan = dy ? 1 : p.fan;
-    const bool vec = dy ? p.dy_vec : p.x_vec;
-    if (dst != nullptr) {
-        const int64_t rows = int64_t(units) * pad;
-        for (int64_t q = int64_t(blockIdx.x) * warps + warp; q < rows; q += int64_t(gridDim.x) * warps) {
-            const int k = find_segment(tab.tile, p.nbins, int(q / pad));
-            const int local = int(q - int64_t(tab.tile[k]) * pad);
-            uint16_t *to = dst + q * dst_ld;
-            int row = -1;
-            if (local < tab.count[k]) row = checked_token(p.sorted[tab.start[k] + local], p.R, p.error_word);
-            if (row >= 0) copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
-            else clear_row(to, dst_ld);
-            if (dy && p.from != nullptr && lane == 0) p.from[q] = row;
-        }
-    }
-    if (blockIdx.y == 0 && p.dx != nullptr && p.fan == 1 && !p.add) {
-        const bool none = *p.no_lora != 0;
-        const int rest = none ? p.R : (tab.id[0] == -1 ? tab.count[0] : 0);
-        for (int64_t i = int64_t(blockIdx.x) * warps + warp; i < rest; i += int64_t(gridDim.x) * warps) {
-            const int row = none ? int(i) : checked_token(p.sorted[i], p.R, p.error_word);
-            if (row < 0) continue;
-            uint16_t *to = p.dx + int64_t(row) * p.dx_ld;
-            if (p.dx_vec) {
-                for (int c = lane; c < p.K / 8; c += 32)
-                    reinterpret_cast<uint4 *>(to)[c] = make_uint4(0, 0, 0, 0);
-            } else {
-                for (int c = lane; c < p.K; c += 32) to[c] = 0;
-            }
-        }
-    }
-    if (blockIdx.x != 0 || blockIdx.y != 0) return;
     if (p.copied != nullptr && threadIdx.x == 0) *p.copied = units;
     if (p.blocks != nullptr) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.blocks[e] = make_int2(0, 0);
@@ -73,7 +28,6 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
     }
     if (p.table == nullptr) return;
     // the segments' rows in the copy, kept while the same memory takes the tiles'
-    int *first_row = ex_tab + 4 * p.nbins + 2;
     for (int k = threadIdx.x; units > 0 && k < p.nbins; k += blockDim.x) first_row[k] = tab.tile[k] * pad;
     __syncthreads();
     const int tiles = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, p.tile_rows, tab, false, 0,
@@ -90,6 +44,61 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
         e.row = first_row[k];
         e.pad0 = e.pad1 = 0;
         p.table[t] = e;
+    }
+}
+
+// The first block writes the tables; the others copy x (blockIdx.y == 0) and
+// dy (1) into the order of experts, a warp a row, and clear the rows of dx
+// that no expert adds to (dx overwritten, one row a token).
+__global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __grid_constant__ ExpertArgs p)
+{
+    extern __shared__ int ex_tab[];
+    pdl_wait();
+    const bool tables = blockIdx.x == 0;
+    if (tables && blockIdx.y != 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t first = int64_t(blockIdx.x - 1) * (EX_PACK_THREADS / 32) + warp;
+    const int64_t step = int64_t(gridDim.x - 1) * (EX_PACK_THREADS / 32);
+    const SegTab tab = seg_tab(ex_tab, p.nbins);
+    const int pad = p.pad ? EX_PAD : 1;
+    const int units = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, pad, tab, false, 0,
+                                    p.R, p.error_word);
+    if (tables) {
+        expert_tables(p, tab, units, ex_tab + 4 * p.nbins + 2);
+        return;
+    }
+    const bool dy = blockIdx.y == 1 || p.later;      // later: dy alone
+    const uint16_t *src = dy ? p.dy : p.x;
+    uint16_t *dst = dy ? p.dys : p.xs;
+    const int64_t src_ld = dy ? p.dy_ld : p.x_ld, dst_ld = dy ? p.dys_ld : p.K;
+    const int cols = dy ? p.N : p.K, fan = dy ? 1 : p.fan;
+    const bool vec = dy ? p.dy_vec : p.x_vec;
+    if (dst != nullptr) {
+        const int64_t rows = int64_t(units) * pad;
+        for (int64_t q = first; q < rows; q += step) {
+            const int k = find_segment(tab.tile, p.nbins, int(q / pad));
+            const int local = int(q - int64_t(tab.tile[k]) * pad);
+            uint16_t *to = dst + q * dst_ld;
+            int row = -1;
+            if (local < tab.count[k]) row = checked_token(p.sorted[tab.start[k] + local], p.R, p.error_word);
+            if (row >= 0) copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
+            else clear_row(to, dst_ld);
+            if (dy && p.from != nullptr && lane == 0) p.from[q] = row;
+        }
+    }
+    if (blockIdx.y == 0 && p.dx != nullptr && p.fan == 1 && !p.add) {
+        const bool none = *p.no_lora != 0;
+        const int rest = none ? p.R : (tab.id[0] == -1 ? tab.count[0] : 0);
+        for (int64_t i = first; i < rest; i += step) {
+            const int row = none ? int(i) : checked_token(p.sorted[i], p.R, p.error_word);
+            if (row < 0) continue;
+            uint16_t *to = p.dx + int64_t(row) * p.dx_ld;
+            if (p.dx_vec) {
+                clear_row(to, p.K);
+            } else {
+                for (int c = lane; c < p.K; c += 32) to[c] = 0;
+            }
+        }
     }
 }
 
@@ -137,6 +146,28 @@ static int forward_tile(int64_t R, int64_t E, bool quantized)
     const int64_t mean = R / E;
     if (!quantized) return mean <= 32 ? 32 : mean <= 96 ? 64 : EX_TILE;
     return mean <= 12 ? 16 : mean <= 128 ? 64 : mean <= 1024 ? 128 : EX_TILE;
+}
+
+// Rows of a tile of the products on CTA pairs: what takes the pairs the least
+// time in whole rounds, if the experts have equal shares (each tile costs
+// about 16 rows more than it has).  4096 rows of one expert, 4096 to 4096: 68
+// us of products with tiles of 224 rows, 77 with 256.
+static int pair_tile(int64_t R, int64_t E, int64_t cols)
+{
+    const int64_t experts = R < E ? R : E, mean = R / experts;
+    const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
+    const int64_t blocks = (cols + EX_TILE - 1) / EX_TILE;
+    int best = EX_TILE;
+    int64_t least = INT64_MAX;
+    for (int t = EX_TILE; t >= 64; t -= 32) {
+        const int64_t tiles = experts * ((mean + t - 1) / t) * blocks;
+        const int64_t cost = (tiles + pairs - 1) / pairs * (t + 16);
+        if (cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return best;
 }
 
 // A batch of R rows; every size grows with R, so that a workspace for a batch
@@ -219,7 +250,7 @@ static int launch_pack(const ExpertArgs &p, int64_t rows, cudaStream_t st)
 {
     const int64_t want = (rows + EX_PACK_THREADS / 32 - 1) / (EX_PACK_THREADS / 32);
     const int64_t most = 6ll * device_sm_count();
-    const dim3 grid(unsigned(want < most ? (want > 0 ? want : 1) : most), p.dys != nullptr && !p.later ? 2 : 1);
+    const dim3 grid(unsigned(1 + (want < most ? (want > 0 ? want : 1) : most)), p.dys != nullptr && !p.later ? 2 : 1);
     return int(launch_kernel(expert_pack_kernel, grid, dim3(EX_PACK_THREADS),
                              seg_tab_bytes(p.nbins) + p.nbins * sizeof(int), st, p));
 }
@@ -253,6 +284,8 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     const ExpertLayout lay = expert_layout(num_rows, 1, hidden, out_features, p.E, true, false, false, decode);
     if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
     if (num_rows == 0) return LORA_OK;
+    const bool pairs = p.tile_rows == EX_TILE;
+    if (pairs) p.tile_rows = pair_tile(num_rows, p.E, out_features);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     p.y = y;
@@ -262,7 +295,7 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);
     p.xs = reinterpret_cast<uint16_t *>(ws + lay.xs);
     if (int e = launch_pack(p, lay.rows, st)) return e;
-    if (p.tile_rows < EX_TILE) return launch_expert_stream(p, lay.rows, st);
+    if (!pairs) return launch_expert_stream(p, lay.rows, st);
     if (decode) {
         uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
         if (int e = launch_expert_decode(p, w, st)) return e;
@@ -318,6 +351,7 @@ LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, i
     p.dw = d_weight;
     p.add = add_inputs != 0;
     p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
+    p.tile_rows = pair_tile(num_rows, p.E, hidden);
     p.table = hx ? reinterpret_cast<ExpertTile *>(ws + lay.table) : nullptr;
     p.blocks = hw ? reinterpret_cast<int2 *>(ws + lay.blocks) : nullptr;
     p.part = hx && fan_out > 1 ? reinterpret_cast<float *>(ws + lay.part) : nullptr;

@@ -77,7 +77,16 @@ __device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int
         for (; c < n; c += 32) to[c] = from[c];
         for (int i = n * 8 + lane; i < cols; i += 32) dst[i] = src[i];
     } else {
-        for (int i = lane; i < cols; i += 32) dst[i] = src[i];
+        // eight loads before their stores: one after another they wait for
+        // each other's way through memory
+        for (int i0 = lane; i0 < cols; i0 += 256) {
+            uint16_t v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i0 + 32 * k < cols ? src[i0 + 32 * k] : uint16_t(0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + 32 * k < cols) dst[i0 + 32 * k] = v[k];
+        }
     }
 }
 

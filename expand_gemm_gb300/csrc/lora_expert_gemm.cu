@@ -39,9 +39,9 @@ __device__ __forceinline__ ExpertItem expert_item(const ExpertArgs &p, int i, in
     const int g = j / (EX_GROUP * cols) * EX_GROUP, many = min(EX_GROUP, a.y - g), k = j - g * cols;
     const int tile = g + k % many;
     ExpertItem it;
-    it.row = b.y + tile * EX_TILE;
-    it.valid = b.x - tile * EX_TILE;
-    it.start = a.w + tile * EX_TILE;
+    it.row = b.y + tile * p.tile_rows;
+    it.valid = min(p.tile_rows, b.x - tile * p.tile_rows);
+    it.start = a.w + tile * p.tile_rows;
     it.col = k / many * EX_TILE;
     it.expert = a.z;
     return it;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void expert_product(const ExpertGemm &g)
     const int total = *p.tiles * cols;
     auto item = [&](int i) {
         const ExpertItem it = expert_item(p, i, cols);
-        return PairItem{it.col, it.row, 0, kb, it.expert, (min(it.valid, EX_TILE) + 31) & ~31};
+        return PairItem{it.col, it.row, 0, kb, it.expert, (it.valid + 31) & ~31};
     };
     auto epilogue = [&](int i, const PairItem &, uint32_t tmem, int r, int c0, int rank, bool) {
         const ExpertItem it = expert_item(p, i, cols);
