@@ -17,6 +17,10 @@
 // = TMEM lane = row of W); with 4-bit weights 6..21 decode and 22 fetches
 // scales.  Two accumulators: the epilogue of one tile runs under the next
 // one's products.
+//
+// Where the tiles are fewer than the SMs, a cluster of CTAs shares a tile, each
+// a run of its K: the others write their sums into the first one's shared
+// memory, which adds them in order.
 #include "lora_expert.cuh"
 #include "lora_tc.cuh"
 
@@ -25,6 +29,7 @@ namespace lora {
 struct StreamArgs {
     ExpertArgs p;
     CUtensorMap w, x;
+    int32_t stages;               // of the ring
     uint32_t pitch;               // 128, the bytes of a byte's row of the table: see decode_block
 };
 
@@ -48,6 +53,9 @@ struct StreamSizes {
     static constexpr int ROOM = (232448 - 1024 - BARS - TABLE) / STAGE;
     static constexpr int STAGES = ROOM < ST_MAX_STAGES ? ROOM : ST_MAX_STAGES;
     static constexpr int SMEM = 1024 + STAGES * STAGE + BARS + TABLE;
+    static constexpr int SUMS = NT * ST_ROWS * 4;               // bytes of one CTA's sums of a tile
+    // stages left beside the others' sums
+    static constexpr int left(int parts) { return (STAGES * STAGE - (parts - 1) * SUMS) / STAGE; }
     static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
     static constexpr int DECODED = 2 * NT;                     // first TMEM column of the decoded stages
     static constexpr int BUFS = (512 - DECODED) / 128 < ST_MAX_BUFS ? (512 - DECODED) / 128 : ST_MAX_BUFS;
@@ -193,13 +201,20 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
-    uint32_t *table = reinterpret_cast<uint32_t *>(smem + Z::STAGES * Z::STAGE);
+    uint32_t *table = reinterpret_cast<uint32_t *>(smem + Z::STAGES * Z::STAGE);      // where the whole ring ends
     const uint32_t bars = base + Z::STAGES * Z::STAGE + Z::TABLE;
     const uint32_t full = bars, empty = full + 8 * ST_MAX_STAGES;
     const uint32_t accf = empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
     const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
+    const uint32_t peers = drain + 16;                              // the others' sums are here
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
     volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    const ExpertArgs &p = g.p;
+    const int cols = (p.N + ST_ROWS - 1) / ST_ROWS, nk = (p.K + Z::KC - 1) / Z::KC;
+    // this CTA's share of a tile's K; parts that would have none are not counted
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = int(cluster_nctarank()), per = (nk + cluster - 1) / cluster, parts = (nk + per - 1) / per;
+    const int kb0 = int(rank) * per, kb1 = min(nk, kb0 + per);
     // the warp as a value that the compiler knows to be the same in its lanes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
@@ -217,6 +232,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             mbar_init(dece + 8 * i, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(peers, parts > 1 ? 4 * (parts - 1) : 1);
         mbar_fence_init();
         *abort = 0;
         tma_prefetch_map(&g.w);
@@ -230,14 +246,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     }
     if (warp == 1) tmem_alloc(smem_addr(s_tmem), Z::COLS);
     tc_fence_before();
-    __syncthreads();
+    if (cluster > 1) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     pdl_wait();
 
-    const ExpertArgs &p = g.p;
-    const int cols = (p.N + ST_ROWS - 1) / ST_ROWS, nk = (p.K + Z::KC - 1) / Z::KC;
-    const int total = *p.tiles * cols;
+    const int total = kb0 < kb1 ? *p.tiles * cols : 0;
+    const int item0 = int(blockIdx.x) / cluster, items = int(gridDim.x) / cluster;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES);
     };
@@ -255,9 +271,9 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             TcPos pos;
             int issued = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            for (int i = item0; ok && i < total; i += items) {
                 const StreamItem it = stream_item<NT>(p, i, cols);
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40)) {
                         ok = false;
                         break;
@@ -268,14 +284,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 #pragma unroll
                     for (int j = 0; j < Z::PANELS; ++j)
                         tma_load_2d(at + ST_TILE + j * NT * 128, &g.x, kb * Z::KC + j * 64, it.row, bar);
-                    pos.next(Z::STAGES);
+                    pos.next(g.stages);
                     ++issued;
                 }
             }
             // no copy may be on its way to this CTA when it exits
             const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-            for (int i = max(0, issued - Z::STAGES); i < issued; ++i) {
-                const uint32_t ph = uint32_t(i / Z::STAGES) & 1u, b8 = 8u * uint32_t(i % Z::STAGES);
+            for (int i = max(0, issued - g.stages); i < issued; ++i) {
+                const uint32_t ph = uint32_t(i / g.stages) & 1u, b8 = 8u * uint32_t(i % g.stages);
                 while (!mbar_try_wait(full + b8, ph) && clock64() < dd) {
                 }
                 while (!mbar_try_wait(empty + b8, ph) && !*abort && clock64() < dd) {
@@ -293,13 +309,13 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         uint32_t acc_phase = 0;
         bool ok = true;
         const bool leader = elect_one();
-        for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+        for (int i = item0; ok && i < total; i += items) {
             const StreamItem it = stream_item<NT>(p, i, cols);
             const uint32_t idesc = __shfl_sync(0xffffffffu, umma_idesc_bf16(ST_ROWS, (it.valid + 15) & ~15), 0);
             if (!wait(acce + 8 * acc, acc_phase ^ 1u)) break;
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
-            for (int kb = 0; ok && kb < nk; ++kb) {
+            for (int kb = kb0; ok && kb < kb1; ++kb) {
                 if (!wait(full + 8 * pos.stage, pos.phase)) {
                     ok = false;
                     break;
@@ -318,16 +334,16 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                         for (int j = 0; j < Z::PANELS; ++j)
                             if (kb * Z::KC + j * 64 < p.K)
                                 umma_k64_tmem_a(d, a + j * 32, at + ST_TILE + j * NT * 128, idesc,
-                                                         kb != 0 || j != 0);
+                                                kb != kb0 || j != 0);
                         umma_commit(dece + 8 * dec.stage);
                     }
                     dec.next(Z::BUFS);
                 } else if (leader) {
-                    umma_k64_smem(d, at, at + ST_TILE, idesc, kb != 0);
+                    umma_k64_smem(d, at, at + ST_TILE, idesc, kb != kb0);
                 }
                 if (leader) umma_commit(empty + 8 * pos.stage);
                 __syncwarp();
-                pos.next(Z::STAGES);
+                pos.next(g.stages);
             }
             if (!ok) break;
             if (leader) umma_commit(accf + 8 * acc);
@@ -347,12 +363,34 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         const int q = warp & 3;                   // TMEM lane quarter of this warp
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        for (int i = item0; i < total; i += items) {
             const StreamItem it = stream_item<NT>(p, i, cols);
             if (!__all_sync(0xffffffffu, lazy_wait(accf + 8 * acc, acc_phase, 200))) break;
             tc_fence_after();
             const int n = it.n0 + q * 32 + lane;
             const uint32_t t = tmem + uint32_t(acc * NT) + (uint32_t(q * 32) << 16);
+            // the others' sums, behind the first CTA's ring: [parts - 1][NT][128]
+            const uint32_t sums = base + g.stages * Z::STAGE + uint32_t(q * 32 + lane) * 4;
+            if (rank != 0) {
+                const uint32_t to = cluster_map(sums, 0) + (rank - 1) * Z::SUMS;
+                for (int c = 0; c < it.valid; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_nowait(t + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        asm volatile("st.shared::cluster.b32 [%0], %1;\n" :: "r"(to + (c + j) * (ST_ROWS * 4)), "r"(v[j])
+                                     : "memory");
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_map(peers, 0));
+                continue;                         // a cluster has one tile at most
+            }
+            if (parts > 1) {
+                if (!__all_sync(0xffffffffu, mbar_try_wait_cluster(peers, 0) ||
+                                             mbar_wait_bounded_cluster(peers, 0, abort, clock64() + PG_TIMEOUT_CYCLES)))
+                    break;
+            }
             for (int c = 0; c < it.valid; c += 16) {
                 uint32_t v[16];
                 tmem_ld16_nowait(t + c, v);
@@ -370,6 +408,12 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 for (int j = 0; j < 16; ++j) {
                     const int r = __shfl_sync(0xffffffffu, row, j);
                     float s = __uint_as_float(v[j]);
+                    for (int k = 1; k < parts; ++k) {
+                        float more;
+                        asm volatile("ld.shared.f32 %0, [%1];\n"
+                                     : "=f"(more) : "r"(sums + (k - 1) * Z::SUMS + (c + j) * (ST_ROWS * 4)));
+                        s += more;
+                    }
                     if (p.add) s += old[j];
                     if (r >= 0 && n < p.N)
                         p.y[int64_t(r) * p.y_ld + n] = uint16_t(pack_bf16x2(s, 0.0f) & 0xFFFFu);
@@ -386,9 +430,9 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             // ---------------------------------------------------- scales
             TcPos pos;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
+            for (int i = item0; ok && i < total; i += items) {
                 const StreamItem it = stream_item<NT>(p, i, cols);
-                for (int kb = 0; kb < nk; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
                     uint8_t *to = smem + pos.stage * Z::STAGE + Z::LOADED;
@@ -397,7 +441,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     // stores before the arrival, which follows when the copies have landed
                     __threadfence_block();
                     cp_async_mbar_arrive_noinc(full + 8 * pos.stage);
-                    pos.next(Z::STAGES);
+                    pos.next(g.stages);
                 }
             }
             cp_async_commit();
@@ -412,8 +456,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             int turn = set >> 1;                  // stages until this warp's next one
             TcPos pos, dec;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < total; i += gridDim.x) {
-                for (int kb = 0; kb < nk; ++kb, pos.next(Z::STAGES), dec.next(Z::BUFS)) {
+            for (int i = item0; ok && i < total; i += items) {
+                for (int kb = kb0; kb < kb1; ++kb, pos.next(g.stages), dec.next(Z::BUFS)) {
                     turn ^= 1;
                     if (turn == 0) continue;
                     ok = __all_sync(0xffffffffu, lazy_wait(full + 8 * pos.stage, pos.phase, 20));
@@ -452,7 +496,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     }
 
     tc_fence_before();
-    __syncthreads();
+    if (cluster > 1) cluster_sync_all();          // nobody writes to a CTA that is gone
+    else __syncthreads();
     tc_fence_after();
     if (tid == 0 && *abort && p.error_word != nullptr) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
     if (warp == 1) tmem_dealloc(tmem, Z::COLS);
@@ -461,13 +506,23 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 // ---------------------------------------------------------------- host
 
 template <bool FOUR, int NT>
-static int run_stream(const StreamArgs &g, cudaStream_t st)
+static int run_stream(StreamArgs &g, cudaStream_t st)
 {
     using Z = StreamSizes<FOUR, NT>;
     static std::atomic<uint64_t> done{0};
     const auto kernel = expert_stream_kernel<FOUR, NT>;
     if (int e = expert_shared_memory((const void *)kernel, Z::SMEM, done)) return e;
-    return int(launch_kernel(kernel, dim3(unsigned(device_sm_count())), dim3(Z::THREADS), Z::SMEM, st, g));
+    // Tiles at most: an expert may end in one that is not full.  Up to half
+    // the SMs, two CTAs share each, up to a quarter four (one token, two
+    // experts of 4096 x 4096 in bf16: 21 us on 64 SMs, with two SMs a tile 18).
+    const int64_t rows = g.p.R, experts = rows < g.p.E ? rows : g.p.E;
+    const int64_t most = (rows / NT + experts) * ((g.p.N + ST_ROWS - 1) / ST_ROWS), sms = device_sm_count();
+    int parts = most * 4 <= sms ? 4 : most * 2 <= sms ? 2 : 1;
+    while (parts > 1 && Z::left(parts) < 3) parts /= 2;
+    g.stages = Z::left(parts);
+    if (parts == 1)
+        return int(launch_kernel(kernel, dim3(unsigned(sms)), dim3(Z::THREADS), Z::SMEM, st, g));
+    return int(launch_clusters(kernel, parts, int(most), st, g, Z::THREADS, Z::SMEM));
 }
 
 int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st)

@@ -164,8 +164,10 @@ static unsigned grid_for(int64_t eighths)
 int launch_expert_decode(const ExpertArgs &p, uint16_t *out, cudaStream_t st)
 {
     DecodeArgs a{p, out};
+    // every segment's blocks could fill the GPU alone; those of segments
+    // without rows return at once
     const int y = p.nbins < 64 ? p.nbins : 64;
-    const unsigned x = (grid_for(int64_t(p.N) * p.K / 8) + 3) / 4;
+    const unsigned x = grid_for(int64_t(p.N) * p.K / 8);
     return int(launch_kernel(expert_decode_kernel, dim3(x, unsigned(y)), dim3(MX_THREADS), 0, st, a));
 }
 

@@ -328,19 +328,19 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// Launch with clusters of two CTAs.
+// Launch of `clusters` clusters of `size` CTAs.
 template <typename Kern, typename Arg>
-cudaError_t launch_pair_kernel(Kern kernel, int pairs, cudaStream_t stream, const Arg &arg,
-                               int threads = PG_THREADS, int smem = PG_SMEM)
+cudaError_t launch_clusters(Kern kernel, int size, int clusters, cudaStream_t stream, const Arg &arg, int threads,
+                            int smem)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(2 * pairs));
+    cfg.gridDim = dim3(unsigned(size * clusters));
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = unsigned(size);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -348,6 +348,14 @@ cudaError_t launch_pair_kernel(Kern kernel, int pairs, cudaStream_t stream, cons
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, arg);
+}
+
+// Launch with clusters of two CTAs.
+template <typename Kern, typename Arg>
+cudaError_t launch_pair_kernel(Kern kernel, int pairs, cudaStream_t stream, const Arg &arg,
+                               int threads = PG_THREADS, int smem = PG_SMEM)
+{
+    return launch_clusters(kernel, 2, pairs, stream, arg, threads, smem);
 }
 
 }  // namespace lora
