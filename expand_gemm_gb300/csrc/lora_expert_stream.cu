@@ -10,8 +10,12 @@
 // through shared memory the decoded tile would be written and read once more
 // (8 bytes for each byte of codes).  A byte's two elements are looked up in a
 // table that each lane has in a bank of its own, and multiplied by their
-// scale: 16 instructions for eight elements, of which the masks' pipe takes
-// four.  (With masks and shifts in its place it was 21 and nine.)
+// scale.  The table's rows are 256 bytes apart and it begins on a 64 KB
+// boundary, so that one byte permutation puts a byte of codes into its
+// address: 12 instructions for eight elements.  (With a row every 128 bytes
+// and a multiply-add for the address it was 16; with masks and shifts in the
+// table's place 21.)  The ring's stages lie on both sides of the table, the
+// barriers in the rows' second halves.
 //
 // Warps: 0 loads, 1 issues UMMAs and owns TMEM, 2..5 run the epilogue (thread
 // = TMEM lane = row of W); with 4-bit weights 6..21 decode and 22 fetches
@@ -30,7 +34,7 @@ struct StreamArgs {
     ExpertArgs p;
     CUtensorMap w, x;
     int32_t stages;               // of the ring
-    uint32_t pitch;               // 128, the bytes of a byte's row of the table: see decode_block
+    uint32_t pitch;               // 128, see decode_block
 };
 
 constexpr int ST_ROWS = 128;                    // of W in a tile
@@ -40,6 +44,7 @@ constexpr int ST_SETS = 4;                      // of four warps that decode
 constexpr int ST_SCALE_WARP = ST_DEC0 + 4 * ST_SETS;
 constexpr int ST_MAX_BUFS = 3;                  // decoded stages in TMEM
 constexpr int ST_MAX_STAGES = 12;
+constexpr int ST_TABLE = 65536;                 // shared address of the wide table
 
 template <bool FOUR, int NT>
 struct StreamSizes {
@@ -49,13 +54,20 @@ struct StreamSizes {
     static constexpr int STAGE = LOADED + (FOUR ? 1024 : 0);    // and the rows' eight scales
     static constexpr int THREADS = 32 * (FOUR ? ST_SCALE_WARP + 1 : ST_DEC0);
     static constexpr int BARS = 512;
-    static constexpr int TABLE = FOUR ? 256 * 128 : 0;
-    static constexpr int ROOM = (232448 - 1024 - BARS - TABLE) / STAGE;
-    static constexpr int STAGES = ROOM < ST_MAX_STAGES ? ROOM : ST_MAX_STAGES;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + BARS + TABLE;
     static constexpr int SUMS = NT * ST_ROWS * 4;               // bytes of one CTA's sums of a tile
-    // stages left beside the others' sums
-    static constexpr int left(int parts) { return (STAGES * STAGE - (parts - 1) * SUMS) / STAGE; }
+    // tiles of 128 rows have no room for the wide table, and the products
+    // bound them
+    static constexpr bool WIDE = FOUR && NT < 128;
+    static constexpr int TABLE = WIDE ? 256 * 256 : FOUR ? 256 * 128 : 0;
+    static constexpr int ALL = 232448;                          // shared memory of a CTA, from address 1024 on
+    // stages of the ring beside the sums of parts - 1 other CTAs
+    __host__ __device__ static constexpr int ring(int parts)
+    {
+        const int sums = (parts - 1) * SUMS;
+        const int n = WIDE ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - sums) / STAGE
+                           : (ALL - 1024 - BARS - TABLE - sums) / STAGE;
+        return n < ST_MAX_STAGES ? n : ST_MAX_STAGES;
+    }
     static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
     static constexpr int DECODED = 2 * NT;                     // first TMEM column of the decoded stages
     static constexpr int BUFS = (512 - DECODED) / 128 < ST_MAX_BUFS ? (512 - DECODED) / 128 : ST_MAX_BUFS;
@@ -90,12 +102,13 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// A block of 32 elements with scale byte c.  `table`: shared memory, a byte's
-// pair of bf16 in this lane's bank every `pitch` bytes.  (The compiler does
-// not know the pitch: it would add by shifts, on the pipe that takes the
-// bytes apart.)  Each product with the scale is exact.  ENDS: c may be 0,
-// which is subnormal, or 255, NaN.
-template <bool ENDS>
+// A block of 32 elements with scale byte c.  `table`: shared address of this
+// lane's entries, a pair of bf16 for each byte; WIDE: a byte's are 256 bytes
+// apart and the table is aligned so that the byte is the address's second.
+// Else they are `pitch` bytes apart, which the compiler does not know (it
+// would add by shifts, on the pipe that takes the bytes apart).  Each product
+// with the scale is exact.  ENDS: c may be 0, which is subnormal, or 255, NaN.
+template <bool ENDS, bool WIDE>
 __device__ __forceinline__ void decode_block(uint32_t table, uint32_t pitch, const uint4 &w, uint32_t c, uint32_t *o)
 {
     uint32_t f = c * 0x00800080u;                  // 2^(c - 127) twice
@@ -106,19 +119,21 @@ __device__ __forceinline__ void decode_block(uint32_t table, uint32_t pitch, con
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const uint32_t at = WIDE ? __byte_perm(words[i], table, 0x7604 + (j << 4))
+                                     : __byte_perm(words[i], 0, 0x4440 + j) * pitch + table;
             uint32_t v;
-            asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(__byte_perm(words[i], 0, 0x4440 + j) * pitch + table));
+            asm("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(at));
             o[4 * i + j] = mul_bf16x2(v, f);
         }
     }
 }
 
 // Two blocks, with the scale bytes in the low half of sc.
-template <bool ENDS>
+template <bool ENDS, bool WIDE>
 __device__ __forceinline__ void decode_two(uint32_t table, uint32_t pitch, const uint4 *w, uint32_t sc, uint32_t (&o)[32])
 {
-    decode_block<ENDS>(table, pitch, w[0], sc & 255u, o);
-    decode_block<ENDS>(table, pitch, w[1], sc >> 8 & 255u, o + 16);
+    decode_block<ENDS, WIDE>(table, pitch, w[0], sc & 255u, o);
+    decode_block<ENDS, WIDE>(table, pitch, w[1], sc >> 8 & 255u, o + 16);
 }
 
 // Whether one of four bytes is 0 or 255.
@@ -201,12 +216,21 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
-    uint32_t *table = reinterpret_cast<uint32_t *>(smem + Z::STAGES * Z::STAGE);      // where the whole ring ends
-    const uint32_t bars = base + Z::STAGES * Z::STAGE + Z::TABLE;
-    const uint32_t full = bars, empty = full + 8 * ST_MAX_STAGES;
-    const uint32_t accf = empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
+    // With the wide table: stages, the table, stages, the others' sums; else
+    // stages, the others' sums, the table, barriers.
+    const uint32_t end = smem_addr(st_smem_raw) + Z::ALL;
+    const uint32_t tab = Z::WIDE ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS - Z::TABLE) & ~uint32_t(1023);
+    uint32_t *table = reinterpret_cast<uint32_t *>(smem + (tab - base));
+    const int below = Z::WIDE ? int(tab - base) / Z::STAGE : ST_MAX_STAGES;
+    auto stage_at = [&](int i) {
+        return Z::WIDE && i >= below ? tab + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
+    };
+    const uint32_t bars = Z::WIDE ? tab + 128 : end - Z::BARS;
+    const uint32_t full = bars, empty = Z::WIDE ? bars + 256 : full + 8 * ST_MAX_STAGES;
+    const uint32_t accf = Z::WIDE ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
     const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
     const uint32_t peers = drain + 16;                              // the others' sums are here
+    static_assert(32 + 16 * ST_MAX_BUFS + 24 <= 128 && 8 * ST_MAX_STAGES <= 128, "barriers in a row's second half");
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
     volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
     const ExpertArgs &p = g.p;
@@ -215,11 +239,17 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     const uint32_t rank = cluster_ctarank();
     const int cluster = int(cluster_nctarank()), per = (nk + cluster - 1) / cluster, parts = (nk + per - 1) / per;
     const int kb0 = int(rank) * per, kb1 = min(nk, kb0 + per);
+    // (the top byte of a shared address is the CTA's rank in its cluster)
+    if (Z::WIDE && (smem_addr(st_smem_raw) & 0xFFFFFFu) != 1024) {  // the ring was counted from there
+        pdl_wait();
+        if (threadIdx.x == 0) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
+        return;
+    }
     // the warp as a value that the compiler knows to be the same in its lanes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < Z::STAGES; ++i) {
+        for (int i = 0; i < g.stages; ++i) {
             mbar_init(full + 8 * i, FOUR ? 33 : 1);                  // the scales' 32 lanes
             mbar_init(empty + 8 * i, FOUR ? 9 : 1);                  // the UMMAs, eight decoding warps
         }
@@ -241,7 +271,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     if constexpr (FOUR) {
         for (int i = tid; i < 256 * 32; i += Z::THREADS) {
             const uint32_t byte = uint32_t(i) / 32;
-            table[i] = e2m1_bf16(byte & 15u) | e2m1_bf16(byte >> 4) << 16;
+            table[byte * (Z::WIDE ? 64 : 32) + i % 32] = e2m1_bf16(byte & 15u) | e2m1_bf16(byte >> 4) << 16;
         }
     }
     if (warp == 1) tmem_alloc(smem_addr(s_tmem), Z::COLS);
@@ -278,7 +308,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                         ok = false;
                         break;
                     }
-                    const uint32_t at = base + pos.stage * Z::STAGE, bar = full + 8 * pos.stage;
+                    const uint32_t at = stage_at(pos.stage), bar = full + 8 * pos.stage;
                     mbar_arrive_expect_tx(bar, Z::LOADED);
                     tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
 #pragma unroll
@@ -321,7 +351,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = base + pos.stage * Z::STAGE;
+                const uint32_t at = stage_at(pos.stage);
                 if constexpr (FOUR) {
                     if (!wait(decf + 8 * dec.stage, dec.phase)) {
                         ok = false;
@@ -369,8 +399,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             tc_fence_after();
             const int n = it.n0 + q * 32 + lane;
             const uint32_t t = tmem + uint32_t(acc * NT) + (uint32_t(q * 32) << 16);
-            // the others' sums, behind the first CTA's ring: [parts - 1][NT][128]
-            const uint32_t sums = base + g.stages * Z::STAGE + uint32_t(q * 32 + lane) * 4;
+            // the others' sums: [parts - 1][NT][128]
+            const uint32_t sums = (Z::WIDE ? end : tab) - (parts - 1) * Z::SUMS + uint32_t(q * 32 + lane) * 4;
             if (rank != 0) {
                 const uint32_t to = cluster_map(sums, 0) + (rank - 1) * Z::SUMS;
                 for (int c = 0; c < it.valid; c += 16) {
@@ -435,7 +465,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
-                    uint8_t *to = smem + pos.stage * Z::STAGE + Z::LOADED;
+                    uint8_t *to = smem + (stage_at(pos.stage) - base) + Z::LOADED;
 #pragma unroll
                     for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 8, it.expert, it.n0 + r, kb);
                     // stores before the arrival, which follows when the copies have landed
@@ -462,7 +492,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     if (turn == 0) continue;
                     ok = __all_sync(0xffffffffu, lazy_wait(full + 8 * pos.stage, pos.phase, 20));
                     if (!ok) break;
-                    const uint8_t *at = smem + pos.stage * Z::STAGE;
+                    const uint8_t *at = smem + (stage_at(pos.stage) - base);
                     const uint32_t sc = *reinterpret_cast<const uint32_t *>(at + Z::LOADED + row * 8 + half * 4);
                     uint4 w[4];
 #pragma unroll
@@ -473,8 +503,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t o[32];
-                        if (ends) decode_two<true>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
-                        else decode_two<false>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
+                        if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
+                        else decode_two<false, Z::WIDE>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
                         if (j == 0) {
                             // what this stage held is in registers
                             __syncwarp();
@@ -511,18 +541,18 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     using Z = StreamSizes<FOUR, NT>;
     static std::atomic<uint64_t> done{0};
     const auto kernel = expert_stream_kernel<FOUR, NT>;
-    if (int e = expert_shared_memory((const void *)kernel, Z::SMEM, done)) return e;
+    if (int e = expert_shared_memory((const void *)kernel, Z::ALL, done)) return e;
     // Tiles at most: an expert may end in one that is not full.  Up to half
     // the SMs, two CTAs share each, up to a quarter four (one token, two
     // experts of 4096 x 4096 in bf16: 21 us on 64 SMs, with two SMs a tile 18).
     const int64_t rows = g.p.R, experts = rows < g.p.E ? rows : g.p.E;
     const int64_t most = (rows / NT + experts) * ((g.p.N + ST_ROWS - 1) / ST_ROWS), sms = device_sm_count();
     int parts = most * 4 <= sms ? 4 : most * 2 <= sms ? 2 : 1;
-    while (parts > 1 && Z::left(parts) < 3) parts /= 2;
-    g.stages = Z::left(parts);
+    while (parts > 1 && Z::ring(parts) < 3) parts /= 2;
+    g.stages = Z::ring(parts);
     if (parts == 1)
-        return int(launch_kernel(kernel, dim3(unsigned(sms)), dim3(Z::THREADS), Z::SMEM, st, g));
-    return int(launch_clusters(kernel, parts, int(most), st, g, Z::THREADS, Z::SMEM));
+        return int(launch_kernel(kernel, dim3(unsigned(sms)), dim3(Z::THREADS), Z::ALL, st, g));
+    return int(launch_clusters(kernel, parts, int(most), st, g, Z::THREADS, Z::ALL));
 }
 
 int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st)
