@@ -483,43 +483,58 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             const int set = (warp - ST_DEC0) >> 2, q = warp & 3, row = q * 32 + lane;
             const int half = set & 1;
             const uint32_t mine = smem_addr(table) + lane * 4;
-            int turn = set >> 1;                  // stages until this warp's next one
-            TcPos pos, dec;
-            bool ok = true;
-            for (int i = item0; ok && i < total; i += items) {
-                for (int kb = kb0; kb < kb1; ++kb, pos.next(g.stages), dec.next(Z::BUFS)) {
-                    turn ^= 1;
-                    if (turn == 0) continue;
-                    ok = __all_sync(0xffffffffu, lazy_wait(full + 8 * pos.stage, pos.phase, 20));
-                    if (!ok) break;
-                    const uint8_t *at = smem + (stage_at(pos.stage) - base);
-                    const uint32_t sc = *reinterpret_cast<const uint32_t *>(at + Z::LOADED + row * 8 + half * 4);
-                    uint4 w[4];
+            const uint32_t chunk = uint32_t(row * 128 + ((4 * half ^ row) & 7) * 16);      // chunk c of the half: ^ 16 c
+            const uint32_t scale = Z::LOADED + uint32_t(row * 8 + half * 4);
+            const uint32_t tcol = tmem + uint32_t(Z::DECODED + half * 64) + (uint32_t(q * 32) << 16);
+            // all stages of all tiles in one run: this warp's are every other
+            // one, from its set's first
+            const int tiles = total > item0 ? (total - item0 + items - 1) / items : 0;
+            int left = tiles * (kb1 - kb0) - (set >> 1);
+            int stage = set >> 1, buf = set >> 1;
+            uint32_t phase = 0, buf_phase = 1;
+            for (; left > 0; left -= 2) {
+                const uint32_t bar = full + 8 * stage;
+                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, phase)) &&
+                    !__all_sync(0xffffffffu, lazy_wait(bar, phase, 20)))
+                    break;
+                const uint32_t at = stage_at(stage);
+                uint32_t sc;
+                asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(sc) : "r"(at + scale) : "memory");
+                uint4 w[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        w[c] = *reinterpret_cast<const uint4 *>(at + row * 128 + (((4 * half + c) ^ row) & 7) * 16);
-                    const bool ends = __any_sync(0xffffffffu, has_end(sc));
-                    const uint32_t to = tmem + uint32_t(Z::DECODED + dec.stage * 128 + half * 64) + (uint32_t(q * 32) << 16);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t o[32];
-                        if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
-                        else decode_two<false, Z::WIDE>(mine, g.pitch, w + 2 * j, sc >> (16 * j), o);
-                        if (j == 0) {
-                            // what this stage held is in registers
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(empty + 8 * pos.stage);
-                            ok = __all_sync(0xffffffffu, lazy_wait(dece + 8 * dec.stage, dec.phase ^ 1u, 20));
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
-                        tmem_st<32>(to + j * 32, o);
-                    }
-                    if (!ok) break;
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(decf + 8 * dec.stage);
+                for (int c = 0; c < 4; ++c)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                 : "=r"(w[c].x), "=r"(w[c].y), "=r"(w[c].z), "=r"(w[c].w)
+                                 : "r"(at + (chunk ^ uint32_t(16 * c))) : "memory");
+                const bool ends = __any_sync(0xffffffffu, has_end(sc));
+                uint32_t o[32];
+                if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w, sc, o);
+                else decode_two<false, Z::WIDE>(mine, g.pitch, w, sc, o);
+                if (!__all_sync(0xffffffffu, mbar_try_wait(dece + 8 * buf, buf_phase)) &&
+                    !__all_sync(0xffffffffu, lazy_wait(dece + 8 * buf, buf_phase, 20)))
+                    break;
+                tc_fence_after();
+                const uint32_t to = tcol + uint32_t(buf * 128);
+                tmem_st<32>(to, o);
+                if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w + 2, sc >> 16, o);
+                else decode_two<false, Z::WIDE>(mine, g.pitch, w + 2, sc >> 16, o);
+                tmem_st<32>(to + 32, o);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(empty + 8 * stage);
+                    mbar_arrive(decf + 8 * buf);
+                }
+                stage += 2;
+                if (stage >= g.stages) {
+                    stage -= g.stages;
+                    phase ^= 1u;
+                }
+                buf += 2;
+                if (buf >= Z::BUFS) {
+                    buf -= Z::BUFS;
+                    buf_phase ^= 1u;
                 }
             }
         }
