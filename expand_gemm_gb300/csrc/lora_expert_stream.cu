@@ -18,8 +18,11 @@
 // barriers in the rows' second halves.
 //
 // Warps: 0 loads, 1 issues UMMAs and owns TMEM, 2..5 run the epilogue (thread
-// = TMEM lane = row of W); with 4-bit weights 6..21 decode and 22 fetches
-// scales.  Two accumulators: the epilogue of one tile runs under the next
+// = TMEM lane = row of W); with 4-bit weights 6..21 decode, 22 fetches scales
+// and 23 loads x, into a ring of its own: codes are done with when they are
+// decoded, x when the products have run (in one ring four stages in six waited
+// for that, and the decoding for codes: 170 us in place of RING_FIGURE for 32
+// tokens of 32 experts 11008 x 4096).  Two accumulators: the epilogue of one tile runs under the next
 // one's products.
 //
 // Where the tiles are fewer than the SMs, a cluster of CTAs shares a tile, each
@@ -42,6 +45,7 @@ constexpr int ST_TILE = ST_ROWS * 128;          // bytes of W in a stage: 64 bf1
 constexpr int ST_DEC0 = 6;                      // first decoding warp
 constexpr int ST_SETS = 4;                      // of four warps that decode
 constexpr int ST_SCALE_WARP = ST_DEC0 + 4 * ST_SETS;
+constexpr int ST_X_WARP = ST_SCALE_WARP + 1;    // loads x, beside codes
 constexpr int ST_MAX_BUFS = 3;                  // decoded stages in TMEM
 constexpr int ST_MAX_STAGES = 12;
 constexpr int ST_TABLE = 65536;                 // shared address of the wide table
@@ -50,9 +54,12 @@ template <bool FOUR, int NT>
 struct StreamSizes {
     static constexpr int KC = FOUR ? 256 : 64;                  // elements of K in a stage
     static constexpr int PANELS = KC / 64;                      // of x: NT rows of 64
-    static constexpr int LOADED = ST_TILE + PANELS * NT * 128;  // bytes of a stage by TMA
-    static constexpr int STAGE = LOADED + (FOUR ? 1024 : 0);    // and the rows' eight scales
-    static constexpr int THREADS = 32 * (FOUR ? ST_SCALE_WARP + 1 : ST_DEC0);
+    static constexpr int X = PANELS * NT * 128;                 // bytes of x in a stage
+    // a stage of the ring: W and x, or the codes and the rows' eight scales,
+    // beside a ring of XS stages of x
+    static constexpr int STAGE = FOUR ? ST_TILE + 1024 : ST_TILE + X;
+    static constexpr int XS = !FOUR ? 0 : NT <= 16 ? 4 : 2;
+    static constexpr int THREADS = 32 * (FOUR ? ST_X_WARP + 1 : ST_DEC0);
     static constexpr int BARS = 512;
     static constexpr int SUMS = NT * ST_ROWS * 4;               // bytes of one CTA's sums of a tile
     // tiles of 128 rows have no room for the wide table, and the products
@@ -60,12 +67,12 @@ struct StreamSizes {
     static constexpr bool WIDE = FOUR && NT < 128;
     static constexpr int TABLE = WIDE ? 256 * 256 : FOUR ? 256 * 128 : 0;
     static constexpr int ALL = 232448;                          // shared memory of a CTA, from address 1024 on
-    // stages of the ring beside the sums of parts - 1 other CTAs
+    // stages of the ring beside that of x and the sums of parts - 1 other CTAs
     __host__ __device__ static constexpr int ring(int parts)
     {
-        const int sums = (parts - 1) * SUMS;
-        const int n = WIDE ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - sums) / STAGE
-                           : (ALL - 1024 - BARS - TABLE - sums) / STAGE;
+        const int rest = XS * X + (parts - 1) * SUMS;
+        const int n = WIDE ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - rest) / STAGE
+                           : (ALL - 1024 - BARS - TABLE - rest) / STAGE;
         return n < ST_MAX_STAGES ? n : ST_MAX_STAGES;
     }
     static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
@@ -208,6 +215,19 @@ __device__ __forceinline__ void umma_k64_smem(uint32_t d_tmem, uint32_t a, uint3
                "r"(kk == 0 ? more : 1u) : "memory");
 }
 
+// No copy may be on its way to this CTA when it exits.
+__device__ __forceinline__ void drain_ring(uint32_t full, uint32_t empty, int stages, int issued, volatile int *abort)
+{
+    const long long dd = clock64() + PG_TIMEOUT_CYCLES;
+    for (int i = max(0, issued - stages); i < issued; ++i) {
+        const uint32_t ph = uint32_t(i / stages) & 1u, b8 = 8u * uint32_t(i % stages);
+        while (!mbar_try_wait(full + b8, ph) && clock64() < dd) {
+        }
+        while (!mbar_try_wait(empty + b8, ph) && !*abort && clock64() < dd) {
+        }
+    }
+}
+
 template <bool FOUR, int NT>
 __global__ void __launch_bounds__(StreamSizes<FOUR, NT>::THREADS, 1)
 expert_stream_kernel(const __grid_constant__ StreamArgs g)
@@ -216,8 +236,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
-    // With the wide table: stages, the table, stages, the others' sums; else
-    // stages, the others' sums, the table, barriers.
+    // With the wide table: stages, the table, stages, x, the others' sums;
+    // else stages, x, the others' sums, the table, barriers.
     const uint32_t end = smem_addr(st_smem_raw) + Z::ALL;
     const uint32_t tab = Z::WIDE ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS - Z::TABLE) & ~uint32_t(1023);
     uint32_t *table = reinterpret_cast<uint32_t *>(smem + (tab - base));
@@ -225,20 +245,24 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     auto stage_at = [&](int i) {
         return Z::WIDE && i >= below ? tab + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
     };
-    const uint32_t bars = Z::WIDE ? tab + 128 : end - Z::BARS;
-    const uint32_t full = bars, empty = Z::WIDE ? bars + 256 : full + 8 * ST_MAX_STAGES;
-    const uint32_t accf = Z::WIDE ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
-    const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
-    const uint32_t peers = drain + 16;                              // the others' sums are here
-    static_assert(32 + 16 * ST_MAX_BUFS + 24 <= 128 && 8 * ST_MAX_STAGES <= 128, "barriers in a row's second half");
-    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
-    volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+    // the others' sums, [parts - 1][NT][128], and x before them
     const ExpertArgs &p = g.p;
     const int cols = (p.N + ST_ROWS - 1) / ST_ROWS, nk = (p.K + Z::KC - 1) / Z::KC;
     // this CTA's share of a tile's K; parts that would have none are not counted
     const uint32_t rank = cluster_ctarank();
     const int cluster = int(cluster_nctarank()), per = (nk + cluster - 1) / cluster, parts = (nk + per - 1) / per;
     const int kb0 = int(rank) * per, kb1 = min(nk, kb0 + per);
+    const uint32_t sums = (Z::WIDE ? end : tab) - (cluster - 1) * Z::SUMS;
+    const uint32_t x_at = sums - Z::XS * Z::X;
+    const uint32_t bars = Z::WIDE ? tab + 128 : end - Z::BARS;
+    const uint32_t full = bars, empty = Z::WIDE ? bars + 256 : full + 8 * ST_MAX_STAGES;
+    const uint32_t accf = Z::WIDE ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
+    const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
+    const uint32_t peers = drain + 16;                              // the others' sums are here
+    const uint32_t xfull = Z::WIDE ? bars + 768 : peers + 8, xempty = xfull + 8 * 4;
+    static_assert(32 + 16 * ST_MAX_BUFS + 24 <= 128 && 8 * ST_MAX_STAGES <= 128, "barriers in a row's second half");
+    uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
+    volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
     // (the top byte of a shared address is the CTA's rank in its cluster)
     if (Z::WIDE && (smem_addr(st_smem_raw) & 0xFFFFFFu) != 1024) {  // the ring was counted from there
         pdl_wait();
@@ -251,7 +275,11 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     if (tid == 0) {
         for (int i = 0; i < g.stages; ++i) {
             mbar_init(full + 8 * i, FOUR ? 33 : 1);                  // the scales' 32 lanes
-            mbar_init(empty + 8 * i, FOUR ? 9 : 1);                  // the UMMAs, eight decoding warps
+            mbar_init(empty + 8 * i, FOUR ? 8 : 1);                  // eight decoding warps; the UMMAs
+        }
+        for (int i = 0; i < Z::XS; ++i) {
+            mbar_init(xfull + 8 * i, 1);
+            mbar_init(xempty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(accf + 8 * i, 1);
@@ -309,24 +337,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                         break;
                     }
                     const uint32_t at = stage_at(pos.stage), bar = full + 8 * pos.stage;
-                    mbar_arrive_expect_tx(bar, Z::LOADED);
+                    mbar_arrive_expect_tx(bar, FOUR ? ST_TILE : Z::STAGE);
                     tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
-#pragma unroll
-                    for (int j = 0; j < Z::PANELS; ++j)
-                        tma_load_2d(at + ST_TILE + j * NT * 128, &g.x, kb * Z::KC + j * 64, it.row, bar);
+                    if (!FOUR) tma_load_2d(at + ST_TILE, &g.x, kb * Z::KC, it.row, bar);
                     pos.next(g.stages);
                     ++issued;
                 }
             }
-            // no copy may be on its way to this CTA when it exits
-            const long long dd = clock64() + PG_TIMEOUT_CYCLES;
-            for (int i = max(0, issued - g.stages); i < issued; ++i) {
-                const uint32_t ph = uint32_t(i / g.stages) & 1u, b8 = 8u * uint32_t(i % g.stages);
-                while (!mbar_try_wait(full + b8, ph) && clock64() < dd) {
-                }
-                while (!mbar_try_wait(empty + b8, ph) && !*abort && clock64() < dd) {
-                }
-            }
+            drain_ring(full, empty, g.stages, issued, abort);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -346,12 +364,12 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             tc_fence_after();
             const uint32_t d = tmem + uint32_t(acc * NT);
             for (int kb = kb0; ok && kb < kb1; ++kb) {
-                if (!wait(full + 8 * pos.stage, pos.phase)) {
+                if (!wait((FOUR ? xfull : full) + 8 * pos.stage, pos.phase)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = stage_at(pos.stage);
+                const uint32_t at = FOUR ? x_at + pos.stage * Z::X : stage_at(pos.stage);
                 if constexpr (FOUR) {
                     if (!wait(decf + 8 * dec.stage, dec.phase)) {
                         ok = false;
@@ -363,7 +381,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 #pragma unroll
                         for (int j = 0; j < Z::PANELS; ++j)
                             if (kb * Z::KC + j * 64 < p.K)
-                                umma_k64_tmem_a(d, a + j * 32, at + ST_TILE + j * NT * 128, idesc,
+                                umma_k64_tmem_a(d, a + j * 32, at + j * NT * 128, idesc,
                                                 kb != kb0 || j != 0);
                         umma_commit(dece + 8 * dec.stage);
                     }
@@ -371,9 +389,9 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 } else if (leader) {
                     umma_k64_smem(d, at, at + ST_TILE, idesc, kb != kb0);
                 }
-                if (leader) umma_commit(empty + 8 * pos.stage);
+                if (leader) umma_commit((FOUR ? xempty : empty) + 8 * pos.stage);
                 __syncwarp();
-                pos.next(g.stages);
+                pos.next(FOUR ? Z::XS : g.stages);
             }
             if (!ok) break;
             if (leader) umma_commit(accf + 8 * acc);
@@ -399,10 +417,9 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             tc_fence_after();
             const int n = it.n0 + q * 32 + lane;
             const uint32_t t = tmem + uint32_t(acc * NT) + (uint32_t(q * 32) << 16);
-            // the others' sums: [parts - 1][NT][128]
-            const uint32_t sums = (Z::WIDE ? end : tab) - (parts - 1) * Z::SUMS + uint32_t(q * 32 + lane) * 4;
+            const uint32_t mine = sums + uint32_t(q * 32 + lane) * 4;
             if (rank != 0) {
-                const uint32_t to = cluster_map(sums, 0) + (rank - 1) * Z::SUMS;
+                const uint32_t to = cluster_map(mine, 0) + (rank - 1) * Z::SUMS;
                 for (int c = 0; c < it.valid; c += 16) {
                     uint32_t v[16];
                     tmem_ld16_nowait(t + c, v);
@@ -441,7 +458,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     for (int k = 1; k < parts; ++k) {
                         float more;
                         asm volatile("ld.shared.f32 %0, [%1];\n"
-                                     : "=f"(more) : "r"(sums + (k - 1) * Z::SUMS + (c + j) * (ST_ROWS * 4)));
+                                     : "=f"(more) : "r"(mine + (k - 1) * Z::SUMS + (c + j) * (ST_ROWS * 4)));
                         s += more;
                     }
                     if (p.add) s += old[j];
@@ -465,7 +482,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
-                    uint8_t *to = smem + (stage_at(pos.stage) - base) + Z::LOADED;
+                    uint8_t *to = smem + (stage_at(pos.stage) - base) + ST_TILE;
 #pragma unroll
                     for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 8, it.expert, it.n0 + r, kb);
                     // stores before the arrival, which follows when the copies have landed
@@ -476,6 +493,32 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             }
             cp_async_commit();
             cp_async_wait<0>();
+        } else if (warp == ST_X_WARP) {
+            // --------------------------------------------------------- x
+            if (lane == 0) {
+                asm volatile("fence.proxy.async.global;\n" ::: "memory");      // written by an ordinary kernel
+                TcPos pos;
+                int issued = 0;
+                bool ok = true;
+                for (int i = item0; ok && i < total; i += items) {
+                    const StreamItem it = stream_item<NT>(p, i, cols);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!lazy_wait(xempty + 8 * pos.stage, pos.phase ^ 1u, 40)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t at = x_at + pos.stage * Z::X, bar = xfull + 8 * pos.stage;
+                        mbar_arrive_expect_tx(bar, Z::X);
+#pragma unroll
+                        for (int j = 0; j < Z::PANELS; ++j)
+                            tma_load_2d(at + j * NT * 128, &g.x, kb * Z::KC + j * 64, it.row, bar);
+                        pos.next(Z::XS);
+                        ++issued;
+                    }
+                }
+                drain_ring(xfull, xempty, Z::XS, issued, abort);
+            }
+            __syncwarp();
         } else {
             // -------------------------------------------------- decoding
             // Two sets of four warps share a stage, the other two the next
@@ -484,7 +527,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             const int half = set & 1;
             const uint32_t mine = smem_addr(table) + lane * 4;
             const uint32_t chunk = uint32_t(row * 128 + ((4 * half ^ row) & 7) * 16);      // chunk c of the half: ^ 16 c
-            const uint32_t scale = Z::LOADED + uint32_t(row * 8 + half * 4);
+            const uint32_t scale = ST_TILE + uint32_t(row * 8 + half * 4);
             const uint32_t tcol = tmem + uint32_t(Z::DECODED + half * 64) + (uint32_t(q * 32) << 16);
             // all stages of all tiles in one run: this warp's are every other
             // one, from its set's first
@@ -506,7 +549,11 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                                  : "=r"(w[c].x), "=r"(w[c].y), "=r"(w[c].z), "=r"(w[c].w)
                                  : "r"(at + (chunk ^ uint32_t(16 * c))) : "memory");
-                const bool ends = __any_sync(0xffffffffu, has_end(sc));
+                // The vote also takes a word of each load, so that they have all
+                // arrived (in every lane) when the stage is given back.  Where
+                // it is true without need the slower form gives the same.
+                const bool ends = __any_sync(0xffffffffu, has_end(sc) || (w[0].x ^ w[1].x ^ w[2].x ^ w[3].x) == 0x9E3779B9u);
+                if (lane == 0) mbar_arrive(empty + 8 * stage);
                 uint32_t o[32];
                 if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w, sc, o);
                 else decode_two<false, Z::WIDE>(mine, g.pitch, w, sc, o);
@@ -522,10 +569,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(empty + 8 * stage);
-                    mbar_arrive(decf + 8 * buf);
-                }
+                if (lane == 0) mbar_arrive(decf + 8 * buf);
                 stage += 2;
                 if (stage >= g.stages) {
                     stage -= g.stages;
