@@ -28,17 +28,6 @@ namespace lora {
 
 constexpr int TC_ROWS = 128;                     // tokens of a tile of g and dx
 
-// Four rows of a 2-D tensor, one 64-column box each.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int col, int r0,
-                                            int r1, int r2, int r3, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n"
-        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r0), "r"(r1), "r"(r2),
-           "r"(r3), "r"(bar) : "memory");
-}
-
 constexpr int TC_HEIGHTS = 6;                    // boxes of 4, 8, ... 128 rows
 
 // The rows a lane loads: its four tokens, or a box of 4 << level rows from

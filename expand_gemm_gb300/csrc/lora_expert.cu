@@ -294,6 +294,10 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
     p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);
     p.xs = reinterpret_cast<uint16_t *>(ws + lay.xs);
+    if (!pairs && expert_stream_gathers(p)) {
+        p.table = nullptr;
+        return launch_expert_stream(p, lay.rows, st);
+    }
     if (int e = launch_pack(p, lay.rows, st)) return e;
     if (!pairs) return launch_expert_stream(p, lay.rows, st);
     if (decode) {

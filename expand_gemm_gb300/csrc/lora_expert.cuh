@@ -169,7 +169,9 @@ int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 
-// lora_expert_stream.cu: few rows an expert, weights in either form.
+// lora_expert_stream.cu: few rows an expert, weights in either form.  Where it
+// gathers it needs no copy of x and no table (p.table is null).
+bool expert_stream_gathers(const ExpertArgs &p);
 int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st);
 
 // lora_mxfp4.cu: the weights of the experts that have rows, decoded to bf16.

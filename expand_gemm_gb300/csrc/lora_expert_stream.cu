@@ -25,6 +25,10 @@
 // tokens of 32 experts 11008 x 4096).  Two accumulators: the epilogue of one tile runs under the next
 // one's products.
 //
+// Batches of a few rows need no copy of x: the kernel walks the metadata's
+// segments itself and gathers rows by TMA (90 clocks for four rows of 128
+// bytes: with more rows that would be what bounds it).
+//
 // Where the tiles are fewer than the SMs, a cluster of CTAs shares a tile, each
 // a run of its K: the others write their sums into the first one's shared
 // memory, which adds them in order.
@@ -48,6 +52,9 @@ constexpr int ST_SCALE_WARP = ST_DEC0 + 4 * ST_SETS;
 constexpr int ST_X_WARP = ST_SCALE_WARP + 1;    // loads x, beside codes
 constexpr int ST_MAX_BUFS = 3;                  // decoded stages in TMEM
 constexpr int ST_MAX_STAGES = 12;
+constexpr int ST_BINS = 257;                    // segments, where the kernel walks them itself
+constexpr int ST_SEGMENTS = 5 * 1024;           // and their bytes
+static_assert(seg_tab_bytes(ST_BINS) <= ST_SEGMENTS, "segments");
 constexpr int ST_TABLE = 65536;                 // shared address of the wide table
 
 template <bool FOUR, int NT>
@@ -70,11 +77,12 @@ struct StreamSizes {
     // stages of the ring beside that of x and the sums of parts - 1 other CTAs
     __host__ __device__ static constexpr int ring(int parts)
     {
-        const int rest = XS * X + (parts - 1) * SUMS;
+        const int rest = XS * X + (parts - 1) * SUMS + (WIDE ? 0 : ST_SEGMENTS);
         const int n = WIDE ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - rest) / STAGE
                            : (ALL - 1024 - BARS - TABLE - rest) / STAGE;
         return n < ST_MAX_STAGES ? n : ST_MAX_STAGES;
     }
+    static_assert(!WIDE || (ST_TABLE - 1024) % STAGE >= ST_SEGMENTS, "the segments lie between stages and table");
     static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
     static constexpr int DECODED = 2 * NT;                     // first TMEM column of the decoded stages
     static constexpr int BUFS = (512 - DECODED) / 128 < ST_MAX_BUFS ? (512 - DECODED) / 128 : ST_MAX_BUFS;
@@ -87,9 +95,14 @@ struct StreamItem {
 
 // Item i: an expert's tiles of rows take 128 rows of its weights one after
 // another, so that they are read from memory once.
-template <int NT>
-__device__ __forceinline__ StreamItem stream_item(const ExpertArgs &p, int i, int cols)
+template <bool DIRECT, int NT>
+__device__ __forceinline__ StreamItem stream_item(const ExpertArgs &p, const SegTab &tab, int i, int cols)
 {
+    if constexpr (DIRECT) {
+        const int k = find_segment(tab.tile, p.nbins, i / cols), first = tab.tile[k], tiles = tab.tile[k + 1] - first;
+        const int j = i - first * cols, tile = j % tiles;
+        return StreamItem{0, min(NT, tab.count[k] - tile * NT), tab.start[k] + tile * NT, j / tiles * ST_ROWS, tab.id[k]};
+    }
     const int4 *at = reinterpret_cast<const int4 *>(p.table + i / cols);
     const int4 a = at[0], b = at[1];          // base, tiles, expert, start; count, row
     const int j = i - a.x * cols, tile = j % a.y;
@@ -228,7 +241,40 @@ __device__ __forceinline__ void drain_ring(uint32_t full, uint32_t empty, int st
     }
 }
 
-template <bool FOUR, int NT>
+// One stage of x, by a whole warp: from the copy, or by gathers of four rows a
+// lane (rows[0] < 0: none); PANELS boxes of 64 columns, `pitch` bytes apart.
+template <bool DIRECT, int PANELS>
+__device__ __forceinline__ void load_x(const StreamArgs &g, uint32_t to, int pitch, int col, int row, const int (&rows)[4],
+                                       uint32_t bar)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < PANELS; ++j) {
+        if constexpr (!DIRECT) {
+            if (lane == 0) tma_load_2d(to + j * pitch, &g.x, col + j * 64, row, bar);
+        } else if (rows[0] >= 0 && col + j * 64 < g.p.K) {
+            tma_gather4(to + j * pitch + lane * 512, &g.x, col + j * 64, rows[0], rows[1], rows[2], rows[3], bar);
+        }
+    }
+}
+
+// The four rows of x that this lane gathers for a tile, outside the matrix
+// behind the tile's last.
+__device__ __forceinline__ void gathered_rows(const ExpertArgs &p, const StreamItem &it, int (&rows)[4])
+{
+    const int first = 4 * int(threadIdx.x & 31);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        int row = p.R;
+        if (first + k < it.valid) {
+            const int i = checked_token(p.sorted[it.start + first + k], p.R, p.error_word);
+            row = i < 0 ? p.R : i / p.fan;
+        }
+        rows[k] = first < it.valid ? row : -1;
+    }
+}
+
+template <bool FOUR, int NT, bool DIRECT>
 __global__ void __launch_bounds__(StreamSizes<FOUR, NT>::THREADS, 1)
 expert_stream_kernel(const __grid_constant__ StreamArgs g)
 {
@@ -236,14 +282,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
-    // With the wide table: stages, the table, stages, x, the others' sums;
-    // else stages, x, the others' sums, the table, barriers.
+    // With the wide table: stages, segments, the table, stages, x, the others'
+    // sums; else stages, segments, x, the others' sums, the table, barriers.
     const uint32_t end = smem_addr(st_smem_raw) + Z::ALL;
-    const uint32_t tab = Z::WIDE ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS - Z::TABLE) & ~uint32_t(1023);
-    uint32_t *table = reinterpret_cast<uint32_t *>(smem + (tab - base));
-    const int below = Z::WIDE ? int(tab - base) / Z::STAGE : ST_MAX_STAGES;
+    const uint32_t lut = Z::WIDE ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS - Z::TABLE) & ~uint32_t(1023);
+    uint32_t *table = reinterpret_cast<uint32_t *>(smem + (lut - base));
+    const int below = Z::WIDE ? int(lut - base) / Z::STAGE : ST_MAX_STAGES;
     auto stage_at = [&](int i) {
-        return Z::WIDE && i >= below ? tab + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
+        return Z::WIDE && i >= below ? lut + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
     };
     // the others' sums, [parts - 1][NT][128], and x before them
     const ExpertArgs &p = g.p;
@@ -252,9 +298,10 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     const uint32_t rank = cluster_ctarank();
     const int cluster = int(cluster_nctarank()), per = (nk + cluster - 1) / cluster, parts = (nk + per - 1) / per;
     const int kb0 = int(rank) * per, kb1 = min(nk, kb0 + per);
-    const uint32_t sums = (Z::WIDE ? end : tab) - (cluster - 1) * Z::SUMS;
+    const uint32_t sums = (Z::WIDE ? end : lut) - (cluster - 1) * Z::SUMS;
     const uint32_t x_at = sums - Z::XS * Z::X;
-    const uint32_t bars = Z::WIDE ? tab + 128 : end - Z::BARS;
+    const SegTab tab = seg_tab(reinterpret_cast<int *>(smem + ((Z::WIDE ? lut : x_at) - ST_SEGMENTS - base)), p.nbins);
+    const uint32_t bars = Z::WIDE ? lut + 128 : end - Z::BARS;
     const uint32_t full = bars, empty = Z::WIDE ? bars + 256 : full + 8 * ST_MAX_STAGES;
     const uint32_t accf = Z::WIDE ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
     const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
@@ -310,7 +357,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
     pdl_wait();
 
-    const int total = kb0 < kb1 ? *p.tiles * cols : 0;
+    int total;
+    if constexpr (DIRECT) {
+        total = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, NT, tab, false, 0, p.R, p.error_word);
+        total = __shfl_sync(0xffffffffu, total, 0);
+    } else {
+        total = *p.tiles;
+    }
+    total = kb0 < kb1 ? total * cols : 0;
     const int item0 = int(blockIdx.x) / cluster, items = int(gridDim.x) / cluster;
     auto wait = [&](uint32_t bar, uint32_t parity) {
         return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES);
@@ -324,27 +378,36 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 
     if (warp == 0) {
         // ---------------------------------------------------------- loads
-        if (lane == 0) {
-            asm volatile("fence.proxy.async.global;\n" ::: "memory");      // x was written by an ordinary kernel
+        // One lane; where rows are gathered, all of them.
+        if (lane == 0 || (!FOUR && DIRECT)) {
+            // x was written by an ordinary kernel
+            asm volatile("fence.proxy.async.global;\n" ::: "memory");
             TcPos pos;
             int issued = 0;
             bool ok = true;
             for (int i = item0; ok && i < total; i += items) {
-                const StreamItem it = stream_item<NT>(p, i, cols);
+                const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+                int rows[4];
+                if (!FOUR && DIRECT) gathered_rows(p, it, rows);
+                const uint32_t bytes = FOUR ? ST_TILE : ST_TILE + (DIRECT ? uint32_t((it.valid + 3) / 4) * 512 : Z::X);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40);
+                    if (!FOUR && DIRECT) ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                     const uint32_t at = stage_at(pos.stage), bar = full + 8 * pos.stage;
-                    mbar_arrive_expect_tx(bar, FOUR ? ST_TILE : Z::STAGE);
-                    tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
-                    if (!FOUR) tma_load_2d(at + ST_TILE, &g.x, kb * Z::KC, it.row, bar);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, bytes);
+                        tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
+                    }
+                    if constexpr (!FOUR) {
+                        if (DIRECT) __syncwarp();
+                        load_x<DIRECT, 1>(g, at + ST_TILE, 0, kb * 64, it.row, rows, bar);
+                    }
                     pos.next(g.stages);
                     ++issued;
                 }
             }
-            drain_ring(full, empty, g.stages, issued, abort);
+            if (lane == 0) drain_ring(full, empty, g.stages, issued, abort);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -358,7 +421,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         bool ok = true;
         const bool leader = elect_one();
         for (int i = item0; ok && i < total; i += items) {
-            const StreamItem it = stream_item<NT>(p, i, cols);
+            const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
             const uint32_t idesc = __shfl_sync(0xffffffffu, umma_idesc_bf16(ST_ROWS, (it.valid + 15) & ~15), 0);
             if (!wait(acce + 8 * acc, acc_phase ^ 1u)) break;
             tc_fence_after();
@@ -412,7 +475,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = item0; i < total; i += items) {
-            const StreamItem it = stream_item<NT>(p, i, cols);
+            const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
             if (!__all_sync(0xffffffffu, lazy_wait(accf + 8 * acc, acc_phase, 200))) break;
             tc_fence_after();
             const int n = it.n0 + q * 32 + lane;
@@ -478,7 +541,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             TcPos pos;
             bool ok = true;
             for (int i = item0; ok && i < total; i += items) {
-                const StreamItem it = stream_item<NT>(p, i, cols);
+                const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
@@ -495,28 +558,31 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             cp_async_wait<0>();
         } else if (warp == ST_X_WARP) {
             // --------------------------------------------------------- x
-            if (lane == 0) {
+            if (lane == 0 || DIRECT) {
                 asm volatile("fence.proxy.async.global;\n" ::: "memory");      // written by an ordinary kernel
                 TcPos pos;
                 int issued = 0;
                 bool ok = true;
                 for (int i = item0; ok && i < total; i += items) {
-                    const StreamItem it = stream_item<NT>(p, i, cols);
+                    const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+                    int rows[4];
+                    if (DIRECT) gathered_rows(p, it, rows);
+                    const uint32_t gathered = uint32_t((it.valid + 3) / 4) * 512;
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!lazy_wait(xempty + 8 * pos.stage, pos.phase ^ 1u, 40)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t at = x_at + pos.stage * Z::X, bar = xfull + 8 * pos.stage;
-                        mbar_arrive_expect_tx(bar, Z::X);
-#pragma unroll
-                        for (int j = 0; j < Z::PANELS; ++j)
-                            tma_load_2d(at + j * NT * 128, &g.x, kb * Z::KC + j * 64, it.row, bar);
+                        const uint32_t bytes =
+                            DIRECT ? gathered * uint32_t(min(Z::PANELS, (p.K - kb * Z::KC + 63) / 64)) : uint32_t(Z::X);
+                        ok = lazy_wait(xempty + 8 * pos.stage, pos.phase ^ 1u, 40);
+                        if (DIRECT) ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint32_t bar = xfull + 8 * pos.stage;
+                        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+                        if (DIRECT) __syncwarp();
+                        load_x<DIRECT, Z::PANELS>(g, x_at + pos.stage * Z::X, NT * 128, kb * Z::KC, it.row, rows, bar);
                         pos.next(Z::XS);
                         ++issued;
                     }
                 }
-                drain_ring(xfull, xempty, Z::XS, issued, abort);
+                if (lane == 0) drain_ring(xfull, xempty, Z::XS, issued, abort);
             }
             __syncwarp();
         } else {
@@ -594,12 +660,12 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 
 // ---------------------------------------------------------------- host
 
-template <bool FOUR, int NT>
+template <bool FOUR, int NT, bool DIRECT = false>
 static int run_stream(StreamArgs &g, cudaStream_t st)
 {
     using Z = StreamSizes<FOUR, NT>;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = expert_stream_kernel<FOUR, NT>;
+    const auto kernel = expert_stream_kernel<FOUR, NT, DIRECT>;
     if (int e = expert_shared_memory((const void *)kernel, Z::ALL, done)) return e;
     // Tiles at most: an expert may end in one that is not full.  Up to half
     // the SMs, two CTAs share each, up to a quarter four (one token, two
@@ -614,17 +680,28 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     return int(launch_clusters(kernel, parts, int(most), st, g, Z::THREADS, Z::ALL));
 }
 
+bool expert_stream_gathers(const ExpertArgs &p)
+{
+    // Gathers of a stage, 90 clocks each, in the time of its 16 KB of W (about
+    // 740; 1100 with the decoding of four panels' codes).
+    return p.x_vec && p.nbins <= ST_BINS && p.R <= (p.scales != nullptr ? 12 : 32);
+}
+
 int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st)
 {
     StreamArgs g;
     g.p = p;
     g.pitch = 128;
-    const bool four = p.scales != nullptr;
-    if (!encode_tile_map(&g.x, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), 64, uint32_t(p.tile_rows),
-                         CU_TENSOR_MAP_SWIZZLE_128B) ||
+    const bool four = p.scales != nullptr, direct = p.table == nullptr;
+    if (!(direct ? encode_tile_map(&g.x, p.x, uint64_t(p.R / p.fan), uint64_t(p.K), uint64_t(p.x_ld), 64, 1,
+                                   CU_TENSOR_MAP_SWIZZLE_128B)
+                 : encode_tile_map(&g.x, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), 64, uint32_t(p.tile_rows),
+                                   CU_TENSOR_MAP_SWIZZLE_128B)) ||
         !(four ? encode_stack_map_u8(&g.w, p.codes, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K / 2), 128, ST_ROWS)
                : encode_stack_map(&g.w, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), 64, ST_ROWS)))
         return LORA_ERR_DEVICE;
+    // tiles are of 16 rows (4 bits) or 32 where rows are gathered
+    if (direct) return four ? run_stream<true, 16, true>(g, st) : run_stream<false, 32, true>(g, st);
     if (four) return p.tile_rows == 16   ? run_stream<true, 16>(g, st)
                      : p.tile_rows == 64 ? run_stream<true, 64>(g, st)
                                          : run_stream<true, 128>(g, st);

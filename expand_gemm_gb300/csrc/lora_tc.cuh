@@ -25,6 +25,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// Four rows of a 2-D tensor, one 64-column box each.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap *map, int col, int r0,
+                                            int r1, int r2, int r3, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(r0), "r"(r1), "r"(r2),
+           "r"(r3), "r"(bar) : "memory");
+}
+
 // The ring of operand stages and the accumulators' barriers of one CTA.
 struct TcRing {
     uint32_t ring, full, empty, accf, acce, drain, stage_bytes;
