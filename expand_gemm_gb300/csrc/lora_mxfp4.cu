@@ -45,53 +45,66 @@ struct MxArgs {
     int64_t eighths;              // elements / 8
 };
 
+constexpr int MX_MANY = 4;             // eights of a thread whose loads go out together
+
 // A thread takes eight elements, four threads a block.
 template <bool F32>
 __global__ void __launch_bounds__(MX_THREADS) quantize_kernel(const MxArgs a)
 {
+    constexpr int MANY = F32 ? MX_MANY / 2 : MX_MANY;
     pdl_wait();
     const int64_t step = int64_t(gridDim.x) * MX_THREADS;
     // whole warps: the block's threads exchange their maxima
     const int64_t end = (a.eighths + 31) / 32 * 32;
-    for (int64_t i = int64_t(blockIdx.x) * MX_THREADS + threadIdx.x; i < end; i += step) {
-        const bool in = i < a.eighths;
-        float v[8];
+    for (int64_t i0 = int64_t(blockIdx.x) * MX_THREADS + threadIdx.x; i0 < end; i0 += MANY * step) {
+        uint4 raw[MANY][F32 ? 2 : 1];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (in) {
+        for (int m = 0; m < MANY; ++m) {
+            const int64_t i = i0 + m * step;
+#pragma unroll
+            for (int h = 0; h < (F32 ? 2 : 1); ++h)
+                raw[m][h] = i < a.eighths ? static_cast<const uint4 *>(a.weight)[F32 ? 2 * i + h : i] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int m = 0; m < MANY; ++m) {
+            const int64_t i = i0 + m * step;
+            if (i >= end) break;               // whole warps
+            float v[8];
             if constexpr (F32) {
-                const float4 *src = static_cast<const float4 *>(a.weight) + 2 * i;
-                const float4 p = src[0], q = src[1];
-                v[0] = p.x; v[1] = p.y; v[2] = p.z; v[3] = p.w;
-                v[4] = q.x; v[5] = q.y; v[6] = q.z; v[7] = q.w;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[4 * h] = __uint_as_float(raw[m][h].x);
+                    v[4 * h + 1] = __uint_as_float(raw[m][h].y);
+                    v[4 * h + 2] = __uint_as_float(raw[m][h].z);
+                    v[4 * h + 3] = __uint_as_float(raw[m][h].w);
+                }
             } else {
-                const uint4 p = static_cast<const uint4 *>(a.weight)[i];
-                const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+                const uint32_t w[4] = {raw[m][0].x, raw[m][0].y, raw[m][0].z, raw[m][0].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     v[2 * j] = bf16_lo(w[j]);
                     v[2 * j + 1] = bf16_hi(w[j]);
                 }
             }
-        }
-        // magnitudes as integers: their order is the values', and a NaN or an
-        // infinity is the largest
-        uint32_t top = 0;
+            // magnitudes as integers: their order is the values', and a NaN
+            // or an infinity is the largest
+            uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // below 2^-126 the exponent field says less than it is, and the scale
-        // is 2^-127 all the same
-        const int s = max(int(top >> 23) - 129, -127);
-        const bool bad = top >= 0x7F800000u;
-        const float f = power2(-s);
-        uint32_t word = 0;
+            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // below 2^-126 the exponent field says less than it is, and the
+            // scale is 2^-127 all the same
+            const int s = max(int(top >> 23) - 129, -127);
+            const bool bad = top >= 0x7F800000u;
+            const float f = power2(-s);
+            uint32_t word = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) word |= to_e2m1x2(v[2 * j] * f, v[2 * j + 1] * f) << (8 * j);
-        if (in) {
-            reinterpret_cast<uint32_t *>(a.codes)[i] = bad ? 0u : word;
-            if ((threadIdx.x & 3) == 0) a.scales[i / 4] = uint8_t(bad ? 255 : s + 127);
+            for (int j = 0; j < 4; ++j) word |= to_e2m1x2(v[2 * j] * f, v[2 * j + 1] * f) << (8 * j);
+            if (i < a.eighths) {
+                reinterpret_cast<uint32_t *>(a.codes)[i] = bad ? 0u : word;
+                if ((threadIdx.x & 3) == 0) a.scales[i / 4] = uint8_t(bad ? 255 : s + 127);
+            }
         }
     }
 }
@@ -115,15 +128,27 @@ __global__ void __launch_bounds__(MX_THREADS) dequantize_kernel(const MxArgs a)
 {
     pdl_wait();
     const int64_t step = int64_t(gridDim.x) * MX_THREADS;
-    for (int64_t i = int64_t(blockIdx.x) * MX_THREADS + threadIdx.x; i < a.eighths; i += step) {
-        float v[8];
-        decode8(reinterpret_cast<const uint32_t *>(a.codes)[i], a.scales[i / 4], v);
-        if constexpr (F32) {
-            float4 *to = static_cast<float4 *>(a.out) + 2 * i;
-            to[0] = make_float4(v[0], v[1], v[2], v[3]);
-            to[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            static_cast<uint4 *>(a.out)[i] = pack8(v);
+    for (int64_t i0 = int64_t(blockIdx.x) * MX_THREADS + threadIdx.x; i0 < a.eighths; i0 += MX_MANY * step) {
+        uint32_t word[MX_MANY], c[MX_MANY];
+#pragma unroll
+        for (int m = 0; m < MX_MANY; ++m) {
+            const int64_t i = i0 + m * step;
+            word[m] = i < a.eighths ? reinterpret_cast<const uint32_t *>(a.codes)[i] : 0u;
+            c[m] = i < a.eighths ? a.scales[i / 4] : 0u;
+        }
+#pragma unroll
+        for (int m = 0; m < MX_MANY; ++m) {
+            const int64_t i = i0 + m * step;
+            if (i >= a.eighths) break;
+            float v[8];
+            decode8(word[m], c[m], v);
+            if constexpr (F32) {
+                float4 *to = static_cast<float4 *>(a.out) + 2 * i;
+                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                static_cast<uint4 *>(a.out)[i] = pack8(v);
+            }
         }
     }
 }
