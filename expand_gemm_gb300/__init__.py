@@ -737,7 +737,7 @@ def lora_orthogonalize(update: torch.Tensor, out: torch.Tensor, *, steps: int = 
 
 # ------------------------------------------------------------ the layers under the adapters
 
-def _expert_weight(weight, scale, meta, index: int, k: int):
+def _expert_weight(weight, scale, meta, k: int):
     """(experts, rows) of the bf16 or MXFP4 stack, checked against hidden size k."""
     if scale is None:
         if weight.dim() != 3 or weight.shape[2] != k or not weight.is_contiguous():
@@ -754,8 +754,8 @@ def _expert_weight(weight, scale, meta, index: int, k: int):
     return weight.shape[0], weight.shape[1]
 
 
-def _expert_types(first, first_name, meta, named, weight, scale, workspace) -> int:
-    """Checks the types and devices of an expert call's tensors; the GPU's index."""
+def _expert_types(first, first_name, meta, named, weight, scale, workspace) -> None:
+    """Checks the types and devices of an expert call's tensors."""
     index = meta.no_lora_flag.get_device()
     try:
         ok = (index >= 0 and all(_is(t, _BF16, index) for t, _ in named) and _is(workspace, _U8, index)
@@ -769,10 +769,9 @@ def _expert_types(first, first_name, meta, named, weight, scale, workspace) -> i
              (weight, _BF16 if scale is None else _U8, "weight"), (scale, _U8, "weight_scale"),
              (workspace, _U8, "workspace"))
         raise TypeError("weight must be a tensor")
-    return index
 
 
-def _fan_out(rows: int, tokens: int, meta) -> int:
+def _fan_out(rows: int, tokens: int) -> int:
     if rows == 0 and tokens == 0:
         return 1
     if tokens == 0 or rows % tokens or rows == 0:
@@ -800,15 +799,17 @@ def lora_expert_linear(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, m
     [max_loras, n, hidden / 2] of :func:`lora_quantize_mxfp4` with their
     weight_scale [max_loras, n, hidden / 32].  A workspace (uint8) is allocated
     when none is given."""
-    index = _expert_types(x, "x", meta, ((x, "x"), (y, "y")), weight, weight_scale, workspace)
+    _expert_types(x, "x", meta, ((x, "x"), (y, "y")), weight, weight_scale, workspace)
     if x is None or y is None:
         raise TypeError("x and y must be tensors")
     T, K, x_ld = _rows(x, "x")
     R, cols, y_ld = _rows(y, "y")
-    E, N = _expert_weight(weight, weight_scale, meta, index, K)
+    E, N = _expert_weight(weight, weight_scale, meta, K)
     if cols != N:
         raise ValueError("y must have %d columns" % N)
-    k = _fan_out(R, T, meta)
+    k = _fan_out(R, T)
+    if y.data_ptr() == x.data_ptr() and R > 0:
+        raise ValueError("y must not be x")
     _call_with("lora_expert_linear", workspace, x.device, (R, K, N, meta.max_loras, int(weight_scale is not None)),
                x.data_ptr(), x_ld, R, k, K, weight.data_ptr(),
                None if weight_scale is None else weight_scale.data_ptr(), N, y.data_ptr(), y_ld,
@@ -835,22 +836,24 @@ def lora_expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch
     are left as they are.  d_weight (bf16 [max_loras, n, hidden], also for
     4-bit weights) is overwritten; experts without rows get zeros, and so do
     those that the weights hold beyond the metadata's."""
-    index = _expert_types(dy, "dy", meta, ((dy, "dy"), (x, "x"), (dx, "dx"), (d_weight, "d_weight")), weight,
-                          weight_scale, workspace)
+    _expert_types(dy, "dy", meta, ((dy, "dy"), (x, "x"), (dx, "dx"), (d_weight, "d_weight")), weight,
+                  weight_scale, workspace)
     if dy is None or x is None:
         raise TypeError("dy and x must be tensors")
     T, K, x_ld = _rows(x, "x")
     R, cols, dy_ld = _rows(dy, "dy")
-    E, N = _expert_weight(weight, weight_scale, meta, index, K)
+    E, N = _expert_weight(weight, weight_scale, meta, K)
     if cols != N:
         raise ValueError("dy must have %d columns" % N)
-    k = _fan_out(R, T, meta)
+    k = _fan_out(R, T)
     dx_ptr, dx_ld, dw_ptr = None, K, None
     if dx is not None:
         rows, cols, dx_ld = _rows(dx, "dx")
         if (rows, cols) != (T, K):
             raise ValueError("dx must be [%d, %d]" % (T, K))
         dx_ptr = dx.data_ptr()
+        if R > 0 and (dx_ptr == x.data_ptr() or dx_ptr == dy.data_ptr()):
+            raise ValueError("dx must be neither x nor dy")
     if d_weight is not None:
         if tuple(d_weight.shape) != (E, N, K) or not d_weight.is_contiguous():
             raise ValueError("d_weight must be a contiguous %s tensor" % [E, N, K])
@@ -866,6 +869,15 @@ def lora_expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch
 
 
 def _mx_tensors(values: torch.Tensor, name: str, codes: torch.Tensor, scales: torch.Tensor) -> int:
+    try:
+        index, (*lead, n) = values.get_device(), values.shape
+        if (index >= 0 and (values.dtype is _BF16 or values.dtype is _F32) and codes.dtype is _U8 and scales.dtype is _U8
+                and codes.get_device() == index and scales.get_device() == index and n % 32 == 0
+                and codes.shape == (*lead, n // 2) and scales.shape == (*lead, n // 32) and values.is_contiguous()
+                and codes.is_contiguous() and scales.is_contiguous()):
+            return index
+    except (AttributeError, ValueError):
+        pass
     index = _gpu(values, name)
     if values.dtype is not _BF16 and values.dtype is not _F32:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (name, values.dtype))
@@ -898,6 +910,24 @@ def lora_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.
           int(out.dtype is _F32), _raw_stream(index))
 
 
+def _refuse_overlaps(grads, out) -> None:
+    """Each tensor is read and written as a whole, in no order: no two of the written ones may share
+    memory, nor may one share another's gradient (its own: only as a whole)."""
+    spans = []
+    for i, g in enumerate(grads):
+        w = g if out is None else out[i]
+        spans.append((w.data_ptr(), w.data_ptr() + w.numel() * w.element_size(), i, True))
+        if w.data_ptr() != g.data_ptr():
+            spans.append((g.data_ptr(), g.data_ptr() + g.numel() * g.element_size(), i, False))
+    end = written = 0                       # of all spans so far, and of those that are written
+    for first, last, i, write in sorted(spans):
+        if first < last:
+            if first < (end if write else written):
+                raise ValueError("grads[%d] or its output overlaps another tensor" % i)
+            end = max(end, last)
+            written = max(written, last) if write else written
+
+
 class LoRAGradients:
     """The gradients of many layers, checked once, for
     :func:`lora_clip_gradients` to be called on them every step.
@@ -905,7 +935,7 @@ class LoRAGradients:
     grads: bf16 or fp32 tensors (None is skipped), contiguous, on one GPU.
     groups: how many adapters their first dimension stacks (1: any shape).
     out: None (they are scaled in place), or tensors like them that receive the
-    scaled gradients.  The tensors are kept; their storage must stay where it
+    scaled gradients.  No two may share memory.  The tensors are kept; their storage must stay where it
     is.  A workspace is allocated with it, so calls on one object must be
     ordered on one stream."""
 
@@ -934,6 +964,7 @@ class LoRAGradients:
             if out is not None and (o is None or o.shape != g.shape or not o.is_contiguous()):
                 raise ValueError("out[%d] must be contiguous like its gradient" % i)
         n = len(pairs)
+        _refuse_overlaps([p[1] for p in pairs], None if out is None else [p[2] for p in pairs])
         self.grads, self.out, self.groups, self.count = [p[1] for p in pairs], [p[2] for p in pairs], groups, n
         self.device = self.grads[0].device
         self.c_grads = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])

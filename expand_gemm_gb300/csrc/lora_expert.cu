@@ -18,7 +18,7 @@ constexpr int EX_PACK_THREADS = 256;
 __device__ __forceinline__ void expert_tables(const ExpertArgs &p, const SegTab &tab, int units, int *first_row)
 {
     const int pad = p.pad ? EX_PAD : 1;
-    if (p.copied != nullptr && threadIdx.x == 0) *p.copied = units;
+    if (p.copied != nullptr && threadIdx.x == 0) *p.copied = int(min(int64_t(units), p.rows / pad));
     if (p.blocks != nullptr) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.blocks[e] = make_int2(0, 0);
         __syncthreads();
@@ -30,8 +30,8 @@ __device__ __forceinline__ void expert_tables(const ExpertArgs &p, const SegTab 
     // the segments' rows in the copy, kept while the same memory takes the tiles'
     for (int k = threadIdx.x; units > 0 && k < p.nbins; k += blockDim.x) first_row[k] = tab.tile[k] * pad;
     __syncthreads();
-    const int tiles = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, p.tile_rows, tab, false, 0,
-                                    p.R, p.error_word);
+    const int tiles = min(p.entries, load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, p.tile_rows, tab,
+                                                   false, 0, p.R, p.error_word));
     if (threadIdx.x == 0) *p.tiles = tiles;
     for (int t = threadIdx.x; t < tiles; t += blockDim.x) {
         const int k = find_segment(tab.tile, p.nbins, t);
@@ -74,13 +74,13 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
     const int cols = dy ? p.N : p.K, fan = dy ? 1 : p.fan;
     const bool vec = dy ? p.dy_vec : p.x_vec;
     if (dst != nullptr) {
-        const int64_t rows = int64_t(units) * pad;
+        const int64_t rows = min(int64_t(units) * pad, p.rows);
         for (int64_t q = first; q < rows; q += step) {
             const int k = find_segment(tab.tile, p.nbins, int(q / pad));
             const int local = int(q - int64_t(tab.tile[k]) * pad);
             uint16_t *to = dst + q * dst_ld;
             int row = -1;
-            if (local < tab.count[k]) row = checked_token(p.sorted[tab.start[k] + local], p.R, p.error_word);
+            if (local < tab.count[k]) row = expert_row(p, tab.start[k] + local);
             if (row >= 0) copy_row(to, src + int64_t(row / fan) * src_ld, cols, vec);
             else clear_row(to, dst_ld);
             if (dy && p.from != nullptr && lane == 0) p.from[q] = row;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
         const bool none = *p.no_lora != 0;
         const int rest = none ? p.R : (tab.id[0] == -1 ? tab.count[0] : 0);
         for (int64_t i = first; i < rest; i += step) {
-            const int row = none ? int(i) : checked_token(p.sorted[i], p.R, p.error_word);
+            const int row = none ? int(i) : expert_row(p, int(i));
             if (row < 0) continue;
             uint16_t *to = p.dx + int64_t(row) * p.dx_ld;
             if (p.dx_vec) {
@@ -129,7 +129,7 @@ static int64_t up256(int64_t v) { return (v + 255) & ~int64_t(255); }
 // Offsets in the workspace, in bytes.
 struct ExpertLayout {
     int64_t tiles, table, blocks, from, xs, dys, part, w, bytes;
-    int64_t rows;                     // of the copies
+    int64_t rows, entries;            // of the copies and of the table
 };
 
 // Rows of a tile of the forward product, by how many rows an expert has on
@@ -181,7 +181,8 @@ static ExpertLayout expert_layout(int64_t R, int fan, int64_t K, int64_t N, int6
     int64_t at = 256;
     l.tiles = 0;
     l.table = at;
-    at += up256((R / EX_LEAST_TILE + active) * int64_t(sizeof(ExpertTile)));
+    l.entries = R / EX_LEAST_TILE + active;
+    at += up256(l.entries * int64_t(sizeof(ExpertTile)));
     l.blocks = at;
     at += dw ? up256(E * 8) : 0;
     l.from = at;
@@ -246,9 +247,9 @@ static int fill(ExpertArgs &p, int32_t R, int32_t fan, int32_t K, int32_t N, con
     return LORA_OK;
 }
 
-static int launch_pack(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+static int launch_pack(const ExpertArgs &p, cudaStream_t st)
 {
-    const int64_t want = (rows + EX_PACK_THREADS / 32 - 1) / (EX_PACK_THREADS / 32);
+    const int64_t want = (p.rows + EX_PACK_THREADS / 32 - 1) / (EX_PACK_THREADS / 32);
     const int64_t most = 6ll * device_sm_count();
     const dim3 grid(unsigned(1 + (want < most ? (want > 0 ? want : 1) : most)), p.dys != nullptr && !p.later ? 2 : 1);
     return int(launch_kernel(expert_pack_kernel, grid, dim3(EX_PACK_THREADS),
@@ -291,21 +292,23 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     p.y = y;
     p.y_ld = y_ld;
     p.add = add_inputs != 0;
+    p.rows = lay.rows;
+    p.entries = int32_t(lay.entries);
     p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
     p.table = reinterpret_cast<ExpertTile *>(ws + lay.table);
     p.xs = reinterpret_cast<uint16_t *>(ws + lay.xs);
     if (!pairs && expert_stream_gathers(p)) {
         p.table = nullptr;
-        return launch_expert_stream(p, lay.rows, st);
+        return launch_expert_stream(p, st);
     }
-    if (int e = launch_pack(p, lay.rows, st)) return e;
-    if (!pairs) return launch_expert_stream(p, lay.rows, st);
+    if (int e = launch_pack(p, st)) return e;
+    if (!pairs) return launch_expert_stream(p, st);
     if (decode) {
         uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
         if (int e = launch_expert_decode(p, w, st)) return e;
         p.w = w;
     }
-    return launch_expert_forward(p, lay.rows, st);
+    return launch_expert_forward(p, st);
 }
 
 LORA_API int64_t lora_expert_linear_backward_workspace(int32_t num_rows, int32_t fan_out, int32_t hidden,
@@ -354,6 +357,8 @@ LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, i
     p.dx_vec = (bits(dx) & 15u) == 0 && dx_ld % 8 == 0;
     p.dw = d_weight;
     p.add = add_inputs != 0;
+    p.rows = lay.rows;
+    p.entries = int32_t(lay.entries);
     p.tiles = reinterpret_cast<int32_t *>(ws + lay.tiles);
     p.tile_rows = pair_tile(num_rows, p.E, hidden);
     p.table = hx ? reinterpret_cast<ExpertTile *>(ws + lay.table) : nullptr;
@@ -365,16 +370,16 @@ LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, i
     p.later = hx && hw;
     p.copied = p.later ? p.tiles + 1 : nullptr;
     p.from = p.later ? reinterpret_cast<int32_t *>(ws + lay.from) : nullptr;
-    if (int e = launch_pack(p, lay.rows, st)) return e;
+    if (int e = launch_pack(p, st)) return e;
     if (hx) {
         if (decode) {
             uint16_t *w = reinterpret_cast<uint16_t *>(ws + lay.w);
             if (int e = launch_expert_decode(p, w, st)) return e;
             p.w = w;
         }
-        if (int e = launch_expert_dx(p, lay.rows, st)) return e;
+        if (int e = launch_expert_dx(p, st)) return e;
     }
-    if (hw) return launch_expert_dw(p, lay.rows, st);
+    if (hw) return launch_expert_dw(p, st);
     if (fan_out == 1) return LORA_OK;
     const int64_t tokens = num_rows / fan_out, want = (tokens + 7) / 8, most = 8ll * device_sm_count();
     return int(launch_kernel(expert_join_kernel, dim3(unsigned(want < most ? want : most)), dim3(256), 0, st, p));

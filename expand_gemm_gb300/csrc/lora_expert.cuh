@@ -51,11 +51,22 @@ struct ExpertArgs {
     int32_t *copied;                  // [1]: padded blocks of the copies, beside it
     int2 *blocks;                     // [E]: first K block and K blocks of dW
     int32_t R, fan, K, N, E, nbins;
+    int64_t rows;                     // that the copies have room for
+    int32_t entries;                  // that the table has room for
     int32_t add, pad, tile_rows;
     int32_t x_vec, dy_vec, dx_vec;
     const int32_t *ids, *sorted, *counts, *start_loc, *active, *no_lora;
     int32_t *error_word;
 };
+
+// The row that the metadata names at `at`, -1 where that is none of the batch's
+// (metadata that were prepared for more rows than the call has).
+__device__ __forceinline__ int expert_row(const ExpertArgs &p, int at)
+{
+    if (at >= p.R) return -1;
+    const int row = checked_token(p.sorted[at], p.R, p.error_word);
+    return row < p.R ? row : -1;
+}
 
 // One row of `cols` bf16, by a warp.  Whole 16-byte pieces where both ends
 // allow it.
@@ -165,14 +176,14 @@ __device__ __forceinline__ void join_rows(const ExpertArgs &p, int64_t warp, int
 int expert_shared_memory(const void *kernel, int bytes, std::atomic<uint64_t> &done);
 
 // lora_expert_gemm.cu: products on CTA pairs over the copies.
-int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st);
-int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st);
-int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st);
+int launch_expert_forward(const ExpertArgs &p, cudaStream_t st);
+int launch_expert_dx(const ExpertArgs &p, cudaStream_t st);
+int launch_expert_dw(const ExpertArgs &p, cudaStream_t st);
 
 // lora_expert_stream.cu: few rows an expert, weights in either form.  Where it
 // gathers it needs no copy of x and no table (p.table is null).
 bool expert_stream_gathers(const ExpertArgs &p);
-int launch_expert_stream(const ExpertArgs &p, int64_t rows, cudaStream_t st);
+int launch_expert_stream(const ExpertArgs &p, cudaStream_t st);
 
 // lora_mxfp4.cu: the weights of the experts that have rows, decoded to bf16.
 int launch_expert_decode(const ExpertArgs &p, uint16_t *out, cudaStream_t st);

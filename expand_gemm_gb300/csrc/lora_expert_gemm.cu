@@ -93,7 +93,7 @@ __device__ __forceinline__ void expert_product(const ExpertGemm &g)
             tmem_ld16_nowait(tmem + c, v);
             int mine = -1, row[16];
             if (lane < 16 && c + lane < it.valid)
-                mine = checked_token(p.sorted[it.start + c + lane], p.R, p.error_word);
+                mine = expert_row(p, it.start + c + lane);
 #pragma unroll
             for (int j = 0; j < 16; ++j) row[j] = __shfl_sync(0xffffffffu, mine, j);
             tmem_wait_ld();
@@ -177,37 +177,37 @@ static int run_pairs(Kern kernel, std::atomic<uint64_t> &done, const ExpertGemm 
     return int(launch_pair_kernel(kernel, pairs, st, g, threads, smem));
 }
 
-int launch_expert_forward(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+int launch_expert_forward(const ExpertArgs &p, cudaStream_t st)
 {
     ExpertGemm g;
     g.p = p;
     if (!encode_stack_map(&g.a, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_HALF) ||
-        !encode_tile_map(&g.b, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_HALF,
+        !encode_tile_map(&g.b, p.xs, uint64_t(p.rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_HALF,
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
     return run_pairs(expert_forward_kernel, done, g, PG_SMEM, PG_THREADS, st);
 }
 
-int launch_expert_dx(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+int launch_expert_dx(const ExpertArgs &p, cudaStream_t st)
 {
     ExpertGemm g;
     g.p = p;
     if (!encode_stack_map(&g.a, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), PG_BK, PG_BK) ||
-        !encode_tile_map(&g.b, p.dys, uint64_t(rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_HALF,
+        !encode_tile_map(&g.b, p.dys, uint64_t(p.rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_HALF,
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};
     return run_pairs(expert_dx_kernel, done, g, PG_SMEM, PG_THREADS + EX_SIDE * 32, st);
 }
 
-int launch_expert_dw(const ExpertArgs &p, int64_t rows, cudaStream_t st)
+int launch_expert_dw(const ExpertArgs &p, cudaStream_t st)
 {
     ExpertGemm g;
     g.p = p;
-    if (!encode_tile_map(&g.a, p.dys, uint64_t(rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_BK,
+    if (!encode_tile_map(&g.a, p.dys, uint64_t(p.rows), uint64_t(p.N), uint64_t(p.dys_ld), PG_BK, PG_BK,
                          CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tile_map(&g.b, p.xs, uint64_t(rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_BK,
+        !encode_tile_map(&g.b, p.xs, uint64_t(p.rows), uint64_t(p.K), uint64_t(p.K), PG_BK, PG_BK,
                          CU_TENSOR_MAP_SWIZZLE_128B))
         return LORA_ERR_DEVICE;
     static std::atomic<uint64_t> done{0};

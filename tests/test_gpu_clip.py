@@ -238,3 +238,18 @@ def test_refusals():
         eg.lora_clip_gradients([a], 1.0, norms.double())
     with pytest.raises(ValueError):
         eg.lora_clip_gradients(eg.LoRAGradients.make([a], 2), 1.0, torch.zeros(3, device="cuda"))
+
+
+def test_overlapping_tensors_are_refused():
+    flat, other = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    norms = torch.zeros(1, device="cuda")
+    for bad in ([flat[:20], flat[19:40]], [flat, flat], [flat[:32], flat[8:16]]):
+        with pytest.raises(ValueError, match="overlaps"):
+            eg.lora_clip_gradients(bad, 1.0, norms)
+    for grads, out in (([flat[:16]], [flat[8:24]]), ([flat[:16], flat[16:32]], [other[:16], other[8:24]]),
+                       ([flat[:16], flat[16:32]], [flat[16:32], other[:16]])):
+        with pytest.raises(ValueError, match="overlaps"):
+            eg.LoRAGradients.make(grads, 1, out=out)
+    # read by two, written by none, and one's own place
+    eg.LoRAGradients.make([flat[:16], flat[8:24]], 1, out=[other[:16], other[16:32]])
+    eg.LoRAGradients.make([flat[:16], flat[16:32]], 1, out=[flat[:16], other[:16]])

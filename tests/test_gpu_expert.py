@@ -404,3 +404,206 @@ def test_adapters_over_experts():
     eg.lora_linear_backward(dy, x, buffer, [A], [B], 0.5, adapters, dx=dx, d_lora_a=[dA], d_lora_b=[dB])
     none = lora < 0
     assert torch.equal(dx[none], base[none]) and not torch.equal(dx, base)
+
+
+# ------------------------------------------------------------ borders between kernels, large sizes, odd calls
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("rows", [11, 12, 13, 31, 32, 33, 64])
+@pytest.mark.parametrize("experts", [1, 3, 256, 257])
+def test_forward_where_the_kernels_change(rows, experts, four):
+    """Batches of up to 12 and 32 rows, and up to 256 experts, take no copy of x."""
+    check_forward((rows, 1, experts, 544, 150, 0.1), four, seed=rows)
+
+
+@pytest.mark.parametrize("mean", [12, 13, 32, 33, 96, 97, 128, 129])
+@pytest.mark.parametrize("four", [False, True])
+def test_forward_by_rows_an_expert(mean, four):
+    check_forward((3 * mean, 1, 3, 96, 140, 0.0), four)
+
+
+@pytest.mark.parametrize("tokens", [1024, 1025])
+def test_forward_of_4_bits_where_weights_are_decoded_first(tokens):
+    check_forward((tokens, 1, 1, 64, 300, 0.1), True)
+
+
+@pytest.mark.parametrize("width", [127, 128, 129, 4 * 128, 19 * 128, 38 * 128 + 1, 76 * 128 + 1])
+@pytest.mark.parametrize("four", [False, True])
+def test_clusters_that_share_a_tile(width, four):
+    """Few tiles: a cluster of four, two or one CTA each; sums of K in several parts, some of them empty."""
+    for hidden in (32, 64, 96, 288, 1056):
+        check_forward((2, 1, 1, hidden, width, 0.0), four)
+
+
+def test_rows_of_x_off_a_16_byte_boundary_in_a_small_batch():
+    ids, x, _, w, _ = inputs(5, 2, 3, 64, 40, 0.0)
+    wide = torch.zeros(5, 67, device="cuda").bfloat16()
+    wide[:, 1:65] = x
+    y = torch.zeros(10, 40, device="cuda").bfloat16()
+    eg.lora_expert_linear(wide[:, 1:65], w, y, meta_of(ids, 3))
+    want, sums = ref.forward(x, w, ids, 2)
+    ref.within(y, want, ref.bound(want, sums, 64), "y")
+
+
+def test_products_with_the_smallest_scales():
+    """Scales down to 2^-127, whose elements are subnormal in bf16, times large rows."""
+    codes = torch.randint(0, 256, (1, 40, 16), dtype=torch.uint8, device="cuda")
+    scales = (torch.arange(40, dtype=torch.int32) // 2).to(torch.uint8).view(1, 40, 1).cuda()
+    for rows in (3, 40):
+        ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+        x = (torch.randint(-3, 4, (rows, 32), device="cuda").float() * 2.0 ** 110).bfloat16()
+        y = torch.zeros(rows, 40, device="cuda").bfloat16()
+        eg.lora_expert_linear(x, codes, y, meta_of(ids, 1), weight_scale=scales)
+        want, sums = ref.forward(x, ref.decode(codes, scales), ids, 1)
+        ref.within(y, want, ref.bound(want, sums, 32), "y")
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_weights_beyond_32_bit_offsets(four):
+    """The last expert of a stack of more than 2^31 weights, and with few rows and many."""
+    experts, width, hidden = 3, 90000, 8192
+    w = torch.zeros(experts, width, hidden // 2 if four else hidden, dtype=torch.uint8 if four else torch.bfloat16,
+                    device="cuda")
+    last = torch.randn(257, hidden, device="cuda").bfloat16() * 0.01
+    scale = None
+    if four:
+        codes, scales = ref.encode(last)
+        scale = torch.full((experts, width, hidden // 32), 127, dtype=torch.uint8, device="cuda")
+        w[2, -257:], scale[2, -257:] = codes, scales
+        last = ref.decode(codes, scales)
+    else:
+        w[2, -257:] = last
+    for rows in (3, 500):
+        ids = torch.full((rows,), 2, dtype=torch.int32, device="cuda")
+        ids[0] = 0
+        x = torch.randn(rows, hidden, device="cuda").bfloat16()
+        y = torch.ones(rows, width, device="cuda").bfloat16()
+        eg.lora_expert_linear(x, w, y, meta_of(ids, experts), weight_scale=scale)
+        assert not bool(y[0].any()) and not bool(y[:, :-257].any())
+        want, sums = ref.forward(x[1:], last[None], torch.zeros_like(ids[1:]), 1)
+        ref.within(y[1:, -257:], want, ref.bound(want, sums, hidden), "y")
+        del x, y
+
+
+def test_rows_beyond_32_bit_offsets():
+    rows, width, hidden = 40000, 60000, 8                   # y has 2.4e9 values
+    ids = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    x = torch.randn(rows, hidden, device="cuda").bfloat16()
+    w = torch.randn(1, width, hidden, device="cuda").bfloat16()
+    y = torch.zeros(rows, width, device="cuda").bfloat16()
+    meta = meta_of(ids, 1)
+    eg.lora_expert_linear(x, w, y, meta)
+    for at in (slice(0, 3), slice(-300, None)):
+        want, sums = ref.forward(x[at], w, ids[at], 1)
+        ref.within(y[at], want, ref.bound(want, sums, hidden), "y")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    eg.lora_expert_linear_backward(y, x, w, meta, dx=dx, d_weight=dw)
+    want = y[-5:].double() @ w[0].double()
+    size = y[-5:].double().abs() @ w[0].double().abs()
+    ref.within(dx[-5:], want, ref.bound(want, size, width), "dx")
+    want, size = y[:, -40:].double().T @ x.double(), y[:, -40:].double().abs().T @ x.double().abs()
+    ref.within(dw[0, -40:], want, ref.bound(want, size, rows), "dw")
+
+
+def test_two_calls_at_once():
+    """On two streams, with workspaces of their own and metadata in common."""
+    sets = []
+    ids, *_ = inputs(300, 2, 6, 128, 200, 0.1)
+    meta = meta_of(ids, 6)
+    for seed in (1, 2):
+        _, x, _, w, dy = inputs(300, 2, 6, 128, 200, 0.1, seed=seed)
+        sets.append(dict(x=x, w=w, dy=dy, y=torch.zeros_like(dy), dx=torch.empty_like(x), dw=torch.empty_like(w),
+                         stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in sets:
+            with torch.cuda.stream(s["stream"]):
+                eg.lora_expert_linear(s["x"], s["w"], s["y"], meta)
+                eg.lora_expert_linear_backward(s["dy"], s["x"], s["w"], meta, dx=s["dx"], d_weight=s["dw"])
+    torch.cuda.synchronize()
+    for s in sets:
+        want, sums = ref.forward(s["x"], s["w"], ids, 2)
+        ref.within(s["y"], want, ref.bound(want, sums, 128), "y")
+        rx, rw, sx, sw = ref.backward(s["dy"], s["x"], s["w"], ids, 2)
+        ref.within(s["dx"], rx, ref.bound(rx, sx, 202), "dx")
+        ref.within(s["dw"], rw, ref.bound(rw, sw, 600), "dw")
+
+
+@pytest.mark.parametrize("rows", [6, 200])
+def test_metadata_of_a_larger_batch_write_nothing_beyond_the_call_s_rows(rows):
+    """Not a documented call; rows that the call does not have are left out."""
+    ids, x, _, w, dy = inputs(3 * rows, 1, 4, 64, 48, 0.0)
+    meta = meta_of(ids, 4)
+    flat = torch.zeros(3 * rows, 48, device="cuda").bfloat16()
+    eg.lora_expert_linear(x[:rows], w, flat[:rows], meta)
+    assert not bool(flat[rows:].any())
+    full, dw = torch.zeros(3 * rows, 64, device="cuda").bfloat16(), torch.empty_like(w)
+    need = eg.lora_expert_linear_backward_workspace(rows, 64, 48, 4, weight_grad=True)
+    ws = torch.full((need + 65536,), 7, dtype=torch.uint8, device="cuda")
+    eg.lora_expert_linear_backward(dy[:rows], x[:rows], w, meta, dx=full[:rows], d_weight=dw, workspace=ws[:need])
+    assert not bool(full[rows:].any()) and bool((ws[need:] == 7).all())
+
+
+def test_refusals():
+    ids, x, _, w, dy = inputs(8, 2, 3, 64, 48, 0.0)
+    meta = meta_of(ids, 3)
+    y = torch.zeros(16, 48, device="cuda").bfloat16()
+    codes, scales = ref.encode(w)
+    ok = dict(x=x, weight=w, y=y, meta=meta)
+    four = dict(ok, weight=codes, weight_scale=scales)
+    for bad, error in (
+            (dict(ok, x=x.float()), TypeError), (dict(ok, x=None), TypeError), (dict(ok, x=x.cpu()), (TypeError, ValueError)),
+            (dict(ok, y=y.cpu()), (TypeError, ValueError)), (dict(ok, weight=w.half()), TypeError),
+            (dict(ok, weight=None), TypeError), (dict(ok, weight=w[:2]), ValueError), (dict(ok, weight=w[0]), ValueError),
+            (dict(ok, weight=w.transpose(1, 2)), ValueError), (dict(ok, y=y[:15]), ValueError),
+            (dict(ok, y=y[:, :40]), ValueError), (dict(ok, y=y[:0]), ValueError), (dict(ok, x=x[:0]), ValueError),
+            (dict(ok, x=x.t()), ValueError), (dict(ok, weight=codes), TypeError), (dict(four, weight=w), TypeError),
+            (dict(four, weight_scale=scales[:, :, :1]), ValueError), (dict(four, weight=codes[:, :, :16]), ValueError),
+            (dict(ok, workspace=torch.zeros(1 << 20, device="cuda")), TypeError),
+            (dict(ok, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")), ValueError),
+            (dict(ok, x=x, y=x, weight=torch.zeros(3, 64, 64, device="cuda").bfloat16()), ValueError)):
+        with pytest.raises(error):
+            eg.lora_expert_linear(**bad)
+    with pytest.raises(eg.LoraError):
+        eg.lora_expert_linear(x[:, :60], w[:, :, :60].contiguous(), y, meta)
+    assert not bool(y.any())
+    ok = dict(dy=dy, x=x, weight=w, meta=meta)
+    for bad, error in (
+            (dict(ok, dy=dy[:, :40]), ValueError), (dict(ok, dy=None), TypeError), (dict(ok, dx=x), ValueError),
+            (dict(ok, dx=torch.zeros(8, 72, device="cuda").bfloat16()), ValueError),
+            (dict(ok, dx=torch.zeros(8, 64, device="cuda")), TypeError),
+            (dict(ok, d_weight=torch.zeros(3, 48, 72, device="cuda").bfloat16()), ValueError),
+            (dict(ok, d_weight=w.transpose(1, 2)), ValueError), (dict(ok, d_weight=w.float()), TypeError)):
+        with pytest.raises(error):
+            eg.lora_expert_linear_backward(**bad)
+
+
+@pytest.mark.parametrize("rows, experts, width, hidden", [(20, 3, 20000, 8192), (200, 3, 20000, 8192), (500, 3, 20000, 8192),
+                                                          (900, 1, 20000, 2048), (10, 3, 20000, 8192)], ids=str)
+@pytest.mark.parametrize("four", [False, True])
+def test_long_runs_of_stages_repeat(rows, experts, width, hidden, four):
+    """Hundreds of thousands of stages through the rings: every call gives the same bits, and the right ones."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(0, experts, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn(rows, hidden, generator=g, device="cuda").bfloat16()
+    scale = None
+    if four:
+        w = torch.randint(0, 256, (experts, width, hidden // 2), generator=g, device="cuda", dtype=torch.uint8)
+        scale = torch.randint(115, 125, (experts, width, hidden // 32), generator=g, device="cuda", dtype=torch.uint8)
+    else:
+        w = (torch.randn(experts, width, hidden, generator=g, device="cuda") * 0.02).bfloat16()
+    meta = meta_of(ids, experts)
+    first = None
+    for _ in range(20):
+        y = torch.zeros(rows, width, device="cuda").bfloat16()
+        eg.lora_expert_linear(x, w, y, meta, weight_scale=scale)
+        if first is None:
+            first = y
+            for e in range(experts):
+                at = (ids == e).nonzero()[:, 0]
+                we = (ref.decode(w[e], scale[e]) if four else w[e].double())
+                want, size = x[at].double() @ we.T, x[at].double().abs() @ we.abs().T
+                ref.within(y[at], want, ref.bound(want, size, hidden), "y")
+        else:
+            assert torch.equal(y, first)
+    assert int(meta.error_word) == 0
