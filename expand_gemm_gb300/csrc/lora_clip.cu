@@ -119,15 +119,19 @@ __device__ __forceinline__ void clip_add(const float (&v)[8], float &acc, double
     }
 }
 
-__device__ __forceinline__ double block_sum(double v, double *warps)
+// The block's sum in thread 0.  One warp adds: fp64 runs at two additions a
+// clock on an SM, and 512 threads' shuffles are 2560 of them.
+__device__ __forceinline__ double block_sum(double v, double *all)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = v;
+    all[threadIdx.x] = v;
     __syncthreads();
     double s = 0.0;
-    for (int w = 0; w < CL_THREADS / 32; ++w) s += warps[w];
+    if (threadIdx.x < 32) {
+        for (int i = threadIdx.x; i < CL_THREADS; i += 32) s += all[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
     return s;
 }
 
@@ -161,7 +165,7 @@ __device__ __forceinline__ float clip_load(const char *p, bool f32, int i)
 template <int MAX>
 __global__ void __launch_bounds__(CL_THREADS, 3) clip_sum_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
-    __shared__ double s_warps[CL_THREADS / 32];
+    __shared__ double s_all[CL_THREADS];
     pdl_wait();
     double far = 0.0;
     for (ClipWalk<MAX> w(a, false); w.left > 0;) {
@@ -201,15 +205,36 @@ __global__ void __launch_bounds__(CL_THREADS, 3) clip_sum_kernel(const __grid_co
         const int group = w.group;
         w.next(a);
         if (w.left == 0 || w.group != group) {
-            const double s = block_sum(far, s_warps);
+            const double s = block_sum(far, s_all);
             if (threadIdx.x == 0) a.s.part[blockIdx.x + group] = s;
             far = 0.0;
         }
     }
 }
 
+// What the gradients of a group with this norm are multiplied by, of the norm
+// in 64 bits: it may lie beyond fp32.  A zero gradient stays one; NaN stays NaN.
+__device__ __forceinline__ float clip_factor(const ClipShared &a, double norm)
+{
+    if (!a.scale) return 1.0f;
+    const float f = float(double(a.max_norm) / (norm + double(a.eps)));
+    return f >= 1.0f || norm == 0.0 ? 1.0f : f;
+}
+
+// The partial sums of a group, by a warp, in an order that depends on their
+// number alone.
+__device__ __forceinline__ double clip_group_sum(const ClipShared &a, int g, int from, int to)
+{
+    double s = 0.0;
+    for (int c = from + int(threadIdx.x & 31); c <= to; c += 32) s += a.part[c + g];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
 // The partial sums of a group, in order; its norm and factor.  One warp a
-// group.
+// group.  (Where one launch holds all tensors and the gradients are written,
+// clip_scale_kernel does this itself.)
 __global__ void __launch_bounds__(256) clip_join_kernel(const ClipShared a)
 {
     pdl_wait();
@@ -217,32 +242,49 @@ __global__ void __launch_bounds__(256) clip_join_kernel(const ClipShared a)
     for (int g = blockIdx.x * 8 + (threadIdx.x >> 5); g < a.groups; g += gridDim.x * 8) {
         const int64_t first = int64_t(g) * a.units, last = first + a.units;
         const int from = int(first / a.run), to = int((last - 1) / a.run);
-        double s = 0.0;
-        for (int c = from + lane; c <= to; c += 32) s += a.part[c + g];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        double s = clip_group_sum(a, g, from, to);
         if (lane == 0) {
             if (a.add) s += a.sum[g];
             const double norm = sqrt(s);
             a.sum[g] = s;
             a.norms[g] = float(norm);
-            // of the norm in 64 bits: it may lie beyond fp32.  A zero gradient
-            // stays one; NaN stays NaN.
-            const float f = float(double(a.max_norm) / (norm + double(a.eps)));
-            a.factor[g] = f >= 1.0f || norm == 0.0 ? 1.0f : f;
+            a.factor[g] = clip_factor(a, norm);
         }
     }
 }
 
 // out = v * factor.  Units are taken from the last one back: the end of what
-// the norm read may still lie in L2.
-template <int MAX>
+// the norm read may still lie in L2.  JOIN: every CTA adds up the partial sums
+// of its groups, which saves a launch (one layer's adapters: 12 -> 9 us); the
+// one with a group's first unit writes its norm.
+template <int MAX, bool JOIN>
 __global__ void __launch_bounds__(CL_THREADS, 3) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
+    __shared__ float s_factor;
     pdl_wait();
+    int known = -1;
+    float f = 1.0f;
     for (ClipWalk<MAX> w(a, true); w.left > 0; w.back(a)) {
         const ClipUnit c = clip_unit(a, w);
-        const float f = a.s.scale ? a.s.factor[w.group] : 1.0f;
+        if (w.group != known) {
+            known = w.group;
+            if constexpr (JOIN) {
+                const int64_t first = int64_t(known) * a.s.units;
+                const int from = int(first / a.s.run), to = int((first + a.s.units - 1) / a.s.run);
+                __syncthreads();
+                if (threadIdx.x < 32) {
+                    const double norm = sqrt(clip_group_sum(a.s, known, from, to));
+                    if (threadIdx.x == 0) {
+                        if (int(blockIdx.x) == from) a.s.norms[known] = float(norm);
+                        s_factor = clip_factor(a.s, norm);
+                    }
+                }
+                __syncthreads();
+                f = s_factor;
+            } else {
+                f = a.s.factor[known];
+            }
+        }
         if (f == 1.0f && c.in == c.out) continue;
         const int size = c.f32 ? 4 : 2, per = 16 / size;
         const bool same = ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
@@ -333,6 +375,7 @@ static int clip_args(ClipArgs<MAX> &a, const ClipCall &c, int first, int most)
 template <int MAX>
 static int run_clip(const ClipCall &c, int most, cudaStream_t st)
 {
+    const bool write = c.s.scale || c.out != nullptr, join = !write || c.tensors > MAX;
     bool any = false;
     ClipArgs<MAX> a;
     for (int first = 0; first < c.tensors; first += MAX) {
@@ -342,16 +385,18 @@ static int run_clip(const ClipCall &c, int most, cudaStream_t st)
         any = true;
         cudaError_t e = launch_kernel(clip_sum_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
         if (e != cudaSuccess) return int(e);
+        if (!join) continue;
         const int joins = (c.s.groups + 7) / 8 < 64 ? (c.s.groups + 7) / 8 : 64;
         e = launch_kernel(clip_join_kernel, dim3(unsigned(joins)), dim3(256), 0, st, a.s);
         if (e != cudaSuccess) return int(e);
     }
     if (!any) return int(cudaMemsetAsync(c.s.norms, 0, size_t(c.s.groups) * sizeof(float), st));
-    if (!c.s.scale && c.out == nullptr) return LORA_OK;
+    if (!write) return LORA_OK;
+    const auto scale = join ? clip_scale_kernel<MAX, false> : clip_scale_kernel<MAX, true>;
     for (int first = 0; first < c.tensors; first += MAX) {
         const int ctas = clip_args(a, c, first, most);
         if (ctas == 0) continue;
-        const cudaError_t e = launch_kernel(clip_scale_kernel<MAX>, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
+        const cudaError_t e = launch_kernel(scale, dim3(unsigned(ctas)), dim3(CL_THREADS), 0, st, a);
         if (e != cudaSuccess) return int(e);
     }
     return LORA_OK;
@@ -378,7 +423,7 @@ LORA_API int lora_clip_gradients(const void *const *grads, void *const *out, con
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return LORA_ERR_ALIGN;
     int64_t elements = 0;
     for (int i = 0; i < num_tensors; ++i) {
-        if (slice_sizes[i] < 0) return LORA_ERR_SIZE;
+        if (slice_sizes[i] < 0 || slice_sizes[i] > INT64_MAX / 16) return LORA_ERR_SIZE;
         elements += slice_sizes[i];
         if (elements > INT64_MAX / 8 / groups || clip_units(elements, CL_UNIT_LOG) + num_tensors > INT32_MAX)
             return LORA_ERR_SIZE;
