@@ -2,7 +2,7 @@
 frozen linear layers and a frozen head, tokens of all adapters mixed in one
 batch, as they are when the adapters are served.
 
-    python examples/train_adapters.py [--steps 40] [--device cuda]
+    python examples/train_adapters.py [--steps 40] [--four] [--clip 1.0] [--device cuda]
 
 A step is one pass of the library's own calls:
 
@@ -13,9 +13,12 @@ A step is one pass of the library's own calls:
     lora_orthogonalize     the momentum of all adapters made orthogonal
                            (the update of the Muon optimiser)
 
-The frozen products are torch matmuls.  Workspaces and buffers are allocated
-once.  The data are random: every adapter learns its own map from 512 inputs
-to labels.
+The frozen products are torch matmuls; with --four the frozen layers are held
+in 4 bits (lora_quantize_mxfp4) and their products and gradients are the
+library's too (lora_expert_linear and its backward, one expert).  With --clip
+each adapter's gradients, of all layers together, are scaled down to that norm
+(lora_clip_gradients).  Workspaces and buffers are allocated once.  The data are
+random: every adapter learns its own map from 512 inputs to labels.
 """
 import argparse
 import os
@@ -31,11 +34,24 @@ import expand_gemm_gb300 as eg
 class Layer:
     """A frozen linear layer of size hidden x hidden with stacked adapters."""
 
-    def __init__(self, hidden, rank, loras, scale, tokens, device, gen):
+    def __init__(self, hidden, rank, loras, scale, tokens, device, gen, four=False):
         bf16 = dict(dtype=torch.bfloat16, device=device)
         f32 = dict(dtype=torch.float32, device=device)
         self.scale = scale
         self.base = (torch.randn(hidden, hidden, generator=gen) * hidden ** -0.5).to(**bf16)
+        self.four = four
+        if four:
+            u8 = dict(dtype=torch.uint8, device=device)
+            self.codes = torch.empty(1, hidden, hidden // 2, **u8)
+            self.scales = torch.empty(1, hidden, hidden // 32, **u8)
+            eg.lora_quantize_mxfp4(self.base[None].contiguous(), self.codes, self.scales)
+            # every token goes to the one expert
+            self.one = eg.LoRAKernelMeta.make(1, tokens, device)
+            self.one.prepare_tensors(torch.zeros(tokens, dtype=torch.int32, device=device))
+            sizes = (tokens, hidden, hidden, 1)
+            self.workspace = torch.empty(max(
+                eg.lora_expert_linear_workspace(*sizes, quantized=True, device=device),
+                eg.lora_expert_linear_backward_workspace(*sizes, quantized=True, device=device)), **u8)
         # masters in fp32, what the kernels read in bf16; B starts at zero
         self.masters = [(torch.randn(loras, rank, hidden, generator=gen) * hidden ** -0.5).to(**f32),
                         torch.zeros(loras, hidden, rank, **f32)]
@@ -47,7 +63,12 @@ class Layer:
 
     def forward(self, x, meta):
         self.x = x
-        y = x + x @ self.base.T
+        if self.four:
+            y = x.clone()
+            eg.lora_expert_linear(x, self.codes, y, self.one, weight_scale=self.scales, add_inputs=True,
+                                  workspace=self.workspace)
+        else:
+            y = x + x @ self.base.T
         self.buffer.zero_()
         eg.add_lora_linear(y, x, [self.weights[0]], [self.weights[1]], None, self.scale, [y.shape[1]], meta,
                            buffer=self.buffer)
@@ -55,7 +76,12 @@ class Layer:
 
     def backward(self, dy, meta, workspace):
         """The adapters' gradients; returns the gradient of the input."""
-        dx = dy + dy @ self.base
+        if self.four:
+            dx = dy.clone()
+            eg.lora_expert_linear_backward(dy, self.x, self.codes, self.one, weight_scale=self.scales, dx=dx,
+                                           add_inputs=True, workspace=self.workspace)
+        else:
+            dx = dy + dy @ self.base
         eg.lora_linear_backward(dy, self.x, self.buffer, [self.weights[0]], [self.weights[1]], self.scale, meta,
                                 dx=dx, d_lora_a=[self.grads[0]], d_lora_b=[self.grads[1]], workspace=workspace)
         return dx
@@ -71,7 +97,7 @@ class Layer:
 
 
 def train(steps=40, tokens=512, hidden=512, vocab=2000, rank=16, loras=4, scale=2.0, lr=0.05, beta=0.9, device="cuda",
-          seed=0):
+          seed=0, four=False, clip=None):
     """The mean loss of every step."""
     gen = torch.Generator().manual_seed(seed)
     ids = torch.randint(0, loras, (tokens,), generator=gen, dtype=torch.int32).to(device)
@@ -82,7 +108,9 @@ def train(steps=40, tokens=512, hidden=512, vocab=2000, rank=16, loras=4, scale=
     learnt = int((targets >= 0).sum())
     targets = targets.to(device)
     weight = torch.full((tokens,), 1.0 / learnt, device=device)
-    layers = [Layer(hidden, rank, loras, scale, tokens, device, gen) for _ in range(2)]
+    layers = [Layer(hidden, rank, loras, scale, tokens, device, gen, four) for _ in range(2)]
+    gradients = eg.LoRAGradients.make([g for layer in layers for g in layer.grads], loras)
+    norms = torch.empty(loras, device=device)
     meta = eg.LoRAKernelMeta.make(loras, tokens, device)
     loss = torch.empty(tokens, device=device)
     dh = torch.empty_like(x)
@@ -101,6 +129,8 @@ def train(steps=40, tokens=512, hidden=512, vocab=2000, rank=16, loras=4, scale=
         grad = dh
         for layer in reversed(layers):
             grad = layer.backward(grad, meta, back_ws)
+        if clip is not None:
+            eg.lora_clip_gradients(gradients, clip, norms)
         for layer in layers:
             layer.update(lr * (1.0 - step / steps), beta)
     return history.tolist()
@@ -109,9 +139,11 @@ def train(steps=40, tokens=512, hidden=512, vocab=2000, rank=16, loras=4, scale=
 def main():
     parser = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     parser.add_argument("--steps", type=int, default=40)
+    parser.add_argument("--four", action="store_true", help="hold the frozen layers in 4 bits")
+    parser.add_argument("--clip", type=float, default=None, help="largest norm of an adapter's gradients")
     parser.add_argument("--device", default="cuda")
     args = parser.parse_args()
-    for step, loss in enumerate(train(args.steps, device=args.device)):
+    for step, loss in enumerate(train(args.steps, device=args.device, four=args.four, clip=args.clip)):
         print("step %3d  loss %.4f" % (step, loss))
 
 
