@@ -134,33 +134,38 @@ struct ExpertLayout {
 
 // Rows of a tile of the forward product, by how many rows an expert has on
 // average; EX_TILE: the product on CTA pairs, where 4-bit weights are decoded
-// first.  Both sides measured (us; hidden 4096, in a graph): bf16, 16 experts
-// of width 4096, 32 rows: 112.8 with tiles of 32 rows, 114.8 with 64; 64 rows:
-// 133 and 117; 128 rows: 141 with 64, 130 on pairs; one expert of width 11008,
-// 192 rows: 51 and 47.  4 bits: 4 rows (32 experts, 11008): 201 with 16, 252
-// with 64; 32 rows: 98 and 74; 64 rows: 89 with 64, 104 with 128; 256 rows
-// (8 experts, 320): 149 and 143; one expert of width 11008, 1024 rows: 124
-// with 128, 131 decoded; of width 4096, 4096 rows: 165 and 126.
+// first.  Both sides measured (us; 16 experts of 4096 x 4096 if nothing else is
+// said, in a graph).  bf16, tiles of 32 rows and pairs: 32 rows: 115 and 119;
+// 40 rows: 124 and 120; 64 rows: 138 and 121; one expert, 16 rows: 23 and 34;
+// one of width 11008, 64 rows: 51 and 44.  4 bits, tiles of 16 and of 64 rows:
+// 12 rows: 60 and 62; 16 rows: 68 and 63; 32 rows: 100 and 66.  4 bits, 64 and
+// pairs: 256 rows: 221 and 274; 375 rows: 293 and 298; 512 rows: 394 and 330;
+// one expert, 512 rows: 46 and 45; one of width 11008, 384 rows: 68 and 78,
+// 1024 rows: 136 and 107.
 static int forward_tile(int64_t R, int64_t E, bool quantized)
 {
     const int64_t mean = R / E;
-    if (!quantized) return mean <= 32 ? 32 : mean <= 96 ? 64 : EX_TILE;
-    return mean <= 12 ? 16 : mean <= 128 ? 64 : mean <= 1024 ? 128 : EX_TILE;
+    if (!quantized) return mean <= 32 ? 32 : EX_TILE;
+    return mean <= 12 ? 16 : mean <= 384 ? 64 : EX_TILE;
 }
 
-// Rows of a tile of the products on CTA pairs: what takes the pairs the least
-// time in whole rounds, if the experts have equal shares (each tile costs
-// about 16 rows more than it has).  4096 rows of one expert, 4096 to 4096: 68
-// us of products with tiles of 224 rows, 77 with 256.
+// Rows of a tile of the products on CTA pairs.  One expert: what takes the
+// pairs the least time in whole rounds, where each tile costs about 16 rows
+// more than it has (4096 rows, 4096 to 4096: 98 us with tiles of 224 rows, 104
+// with 256, 107 with 192).  Several have shares that vary, and a tile costs
+// what its rows need, so that short tiles only split experts that one tile
+// would have held (16 experts of 4096 x 4096, 128 rows on average: 139 with
+// 128, 125 with 256; 256 rows: 155 with 192, 151 with 256; 1024 rows of 8: 196
+// with 224, 195 with 256).
 static int pair_tile(int64_t R, int64_t E, int64_t cols)
 {
-    const int64_t experts = R < E ? R : E, mean = R / experts;
+    if (E > 1) return EX_TILE;
     const int64_t pairs = device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1;
     const int64_t blocks = (cols + EX_TILE - 1) / EX_TILE;
     int best = EX_TILE;
     int64_t least = INT64_MAX;
     for (int t = EX_TILE; t >= 64; t -= 32) {
-        const int64_t tiles = experts * ((mean + t - 1) / t) * blocks;
+        const int64_t tiles = (R + t - 1) / t * blocks;
         const int64_t cost = (tiles + pairs - 1) / pairs * (t + 16);
         if (cost < least) {
             least = cost;

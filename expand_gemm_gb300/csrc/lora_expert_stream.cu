@@ -21,8 +21,8 @@
 // = TMEM lane = row of W); with 4-bit weights 6..21 decode, 22 fetches scales
 // and 23 loads x, into a ring of its own: codes are done with when they are
 // decoded, x when the products have run (in one ring the decoding waited for
-// codes: 256 tokens of 16 experts 4096 x 4096 75 us in place of 66).  Two accumulators: the epilogue of one tile runs under the next
-// one's products.
+// codes: 256 tokens of 16 experts 4096 x 4096 75 us in place of 66).  Two
+// accumulators: the epilogue of one tile runs under the next one's products.
 //
 // Batches of a few rows need no copy of x: the kernel walks the metadata's
 // segments itself and gathers rows by TMA (90 clocks for four rows of 128
@@ -40,7 +40,6 @@ struct StreamArgs {
     ExpertArgs p;
     CUtensorMap w, x;
     int32_t stages;               // of the ring
-    uint32_t pitch;               // 128, see decode_block
 };
 
 constexpr int ST_ROWS = 128;                    // of W in a tile
@@ -60,29 +59,25 @@ template <bool FOUR, int NT>
 struct StreamSizes {
     static constexpr int KC = FOUR ? 256 : 64;                  // elements of K in a stage
     static constexpr int PANELS = KC / 64;                      // of x: NT rows of 64
-    static constexpr int XP = FOUR && NT < 128 ? 4 : FOUR ? 2 : 1;          // panels of x in a stage of its ring
-    static constexpr int X = XP * NT * 128;                     // their bytes
+    static constexpr int X = PANELS * NT * 128;                 // their bytes
     // a stage of the ring: W and x, or the codes and the rows' eight scales,
     // beside a ring of XS stages of x
     static constexpr int STAGE = FOUR ? ST_TILE + 1024 : ST_TILE + X;
-    static constexpr int XS = !FOUR ? 0 : NT <= 16 ? 4 : NT < 128 ? 2 : 3;
+    static constexpr int XS = !FOUR ? 0 : NT <= 16 ? 4 : 2;
     static constexpr int THREADS = 32 * (FOUR ? ST_X_WARP + 1 : ST_DEC0);
     static constexpr int BARS = 512;
     static constexpr int SUMS = NT * ST_ROWS * 4;               // bytes of one CTA's sums of a tile
-    // tiles of 128 rows have no room for the wide table, and the products
-    // bound them
-    static constexpr bool WIDE = FOUR && NT < 128;
-    static constexpr int TABLE = WIDE ? 256 * 256 : FOUR ? 256 * 128 : 0;
+    static constexpr int TABLE = FOUR ? 256 * 256 : 0;
     static constexpr int ALL = 232448;                          // shared memory of a CTA, from address 1024 on
     // stages of the ring beside that of x and the sums of parts - 1 other CTAs
     __host__ __device__ static constexpr int ring(int parts)
     {
-        const int rest = XS * X + (parts - 1) * SUMS + (WIDE ? 0 : ST_SEGMENTS);
-        const int n = WIDE ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - rest) / STAGE
-                           : (ALL - 1024 - BARS - TABLE - rest) / STAGE;
+        const int rest = XS * X + (parts - 1) * SUMS;
+        const int n = FOUR ? (ST_TABLE - 1024) / STAGE + (1024 + ALL - ST_TABLE - TABLE - rest) / STAGE
+                           : (ALL - 1024 - BARS - ST_SEGMENTS - rest) / STAGE;
         return n < ST_MAX_STAGES ? n : ST_MAX_STAGES;
     }
-    static_assert(!WIDE || (ST_TABLE - 1024) % STAGE >= ST_SEGMENTS, "the segments lie between stages and table");
+    static_assert(!FOUR || (ST_TABLE - 1024) % STAGE >= ST_SEGMENTS, "the segments lie between stages and table");
     static constexpr int COLS = FOUR ? 512 : 2 * NT < 32 ? 32 : 2 * NT;      // of TMEM
     static constexpr int DECODED = 2 * NT;                     // first TMEM column of the decoded stages
     static constexpr int BUFS = (512 - DECODED) / 128 < ST_MAX_BUFS ? (512 - DECODED) / 128 : ST_MAX_BUFS;
@@ -130,13 +125,12 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 }
 
 // A block of 32 elements with scale byte c.  `table`: shared address of this
-// lane's entries, a pair of bf16 for each byte; WIDE: a byte's are 256 bytes
-// apart and the table is aligned so that the byte is the address's second.
-// Else they are `pitch` bytes apart, which the compiler does not know (it
-// would add by shifts, on the pipe that takes the bytes apart).  Each product
-// with the scale is exact.  ENDS: c may be 0, which is subnormal, or 255, NaN.
-template <bool ENDS, bool WIDE>
-__device__ __forceinline__ void decode_block(uint32_t table, uint32_t pitch, const uint4 &w, uint32_t c, uint32_t *o)
+// lane's entries, a pair of bf16 for each byte; a byte's are 256 bytes apart
+// and the table is aligned so that the byte is the address's second.  Each
+// product with the scale is exact.  ENDS: c may be 0, which is subnormal, or
+// 255, NaN.
+template <bool ENDS>
+__device__ __forceinline__ void decode_block(uint32_t table, const uint4 &w, uint32_t c, uint32_t *o)
 {
     uint32_t f = c * 0x00800080u;                  // 2^(c - 127) twice
     if (ENDS && c == 0u) f = 0x00400040u;
@@ -146,21 +140,19 @@ __device__ __forceinline__ void decode_block(uint32_t table, uint32_t pitch, con
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t at = WIDE ? __byte_perm(words[i], table, 0x7604 + (j << 4))
-                                     : __byte_perm(words[i], 0, 0x4440 + j) * pitch + table;
             uint32_t v;
-            asm("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(at));
+            asm("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(__byte_perm(words[i], table, 0x7604 + (j << 4))));
             o[4 * i + j] = mul_bf16x2(v, f);
         }
     }
 }
 
 // Two blocks, with the scale bytes in the low half of sc.
-template <bool ENDS, bool WIDE>
-__device__ __forceinline__ void decode_two(uint32_t table, uint32_t pitch, const uint4 *w, uint32_t sc, uint32_t (&o)[32])
+template <bool ENDS>
+__device__ __forceinline__ void decode_two(uint32_t table, const uint4 *w, uint32_t sc, uint32_t (&o)[32])
 {
-    decode_block<ENDS, WIDE>(table, pitch, w[0], sc & 255u, o);
-    decode_block<ENDS, WIDE>(table, pitch, w[1], sc >> 8 & 255u, o + 16);
+    decode_block<ENDS>(table, w[0], sc & 255u, o);
+    decode_block<ENDS>(table, w[1], sc >> 8 & 255u, o + 16);
 }
 
 // Whether one of four bytes is 0 or 255.
@@ -289,14 +281,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
-    // With the wide table: stages, segments, the table, stages, x, the others'
-    // sums; else stages, segments, x, the others' sums, the table, barriers.
+    // With 4-bit weights: stages, segments, the table, stages, x, the others'
+    // sums; else stages, segments, the others' sums, barriers.
     const uint32_t end = smem_addr(st_smem_raw) + Z::ALL;
-    const uint32_t lut = Z::WIDE ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS - Z::TABLE) & ~uint32_t(1023);
+    const uint32_t lut = FOUR ? (base & 0xFF000000u) + ST_TABLE : (end - Z::BARS) & ~uint32_t(1023);
     uint32_t *table = reinterpret_cast<uint32_t *>(smem + (lut - base));
-    const int below = Z::WIDE ? int(lut - base) / Z::STAGE : ST_MAX_STAGES;
+    const int below = FOUR ? int(lut - base) / Z::STAGE : ST_MAX_STAGES;
     auto stage_at = [&](int i) {
-        return Z::WIDE && i >= below ? lut + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
+        return FOUR && i >= below ? lut + Z::TABLE + uint32_t(i - below) * Z::STAGE : base + uint32_t(i) * Z::STAGE;
     };
     // the others' sums, [parts - 1][NT][128], and x before them
     const ExpertArgs &p = g.p;
@@ -305,20 +297,20 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     const uint32_t rank = cluster_ctarank();
     const int cluster = int(cluster_nctarank()), per = (nk + cluster - 1) / cluster, parts = (nk + per - 1) / per;
     const int kb0 = int(rank) * per, kb1 = min(nk, kb0 + per);
-    const uint32_t sums = (Z::WIDE ? end : lut) - (cluster - 1) * Z::SUMS;
+    const uint32_t sums = (FOUR ? end : lut) - (cluster - 1) * Z::SUMS;
     const uint32_t x_at = sums - Z::XS * Z::X;
-    const SegTab tab = seg_tab(reinterpret_cast<int *>(smem + ((Z::WIDE ? lut : x_at) - ST_SEGMENTS - base)), p.nbins);
-    const uint32_t bars = Z::WIDE ? lut + 128 : end - Z::BARS;
-    const uint32_t full = bars, empty = Z::WIDE ? bars + 256 : full + 8 * ST_MAX_STAGES;
-    const uint32_t accf = Z::WIDE ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
+    const SegTab tab = seg_tab(reinterpret_cast<int *>(smem + ((FOUR ? lut : x_at) - ST_SEGMENTS - base)), p.nbins);
+    const uint32_t bars = FOUR ? lut + 128 : end - Z::BARS;
+    const uint32_t full = bars, empty = FOUR ? bars + 256 : full + 8 * ST_MAX_STAGES;
+    const uint32_t accf = FOUR ? bars + 512 : empty + 8 * ST_MAX_STAGES, acce = accf + 16;       // [2] each
     const uint32_t decf = acce + 16, dece = decf + 8 * ST_MAX_BUFS, drain = dece + 8 * ST_MAX_BUFS;
     const uint32_t peers = drain + 16;                              // the others' sums are here
-    const uint32_t xfull = Z::WIDE ? bars + 768 : peers + 8, xempty = xfull + 8 * 4;
+    const uint32_t xfull = FOUR ? bars + 768 : peers + 8, xempty = xfull + 8 * 4;
     static_assert(32 + 16 * ST_MAX_BUFS + 24 <= 128 && 8 * ST_MAX_STAGES <= 128, "barriers in a row's second half");
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + (drain + 8 - base));
     volatile int *abort = reinterpret_cast<volatile int *>(s_tmem + 1);
     // (the top byte of a shared address is the CTA's rank in its cluster)
-    if (Z::WIDE && (smem_addr(st_smem_raw) & 0xFFFFFFu) != 1024) {  // the ring was counted from there
+    if (FOUR && (smem_addr(st_smem_raw) & 0xFFFFFFu) != 1024) {  // the ring was counted from there
         pdl_wait();
         if (threadIdx.x == 0) atomicOr(p.error_word, LORA_TIMEOUT_BIT);
         return;
@@ -353,7 +345,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     if constexpr (FOUR) {
         for (int i = tid; i < 256 * 32; i += Z::THREADS) {
             const uint32_t byte = uint32_t(i) / 32;
-            table[byte * (Z::WIDE ? 64 : 32) + i % 32] = e2m1_bf16(byte & 15u) | e2m1_bf16(byte >> 4) << 16;
+            table[byte * 64 + i % 32] = e2m1_bf16(byte & 15u) | e2m1_bf16(byte >> 4) << 16;
         }
     }
     if (warp == 1) tmem_alloc(smem_addr(s_tmem), Z::COLS);
@@ -373,8 +365,10 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     }
     total = kb0 < kb1 ? total * cols : 0;
     const int item0 = int(blockIdx.x) / cluster, items = int(gridDim.x) / cluster;
+    // by a whole warp, whose lanes give up together
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return mbar_try_wait(bar, parity) || mbar_wait_bounded(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES);
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) ||
+                                           mbar_wait_bounded(bar, parity, abort, clock64() + PG_TIMEOUT_CYCLES));
     };
     // for warps that may be late: between polls they leave the issue slots to
     // the decoding warps
@@ -435,31 +429,23 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             const uint32_t d = tmem + uint32_t(acc * NT);
             for (int kb = kb0; ok && kb < kb1; ++kb) {
                 if constexpr (FOUR) {
-                    if (!wait(decf + 8 * dec.stage, dec.phase)) {
+                    if (!wait(decf + 8 * dec.stage, dec.phase) || !wait(xfull + 8 * pos.stage, pos.phase)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t a = tmem + uint32_t(Z::DECODED + dec.stage * 128);
+                    if (leader) {
+                        const uint32_t at = x_at + pos.stage * Z::X;
 #pragma unroll
-                    for (int h = 0; h < Z::PANELS; h += Z::XP) {
-                        ok = ok && wait(xfull + 8 * pos.stage, pos.phase);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (leader) {
-                            const uint32_t at = x_at + pos.stage * Z::X;
-#pragma unroll
-                            for (int j = h; j < h + Z::XP; ++j)
-                                if (kb * Z::KC + j * 64 < p.K)
-                                    umma_k64_tmem_a(d, a + j * 32, at + (j - h) * NT * 128, idesc, kb != kb0 || j != 0);
-                            umma_commit(xempty + 8 * pos.stage);
-                        }
-                        __syncwarp();
-                        pos.next(Z::XS);
+                        for (int j = 0; j < Z::PANELS; ++j)
+                            if (kb * Z::KC + j * 64 < p.K)
+                                umma_k64_tmem_a(d, a + j * 32, at + j * NT * 128, idesc, kb != kb0 || j != 0);
+                        umma_commit(xempty + 8 * pos.stage);
+                        umma_commit(dece + 8 * dec.stage);
                     }
-                    if (!ok) break;
-                    if (leader) umma_commit(dece + 8 * dec.stage);
                     __syncwarp();
+                    pos.next(Z::XS);
                     dec.next(Z::BUFS);
                 } else {
                     if (!wait(full + 8 * pos.stage, pos.phase)) {
@@ -588,17 +574,17 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     int rows[4];
                     if (DIRECT) gathered_rows(p, it, rows);
                     const uint32_t gathered = uint32_t((it.valid + 3) / 4) * 512;
-                    // by panels: a stage of its ring holds XP of the PANELS of each block of K
-                    for (int k = kb0 * Z::KC; ok && k < kb1 * Z::KC; k += Z::XP * 64) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        const int k = kb * Z::KC;
                         const uint32_t bytes =
-                            DIRECT ? gathered * uint32_t(max(0, min(Z::XP, (p.K - k + 63) / 64))) : uint32_t(Z::X);
+                            DIRECT ? gathered * uint32_t(min(Z::PANELS, (p.K - k + 63) / 64)) : uint32_t(Z::X);
                         ok = lazy_wait(xempty + 8 * pos.stage, pos.phase ^ 1u, 40);
                         if (DIRECT) ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         const uint32_t bar = xfull + 8 * pos.stage;
                         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
                         if (DIRECT) __syncwarp();
-                        load_x<DIRECT, Z::XP>(g, x_at + pos.stage * Z::X, NT * 128, k, it.row, rows, bar);
+                        load_x<DIRECT, Z::PANELS>(g, x_at + pos.stage * Z::X, NT * 128, k, it.row, rows, bar);
                         pos.next(Z::XS);
                         ++issued;
                     }
@@ -638,16 +624,16 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                                  : "r"(at + (chunk ^ uint32_t(16 * c))) : "memory");
                 const bool ends = __any_sync(0xffffffffu, has_end(sc));
                 uint32_t o[32];
-                if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w, sc, o);
-                else decode_two<false, Z::WIDE>(mine, g.pitch, w, sc, o);
+                if (ends) decode_two<true>(mine, w, sc, o);
+                else decode_two<false>(mine, w, sc, o);
                 if (!__all_sync(0xffffffffu, mbar_try_wait(dece + 8 * buf, buf_phase)) &&
                     !__all_sync(0xffffffffu, lazy_wait(dece + 8 * buf, buf_phase, 20)))
                     break;
                 tc_fence_after();
                 const uint32_t to = tcol + uint32_t(buf * 128);
                 tmem_st<32>(to, o);
-                if (ends) decode_two<true, Z::WIDE>(mine, g.pitch, w + 2, sc >> 16, o);
-                else decode_two<false, Z::WIDE>(mine, g.pitch, w + 2, sc >> 16, o);
+                if (ends) decode_two<true>(mine, w + 2, sc >> 16, o);
+                else decode_two<false>(mine, w + 2, sc >> 16, o);
                 tmem_st<32>(to + 32, o);
                 tmem_wait_st();
                 tc_fence_before();
@@ -690,8 +676,10 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     const auto kernel = expert_stream_kernel<FOUR, NT, DIRECT>;
     if (int e = expert_shared_memory((const void *)kernel, Z::ALL, done)) return e;
     // Tiles at most: an expert may end in one that is not full.  Up to half
-    // the SMs, two CTAs share each, up to a quarter four (one token, two
-    // experts of 4096 x 4096 in bf16: 21 us on 64 SMs, with two SMs a tile 18).
+    // the SMs, two CTAs share each, up to a quarter four (us with one, two and
+    // four, in a graph: 64 tiles of 4096 x 4096 for one token in bf16 30.3,
+    // 28.8, 29.8, in 4 bits 24.6, 23.6, 23.0; 32 tiles, 16 rows: 35.3, 26.2,
+    // 22.5 and 29.0, 28.9, 28.5).
     const int64_t rows = g.p.R, experts = rows < g.p.E ? rows : g.p.E;
     const int64_t most = (rows / NT + experts) * ((g.p.N + ST_ROWS - 1) / ST_ROWS), sms = device_sm_count();
     int parts = most * 4 <= sms ? 4 : most * 2 <= sms ? 2 : 1;
@@ -705,15 +693,18 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
 bool expert_stream_gathers(const ExpertArgs &p)
 {
     // Gathers of a stage, 90 clocks each, in the time of its 16 KB of W (about
-    // 740; 1100 with the decoding of four panels' codes).
-    return p.x_vec && p.nbins <= ST_BINS && p.R <= (p.scales != nullptr ? 12 : 32);
+    // 740; 1100 with the decoding of four panels' codes).  Measured with a
+    // copy and with gathers (us, experts of 4096 x 4096, in a graph): bf16, two
+    // rows of 8 experts 33.7 and 28.9, 24 rows of one expert 31 and 25, 32 rows
+    // 31 and 32 (width 11008: 40 and 44); 4 bits, two rows 29 and 23, 12 rows
+    // of one expert 27 and 21, 64 rows of 16 experts 60 and 62.
+    return p.x_vec && p.nbins <= ST_BINS && p.R <= (p.scales != nullptr ? 12 : 24);
 }
 
 int launch_expert_stream(const ExpertArgs &p, cudaStream_t st)
 {
     StreamArgs g;
     g.p = p;
-    g.pitch = 128;
     const bool four = p.scales != nullptr, direct = p.table == nullptr;
     if (!(direct ? encode_tile_map(&g.x, p.x, uint64_t(p.R / p.fan), uint64_t(p.K), uint64_t(p.x_ld), 64, 1,
                                    CU_TENSOR_MAP_SWIZZLE_128B)
@@ -724,10 +715,8 @@ int launch_expert_stream(const ExpertArgs &p, cudaStream_t st)
         return LORA_ERR_DEVICE;
     // tiles are of 16 rows (4 bits) or 32 where rows are gathered
     if (direct) return four ? run_stream<true, 16, true>(g, st) : run_stream<false, 32, true>(g, st);
-    if (four) return p.tile_rows == 16   ? run_stream<true, 16>(g, st)
-                     : p.tile_rows == 64 ? run_stream<true, 64>(g, st)
-                                         : run_stream<true, 128>(g, st);
-    return p.tile_rows == 32 ? run_stream<false, 32>(g, st) : run_stream<false, 64>(g, st);
+    if (four) return p.tile_rows == 16 ? run_stream<true, 16>(g, st) : run_stream<true, 64>(g, st);
+    return run_stream<false, 32>(g, st);
 }
 
 }  // namespace lora

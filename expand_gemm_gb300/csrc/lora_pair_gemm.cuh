@@ -228,6 +228,10 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
             // four of them and the waits nearly as long as they run.
             constexpr uint32_t turned = (A_T ? 1u << 15 : 0u) | (B_T ? 1u << 16 : 0u);
             const bool leader = elect_one();
+            // the lanes give up together
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, pg_wait(bar, parity, s_abort));
+            };
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
@@ -236,13 +240,13 @@ __device__ __forceinline__ void pair_gemm(const CUtensorMap *map_a, const CUtens
                 if (it.kb0 >= it.kb1) continue;
                 const uint32_t idesc =
                     __shfl_sync(0xffffffffu, umma_idesc_bf16(PG_TILE, A_STACK ? it.n : PG_TILE) | turned, 0);
-                if (!pg_wait(bar_acce + 8 * acc, acc_phase ^ 1u, s_abort) ||
-                    !pg_wait(bar_odd + 8 * acc, acc_phase ^ 1u, s_abort))
+                if (!wait(bar_acce + 8 * acc, acc_phase ^ 1u) ||
+                    !wait(bar_odd + 8 * acc, acc_phase ^ 1u))
                     break;
                 tc_fence_after();
                 const int blocks = __shfl_sync(0xffffffffu, it.kb1 - it.kb0, 0);
                 for (int kb = 0; kb < blocks; ++kb) {
-                    if (!pg_wait(bar_full + 8 * stage, phase, s_abort)) {
+                    if (!wait(bar_full + 8 * stage, phase)) {
                         ok = false;
                         break;
                     }
