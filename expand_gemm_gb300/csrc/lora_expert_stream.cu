@@ -38,12 +38,14 @@ namespace lora {
 
 struct StreamArgs {
     ExpertArgs p;
-    CUtensorMap w, x;
+    CUtensorMap w, x, s;
     int32_t stages;               // of the ring
+    int32_t boxed;                // scales come by TMA
 };
 
 constexpr int ST_ROWS = 128;                    // of W in a tile
 constexpr int ST_TILE = ST_ROWS * 128;          // bytes of W in a stage: 64 bf16 or 256 codes a row
+constexpr int ST_SCALES = ST_ROWS * 16;         // bytes of scales: of two stages, the least box of TMA
 constexpr int ST_DEC0 = 6;                      // first decoding warp
 constexpr int ST_SETS = 4;                      // of four warps that decode
 constexpr int ST_SCALE_WARP = ST_DEC0 + 4 * ST_SETS;
@@ -60,9 +62,9 @@ struct StreamSizes {
     static constexpr int KC = FOUR ? 256 : 64;                  // elements of K in a stage
     static constexpr int PANELS = KC / 64;                      // of x: NT rows of 64
     static constexpr int X = PANELS * NT * 128;                 // their bytes
-    // a stage of the ring: W and x, or the codes and the rows' eight scales,
-    // beside a ring of XS stages of x
-    static constexpr int STAGE = FOUR ? ST_TILE + 1024 : ST_TILE + X;
+    // a stage of the ring: W and x, or the codes and the rows' scales, beside a
+    // ring of XS stages of x
+    static constexpr int STAGE = ST_TILE + (FOUR ? ST_SCALES : X);
     static constexpr int XS = !FOUR ? 0 : NT <= 16 ? 4 : 2;
     static constexpr int THREADS = 32 * (FOUR ? ST_X_WARP + 1 : ST_DEC0);
     static constexpr int BARS = 512;
@@ -127,14 +129,13 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 // A block of 32 elements with scale byte c.  `table`: shared address of this
 // lane's entries, a pair of bf16 for each byte; a byte's are 256 bytes apart
 // and the table is aligned so that the byte is the address's second.  Each
-// product with the scale is exact.  ENDS: c may be 0, which is subnormal, or
-// 255, NaN.
-template <bool ENDS>
+// product with the scale is exact, also by 2^-127 (c = 0), which is subnormal;
+// c = 255 is NaN.
 __device__ __forceinline__ void decode_block(uint32_t table, const uint4 &w, uint32_t c, uint32_t *o)
 {
     uint32_t f = c * 0x00800080u;                  // 2^(c - 127) twice
-    if (ENDS && c == 0u) f = 0x00400040u;
-    if (ENDS && c == 255u) f = 0x7FC07FC0u;
+    if (c == 0u) f = 0x00400040u;
+    if (c == 255u) f = 0x7FC07FC0u;
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -145,20 +146,6 @@ __device__ __forceinline__ void decode_block(uint32_t table, const uint4 &w, uin
             o[4 * i + j] = mul_bf16x2(v, f);
         }
     }
-}
-
-// Two blocks, with the scale bytes in the low half of sc.
-template <bool ENDS>
-__device__ __forceinline__ void decode_two(uint32_t table, const uint4 *w, uint32_t sc, uint32_t (&o)[32])
-{
-    decode_block<ENDS>(table, w[0], sc & 255u, o);
-    decode_block<ENDS>(table, w[1], sc >> 8 & 255u, o + 16);
-}
-
-// Whether one of four bytes is 0 or 255.
-__device__ __forceinline__ bool has_end(uint32_t v)
-{
-    return (((v - 0x01010101u) & ~v) | ((~v - 0x01010101u) & v)) & 0x80808080u;
 }
 
 // The 4-bit element as bf16.
@@ -320,7 +307,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 
     if (tid == 0) {
         for (int i = 0; i < g.stages; ++i) {
-            mbar_init(full + 8 * i, FOUR ? 33 : 1);                  // the scales' 32 lanes
+            mbar_init(full + 8 * i, FOUR && !g.boxed ? 33 : 1);      // the scales' 32 lanes
             mbar_init(empty + 8 * i, FOUR ? 8 : 1);                  // eight decoding warps; the UMMAs
         }
         for (int i = 0; i < Z::XS; ++i) {
@@ -341,6 +328,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         *abort = 0;
         tma_prefetch_map(&g.w);
         tma_prefetch_map(&g.x);
+        if (FOUR && g.boxed) tma_prefetch_map(&g.s);
     }
     if constexpr (FOUR) {
         for (int i = tid; i < 256 * 32; i += Z::THREADS) {
@@ -390,7 +378,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
                 int rows[4];
                 if (!FOUR && DIRECT) gathered_rows(p, it, rows);
-                const uint32_t bytes = FOUR ? ST_TILE : ST_TILE + (DIRECT ? uint32_t((it.valid + 3) / 4) * 512 : Z::X);
+                const uint32_t bytes = FOUR ? ST_TILE + (g.boxed ? ST_SCALES : 0) : ST_TILE + (DIRECT ? uint32_t((it.valid + 3) / 4) * 512 : Z::X);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40);
                     if (!FOUR && DIRECT) ok = __all_sync(0xffffffffu, ok);
@@ -399,6 +387,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, bytes);
                         tma_load_3d(at, &g.w, kb * (FOUR ? 128 : 64), it.n0, it.expert, bar);
+                        if (FOUR && g.boxed) tma_load_3d(at + ST_TILE, &g.s, (kb & ~1) * 8, it.n0, it.expert, bar);
                     }
                     if constexpr (!FOUR) {
                         if (DIRECT) __syncwarp();
@@ -545,7 +534,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         if (warp == ST_SCALE_WARP) {
             // ---------------------------------------------------- scales
             TcPos pos;
-            bool ok = true;
+            bool ok = !g.boxed;
             for (int i = item0; ok && i < total; i += items) {
                 const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
                 for (int kb = kb0; kb < kb1; ++kb) {
@@ -553,7 +542,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     if (!ok) break;
                     uint8_t *to = smem + (stage_at(pos.stage) - base) + ST_TILE;
 #pragma unroll
-                    for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 8, it.expert, it.n0 + r, kb);
+                    for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 16 + (kb & 1) * 8, it.expert, it.n0 + r, kb);
                     // stores before the arrival, which follows when the copies have landed
                     __threadfence_block();
                     cp_async_mbar_arrive_noinc(full + 8 * pos.stage);
@@ -600,41 +589,41 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             const int half = set & 1;
             const uint32_t mine = smem_addr(table) + lane * 4;
             const uint32_t chunk = uint32_t(row * 128 + ((4 * half ^ row) & 7) * 16);      // chunk c of the half: ^ 16 c
-            const uint32_t scale = ST_TILE + uint32_t(row * 8 + half * 4);
+            const uint32_t scale = ST_TILE + uint32_t(row * 16 + half * 4);
             const uint32_t tcol = tmem + uint32_t(Z::DECODED + half * 64) + (uint32_t(q * 32) << 16);
             // all stages of all tiles in one run: this warp's are every other
             // one, from its set's first
             const int tiles = total > item0 ? (total - item0 + items - 1) / items : 0;
             int left = tiles * (kb1 - kb0) - (set >> 1);
+            int kb = kb0 + (set >> 1);            // its scales are half of a box
             int stage = set >> 1, buf = set >> 1;
             uint32_t phase = 0, buf_phase = 1;
             for (; left > 0; left -= 2) {
                 const uint32_t bar = full + 8 * stage;
+                while (kb >= kb1) kb -= kb1 - kb0;
                 if (!__all_sync(0xffffffffu, mbar_try_wait(bar, phase)) &&
                     !__all_sync(0xffffffffu, lazy_wait(bar, phase, 20)))
                     break;
                 const uint32_t at = stage_at(stage);
                 uint32_t sc;
-                asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(sc) : "r"(at + scale) : "memory");
+                asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(sc) : "r"(at + scale + (kb & 1) * 8) : "memory");
                 uint4 w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                                  : "=r"(w[c].x), "=r"(w[c].y), "=r"(w[c].z), "=r"(w[c].w)
                                  : "r"(at + (chunk ^ uint32_t(16 * c))) : "memory");
-                const bool ends = __any_sync(0xffffffffu, has_end(sc));
-                uint32_t o[32];
-                if (ends) decode_two<true>(mine, w, sc, o);
-                else decode_two<false>(mine, w, sc, o);
                 if (!__all_sync(0xffffffffu, mbar_try_wait(dece + 8 * buf, buf_phase)) &&
                     !__all_sync(0xffffffffu, lazy_wait(dece + 8 * buf, buf_phase, 20)))
                     break;
                 tc_fence_after();
                 const uint32_t to = tcol + uint32_t(buf * 128);
-                tmem_st<32>(to, o);
-                if (ends) decode_two<true>(mine, w + 2, sc >> 16, o);
-                else decode_two<false>(mine, w + 2, sc >> 16, o);
-                tmem_st<32>(to + 32, o);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[16];
+                    decode_block(mine, w[c], sc >> (8 * c) & 255u, o);
+                    tmem_st<16>(to + 16 * c, o);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -644,6 +633,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     mbar_arrive(decf + 8 * buf);
                     mbar_arrive(empty + 8 * stage);
                 }
+                kb += 2;
                 stage += 2;
                 if (stage >= g.stages) {
                     stage -= g.stages;
@@ -706,6 +696,13 @@ int launch_expert_stream(const ExpertArgs &p, cudaStream_t st)
     StreamArgs g;
     g.p = p;
     const bool four = p.scales != nullptr, direct = p.table == nullptr;
+    // Boxes of 16 bytes on rows of whole ones; else 32 lanes fetch eight bytes
+    // a row, whose writes to shared memory are in the way of the decoding's
+    // table (128 rows of 32 experts, 4096 to 11008, in a graph:
+    // 184 us, boxed 176).
+    g.boxed = four && p.K % 512 == 0;
+    if (g.boxed && !encode_stack_map_u8(&g.s, p.scales, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K / 32), 16, ST_ROWS))
+        return LORA_ERR_DEVICE;
     if (!(direct ? encode_tile_map(&g.x, p.x, uint64_t(p.R / p.fan), uint64_t(p.K), uint64_t(p.x_ld), 64, 1,
                                    CU_TENSOR_MAP_SWIZZLE_128B)
                  : encode_tile_map(&g.x, p.xs, uint64_t(p.rows), uint64_t(p.K), uint64_t(p.K), 64, uint32_t(p.tile_rows),

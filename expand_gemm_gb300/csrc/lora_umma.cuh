@@ -624,7 +624,8 @@ bool encode_tile_map_f32(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_
 bool encode_stack_map(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
                       uint32_t box_cols, uint32_t box_rows);
 
-// The same over bytes (row and box columns in bytes).
+// The same over bytes (row and box columns in bytes; boxes of other than 128
+// bytes are not swizzled).
 bool encode_stack_map_u8(CUtensorMap *m, const void *ptr, uint64_t count, uint64_t rows, uint64_t cols,
                          uint32_t box_cols, uint32_t box_rows);
 

@@ -435,6 +435,14 @@ def test_clusters_that_share_a_tile(width, four):
         check_forward((2, 1, 1, hidden, width, 0.0), four)
 
 
+@pytest.mark.parametrize("size", [(1, 1, 1, 2560, 129, 0.0), (9, 1, 1, 1536, 200, 0.0), (20, 2, 3, 512, 140, 0.1),
+                                  (40, 1, 2, 6656, 257, 0.0), (300, 1, 2, 1536, 100, 0.1), (1, 2, 4, 2560, 64, 0.0),
+                                  (6, 2, 5, 7680, 300, 0.0)], ids=str)
+def test_scales_in_boxes_of_two_blocks(size):
+    """Hidden sizes whose blocks of 256 are even and odd in number, also in the parts of a cluster."""
+    check_forward(size, True)
+
+
 def test_rows_of_x_off_a_16_byte_boundary_in_a_small_batch():
     ids, x, _, w, _ = inputs(5, 2, 3, 64, 40, 0.0)
     wide = torch.zeros(5, 67, device="cuda").bfloat16()
