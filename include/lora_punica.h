@@ -574,6 +574,8 @@ int64_t lora_expert_linear_backward_workspace(int32_t num_rows, int32_t fan_out,
  *   out        device bf16 (out_f32 == 0) or fp32 [elements], 16-byte
  *              aligned.  Exact in both (6 x 2^127 is an infinity).
  *
+ * What is written overlaps nothing that is read.
+ *
  * Errors: LORA_ERR_NULL, LORA_ERR_SIZE, LORA_ERR_ALIGN.
  */
 int lora_quantize_mxfp4(const void *weight, int32_t weight_f32, int64_t elements, uint8_t *codes,
