@@ -45,6 +45,7 @@ struct ExpertArgs {
     uint16_t *xs, *dys;               // copies in the metadata's order
     int32_t *from;                    // the row that each row of the copies holds, -1: padding
     int32_t later;                    // x is copied beside the product of dx, not before it
+    int32_t early;                    // the product begins while x is copied
     int64_t dys_ld;
     ExpertTile *table;
     int32_t *tiles;                   // [1]: entries of the table
@@ -181,7 +182,9 @@ int launch_expert_dx(const ExpertArgs &p, cudaStream_t st);
 int launch_expert_dw(const ExpertArgs &p, cudaStream_t st);
 
 // lora_expert_stream.cu: few rows an expert, weights in either form.  Where it
-// gathers it needs no copy of x and no table (p.table is null).
+// walks the metadata's segments itself it needs no table (p.table is null): to
+// ask for weights while x is copied, and where it gathers, without a copy.
+bool expert_stream_early(const ExpertArgs &p);
 bool expert_stream_gathers(const ExpertArgs &p);
 int launch_expert_stream(const ExpertArgs &p, cudaStream_t st);
 

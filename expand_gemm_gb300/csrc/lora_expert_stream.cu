@@ -62,6 +62,12 @@ constexpr int ST_SEGMENTS = 5 * 1024;           // and their bytes
 static_assert(seg_tab_bytes(ST_BINS) <= ST_SEGMENTS, "segments");
 constexpr int ST_TABLE = 65536;                 // shared address of the wide table
 
+// Where a kernel's rows of x come from: the copy, once it is complete, by its
+// table of tiles; the copy, while weights are asked for, by the metadata's
+// segments; gathers by TMA.  (Of a template: as values of the launch the same
+// choices cost 3% of the time.)
+constexpr int ST_COPY = 0, ST_EARLY = 1, ST_GATHER = 2;
+
 template <bool FOUR, int NT>
 struct StreamSizes {
     static constexpr int KC = FOUR ? 256 : 64;                  // elements of K in a stage
@@ -104,13 +110,14 @@ struct StreamItem {
 
 // Item i: an expert's tiles of rows take 128 rows of its weights one after
 // another, so that they are read from memory once.
-template <bool DIRECT, int NT>
+template <int FROM, int NT>
 __device__ __forceinline__ StreamItem stream_item(const ExpertArgs &p, const SegTab &tab, int i, int cols)
 {
-    if constexpr (DIRECT) {
+    if constexpr (FROM != ST_COPY) {
         const int k = find_segment(tab.tile, p.nbins, i / cols), first = tab.tile[k], tiles = tab.tile[k + 1] - first;
         const int j = i - first * cols, tile = j % tiles;
-        return StreamItem{0, min(NT, tab.count[k] - tile * NT), tab.start[k] + tile * NT, j / tiles * ST_ROWS, tab.id[k]};
+        const int at = tab.start[k] + tile * NT, none = tab.id[0] == -1 ? tab.count[0] : 0;
+        return StreamItem{at - none, min(NT, tab.count[k] - tile * NT), at, j / tiles * ST_ROWS, tab.id[k]};
     }
     const int4 *at = reinterpret_cast<const int4 *>(p.table + i / cols);
     const int4 a = at[0], b = at[1];          // base, tiles, expert, start; count, row
@@ -265,11 +272,12 @@ __device__ __forceinline__ void gathered_rows(const ExpertArgs &p, const StreamI
     }
 }
 
-template <bool FOUR, int NT, bool DIRECT>
+template <bool FOUR, int NT, int FROM>
 __global__ void __launch_bounds__(StreamSizes<FOUR, NT>::THREADS, 1)
 expert_stream_kernel(const __grid_constant__ StreamArgs g)
 {
     using Z = StreamSizes<FOUR, NT>;
+    constexpr bool DIRECT = FROM == ST_GATHER, early = FROM == ST_EARLY;
     extern __shared__ uint8_t st_smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(st_smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t base = smem_addr(smem);
@@ -347,10 +355,13 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *s_tmem, 0);
-    pdl_wait();
+    // The copy of x is waited for by the warp that loads it, while weights are
+    // on their way; the kernels before it are complete when it lets this one
+    // begin.
+    if (!early) pdl_wait();
 
     int total;
-    if constexpr (DIRECT) {
+    if constexpr (FROM != ST_COPY) {
         total = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, NT, tab, false, 0, p.R, p.error_word);
         total = __shfl_sync(0xffffffffu, total, 0);
     } else {
@@ -378,13 +389,31 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             asm volatile("fence.proxy.async.global;\n" ::: "memory");
             TcPos pos;
             int issued = 0;
-            bool ok = true;
+            bool ok = true, here = !early;
+            // x of the first stages, whose weights were asked for before it was there
+            [[maybe_unused]] auto first_x = [&] {
+                pdl_wait();
+                asm volatile("fence.proxy.async.global;\n" ::: "memory");
+                const int none[4] = {};
+                int n = 0;
+                for (int i = item0; n < issued; i += items) {
+                    const int row = stream_item<FROM, NT>(p, tab, i, cols).row;
+                    for (int kb = kb0; kb < kb1 && n < issued; ++kb, ++n)
+                        load_x<DIRECT, 1>(g, stage_at(n) + ST_TILE, 0, kb * 64, row, none, full + 8 * n);
+                }
+            };
             for (int i = item0; ok && i < total; i += items) {
-                const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+                const StreamItem it = stream_item<FROM, NT>(p, tab, i, cols);
                 int rows[4];
                 if (!FOUR && DIRECT) gathered_rows(p, it, rows);
                 const uint32_t bytes = FOUR ? ST_TILE + (g.boxed ? ST_SCALES : 0) : ST_TILE + (DIRECT ? uint32_t((it.valid + 3) / 4) * 512 : Z::X);
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    if constexpr (!FOUR && early) {
+                        if (!here && issued == g.stages) {
+                            first_x();
+                            here = true;
+                        }
+                    }
                     ok = lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40);
                     if (!FOUR && DIRECT) ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -396,11 +425,14 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     }
                     if constexpr (!FOUR) {
                         if (DIRECT) __syncwarp();
-                        load_x<DIRECT, 1>(g, at + ST_TILE, 0, kb * 64, it.row, rows, bar);
+                        if (!early || here) load_x<DIRECT, 1>(g, at + ST_TILE, 0, kb * 64, it.row, rows, bar);
                     }
                     pos.next(g.stages);
                     ++issued;
                 }
+            }
+            if constexpr (!FOUR && early) {
+                if (!here) first_x();
             }
             if (lane == 0) drain_ring(full, empty, g.stages, issued, abort);
         }
@@ -416,7 +448,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         bool ok = true;
         const bool leader = elect_one();
         for (int i = item0; ok && i < total; i += items) {
-            const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+            const StreamItem it = stream_item<FROM, NT>(p, tab, i, cols);
             const uint32_t idesc = __shfl_sync(0xffffffffu, umma_idesc_bf16(ST_ROWS, (it.valid + 15) & ~15), 0);
             if (!wait(acce + 8 * acc, acc_phase ^ 1u)) break;
             tc_fence_after();
@@ -475,7 +507,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int i = item0; i < total; i += items) {
-            const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+            const StreamItem it = stream_item<FROM, NT>(p, tab, i, cols);
             if (!__all_sync(0xffffffffu, lazy_wait(accf + 8 * acc, acc_phase, 200))) break;
             tc_fence_after();
             const int n = it.n0 + q * 32 + lane;
@@ -541,7 +573,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             TcPos pos;
             bool ok = !g.boxed;
             for (int i = item0; ok && i < total; i += items) {
-                const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+                const StreamItem it = stream_item<FROM, NT>(p, tab, i, cols);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
@@ -559,12 +591,13 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         } else if (warp == ST_X_WARP) {
             // --------------------------------------------------------- x
             if (lane == 0 || DIRECT) {
+                if (early) pdl_wait();
                 asm volatile("fence.proxy.async.global;\n" ::: "memory");      // written by an ordinary kernel
                 TcPos pos;
                 int issued = 0;
                 bool ok = true;
                 for (int i = item0; ok && i < total; i += items) {
-                    const StreamItem it = stream_item<DIRECT, NT>(p, tab, i, cols);
+                    const StreamItem it = stream_item<FROM, NT>(p, tab, i, cols);
                     int rows[4];
                     if (DIRECT) gathered_rows(p, it, rows);
                     const uint32_t gathered = uint32_t((it.valid + 3) / 4) * 512;
@@ -653,6 +686,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
         }
     }
 
+    // not over before the copy: what waits for this kernel may write there
+    if (early) pdl_wait();
     tc_fence_before();
     if (cluster > 1) cluster_sync_all();          // nobody writes to a CTA that is gone
     else __syncthreads();
@@ -663,12 +698,12 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 
 // ---------------------------------------------------------------- host
 
-template <bool FOUR, int NT, bool DIRECT = false>
+template <bool FOUR, int NT, int FROM>
 static int run_stream(StreamArgs &g, cudaStream_t st)
 {
     using Z = StreamSizes<FOUR, NT>;
     static std::atomic<uint64_t> done{0};
-    const auto kernel = expert_stream_kernel<FOUR, NT, DIRECT>;
+    const auto kernel = expert_stream_kernel<FOUR, NT, FROM>;
     if (int e = expert_shared_memory((const void *)kernel, Z::ALL, done)) return e;
     // Tiles at most: an expert may end in one that is not full.  Up to half
     // the SMs, two CTAs share each, up to a quarter four (us with one, two and
@@ -683,6 +718,18 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     if (parts == 1)
         return int(launch_kernel(kernel, dim3(unsigned(sms)), dim3(Z::THREADS), Z::ALL, st, g));
     return int(launch_clusters(kernel, parts, int(most), st, g, Z::THREADS, Z::ALL));
+}
+
+// Weights are asked for while x is copied, where they are few: this saves a
+// part of the copy's time, and costs a walk of the segments for every tile
+// (us in a graph, after the copy and beside it: 4 bits, 128 rows of 16 experts
+// 4096 x 4096, 143 MB: 57 and 52; 32 rows of one of 8192 x 8192: 40 and 37; bf16, 32
+// rows of one of 4096 x 4096: 29.5 and 27.6; 128 rows of 8, 268 MB: 71.5 and 69.8; of
+// 16, 537 MB: 117 and 118; 4 bits, 767 MB: 171 and 175).
+bool expert_stream_early(const ExpertArgs &p)
+{
+    const int64_t experts = p.R < p.E ? p.R : p.E, row = p.scales != nullptr ? p.K / 2 + p.K / 32 : 2 * p.K;
+    return p.nbins <= ST_BINS && experts * p.N * row <= int64_t(256) << 20;
 }
 
 bool expert_stream_gathers(const ExpertArgs &p)
@@ -700,7 +747,7 @@ int launch_expert_stream(const ExpertArgs &p, cudaStream_t st)
 {
     StreamArgs g;
     g.p = p;
-    const bool four = p.scales != nullptr, direct = p.table == nullptr;
+    const bool four = p.scales != nullptr, direct = expert_stream_gathers(p);
     // Boxes of 16 bytes on rows of whole ones; else 32 lanes fetch eight bytes
     // a row, whose writes to shared memory are in the way of the decoding's
     // table (128 rows of 32 experts, 4096 to 11008, in a graph:
@@ -716,9 +763,11 @@ int launch_expert_stream(const ExpertArgs &p, cudaStream_t st)
                : encode_stack_map(&g.w, p.w, uint64_t(p.E), uint64_t(p.N), uint64_t(p.K), 64, ST_ROWS)))
         return LORA_ERR_DEVICE;
     // tiles are of 16 rows (4 bits) or 32 where rows are gathered
-    if (direct) return four ? run_stream<true, 16, true>(g, st) : run_stream<false, 32, true>(g, st);
-    if (four) return p.tile_rows == 16 ? run_stream<true, 16>(g, st) : run_stream<true, 64>(g, st);
-    return run_stream<false, 32>(g, st);
+    if (direct) return four ? run_stream<true, 16, ST_GATHER>(g, st) : run_stream<false, 32, ST_GATHER>(g, st);
+    if (four && p.tile_rows == 16)
+        return p.early ? run_stream<true, 16, ST_EARLY>(g, st) : run_stream<true, 16, ST_COPY>(g, st);
+    if (four) return p.early ? run_stream<true, 64, ST_EARLY>(g, st) : run_stream<true, 64, ST_COPY>(g, st);
+    return p.early ? run_stream<false, 32, ST_EARLY>(g, st) : run_stream<false, 32, ST_COPY>(g, st);
 }
 
 }  // namespace lora
