@@ -797,8 +797,8 @@ def lora_expert_linear(x: torch.Tensor, weight: torch.Tensor, y: torch.Tensor, m
     as it is); x has a k-th of the rows, k of them in a row for each token (k =
     1: as many).  weight is bf16 [max_loras, n, hidden], or the uint8 codes
     [max_loras, n, hidden / 2] of :func:`lora_quantize_mxfp4` with their
-    weight_scale [max_loras, n, hidden / 32].  A workspace (uint8) is allocated
-    when none is given."""
+    weight_scale [max_loras, n, hidden / 32].  y overlaps nothing that is read.
+    A workspace (uint8) is allocated when none is given."""
     _expert_types(x, "x", meta, ((x, "x"), (y, "y")), weight, weight_scale, workspace)
     if x is None or y is None:
         raise TypeError("x and y must be tensors")
@@ -835,7 +835,8 @@ def lora_expert_linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch
     add_inputs added to what is there; tokens without an expert get zeros, or
     are left as they are.  d_weight (bf16 [max_loras, n, hidden], also for
     4-bit weights) is overwritten; experts without rows get zeros, and so do
-    those that the weights hold beyond the metadata's."""
+    those that the weights hold beyond the metadata's.  Neither output overlaps
+    an input or the other."""
     _expert_types(dy, "dy", meta, ((dy, "dy"), (x, "x"), (dx, "dx"), (d_weight, "d_weight")), weight,
                   weight_scale, workspace)
     if dy is None or x is None:
@@ -935,9 +936,9 @@ class LoRAGradients:
     grads: bf16 or fp32 tensors (None is skipped), contiguous, on one GPU.
     groups: how many adapters their first dimension stacks (1: any shape).
     out: None (they are scaled in place), or tensors like them that receive the
-    scaled gradients.  No two may share memory.  The tensors are kept; their storage must stay where it
-    is.  A workspace is allocated with it, so calls on one object must be
-    ordered on one stream."""
+    scaled gradients.  No two may share memory.  The tensors are kept; their
+    storage must stay where it is.  A workspace is allocated with it, so calls
+    on one object must be ordered on one stream."""
 
     def __init__(self, grads, groups: int = 1, out=None):
         if isinstance(grads, torch.Tensor):
@@ -987,8 +988,9 @@ def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *
 
     grads is a :class:`LoRAGradients` (for every step), or the tensors
     themselves, which are then scaled in place and stack norms.numel() adapters.
-    max_norm None (or infinite) computes the norms alone.  Nothing is read back to the host: a
-    NaN norm makes its adapter's gradients NaN, and leaves the others'."""
+    max_norm None (or infinite) computes the norms alone.  Nothing is read back
+    to the host: a NaN norm makes its adapter's gradients NaN, and leaves the
+    others'."""
     if not isinstance(norms, torch.Tensor):
         raise TypeError("norms must be a torch.Tensor")
     if not isinstance(grads, LoRAGradients):

@@ -552,6 +552,32 @@ def test_metadata_of_a_larger_batch_write_nothing_beyond_the_call_s_rows(rows):
     assert not bool(full[rows:].any()) and bool((ws[need:] == 7).all())
 
 
+@pytest.mark.parametrize("four", [False, True])
+def test_calls_one_after_another_share_a_workspace(four):
+    """No call begins to write what the one before still reads: batches that gather, copy and run on pairs."""
+    cases = []
+    for k, tokens in enumerate((1, 30, 700, 3, 64, 200, 40, 9, 2000, 26)):
+        ids, x, (w, scale), _, _ = inputs(tokens, 2, 3, 512, 384, 0.1, four=four, seed=k)
+        cases.append((ids, x, w, scale, meta_of(ids, 3)))
+    y = [torch.zeros(len(c[0]), 384, device="cuda").bfloat16() for c in cases]
+    alone = []
+    for (ids, x, w, scale, meta), out in zip(cases, y):
+        eg.lora_expert_linear(x, w, out, meta, weight_scale=scale)
+        torch.cuda.synchronize()
+        alone.append(out.clone())
+    workspace = torch.empty(eg.lora_expert_linear_workspace(4000, 512, 384, 3, quantized=four), dtype=torch.uint8,
+                            device="cuda")
+    for _ in range(20):
+        for out in y:
+            out.zero_()
+        for n, (ids, x, w, scale, meta) in enumerate(cases * 3):
+            if n % 4 == 0:
+                meta.prepare_tensors(ids)
+            eg.lora_expert_linear(x, w, y[n % len(y)], meta, weight_scale=scale, workspace=workspace)
+        for out, want in zip(y, alone):
+            assert torch.equal(out, want)
+
+
 def test_refusals():
     ids, x, _, w, dy = inputs(8, 2, 3, 64, 48, 0.0)
     meta = meta_of(ids, 3)
