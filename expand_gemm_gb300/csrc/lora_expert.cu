@@ -56,9 +56,9 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
 {
     extern __shared__ int ex_tab[];
     pdl_wait();
-    // the product may begin: the metadata are complete, and what it needs of
-    // this kernel it waits for
-    if (p.early) pdl_launch_dependents();
+    // the next kernel may begin: the metadata are complete, and what it needs
+    // of this one it waits for
+    pdl_launch_dependents();
     const bool tables = blockIdx.x == 0;
     if (tables && blockIdx.y != 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -296,10 +296,7 @@ LORA_API int lora_expert_linear(const lora_bf16_t *x, int64_t x_ld, int32_t num_
     if (workspace_bytes < lay.bytes) return LORA_ERR_WORKSPACE;
     if (num_rows == 0) return LORA_OK;
     const bool pairs = p.tile_rows == EX_TILE;
-    if (pairs) {
-        p.tile_rows = pair_tile(num_rows, p.E, out_features);
-        p.early = !decode;                // (4096 rows of one 4096 x 4096: 99 us, 97 so)
-    }
+    if (pairs) p.tile_rows = pair_tile(num_rows, p.E, out_features);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
     p.y = y;

@@ -45,7 +45,7 @@ struct ExpertArgs {
     uint16_t *xs, *dys;               // copies in the metadata's order
     int32_t *from;                    // the row that each row of the copies holds, -1: padding
     int32_t later;                    // x is copied beside the product of dx, not before it
-    int32_t early;                    // the product begins while x is copied
+    int32_t early;                    // weights are asked for while x is copied
     int64_t dys_ld;
     ExpertTile *table;
     int32_t *tiles;                   // [1]: entries of the table

@@ -162,13 +162,15 @@ struct DecodeArgs {
 
 // The same for the experts of the metadata's segments only: blockIdx.y takes
 // every gridDim.y-th segment.
+// Runs beside the copy of x, which it needs nothing of: the kernels before that
+// are complete when it lets this one begin.  It ends after it, for the product
+// waits for this one alone.
 __global__ void __launch_bounds__(MX_THREADS) expert_decode_kernel(const __grid_constant__ DecodeArgs a)
 {
-    pdl_wait();
     const ExpertArgs &p = a.p;
-    if (*p.no_lora) return;
+    const int bins = *p.no_lora ? 0 : p.nbins;
     const int64_t per = int64_t(p.N) * p.K / 8, step = int64_t(gridDim.x) * MX_THREADS;
-    for (int k = blockIdx.y; k < p.nbins; k += gridDim.y) {
+    for (int k = blockIdx.y; k < bins; k += gridDim.y) {
         const int e = p.active[k];
         if (e < 0 || e >= p.E || p.counts[k] <= 0) continue;
         const uint32_t *codes = reinterpret_cast<const uint32_t *>(p.codes) + e * per;
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(MX_THREADS) expert_decode_kernel(const __grid_
             out[i] = pack8(v);
         }
     }
+    pdl_wait();
 }
 
 static unsigned grid_for(int64_t eighths)
