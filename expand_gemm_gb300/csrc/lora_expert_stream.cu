@@ -166,30 +166,39 @@ __device__ __forceinline__ uint32_t e2m1_bf16(uint32_t code)
     return (__float_as_uint(__uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f)) >> 16;
 }
 
-// One row's eight scale bytes of a stage to `dst` (shared memory) and an
-// arrival at `bar` once they are there; bytes that do not exist stand for 1
-// (their codes are zero).
-__device__ __forceinline__ void fetch_scales(const ExpertArgs &p, uint8_t *dst, int expert, int n, int kb)
+// One row's eight scale bytes of a stage, at any alignment, to `dst` (shared
+// memory, 16 bytes): the words that they lie in, and in the fourth word which
+// byte of the first is theirs.  In a row's last stage bytes that do not exist
+// stand for 1 (their codes are zero).  (Bytes one by one, and waited for, took
+// 128 rows of 16 experts 4096 x 2016 62 us; so 43.)
+__device__ __forceinline__ void fetch_scales(const ExpertArgs &p, uint32_t dst, int expert, int n, int kb)
 {
     const int per = p.K / 32, at = kb * 8;
-    const uint8_t *src = p.scales + (int64_t(expert) * p.N + n) * per + at;
-    if (n < p.N && at + 8 <= per && per % 4 == 0) {
-        if (per % 8 == 0)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" :: "r"(smem_addr(dst)), "l"(src) : "memory");
-        else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n"
-                         "cp.async.ca.shared.global [%0+4], [%1+4], 4;\n" :: "r"(smem_addr(dst)), "l"(src) : "memory");
-        return;
-    }
-    uint32_t lo = 0, hi = 0;
+    const int64_t off = (int64_t(expert) * p.N + min(n, p.N - 1)) * per + at;
+    uint32_t first = 0;
+    if (at + 8 <= per) {
+        first = uint32_t(off) & 3u;
+        const uint8_t *src = p.scales + (off - first);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n"
+                     "cp.async.ca.shared.global [%0+4], [%1+4], 4;\n" :: "r"(dst), "l"(src) : "memory");
+        if (first != 0) {
+            // nothing is read behind the last expert's scales
+            const int64_t left = int64_t(p.E) * p.N * per - (off - first) - 8;
+            asm volatile("cp.async.ca.shared.global [%0+8], [%1+8], 4, %2;\n"
+                         :: "r"(dst), "l"(src), "r"(int(min(int64_t(4), left))) : "memory");
+        }
+    } else {
+        const uint8_t *src = p.scales + off;
+        uint32_t lo = 0, hi = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t c = 127u;
-        if (n < p.N && at + i < per) c = src[i];
-        if (i < 4) lo |= c << (8 * i);
-        else hi |= c << (8 * i - 32);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t c = at + i < per ? src[i] : 127u;
+            if (i < 4) lo |= c << (8 * i);
+            else hi |= c << (8 * i - 32);
+        }
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};\n" :: "r"(dst), "r"(lo), "r"(hi) : "memory");
     }
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+    asm volatile("st.shared.b32 [%0+12], %1;\n" :: "r"(dst), "r"(first) : "memory");
 }
 
 // D += A B over 64 of K, as four UMMAs: A decoded in TMEM, B K-major; one add
@@ -577,9 +586,9 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = __all_sync(0xffffffffu, lazy_wait(empty + 8 * pos.stage, pos.phase ^ 1u, 40));
                     if (!ok) break;
-                    uint8_t *to = smem + (stage_at(pos.stage) - base) + ST_TILE;
+                    const uint32_t to = stage_at(pos.stage) + ST_TILE;
 #pragma unroll
-                    for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 16 + (kb & 1) * 8, it.expert, it.n0 + r, kb);
+                    for (int r = lane; r < ST_ROWS; r += 32) fetch_scales(p, to + r * 16, it.expert, it.n0 + r, kb);
                     // stores before the arrival, which follows when the copies have landed
                     __threadfence_block();
                     cp_async_mbar_arrive_noinc(full + 8 * pos.stage);
@@ -627,7 +636,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
             const int half = set & 1;
             const uint32_t mine = smem_addr(table) + lane * 4;
             const uint32_t chunk = uint32_t(row * 128 + ((4 * half ^ row) & 7) * 16);      // chunk c of the half: ^ 16 c
-            const uint32_t scale = ST_TILE + uint32_t(row * 16 + half * 4);
+            const uint32_t scale = ST_TILE + uint32_t(row * 16);
             const uint32_t tcol = tmem + uint32_t(Z::DECODED + half * 64) + (uint32_t(q * 32) << 16);
             // all stages of all tiles in one run: this warp's are every other
             // one, from its set's first
@@ -644,7 +653,15 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                     break;
                 const uint32_t at = stage_at(stage);
                 uint32_t sc;
-                asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(sc) : "r"(at + scale + (kb & 1) * 8) : "memory");
+                if (g.boxed) {
+                    asm volatile("ld.shared.b32 %0, [%1];\n"
+                                 : "=r"(sc) : "r"(at + scale + (kb & 1) * 8 + half * 4) : "memory");
+                } else {
+                    uint32_t a, b, c, first;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                 : "=r"(a), "=r"(b), "=r"(c), "=r"(first) : "r"(at + scale) : "memory");
+                    sc = __funnelshift_r(half ? b : a, half ? c : b, 8 * first);
+                }
                 uint4 w[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)

@@ -435,6 +435,27 @@ def test_clusters_that_share_a_tile(width, four):
         check_forward((2, 1, 1, hidden, width, 0.0), four)
 
 
+@pytest.mark.parametrize("size", [(12, 1, 3, 32 * 9, 131, 0.0), (30, 2, 5, 32 * 21, 67, 0.1), (7, 1, 2, 32 * 34, 33, 0.0),
+                                  (90, 1, 2, 32 * 43, 257, 0.0), (3, 2, 4, 32 * 115, 301, 0.0), (200, 1, 1, 32 * 47, 129, 0.0),
+                                  (5, 1, 3, 32 * 8, 65, 0.0), (5, 1, 3, 32 * 7, 65, 0.0), (20, 1, 3, 32 * 17, 3, 0.0)], ids=str)
+def test_scales_at_any_alignment(size):
+    """Rows of scales whose bytes are no whole words, in number or in place."""
+    check_forward(size, True)
+
+
+@pytest.mark.parametrize("blocks", [3, 9, 10, 11, 13])
+def test_scales_end_with_their_array(blocks):
+    """The last row's scales, with NaN behind them: they are not this weight's."""
+    T, N, K = 20, 67, 32 * blocks
+    ids, x, (codes, scales), values, _ = inputs(T, 1, 2, K, N, 0.0, four=True)
+    room = torch.full((scales.numel() + 64,), 255, dtype=torch.uint8, device="cuda")
+    room[:scales.numel()] = scales.view(-1)
+    y = torch.zeros(T, N, device="cuda").bfloat16()
+    eg.lora_expert_linear(x, codes, y, meta_of(ids, 2), weight_scale=room[:scales.numel()].view(scales.shape))
+    want, sums = ref.forward(x, values, ids, 1)
+    ref.within(y, want, ref.bound(want, sums, K), "y")
+
+
 @pytest.mark.parametrize("size", [(1, 1, 1, 2560, 129, 0.0), (9, 1, 1, 1536, 200, 0.0), (20, 2, 3, 512, 140, 0.1),
                                   (40, 1, 2, 6656, 257, 0.0), (300, 1, 2, 1536, 100, 0.1), (1, 2, 4, 2560, 64, 0.0),
                                   (6, 2, 5, 7680, 300, 0.0)], ids=str)
