@@ -178,11 +178,16 @@ __host__ __device__ constexpr size_t seg_tab_bytes(int nbins)
 //   num_tokens, err: a debug build drops (and reports in err) segments
 //                    whose id is outside [-1, nbins - 1) or whose tokens
 //                    leave [0, num_tokens).
+//   clamp:           segments end with the first num_tokens of the sorted
+//                    tokens, so that they have num_tokens / tile_rows tiles
+//                    and one more each at most, whatever batch the metadata
+//                    were prepared for.
 __device__ __forceinline__ int load_segments(const int32_t *no_lora, const int32_t *active,
                                              const int32_t *counts, const int32_t *start_loc,
                                              int nbins, int tile_rows, SegTab t,
                                              bool full_tiles_only = false, int skip_rows = 0,
-                                             int num_tokens = 0, int32_t *err = nullptr)
+                                             int num_tokens = 0, int32_t *err = nullptr,
+                                             bool clamp = false)
 {
     int *s_flag = t.count + nbins;
     for (int k = threadIdx.x; k < nbins; k += blockDim.x) {
@@ -197,6 +202,7 @@ __device__ __forceinline__ int load_segments(const int32_t *no_lora, const int32
                 c = 0;
             }
         }
+        if (clamp) c = max(0, min(c, num_tokens - st));
         if (skip_rows > 0) {
             const int skip = (c / skip_rows) * skip_rows;
             st += skip;

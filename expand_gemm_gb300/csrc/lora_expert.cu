@@ -31,7 +31,7 @@ __device__ __forceinline__ void expert_tables(const ExpertArgs &p, const SegTab 
     for (int k = threadIdx.x; units > 0 && k < p.nbins; k += blockDim.x) first_row[k] = tab.tile[k] * pad;
     __syncthreads();
     const int tiles = min(p.entries, load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, p.tile_rows, tab,
-                                                   false, 0, p.R, p.error_word));
+                                                   false, 0, p.R, p.error_word, true));
     if (threadIdx.x == 0) *p.tiles = tiles;
     for (int t = threadIdx.x; t < tiles; t += blockDim.x) {
         const int k = find_segment(tab.tile, p.nbins, t);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(EX_PACK_THREADS) expert_pack_kernel(const __gr
     const SegTab tab = seg_tab(ex_tab, p.nbins);
     const int pad = p.pad ? EX_PAD : 1;
     const int units = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, pad, tab, false, 0,
-                                    p.R, p.error_word);
+                                    p.R, p.error_word, true);
     if (tables) {
         expert_tables(p, tab, units, ex_tab + 4 * p.nbins + 2);
         return;

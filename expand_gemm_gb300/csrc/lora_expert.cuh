@@ -60,11 +60,10 @@ struct ExpertArgs {
     int32_t *error_word;
 };
 
-// The row that the metadata names at `at`, -1 where that is none of the batch's
-// (metadata that were prepared for more rows than the call has).
+// The row that the metadata names at `at` < R, -1 where that is none of the
+// batch's (metadata that were prepared for more rows than the call has).
 __device__ __forceinline__ int expert_row(const ExpertArgs &p, int at)
 {
-    if (at >= p.R) return -1;
     const int row = checked_token(p.sorted[at], p.R, p.error_word);
     return row < p.R ? row : -1;
 }

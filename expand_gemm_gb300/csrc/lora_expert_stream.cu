@@ -371,7 +371,8 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
 
     int total;
     if constexpr (FROM != ST_COPY) {
-        total = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, NT, tab, false, 0, p.R, p.error_word);
+        total = load_segments(p.no_lora, p.active, p.counts, p.start_loc, p.nbins, NT, tab, false, 0, p.R, p.error_word,
+                              true);
         total = __shfl_sync(0xffffffffu, total, 0);
     } else {
         total = *p.tiles;
@@ -535,7 +536,7 @@ expert_stream_kernel(const __grid_constant__ StreamArgs g)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(cluster_map(peers, 0));
-                continue;                         // a cluster has one tile at most
+                continue;                         // a cluster has one tile at most (run_stream)
             }
             if (parts > 1) {
                 if (!__all_sync(0xffffffffu, mbar_try_wait_cluster(peers, 0) ||
@@ -722,8 +723,10 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     static std::atomic<uint64_t> done{0};
     const auto kernel = expert_stream_kernel<FOUR, NT, FROM>;
     if (int e = expert_shared_memory((const void *)kernel, Z::ALL, done)) return e;
-    // Tiles at most: an expert may end in one that is not full.  Up to half
-    // the SMs, two CTAs share each, up to a quarter four (us with one, two and
+    // Tiles at most: an expert may end in one that is not full.  The segments
+    // are those of the call's rows (load_segments: clamp), so a cluster that
+    // shares a tile has one, and its barriers' first phases are all it needs.
+    // Up to half the SMs, two CTAs share each, up to a quarter four (us with one, two and
     // four, in a graph: 64 tiles of 4096 x 4096 for one token in bf16 30.3,
     // 28.8, 29.8, in 4 bits 24.6, 23.6, 23.0; 32 tiles, 16 rows: 35.3, 26.2,
     // 22.5 and 29.0, 28.9, 28.5).
