@@ -911,6 +911,14 @@ def lora_dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, out: torch.
           int(out.dtype is _F32), _raw_stream(index))
 
 
+def _capturing(index: int) -> bool:
+    """Whether the current stream of GPU `index` is being captured into a graph."""
+    if torch.cuda.current_device() == index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _refuse_overlaps(grads, out) -> None:
     """Each tensor is read and written as a whole, in no order: no two of the written ones may share
     memory, nor may one share another's gradient (its own: only as a whole)."""
@@ -937,8 +945,9 @@ class LoRAGradients:
     groups: how many adapters their first dimension stacks (1: any shape).
     out: None (they are scaled in place), or tensors like them that receive the
     scaled gradients.  No two may share memory.  The tensors are kept; their
-    storage must stay where it is.  A workspace is allocated with it, so calls
-    on one object must be ordered on one stream."""
+    storage must stay where it is.  Workspaces are kept for each stream, and a
+    captured call has one of its own, so an object may be used on any stream,
+    captured, and dropped while its calls run or graphs hold them."""
 
     def __init__(self, grads, groups: int = 1, out=None):
         if isinstance(grads, torch.Tensor):
@@ -972,12 +981,26 @@ class LoRAGradients:
         self.c_out = None if out is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out])
         self.c_sizes = (ctypes.c_int64 * n)(*[g.numel() // groups for g in self.grads])
         self.c_f32 = (ctypes.c_int32 * n)(*[int(g.dtype is _F32) for g in self.grads])
-        self.workspace = torch.empty(_workspace_bytes("lora_clip_gradients_workspace", self.device, groups),
-                                     dtype=_U8, device=self.device)
+        self.workspace_bytes = _workspace_bytes("lora_clip_gradients_workspace", self.device, groups)
+        self.workspaces = {}
 
     @staticmethod
     def make(grads, groups: int = 1, *, out=None) -> "LoRAGradients":
         return LoRAGradients(grads, groups, out)
+
+    def workspace(self, stream: int) -> torch.Tensor:
+        """The workspace of a call on the current stream, whose handle is `stream`.
+
+        Memory belongs to the stream that it was allocated on: given back while
+        calls on another stream run, it would be handed out again under them.
+        A captured call's belongs to its graph, which may outlive the object and
+        be replayed beside another one."""
+        if _capturing(self.index):
+            return torch.empty(self.workspace_bytes, dtype=_U8, device=self.device)
+        kept = self.workspaces.get(stream)
+        if kept is None:
+            kept = self.workspaces[stream] = torch.empty(self.workspace_bytes, dtype=_U8, device=self.device)
+        return kept
 
 
 def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *, eps: float = 1e-6) -> None:
@@ -999,6 +1022,7 @@ def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *
     limit = math.inf if max_norm is None else float(max_norm)
     if not limit >= 0.0 or not eps >= 0.0:
         raise ValueError("max_norm and eps must not be negative")
+    norms_ptr, stream = _vector(norms, "norms", grads.groups), _raw_stream(grads.index)
+    workspace = grads.workspace(stream)
     _call("lora_clip_gradients", grads.device, grads.c_grads, grads.c_out, grads.c_sizes, grads.c_f32, grads.count,
-          grads.groups, limit, float(eps), _vector(norms, "norms", grads.groups), grads.workspace.data_ptr(),
-          grads.workspace.numel(), _raw_stream(grads.index))
+          grads.groups, limit, float(eps), norms_ptr, workspace.data_ptr(), grads.workspace_bytes, stream)
