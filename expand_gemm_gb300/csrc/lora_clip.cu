@@ -27,6 +27,15 @@ constexpr int CL_LONG_LOG = 17;                // 2^17 where there are many
 constexpr int CL_FEW = 64;                     // tensors of a launch: with so many
 constexpr int CL_MANY = 1024;                  // or so many, 28 bytes of arguments each
 
+// What a group's gradients are multiplied by, mantissa * 2^exponent: a norm of
+// 2^126 largest norms leaves a factor that 32 bits hold with few digits or as
+// zero, and its largest gradients still count.  The exponent is 0 where the
+// mantissa alone, a normal number or zero, is the factor.
+struct ClipFactor {
+    float mantissa;
+    int32_t exponent;
+};
+
 struct ClipShared {
     int32_t tensors, groups;
     int32_t unit_log;
@@ -35,7 +44,8 @@ struct ClipShared {
     int32_t add;                               // the sums are added to those of earlier tensors
     double *part;                              // [CTAs + groups]: CTA c's sum for group g at c + g
     double *sum;                               // [groups]
-    float *factor, *norms;                     // [groups]
+    ClipFactor *factor;                        // [groups]
+    float *norms;                              // [groups]
     float max_norm, eps;
     int32_t scale;                             // 0: norms only (out then receives copies)
 };
@@ -213,13 +223,19 @@ __global__ void __launch_bounds__(CL_THREADS, 3) clip_sum_kernel(const __grid_co
     }
 }
 
-// What the gradients of a group with this norm are multiplied by, of the norm
-// in 64 bits: it may lie beyond fp32.  A zero gradient stays one; NaN stays NaN.
-__device__ __forceinline__ float clip_factor(const ClipShared &a, double norm)
+// The factor of a group with this norm, which is in 64 bits: it may lie beyond
+// fp32.  A zero gradient stays one; NaN stays NaN.
+__device__ __forceinline__ ClipFactor clip_factor(const ClipShared &a, double norm)
 {
-    if (!a.scale) return 1.0f;
-    const float f = float(double(a.max_norm) / (norm + double(a.eps)));
-    return f >= 1.0f || norm == 0.0 ? 1.0f : f;
+    if (!a.scale) return {1.0f, 0};
+    const double f = double(a.max_norm) / (norm + double(a.eps));
+    if (f >= 1.0 || norm == 0.0) return {1.0f, 0};
+    if (f > 0.0 && f < 0x1p-126) {
+        int e;
+        const double m = frexp(f, &e);
+        return {float(m), e};
+    }
+    return {float(f), 0};
 }
 
 // The partial sums of a group, by a warp, in an order that depends on their
@@ -261,10 +277,10 @@ __global__ void __launch_bounds__(256) clip_join_kernel(const ClipShared a)
 template <int MAX, bool JOIN>
 __global__ void __launch_bounds__(CL_THREADS, 3) clip_scale_kernel(const __grid_constant__ ClipArgs<MAX> a)
 {
-    __shared__ float s_factor;
+    __shared__ ClipFactor s_factor;
     pdl_wait();
     int known = -1;
-    float f = 1.0f;
+    ClipFactor by{1.0f, 0};
     for (ClipWalk<MAX> w(a, true); w.left > 0; w.back(a)) {
         const ClipUnit c = clip_unit(a, w);
         if (w.group != known) {
@@ -281,12 +297,21 @@ __global__ void __launch_bounds__(CL_THREADS, 3) clip_scale_kernel(const __grid_
                     }
                 }
                 __syncthreads();
-                f = s_factor;
+                by = s_factor;
             } else {
-                f = a.s.factor[known];
+                by = a.s.factor[known];
             }
         }
-        if (f == 1.0f && c.in == c.out) continue;
+        const float f = by.mantissa;
+        if (f == 1.0f && by.exponent == 0 && c.in == c.out) continue;
+        if (by.exponent != 0) {                // rare
+            for (int i = threadIdx.x; i < c.count; i += CL_THREADS) {
+                const float v = scalbnf(clip_load(c.in, c.f32, i) * f, by.exponent);
+                if (c.f32) reinterpret_cast<float *>(c.out)[i] = v;
+                else reinterpret_cast<uint16_t *>(c.out)[i] = uint16_t(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+            }
+            continue;
+        }
         const int size = c.f32 ? 4 : 2, per = 16 / size;
         const bool same = ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15u) == 0;
         const int head = same ? min(c.count, int((16 - (reinterpret_cast<uintptr_t>(c.in) & 15u)) & 15u) / size)
@@ -337,7 +362,7 @@ static ClipPlan clip_plan(int32_t groups)
     const int64_t part = (int64_t(p.ctas) + groups) * 8;
     p.sum = (part + 255) / 256 * 256;
     p.factor = p.sum + (int64_t(groups) * 8 + 255) / 256 * 256;
-    p.bytes = p.factor + (int64_t(groups) * 4 + 255) / 256 * 256;
+    p.bytes = p.factor + (int64_t(groups) * 8 + 255) / 256 * 256;
     return p;
 }
 
@@ -452,7 +477,7 @@ LORA_API int lora_clip_gradients(const void *const *grads, void *const *out, con
     c.s.unit_log = elements * groups >= (int64_t(plan.ctas) << CL_LONG_LOG) ? CL_LONG_LOG : CL_UNIT_LOG;
     c.s.part = reinterpret_cast<double *>(ws);
     c.s.sum = reinterpret_cast<double *>(ws + plan.sum);
-    c.s.factor = reinterpret_cast<float *>(ws + plan.factor);
+    c.s.factor = reinterpret_cast<ClipFactor *>(ws + plan.factor);
     c.s.norms = norms;
     c.s.max_norm = max_norm;
     c.s.eps = eps;

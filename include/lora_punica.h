@@ -603,7 +603,9 @@ int lora_dequantize_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t e
  *   workspace    256-byte aligned, lora_clip_gradients_workspace bytes.
  *
  * Sums of squares are fp64 beyond an fp32 sum of a few dozen each, and do not
- * overflow or underflow for any fp32 values; each gradient is rounded once.
+ * overflow or underflow for any fp32 values.  The factor keeps fp32's digits
+ * however far the norm lies above max_norm; its product with a gradient is
+ * rounded to fp32, and then to bf16 where the gradient is.
  * A NaN norm makes its group's gradients NaN, an infinite one makes finite
  * gradients zero.  Deterministic.  Any number of tensors (1024 a launch).
  * The host arrays are read during the call only.  Errors: LORA_ERR_NULL,
