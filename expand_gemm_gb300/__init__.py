@@ -412,6 +412,7 @@ def lora_linear_noalloc(token_lora_mapping: torch.Tensor, x: torch.Tensor, lora_
 # fails.
 
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+_F32_MAX = torch.finfo(torch.float32).max
 _PTRS = [ctypes.c_void_p * n for n in range(LORA_MAX_SLICES + 1)]
 _SIZES = [ctypes.c_int32 * n for n in range(LORA_MAX_SLICES + 1)]
 try:
@@ -1011,7 +1012,8 @@ def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *
 
     grads is a :class:`LoRAGradients` (for every step), or the tensors
     themselves, which are then scaled in place and stack norms.numel() adapters.
-    max_norm None (or infinite) computes the norms alone.  Nothing is read back
+    max_norm None (or infinite) computes the norms alone; other values of it
+    and of eps fit into 32 bits.  Nothing is read back
     to the host: a NaN norm makes its adapter's gradients NaN, and leaves the
     others'."""
     if not isinstance(norms, torch.Tensor):
@@ -1019,10 +1021,13 @@ def lora_clip_gradients(grads, max_norm: Optional[float], norms: torch.Tensor, *
     if not isinstance(grads, LoRAGradients):
         grads = LoRAGradients(grads, norms.numel())
     _all(grads.index, (norms, _F32, "norms"))
-    limit = math.inf if max_norm is None else float(max_norm)
+    limit, eps = math.inf if max_norm is None else float(max_norm), float(eps)
     if not limit >= 0.0 or not eps >= 0.0:
         raise ValueError("max_norm and eps must not be negative")
+    # the library takes them in 32 bits, where larger ones would be infinite
+    if _F32_MAX < limit < math.inf or eps > _F32_MAX:
+        raise ValueError("max_norm must be None, infinite or at most %g, eps at most that" % _F32_MAX)
     norms_ptr, stream = _vector(norms, "norms", grads.groups), _raw_stream(grads.index)
     workspace = grads.workspace(stream)
     _call("lora_clip_gradients", grads.device, grads.c_grads, grads.c_out, grads.c_sizes, grads.c_f32, grads.count,
-          grads.groups, limit, float(eps), norms_ptr, workspace.data_ptr(), grads.workspace_bytes, stream)
+          grads.groups, limit, eps, norms_ptr, workspace.data_ptr(), grads.workspace_bytes, stream)

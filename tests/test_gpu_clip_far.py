@@ -3,6 +3,7 @@ that the factor is no normal number of 32 bits (GPU)."""
 import pytest
 import torch
 
+import expand_gemm_gb300 as eg
 from test_gpu_clip import BF16, F32, check
 
 pytestmark = pytest.mark.gpu
@@ -44,3 +45,16 @@ def test_small_values_beside_large_ones():
     v[0, 0], v[0, 1], v[0, 4999], v[0, 2500] = 3e38, 1e30, 1e38, 1e-10
     check([v.cuda()], 1, 1.0, eps=0.0)
     check([v.cuda().bfloat16()], 1, 1.0, eps=0.0)
+
+
+def test_limits_that_32_bits_do_not_hold_are_refused():
+    """Infinite in 32 bits they would leave the gradients as they are, or make them zero."""
+    g, norms = torch.full((4,), 3e38, device="cuda"), torch.zeros(1, device="cuda")
+    for kw in (dict(max_norm=4e38), dict(max_norm=1e300), dict(max_norm=1.0, eps=1e39), dict(max_norm=1.0, eps=float("inf"))):
+        with pytest.raises(ValueError, match="max_norm"):
+            eg.lora_clip_gradients([g], norms=norms, **kw)
+    assert bool((g == torch.full_like(g, 3e38)).all()) and not bool(norms.any())
+    eg.lora_clip_gradients([g], float(torch.finfo(F32).max), norms, eps=0.0)
+    want = 3.4028234663852886e38 / (2 * float(torch.tensor(3e38))) * 3e38
+    assert bool(((g.double() - want).abs() <= 22 * 2.0 ** -24 * want).all())
+    eg.lora_clip_gradients([g], float("inf"), norms)
