@@ -139,7 +139,9 @@ struct ExpertLayout {
 
 // Rows of a tile of the forward product, by how many rows an expert has on
 // average; EX_TILE: the product on CTA pairs, where 4-bit weights are decoded
-// first.  Both sides measured (us; 16 experts of 4096 x 4096 if nothing else is
+// first.  The host knows neither the rows' shares nor which have an id: every
+// row and every expert counts.  Both sides measured, with equal shares and an id
+// for every row (us; 16 experts of 4096 x 4096 if nothing else is
 // said, in a graph).  bf16, tiles of 32 rows and pairs: 32 rows: 115 and 119;
 // 40 rows: 124 and 120; 64 rows: 138 and 121; one expert, 16 rows: 23 and 34;
 // one of width 11008, 64 rows: 51 and 44.  4 bits, tiles of 16 and of 64 rows:
@@ -147,6 +149,12 @@ struct ExpertLayout {
 // pairs: 256 rows: 221 and 274; 375 rows: 293 and 298; 512 rows: 394 and 330;
 // one expert, 512 rows: 46 and 45; one of width 11008, 384 rows: 68 and 78,
 // 1024 rows: 136 and 107.
+// Where the average is far from the shares (experts of 4096 x 4096, and the same
+// rows by metadata of the experts in use): bf16, 2048 rows of 64 experts, all on
+// one 200 and 67, on eight 200 and 81; 512 rows of 16, on one 69 and 38, on four
+// 71 and 50; 4 bits, 2048 rows of 64, on one 92 and 73; 512 of 16, on one 42 and
+// 44.  Rows without an id cost little: half of 1024 rows of 16 experts, on pairs
+// 116, the other half alone, in tiles of 32, 120; in 4 bits 61 and 62.
 static int forward_tile(int64_t R, int64_t E, bool quantized)
 {
     const int64_t mean = R / E;
@@ -157,7 +165,8 @@ static int forward_tile(int64_t R, int64_t E, bool quantized)
 // Rows of a tile of the products on CTA pairs.  One expert: what takes the
 // pairs the least time in whole rounds, where each tile costs about 16 rows
 // more than it has (4096 rows, 4096 to 4096: 98 us with tiles of 224 rows, 104
-// with 256, 107 with 192).  Several have shares that vary, and a tile costs
+// with 256, 107 with 192).  Rows without an id count too (a tenth of the 4096:
+// 93, as those with one alone; half: 73, those alone 68).  Several have shares that vary, and a tile costs
 // what its rows need, so that short tiles only split experts that one tile
 // would have held (16 experts of 4096 x 4096, 128 rows on average: 139 with
 // 128, 125 with 256; 256 rows: 155 with 192, 151 with 256; 1024 rows of 8: 196

@@ -10,10 +10,12 @@
 // expert's last row or column arrives as zeros, never as its neighbour's
 // values.
 //
-// Bound by the tensor cores.  One GB300, cold: 8192 tokens, 2 of 16 experts
-// 4096 to 11008: 895 us, 1.65 PFLOP/s of what the result needs (a dense library
-// product of the same operations: 767 in a burst, 825 sustained); gradients of
-// 4096 tokens, 2 of 8 experts 4096 x 4096: dx 174, dW 168 (1.58, 1.64).
+// Bound by the tensor cores.  One GB300, each kernel's launch alone on a cool
+// machine: 8192 tokens, 2 of 16 experts 4096 to 11008: 895 us, 1.65 PFLOP/s of
+// what the result needs (a dense library product of the same operations: 767
+// in a burst, 825 sustained); gradients of 4096 tokens, 2 of 8 experts 4096 x
+// 4096: dx 174, dW 168 (1.58, 1.64).  Whole calls, one after another: 990 to
+// 1040 and 420 to 430.
 #include "lora_expert.cuh"
 #include "lora_tc.cuh"
 

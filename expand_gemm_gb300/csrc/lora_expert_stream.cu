@@ -34,8 +34,9 @@
 // memory, which adds them in order.
 //
 // One GB300, whole calls, cold: 256 tokens, 2 of 16 experts 4096 x 4096 in bf16:
-// 100 us, 5.4 TB/s; 32 tokens, 4 of 32 experts 4096 to 11008 in 4 bits: 157, 4.9
-// TB/s, bound by the decoding; one token, two experts 4096 x 4096 in bf16: 20.
+// 99 to 103 us, 5.4 TB/s; 32 tokens, 4 of 32 experts 4096 to 11008 in 4 bits: 156
+// to 160, 4.9 TB/s, bound by the decoding; one token, two experts 4096 x 4096 in
+// bf16: 21 (64 tiles, two CTAs each: 24 of 152 SMs have none).
 #include "lora_expert.cuh"
 #include "lora_tc.cuh"
 
@@ -726,10 +727,10 @@ static int run_stream(StreamArgs &g, cudaStream_t st)
     // Tiles at most: an expert may end in one that is not full.  The segments
     // are those of the call's rows (load_segments: clamp), so a cluster that
     // shares a tile has one, and its barriers' first phases are all it needs.
-    // Up to half the SMs, two CTAs share each, up to a quarter four (us with one, two and
-    // four, in a graph: 64 tiles of 4096 x 4096 for one token in bf16 30.3,
-    // 28.8, 29.8, in 4 bits 24.6, 23.6, 23.0; 32 tiles, 16 rows: 35.3, 26.2,
-    // 22.5 and 29.0, 28.9, 28.5).
+    // Up to half the SMs, two CTAs share each, up to a quarter four (us with
+    // one, two and four, in a graph: 64 tiles of 4096 x 4096 for one token in
+    // bf16 30.3, 28.8, 29.8, in 4 bits 24.6, 23.6, 23.0; 32 tiles, 16 rows: 35.3,
+    // 26.2, 22.5 and 29.0, 28.9, 28.5).
     const int64_t rows = g.p.R, experts = rows < g.p.E ? rows : g.p.E;
     const int64_t most = (rows / NT + experts) * ((g.p.N + ST_ROWS - 1) / ST_ROWS), sms = device_sm_count();
     int parts = most * 4 <= sms ? 4 : most * 2 <= sms ? 2 : 1;

@@ -495,11 +495,12 @@ int64_t lora_orthogonalize_workspace(int32_t count, int32_t rows, int32_t cols);
  *                hidden / 2].
  *   weight_scale NULL, or the scales of the codes, 16-byte aligned uint8
  *                [max_loras, out_features, hidden / 32].
- *   y            device bf16 [num_rows, y_ld], any alignment (rows on 16-byte
- *                boundaries are written faster).  Must not overlap an input.
+ *   y            device bf16 [num_rows, y_ld], any alignment.  Must not overlap an
+ *                input.
  *   add_inputs   nonzero: added to y; zero: y is overwritten.
  *   meta         prepared for these num_rows ids; max_loras is the number of
- *                experts.
+ *                experts.  (Metadata of a larger batch write nothing beyond
+ *                num_rows, and leave rows out.)
  *   workspace    256-byte aligned, at least lora_expert_linear_workspace
  *                bytes; a workspace for a batch holds every smaller one.
  *
