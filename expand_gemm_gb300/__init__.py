@@ -948,7 +948,8 @@ class LoRAGradients:
     scaled gradients.  No two may share memory.  The tensors are kept; their
     storage must stay where it is.  Workspaces are kept for each stream, and a
     captured call has one of its own, so an object may be used on any stream,
-    captured, and dropped while its calls run or graphs hold them."""
+    captured, and dropped while its calls run or graphs hold them (the tensors
+    themselves are the caller's to keep until then)."""
 
     def __init__(self, grads, groups: int = 1, out=None):
         if isinstance(grads, torch.Tensor):
